@@ -1,6 +1,7 @@
-"""What is measured of the training operators around the experts: the layer
-norm with its gradient, and activation checkpoints in 8 bits with their use in
-the backward pass.
+"""What is measured of the operators around the experts: the layer norm with
+its gradient, activation checkpoints in 8 bits with their use in the backward
+pass, and the experts' matrix-vector products with weights in 4 bits, for
+tokens that are generated.
 
 A case names one operator (or a forward with its backward, where the 8-bit
 checkpoint that the one writes is what the other reads), its sizes and its
@@ -11,7 +12,9 @@ The 8-bit format is OCP MXINT8: per 32 neighbouring elements of a row one
 power-of-two scale X = 2^floor(log2 amax), and whole numbers c in [-127, 127]
 that stand for c * X / 64, rounded to nearest even. A checkpoint is a uint8
 tensor of the elements (two's complement) and one of the scales' exponents
-(biased by 127).
+(biased by 127). The 4-bit weights are OCP MXFP4: per 32 neighbouring elements
+of a row one such exponent, and elements of one sign and three magnitude bits
+that stand for 0, 1/2, 1, 3/2, 2, 3, 4, 6; two a byte, the first in the low half.
 """
 import math
 
@@ -30,10 +33,6 @@ def listed():
         {"name": "norm_train_bf16", "op": "norm_train", "T": 16384, "d": 2048, "bf16": True, "bias": True, "stream": True, "act8": True},
         # the widest of the layer's sizes, the largest case
         {"name": "norm_train_wide", "op": "norm_train", "T": 32768, "d": 4096, "bf16": True, "bias": False, "stream": True, "act8": True},
-        # the smallest of the layer's sizes, in fp32 and without a checkpoint: latency counts
-        {"name": "norm_train_small", "op": "norm_train", "T": 256, "d": 128, "bf16": False, "bias": True, "stream": False, "act8": False},
-        # many short rows of an odd width
-        {"name": "norm_train_narrow", "op": "norm_train", "T": 50021, "d": 160, "bf16": True, "bias": True, "stream": False, "act8": True},
         # one token while text is generated
         {"name": "norm_one_token", "op": "norm", "T": 1, "d": 2048, "bf16": True, "bias": True, "stream": True},
         # the gradient alone, fp32, odd sizes in both directions
@@ -50,6 +49,10 @@ def listed():
         {"name": "combine_train_bf16", "op": "combine_train", "T": 16384, "d": 2048, "E": 128, "k": 4, "bf16": True},
         # the combine's backward alone on a handful of tokens
         {"name": "combine_back_f32", "op": "combine_back", "T": 37, "d": 352, "E": 8, "k": 2, "bf16": False},
+        # the experts of one generated token, of the layer's own widths
+        {"name": "w4_one_token", "op": "w4", "T": 1, "d": 2048, "h": 1024, "E": 128, "k": 4, "bf16": True},
+        # the experts of a batch of sequences that are generated together
+        {"name": "w4_batch", "op": "w4", "T": 64, "d": 2048, "h": 1024, "E": 128, "k": 4, "bf16": True},
     ]
 
 
@@ -66,7 +69,7 @@ def draw(rng):
     steps of 32, no more bytes than the largest listed case."""
     most = work(listed()[1])["bytes"]
     while True:
-        op = rng.choice(["norm_train", "norm", "norm_back", "act8", "swiglu", "combine_train", "combine_back"])
+        op = rng.choice(["norm_train", "norm", "norm_back", "act8", "swiglu", "combine_train", "combine_back", "w4", "w4"])
         bf16 = rng.random() < 0.6
         if op.startswith("norm"):
             c = {"op": op, "T": _size(rng, 1, 65536), "d": _width(rng, 32, 16384), "bf16": bf16, "bias": rng.random() < 0.5, "stream": rng.random() < 0.5}
@@ -76,6 +79,11 @@ def draw(rng):
             c = {"op": op, "rows": _size(rng, 1, 131072), "cols": _width(rng, 32, 16384), "bf16": bf16}
         elif op == "swiglu":
             c = {"op": op, "rows": _size(rng, 1, 131072), "h": _width(rng, 32, 8192), "bf16": bf16}
+        elif op == "w4":
+            E = _size(rng, 2, 256)
+            c = {"op": op, "T": _size(rng, 1, 256), "d": _width(rng, 32, 8192), "h": _width(rng, 32, 4096), "E": E, "k": rng.randint(1, min(8, E)), "bf16": True}
+            if E * c["h"] * c["d"] > 128 * 2048 * 1024:
+                continue
         else:
             E = _size(rng, 2, 256)
             c = {"op": op, "T": _size(rng, 1, 32768), "d": _width(rng, 32, 16384), "E": E, "k": rng.randint(1, min(8, E)), "bf16": bf16}
@@ -107,6 +115,11 @@ def work(case):
         n = case["rows"] * case["h"]
         return {"bytes": n * (2 * q + 3 * s), "flops": 12 * n}
     T, d, E, k = case["T"], case["d"], case["E"], case["k"]
+    if op == "w4":
+        h = case["h"]
+        # the experts that T tokens choose at random, their weights read once
+        n = E * (1 - (1 - k / E) ** T) * 3 * h * d
+        return {"bytes": n * (1 / 2 + 1 / 32) + 2 * T * d * s + 20 * T * k + 4 * E, "flops": 6 * T * k * h * d}
     n = T * k * d
     bwd = T * d * s + n * (q + s) + 12 * T * k + 4 * T * E + 4 * T * k
     if op == "combine_back":
@@ -131,6 +144,20 @@ def _randn(g, *shape):
 def _channels(g, d):
     """Widths of a model's channels: most alike, some several times larger."""
     return torch.exp(0.5 * _randn(g, d))
+
+
+_E2M1 = (0.0, 0.5, 1.0, 1.5, 2.0, 3.0, 4.0, 6.0)
+
+
+def _weights4(g, E, rows, cols):
+    """E matrices of normal weights in 4 bits (nearest element): bytes and scales' exponents."""
+    w = (_randn(g, E, rows, cols) * cols ** -0.5).view(E, rows, cols // 32, 32)
+    e = (w.abs().amax(3).view(torch.int32) >> 23) - 2  # the largest element, 6, is 1.5 * 2^2
+    v = torch.ldexp(w.abs(), 127 - e[..., None])
+    mid = torch.tensor([0.25, 0.75, 1.25, 1.75, 2.5, 3.5, 5.0], device="cuda")
+    c = torch.bucketize(v, mid, out_int32=True).to(torch.uint8) | (w < 0).to(torch.uint8) << 3
+    c = c.view(E, rows, cols // 2, 2)
+    return c[..., 0] | c[..., 1] << 4, e.to(torch.uint8)
 
 
 def prepare(case, seed):
@@ -163,13 +190,23 @@ def prepare(case, seed):
         st["ab8"], st["ab8_scale"] = _encode(ab)
     else:
         T, d, E, k = case["T"], case["d"], case["E"], case["k"]
+        if op == "w4":
+            h = case["h"]
+            st["w1q"], st["w1s"] = _weights4(g, E, 2 * h, d)
+            st["w2q"], st["w2s"] = _weights4(g, E, d, h)
+            st["x"] = _randn(g, T, d).to(dt)
         top, idx = _randn(g, T, E).topk(k, dim=1)
-        st["gate"] = torch.softmax(top, 1).contiguous()
+        st["topk_gate"] = torch.softmax(top, 1).contiguous()
         st["topk_idx"] = idx.int().contiguous()
         order = torch.argsort(idx.reshape(-1), stable=True)  # rows by expert, then by token
         pos = torch.empty(T * k, dtype=torch.int32, device="cuda")
         pos[order] = torch.arange(T * k, dtype=torch.int32, device="cuda")
         st["token_pos"] = pos.view(T, k)
+        if op == "w4":  # the rest of what the routing hands on
+            st["sorted_token"] = torch.div(order, k, rounding_mode="floor").int()
+            ends = torch.bincount(idx.reshape(-1), minlength=E).cumsum(0).int()
+            st["offsets"] = torch.cat([ends.new_zeros(1), ends])
+            return st
         y = (_randn(g, T * k, d) * _channels(g, d)).to(dt)
         st["dout"] = _randn(g, T, d).to(dt)
         if op == "combine_train":
@@ -222,7 +259,7 @@ def _norm_back(f, mean, rstd, dy, weight, dsum, has_bias):
 
 def _combine_back(y, st):
     """y: the experts' rows that the checkpoint stands for, in fp32."""
-    gate, pos, go = st["gate"], st["token_pos"].long(), st["dout"].float()
+    gate, pos, go = st["topk_gate"], st["token_pos"].long(), st["dout"].float()
     dgate = (y[pos] * go[:, None]).sum(2)
     dy = torch.empty(y.shape, dtype=st["dout"].dtype, device=y.device)
     dy[pos.reshape(-1)] = (gate[..., None] * go[:, None]).to(dy.dtype).reshape(y.shape)
@@ -232,8 +269,32 @@ def _combine_back(y, st):
     return {"dy_perm": dy, "dlogits": dlogits.scatter(1, st["topk_idx"].long(), rows), "dgate": dgate}
 
 
+def _decode4(q, scale):
+    """The weights that 4-bit elements [..., rows, cols/2] and scales stand for, in fp32."""
+    both = torch.stack((q & 15, q >> 4), -1).reshape(*scale.shape, 32).int()
+    v = torch.tensor(_E2M1 + tuple(-x for x in _E2M1), device=q.device)[both]
+    return torch.ldexp(v, scale[..., None].int() - 127).flatten(-2)
+
+
+def _experts4(st):
+    x, idx, E, T, k, h = st["x"].float(), st["topk_idx"].long(), st["E"], st["T"], st["k"], st["h"]
+    if T * k < E:  # the chosen experts' weights for every token
+        w1, w2 = (_decode4(st[q][idx.reshape(-1)], st[s][idx.reshape(-1)]) for q, s in (("w1q", "w1s"), ("w2q", "w2s")))
+        ab = torch.bmm(w1, x.repeat_interleave(k, 0)[:, :, None])[:, :, 0]
+        a, b = ab[:, :h], ab[:, h:]
+        y = torch.bmm(w2, (a / (1 + torch.exp(-a)) * b)[:, :, None]).view(T, k, -1)
+    else:  # all experts for all tokens, then the chosen ones
+        ab = torch.matmul(_decode4(st["w1q"], st["w1s"]), x.t())
+        a, b = ab[:, :h], ab[:, h:]
+        y = torch.bmm(_decode4(st["w2q"], st["w2s"]), a / (1 + torch.exp(-a)) * b)  # [E, d, T]
+        y = y[idx, :, torch.arange(T, device=x.device)[:, None]]
+    return (st["topk_gate"][..., None] * y).sum(1).to(st["x"].dtype)
+
+
 def _plain(st):
     op = st["op"]
+    if op == "w4":
+        return _experts4(st)
     if op == "norm" or op == "norm_train":
         s = st["x"] if st["res"] is None else (st["x"].float() + st["res"].float()).to(st["x"].dtype)
         y, mean, rstd = _norm(s, st["weight"], st["bias_v"])
@@ -255,7 +316,7 @@ def _plain(st):
         return {"ab": ab.to(dt), "hp": (a / (1 + torch.exp(-a)) * b).to(dt)}
     if op == "combine_train":
         y, pos = st["y"], st["token_pos"].long()
-        out = (y.float()[pos] * st["gate"][..., None]).sum(1).to(y.dtype)
+        out = (y.float()[pos] * st["topk_gate"][..., None]).sum(1).to(y.dtype)
         return {"out": out, **_combine_back(_decode(*_encode(y)), st)}
     return _combine_back(_decode(st["y8"], st["y8_scale"]), st)
 
@@ -288,11 +349,13 @@ def _calls(st):
     if op == "swiglu":
         ab, hp = moe.moe_act8_swiglu(st["ab8"], st["ab8_scale"], torch.bfloat16 if st["bf16"] else torch.float32)
         return {"ab": ab, "hp": hp}
+    if op == "w4":
+        return moe.moe_w4_experts(st["x"], st, st["w1q"], st["w1s"], st["w2q"], st["w2s"])
     out = {}
     y8, scale = st.get("y8"), st.get("y8_scale")
     if op == "combine_train":
-        out["out"], y8, scale = moe.moe_combine_act8(st["y"], st["gate"], st["token_pos"])
-    b = moe.moe_combine_backward_act8(st["dout"], y8, scale, st["gate"], st["topk_idx"], st["token_pos"], st["E"])
+        out["out"], y8, scale = moe.moe_combine_act8(st["y"], st["topk_gate"], st["token_pos"])
+    b = moe.moe_combine_backward_act8(st["dout"], y8, scale, st["topk_gate"], st["topk_idx"], st["token_pos"], st["E"])
     return {**out, "dy_perm": b["dy_perm"], "dlogits": b["dlogits"], "dgate": b["dgate"]}
 
 
@@ -317,6 +380,15 @@ def _exact_codes(q, scale):
     n = q.to(torch.int16)
     n = torch.where(n > 127, n - 256, n).double()
     return n * torch.exp2(scale.double() - 133).repeat_interleave(32, dim=1)
+
+
+def _exact_weights4(q, scale):
+    """Sign, two exponent bits, one mantissa bit: (1 + m/2) 2^(e-1), or m/2 where e is 0."""
+    c = torch.empty(q.shape[0], 2 * q.shape[1], dtype=torch.int64, device=q.device)
+    c[:, 0::2], c[:, 1::2] = (q % 16).long(), (q // 16).long()
+    e, m, sign = (c // 2) % 4, (c % 2).double(), 1 - 2 * (c // 8).double()
+    v = torch.where(e == 0, m / 2, (1 + m / 2) * torch.exp2(e.double() - 1))
+    return sign * v * torch.exp2(scale.double() - 127).repeat_interleave(32, dim=1)
 
 
 def exact(case, seed):
@@ -353,7 +425,17 @@ def exact(case, seed):
         ab = _exact_codes(st["ab8"], st["ab8_scale"])
         return {"ab": ab, "hp": torch.sigmoid(ab[:, :case["h"]]) * ab[:, :case["h"]] * ab[:, case["h"]:]}
     T, k = case["T"], case["k"]
-    gate, pos, out = st["gate"].double(), st["token_pos"].long(), {}
+    if op == "w4":
+        x, h = st["x"].double(), case["h"]
+        out = torch.zeros_like(x)
+        for e in range(case["E"]):
+            t, j = torch.nonzero(st["topk_idx"] == e, as_tuple=True)
+            if len(t):
+                ab = x[t] @ _exact_weights4(st["w1q"][e], st["w1s"][e]).T
+                y = (torch.sigmoid(ab[:, :h]) * ab[:, :h] * ab[:, h:]) @ _exact_weights4(st["w2q"][e], st["w2s"][e]).T
+                out[t] += st["topk_gate"][t, j].double()[:, None] * y
+        return out
+    gate, pos, out = st["topk_gate"].double(), st["token_pos"].long(), {}
     y = _exact_act8(st["y"]) if op == "combine_train" else _exact_codes(st["y8"], st["y8_scale"])
     go = st["dout"].double()
     dy = torch.zeros_like(y)
