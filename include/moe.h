@@ -76,7 +76,9 @@ const char *moe_status_str(moe_status s);
  * with hp_cols, hp_cols_scale (zero them when unused), and the MXFP8
  * backward uses dy_perm as scratch. 102: moe_gemm_desc ends with
  * aux_out_cols, aux_out_cols_scale, and aux_out_scale selects the MXFP8
- * SwiGLU forward that stores H' quantised (zero all three when unused). */
+ * SwiGLU forward that stores H' quantised (zero all three when unused).
+ * The 8-bit checkpoints and the layer norm are calls of their own beside
+ * these and change no descriptor. */
 int32_t moe_version(void);
 
 /* ------------------------------------------------------------------ */
@@ -513,6 +515,119 @@ size_t moe_load_balance_workspace_size(int64_t T, int32_t E);
 moe_status moe_load_balance(const float *logits, const int32_t *counts, int64_t T, int32_t E,
                             int32_t k, float alpha, float *stats, float *dlogits, void *ws,
                             size_t ws_bytes, void *stream);
+
+/* ------------------------------------------------------------------ */
+/* Activation checkpoints in 8 bits                                     */
+
+/* What a layer holds from its forward to its backward, in 8 bits instead of
+ * 16 or 32 (the report trades that memory for recomputation: about two
+ * thirds of the activations for about a fifth of the throughput,
+ * kongchang.com, "where the costs are"). The format is OCP MXINT8
+ * (Microscaling v1.0): per block of 32 neighbouring elements of a row
+ *   scale byte e = the biased fp32 exponent of the largest magnitude amax
+ *                  (0 for an all-zero or subnormal block),
+ *   elements     c = x * 2^(133-e) rounded to the nearest whole number (ties
+ *                to even) and clamped to [-127, 127], one byte each (two's
+ *                complement), standing for c * 2^(e-133).
+ * An element is off by at most half a step of 2^(e-133) <= amax / 64; only
+ * magnitudes beyond 127.5 steps are off by up to one. A block that holds a
+ * NaN or an infinity has scale byte 255 and zero elements and stands for 32
+ * NaNs. Every other value a checkpoint stands for is exact in bf16, so what
+ * is loaded as bf16 or as fp32 is the same. -0 becomes +0.
+ * Layout: elements [rows, cols], scales [rows, cols/32]. cols: a multiple of
+ * 32 below 2^20; rows < 2^31. Tensors and elements 16-byte aligned, scales
+ * at any address. dt: MOE_F32 or MOE_BF16. rows = 0 (or T = 0) is a no-op.
+ * Outputs must not overlap inputs.
+ *
+ * moe_act8_store: q, scale = the checkpoint of in [rows, cols].
+ * moe_act8_load:  out [rows, cols] = the values a checkpoint stands for.
+ * moe_act8_swiglu: from the checkpoint of AB [rows, 2h], the two tensors the
+ *   backward reads: ab [rows, 2h] = its values and hp [rows, h] = silu(a) b of
+ *   them (fp32, rounded once). h: a multiple of 32, at most 8192. */
+moe_status moe_act8_store(const void *in, moe_dtype dt, int64_t rows, int64_t cols, uint8_t *q,
+                          uint8_t *scale, void *stream);
+moe_status moe_act8_load(const uint8_t *q, const uint8_t *scale, moe_dtype dt, int64_t rows,
+                         int64_t cols, void *out, void *stream);
+moe_status moe_act8_swiglu(const uint8_t *ab8, const uint8_t *ab8_scale, moe_dtype dt,
+                           int64_t rows, int32_t h, void *ab, void *hp, void *stream);
+
+/* moe_combine (the same out, bit for bit) that also stores the checkpoint of
+ * every y_perm row it reads, from the same read: y8 [R, d], y8_scale
+ * [R, d/32], R = the rows of y_perm. Rows that no token_pos names are left
+ * as they were. */
+moe_status moe_combine_act8(const void *y_perm, moe_dtype dt, const float *topk_gate,
+                            const int32_t *token_pos, int64_t T, int32_t d, int32_t k, void *out,
+                            uint8_t *y8, uint8_t *y8_scale, void *stream);
+
+/* The first stage of moe_backward with y_perm read from its checkpoint, y8 =
+ * the values it stands for (for the meaning of the others see moe_bwd_desc):
+ *   dgate[t, j] = <dout[t], y8[token_pos[t, j]]>        (dgate may be null)
+ *   dy_perm[token_pos[t, j]] = topk_gate[t, j] * dout[t], rounded to dt
+ *   dlogits[t, e_i] = g_i sum_j g_j (dgate_i - dgate_j), 0 for unselected
+ *   experts. A slot with token_pos < 0 counts as dgate = 0; rows of dy_perm
+ *   that no token_pos names are left as they were. */
+moe_status moe_combine_backward_act8(const void *dout, moe_dtype dt, const uint8_t *y8,
+                                     const uint8_t *y8_scale, const float *topk_gate,
+                                     const int32_t *topk_idx, const int32_t *token_pos, int64_t T,
+                                     int32_t d, int32_t k, int32_t E, void *dy_perm,
+                                     float *dlogits, float *dgate, void *stream);
+
+/* moe_backward of a layer that held AB and y_perm as checkpoints. b is
+ * moe_backward's descriptor, with three differences: y_perm is not read (may
+ * be null); ab [T*k, 2h] and hp [T*k, h] are scratch that the call WRITES (AB
+ * and H' rebuilt from ab8, as moe_act8_swiglu; MXFP8 with hp_cols given:
+ * AB alone, hp not touched); stage 0 of stage_events ends after that
+ * rebuilding. c is read during the call only. With T = 0 its pointers may be
+ * null. */
+typedef struct moe_act8_saved {
+    const uint8_t *ab8;        /* [T*k, 2h] */
+    const uint8_t *ab8_scale;  /* [T*k, 2h/32] */
+    const uint8_t *y8;         /* [T*k, d] */
+    const uint8_t *y8_scale;   /* [T*k, d/32] */
+} moe_act8_saved;
+
+moe_status moe_backward_act8(const moe_bwd_desc *b, const moe_act8_saved *c, void *stream);
+
+/* ------------------------------------------------------------------ */
+/* Layer norm                                                           */
+
+/* The norm in front of (or behind) the layer, over rows of d elements:
+ *   s = x, or s = x + residual rounded to dt (then stored in sum: the residual
+ *       stream after this point)
+ *   mean = sum(s) / d,  rstd = 1 / sqrt(sum((s - mean)^2) / d + eps)
+ *   y = (s - mean) * rstd * gamma + beta, rounded to dt
+ * x, residual, sum, y [T, d] in dt (MOE_F32 or MOE_BF16); gamma, beta [d]
+ * fp32, beta may be null (0). residual and sum are given together or both
+ * null. mean, rstd [T] fp32, each may be null (a forward without a backward).
+ * x8 [T, d], x8_scale [T, d/32]: both or neither; s as an 8-bit checkpoint
+ * (the format of moe_act8_store), written from the same read. d: a multiple
+ * of 32, at most 16384; T < 2^31; 0 < eps <= 1 (MOE_ERR_SHAPE otherwise).
+ * Tensors, gamma, beta and x8 16-byte aligned. Sums are fp32 in a fixed order. A row
+ * with a NaN or an infinity gives NaNs in that row alone. Outputs must not
+ * overlap inputs. T = 0 is a no-op. */
+moe_status moe_layer_norm(const void *x, moe_dtype dt, const void *residual, const float *gamma,
+                          const float *beta, float eps, int64_t T, int32_t d, void *y, void *sum,
+                          float *mean, float *rstd, uint8_t *x8, uint8_t *x8_scale, void *stream);
+
+/* Its backward, with xh = (s - mean) * rstd and g = dy * gamma:
+ *   dx = rstd * (g - mean(g) - xh * mean(g * xh)) (+ dsum), rounded to dt: the
+ *        gradient of x and, with a residual, of it too (the same tensor)
+ *   dgamma[c] = sum_t dy[t, c] xh[t, c],  dbeta[c] = sum_t dy[t, c]
+ * s comes in as x [T, d] (the forward's x, or its sum) or as its checkpoint
+ * x8, x8_scale: exactly one of the two (MOE_ERR_NULL otherwise). mean, rstd:
+ * the forward's. dsum [T, d], nullable: the gradient arriving at sum by its
+ * other uses. dgamma, dbeta [d] fp32, each may be null; overwritten, or with
+ * accumulate_dw = 1 added to (one fp32 add per element; T = 0 then leaves
+ * them unchanged, and zeroes them otherwise). ws:
+ * moe_layer_norm_backward_workspace_size bytes, 16-byte aligned, needed when
+ * dgamma or dbeta is given. Deterministic: fixed-order sums, no atomics.
+ * Limits and types as moe_layer_norm. */
+size_t moe_layer_norm_backward_workspace_size(moe_dtype dt, int64_t T, int32_t d);
+moe_status moe_layer_norm_backward(const void *dy, moe_dtype dt, const void *x, const uint8_t *x8,
+                                   const uint8_t *x8_scale, const float *mean, const float *rstd,
+                                   const float *gamma, const void *dsum, int64_t T, int32_t d,
+                                   void *dx, float *dgamma, float *dbeta, int32_t accumulate_dw,
+                                   void *ws, size_t ws_bytes, void *stream);
 
 #ifdef __cplusplus
 }

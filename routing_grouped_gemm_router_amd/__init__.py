@@ -64,6 +64,10 @@ class CopyWalk(ctypes.Structure):
                 ("bad_offset", _I64), ("bad_bytes", _I64)]
 
 
+class Act8Saved(ctypes.Structure):
+    _fields_ = [("ab8", _P), ("ab8_scale", _P), ("y8", _P), ("y8_scale", _P)]
+
+
 class BwdWsLayout(ctypes.Structure):
     _fields_ = [(n, _SZ) for n in ("row_q", "row_s", "col0_q", "col0_s", "col1_q", "col1_s",
                                    "total")]
@@ -125,6 +129,27 @@ def _load():
     lib.moe_load_balance_workspace_size.restype = _SZ
     lib.moe_load_balance.argtypes = [_P, _P, _I64, _I32, _I32, ctypes.c_float, _P, _P, _P, _SZ, _P]
     lib.moe_load_balance.restype = _I32
+    lib.moe_act8_store.argtypes = [_P, _I32, _I64, _I64, _P, _P, _P]
+    lib.moe_act8_store.restype = _I32
+    lib.moe_act8_load.argtypes = [_P, _P, _I32, _I64, _I64, _P, _P]
+    lib.moe_act8_load.restype = _I32
+    lib.moe_act8_swiglu.argtypes = [_P, _P, _I32, _I64, _I32, _P, _P, _P]
+    lib.moe_act8_swiglu.restype = _I32
+    lib.moe_combine_act8.argtypes = [_P, _I32, _P, _P, _I64, _I32, _I32, _P, _P, _P, _P]
+    lib.moe_combine_act8.restype = _I32
+    lib.moe_combine_backward_act8.argtypes = [_P, _I32, _P, _P, _P, _P, _P, _I64, _I32, _I32,
+                                              _I32, _P, _P, _P, _P]
+    lib.moe_combine_backward_act8.restype = _I32
+    lib.moe_backward_act8.argtypes = [ctypes.POINTER(BwdDesc), ctypes.POINTER(Act8Saved), _P]
+    lib.moe_backward_act8.restype = _I32
+    lib.moe_layer_norm.argtypes = [_P, _I32, _P, _P, _P, ctypes.c_float, _I64, _I32, _P, _P, _P,
+                                   _P, _P, _P, _P]
+    lib.moe_layer_norm.restype = _I32
+    lib.moe_layer_norm_backward_workspace_size.argtypes = [_I32, _I64, _I32]
+    lib.moe_layer_norm_backward_workspace_size.restype = _SZ
+    lib.moe_layer_norm_backward.argtypes = [_P, _I32, _P, _P, _P, _P, _P, _P, _P, _I64, _I32, _P,
+                                            _P, _P, _I32, _P, _SZ, _P]
+    lib.moe_layer_norm_backward.restype = _I32
     return lib
 
 
@@ -375,11 +400,14 @@ def moe_grouped_gemm(mode: int, A: torch.Tensor, B: torch.Tensor, C: torch.Tenso
 
 def moe_backward(saved: dict, dout: torch.Tensor, E: int, k: int, d: int, h: int,
                  out: dict | None = None, want_dgate: bool = True, mxfp8: bool = False,
-                 accumulate_dw: bool = False, stage_events=None) -> dict:
+                 accumulate_dw: bool = False, stage_events=None,
+                 act8: dict | None = None) -> dict:
     """Backward of the whole layer. `saved` holds the forward tensors
     (x_perm, ab, hp, y_perm, topk_gate, topk_idx, token_pos, offsets, w1, w2;
     with mxfp8: x, sorted_token, w1t, w1t_scale, w2t, w2t_scale instead of
-    x_perm, w1, w2)."""
+    x_perm, w1, w2). act8: the checkpoints ab8, ab8_scale, y8, y8_scale of a
+    layer that held these instead of ab and y_perm (moe_backward_act8): saved's
+    ab and hp are then scratch that the call writes, its y_perm is not used."""
     T = dout.shape[0]
     R = T * k
     dev, dt = dout.device, dout.dtype
@@ -396,7 +424,16 @@ def moe_backward(saved: dict, dout: torch.Tensor, E: int, k: int, d: int, h: int
     b.accumulate_dw = 1 if accumulate_dw else 0
     b.dtype = MOE_MXFP8 if mxfp8 else _dt(dout)
     b.d, b.h, b.E, b.k, b.T = d, h, E, k, T
-    names = ("ab", "hp", "y_perm", "topk_gate", "topk_idx", "token_pos", "offsets")
+    names = ("ab", "hp", "topk_gate", "topk_idx", "token_pos", "offsets")
+    if act8 is None:
+        names += ("y_perm",)
+    else:
+        act = torch.bfloat16 if mxfp8 else dt
+        _act8_need(act8["ab8"], act8["ab8_scale"], R, 2 * h, dev, "ab8")
+        _act8_need(act8["y8"], act8["y8_scale"], R, d, dev, "y8")
+        _need(saved["ab"], (R, 2 * h), act, "ab")
+        if saved.get("hp") is not None or not mxfp8:
+            _need(saved["hp"], (R, h), act, "hp")
     names += (("x", "sorted_token", "w1t", "w1t_scale", "w2t", "w2t_scale") if mxfp8
               else ("x_perm", "w1", "w2"))
     for name in names:
@@ -423,7 +460,12 @@ def moe_backward(saved: dict, dout: torch.Tensor, E: int, k: int, d: int, h: int
                                           for e in list(stage_events) +
                                           [None] * (MOE_BWD_MAX_STAGES - len(stage_events))])
         b.stage_events = ctypes.cast(arr, ctypes.POINTER(_P))
-    _check("moe_backward", _lib.moe_backward(ctypes.byref(b), _stream()))
+    if act8 is None:
+        _check("moe_backward", _lib.moe_backward(ctypes.byref(b), _stream()))
+    else:
+        c = Act8Saved(*(act8[n].data_ptr() for n, _ in Act8Saved._fields_))
+        _check("moe_backward_act8", _lib.moe_backward_act8(ctypes.byref(b), ctypes.byref(c),
+                                                           _stream()))
     return out
 
 
@@ -563,20 +605,301 @@ def moe_capacity_zero_rows(buf: torch.Tensor, offsets: torch.Tensor, capacity: i
 
 
 # ---------------------------------------------------------------------------
+# 8-bit activation checkpoints and the layer norm
+
+
+class _On:
+    """The stream of `dev` that work is issued on, with `dev` current while
+    the call is made (tensors need not be on the current device)."""
+
+    def __init__(self, dev):
+        self.dev = dev
+
+    def __enter__(self):
+        self.before = torch.cuda.current_device()
+        if self.dev.index != self.before:
+            torch.cuda.set_device(self.dev)
+        return torch.cuda.current_stream(self.dev).cuda_stream
+
+    def __exit__(self, *exc):
+        if self.dev.index != self.before:
+            torch.cuda.set_device(self.before)
+
+
+def _ptr(t):
+    return None if t is None else t.data_ptr()
+
+
+def _need_on(t, shape, dtype, dev, name):
+    """t is a contiguous tensor of this shape and dtype on the GPU `dev`."""
+    if t is None:
+        raise ValueError(f"{name} is required")
+    if t.shape != shape or t.dtype != dtype or not t.is_contiguous() or not t.is_cuda or \
+            t.device != dev:
+        raise ValueError(f"{name}: expected contiguous {dtype} {tuple(shape)} on {dev}, got "
+                         f"{t.dtype} {tuple(t.shape)} (contiguous={t.is_contiguous()}, "
+                         f"device={t.device})")
+
+
+def _act_matrix(x, name):
+    """rows, cols of a contiguous 2-d f32 / bf16 GPU tensor whose rows are
+    whole blocks of 32, and its C dtype."""
+    if x is None:
+        raise ValueError(f"{name} is required")
+    if x.dtype != torch.bfloat16 and x.dtype != torch.float32:
+        raise ValueError(f"{name}: expected bf16 or f32, got {x.dtype}")
+    if x.dim() != 2 or x.shape[1] < 32 or x.shape[1] % 32:
+        raise ValueError(f"{name}: expected [rows, a multiple of 32], got {tuple(x.shape)}")
+    _need_on(x, x.shape, x.dtype, x.device, name)
+    return x.shape[0], x.shape[1], MOE_BF16 if x.dtype == torch.bfloat16 else MOE_F32
+
+
+def _act8_need(q, scale, rows, cols, dev, name):
+    _need_on(q, (rows, cols), torch.uint8, dev, name)
+    _need_on(scale, (rows, cols // 32), torch.uint8, dev, name + "_scale")
+
+
+def _act8_out(rows, cols, dev, q, scale, name):
+    """The tensors of a checkpoint to be written: the caller's, or new ones."""
+    if q is None:
+        q = torch.empty((rows, cols), dtype=torch.uint8, device=dev)
+    if scale is None:
+        scale = torch.empty((rows, cols // 32), dtype=torch.uint8, device=dev)
+    _act8_need(q, scale, rows, cols, dev, name)
+    return q, scale
+
+
+def _act8_in(q, scale, dtype, name):
+    if dtype != torch.bfloat16 and dtype != torch.float32:
+        raise ValueError(f"dtype: expected bf16 or f32, got {dtype}")
+    if q is None or q.dim() != 2 or q.shape[1] < 32 or q.shape[1] % 32:
+        raise ValueError(f"{name}: expected [rows, a multiple of 32], got "
+                         f"{None if q is None else tuple(q.shape)}")
+    rows, cols = q.shape
+    _act8_need(q, scale, rows, cols, q.device, name)
+    return rows, cols, MOE_BF16 if dtype == torch.bfloat16 else MOE_F32
+
+
+def moe_act8_store(x: torch.Tensor, q: torch.Tensor | None = None,
+                   scale: torch.Tensor | None = None):
+    """The 8-bit checkpoint (MXINT8, see moe.h) of x [rows, cols]: uint8 q
+    [rows, cols] and scale [rows, cols/32]."""
+    rows, cols, dt = _act_matrix(x, "x")
+    q, scale = _act8_out(rows, cols, x.device, q, scale, "q")
+    with _On(x.device) as s:
+        _check("moe_act8_store", _lib.moe_act8_store(_ptr(x), dt, rows, cols, _ptr(q),
+                                                     _ptr(scale), s))
+    return q, scale
+
+
+def moe_act8_load(q: torch.Tensor, scale: torch.Tensor, dtype: torch.dtype = torch.bfloat16,
+                  out: torch.Tensor | None = None) -> torch.Tensor:
+    """The values that a checkpoint stands for, as `dtype` (exact in both)."""
+    rows, cols, dt = _act8_in(q, scale, dtype, "q")
+    if out is None:
+        out = torch.empty((rows, cols), dtype=dtype, device=q.device)
+    _need_on(out, (rows, cols), dtype, q.device, "out")
+    with _On(q.device) as s:
+        _check("moe_act8_load", _lib.moe_act8_load(_ptr(q), _ptr(scale), dt, rows, cols, _ptr(out),
+                                                   s))
+    return out
+
+
+def moe_act8_swiglu(ab8: torch.Tensor, ab8_scale: torch.Tensor,
+                    dtype: torch.dtype = torch.bfloat16, ab: torch.Tensor | None = None,
+                    hp: torch.Tensor | None = None):
+    """From the checkpoint of A||B [rows, 2h]: (ab, hp), its values and
+    H' = silu(a) b of them."""
+    rows, cols, dt = _act8_in(ab8, ab8_scale, dtype, "ab8")
+    h = cols // 2
+    if h % 32:
+        raise ValueError(f"ab8: the hidden width must be a multiple of 32, got {h}")
+    if ab is None:
+        ab = torch.empty((rows, cols), dtype=dtype, device=ab8.device)
+    if hp is None:
+        hp = torch.empty((rows, h), dtype=dtype, device=ab8.device)
+    _need_on(ab, (rows, cols), dtype, ab8.device, "ab")
+    _need_on(hp, (rows, h), dtype, ab8.device, "hp")
+    with _On(ab8.device) as s:
+        _check("moe_act8_swiglu", _lib.moe_act8_swiglu(_ptr(ab8), _ptr(ab8_scale), dt, rows, h,
+                                                       _ptr(ab), _ptr(hp), s))
+    return ab, hp
+
+
+def moe_combine_act8(y_perm: torch.Tensor, topk_gate: torch.Tensor, token_pos: torch.Tensor,
+                     out: torch.Tensor | None = None, y8: torch.Tensor | None = None,
+                     y8_scale: torch.Tensor | None = None):
+    """moe_combine that also stores the checkpoint of the rows it reads:
+    (out [T, d], y8 [R, d], y8_scale [R, d/32]). token_pos must stay below R,
+    the rows of y_perm."""
+    rows, d, dt = _act_matrix(y_perm, "y_perm")
+    dev = y_perm.device
+    T, k = token_pos.shape
+    _need_on(token_pos, (T, k), torch.int32, dev, "token_pos")
+    _need_on(topk_gate, (T, k), torch.float32, dev, "topk_gate")
+    if out is None:
+        out = torch.empty((T, d), dtype=y_perm.dtype, device=dev)
+    _need_on(out, (T, d), y_perm.dtype, dev, "out")
+    y8, y8_scale = _act8_out(rows, d, dev, y8, y8_scale, "y8")
+    with _On(dev) as s:
+        _check("moe_combine_act8", _lib.moe_combine_act8(
+            _ptr(y_perm), dt, _ptr(topk_gate), _ptr(token_pos), T, d, k, _ptr(out), _ptr(y8),
+            _ptr(y8_scale), s))
+    return out, y8, y8_scale
+
+
+def moe_combine_backward_act8(dout: torch.Tensor, y8: torch.Tensor, y8_scale: torch.Tensor,
+                              topk_gate: torch.Tensor, topk_idx: torch.Tensor,
+                              token_pos: torch.Tensor, E: int, out: dict | None = None,
+                              want_dgate: bool = True) -> dict:
+    """The combine's backward with the router's, y_perm read from its
+    checkpoint (see moe.h): dict of dy_perm [R, d], dlogits [T, E], dgate
+    [T, k]. With `out`, into its tensors (dgate only if it has one)."""
+    T, d, dt = _act_matrix(dout, "dout")
+    dev = dout.device
+    if y8 is None or y8.dim() != 2:
+        raise ValueError("y8: expected [rows, d]")
+    R, k = y8.shape[0], token_pos.shape[1]
+    _act8_need(y8, y8_scale, R, d, dev, "y8")
+    _need_on(topk_gate, (T, k), torch.float32, dev, "topk_gate")
+    _need_on(topk_idx, (T, k), torch.int32, dev, "topk_idx")
+    _need_on(token_pos, (T, k), torch.int32, dev, "token_pos")
+    if out is None:
+        out = dict(dy_perm=torch.empty((R, d), dtype=dout.dtype, device=dev),
+                   dlogits=torch.empty((T, E), dtype=torch.float32, device=dev))
+        if want_dgate:
+            out["dgate"] = torch.empty((T, k), dtype=torch.float32, device=dev)
+    _need_on(out["dy_perm"], (R, d), dout.dtype, dev, "dy_perm")
+    _need_on(out["dlogits"], (T, E), torch.float32, dev, "dlogits")
+    dgate = out.get("dgate")
+    if dgate is not None:
+        _need_on(dgate, (T, k), torch.float32, dev, "dgate")
+    with _On(dev) as s:
+        _check("moe_combine_backward_act8", _lib.moe_combine_backward_act8(
+            _ptr(dout), dt, _ptr(y8), _ptr(y8_scale), _ptr(topk_gate), _ptr(topk_idx),
+            _ptr(token_pos), T, d, k, E, _ptr(out["dy_perm"]), _ptr(out["dlogits"]), _ptr(dgate),
+            s))
+    return out
+
+
+def moe_layer_norm(x: torch.Tensor, weight: torch.Tensor, bias: torch.Tensor | None = None,
+                   eps: float = 1e-5, residual: torch.Tensor | None = None, act8: bool = False,
+                   stats: bool = True, out: dict | None = None) -> dict:
+    """Layer norm over the rows of x [T, d], or of x + residual (see moe.h).
+    Returns a dict: y; with a residual sum (x + residual, the stream); with
+    stats mean and rstd [T] fp32 for the backward; with act8 x8 and x8_scale,
+    the normalised input's 8-bit checkpoint. `out`: a dict of an earlier call
+    with the same arguments, whose tensors are written again."""
+    T, d, dt = _act_matrix(x, "x")
+    dev, f32 = x.device, torch.float32
+    _need_on(weight, (d,), f32, dev, "weight")
+    if bias is not None:
+        _need_on(bias, (d,), f32, dev, "bias")
+    if residual is not None:
+        _need_on(residual, (T, d), x.dtype, dev, "residual")
+    if out is None:
+        out = dict(y=torch.empty((T, d), dtype=x.dtype, device=dev))
+        if residual is not None:
+            out["sum"] = torch.empty((T, d), dtype=x.dtype, device=dev)
+        if stats:
+            out["mean"] = torch.empty(T, dtype=f32, device=dev)
+            out["rstd"] = torch.empty(T, dtype=f32, device=dev)
+        if act8:
+            out["x8"], out["x8_scale"] = _act8_out(T, d, dev, None, None, "x8")
+    else:
+        _need_on(out.get("y"), (T, d), x.dtype, dev, "y")
+        if residual is not None:
+            _need_on(out.get("sum"), (T, d), x.dtype, dev, "sum")
+        if stats:
+            _need_on(out.get("mean"), (T,), f32, dev, "mean")
+            _need_on(out.get("rstd"), (T,), f32, dev, "rstd")
+        if act8:
+            _act8_need(out.get("x8"), out.get("x8_scale"), T, d, dev, "x8")
+    with _On(dev) as s:
+        _check("moe_layer_norm", _lib.moe_layer_norm(
+            _ptr(x), dt, _ptr(residual), _ptr(weight), _ptr(bias), eps, T, d, _ptr(out["y"]),
+            _ptr(out["sum"]) if residual is not None else None,
+            _ptr(out["mean"]) if stats else None, _ptr(out["rstd"]) if stats else None,
+            _ptr(out["x8"]) if act8 else None, _ptr(out["x8_scale"]) if act8 else None, s))
+    return out
+
+
+def moe_layer_norm_backward_workspace_size(dtype: int, T: int, d: int) -> int:
+    return int(_lib.moe_layer_norm_backward_workspace_size(dtype, T, d))
+
+
+def moe_layer_norm_backward(saved: dict, dy: torch.Tensor, weight: torch.Tensor,
+                            dsum: torch.Tensor | None = None, out: dict | None = None,
+                            accumulate_dw: bool = False, want_dweight: bool = True,
+                            want_dbias: bool = True, ws: torch.Tensor | None = None) -> dict:
+    """Backward of moe_layer_norm (see moe.h). saved: mean and rstd, and the
+    normalised input as x or as x8 and x8_scale (x, if both are there).
+    Returns a dict: dx [T, d] (with a residual, its gradient too), dweight and
+    dbias [d] fp32. dsum: the gradient that reaches x (or sum) by its other
+    uses, added to dx. out: tensors of an earlier call; accumulate_dw adds to
+    its dweight and dbias."""
+    T, d, dt = _act_matrix(dy, "dy")
+    dev, f32 = dy.device, torch.float32
+    x = saved.get("x")
+    x8 = x8s = None
+    if x is not None:
+        _need_on(x, (T, d), dy.dtype, dev, "x")
+    else:
+        x8, x8s = saved.get("x8"), saved.get("x8_scale")
+        _act8_need(x8, x8s, T, d, dev, "x8")
+    _need_on(saved.get("mean"), (T,), f32, dev, "mean")
+    _need_on(saved.get("rstd"), (T,), f32, dev, "rstd")
+    _need_on(weight, (d,), f32, dev, "weight")
+    if dsum is not None:
+        _need_on(dsum, (T, d), dy.dtype, dev, "dsum")
+    if out is None:
+        if accumulate_dw:
+            raise ValueError("accumulate_dw needs the gradients of an earlier backward (out)")
+        out = dict(dx=torch.empty((T, d), dtype=dy.dtype, device=dev))
+        if want_dweight:
+            out["dweight"] = torch.empty(d, dtype=f32, device=dev)
+        if want_dbias:
+            out["dbias"] = torch.empty(d, dtype=f32, device=dev)
+    else:
+        _need_on(out.get("dx"), (T, d), dy.dtype, dev, "dx")
+        if want_dweight:
+            _need_on(out.get("dweight"), (d,), f32, dev, "dweight")
+        if want_dbias:
+            _need_on(out.get("dbias"), (d,), f32, dev, "dbias")
+    if want_dweight or want_dbias:
+        wsb = moe_layer_norm_backward_workspace_size(dt, T, d)
+        if ws is None:
+            ws = torch.empty(max(wsb, 16), dtype=torch.uint8, device=dev)
+        _need_bytes(ws, wsb, "ws")
+        if ws.device != dev:
+            raise ValueError(f"ws: expected on {dev}, got {ws.device}")
+    with _On(dev) as s:
+        _check("moe_layer_norm_backward", _lib.moe_layer_norm_backward(
+            _ptr(dy), dt, _ptr(x), _ptr(x8), _ptr(x8s), _ptr(saved["mean"]), _ptr(saved["rstd"]),
+            _ptr(weight), _ptr(dsum), T, d, _ptr(out["dx"]),
+            _ptr(out["dweight"]) if want_dweight else None,
+            _ptr(out["dbias"]) if want_dbias else None, 1 if accumulate_dw else 0, _ptr(ws),
+            ws.numel() if ws is not None else 0, s))
+    return out
+
+
+# ---------------------------------------------------------------------------
 # the layer
 
 
-# Scratch tensors shared by every recomputing layer of one shape: what a
-# layer rebuilds in its backward lives here instead of being held from its
-# forward to its backward.
+# Scratch tensors shared by every recomputing (or 8-bit checkpointing) layer
+# of one shape: what a layer rebuilds in its backward lives here instead of
+# being held from its forward to its backward. Layers may be given a dict of
+# their own instead (their `scratch` argument).
 _SCRATCH: dict = {}
 
 
-def _scratch(name: str, shape, dtype, device) -> torch.Tensor:
+def _scratch(name: str, shape, dtype, device, store: dict | None = None) -> torch.Tensor:
+    store = _SCRATCH if store is None else store
     key = (name, tuple(shape), dtype, str(device))
-    t = _SCRATCH.get(key)
+    t = store.get(key)
     if t is None:
-        t = _SCRATCH[key] = torch.empty(shape, dtype=dtype, device=device)
+        t = store[key] = torch.empty(shape, dtype=dtype, device=device)
     return t
 
 
@@ -638,6 +961,76 @@ class _Balance:
                          dlogits=dlogits, ws=self.ws)
 
 
+class LayerNorm:
+    """A layer norm with its gradient, in front of the layer (y is what the
+    router and the layer take) or behind it (the layers' `out_norm`).
+
+    weight, bias (may be None): [d] fp32. forward(x, residual) normalises x +
+    residual and leaves that stream in `sum`. act8=True holds the normalised
+    input from forward to backward as an 8-bit checkpoint (33/64 of its bf16
+    size), written by the forward's kernel; otherwise the backward reads x (or
+    sum), which the caller must leave as it was. Buffers are allocated once
+    per (T, dtype, device) and reused."""
+
+    def __init__(self, weight: torch.Tensor, bias: torch.Tensor | None = None, eps: float = 1e-5,
+                 act8: bool = False):
+        self.weight, self.bias, self.eps, self.act8 = weight, bias, eps, act8
+        self.sum = None
+        self._key = None
+
+    def forward(self, x: torch.Tensor, residual: torch.Tensor | None = None) -> torch.Tensor:
+        key = (x.shape, x.dtype, x.device, residual is None)
+        if self._key != key:
+            self._out, self._ws, self.grads = None, None, None
+        self._out = moe_layer_norm(x, self.weight, self.bias, self.eps, residual, self.act8,
+                                   out=self._out)
+        self._key = key
+        self.sum = self._out.get("sum")
+        self._x = None if self.act8 else (x if residual is None else self.sum)
+        return self._out["y"]
+
+    def backward(self, dy: torch.Tensor, dsum: torch.Tensor | None = None,
+                 accumulate_dw: bool = False) -> dict:
+        """dict of dx (the gradient of x and of the residual), dweight, dbias.
+        dsum: the gradient that reaches sum by its other uses."""
+        if self._key is None:
+            raise ValueError("backward without a forward")
+        if accumulate_dw and self.grads is None:
+            raise ValueError("accumulate_dw needs the gradients of an earlier backward")
+        if self._ws is None:
+            wsb = moe_layer_norm_backward_workspace_size(_dt(dy), dy.shape[0], dy.shape[-1])
+            self._ws = torch.empty(max(wsb, 16), dtype=torch.uint8, device=dy.device)
+        self.grads = moe_layer_norm_backward(dict(self._out, x=self._x), dy, self.weight, dsum,
+                                             out=self.grads, accumulate_dw=accumulate_dw,
+                                             want_dbias=self.bias is not None, ws=self._ws)
+        return self.grads
+
+    def held_bytes(self) -> int:
+        """Bytes held from forward to backward (x, or sum, is the caller's)."""
+        o = self._out
+        return _nbytes([o["mean"], o["rstd"], o.get("x8"), o.get("x8_scale")])
+
+
+def _norm_backward(norm, dout, accumulate_dw):
+    """dout taken back through a layer's out_norm."""
+    if norm is None:
+        return dout
+    return norm.backward(dout, accumulate_dw=accumulate_dw)["dx"]
+
+
+def _norm_grads(norm, grads):
+    if norm is not None:
+        grads["dnorm_weight"], grads["dnorm_bias"] = norm.grads["dweight"], norm.grads.get("dbias")
+    return grads
+
+
+def _act8_buffers(R, d, h, dev):
+    """The checkpoints that a layer holds: of A||B and of y_perm."""
+    ab8, ab8_scale = _act8_out(R, 2 * h, dev, None, None, "ab8")
+    y8, y8_scale = _act8_out(R, d, dev, None, None, "y8")
+    return dict(ab8=ab8, ab8_scale=ab8_scale, y8=y8, y8_scale=y8_scale)
+
+
 class MoELayer:
     """Forward and backward of the MoE expert layer through the C ABI.
 
@@ -654,14 +1047,33 @@ class MoELayer:
 
     aux_alpha adds the balancing loss of moe_load_balance: its statistics
     are in `lb_stats` (device) after forward, and backward adds its
-    gradient to dlogits."""
+    gradient to dlogits.
+
+    act8=True holds 8-bit checkpoints (moe_act8_store) of A||B and y_perm and
+    the routing metadata, nothing else: the backward dispatches x again,
+    rebuilds A||B and H' from the checkpoint and reads y_perm's in the combine
+    backward. The output is the plain layer's; the gradients are those of the
+    rounded A||B and y_perm. x must be unchanged until the backward (as with
+    recompute).
+
+    What recompute and act8 rebuild lives in scratch shared by all such layers
+    of a shape in the process. Layers whose work may overlap in time (on
+    different streams, in graphs replayed side by side) need `scratch` dicts
+    of their own; layers that run one after the other may share one.
+
+    out_norm: a LayerNorm applied to the layer's output; the backward's dict
+    then has dnorm_weight and dnorm_bias."""
 
     def __init__(self, w1: torch.Tensor, w2: torch.Tensor, k: int, recompute: bool = False,
-                 aux_alpha: float | None = None):
+                 aux_alpha: float | None = None, act8: bool = False,
+                 scratch: dict | None = None, out_norm: LayerNorm | None = None):
+        if recompute and act8:
+            raise ValueError("recompute and act8 exclude each other")
         self.w1, self.w2, self.k = w1, w2, k
         self.E, h2, self.d = w1.shape
         self.h = h2 // 2
-        self.recompute = recompute
+        self.recompute, self.act8 = recompute, act8
+        self.scratch, self.out_norm = scratch, out_norm
         self.balance = _Balance(aux_alpha) if aux_alpha is not None else None
         self.lb_stats = None
         self._T = None
@@ -692,11 +1104,13 @@ class MoELayer:
         self.route_ws = torch.empty(max(moe_route_workspace_size(T, E, k), 1), dtype=torch.uint8,
                                     device=dev)
         own = (lambda name, shape: torch.empty(shape, dtype=dt, device=dev))
-        tmp = (lambda name, shape: _scratch(name, shape, dt, dev)) if self.recompute else own
+        tmp = ((lambda name, shape: _scratch(name, shape, dt, dev, self.scratch))
+               if self.recompute or self.act8 else own)
         self.x_perm = tmp("x_perm", (R, d))
         self.ab = tmp("ab", (R, 2 * h))
         self.hp = tmp("hp", (R, h))
-        self.y_perm = own("y_perm", (R, d))
+        self.y_perm = (tmp if self.act8 else own)("y_perm", (R, d))
+        self.ckpt = _act8_buffers(R, d, h, dev) if self.act8 else None
         self.out = torch.empty((T, d), dtype=dt, device=dev)
         self.grads = None
         self._T = key
@@ -715,9 +1129,15 @@ class MoELayer:
             self.lb_stats = self.balance.forward(logits, r["counts"], self.k)
         moe_permute(x, r["token_pos"], self.x_perm)
         self._gemm1(r["offsets"])
+        if self.act8:
+            moe_act8_store(self.ab, self.ckpt["ab8"], self.ckpt["ab8_scale"])
         moe_grouped_gemm(MOE_GG_FWD, self.hp, self.w2, self.y_perm, r["offsets"], N=d, K=self.h)
-        moe_combine(self.y_perm, r["topk_gate"], r["token_pos"], self.out)
-        return self.out
+        if self.act8:
+            moe_combine_act8(self.y_perm, r["topk_gate"], r["token_pos"], self.out,
+                             self.ckpt["y8"], self.ckpt["y8_scale"])
+        else:
+            moe_combine(self.y_perm, r["topk_gate"], r["token_pos"], self.out)
+        return self.out if self.out_norm is None else self.out_norm.forward(self.out)
 
     def saved(self) -> dict:
         r = self.route
@@ -730,6 +1150,10 @@ class MoELayer:
         backward (the input x and the weights are the caller's)."""
         r = self.route
         meta = _nbytes(r.values())
+        if self.out_norm is not None:
+            meta += self.out_norm.held_bytes() + (0 if self.out_norm.act8 else _nbytes([self.out]))
+        if self.act8:
+            return meta + _nbytes(self.ckpt.values())
         if self.recompute:
             return meta + _nbytes([self.y_perm])
         return meta + _nbytes([self.x_perm, self.ab, self.hp, self.y_perm])
@@ -741,17 +1165,19 @@ class MoELayer:
         stage_events: optional recorded torch.cuda.Event per backward stage
         (moe_bwd_desc.stage_events)."""
         _need(dout, tuple(self.x.shape), self.x.dtype, "dout")
-        if self.recompute:
-            moe_permute(self.x, self.route["token_pos"], self.x_perm)
-            self._gemm1(self.route["offsets"])
         if accumulate_dw and self.grads is None:
             raise ValueError("accumulate_dw needs the gradients of an earlier backward")
+        dout = _norm_backward(self.out_norm, dout, accumulate_dw)
+        if self.recompute or self.act8:
+            moe_permute(self.x, self.route["token_pos"], self.x_perm)
+        if self.recompute:
+            self._gemm1(self.route["offsets"])
         self.grads = moe_backward(self.saved(), dout, self.E, self.k, self.d, self.h,
                                   out=self.grads, accumulate_dw=accumulate_dw,
-                                  stage_events=stage_events)
+                                  stage_events=stage_events, act8=self.ckpt)
         if self.balance is not None:
             self.balance.backward(self.grads["dlogits"])
-        return self.grads
+        return _norm_grads(self.out_norm, self.grads)
 
 
 class MoELayerPadded(MoELayer):
@@ -827,14 +1253,22 @@ class MoELayerMX:
     gradient (fuse_hp; with fuse_hp = False GEMM1 writes bf16 H' and a
     separate pass quantises it: the same bytes); y and out stay
     bf16. The backward (moe_backward with MXFP8) quantises its own GEMM
-    operands."""
+    operands.
+
+    act8, scratch and out_norm as in MoELayer: with act8 the layer holds
+    checkpoints of A||B and y_perm in their place (H' is held in MXFP8 along
+    rows either way)."""
 
     def __init__(self, w1_master: torch.Tensor, w2_master: torch.Tensor, k: int,
-                 recompute: bool = False, aux_alpha: float | None = None):
+                 recompute: bool = False, aux_alpha: float | None = None, act8: bool = False,
+                 scratch: dict | None = None, out_norm: LayerNorm | None = None):
+        if recompute and act8:
+            raise ValueError("recompute and act8 exclude each other")
         self.E, h2, self.d = w1_master.shape
         self.h = h2 // 2
         self.k = k
-        self.recompute = recompute
+        self.recompute, self.act8 = recompute, act8
+        self.scratch, self.out_norm = scratch, out_norm
         self.fuse_hp = True
         self.balance = _Balance(aux_alpha) if aux_alpha is not None else None
         self.lb_stats = None
@@ -869,17 +1303,18 @@ class MoELayerMX:
                           sorted_slot=torch.empty(R, **i32), tile_offsets=torch.empty(E + 1, **i32))
         self.route_ws = torch.empty(max(moe_route_workspace_size(T, E, k), 1), **u8)
         # dispatch payload, A||B, H' and its MXFP8 copy: scratch when recomputing
-        tmp = ((lambda name, shape, dt: _scratch("mx_" + name, shape, dt, dev)) if self.recompute
+        shared = lambda name, shape, dt: _scratch("mx_" + name, shape, dt, dev, self.scratch)
+        tmp = (shared if self.recompute
                else (lambda name, shape, dt: torch.empty(shape, dtype=dt, device=dev)))
         self.xq = tmp("xq", (T, d), torch.uint8)
         self.xs = tmp("xs", (T, d // 32), torch.uint8)
         self.xpq = tmp("xpq", (R, d), torch.uint8)
         self.xps = tmp("xps", (R, d // 32), torch.uint8)
-        self.ab = tmp("ab", (R, 2 * h), torch.bfloat16)
+        self.ab = (shared if self.act8 else tmp)("ab", (R, 2 * h), torch.bfloat16)
         # H' and its GEMM2 operand are read in the forward only
-        self.hp = _scratch("mx_hp", (R, h), torch.bfloat16, dev)
-        self.hpq = _scratch("mx_hpq", (R, h), torch.uint8, dev)
-        self.hps = _scratch("mx_hps", (R, h // 32), torch.uint8, dev)
+        self.hp = shared("hp", (R, h), torch.bfloat16)
+        self.hpq = shared("hpq", (R, h), torch.uint8)
+        self.hps = shared("hps", (R, h // 32), torch.uint8)
         # H' along rows per expert (GEMM2 wgrad's operand), written by GEMM1
         # with GEMM2's; held instead of bf16 H' (when recomputing, the backward
         # quantises the H' it recomputes and these are scratch)
@@ -888,9 +1323,11 @@ class MoELayerMX:
             self.hpc = torch.empty(nb * 32 * h, **u8)
             self.hpcs = torch.empty(nb * h, **u8)
         else:
-            self.hpc = _scratch("mx_hpc", (nb * 32 * h,), torch.uint8, dev)
-            self.hpcs = _scratch("mx_hpcs", (nb * h,), torch.uint8, dev)
-        self.y_perm = torch.empty((R, d), **bf)
+            self.hpc = shared("hpc", (nb * 32 * h,), torch.uint8)
+            self.hpcs = shared("hpcs", (nb * h,), torch.uint8)
+        self.y_perm = (shared("y_perm", (R, d), torch.bfloat16) if self.act8
+                       else torch.empty((R, d), **bf))
+        self.ckpt = _act8_buffers(R, d, h, dev) if self.act8 else None
         self.out = torch.empty((T, d), **bf)
         self.grads = None
         self.bwd_ws = None
@@ -929,12 +1366,18 @@ class MoELayerMX:
             self.lb_stats = self.balance.forward(logits, r["counts"], self.k)
         fused = self.hp_quantised_in_gemm1()
         self._gemm1(x, r["offsets"], r["token_pos"], quantised_hp=fused)
+        if self.act8:
+            moe_act8_store(self.ab, self.ckpt["ab8"], self.ckpt["ab8_scale"])
         if not fused:
             self.quantize_hp(r["offsets"])
         moe_grouped_gemm(MOE_GG_FWD, self.hpq, self.w2q, self.y_perm, r["offsets"], N=d, K=h,
                          a_scale=self.hps, b_scale=self.w2s, dtype=MOE_MXFP8)
-        moe_combine(self.y_perm, r["topk_gate"], r["token_pos"], self.out)
-        return self.out
+        if self.act8:
+            moe_combine_act8(self.y_perm, r["topk_gate"], r["token_pos"], self.out,
+                             self.ckpt["y8"], self.ckpt["y8_scale"])
+        else:
+            moe_combine(self.y_perm, r["topk_gate"], r["token_pos"], self.out)
+        return self.out if self.out_norm is None else self.out_norm.forward(self.out)
 
     def quantize_hp(self, offsets):
         """H' along h for GEMM2 and, unless recomputing (the backward then
@@ -959,6 +1402,10 @@ class MoELayerMX:
         """Bytes of activations held from forward to backward (x and the
         weights are the caller's)."""
         meta = _nbytes(self.route.values())
+        if self.out_norm is not None:
+            meta += self.out_norm.held_bytes() + (0 if self.out_norm.act8 else _nbytes([self.out]))
+        if self.act8:
+            return meta + _nbytes([self.hpc, self.hpcs, *self.ckpt.values()])
         if self.recompute:
             return meta + _nbytes([self.y_perm])
         return meta + _nbytes([self.ab, self.hpc, self.hpcs, self.y_perm])
@@ -968,13 +1415,14 @@ class MoELayerMX:
         """accumulate_dw: add this micro-batch's dW1, dW2 to the ones already
         in self.grads. stage_events: as MoELayer.backward."""
         _need(dout, tuple(self.x.shape), torch.bfloat16, "dout")
-        if self.recompute:
-            self._gemm1(self.x, self.route["offsets"], self.route["token_pos"])
         if accumulate_dw and self.grads is None:
             raise ValueError("accumulate_dw needs the gradients of an earlier backward")
+        dout = _norm_backward(self.out_norm, dout, accumulate_dw)
+        if self.recompute:
+            self._gemm1(self.x, self.route["offsets"], self.route["token_pos"])
         self.grads = moe_backward(self.saved(), dout, self.E, self.k, self.d, self.h,
                                   out=self.grads, mxfp8=True, accumulate_dw=accumulate_dw,
-                                  stage_events=stage_events)
+                                  stage_events=stage_events, act8=self.ckpt)
         if self.balance is not None:
             self.balance.backward(self.grads["dlogits"])
-        return self.grads
+        return _norm_grads(self.out_norm, self.grads)

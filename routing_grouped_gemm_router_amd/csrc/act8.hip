@@ -1,0 +1,297 @@
+// act8.hip -- 8-bit activation checkpoints (MXINT8, act8.h) and their use in
+// the layer's backward pass.
+//
+// The layer's activations between forward and backward are what limits the
+// batch (kongchang.com, "where the costs are": recomputing them saves about
+// two thirds of that memory for about a fifth of the throughput). Kept in 8
+// bits they take 33/64 of their bf16 size and nothing is computed twice but
+// H' = silu(a) b, which follows from A||B. All kernels are bound by memory:
+// each reads its inputs once and writes its outputs once.
+#include "act8.h"
+
+namespace moe {
+
+// store: q, scale = checkpoint of in. Blocks of 32 lie in rows of a multiple
+// of 32, so the matrix is one run of blocks.
+template <bool BF16>
+__global__ __launch_bounds__(256) void act8_store_vecs(const uint4 *__restrict__ in, int64_t n_vec,
+                                                       typename Codes<BF16>::type *__restrict__ q,
+                                                       uint8_t *__restrict__ scale) {
+    typedef Row16<BF16> R;
+    const int64_t v = (int64_t)blockIdx.x * 256 + threadIdx.x;
+    if (v >= n_vec) return;                       // whole blocks of 32: n_vec % LPB == 0
+    const uint4 w = in[v];
+    const uint32_t sb = act8_scale_byte<BF16>(w);
+    float f[R::N];
+    R::unpack(w, f);
+    typename Codes<BF16>::type c;
+    act8_encode(f, sb, c);
+    q[v] = c;
+    if (v % R::LPB == 0) scale[v / R::LPB] = (uint8_t)sb;
+}
+
+// load: the values a checkpoint stands for
+template <bool BF16>
+__global__ __launch_bounds__(256) void act8_load_vecs(const typename Codes<BF16>::type *__restrict__ q,
+                                                      const uint8_t *__restrict__ scale,
+                                                      int64_t n_vec, uint4 *__restrict__ out) {
+    typedef Row16<BF16> R;
+    const int64_t v = (int64_t)blockIdx.x * 256 + threadIdx.x;
+    if (v >= n_vec) return;
+    float f[R::N];
+    act8_decode(q[v], act8_step(scale[v / R::LPB]), f);
+    out[v] = R::pack(f);
+}
+
+// silu(a) = a sigmoid(a), from E = exp(-|a| / 2): E^2 / (1 + E^2) for a < 0,
+// 1 / (1 + E^2) otherwise. exp(-a) itself would overflow below a = -88 and
+// lose the product a exp(a) where it is still a normal number.
+MOE_DEV float silu(float a) {
+    const float e = expf(-0.5f * fabsf(a));
+    return (a < 0.f ? (a * e) * e : a) / fmaf(e, e, 1.f);
+}
+
+// A||B and H' = silu(a) b from the checkpoint of A||B [rows, 2h]; hv = vectors of h
+template <bool BF16>
+__global__ __launch_bounds__(256) void act8_swiglu_vecs(const typename Codes<BF16>::type *__restrict__ q,
+                                                        const uint8_t *__restrict__ scale,
+                                                        int64_t n_vec, int hv,
+                                                        uint4 *__restrict__ ab,
+                                                        uint4 *__restrict__ hp) {
+    typedef Row16<BF16> R;
+    const int64_t v = (int64_t)blockIdx.x * 256 + threadIdx.x;
+    if (v >= n_vec) return;
+    const int64_t row = v / hv;
+    const int64_t va = v + row * hv, vb = va + hv;      // row * 2 hv + column
+    float a[R::N], b[R::N], y[R::N];
+    act8_decode(q[va], act8_step(scale[va / R::LPB]), a);
+    act8_decode(q[vb], act8_step(scale[vb / R::LPB]), b);
+    ab[va] = R::pack(a);
+    ab[vb] = R::pack(b);
+#pragma unroll
+    for (int i = 0; i < R::N; i++) y[i] = silu(a[i]) * b[i];
+    hp[v] = R::pack(y);
+}
+
+// combine that keeps the experts' rows: out[t] = sum_j g[t,j] y[token_pos[t,j]]
+// (fp32 sum, ascending j) and the checkpoint of every row it reads. One wave
+// per token.
+template <bool BF16>
+__global__ __launch_bounds__(256) void combine_act8_rows(
+    const uint4 *__restrict__ y, const float *__restrict__ gate,
+    const int32_t *__restrict__ token_pos, int64_t T, int nv, int k, uint4 *__restrict__ out,
+    typename Codes<BF16>::type *__restrict__ y8, uint8_t *__restrict__ y8_scale) {
+    typedef Row16<BF16> R;
+    const int lane = threadIdx.x & 63;
+    const int64_t t = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6);
+    if (t >= T) return;
+    for (int c = lane; c < nv; c += 64) {
+        float acc[R::N];
+#pragma unroll
+        for (int i = 0; i < R::N; i++) acc[i] = 0.f;
+        for (int j = 0; j < k; j++) {
+            const int32_t p = token_pos[t * k + j];
+            if (p < 0) continue;                       // dropped row
+            const float g = gate[t * k + j];
+            const int64_t v = (int64_t)p * nv + c;
+            const uint4 w = y[v];
+            const uint32_t sb = act8_scale_byte<BF16>(w);
+            float f[R::N];
+            R::unpack(w, f);
+            typename Codes<BF16>::type q;
+            act8_encode(f, sb, q);
+            y8[v] = q;
+            if (c % R::LPB == 0) y8_scale[v / R::LPB] = (uint8_t)sb;
+#pragma unroll
+            for (int i = 0; i < R::N; i++) acc[i] = fmaf(g, f[i], acc[i]);
+        }
+        out[t * nv + c] = R::pack(acc);
+    }
+}
+
+// combine backward with the router backward, the experts' rows read from
+// their checkpoint:
+//   dg_j = <dOut[t], y8[p_j]>,  dy_perm[p_j] = round(g_j dOut[t]),
+//   dlogits[t, e_j] = g_j sum_i g_i (dg_j - dg_i), 0 for unselected experts
+// (the gates sum to one; this form has no cancellation between large terms).
+template <bool BF16, int KMAX>
+__global__ __launch_bounds__(256) void combine_bwd_act8_rows(
+    const uint4 *__restrict__ dout, const typename Codes<BF16>::type *__restrict__ y8,
+    const uint8_t *__restrict__ y8_scale, const float *__restrict__ gate,
+    const int32_t *__restrict__ topk_idx, const int32_t *__restrict__ token_pos, int64_t T, int nv,
+    int k, int E, uint4 *__restrict__ dy, float *__restrict__ row_gate,
+    float *__restrict__ dlogits, float *__restrict__ dgate) {
+    typedef Row16<BF16> R;
+    const int lane = threadIdx.x & 63;
+    const int64_t t = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6);
+    if (t >= T) return;
+    int32_t pos[KMAX], ex[KMAX];
+    float g[KMAX], dot[KMAX];
+#pragma unroll
+    for (int j = 0; j < KMAX; j++) {
+        pos[j] = j < k ? token_pos[t * k + j] : -1;
+        ex[j] = j < k ? topk_idx[t * k + j] : -1;
+        g[j] = j < k ? gate[t * k + j] : 0.f;
+        dot[j] = 0.f;
+    }
+    for (int c = lane; c < nv; c += 64) {
+        float fo[R::N];
+        R::unpack(dout[t * nv + c], fo);
+#pragma unroll
+        for (int j = 0; j < KMAX; j++) {
+            if (pos[j] < 0) continue;
+            const int64_t v = (int64_t)pos[j] * nv + c;
+            float fy[R::N], fd[R::N];
+            act8_decode(y8[v], act8_step(y8_scale[v / R::LPB]), fy);
+#pragma unroll
+            for (int i = 0; i < R::N; i++) {
+                dot[j] = fmaf(fo[i], fy[i], dot[j]);
+                fd[i] = g[j] * fo[i];
+            }
+            if (dy) dy[v] = R::pack(fd);
+        }
+    }
+#pragma unroll
+    for (int j = 0; j < KMAX; j++) {
+        dot[j] = wave_sum(dot[j]);
+        if (pos[j] < 0) dot[j] = 0.f;   // dropped row: its gate had no effect
+    }
+    float rg[KMAX];
+#pragma unroll
+    for (int j = 0; j < KMAX; j++) {
+        float s = 0.f;
+#pragma unroll
+        for (int i = 0; i < KMAX; i++) s = fmaf(g[i], dot[j] - dot[i], s);
+        rg[j] = g[j] * s;
+    }
+    for (int e = lane; e < E; e += 64) {
+        float v = 0.f;
+#pragma unroll
+        for (int j = 0; j < KMAX; j++)
+            if (ex[j] == e) v = rg[j];
+        dlogits[t * E + e] = v;
+    }
+    if (lane == 0) {
+#pragma unroll
+        for (int j = 0; j < KMAX; j++) {
+            if (dgate && j < k) dgate[t * k + j] = dot[j];
+            if (row_gate && pos[j] >= 0) row_gate[pos[j]] = g[j];
+        }
+    }
+}
+
+// ---------------------------------------------------------------------------
+// launchers
+
+moe_status act8_store_launch(const void *in, moe_dtype dt, int64_t rows, int64_t cols, uint8_t *q,
+                             uint8_t *scale, hipStream_t s) {
+    const bool bf = dt == MOE_BF16;
+    const int64_t n_vec = rows * (cols / (bf ? 8 : 4));
+    for (int64_t at = 0; at < n_vec; at += kMaxBlocks * 256) {
+        const int64_t n = n_vec - at < kMaxBlocks * 256 ? n_vec - at : kMaxBlocks * 256;
+        const unsigned nb = (unsigned)((n + 255) / 256);
+        const uint4 *src = reinterpret_cast<const uint4 *>(in) + at;
+        if (bf)
+            act8_store_vecs<true><<<nb, 256, 0, s>>>(src, n, reinterpret_cast<uint2 *>(q) + at,
+                                                     scale + at / 4);
+        else
+            act8_store_vecs<false><<<nb, 256, 0, s>>>(src, n, reinterpret_cast<uint32_t *>(q) + at,
+                                                      scale + at / 8);
+    }
+    return launch_status();
+}
+
+moe_status act8_load_launch(const uint8_t *q, const uint8_t *scale, moe_dtype dt, int64_t rows,
+                            int64_t cols, void *out, hipStream_t s) {
+    const bool bf = dt == MOE_BF16;
+    const int64_t n_vec = rows * (cols / (bf ? 8 : 4));
+    for (int64_t at = 0; at < n_vec; at += kMaxBlocks * 256) {
+        const int64_t n = n_vec - at < kMaxBlocks * 256 ? n_vec - at : kMaxBlocks * 256;
+        const unsigned nb = (unsigned)((n + 255) / 256);
+        uint4 *dst = reinterpret_cast<uint4 *>(out) + at;
+        if (bf)
+            act8_load_vecs<true><<<nb, 256, 0, s>>>(reinterpret_cast<const uint2 *>(q) + at,
+                                                    scale + at / 4, n, dst);
+        else
+            act8_load_vecs<false><<<nb, 256, 0, s>>>(reinterpret_cast<const uint32_t *>(q) + at,
+                                                     scale + at / 8, n, dst);
+    }
+    return launch_status();
+}
+
+moe_status act8_swiglu_launch(const uint8_t *q, const uint8_t *scale, moe_dtype dt, int64_t rows,
+                              int h, void *ab, void *hp, hipStream_t s) {
+    const bool bf = dt == MOE_BF16;
+    const int hv = h / (bf ? 8 : 4);
+    const int64_t step = kMaxBlocks * 256 / hv;        // rows of a launch
+    for (int64_t r = 0; r < rows; r += step) {
+        const int64_t n = (rows - r < step ? rows - r : step) * hv;
+        const unsigned nb = (unsigned)((n + 255) / 256);
+        uint4 *a = reinterpret_cast<uint4 *>(ab) + r * 2 * hv, *y = reinterpret_cast<uint4 *>(hp) + r * hv;
+        const uint8_t *qq = q + r * 2 * h, *ss = scale + r * 2 * h / 32;
+        if (bf)
+            act8_swiglu_vecs<true><<<nb, 256, 0, s>>>(reinterpret_cast<const uint2 *>(qq), ss, n, hv, a, y);
+        else
+            act8_swiglu_vecs<false><<<nb, 256, 0, s>>>(reinterpret_cast<const uint32_t *>(qq), ss, n, hv, a, y);
+    }
+    return launch_status();
+}
+
+constexpr int64_t kTokensALaunch = kMaxBlocks * 4;    // four tokens a workgroup
+
+moe_status combine_act8_launch(const void *y, moe_dtype dt, const float *gate,
+                               const int32_t *token_pos, int64_t T, int d, int k, void *out,
+                               uint8_t *y8, uint8_t *y8_scale, hipStream_t s) {
+    const bool bf = dt == MOE_BF16;
+    const int nv = d / (bf ? 8 : 4);
+    const uint4 *yy = reinterpret_cast<const uint4 *>(y);
+    for (int64_t t = 0; t < T; t += kTokensALaunch) {
+        const int64_t n = T - t < kTokensALaunch ? T - t : kTokensALaunch;
+        const unsigned nb = (unsigned)((n + 3) / 4);
+        uint4 *oo = reinterpret_cast<uint4 *>(out) + t * nv;
+        const float *g = gate + t * k;
+        const int32_t *tp = token_pos + t * k;
+        if (bf)
+            combine_act8_rows<true><<<nb, 256, 0, s>>>(yy, g, tp, n, nv, k, oo,
+                                                       reinterpret_cast<uint2 *>(y8), y8_scale);
+        else
+            combine_act8_rows<false><<<nb, 256, 0, s>>>(yy, g, tp, n, nv, k, oo,
+                                                        reinterpret_cast<uint32_t *>(y8), y8_scale);
+    }
+    return launch_status();
+}
+
+#define ACT8_KSWITCH(k, F) \
+    ((k) <= 1 ? F(1) : (k) <= 2 ? F(2) : (k) <= 4 ? F(4) : F(8))
+
+// Exactly one of dy (the rows of dy_perm) and row_gate (each routed row's
+// gate, fp32) is given.
+moe_status combine_bwd_act8_launch(const void *dout, moe_dtype dt, const uint8_t *y8,
+                                   const uint8_t *y8_scale, const float *gate,
+                                   const int32_t *topk_idx, const int32_t *token_pos, int64_t T,
+                                   int d, int k, int E, void *dy, float *row_gate, float *dlogits,
+                                   float *dgate, hipStream_t s) {
+    const bool bf = dt == MOE_BF16;
+    const int nv = d / (bf ? 8 : 4);
+    uint4 *oo = reinterpret_cast<uint4 *>(dy);
+    for (int64_t t = 0; t < T; t += kTokensALaunch) {
+        const int64_t n = T - t < kTokensALaunch ? T - t : kTokensALaunch;
+        const unsigned nb = (unsigned)((n + 3) / 4);
+        const uint4 *dd = reinterpret_cast<const uint4 *>(dout) + t * nv;
+        const float *g = gate + t * k;
+        const int32_t *ti = topk_idx + t * k, *tp = token_pos + t * k;
+        float *dl = dlogits + t * E, *dg = dgate ? dgate + t * k : nullptr;
+#define L(K)                                                                                      \
+    (bf ? (combine_bwd_act8_rows<true, K><<<nb, 256, 0, s>>>(                                     \
+               dd, reinterpret_cast<const uint2 *>(y8), y8_scale, g, ti, tp, n, nv, k, E, oo,     \
+               row_gate, dl, dg), 0)                                                              \
+        : (combine_bwd_act8_rows<false, K><<<nb, 256, 0, s>>>(                                    \
+               dd, reinterpret_cast<const uint32_t *>(y8), y8_scale, g, ti, tp, n, nv, k, E, oo,  \
+               row_gate, dl, dg), 0))
+        ACT8_KSWITCH(k, L);
+#undef L
+    }
+    return launch_status();
+}
+
+}  // namespace moe

@@ -49,6 +49,31 @@ moe_status load_balance_launch(const float *logits, const int32_t *counts, int64
                                float alpha, float *stats, float *dlogits, void *ws, hipStream_t s);
 size_t load_balance_ws_bytes(int64_t T, int E);
 
+moe_status act8_store_launch(const void *in, moe_dtype dt, int64_t rows, int64_t cols, uint8_t *q,
+                             uint8_t *scale, hipStream_t s);
+moe_status act8_load_launch(const uint8_t *q, const uint8_t *scale, moe_dtype dt, int64_t rows,
+                            int64_t cols, void *out, hipStream_t s);
+moe_status act8_swiglu_launch(const uint8_t *q, const uint8_t *scale, moe_dtype dt, int64_t rows,
+                              int h, void *ab, void *hp, hipStream_t s);
+moe_status combine_act8_launch(const void *y, moe_dtype dt, const float *gate,
+                               const int32_t *token_pos, int64_t T, int d, int k, void *out,
+                               uint8_t *y8, uint8_t *y8_scale, hipStream_t s);
+moe_status combine_bwd_act8_launch(const void *dout, moe_dtype dt, const uint8_t *y8,
+                                   const uint8_t *y8_scale, const float *gate,
+                                   const int32_t *topk_idx, const int32_t *token_pos, int64_t T,
+                                   int d, int k, int E, void *dy, float *row_gate, float *dlogits,
+                                   float *dgate, hipStream_t s);
+moe_status norm_fwd_launch(const void *x, moe_dtype dt, const void *res, const float *gamma,
+                           const float *beta, float eps, int64_t T, int d, void *y, void *sum,
+                           float *mean, float *rstd, uint8_t *x8, uint8_t *x8_scale,
+                           hipStream_t s);
+size_t norm_bwd_ws_bytes(moe_dtype dt, int64_t T, int d);
+moe_status norm_bwd_launch(const void *dy, moe_dtype dt, const void *x, const uint8_t *x8,
+                           const uint8_t *x8_scale, const float *mean, const float *rstd,
+                           const float *gamma, const void *dsum, int64_t T, int d, void *dx,
+                           float *dgamma, float *dbeta, bool accumulate, float *part,
+                           hipStream_t s);
+
 // Queried at every launch (a host-side lookup in the runtime, no device
 // work), so the library holds no mutable state for it.
 int num_cus() {
@@ -307,30 +332,49 @@ moe_status moe_backward_workspace_layout(const moe_bwd_desc *b, moe_bwd_ws_layou
     return MOE_OK;
 }
 
-static moe_status backward_mxfp8(const moe_bwd_desc *b, hipStream_t s);
+// The 8-bit checkpoints of moe_backward_act8: null pointers fail as any other
+// missing input does, before anything is enqueued.
+static moe_status check_act8(const moe_act8_saved *c) {
+    if (!c->ab8 || !c->ab8_scale || !c->y8 || !c->y8_scale) return MOE_ERR_NULL;
+    return aligned16(c->ab8) && aligned16(c->y8) ? MOE_OK : MOE_ERR_ALIGN;
+}
 
-moe_status moe_backward(const moe_bwd_desc *b, void *stream) {
+static moe_status backward_mxfp8(const moe_bwd_desc *b, const moe_act8_saved *c, hipStream_t s);
+
+// c: the checkpoints that stand for ab, hp and y_perm (null = none)
+static moe_status backward(const moe_bwd_desc *b, const moe_act8_saved *c, hipStream_t s) {
     if (!b) return MOE_ERR_NULL;
-    if (b->dtype == MOE_MXFP8) return backward_mxfp8(b, (hipStream_t)stream);
+    if (b->dtype == MOE_MXFP8) return backward_mxfp8(b, c, s);
     if (b->dtype != MOE_F32 && b->dtype != MOE_BF16) return MOE_ERR_DTYPE;
     if (b->accumulate_dw != 0 && b->accumulate_dw != 1) return MOE_ERR_DTYPE;
     if (!routing_shape_ok(b->T, b->E, b->k) || !width_ok(b->d) || !hidden_ok(b->h))
         return MOE_ERR_SHAPE;
     if (!b->dw1 || !b->dw2 || !b->offsets || !b->w1 || !b->w2) return MOE_ERR_NULL;
     const bool any = b->T > 0;
-    if (any && (!b->x_perm || !b->ab || !b->hp || !b->y_perm || !b->topk_gate || !b->topk_idx ||
-                !b->token_pos || !b->dout || !b->dx || !b->dlogits || !b->dy_perm || !b->dab ||
+    if (any && (!b->x_perm || !b->ab || !b->hp || (!c && !b->y_perm) || !b->topk_gate ||
+                !b->topk_idx || !b->token_pos || !b->dout || !b->dx || !b->dlogits || !b->dy_perm || !b->dab ||
                 !b->dx_perm))
         return MOE_ERR_NULL;
     const void *al[] = {b->x_perm, b->ab, b->hp, b->y_perm, b->w1, b->w2, b->dout, b->dx,
                         b->dw1, b->dw2, b->dy_perm, b->dab, b->dx_perm};
     for (const void *p : al)
         if (p && !aligned16(p)) return MOE_ERR_ALIGN;
-    hipStream_t s = (hipStream_t)stream;
     const int64_t R = b->T * b->k;
-    moe_status st = combine_bwd_launch(b->dout, b->y_perm, b->dtype, b->topk_gate, b->topk_idx,
-                                       b->token_pos, b->T, b->d, b->k, b->E, b->dy_perm,
-                                       b->dlogits, b->dgate, s);
+    moe_status st;
+    if (c && any && (st = check_act8(c)) != MOE_OK) return st;
+    if (!c)
+        st = combine_bwd_launch(b->dout, b->y_perm, b->dtype, b->topk_gate, b->topk_idx,
+                                b->token_pos, b->T, b->d, b->k, b->E, b->dy_perm, b->dlogits,
+                                b->dgate, s);
+    else if (any) {
+        st = combine_bwd_act8_launch(b->dout, b->dtype, c->y8, c->y8_scale, b->topk_gate,
+                                     b->topk_idx, b->token_pos, b->T, b->d, b->k, b->E, b->dy_perm,
+                                     nullptr, b->dlogits, b->dgate, s);
+        if (st == MOE_OK)
+            st = act8_swiglu_launch(c->ab8, c->ab8_scale, b->dtype, R, b->h,
+                                    const_cast<void *>(b->ab), const_cast<void *>(b->hp), s);
+    } else
+        st = MOE_OK;
     if (st != MOE_OK || (st = stage_mark(b, 0, s)) != MOE_OK) return st;
     moe_gemm_desc g;
     memset(&g, 0, sizeof(g));
@@ -369,7 +413,7 @@ moe_status moe_backward(const moe_bwd_desc *b, void *stream) {
     return stage_mark(b, 5, s);
 }
 
-static moe_status backward_mxfp8(const moe_bwd_desc *b, hipStream_t s) {
+static moe_status backward_mxfp8(const moe_bwd_desc *b, const moe_act8_saved *c, hipStream_t s) {
     if (b->accumulate_dw != 0 && b->accumulate_dw != 1) return MOE_ERR_DTYPE;
     if (!routing_shape_ok(b->T, b->E, b->k) || !width_ok(b->d) || !hidden_ok(b->h) ||
         b->d % 128 || b->h % 128)
@@ -382,8 +426,8 @@ static moe_status backward_mxfp8(const moe_bwd_desc *b, hipStream_t s) {
         return MOE_ERR_NULL;
     const bool any = b->T > 0;
     if (!b->hp_cols != !b->hp_cols_scale) return MOE_ERR_NULL;
-    if (any && (!b->x || !b->sorted_token || !b->ab || (!b->hp && !b->hp_cols) || !b->y_perm || !b->topk_gate ||
-                !b->topk_idx || !b->token_pos || !b->dout || !b->dx || !b->dlogits ||
+    if (any && (!b->x || !b->sorted_token || !b->ab || (!b->hp && !b->hp_cols) || (!c && !b->y_perm) ||
+                !b->topk_gate || !b->topk_idx || !b->token_pos || !b->dout || !b->dx || !b->dlogits ||
                 !b->dy_perm || !b->dab || !b->dx_perm || !b->ws))
         return MOE_ERR_NULL;
     const void *al[] = {b->x, b->ab, b->hp, b->y_perm, b->dout, b->dx, b->dw1, b->dw2,
@@ -406,11 +450,25 @@ static moe_status backward_mxfp8(const moe_bwd_desc *b, hipStream_t s) {
     // and the quantiser below forms dy = round_bf16(gate * dOut[token]) as it
     // reads the dOut rows
     float *row_gate = reinterpret_cast<float *>(b->dy_perm);
-    if ((st = combine_bwd_launch(b->dout, b->y_perm, MOE_BF16, b->topk_gate, b->topk_idx,
-                                 b->token_pos, b->T, d, b->k, E, row_gate, b->dlogits,
-                                 b->dgate, s, true)) != MOE_OK ||
-        (st = stage_mark(b, 0, s)) != MOE_OK)
-        return st;
+    if (c && any && (st = check_act8(c)) != MOE_OK) return st;
+    if (!c)
+        st = combine_bwd_launch(b->dout, b->y_perm, MOE_BF16, b->topk_gate, b->topk_idx,
+                                b->token_pos, b->T, d, b->k, E, row_gate, b->dlogits, b->dgate, s,
+                                true);
+    else if (any) {
+        st = combine_bwd_act8_launch(b->dout, MOE_BF16, c->y8, c->y8_scale, b->topk_gate,
+                                     b->topk_idx, b->token_pos, b->T, d, b->k, E, nullptr,
+                                     row_gate, b->dlogits, b->dgate, s);
+        // AB, and H' unless the caller brings it in its column layout
+        if (st == MOE_OK)
+            st = b->hp_cols ? act8_load_launch(c->ab8, c->ab8_scale, MOE_BF16, R, 2 * (int64_t)h,
+                                               const_cast<void *>(b->ab), s)
+                            : act8_swiglu_launch(c->ab8, c->ab8_scale, MOE_BF16, R, h,
+                                                 const_cast<void *>(b->ab),
+                                                 const_cast<void *>(b->hp), s);
+    } else
+        st = MOE_OK;
+    if (st != MOE_OK || (st = stage_mark(b, 0, s)) != MOE_OK) return st;
     moe_gemm_desc g;
     memset(&g, 0, sizeof(g));
     g.dtype = MOE_MXFP8;
@@ -473,6 +531,134 @@ static moe_status backward_mxfp8(const moe_bwd_desc *b, hipStream_t s) {
     g.A = b0q; g.a_scale = b0s; g.B = b1q; g.b_scale = b1s; g.C = b->dw1;
     if ((st = gemm_launch(&g, s)) != MOE_OK) return st;
     return stage_mark(b, 9, s);
+}
+
+moe_status moe_backward(const moe_bwd_desc *b, void *stream) {
+    return backward(b, nullptr, (hipStream_t)stream);
+}
+
+moe_status moe_backward_act8(const moe_bwd_desc *b, const moe_act8_saved *c, void *stream) {
+    if (!c) return MOE_ERR_NULL;
+    return backward(b, c, (hipStream_t)stream);
+}
+
+// dtype and sizes of a checkpointed [rows, cols] matrix
+static moe_status check_act8_matrix(moe_dtype dt, int64_t rows, int64_t cols) {
+    if (dt != MOE_F32 && dt != MOE_BF16) return MOE_ERR_DTYPE;
+    if (rows < 0 || rows >= ((int64_t)1 << 31) || cols < 32 || cols % 32 ||
+        cols >= ((int64_t)1 << 20))
+        return MOE_ERR_SHAPE;
+    return MOE_OK;
+}
+
+moe_status moe_act8_store(const void *in, moe_dtype dt, int64_t rows, int64_t cols, uint8_t *q,
+                          uint8_t *scale, void *stream) {
+    moe_status st = check_act8_matrix(dt, rows, cols);
+    if (st != MOE_OK || rows == 0) return st;
+    if (!in || !q || !scale) return MOE_ERR_NULL;
+    if (!aligned16(in) || !aligned16(q)) return MOE_ERR_ALIGN;
+    return act8_store_launch(in, dt, rows, cols, q, scale, (hipStream_t)stream);
+}
+
+moe_status moe_act8_load(const uint8_t *q, const uint8_t *scale, moe_dtype dt, int64_t rows,
+                         int64_t cols, void *out, void *stream) {
+    moe_status st = check_act8_matrix(dt, rows, cols);
+    if (st != MOE_OK || rows == 0) return st;
+    if (!q || !scale || !out) return MOE_ERR_NULL;
+    if (!aligned16(q) || !aligned16(out)) return MOE_ERR_ALIGN;
+    return act8_load_launch(q, scale, dt, rows, cols, out, (hipStream_t)stream);
+}
+
+moe_status moe_act8_swiglu(const uint8_t *ab8, const uint8_t *ab8_scale, moe_dtype dt,
+                           int64_t rows, int32_t h, void *ab, void *hp, void *stream) {
+    if (dt != MOE_F32 && dt != MOE_BF16) return MOE_ERR_DTYPE;
+    if (rows < 0 || rows >= ((int64_t)1 << 31) || !hidden_ok(h)) return MOE_ERR_SHAPE;
+    if (rows == 0) return MOE_OK;
+    if (!ab8 || !ab8_scale || !ab || !hp) return MOE_ERR_NULL;
+    if (!aligned16(ab8) || !aligned16(ab) || !aligned16(hp)) return MOE_ERR_ALIGN;
+    return act8_swiglu_launch(ab8, ab8_scale, dt, rows, h, ab, hp, (hipStream_t)stream);
+}
+
+moe_status moe_combine_act8(const void *y_perm, moe_dtype dt, const float *topk_gate,
+                            const int32_t *token_pos, int64_t T, int32_t d, int32_t k, void *out,
+                            uint8_t *y8, uint8_t *y8_scale, void *stream) {
+    if (dt != MOE_F32 && dt != MOE_BF16) return MOE_ERR_DTYPE;
+    if (T < 0 || k < 1 || k > 8 || T * (int64_t)k >= ((int64_t)1 << 31) || !width_ok(d))
+        return MOE_ERR_SHAPE;
+    if (T == 0) return MOE_OK;
+    if (!y_perm || !topk_gate || !token_pos || !out || !y8 || !y8_scale) return MOE_ERR_NULL;
+    if (!aligned16(y_perm) || !aligned16(out) || !aligned16(y8)) return MOE_ERR_ALIGN;
+    return combine_act8_launch(y_perm, dt, topk_gate, token_pos, T, d, k, out, y8, y8_scale,
+                               (hipStream_t)stream);
+}
+
+moe_status moe_combine_backward_act8(const void *dout, moe_dtype dt, const uint8_t *y8,
+                                     const uint8_t *y8_scale, const float *topk_gate,
+                                     const int32_t *topk_idx, const int32_t *token_pos, int64_t T,
+                                     int32_t d, int32_t k, int32_t E, void *dy_perm,
+                                     float *dlogits, float *dgate, void *stream) {
+    if (dt != MOE_F32 && dt != MOE_BF16) return MOE_ERR_DTYPE;
+    if (!routing_shape_ok(T, E, k) || !width_ok(d)) return MOE_ERR_SHAPE;
+    if (T == 0) return MOE_OK;
+    if (!dout || !y8 || !y8_scale || !topk_gate || !topk_idx || !token_pos || !dy_perm || !dlogits)
+        return MOE_ERR_NULL;
+    if (!aligned16(dout) || !aligned16(y8) || !aligned16(dy_perm)) return MOE_ERR_ALIGN;
+    return combine_bwd_act8_launch(dout, dt, y8, y8_scale, topk_gate, topk_idx, token_pos, T, d, k,
+                                   E, dy_perm, nullptr, dlogits, dgate, (hipStream_t)stream);
+}
+
+static moe_status check_norm(moe_dtype dt, int64_t T, int32_t d) {
+    if (dt != MOE_F32 && dt != MOE_BF16) return MOE_ERR_DTYPE;
+    return T >= 0 && T < ((int64_t)1 << 31) && width_ok(d) ? MOE_OK : MOE_ERR_SHAPE;
+}
+
+moe_status moe_layer_norm(const void *x, moe_dtype dt, const void *residual, const float *gamma,
+                          const float *beta, float eps, int64_t T, int32_t d, void *y, void *sum,
+                          float *mean, float *rstd, uint8_t *x8, uint8_t *x8_scale, void *stream) {
+    moe_status st = check_norm(dt, T, d);
+    if (st != MOE_OK) return st;
+    if (!(eps > 0.f) || eps > 1.f) return MOE_ERR_SHAPE;
+    if (T == 0) return MOE_OK;
+    if (!x || !gamma || !y || !residual != !sum || !x8 != !x8_scale) return MOE_ERR_NULL;
+    const void *al[] = {x, residual, gamma, beta, y, sum, x8};
+    for (const void *p : al)
+        if (!aligned16(p)) return MOE_ERR_ALIGN;
+    if (!aligned4(mean) || !aligned4(rstd)) return MOE_ERR_ALIGN;
+    return norm_fwd_launch(x, dt, residual, gamma, beta, eps, T, d, y, sum, mean, rstd, x8,
+                           x8_scale, (hipStream_t)stream);
+}
+
+size_t moe_layer_norm_backward_workspace_size(moe_dtype dt, int64_t T, int32_t d) {
+    return check_norm(dt, T, d) == MOE_OK ? norm_bwd_ws_bytes(dt, T, d) : 0;
+}
+
+moe_status moe_layer_norm_backward(const void *dy, moe_dtype dt, const void *x, const uint8_t *x8,
+                                   const uint8_t *x8_scale, const float *mean, const float *rstd,
+                                   const float *gamma, const void *dsum, int64_t T, int32_t d,
+                                   void *dx, float *dgamma, float *dbeta, int32_t accumulate_dw,
+                                   void *ws, size_t ws_bytes, void *stream) {
+    moe_status st = check_norm(dt, T, d);
+    if (st != MOE_OK) return st;
+    if (accumulate_dw != 0 && accumulate_dw != 1) return MOE_ERR_DTYPE;
+    const bool params = dgamma || dbeta;
+    if (T > 0) {
+        if (!dy || !gamma || !mean || !rstd || !dx || !x == !x8 || !x8 != !x8_scale)
+            return MOE_ERR_NULL;
+        const void *al[] = {dy, x, x8, gamma, dsum, dx};
+        for (const void *p : al)
+            if (!aligned16(p)) return MOE_ERR_ALIGN;
+        if (params) {
+            if (ws_bytes < norm_bwd_ws_bytes(dt, T, d)) return MOE_ERR_WORKSPACE;
+            if (!ws) return MOE_ERR_NULL;
+            if (!aligned16(ws)) return MOE_ERR_ALIGN;
+        }
+    }
+    const float *al4[] = {mean, rstd, dgamma, dbeta};
+    for (const float *p : al4)
+        if (!aligned4(p)) return MOE_ERR_ALIGN;
+    return norm_bwd_launch(dy, dt, x, x8, x8_scale, mean, rstd, gamma, dsum, T, d, dx, dgamma,
+                           dbeta, accumulate_dw, params ? (float *)ws : nullptr,
+                           (hipStream_t)stream);
 }
 
 size_t mxfp8_col_blocks(int64_t rows, int32_t n_groups) { return moe::mxfp8_col_blocks(rows, n_groups); }

@@ -1,0 +1,380 @@
+// norm.hip -- layer norm, forward and backward.
+//
+//   s = x (+ res),  mu = mean(s),  r = 1 / sqrt(mean((s - mu)^2) + eps)
+//   y = (s - mu) r gamma + beta
+// and, with g = dy gamma and xh = (s - mu) r,
+//   dx = r (g - mean(g) - xh mean(g xh)) (+ dsum),
+//   dgamma = sum_t dy xh,  dbeta = sum_t dy.
+// s may be kept between the two passes as an 8-bit checkpoint (act8.h),
+// written from the forward's registers and read by the backward in place of
+// s. All sums and statistics are fp32, in a fixed order (no atomics); the
+// variance is taken about the mean, from the row in registers.
+#include "act8.h"
+
+namespace moe {
+
+// Sum of v over the G threads of a row: G = 8 or 64 neighbouring lanes.
+MOE_DEV float swap16_sum(float v) {
+    const auto r = __builtin_amdgcn_permlane16_swap(__float_as_uint(v), __float_as_uint(v), false,
+                                                    false);
+    return __uint_as_float(r[0]) + __uint_as_float(r[1]);
+}
+MOE_DEV float swap32_sum(float v) {
+    const auto r = __builtin_amdgcn_permlane32_swap(__float_as_uint(v), __float_as_uint(v), false,
+                                                    false);
+    return __uint_as_float(r[0]) + __uint_as_float(r[1]);
+}
+template <int G>
+MOE_DEV float group_sum(float v) {
+    v += dpp_move<kDppXor1>(v);
+    v += dpp_move<kDppXor2>(v);
+    v += dpp_move<kDppHalfMirror>(v);
+    if constexpr (G >= 64) {
+        v += dpp_move<kDppRowRor8>(v);
+        v = swap16_sum(v);
+        v = swap32_sum(v);
+    }
+    return v;
+}
+
+// Sum over the row's G threads; with G = 256 a row is a workgroup: the four
+// waves' sums go through LDS (red: 4 floats, its own for every call between
+// two barriers of the row).
+template <int G>
+MOE_DEV float row_sum(float v, float *red) {
+    v = group_sum<G>(v);
+    if constexpr (G == 256) {
+        if ((threadIdx.x & 63) == 0) red[threadIdx.x >> 6] = v;
+        __syncthreads();
+        v = (red[0] + red[1]) + (red[2] + red[3]);
+    }
+    return v;
+}
+
+template <bool BF16>
+MOE_DEV void load_params(const float *p, int c, float *f) {
+    const float4 *q = reinterpret_cast<const float4 *>(p) + (int64_t)c * (Row16<BF16>::N / 4);
+#pragma unroll
+    for (int i = 0; i < Row16<BF16>::N / 4; i++) {
+        const float4 v = q[i];
+        f[4 * i] = v.x; f[4 * i + 1] = v.y; f[4 * i + 2] = v.z; f[4 * i + 3] = v.w;
+    }
+}
+
+// G threads a row, V 16-byte vectors a thread (vector lane + i G of the row).
+template <bool BF16, int G, int V>
+__global__ __launch_bounds__(256) void norm_fwd(
+    const uint4 *__restrict__ x, const uint4 *__restrict__ res, const float *__restrict__ gamma,
+    const float *__restrict__ beta, float eps, int64_t T, int nv, float inv_d,
+    uint4 *__restrict__ y, uint4 *__restrict__ sum, float *__restrict__ mean,
+    float *__restrict__ rstd, typename Codes<BF16>::type *__restrict__ x8,
+    uint8_t *__restrict__ x8_scale) {
+    typedef Row16<BF16> R;
+    __shared__ float red[8];
+    const int lane = threadIdx.x % G;
+    const int64_t t = (int64_t)blockIdx.x * (256 / G) + threadIdx.x / G;
+    if (t >= T) return;                         // G = 256: never (one row a block)
+    const int64_t base = t * nv;
+    uint4 w[V];
+    float s1 = 0.f;
+#pragma unroll
+    for (int i = 0; i < V; i++) {
+        const int c = lane + i * G;
+        w[i] = make_uint4(0, 0, 0, 0);
+        if (c >= nv) continue;
+        w[i] = x[base + c];
+        float f[R::N];
+        R::unpack(w[i], f);
+        if (res) {
+            float q[R::N];
+            R::unpack(res[base + c], q);
+#pragma unroll
+            for (int e = 0; e < R::N; e++) f[e] += q[e];
+            w[i] = R::pack(f);                  // the stream in its own type: what the norm sees
+            sum[base + c] = w[i];
+            R::unpack(w[i], f);
+        }
+#pragma unroll
+        for (int e = 0; e < R::N; e++) s1 += f[e];
+    }
+    const float mu = row_sum<G>(s1, red) * inv_d;
+    float s2 = 0.f;
+#pragma unroll
+    for (int i = 0; i < V; i++) {
+        if (lane + i * G >= nv) continue;
+        float f[R::N];
+        R::unpack(w[i], f);
+#pragma unroll
+        for (int e = 0; e < R::N; e++) s2 = fmaf(f[e] - mu, f[e] - mu, s2);
+    }
+    const float r = 1.f / sqrtf(fmaf(row_sum<G>(s2, red + 4), inv_d, eps));
+    if (lane == 0) {
+        if (mean) mean[t] = mu;
+        if (rstd) rstd[t] = r;
+    }
+#pragma unroll
+    for (int i = 0; i < V; i++) {
+        const int c = lane + i * G;
+        if (c >= nv) continue;
+        float f[R::N], ga[R::N], o[R::N];
+        R::unpack(w[i], f);
+        load_params<BF16>(gamma, c, ga);
+#pragma unroll
+        for (int e = 0; e < R::N; e++) o[e] = (f[e] - mu) * r * ga[e];
+        if (beta) {
+            load_params<BF16>(beta, c, ga);
+#pragma unroll
+            for (int e = 0; e < R::N; e++) o[e] += ga[e];
+        }
+        y[base + c] = R::pack(o);
+        if (x8) {
+            const uint32_t sb = act8_scale_byte<BF16>(w[i]);
+            typename Codes<BF16>::type q;
+            act8_encode(f, sb, q);
+            x8[base + c] = q;
+            if (c % R::LPB == 0) x8_scale[(base + c) / R::LPB] = (uint8_t)sb;
+        }
+    }
+}
+
+// Backward: every workgroup takes rows blockIdx.x * (256 / G) + ..., strided
+// by the grid, and leaves its sums of dy xh and dy in part[blockIdx.x][0..1][d].
+template <bool BF16, int G, int V, bool CKPT>
+__global__ __launch_bounds__(256) void norm_bwd(
+    const uint4 *__restrict__ dy, const uint4 *__restrict__ x,
+    const typename Codes<BF16>::type *__restrict__ x8, const uint8_t *__restrict__ x8_scale,
+    const float *__restrict__ mean, const float *__restrict__ rstd,
+    const float *__restrict__ gamma, const uint4 *__restrict__ dsum, int64_t T, int nv, float inv_d,
+    uint4 *__restrict__ dx, float *__restrict__ part) {
+    typedef Row16<BF16> R;
+    constexpr int RPB = 256 / G;
+    __shared__ float red[2][8];
+    __shared__ float acc_s[G == 256 ? 1 : 256 * R::N];
+    const int lane = threadIdx.x % G;
+    float dg[V * R::N], db[V * R::N], ga[V * R::N];
+#pragma unroll
+    for (int i = 0; i < V; i++) {
+#pragma unroll
+        for (int e = 0; e < R::N; e++) dg[i * R::N + e] = db[i * R::N + e] = ga[i * R::N + e] = 0.f;
+        if (lane + i * G < nv) load_params<BF16>(gamma, lane + i * G, ga + i * R::N);
+    }
+    int par = 0;
+    for (int64_t t = (int64_t)blockIdx.x * RPB + threadIdx.x / G; t < T;
+         t += (int64_t)gridDim.x * RPB, par ^= 1) {
+        const int64_t base = t * nv;
+        const float mu = mean[t], r = rstd[t];
+        uint4 wy[V];
+        float xh[V * R::N];
+        float c1 = 0.f, c2 = 0.f;
+#pragma unroll
+        for (int i = 0; i < V; i++) {
+            const int c = lane + i * G;
+            if (c >= nv) continue;
+            wy[i] = dy[base + c];
+            float f[R::N], g[R::N];
+            if constexpr (CKPT)
+                act8_decode(x8[base + c], act8_step(x8_scale[(base + c) / R::LPB]), f);
+            else
+                R::unpack(x[base + c], f);
+            R::unpack(wy[i], g);
+#pragma unroll
+            for (int e = 0; e < R::N; e++) {
+                const float h = (f[e] - mu) * r;
+                xh[i * R::N + e] = h;
+                dg[i * R::N + e] = fmaf(g[e], h, dg[i * R::N + e]);
+                db[i * R::N + e] += g[e];
+                const float gw = g[e] * ga[i * R::N + e];
+                c1 += gw;
+                c2 = fmaf(gw, h, c2);
+            }
+        }
+        c1 = group_sum<G>(c1);
+        c2 = group_sum<G>(c2);
+        if constexpr (G == 256) {
+            // one barrier a row: the next row writes the other half
+            float *q = red[par];
+            if ((threadIdx.x & 63) == 0) { q[threadIdx.x >> 6] = c1; q[4 + (threadIdx.x >> 6)] = c2; }
+            __syncthreads();
+            c1 = (q[0] + q[1]) + (q[2] + q[3]);
+            c2 = (q[4] + q[5]) + (q[6] + q[7]);
+        }
+        c1 *= inv_d;
+        c2 *= inv_d;
+#pragma unroll
+        for (int i = 0; i < V; i++) {
+            const int c = lane + i * G;
+            if (c >= nv) continue;
+            float g[R::N], o[R::N];
+            R::unpack(wy[i], g);
+#pragma unroll
+            for (int e = 0; e < R::N; e++)
+                o[e] = r * (fmaf(-xh[i * R::N + e], c2, g[e] * ga[i * R::N + e]) - c1);
+            if (dsum) {
+                float q[R::N];
+                R::unpack(dsum[base + c], q);
+#pragma unroll
+                for (int e = 0; e < R::N; e++) o[e] += q[e];
+            }
+            dx[base + c] = R::pack(o);
+        }
+    }
+    if (!part) return;
+    // the workgroup's rows together, in the order of their row slots
+    const int64_t d = (int64_t)nv * R::N;
+    float *pg = part + (int64_t)blockIdx.x * 2 * d, *pb = pg + d;
+#pragma unroll
+    for (int i = 0; i < V; i++) {
+        const int c = lane + i * G;
+#pragma unroll
+        for (int z = 0; z < 2; z++) {
+            float *a = (z ? db : dg) + i * R::N, *p = z ? pb : pg;
+            if constexpr (G == 256) {
+                if (c < nv)
+#pragma unroll
+                    for (int e = 0; e < R::N; e++) p[(int64_t)c * R::N + e] = a[e];
+            } else {
+                __syncthreads();
+#pragma unroll
+                for (int e = 0; e < R::N; e++) acc_s[(threadIdx.x / G * R::N + e) * G + lane] = a[e];
+                __syncthreads();
+                // G * N columns, RPB terms each
+                for (int m = threadIdx.x; m < G * R::N; m += 256) {
+                    const int e = m / G, l = m % G;
+                    float s = 0.f;
+                    for (int b = 0; b < RPB; b++) s += acc_s[(b * R::N + e) * G + l];
+                    if (l + i * G < nv) p[(int64_t)(l + i * G) * R::N + e] = s;
+                }
+            }
+        }
+    }
+}
+
+// dgamma, dbeta = (+=) the workgroups' sums, in their order: 32 columns a
+// workgroup, 8 slices of the rows each, then the slices in order.
+__global__ __launch_bounds__(256) void norm_bwd_params(const float *__restrict__ part, int np,
+                                                       int d, float *__restrict__ dgamma,
+                                                       float *__restrict__ dbeta, int accumulate) {
+    __shared__ float s_p[8][33];
+    const int z = blockIdx.y;
+    float *out = z ? dbeta : dgamma;
+    if (!out) return;
+    const int col = blockIdx.x * 32 + (threadIdx.x & 31), sl = threadIdx.x >> 5;
+    float s = 0.f;
+    for (int p = sl; p < np; p += 8) s += part[((int64_t)p * 2 + z) * d + col];
+    s_p[sl][threadIdx.x & 31] = s;
+    __syncthreads();
+    if (sl) return;
+    s = 0.f;
+#pragma unroll
+    for (int i = 0; i < 8; i++) s += s_p[i][threadIdx.x];
+    out[col] = accumulate ? out[col] + s : s;
+}
+
+// ---------------------------------------------------------------------------
+// launchers
+
+// p + n elements of T, null if p is
+template <typename E, typename P>
+static E *at(P *p, int64_t n) { return p ? reinterpret_cast<E *>(p) + n : nullptr; }
+
+// threads a row for nv vectors
+static int norm_group(int nv) { return nv <= 32 ? 8 : nv <= 256 ? 64 : 256; }
+
+#define NORM_VSWITCH(v, F)                                                                     \
+    ((v) <= 1 ? F(1) : (v) <= 2 ? F(2) : (v) <= 3 ? F(3) : (v) <= 4 ? F(4) : (v) <= 6 ? F(6)   \
+     : (v) <= 8 ? F(8) : F(16))
+#define NORM_GVSWITCH(g, v, F)                                                                 \
+    ((g) == 8 ? NORM_VSWITCH(v, F##8) : (g) == 64 ? NORM_VSWITCH(v, F##64) : NORM_VSWITCH(v, F##256))
+
+template <bool BF16>
+static moe_status norm_fwd_run(const void *x, const void *res, const float *gamma,
+                               const float *beta, float eps, int64_t T, int d, void *y, void *sum,
+                               float *mean, float *rstd, uint8_t *x8, uint8_t *x8_scale,
+                               hipStream_t s) {
+    const int nv = d / Row16<BF16>::N, g = norm_group(nv), v = (nv + g - 1) / g;
+    const float inv_d = 1.f / (float)d;
+    typedef typename Codes<BF16>::type C;
+    // rows in pieces of at most kMaxBlocks workgroups (a grid has fewer than 2^32 threads)
+    const int64_t piece = kMaxBlocks * (256 / g);
+    for (int64_t t = 0; t < T; t += piece) {
+        const int64_t n = T - t < piece ? T - t : piece;
+        const unsigned nb = (unsigned)((n + 256 / g - 1) / (256 / g));
+        const int64_t o = t * nv;
+#define F(G, V)                                                                                  \
+    (norm_fwd<BF16, G, V><<<nb, 256, 0, s>>>(                                                    \
+         at<const uint4>(x, o), at<const uint4>(res, o), gamma, beta, eps, n, nv, inv_d,         \
+         at<uint4>(y, o), at<uint4>(sum, o), at<float>(mean, t), at<float>(rstd, t),             \
+         at<C>(x8, o), at<uint8_t>(x8_scale, o / Row16<BF16>::LPB)), 0)
+#define F8(V) F(8, V)
+#define F64(V) F(64, V)
+#define F256(V) F(256, V)
+        NORM_GVSWITCH(g, v, F);
+#undef F
+#undef F8
+#undef F64
+#undef F256
+    }
+    return launch_status();
+}
+
+moe_status norm_fwd_launch(const void *x, moe_dtype dt, const void *res, const float *gamma,
+                           const float *beta, float eps, int64_t T, int d, void *y, void *sum,
+                           float *mean, float *rstd, uint8_t *x8, uint8_t *x8_scale,
+                           hipStream_t s) {
+    return dt == MOE_BF16
+               ? norm_fwd_run<true>(x, res, gamma, beta, eps, T, d, y, sum, mean, rstd, x8, x8_scale, s)
+               : norm_fwd_run<false>(x, res, gamma, beta, eps, T, d, y, sum, mean, rstd, x8, x8_scale, s);
+}
+
+// workgroups of the backward (and rows of its partial sums): by the sizes
+// alone, so that the workspace is the same on every device
+static int64_t norm_bwd_blocks(int64_t T, int d, int elems) {
+    const int rpb = 256 / norm_group(d / elems);
+    const int64_t most = (T + rpb - 1) / rpb;
+    return most < 512 ? most : 512;
+}
+
+size_t norm_bwd_ws_bytes(moe_dtype dt, int64_t T, int d) {
+    return (size_t)norm_bwd_blocks(T, d, dt == MOE_BF16 ? 8 : 4) * 2 * d * sizeof(float);
+}
+
+template <bool BF16>
+static moe_status norm_bwd_run(const void *dy, const void *x, const uint8_t *x8,
+                               const uint8_t *x8_scale, const float *mean, const float *rstd,
+                               const float *gamma, const void *dsum, int64_t T, int d, void *dx,
+                               float *dgamma, float *dbeta, bool accumulate, float *part,
+                               hipStream_t s) {
+    const int nv = d / Row16<BF16>::N, g = norm_group(nv), v = (nv + g - 1) / g;
+    const int np = (int)norm_bwd_blocks(T, d, Row16<BF16>::N);
+    const float inv_d = 1.f / (float)d;
+    typedef typename Codes<BF16>::type C;
+#define F2(G, V, K)                                                                              \
+    (norm_bwd<BF16, G, V, K><<<np, 256, 0, s>>>(                                                 \
+         reinterpret_cast<const uint4 *>(dy), reinterpret_cast<const uint4 *>(x),                \
+         reinterpret_cast<const C *>(x8), x8_scale, mean, rstd, gamma,                           \
+         reinterpret_cast<const uint4 *>(dsum), T, nv, inv_d, reinterpret_cast<uint4 *>(dx),     \
+         part), 0)
+#define F8(V) (x8 ? F2(8, V, true) : F2(8, V, false))
+#define F64(V) (x8 ? F2(64, V, true) : F2(64, V, false))
+#define F256(V) (x8 ? F2(256, V, true) : F2(256, V, false))
+    if (np > 0) NORM_GVSWITCH(g, v, F);
+#undef F2
+#undef F8
+#undef F64
+#undef F256
+    if (dgamma || dbeta)
+        norm_bwd_params<<<dim3(d / 32, 2), 256, 0, s>>>(part, np, d, dgamma, dbeta, accumulate);
+    return launch_status();
+}
+
+moe_status norm_bwd_launch(const void *dy, moe_dtype dt, const void *x, const uint8_t *x8,
+                           const uint8_t *x8_scale, const float *mean, const float *rstd,
+                           const float *gamma, const void *dsum, int64_t T, int d, void *dx,
+                           float *dgamma, float *dbeta, bool accumulate, float *part,
+                           hipStream_t s) {
+    return dt == MOE_BF16
+               ? norm_bwd_run<true>(dy, x, x8, x8_scale, mean, rstd, gamma, dsum, T, d, dx, dgamma, dbeta, accumulate, part, s)
+               : norm_bwd_run<false>(dy, x, x8, x8_scale, mean, rstd, gamma, dsum, T, d, dx, dgamma, dbeta, accumulate, part, s);
+}
+
+}  // namespace moe
