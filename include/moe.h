@@ -629,6 +629,53 @@ moe_status moe_layer_norm_backward(const void *dy, moe_dtype dt, const void *x, 
                                    void *dx, float *dgamma, float *dbeta, int32_t accumulate_dw,
                                    void *ws, size_t ws_bytes, void *stream);
 
+/* ------------------------------------------------------------------ */
+/* The experts for few tokens, weights in 4 bits                        */
+
+/* Quantise a [rows, cols] fp32 or bf16 matrix to OCP MXFP4 (Microscaling
+ * v1.0): per block of 32 along a row the E8M0 shared exponent is
+ * floor(log2(amax)) - 2 (2 = E2M1's maximum exponent), -127 at least; the
+ * elements are x * 2^-shared rounded to nearest even E2M1 (0, 1/2, 1, 3/2, 2,
+ * 3, 4, 6 and their negatives) and saturated to +-6. q [rows, cols/2]: two
+ * elements a byte, the first in the low half; scale [rows, cols/32]. cols: a
+ * multiple of 32 below 2^20; in and q 16-byte aligned. Infinite and NaN
+ * inputs are outside the contract. Done once per set of weights. */
+moe_status moe_w4_quantize(const void *in, moe_dtype in_dt, int64_t rows, int64_t cols, uint8_t *q,
+                           uint8_t *scale, void *stream);
+
+/* The expert layer's forward after the routing, for the few tokens of a
+ * generation step (a few rows per expert; the weights of an expert are read
+ * once per 64 of its rows), with W1, W2 in 4 bits:
+ *   H' = silu(a) b with a, b = W1[e] x[t],  out[t] = sum_j g[t, j] W2[e_j] H'
+ * x, out [T, d] bf16; accumulation, H' (to 16 significant bits) and the
+ * experts' outputs stay wider than bf16 until out is rounded. topk_gate,
+ * token_pos, sorted_token and offsets are moe_route's for the T tokens
+ * (token_pos < 0: that slot adds nothing). w1q [E, 2h, d/2], w1_scale [E, 2h,
+ * d/32], w2q [E, d, h/2], w2_scale [E, d, h/32] as moe_w4_quantize writes
+ * them. ws: moe_w4_experts_workspace_size bytes, one for every call that may
+ * overlap in time. x, out, w1q, w2q and ws 16-byte aligned. Limits as
+ * moe_route; d and h multiples of 32, d <= 16384, h <= 8192. T = 0 is a
+ * no-op. */
+typedef struct moe_w4_desc {
+    int32_t d, h, E, k;
+    int64_t T;
+    const void *x;
+    const float *topk_gate;
+    const int32_t *token_pos;
+    const int32_t *sorted_token;
+    const int32_t *offsets;
+    const uint8_t *w1q;
+    const uint8_t *w1_scale;
+    const uint8_t *w2q;
+    const uint8_t *w2_scale;
+    void *out;
+    void *ws;
+    size_t ws_bytes;
+} moe_w4_desc;
+
+size_t moe_w4_experts_workspace_size(int64_t T, int32_t k, int32_t d, int32_t h);
+moe_status moe_w4_experts(const moe_w4_desc *w, void *stream);
+
 #ifdef __cplusplus
 }
 #endif

@@ -68,6 +68,13 @@ class Act8Saved(ctypes.Structure):
     _fields_ = [("ab8", _P), ("ab8_scale", _P), ("y8", _P), ("y8_scale", _P)]
 
 
+class W4Desc(ctypes.Structure):
+    _fields_ = [("d", _I32), ("h", _I32), ("E", _I32), ("k", _I32), ("T", _I64), ("x", _P),
+                ("topk_gate", _P), ("token_pos", _P), ("sorted_token", _P), ("offsets", _P),
+                ("w1q", _P), ("w1_scale", _P), ("w2q", _P), ("w2_scale", _P), ("out", _P),
+                ("ws", _P), ("ws_bytes", _SZ)]
+
+
 class BwdWsLayout(ctypes.Structure):
     _fields_ = [(n, _SZ) for n in ("row_q", "row_s", "col0_q", "col0_s", "col1_q", "col1_s",
                                    "total")]
@@ -150,6 +157,12 @@ def _load():
     lib.moe_layer_norm_backward.argtypes = [_P, _I32, _P, _P, _P, _P, _P, _P, _P, _I64, _I32, _P,
                                             _P, _P, _I32, _P, _SZ, _P]
     lib.moe_layer_norm_backward.restype = _I32
+    lib.moe_w4_quantize.argtypes = [_P, _I32, _I64, _I64, _P, _P, _P]
+    lib.moe_w4_quantize.restype = _I32
+    lib.moe_w4_experts_workspace_size.argtypes = [_I64, _I32, _I32, _I32]
+    lib.moe_w4_experts_workspace_size.restype = _SZ
+    lib.moe_w4_experts.argtypes = [ctypes.POINTER(W4Desc), _P]
+    lib.moe_w4_experts.restype = _I32
     return lib
 
 
@@ -884,6 +897,73 @@ def moe_layer_norm_backward(saved: dict, dy: torch.Tensor, weight: torch.Tensor,
 
 
 # ---------------------------------------------------------------------------
+# the experts for few tokens, weights in 4 bits
+
+
+def moe_w4_quantize(w: torch.Tensor, q: torch.Tensor | None = None,
+                    scale: torch.Tensor | None = None):
+    """OCP MXFP4 quantisation (see moe.h) of w [..., rows, cols] (f32 or
+    bf16) along its rows: q [..., rows, cols/2] and scale [..., rows, cols/32]."""
+    if w is None or w.dim() < 2:
+        raise ValueError("w: expected [..., rows, cols]")
+    rows, cols, dt = _act_matrix(w.reshape(-1, w.shape[-1]) if w.is_contiguous() else w, "w")
+    lead = tuple(w.shape[:-1])
+    if q is None:
+        q = torch.empty(lead + (cols // 2,), dtype=torch.uint8, device=w.device)
+    if scale is None:
+        scale = torch.empty(lead + (cols // 32,), dtype=torch.uint8, device=w.device)
+    _need_on(q, lead + (cols // 2,), torch.uint8, w.device, "q")
+    _need_on(scale, lead + (cols // 32,), torch.uint8, w.device, "scale")
+    with _On(w.device) as s:
+        _check("moe_w4_quantize", _lib.moe_w4_quantize(_ptr(w), dt, rows, cols, _ptr(q),
+                                                       _ptr(scale), s))
+    return q, scale
+
+
+def moe_w4_experts_workspace_size(T: int, k: int, d: int, h: int) -> int:
+    return int(_lib.moe_w4_experts_workspace_size(T, k, d, h))
+
+
+def moe_w4_experts(x: torch.Tensor, route: dict, w1q: torch.Tensor, w1_scale: torch.Tensor,
+                   w2q: torch.Tensor, w2_scale: torch.Tensor, out: torch.Tensor | None = None,
+                   ws: torch.Tensor | None = None) -> torch.Tensor:
+    """The expert layer's forward for few tokens after the routing, weights
+    as moe_w4_quantize writes them (see moe.h). route: moe_route's dict for
+    these tokens (topk_gate, token_pos, sorted_token, offsets are read)."""
+    T, d, dt = _act_matrix(x, "x")
+    if dt != MOE_BF16:
+        raise ValueError(f"x: expected bf16, got {x.dtype}")
+    dev, u8, i32 = x.device, torch.uint8, torch.int32
+    if w1q is None or w1q.dim() != 3 or w1q.shape[1] % 64:
+        raise ValueError("w1q: expected [E, 2h, d/2] with h a multiple of 32")
+    E, h = w1q.shape[0], w1q.shape[1] // 2
+    k = route["token_pos"].shape[-1]
+    _need_on(w1q, (E, 2 * h, d // 2), u8, dev, "w1q")
+    _need_on(w1_scale, (E, 2 * h, d // 32), u8, dev, "w1_scale")
+    _need_on(w2q, (E, d, h // 2), u8, dev, "w2q")
+    _need_on(w2_scale, (E, d, h // 32), u8, dev, "w2_scale")
+    _need_on(route["topk_gate"], (T, k), torch.float32, dev, "topk_gate")
+    _need_on(route["token_pos"], (T, k), i32, dev, "token_pos")
+    _need_on(route["sorted_token"], (T * k,), i32, dev, "sorted_token")
+    _need_on(route["offsets"], (E + 1,), i32, dev, "offsets")
+    if out is None:
+        out = torch.empty((T, d), dtype=x.dtype, device=dev)
+    _need_on(out, (T, d), x.dtype, dev, "out")
+    wsb = moe_w4_experts_workspace_size(T, k, d, h)
+    if ws is None:
+        ws = torch.empty(max(wsb, 16), dtype=u8, device=dev)
+    _need_bytes(ws, wsb, "ws")
+    if ws.device != dev:
+        raise ValueError(f"ws: expected on {dev}, got {ws.device}")
+    w = W4Desc(d, h, E, k, T, _ptr(x), _ptr(route["topk_gate"]), _ptr(route["token_pos"]),
+               _ptr(route["sorted_token"]), _ptr(route["offsets"]), _ptr(w1q), _ptr(w1_scale),
+               _ptr(w2q), _ptr(w2_scale), _ptr(out), _ptr(ws), ws.numel())
+    with _On(dev) as s:
+        _check("moe_w4_experts", _lib.moe_w4_experts(ctypes.byref(w), s))
+    return out
+
+
+# ---------------------------------------------------------------------------
 # the layer
 
 
@@ -1426,3 +1506,41 @@ class MoELayerMX:
         if self.balance is not None:
             self.balance.backward(self.grads["dlogits"])
         return _norm_grads(self.out_norm, self.grads)
+
+
+class MoELayerW4:
+    """The layer's forward for text generation: routing, then the experts
+    with MXFP4 weights (moe_w4_experts), for a step's few tokens. w1 [E, 2h,
+    d], w2 [E, d, h] (f32 or bf16) are quantised once and not kept. Buffers
+    are allocated once per (T, device), so a step is kernel launches alone
+    and can be captured in a HIP graph."""
+
+    def __init__(self, w1: torch.Tensor, w2: torch.Tensor, k: int):
+        self.E, h2, self.d = w1.shape
+        self.h, self.k = h2 // 2, k
+        _need_on(w2, (self.E, self.d, self.h), w2.dtype, w1.device, "w2")
+        self.prepare_weights(w1, w2)
+        self._T = None
+
+    def prepare_weights(self, w1: torch.Tensor, w2: torch.Tensor):
+        """Quantise the weights (again after they have changed)."""
+        self.w1q, self.w1s = moe_w4_quantize(w1)
+        self.w2q, self.w2s = moe_w4_quantize(w2)
+
+    def forward(self, x: torch.Tensor, logits: torch.Tensor) -> torch.Tensor:
+        if x.dim() != 2 or x.shape[1] != self.d or x.dtype != torch.bfloat16:
+            raise ValueError(f"x: expected bf16 [T, {self.d}], got {x.dtype} {tuple(x.shape)}")
+        T, dev = x.shape[0], self.w1q.device
+        _need_on(x, (T, self.d), torch.bfloat16, dev, "x")
+        _need_on(logits, (T, self.E), torch.float32, dev, "logits")
+        if self._T != T:
+            self.route, self.out = None, torch.empty((T, self.d), dtype=x.dtype, device=dev)
+            self.route_ws = torch.empty(max(moe_route_workspace_size(T, self.E, self.k), 1),
+                                        dtype=torch.uint8, device=dev)
+            wsb = moe_w4_experts_workspace_size(T, self.k, self.d, self.h)
+            self.ws = torch.empty(max(wsb, 16), dtype=torch.uint8, device=dev)
+            self._T = T
+        with _On(dev):
+            self.route = moe_route(logits, self.k, out=self.route, ws=self.route_ws)
+            return moe_w4_experts(x, self.route, self.w1q, self.w1s, self.w2q, self.w2s, self.out,
+                                  self.ws)

@@ -74,6 +74,11 @@ moe_status norm_bwd_launch(const void *dy, moe_dtype dt, const void *x, const ui
                            float *dgamma, float *dbeta, bool accumulate, float *part,
                            hipStream_t s);
 
+moe_status w4_quantize_launch(const void *in, moe_dtype dt, int64_t rows, int64_t cols, uint8_t *q,
+                              uint8_t *scale, hipStream_t s);
+size_t w4_ws_bytes(int64_t R, int d, int h);
+moe_status w4_experts_launch(const moe_w4_desc *w, hipStream_t s);
+
 // Queried at every launch (a host-side lookup in the runtime, no device
 // work), so the library holds no mutable state for it.
 int num_cus() {
@@ -659,6 +664,39 @@ moe_status moe_layer_norm_backward(const void *dy, moe_dtype dt, const void *x, 
     return norm_bwd_launch(dy, dt, x, x8, x8_scale, mean, rstd, gamma, dsum, T, d, dx, dgamma,
                            dbeta, accumulate_dw, params ? (float *)ws : nullptr,
                            (hipStream_t)stream);
+}
+
+moe_status moe_w4_quantize(const void *in, moe_dtype in_dt, int64_t rows, int64_t cols, uint8_t *q,
+                           uint8_t *scale, void *stream) {
+    moe_status st = check_act8_matrix(in_dt, rows, cols);
+    if (st != MOE_OK || rows == 0) return st;
+    if (!in || !q || !scale) return MOE_ERR_NULL;
+    if (!aligned16(in) || !aligned16(q)) return MOE_ERR_ALIGN;
+    return w4_quantize_launch(in, in_dt, rows, cols, q, scale, (hipStream_t)stream);
+}
+
+static bool w4_shape_ok(int64_t T, int32_t k, int32_t d, int32_t h) {
+    return T >= 0 && k >= 1 && k <= 8 && T * (int64_t)k < ((int64_t)1 << 31) && width_ok(d) &&
+           hidden_ok(h);
+}
+
+size_t moe_w4_experts_workspace_size(int64_t T, int32_t k, int32_t d, int32_t h) {
+    return w4_shape_ok(T, k, d, h) ? w4_ws_bytes(T * k, d, h) : 0;
+}
+
+moe_status moe_w4_experts(const moe_w4_desc *w, void *stream) {
+    if (!w) return MOE_ERR_NULL;
+    if (!routing_shape_ok(w->T, w->E, w->k) || !w4_shape_ok(w->T, w->k, w->d, w->h))
+        return MOE_ERR_SHAPE;
+    if (w->T == 0) return MOE_OK;
+    if (!w->x || !w->topk_gate || !w->token_pos || !w->sorted_token || !w->offsets || !w->w1q ||
+        !w->w1_scale || !w->w2q || !w->w2_scale || !w->out || !w->ws)
+        return MOE_ERR_NULL;
+    if (!aligned16(w->x) || !aligned16(w->out) || !aligned16(w->w1q) || !aligned16(w->w2q) ||
+        !aligned16(w->ws))
+        return MOE_ERR_ALIGN;
+    if (w->ws_bytes < w4_ws_bytes(w->T * w->k, w->d, w->h)) return MOE_ERR_WORKSPACE;
+    return w4_experts_launch(w, (hipStream_t)stream);
 }
 
 size_t mxfp8_col_blocks(int64_t rows, int32_t n_groups) { return moe::mxfp8_col_blocks(rows, n_groups); }
