@@ -442,8 +442,8 @@ def moe_backward(saved: dict, dout: torch.Tensor, E: int, k: int, d: int, h: int
         names += ("y_perm",)
     else:
         act = torch.bfloat16 if mxfp8 else dt
-        _act8_need(act8["ab8"], act8["ab8_scale"], R, 2 * h, dev, "ab8")
-        _act8_need(act8["y8"], act8["y8_scale"], R, d, dev, "y8")
+        _act8_need(act8["ab8"], act8["ab8_scale"], R, 2 * h, dout.get_device(), "ab8")
+        _act8_need(act8["y8"], act8["y8_scale"], R, d, dout.get_device(), "y8")
         _need(saved["ab"], (R, 2 * h), act, "ab")
         if saved.get("hp") is not None or not mxfp8:
             _need(saved["hp"], (R, h), act, "hp")
@@ -621,100 +621,112 @@ def moe_capacity_zero_rows(buf: torch.Tensor, offsets: torch.Tensor, capacity: i
 # 8-bit activation checkpoints and the layer norm
 
 
-class _On:
-    """The stream of `dev` that work is issued on, with `dev` current while
-    the call is made (tensors need not be on the current device)."""
+# The stream handle and the current device without the objects around them:
+# torch.cuda.current_stream() costs as much host time as a kernel launch.
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
+    lambda index: torch.cuda.current_stream(index).cuda_stream)
+_cur_device = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
 
-    def __init__(self, dev):
-        self.dev = dev
 
-    def __enter__(self):
-        self.before = torch.cuda.current_device()
-        if self.dev.index != self.before:
-            torch.cuda.set_device(self.dev)
-        return torch.cuda.current_stream(self.dev).cuda_stream
-
-    def __exit__(self, *exc):
-        if self.dev.index != self.before:
-            torch.cuda.set_device(self.before)
+def _enqueue(name, fn, index, *args):
+    """fn(*args, stream) on GPU `index`'s current stream, with that GPU
+    current while the call is made (tensors need not be on the current one)."""
+    if _cur_device() == index:
+        st = fn(*args, _raw_stream(index))
+    else:
+        with torch.cuda.device(index):
+            st = fn(*args, _raw_stream(index))
+    if st != MOE_OK:
+        raise MoeError(name, st)
 
 
 def _ptr(t):
     return None if t is None else t.data_ptr()
 
 
-def _need_on(t, shape, dtype, dev, name):
-    """t is a contiguous tensor of this shape and dtype on the GPU `dev`."""
+def _need_on(t, shape, dtype, index, name):
+    """t is a contiguous tensor of this shape and dtype on GPU `index`."""
     if t is None:
         raise ValueError(f"{name} is required")
-    if t.shape != shape or t.dtype != dtype or not t.is_contiguous() or not t.is_cuda or \
-            t.device != dev:
-        raise ValueError(f"{name}: expected contiguous {dtype} {tuple(shape)} on {dev}, got "
+    if t.dtype is not dtype or t.get_device() != index or index < 0 or t.shape != shape or \
+            not t.is_contiguous():
+        raise ValueError(f"{name}: expected contiguous {dtype} {tuple(shape)} on "
+                         f"{'a GPU' if index < 0 else f'cuda:{index}'}, got "
                          f"{t.dtype} {tuple(t.shape)} (contiguous={t.is_contiguous()}, "
                          f"device={t.device})")
 
 
 def _act_matrix(x, name):
     """rows, cols of a contiguous 2-d f32 / bf16 GPU tensor whose rows are
-    whole blocks of 32, and its C dtype."""
+    whole blocks of 32, its C dtype and its GPU."""
     if x is None:
         raise ValueError(f"{name} is required")
-    if x.dtype != torch.bfloat16 and x.dtype != torch.float32:
+    if x.dtype is torch.bfloat16:
+        dt = MOE_BF16
+    elif x.dtype is torch.float32:
+        dt = MOE_F32
+    else:
         raise ValueError(f"{name}: expected bf16 or f32, got {x.dtype}")
-    if x.dim() != 2 or x.shape[1] < 32 or x.shape[1] % 32:
-        raise ValueError(f"{name}: expected [rows, a multiple of 32], got {tuple(x.shape)}")
-    _need_on(x, x.shape, x.dtype, x.device, name)
-    return x.shape[0], x.shape[1], MOE_BF16 if x.dtype == torch.bfloat16 else MOE_F32
+    shape, index = x.shape, x.get_device()
+    if len(shape) != 2 or shape[1] < 32 or shape[1] % 32:
+        raise ValueError(f"{name}: expected [rows, a multiple of 32], got {tuple(shape)}")
+    if index < 0 or not x.is_contiguous():
+        raise ValueError(f"{name}: expected a contiguous tensor on a GPU, got device={x.device}, "
+                         f"contiguous={x.is_contiguous()}")
+    return shape[0], shape[1], dt, index
 
 
-def _act8_need(q, scale, rows, cols, dev, name):
-    _need_on(q, (rows, cols), torch.uint8, dev, name)
-    _need_on(scale, (rows, cols // 32), torch.uint8, dev, name + "_scale")
+def _act8_need(q, scale, rows, cols, index, name):
+    _need_on(q, (rows, cols), torch.uint8, index, name)
+    _need_on(scale, (rows, cols // 32), torch.uint8, index, name + "_scale")
 
 
-def _act8_out(rows, cols, dev, q, scale, name):
+def _act8_new(rows, cols, dev):
+    u8 = dict(dtype=torch.uint8, device=dev)
+    return torch.empty((rows, cols), **u8), torch.empty((rows, cols // 32), **u8)
+
+
+def _act8_out(rows, cols, like, index, q, scale, name):
     """The tensors of a checkpoint to be written: the caller's, or new ones."""
-    if q is None:
-        q = torch.empty((rows, cols), dtype=torch.uint8, device=dev)
-    if scale is None:
-        scale = torch.empty((rows, cols // 32), dtype=torch.uint8, device=dev)
-    _act8_need(q, scale, rows, cols, dev, name)
+    if q is None and scale is None:
+        return _act8_new(rows, cols, like.device)
+    _act8_need(q, scale, rows, cols, index, name)
     return q, scale
 
 
 def _act8_in(q, scale, dtype, name):
-    if dtype != torch.bfloat16 and dtype != torch.float32:
+    if dtype is not torch.bfloat16 and dtype is not torch.float32:
         raise ValueError(f"dtype: expected bf16 or f32, got {dtype}")
     if q is None or q.dim() != 2 or q.shape[1] < 32 or q.shape[1] % 32:
         raise ValueError(f"{name}: expected [rows, a multiple of 32], got "
                          f"{None if q is None else tuple(q.shape)}")
     rows, cols = q.shape
-    _act8_need(q, scale, rows, cols, q.device, name)
-    return rows, cols, MOE_BF16 if dtype == torch.bfloat16 else MOE_F32
+    index = q.get_device()
+    _act8_need(q, scale, rows, cols, index, name)
+    return rows, cols, MOE_BF16 if dtype is torch.bfloat16 else MOE_F32, index
 
 
 def moe_act8_store(x: torch.Tensor, q: torch.Tensor | None = None,
                    scale: torch.Tensor | None = None):
     """The 8-bit checkpoint (MXINT8, see moe.h) of x [rows, cols]: uint8 q
     [rows, cols] and scale [rows, cols/32]."""
-    rows, cols, dt = _act_matrix(x, "x")
-    q, scale = _act8_out(rows, cols, x.device, q, scale, "q")
-    with _On(x.device) as s:
-        _check("moe_act8_store", _lib.moe_act8_store(_ptr(x), dt, rows, cols, _ptr(q),
-                                                     _ptr(scale), s))
+    rows, cols, dt, gpu = _act_matrix(x, "x")
+    q, scale = _act8_out(rows, cols, x, gpu, q, scale, "q")
+    _enqueue("moe_act8_store", _lib.moe_act8_store, gpu, x.data_ptr(), dt, rows, cols,
+             q.data_ptr(), scale.data_ptr())
     return q, scale
 
 
 def moe_act8_load(q: torch.Tensor, scale: torch.Tensor, dtype: torch.dtype = torch.bfloat16,
                   out: torch.Tensor | None = None) -> torch.Tensor:
     """The values that a checkpoint stands for, as `dtype` (exact in both)."""
-    rows, cols, dt = _act8_in(q, scale, dtype, "q")
+    rows, cols, dt, gpu = _act8_in(q, scale, dtype, "q")
     if out is None:
         out = torch.empty((rows, cols), dtype=dtype, device=q.device)
-    _need_on(out, (rows, cols), dtype, q.device, "out")
-    with _On(q.device) as s:
-        _check("moe_act8_load", _lib.moe_act8_load(_ptr(q), _ptr(scale), dt, rows, cols, _ptr(out),
-                                                   s))
+    else:
+        _need_on(out, (rows, cols), dtype, gpu, "out")
+    _enqueue("moe_act8_load", _lib.moe_act8_load, gpu, q.data_ptr(), scale.data_ptr(), dt, rows,
+             cols, out.data_ptr())
     return out
 
 
@@ -723,20 +735,29 @@ def moe_act8_swiglu(ab8: torch.Tensor, ab8_scale: torch.Tensor,
                     hp: torch.Tensor | None = None):
     """From the checkpoint of A||B [rows, 2h]: (ab, hp), its values and
     H' = silu(a) b of them."""
-    rows, cols, dt = _act8_in(ab8, ab8_scale, dtype, "ab8")
+    rows, cols, dt, gpu = _act8_in(ab8, ab8_scale, dtype, "ab8")
     h = cols // 2
     if h % 32:
         raise ValueError(f"ab8: the hidden width must be a multiple of 32, got {h}")
     if ab is None:
         ab = torch.empty((rows, cols), dtype=dtype, device=ab8.device)
+    else:
+        _need_on(ab, (rows, cols), dtype, gpu, "ab")
     if hp is None:
         hp = torch.empty((rows, h), dtype=dtype, device=ab8.device)
-    _need_on(ab, (rows, cols), dtype, ab8.device, "ab")
-    _need_on(hp, (rows, h), dtype, ab8.device, "hp")
-    with _On(ab8.device) as s:
-        _check("moe_act8_swiglu", _lib.moe_act8_swiglu(_ptr(ab8), _ptr(ab8_scale), dt, rows, h,
-                                                       _ptr(ab), _ptr(hp), s))
+    else:
+        _need_on(hp, (rows, h), dtype, gpu, "hp")
+    _enqueue("moe_act8_swiglu", _lib.moe_act8_swiglu, gpu, ab8.data_ptr(), ab8_scale.data_ptr(),
+             dt, rows, h, ab.data_ptr(), hp.data_ptr())
     return ab, hp
+
+
+def _slots(token_pos, T=None):
+    """(T, k) of a [T, k] tensor."""
+    if token_pos is None or token_pos.dim() != 2 or T not in (None, token_pos.shape[0]):
+        raise ValueError(f"token_pos: expected [{'T' if T is None else T}, k], got "
+                         f"{None if token_pos is None else tuple(token_pos.shape)}")
+    return token_pos.shape[0], token_pos.shape[1]
 
 
 def moe_combine_act8(y_perm: torch.Tensor, topk_gate: torch.Tensor, token_pos: torch.Tensor,
@@ -745,19 +766,18 @@ def moe_combine_act8(y_perm: torch.Tensor, topk_gate: torch.Tensor, token_pos: t
     """moe_combine that also stores the checkpoint of the rows it reads:
     (out [T, d], y8 [R, d], y8_scale [R, d/32]). token_pos must stay below R,
     the rows of y_perm."""
-    rows, d, dt = _act_matrix(y_perm, "y_perm")
-    dev = y_perm.device
-    T, k = token_pos.shape
-    _need_on(token_pos, (T, k), torch.int32, dev, "token_pos")
-    _need_on(topk_gate, (T, k), torch.float32, dev, "topk_gate")
+    rows, d, dt, gpu = _act_matrix(y_perm, "y_perm")
+    T, k = _slots(token_pos)
+    _need_on(token_pos, (T, k), torch.int32, gpu, "token_pos")
+    _need_on(topk_gate, (T, k), torch.float32, gpu, "topk_gate")
     if out is None:
-        out = torch.empty((T, d), dtype=y_perm.dtype, device=dev)
-    _need_on(out, (T, d), y_perm.dtype, dev, "out")
-    y8, y8_scale = _act8_out(rows, d, dev, y8, y8_scale, "y8")
-    with _On(dev) as s:
-        _check("moe_combine_act8", _lib.moe_combine_act8(
-            _ptr(y_perm), dt, _ptr(topk_gate), _ptr(token_pos), T, d, k, _ptr(out), _ptr(y8),
-            _ptr(y8_scale), s))
+        out = torch.empty((T, d), dtype=y_perm.dtype, device=y_perm.device)
+    else:
+        _need_on(out, (T, d), y_perm.dtype, gpu, "out")
+    y8, y8_scale = _act8_out(rows, d, y_perm, gpu, y8, y8_scale, "y8")
+    _enqueue("moe_combine_act8", _lib.moe_combine_act8, gpu, y_perm.data_ptr(), dt,
+             topk_gate.data_ptr(), token_pos.data_ptr(), T, d, k, out.data_ptr(), y8.data_ptr(),
+             y8_scale.data_ptr())
     return out, y8, y8_scale
 
 
@@ -768,30 +788,30 @@ def moe_combine_backward_act8(dout: torch.Tensor, y8: torch.Tensor, y8_scale: to
     """The combine's backward with the router's, y_perm read from its
     checkpoint (see moe.h): dict of dy_perm [R, d], dlogits [T, E], dgate
     [T, k]. With `out`, into its tensors (dgate only if it has one)."""
-    T, d, dt = _act_matrix(dout, "dout")
-    dev = dout.device
+    T, d, dt, gpu = _act_matrix(dout, "dout")
     if y8 is None or y8.dim() != 2:
         raise ValueError("y8: expected [rows, d]")
-    R, k = y8.shape[0], token_pos.shape[1]
-    _act8_need(y8, y8_scale, R, d, dev, "y8")
-    _need_on(topk_gate, (T, k), torch.float32, dev, "topk_gate")
-    _need_on(topk_idx, (T, k), torch.int32, dev, "topk_idx")
-    _need_on(token_pos, (T, k), torch.int32, dev, "token_pos")
+    R = y8.shape[0]
+    _, k = _slots(token_pos, T)
+    _act8_need(y8, y8_scale, R, d, gpu, "y8")
+    _need_on(topk_gate, (T, k), torch.float32, gpu, "topk_gate")
+    _need_on(topk_idx, (T, k), torch.int32, gpu, "topk_idx")
+    _need_on(token_pos, (T, k), torch.int32, gpu, "token_pos")
     if out is None:
+        dev = dout.device
         out = dict(dy_perm=torch.empty((R, d), dtype=dout.dtype, device=dev),
                    dlogits=torch.empty((T, E), dtype=torch.float32, device=dev))
         if want_dgate:
             out["dgate"] = torch.empty((T, k), dtype=torch.float32, device=dev)
-    _need_on(out["dy_perm"], (R, d), dout.dtype, dev, "dy_perm")
-    _need_on(out["dlogits"], (T, E), torch.float32, dev, "dlogits")
-    dgate = out.get("dgate")
-    if dgate is not None:
-        _need_on(dgate, (T, k), torch.float32, dev, "dgate")
-    with _On(dev) as s:
-        _check("moe_combine_backward_act8", _lib.moe_combine_backward_act8(
-            _ptr(dout), dt, _ptr(y8), _ptr(y8_scale), _ptr(topk_gate), _ptr(topk_idx),
-            _ptr(token_pos), T, d, k, E, _ptr(out["dy_perm"]), _ptr(out["dlogits"]), _ptr(dgate),
-            s))
+    else:
+        _need_on(out.get("dy_perm"), (R, d), dout.dtype, gpu, "dy_perm")
+        _need_on(out.get("dlogits"), (T, E), torch.float32, gpu, "dlogits")
+        if out.get("dgate") is not None:
+            _need_on(out["dgate"], (T, k), torch.float32, gpu, "dgate")
+    _enqueue("moe_combine_backward_act8", _lib.moe_combine_backward_act8, gpu, dout.data_ptr(), dt,
+             y8.data_ptr(), y8_scale.data_ptr(), topk_gate.data_ptr(), topk_idx.data_ptr(),
+             token_pos.data_ptr(), T, d, k, E, out["dy_perm"].data_ptr(),
+             out["dlogits"].data_ptr(), _ptr(out.get("dgate")))
     return out
 
 
@@ -803,14 +823,15 @@ def moe_layer_norm(x: torch.Tensor, weight: torch.Tensor, bias: torch.Tensor | N
     stats mean and rstd [T] fp32 for the backward; with act8 x8 and x8_scale,
     the normalised input's 8-bit checkpoint. `out`: a dict of an earlier call
     with the same arguments, whose tensors are written again."""
-    T, d, dt = _act_matrix(x, "x")
-    dev, f32 = x.device, torch.float32
-    _need_on(weight, (d,), f32, dev, "weight")
+    T, d, dt, gpu = _act_matrix(x, "x")
+    f32 = torch.float32
+    _need_on(weight, (d,), f32, gpu, "weight")
     if bias is not None:
-        _need_on(bias, (d,), f32, dev, "bias")
+        _need_on(bias, (d,), f32, gpu, "bias")
     if residual is not None:
-        _need_on(residual, (T, d), x.dtype, dev, "residual")
+        _need_on(residual, (T, d), x.dtype, gpu, "residual")
     if out is None:
+        dev = x.device
         out = dict(y=torch.empty((T, d), dtype=x.dtype, device=dev))
         if residual is not None:
             out["sum"] = torch.empty((T, d), dtype=x.dtype, device=dev)
@@ -818,27 +839,37 @@ def moe_layer_norm(x: torch.Tensor, weight: torch.Tensor, bias: torch.Tensor | N
             out["mean"] = torch.empty(T, dtype=f32, device=dev)
             out["rstd"] = torch.empty(T, dtype=f32, device=dev)
         if act8:
-            out["x8"], out["x8_scale"] = _act8_out(T, d, dev, None, None, "x8")
+            out["x8"], out["x8_scale"] = _act8_new(T, d, dev)
     else:
-        _need_on(out.get("y"), (T, d), x.dtype, dev, "y")
+        _need_on(out.get("y"), (T, d), x.dtype, gpu, "y")
         if residual is not None:
-            _need_on(out.get("sum"), (T, d), x.dtype, dev, "sum")
+            _need_on(out.get("sum"), (T, d), x.dtype, gpu, "sum")
         if stats:
-            _need_on(out.get("mean"), (T,), f32, dev, "mean")
-            _need_on(out.get("rstd"), (T,), f32, dev, "rstd")
+            _need_on(out.get("mean"), (T,), f32, gpu, "mean")
+            _need_on(out.get("rstd"), (T,), f32, gpu, "rstd")
         if act8:
-            _act8_need(out.get("x8"), out.get("x8_scale"), T, d, dev, "x8")
-    with _On(dev) as s:
-        _check("moe_layer_norm", _lib.moe_layer_norm(
-            _ptr(x), dt, _ptr(residual), _ptr(weight), _ptr(bias), eps, T, d, _ptr(out["y"]),
-            _ptr(out["sum"]) if residual is not None else None,
-            _ptr(out["mean"]) if stats else None, _ptr(out["rstd"]) if stats else None,
-            _ptr(out["x8"]) if act8 else None, _ptr(out["x8_scale"]) if act8 else None, s))
+            _act8_need(out.get("x8"), out.get("x8_scale"), T, d, gpu, "x8")
+    _enqueue("moe_layer_norm", _lib.moe_layer_norm, gpu, x.data_ptr(), dt, _ptr(residual),
+             weight.data_ptr(), _ptr(bias), eps, T, d, out["y"].data_ptr(),
+             None if residual is None else out["sum"].data_ptr(),
+             out["mean"].data_ptr() if stats else None, out["rstd"].data_ptr() if stats else None,
+             out["x8"].data_ptr() if act8 else None,
+             out["x8_scale"].data_ptr() if act8 else None)
     return out
 
 
 def moe_layer_norm_backward_workspace_size(dtype: int, T: int, d: int) -> int:
-    return int(_lib.moe_layer_norm_backward_workspace_size(dtype, T, d))
+    return _lib.moe_layer_norm_backward_workspace_size(dtype, T, d)
+
+
+def _need_ws(ws, nbytes, like, gpu):
+    """The caller's workspace, checked, or a new one."""
+    if ws is None:
+        return torch.empty(max(nbytes, 16), dtype=torch.uint8, device=like.device)
+    _need_bytes(ws, nbytes, "ws")
+    if ws.get_device() != gpu:
+        raise ValueError(f"ws: expected on cuda:{gpu}, got {ws.device}")
+    return ws
 
 
 def moe_layer_norm_backward(saved: dict, dy: torch.Tensor, weight: torch.Tensor,
@@ -851,48 +882,44 @@ def moe_layer_norm_backward(saved: dict, dy: torch.Tensor, weight: torch.Tensor,
     dbias [d] fp32. dsum: the gradient that reaches x (or sum) by its other
     uses, added to dx. out: tensors of an earlier call; accumulate_dw adds to
     its dweight and dbias."""
-    T, d, dt = _act_matrix(dy, "dy")
-    dev, f32 = dy.device, torch.float32
+    T, d, dt, gpu = _act_matrix(dy, "dy")
+    f32 = torch.float32
     x = saved.get("x")
     x8 = x8s = None
     if x is not None:
-        _need_on(x, (T, d), dy.dtype, dev, "x")
+        _need_on(x, (T, d), dy.dtype, gpu, "x")
     else:
         x8, x8s = saved.get("x8"), saved.get("x8_scale")
-        _act8_need(x8, x8s, T, d, dev, "x8")
-    _need_on(saved.get("mean"), (T,), f32, dev, "mean")
-    _need_on(saved.get("rstd"), (T,), f32, dev, "rstd")
-    _need_on(weight, (d,), f32, dev, "weight")
+        _act8_need(x8, x8s, T, d, gpu, "x8")
+    mean, rstd = saved.get("mean"), saved.get("rstd")
+    _need_on(mean, (T,), f32, gpu, "mean")
+    _need_on(rstd, (T,), f32, gpu, "rstd")
+    _need_on(weight, (d,), f32, gpu, "weight")
     if dsum is not None:
-        _need_on(dsum, (T, d), dy.dtype, dev, "dsum")
+        _need_on(dsum, (T, d), dy.dtype, gpu, "dsum")
     if out is None:
         if accumulate_dw:
             raise ValueError("accumulate_dw needs the gradients of an earlier backward (out)")
+        dev = dy.device
         out = dict(dx=torch.empty((T, d), dtype=dy.dtype, device=dev))
         if want_dweight:
             out["dweight"] = torch.empty(d, dtype=f32, device=dev)
         if want_dbias:
             out["dbias"] = torch.empty(d, dtype=f32, device=dev)
     else:
-        _need_on(out.get("dx"), (T, d), dy.dtype, dev, "dx")
+        _need_on(out.get("dx"), (T, d), dy.dtype, gpu, "dx")
         if want_dweight:
-            _need_on(out.get("dweight"), (d,), f32, dev, "dweight")
+            _need_on(out.get("dweight"), (d,), f32, gpu, "dweight")
         if want_dbias:
-            _need_on(out.get("dbias"), (d,), f32, dev, "dbias")
+            _need_on(out.get("dbias"), (d,), f32, gpu, "dbias")
     if want_dweight or want_dbias:
-        wsb = moe_layer_norm_backward_workspace_size(dt, T, d)
-        if ws is None:
-            ws = torch.empty(max(wsb, 16), dtype=torch.uint8, device=dev)
-        _need_bytes(ws, wsb, "ws")
-        if ws.device != dev:
-            raise ValueError(f"ws: expected on {dev}, got {ws.device}")
-    with _On(dev) as s:
-        _check("moe_layer_norm_backward", _lib.moe_layer_norm_backward(
-            _ptr(dy), dt, _ptr(x), _ptr(x8), _ptr(x8s), _ptr(saved["mean"]), _ptr(saved["rstd"]),
-            _ptr(weight), _ptr(dsum), T, d, _ptr(out["dx"]),
-            _ptr(out["dweight"]) if want_dweight else None,
-            _ptr(out["dbias"]) if want_dbias else None, 1 if accumulate_dw else 0, _ptr(ws),
-            ws.numel() if ws is not None else 0, s))
+        ws = _need_ws(ws, moe_layer_norm_backward_workspace_size(dt, T, d), dy, gpu)
+    _enqueue("moe_layer_norm_backward", _lib.moe_layer_norm_backward, gpu, dy.data_ptr(), dt,
+             _ptr(x), _ptr(x8), _ptr(x8s), mean.data_ptr(), rstd.data_ptr(), weight.data_ptr(),
+             _ptr(dsum), T, d, out["dx"].data_ptr(),
+             out["dweight"].data_ptr() if want_dweight else None,
+             out["dbias"].data_ptr() if want_dbias else None, 1 if accumulate_dw else 0, _ptr(ws),
+             0 if ws is None else ws.numel())
     return out
 
 
@@ -906,22 +933,23 @@ def moe_w4_quantize(w: torch.Tensor, q: torch.Tensor | None = None,
     bf16) along its rows: q [..., rows, cols/2] and scale [..., rows, cols/32]."""
     if w is None or w.dim() < 2:
         raise ValueError("w: expected [..., rows, cols]")
-    rows, cols, dt = _act_matrix(w.reshape(-1, w.shape[-1]) if w.is_contiguous() else w, "w")
+    if not w.is_contiguous():
+        raise ValueError("w: expected a contiguous tensor")
+    rows, cols, dt, gpu = _act_matrix(w.reshape(-1, w.shape[-1]), "w")
     lead = tuple(w.shape[:-1])
     if q is None:
         q = torch.empty(lead + (cols // 2,), dtype=torch.uint8, device=w.device)
     if scale is None:
         scale = torch.empty(lead + (cols // 32,), dtype=torch.uint8, device=w.device)
-    _need_on(q, lead + (cols // 2,), torch.uint8, w.device, "q")
-    _need_on(scale, lead + (cols // 32,), torch.uint8, w.device, "scale")
-    with _On(w.device) as s:
-        _check("moe_w4_quantize", _lib.moe_w4_quantize(_ptr(w), dt, rows, cols, _ptr(q),
-                                                       _ptr(scale), s))
+    _need_on(q, lead + (cols // 2,), torch.uint8, gpu, "q")
+    _need_on(scale, lead + (cols // 32,), torch.uint8, gpu, "scale")
+    _enqueue("moe_w4_quantize", _lib.moe_w4_quantize, gpu, w.data_ptr(), dt, rows, cols,
+             q.data_ptr(), scale.data_ptr())
     return q, scale
 
 
 def moe_w4_experts_workspace_size(T: int, k: int, d: int, h: int) -> int:
-    return int(_lib.moe_w4_experts_workspace_size(T, k, d, h))
+    return _lib.moe_w4_experts_workspace_size(T, k, d, h)
 
 
 def moe_w4_experts(x: torch.Tensor, route: dict, w1q: torch.Tensor, w1_scale: torch.Tensor,
@@ -930,36 +958,34 @@ def moe_w4_experts(x: torch.Tensor, route: dict, w1q: torch.Tensor, w1_scale: to
     """The expert layer's forward for few tokens after the routing, weights
     as moe_w4_quantize writes them (see moe.h). route: moe_route's dict for
     these tokens (topk_gate, token_pos, sorted_token, offsets are read)."""
-    T, d, dt = _act_matrix(x, "x")
+    T, d, dt, gpu = _act_matrix(x, "x")
     if dt != MOE_BF16:
         raise ValueError(f"x: expected bf16, got {x.dtype}")
-    dev, u8, i32 = x.device, torch.uint8, torch.int32
+    u8, i32 = torch.uint8, torch.int32
     if w1q is None or w1q.dim() != 3 or w1q.shape[1] % 64:
         raise ValueError("w1q: expected [E, 2h, d/2] with h a multiple of 32")
-    E, h = w1q.shape[0], w1q.shape[1] // 2
-    k = route["token_pos"].shape[-1]
-    _need_on(w1q, (E, 2 * h, d // 2), u8, dev, "w1q")
-    _need_on(w1_scale, (E, 2 * h, d // 32), u8, dev, "w1_scale")
-    _need_on(w2q, (E, d, h // 2), u8, dev, "w2q")
-    _need_on(w2_scale, (E, d, h // 32), u8, dev, "w2_scale")
-    _need_on(route["topk_gate"], (T, k), torch.float32, dev, "topk_gate")
-    _need_on(route["token_pos"], (T, k), i32, dev, "token_pos")
-    _need_on(route["sorted_token"], (T * k,), i32, dev, "sorted_token")
-    _need_on(route["offsets"], (E + 1,), i32, dev, "offsets")
+    E, h2 = w1q.shape[0], w1q.shape[1]
+    h = h2 // 2
+    gate, pos, tok, off = (route.get(n) for n in ("topk_gate", "token_pos", "sorted_token",
+                                                  "offsets"))
+    _, k = _slots(pos, T)
+    _need_on(w1q, (E, h2, d // 2), u8, gpu, "w1q")
+    _need_on(w1_scale, (E, h2, d // 32), u8, gpu, "w1_scale")
+    _need_on(w2q, (E, d, h // 2), u8, gpu, "w2q")
+    _need_on(w2_scale, (E, d, h // 32), u8, gpu, "w2_scale")
+    _need_on(gate, (T, k), torch.float32, gpu, "topk_gate")
+    _need_on(pos, (T, k), i32, gpu, "token_pos")
+    _need_on(tok, (T * k,), i32, gpu, "sorted_token")
+    _need_on(off, (E + 1,), i32, gpu, "offsets")
     if out is None:
-        out = torch.empty((T, d), dtype=x.dtype, device=dev)
-    _need_on(out, (T, d), x.dtype, dev, "out")
-    wsb = moe_w4_experts_workspace_size(T, k, d, h)
-    if ws is None:
-        ws = torch.empty(max(wsb, 16), dtype=u8, device=dev)
-    _need_bytes(ws, wsb, "ws")
-    if ws.device != dev:
-        raise ValueError(f"ws: expected on {dev}, got {ws.device}")
-    w = W4Desc(d, h, E, k, T, _ptr(x), _ptr(route["topk_gate"]), _ptr(route["token_pos"]),
-               _ptr(route["sorted_token"]), _ptr(route["offsets"]), _ptr(w1q), _ptr(w1_scale),
-               _ptr(w2q), _ptr(w2_scale), _ptr(out), _ptr(ws), ws.numel())
-    with _On(dev) as s:
-        _check("moe_w4_experts", _lib.moe_w4_experts(ctypes.byref(w), s))
+        out = torch.empty((T, d), dtype=x.dtype, device=x.device)
+    else:
+        _need_on(out, (T, d), x.dtype, gpu, "out")
+    ws = _need_ws(ws, moe_w4_experts_workspace_size(T, k, d, h), x, gpu)
+    w = W4Desc(d, h, E, k, T, x.data_ptr(), gate.data_ptr(), pos.data_ptr(), tok.data_ptr(),
+               off.data_ptr(), w1q.data_ptr(), w1_scale.data_ptr(), w2q.data_ptr(),
+               w2_scale.data_ptr(), out.data_ptr(), ws.data_ptr(), ws.numel())
+    _enqueue("moe_w4_experts", _lib.moe_w4_experts, gpu, ctypes.byref(w))
     return out
 
 
@@ -1106,8 +1132,8 @@ def _norm_grads(norm, grads):
 
 def _act8_buffers(R, d, h, dev):
     """The checkpoints that a layer holds: of A||B and of y_perm."""
-    ab8, ab8_scale = _act8_out(R, 2 * h, dev, None, None, "ab8")
-    y8, y8_scale = _act8_out(R, d, dev, None, None, "y8")
+    ab8, ab8_scale = _act8_new(R, 2 * h, dev)
+    y8, y8_scale = _act8_new(R, d, dev)
     return dict(ab8=ab8, ab8_scale=ab8_scale, y8=y8, y8_scale=y8_scale)
 
 
@@ -1518,7 +1544,7 @@ class MoELayerW4:
     def __init__(self, w1: torch.Tensor, w2: torch.Tensor, k: int):
         self.E, h2, self.d = w1.shape
         self.h, self.k = h2 // 2, k
-        _need_on(w2, (self.E, self.d, self.h), w2.dtype, w1.device, "w2")
+        _need_on(w2, (self.E, self.d, self.h), w2.dtype, w1.get_device(), "w2")
         self.prepare_weights(w1, w2)
         self._T = None
 
@@ -1530,9 +1556,9 @@ class MoELayerW4:
     def forward(self, x: torch.Tensor, logits: torch.Tensor) -> torch.Tensor:
         if x.dim() != 2 or x.shape[1] != self.d or x.dtype != torch.bfloat16:
             raise ValueError(f"x: expected bf16 [T, {self.d}], got {x.dtype} {tuple(x.shape)}")
-        T, dev = x.shape[0], self.w1q.device
-        _need_on(x, (T, self.d), torch.bfloat16, dev, "x")
-        _need_on(logits, (T, self.E), torch.float32, dev, "logits")
+        T, dev, gpu = x.shape[0], self.w1q.device, self.w1q.get_device()
+        _need_on(x, (T, self.d), torch.bfloat16, gpu, "x")
+        _need_on(logits, (T, self.E), torch.float32, gpu, "logits")
         if self._T != T:
             self.route, self.out = None, torch.empty((T, self.d), dtype=x.dtype, device=dev)
             self.route_ws = torch.empty(max(moe_route_workspace_size(T, self.E, self.k), 1),
@@ -1540,7 +1566,7 @@ class MoELayerW4:
             wsb = moe_w4_experts_workspace_size(T, self.k, self.d, self.h)
             self.ws = torch.empty(max(wsb, 16), dtype=torch.uint8, device=dev)
             self._T = T
-        with _On(dev):
+        with torch.cuda.device(gpu):
             self.route = moe_route(logits, self.k, out=self.route, ws=self.route_ws)
-            return moe_w4_experts(x, self.route, self.w1q, self.w1s, self.w2q, self.w2s, self.out,
-                                  self.ws)
+        return moe_w4_experts(x, self.route, self.w1q, self.w1s, self.w2q, self.w2s, self.out,
+                              self.ws)
