@@ -37,19 +37,30 @@ MOE_DEV float group_sum(float v) {
     return v;
 }
 
-// Sum over the row's G threads; with G = 256 a row is a workgroup: the four
-// waves' sums go through LDS (red: 4 floats, its own for every call between
-// two barriers of the row).
+// The waves' sums of a row that is a workgroup (G = 256 or 512 threads),
+// added in wave order.
+template <int G>
+MOE_DEV float waves_sum(const float *q) {
+    float v = (q[0] + q[1]) + (q[2] + q[3]);
+    if constexpr (G == 512) v += (q[4] + q[5]) + (q[6] + q[7]);
+    return v;
+}
+
+// Sum over the row's G threads (red: G / 64 floats of LDS, its own for every
+// call between two barriers of the row).
 template <int G>
 MOE_DEV float row_sum(float v, float *red) {
     v = group_sum<G>(v);
-    if constexpr (G == 256) {
+    if constexpr (G >= 256) {
         if ((threadIdx.x & 63) == 0) red[threadIdx.x >> 6] = v;
         __syncthreads();
-        v = (red[0] + red[1]) + (red[2] + red[3]);
+        v = waves_sum<G>(red);
     }
     return v;
 }
+
+// threads of a workgroup: its rows are G threads each
+constexpr int norm_threads(int g) { return g > 256 ? g : 256; }
 
 template <bool BF16>
 MOE_DEV void load_params(const float *p, int c, float *f) {
@@ -63,17 +74,17 @@ MOE_DEV void load_params(const float *p, int c, float *f) {
 
 // G threads a row, V 16-byte vectors a thread (vector lane + i G of the row).
 template <bool BF16, int G, int V>
-__global__ __launch_bounds__(256) void norm_fwd(
+__global__ __launch_bounds__(norm_threads(G)) void norm_fwd(
     const uint4 *__restrict__ x, const uint4 *__restrict__ res, const float *__restrict__ gamma,
     const float *__restrict__ beta, float eps, int64_t T, int nv, float inv_d,
     uint4 *__restrict__ y, uint4 *__restrict__ sum, float *__restrict__ mean,
     float *__restrict__ rstd, typename Codes<BF16>::type *__restrict__ x8,
     uint8_t *__restrict__ x8_scale) {
     typedef Row16<BF16> R;
-    __shared__ float red[8];
+    __shared__ float red[2][8];
     const int lane = threadIdx.x % G;
-    const int64_t t = (int64_t)blockIdx.x * (256 / G) + threadIdx.x / G;
-    if (t >= T) return;                         // G = 256: never (one row a block)
+    const int64_t t = (int64_t)blockIdx.x * (norm_threads(G) / G) + threadIdx.x / G;
+    if (t >= T) return;                         // G >= 256: never (one row a workgroup)
     const int64_t base = t * nv;
     uint4 w[V];
     float s1 = 0.f;
@@ -97,7 +108,7 @@ __global__ __launch_bounds__(256) void norm_fwd(
 #pragma unroll
         for (int e = 0; e < R::N; e++) s1 += f[e];
     }
-    const float mu = row_sum<G>(s1, red) * inv_d;
+    const float mu = row_sum<G>(s1, red[0]) * inv_d;
     float s2 = 0.f;
 #pragma unroll
     for (int i = 0; i < V; i++) {
@@ -107,7 +118,7 @@ __global__ __launch_bounds__(256) void norm_fwd(
 #pragma unroll
         for (int e = 0; e < R::N; e++) s2 = fmaf(f[e] - mu, f[e] - mu, s2);
     }
-    const float r = 1.f / sqrtf(fmaf(row_sum<G>(s2, red + 4), inv_d, eps));
+    const float r = 1.f / sqrtf(fmaf(row_sum<G>(s2, red[1]), inv_d, eps));
     if (lane == 0) {
         if (mean) mean[t] = mu;
         if (rstd) rstd[t] = r;
@@ -137,19 +148,30 @@ __global__ __launch_bounds__(256) void norm_fwd(
     }
 }
 
-// Backward: every workgroup takes rows blockIdx.x * (256 / G) + ..., strided
-// by the grid, and leaves its sums of dy xh and dy in part[blockIdx.x][0..1][d].
+// What a thread reads of one row in the backward pass.
+template <bool BF16, int V, bool CKPT>
+struct NormRow {
+    typedef typename Codes<BF16>::type C;
+    uint4 dy[V], ds[V], x[CKPT ? 1 : V];
+    C q[CKPT ? V : 1];
+    uint8_t sc[CKPT ? V : 1];
+    float mu, r;
+};
+
+// Backward: every workgroup takes rows blockIdx.x * RPB + ..., strided by the
+// grid, and leaves its sums of dy xh and dy in part[blockIdx.x][0..1][d]. A
+// row's loads are issued before the row in front of it is computed.
 template <bool BF16, int G, int V, bool CKPT>
-__global__ __launch_bounds__(256) void norm_bwd(
+__global__ __launch_bounds__(norm_threads(G)) void norm_bwd(
     const uint4 *__restrict__ dy, const uint4 *__restrict__ x,
     const typename Codes<BF16>::type *__restrict__ x8, const uint8_t *__restrict__ x8_scale,
     const float *__restrict__ mean, const float *__restrict__ rstd,
     const float *__restrict__ gamma, const uint4 *__restrict__ dsum, int64_t T, int nv, float inv_d,
     uint4 *__restrict__ dx, float *__restrict__ part) {
     typedef Row16<BF16> R;
-    constexpr int RPB = 256 / G;
-    __shared__ float red[2][8];
-    __shared__ float acc_s[G == 256 ? 1 : 256 * R::N];
+    constexpr int RPB = norm_threads(G) / G;
+    __shared__ float red[2][2][8];
+    __shared__ float acc_s[G >= 256 ? 1 : 256 * R::N];
     const int lane = threadIdx.x % G;
     float dg[V * R::N], db[V * R::N], ga[V * R::N];
 #pragma unroll
@@ -158,28 +180,46 @@ __global__ __launch_bounds__(256) void norm_bwd(
         for (int e = 0; e < R::N; e++) dg[i * R::N + e] = db[i * R::N + e] = ga[i * R::N + e] = 0.f;
         if (lane + i * G < nv) load_params<BF16>(gamma, lane + i * G, ga + i * R::N);
     }
-    int par = 0;
-    for (int64_t t = (int64_t)blockIdx.x * RPB + threadIdx.x / G; t < T;
-         t += (int64_t)gridDim.x * RPB, par ^= 1) {
+    typedef NormRow<BF16, V, CKPT> Row;
+    auto load = [&](Row &w, int64_t t) {
+        if (t >= T) return;
         const int64_t base = t * nv;
-        const float mu = mean[t], r = rstd[t];
-        uint4 wy[V];
-        float xh[V * R::N];
-        float c1 = 0.f, c2 = 0.f;
+        w.mu = mean[t];
+        w.r = rstd[t];
 #pragma unroll
         for (int i = 0; i < V; i++) {
             const int c = lane + i * G;
             if (c >= nv) continue;
-            wy[i] = dy[base + c];
+            w.dy[i] = dy[base + c];
+            if constexpr (CKPT) {
+                w.q[i] = x8[base + c];
+                w.sc[i] = x8_scale[(base + c) / R::LPB];
+            } else
+                w.x[i] = x[base + c];
+            if (dsum) w.ds[i] = dsum[base + c];
+        }
+    };
+    int par = 0;
+    const int64_t step = (int64_t)gridDim.x * RPB;
+    int64_t t = (int64_t)blockIdx.x * RPB + threadIdx.x / G;
+    Row next;
+    load(next, t);
+    for (; t < T; t += step, par ^= 1) {
+        const Row w = next;
+        load(next, t + step);
+        const int64_t base = t * nv;
+        float xh[V * R::N];
+        float c1 = 0.f, c2 = 0.f;
+#pragma unroll
+        for (int i = 0; i < V; i++) {
+            if (lane + i * G >= nv) continue;
             float f[R::N], g[R::N];
-            if constexpr (CKPT)
-                act8_decode(x8[base + c], act8_step(x8_scale[(base + c) / R::LPB]), f);
-            else
-                R::unpack(x[base + c], f);
-            R::unpack(wy[i], g);
+            if constexpr (CKPT) act8_decode(w.q[i], act8_step(w.sc[i]), f);
+            else R::unpack(w.x[i], f);
+            R::unpack(w.dy[i], g);
 #pragma unroll
             for (int e = 0; e < R::N; e++) {
-                const float h = (f[e] - mu) * r;
+                const float h = (f[e] - w.mu) * w.r;
                 xh[i * R::N + e] = h;
                 dg[i * R::N + e] = fmaf(g[e], h, dg[i * R::N + e]);
                 db[i * R::N + e] += g[e];
@@ -190,13 +230,15 @@ __global__ __launch_bounds__(256) void norm_bwd(
         }
         c1 = group_sum<G>(c1);
         c2 = group_sum<G>(c2);
-        if constexpr (G == 256) {
+        if constexpr (G >= 256) {
             // one barrier a row: the next row writes the other half
-            float *q = red[par];
-            if ((threadIdx.x & 63) == 0) { q[threadIdx.x >> 6] = c1; q[4 + (threadIdx.x >> 6)] = c2; }
+            if ((threadIdx.x & 63) == 0) {
+                red[par][0][threadIdx.x >> 6] = c1;
+                red[par][1][threadIdx.x >> 6] = c2;
+            }
             __syncthreads();
-            c1 = (q[0] + q[1]) + (q[2] + q[3]);
-            c2 = (q[4] + q[5]) + (q[6] + q[7]);
+            c1 = waves_sum<G>(red[par][0]);
+            c2 = waves_sum<G>(red[par][1]);
         }
         c1 *= inv_d;
         c2 *= inv_d;
@@ -205,13 +247,13 @@ __global__ __launch_bounds__(256) void norm_bwd(
             const int c = lane + i * G;
             if (c >= nv) continue;
             float g[R::N], o[R::N];
-            R::unpack(wy[i], g);
+            R::unpack(w.dy[i], g);
 #pragma unroll
             for (int e = 0; e < R::N; e++)
-                o[e] = r * (fmaf(-xh[i * R::N + e], c2, g[e] * ga[i * R::N + e]) - c1);
+                o[e] = w.r * (fmaf(-xh[i * R::N + e], c2, g[e] * ga[i * R::N + e]) - c1);
             if (dsum) {
                 float q[R::N];
-                R::unpack(dsum[base + c], q);
+                R::unpack(w.ds[i], q);
 #pragma unroll
                 for (int e = 0; e < R::N; e++) o[e] += q[e];
             }
@@ -228,10 +270,12 @@ __global__ __launch_bounds__(256) void norm_bwd(
 #pragma unroll
         for (int z = 0; z < 2; z++) {
             float *a = (z ? db : dg) + i * R::N, *p = z ? pb : pg;
-            if constexpr (G == 256) {
+            if constexpr (G >= 256) {
                 if (c < nv)
 #pragma unroll
-                    for (int e = 0; e < R::N; e++) p[(int64_t)c * R::N + e] = a[e];
+                    for (int e = 0; e < R::N; e += 4)
+                        *reinterpret_cast<float4 *>(p + (int64_t)c * R::N + e) =
+                            make_float4(a[e], a[e + 1], a[e + 2], a[e + 3]);
             } else {
                 __syncthreads();
 #pragma unroll
@@ -239,34 +283,42 @@ __global__ __launch_bounds__(256) void norm_bwd(
                 __syncthreads();
                 // G * N columns, RPB terms each
                 for (int m = threadIdx.x; m < G * R::N; m += 256) {
-                    const int e = m / G, l = m % G;
+                    const int e = m % R::N, l = m / R::N;
                     float s = 0.f;
+#pragma unroll
                     for (int b = 0; b < RPB; b++) s += acc_s[(b * R::N + e) * G + l];
-                    if (l + i * G < nv) p[(int64_t)(l + i * G) * R::N + e] = s;
+                    if (l + i * G < nv) p[(int64_t)i * G * R::N + m] = s;
                 }
             }
         }
     }
 }
 
-// dgamma, dbeta = (+=) the workgroups' sums, in their order: 32 columns a
-// workgroup, 8 slices of the rows each, then the slices in order.
-__global__ __launch_bounds__(256) void norm_bwd_params(const float *__restrict__ part, int np,
-                                                       int d, float *__restrict__ dgamma,
-                                                       float *__restrict__ dbeta, int accumulate) {
-    __shared__ float s_p[8][33];
+// dgamma, dbeta = (+=) the workgroups' sums: 32 columns a workgroup, the sums
+// dealt to 32 slices (16 loads of each in flight), the slices added in order.
+__global__ __launch_bounds__(1024) void norm_bwd_params(const float *__restrict__ part, int np,
+                                                        int d, float *__restrict__ dgamma,
+                                                        float *__restrict__ dbeta, int accumulate) {
+    __shared__ float s_p[32][33];
     const int z = blockIdx.y;
     float *out = z ? dbeta : dgamma;
     if (!out) return;
     const int col = blockIdx.x * 32 + (threadIdx.x & 31), sl = threadIdx.x >> 5;
+    const float *p = part + (int64_t)z * d + col;
     float s = 0.f;
-    for (int p = sl; p < np; p += 8) s += part[((int64_t)p * 2 + z) * d + col];
+    for (int i0 = sl; i0 < np; i0 += 32 * 16) {
+        float v[16];
+#pragma unroll
+        for (int i = 0; i < 16; i++) v[i] = i0 + 32 * i < np ? p[(int64_t)(i0 + 32 * i) * 2 * d] : 0.f;
+#pragma unroll
+        for (int i = 0; i < 16; i++) s += v[i];
+    }
     s_p[sl][threadIdx.x & 31] = s;
     __syncthreads();
     if (sl) return;
     s = 0.f;
 #pragma unroll
-    for (int i = 0; i < 8; i++) s += s_p[i][threadIdx.x];
+    for (int i = 0; i < 32; i++) s += s_p[i][threadIdx.x];
     out[col] = accumulate ? out[col] + s : s;
 }
 
@@ -277,42 +329,48 @@ __global__ __launch_bounds__(256) void norm_bwd_params(const float *__restrict__
 template <typename E, typename P>
 static E *at(P *p, int64_t n) { return p ? reinterpret_cast<E *>(p) + n : nullptr; }
 
-// threads a row for nv vectors
-static int norm_group(int nv) { return nv <= 32 ? 8 : nv <= 256 ? 64 : 256; }
+// threads a row for nv vectors: at most 32 elements a thread
+template <bool BF16>
+static int norm_group(int nv) {
+    return nv <= 32 ? 8 : nv <= 256 ? 64 : nv <= 1024 ? 256 : 512;
+}
 
-#define NORM_VSWITCH(v, F)                                                                     \
-    ((v) <= 1 ? F(1) : (v) <= 2 ? F(2) : (v) <= 3 ? F(3) : (v) <= 4 ? F(4) : (v) <= 6 ? F(6)   \
-     : (v) <= 8 ? F(8) : F(16))
-#define NORM_GVSWITCH(g, v, F)                                                                 \
-    ((g) == 8 ? NORM_VSWITCH(v, F##8) : (g) == 64 ? NORM_VSWITCH(v, F##64) : NORM_VSWITCH(v, F##256))
+// vectors a thread: 1..4 (bf16: 8 elements each; fp32 at 512 threads: up to 8)
+#define NORM_VSWITCH(v, F) ((v) <= 1 ? F(1) : (v) <= 2 ? F(2) : (v) <= 3 ? F(3) : F(4))
+#define NORM_GVSWITCH(g, v, F)                                                                  \
+    ((g) == 8 ? NORM_VSWITCH(v, F##8) : (g) == 64 ? NORM_VSWITCH(v, F##64)                      \
+     : (g) == 256 ? NORM_VSWITCH(v, F##256) : (v) <= 4 ? F##512(4) : F##512(8))
 
 template <bool BF16>
 static moe_status norm_fwd_run(const void *x, const void *res, const float *gamma,
                                const float *beta, float eps, int64_t T, int d, void *y, void *sum,
                                float *mean, float *rstd, uint8_t *x8, uint8_t *x8_scale,
                                hipStream_t s) {
-    const int nv = d / Row16<BF16>::N, g = norm_group(nv), v = (nv + g - 1) / g;
+    const int nv = d / Row16<BF16>::N, g = norm_group<BF16>(nv), v = (nv + g - 1) / g;
     const float inv_d = 1.f / (float)d;
     typedef typename Codes<BF16>::type C;
     // rows in pieces of at most kMaxBlocks workgroups (a grid has fewer than 2^32 threads)
-    const int64_t piece = kMaxBlocks * (256 / g);
+    const int nt = norm_threads(g), rows = nt / g;
+    const int64_t piece = kMaxBlocks / 2 * rows;
     for (int64_t t = 0; t < T; t += piece) {
         const int64_t n = T - t < piece ? T - t : piece;
-        const unsigned nb = (unsigned)((n + 256 / g - 1) / (256 / g));
+        const unsigned nb = (unsigned)((n + rows - 1) / rows);
         const int64_t o = t * nv;
 #define F(G, V)                                                                                  \
-    (norm_fwd<BF16, G, V><<<nb, 256, 0, s>>>(                                                    \
+    (norm_fwd<BF16, G, V><<<nb, nt, 0, s>>>(                                                     \
          at<const uint4>(x, o), at<const uint4>(res, o), gamma, beta, eps, n, nv, inv_d,         \
          at<uint4>(y, o), at<uint4>(sum, o), at<float>(mean, t), at<float>(rstd, t),             \
          at<C>(x8, o), at<uint8_t>(x8_scale, o / Row16<BF16>::LPB)), 0)
 #define F8(V) F(8, V)
 #define F64(V) F(64, V)
 #define F256(V) F(256, V)
+#define F512(V) F(512, V)
         NORM_GVSWITCH(g, v, F);
 #undef F
 #undef F8
 #undef F64
 #undef F256
+#undef F512
     }
     return launch_status();
 }
@@ -328,14 +386,16 @@ moe_status norm_fwd_launch(const void *x, moe_dtype dt, const void *res, const f
 
 // workgroups of the backward (and rows of its partial sums): by the sizes
 // alone, so that the workspace is the same on every device
-static int64_t norm_bwd_blocks(int64_t T, int d, int elems) {
-    const int rpb = 256 / norm_group(d / elems);
+template <bool BF16>
+static int64_t norm_bwd_blocks(int64_t T, int d) {
+    const int g = norm_group<BF16>(d / Row16<BF16>::N), rpb = norm_threads(g) / g;
     const int64_t most = (T + rpb - 1) / rpb;
     return most < 512 ? most : 512;
 }
 
 size_t norm_bwd_ws_bytes(moe_dtype dt, int64_t T, int d) {
-    return (size_t)norm_bwd_blocks(T, d, dt == MOE_BF16 ? 8 : 4) * 2 * d * sizeof(float);
+    const int64_t np = dt == MOE_BF16 ? norm_bwd_blocks<true>(T, d) : norm_bwd_blocks<false>(T, d);
+    return (size_t)np * 2 * d * sizeof(float);
 }
 
 template <bool BF16>
@@ -344,12 +404,12 @@ static moe_status norm_bwd_run(const void *dy, const void *x, const uint8_t *x8,
                                const float *gamma, const void *dsum, int64_t T, int d, void *dx,
                                float *dgamma, float *dbeta, bool accumulate, float *part,
                                hipStream_t s) {
-    const int nv = d / Row16<BF16>::N, g = norm_group(nv), v = (nv + g - 1) / g;
-    const int np = (int)norm_bwd_blocks(T, d, Row16<BF16>::N);
+    const int nv = d / Row16<BF16>::N, g = norm_group<BF16>(nv), v = (nv + g - 1) / g;
+    const int np = (int)norm_bwd_blocks<BF16>(T, d);
     const float inv_d = 1.f / (float)d;
     typedef typename Codes<BF16>::type C;
 #define F2(G, V, K)                                                                              \
-    (norm_bwd<BF16, G, V, K><<<np, 256, 0, s>>>(                                                 \
+    (norm_bwd<BF16, G, V, K><<<np, norm_threads(g), 0, s>>>(                                                 \
          reinterpret_cast<const uint4 *>(dy), reinterpret_cast<const uint4 *>(x),                \
          reinterpret_cast<const C *>(x8), x8_scale, mean, rstd, gamma,                           \
          reinterpret_cast<const uint4 *>(dsum), T, nv, inv_d, reinterpret_cast<uint4 *>(dx),     \
@@ -357,13 +417,15 @@ static moe_status norm_bwd_run(const void *dy, const void *x, const uint8_t *x8,
 #define F8(V) (x8 ? F2(8, V, true) : F2(8, V, false))
 #define F64(V) (x8 ? F2(64, V, true) : F2(64, V, false))
 #define F256(V) (x8 ? F2(256, V, true) : F2(256, V, false))
+#define F512(V) (x8 ? F2(512, V, true) : F2(512, V, false))
     if (np > 0) NORM_GVSWITCH(g, v, F);
 #undef F2
 #undef F8
 #undef F64
 #undef F256
+#undef F512
     if (dgamma || dbeta)
-        norm_bwd_params<<<dim3(d / 32, 2), 256, 0, s>>>(part, np, d, dgamma, dbeta, accumulate);
+        norm_bwd_params<<<dim3(d / 32, 2), 1024, 0, s>>>(part, np, d, dgamma, dbeta, accumulate);
     return launch_status();
 }
 
