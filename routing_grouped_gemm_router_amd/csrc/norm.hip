@@ -13,7 +13,8 @@
 
 namespace moe {
 
-// Sum of v over the G threads of a row: G = 8 or 64 neighbouring lanes.
+// Sum of v over the threads of a row within their wave: G = 4, 8, 16, 32 or
+// all 64 neighbouring lanes (G >= 64).
 MOE_DEV float swap16_sum(float v) {
     const auto r = __builtin_amdgcn_permlane16_swap(__float_as_uint(v), __float_as_uint(v), false,
                                                     false);
@@ -28,21 +29,20 @@ template <int G>
 MOE_DEV float group_sum(float v) {
     v += dpp_move<kDppXor1>(v);
     v += dpp_move<kDppXor2>(v);
-    v += dpp_move<kDppHalfMirror>(v);
-    if constexpr (G >= 64) {
-        v += dpp_move<kDppRowRor8>(v);
-        v = swap16_sum(v);
-        v = swap32_sum(v);
-    }
+    if constexpr (G >= 8) v += dpp_move<kDppHalfMirror>(v);
+    if constexpr (G >= 16) v += dpp_move<kDppRowRor8>(v);
+    if constexpr (G >= 32) v = swap16_sum(v);
+    if constexpr (G >= 64) v = swap32_sum(v);
     return v;
 }
 
-// The waves' sums of a row that is a workgroup (G = 256 or 512 threads),
-// added in wave order.
+// The waves' sums of a row that is a workgroup (G = 256, 512 or 1024
+// threads), added in a fixed order.
 template <int G>
 MOE_DEV float waves_sum(const float *q) {
-    float v = (q[0] + q[1]) + (q[2] + q[3]);
-    if constexpr (G == 512) v += (q[4] + q[5]) + (q[6] + q[7]);
+    float v = 0.f;
+#pragma unroll
+    for (int i = 0; i < G / 64; i += 4) v += (q[i] + q[i + 1]) + (q[i + 2] + q[i + 3]);
     return v;
 }
 
@@ -73,6 +73,7 @@ MOE_DEV void load_params(const float *p, int c, float *f) {
 }
 
 // G threads a row, V 16-byte vectors a thread (vector lane + i G of the row).
+
 template <bool BF16, int G, int V>
 __global__ __launch_bounds__(norm_threads(G)) void norm_fwd(
     const uint4 *__restrict__ x, const uint4 *__restrict__ res, const float *__restrict__ gamma,
@@ -81,7 +82,7 @@ __global__ __launch_bounds__(norm_threads(G)) void norm_fwd(
     float *__restrict__ rstd, typename Codes<BF16>::type *__restrict__ x8,
     uint8_t *__restrict__ x8_scale) {
     typedef Row16<BF16> R;
-    __shared__ float red[2][8];
+    __shared__ float red[2][16];
     const int lane = threadIdx.x % G;
     const int64_t t = (int64_t)blockIdx.x * (norm_threads(G) / G) + threadIdx.x / G;
     if (t >= T) return;                         // G >= 256: never (one row a workgroup)
@@ -170,15 +171,19 @@ __global__ __launch_bounds__(norm_threads(G)) void norm_bwd(
     uint4 *__restrict__ dx, float *__restrict__ part) {
     typedef Row16<BF16> R;
     constexpr int RPB = norm_threads(G) / G;
-    __shared__ float red[2][2][8];
+    __shared__ float red[2][2][16];
     __shared__ float acc_s[G >= 256 ? 1 : 256 * R::N];
     const int lane = threadIdx.x % G;
+    // a workgroup of 1024 threads has 128 registers a thread: it does not load
+    // ahead, and with 16 elements a thread it does not keep gamma either (d
+    // fp32 that stay in the caches)
+    constexpr bool LEAN = G == 1024, RELOAD = LEAN && V * R::N == 16;
     float dg[V * R::N], db[V * R::N], ga[V * R::N];
 #pragma unroll
     for (int i = 0; i < V; i++) {
 #pragma unroll
-        for (int e = 0; e < R::N; e++) dg[i * R::N + e] = db[i * R::N + e] = ga[i * R::N + e] = 0.f;
-        if (lane + i * G < nv) load_params<BF16>(gamma, lane + i * G, ga + i * R::N);
+        for (int e = 0; e < R::N; e++) dg[i * R::N + e] = db[i * R::N + e] = 0.f;
+        if (!RELOAD && lane + i * G < nv) load_params<BF16>(gamma, lane + i * G, ga + i * R::N);
     }
     typedef NormRow<BF16, V, CKPT> Row;
     auto load = [&](Row &w, int64_t t) {
@@ -203,10 +208,11 @@ __global__ __launch_bounds__(norm_threads(G)) void norm_bwd(
     const int64_t step = (int64_t)gridDim.x * RPB;
     int64_t t = (int64_t)blockIdx.x * RPB + threadIdx.x / G;
     Row next;
-    load(next, t);
+    if (!LEAN) load(next, t);
     for (; t < T; t += step, par ^= 1) {
+        if (LEAN) load(next, t);
         const Row w = next;
-        load(next, t + step);
+        if (!LEAN) load(next, t + step);
         const int64_t base = t * nv;
         float xh[V * R::N];
         float c1 = 0.f, c2 = 0.f;
@@ -217,6 +223,7 @@ __global__ __launch_bounds__(norm_threads(G)) void norm_bwd(
             if constexpr (CKPT) act8_decode(w.q[i], act8_step(w.sc[i]), f);
             else R::unpack(w.x[i], f);
             R::unpack(w.dy[i], g);
+            if (RELOAD) load_params<BF16>(gamma, lane + i * G, ga + i * R::N);
 #pragma unroll
             for (int e = 0; e < R::N; e++) {
                 const float h = (f[e] - w.mu) * w.r;
@@ -248,6 +255,7 @@ __global__ __launch_bounds__(norm_threads(G)) void norm_bwd(
             if (c >= nv) continue;
             float g[R::N], o[R::N];
             R::unpack(w.dy[i], g);
+            if (RELOAD) load_params<BF16>(gamma, c, ga + i * R::N);
 #pragma unroll
             for (int e = 0; e < R::N; e++)
                 o[e] = w.r * (fmaf(-xh[i * R::N + e], c2, g[e] * ga[i * R::N + e]) - c1);
@@ -329,48 +337,67 @@ __global__ __launch_bounds__(1024) void norm_bwd_params(const float *__restrict_
 template <typename E, typename P>
 static E *at(P *p, int64_t n) { return p ? reinterpret_cast<E *>(p) + n : nullptr; }
 
-// threads a row for nv vectors: at most 32 elements a thread
+// Threads of a row of nv vectors. One vector a thread is fastest where it
+// keeps the threads busy (256 MiB of rows, forward: bf16 d = 2048 with 256 x 1
+// 57 us, 64 x 4 72 us; d = 512 with 64 x 1 58 us, 32 x 2 62 us, 16 x 4 67 us), two
+// or three where the next group would be mostly idle (forward d = 544: 64 x 2
+// 67 us, 256 x 1 half of that filled; backward, which also pays for idle
+// threads' registers, d = 320: 32 x 2 52 us, 64 x 1 60 us; d = 1280: 64 x 3 51
+// us, 256 x 1 61 us). The backward stays below 1024 threads, where it has no
+// registers to load ahead, up to three vectors a thread (bf16 d = 5120: 512 x 2
+// 55 us, 1024 x 1 62 us).
+constexpr int kNormGroups[] = {4, 8, 16, 32, 64, 256, 512, 1024};
+constexpr int norm_group(int nv, bool bwd) {
+    if (nv > (bwd ? 1536 : 1024)) return 1024;
+    int i = 0;
+    while (i < 7 && kNormGroups[i] < nv) i++;
+    if (bwd && i == 7) return 512;
+    return i > 0 && nv * 100 < kNormGroups[i] * (bwd ? 80 : 70) ? kNormGroups[i - 1] : kNormGroups[i];
+}
+constexpr int norm_vecs(int nv, bool bwd) {
+    return (nv + norm_group(nv, bwd) - 1) / norm_group(nv, bwd);
+}
+// whether any width (d = 32, 64, ..) of the type uses G threads of V vectors
 template <bool BF16>
-static int norm_group(int nv) {
-    return nv <= 32 ? 8 : nv <= 256 ? 64 : nv <= 1024 ? 256 : 512;
+constexpr bool norm_used(int g, int v, bool bwd) {
+    for (int nv = 32 / Row16<BF16>::N; nv <= 16384 / Row16<BF16>::N; nv += 32 / Row16<BF16>::N)
+        if (norm_group(nv, bwd) == g && norm_vecs(nv, bwd) == v) return true;
+    return false;
 }
 
-// vectors a thread: 1..4 (bf16: 8 elements each; fp32 at 512 threads: up to 8)
-#define NORM_VSWITCH(v, F) ((v) <= 1 ? F(1) : (v) <= 2 ? F(2) : (v) <= 3 ? F(3) : F(4))
-#define NORM_GVSWITCH(g, v, F)                                                                  \
-    ((g) == 8 ? NORM_VSWITCH(v, F##8) : (g) == 64 ? NORM_VSWITCH(v, F##64)                      \
-     : (g) == 256 ? NORM_VSWITCH(v, F##256) : (v) <= 4 ? F##512(4) : F##512(8))
+// F(G, V) for the G and V of a row
+#define NORM_IF(G, V, BWD, F)                            \
+    if constexpr (norm_used<BF16>(G, V, BWD)) {          \
+        if (g == G && v == V) { F(G, V); }               \
+    }
+#define NORM_IFS(G, BWD, F)                                                                  \
+    NORM_IF(G, 1, BWD, F) NORM_IF(G, 2, BWD, F) NORM_IF(G, 3, BWD, F) NORM_IF(G, 4, BWD, F)
+#define NORM_SWITCH(BWD, F)                                                                  \
+    NORM_IFS(4, BWD, F) NORM_IFS(8, BWD, F) NORM_IFS(16, BWD, F) NORM_IFS(32, BWD, F)        \
+    NORM_IFS(64, BWD, F) NORM_IFS(256, BWD, F) NORM_IFS(512, BWD, F) NORM_IFS(1024, BWD, F)
 
 template <bool BF16>
 static moe_status norm_fwd_run(const void *x, const void *res, const float *gamma,
                                const float *beta, float eps, int64_t T, int d, void *y, void *sum,
                                float *mean, float *rstd, uint8_t *x8, uint8_t *x8_scale,
                                hipStream_t s) {
-    const int nv = d / Row16<BF16>::N, g = norm_group<BF16>(nv), v = (nv + g - 1) / g;
-    const float inv_d = 1.f / (float)d;
     typedef typename Codes<BF16>::type C;
-    // rows in pieces of at most kMaxBlocks workgroups (a grid has fewer than 2^32 threads)
+    const int nv = d / Row16<BF16>::N, g = norm_group(nv, false), v = norm_vecs(nv, false);
     const int nt = norm_threads(g), rows = nt / g;
-    const int64_t piece = kMaxBlocks / 2 * rows;
+    const float inv_d = 1.f / (float)d;
+    // rows in pieces of at most kMaxBlocks / 4 workgroups (of up to 1024 threads)
+    const int64_t piece = kMaxBlocks / 4 * rows;
     for (int64_t t = 0; t < T; t += piece) {
         const int64_t n = T - t < piece ? T - t : piece;
         const unsigned nb = (unsigned)((n + rows - 1) / rows);
         const int64_t o = t * nv;
 #define F(G, V)                                                                                  \
-    (norm_fwd<BF16, G, V><<<nb, nt, 0, s>>>(                                                     \
-         at<const uint4>(x, o), at<const uint4>(res, o), gamma, beta, eps, n, nv, inv_d,         \
-         at<uint4>(y, o), at<uint4>(sum, o), at<float>(mean, t), at<float>(rstd, t),             \
-         at<C>(x8, o), at<uint8_t>(x8_scale, o / Row16<BF16>::LPB)), 0)
-#define F8(V) F(8, V)
-#define F64(V) F(64, V)
-#define F256(V) F(256, V)
-#define F512(V) F(512, V)
-        NORM_GVSWITCH(g, v, F);
+    norm_fwd<BF16, G, V><<<nb, nt, 0, s>>>(                                                      \
+        at<const uint4>(x, o), at<const uint4>(res, o), gamma, beta, eps, n, nv, inv_d,          \
+        at<uint4>(y, o), at<uint4>(sum, o), at<float>(mean, t), at<float>(rstd, t), at<C>(x8, o), \
+        at<uint8_t>(x8_scale, o / Row16<BF16>::LPB))
+        NORM_SWITCH(false, F)
 #undef F
-#undef F8
-#undef F64
-#undef F256
-#undef F512
     }
     return launch_status();
 }
@@ -384,18 +411,19 @@ moe_status norm_fwd_launch(const void *x, moe_dtype dt, const void *res, const f
                : norm_fwd_run<false>(x, res, gamma, beta, eps, T, d, y, sum, mean, rstd, x8, x8_scale, s);
 }
 
-// workgroups of the backward (and rows of its partial sums): by the sizes
-// alone, so that the workspace is the same on every device
-template <bool BF16>
-static int64_t norm_bwd_blocks(int64_t T, int d) {
-    const int g = norm_group<BF16>(d / Row16<BF16>::N), rpb = norm_threads(g) / g;
-    const int64_t most = (T + rpb - 1) / rpb;
-    return most < 512 ? most : 512;
+// Workgroups of the backward, and rows of its partial sums: by the sizes
+// alone, so that the workspace is the same on every device. Two a compute
+// unit, but the partial sums (8 bytes a column, written and read back) stay
+// an eighth of the rows' bytes, while there is one a compute unit.
+static int64_t norm_bwd_blocks(int64_t T, int nv) {
+    const int g = norm_group(nv, true), rpb = norm_threads(g) / g;
+    const int64_t most = (T + rpb - 1) / rpb, few = most < 256 ? most : 256;
+    const int64_t want = T / 8 < 512 ? T / 8 : 512;
+    return want > few ? (want < most ? want : most) : few;
 }
 
 size_t norm_bwd_ws_bytes(moe_dtype dt, int64_t T, int d) {
-    const int64_t np = dt == MOE_BF16 ? norm_bwd_blocks<true>(T, d) : norm_bwd_blocks<false>(T, d);
-    return (size_t)np * 2 * d * sizeof(float);
+    return (size_t)norm_bwd_blocks(T, d / (dt == MOE_BF16 ? 8 : 4)) * 2 * d * sizeof(float);
 }
 
 template <bool BF16>
@@ -404,26 +432,18 @@ static moe_status norm_bwd_run(const void *dy, const void *x, const uint8_t *x8,
                                const float *gamma, const void *dsum, int64_t T, int d, void *dx,
                                float *dgamma, float *dbeta, bool accumulate, float *part,
                                hipStream_t s) {
-    const int nv = d / Row16<BF16>::N, g = norm_group<BF16>(nv), v = (nv + g - 1) / g;
-    const int np = (int)norm_bwd_blocks<BF16>(T, d);
-    const float inv_d = 1.f / (float)d;
     typedef typename Codes<BF16>::type C;
+    const int nv = d / Row16<BF16>::N, g = norm_group(nv, true), v = norm_vecs(nv, true);
+    const int np = (int)norm_bwd_blocks(T, nv);
+    const float inv_d = 1.f / (float)d;
 #define F2(G, V, K)                                                                              \
-    (norm_bwd<BF16, G, V, K><<<np, norm_threads(g), 0, s>>>(                                                 \
-         reinterpret_cast<const uint4 *>(dy), reinterpret_cast<const uint4 *>(x),                \
-         reinterpret_cast<const C *>(x8), x8_scale, mean, rstd, gamma,                           \
-         reinterpret_cast<const uint4 *>(dsum), T, nv, inv_d, reinterpret_cast<uint4 *>(dx),     \
-         part), 0)
-#define F8(V) (x8 ? F2(8, V, true) : F2(8, V, false))
-#define F64(V) (x8 ? F2(64, V, true) : F2(64, V, false))
-#define F256(V) (x8 ? F2(256, V, true) : F2(256, V, false))
-#define F512(V) (x8 ? F2(512, V, true) : F2(512, V, false))
-    if (np > 0) NORM_GVSWITCH(g, v, F);
+    norm_bwd<BF16, G, V, K><<<np, norm_threads(G), 0, s>>>(                                      \
+        at<const uint4>(dy, 0), at<const uint4>(x, 0), at<const C>(x8, 0), x8_scale, mean, rstd, \
+        gamma, at<const uint4>(dsum, 0), T, nv, inv_d, at<uint4>(dx, 0), part)
+#define F(G, V) if (x8) F2(G, V, true); else F2(G, V, false)
+    if (np > 0) { NORM_SWITCH(true, F) }
+#undef F
 #undef F2
-#undef F8
-#undef F64
-#undef F256
-#undef F512
     if (dgamma || dbeta)
         norm_bwd_params<<<dim3(d / 32, 2), 1024, 0, s>>>(part, np, d, dgamma, dbeta, accumulate);
     return launch_status();
