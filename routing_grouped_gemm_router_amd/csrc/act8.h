@@ -58,6 +58,26 @@ template <bool BF16> struct Codes;
 template <> struct Codes<true> { typedef uint2 type; };
 template <> struct Codes<false> { typedef uint32_t type; };
 
+// Loads of what this kernel reads once and nobody reads soon again, stores
+// likewise: they leave the last-level cache to the others.
+typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
+MOE_DEV uint4 load_once(const uint4 *p) {
+    const u32x4 w = __builtin_nontemporal_load(reinterpret_cast<const u32x4 *>(p));
+    return make_uint4(w.x, w.y, w.z, w.w);
+}
+MOE_DEV uint2 load_once(const uint2 *p) {
+    const u32x2 w = __builtin_nontemporal_load(reinterpret_cast<const u32x2 *>(p));
+    return make_uint2(w.x, w.y);
+}
+MOE_DEV uint32_t load_once(const uint32_t *p) { return __builtin_nontemporal_load(p); }
+MOE_DEV void store_once(uint4 *p, const uint4 &v) {
+    __builtin_nontemporal_store(u32x4{v.x, v.y, v.z, v.w}, reinterpret_cast<u32x4 *>(p));
+}
+MOE_DEV void store_once(uint2 *p, const uint2 &v) {
+    __builtin_nontemporal_store(u32x2{v.x, v.y}, reinterpret_cast<u32x2 *>(p));
+}
+MOE_DEV void store_once(uint32_t *p, uint32_t v) { __builtin_nontemporal_store(v, p); }
+
 MOE_DEV uint32_t umax(uint32_t a, uint32_t b) { return a > b ? a : b; }
 
 // The scale byte of the block that this lane's vector belongs to: the

@@ -11,6 +11,8 @@
 
 namespace moe {
 
+constexpr int kCombineU = 1, kCombineBwdU = 2;
+
 // store: q, scale = checkpoint of in. Blocks of 32 lie in rows of a multiple
 // of 32, so the matrix is one run of blocks.
 template <bool BF16>
@@ -20,13 +22,13 @@ __global__ __launch_bounds__(256) void act8_store_vecs(const uint4 *__restrict__
     typedef Row16<BF16> R;
     const int64_t v = (int64_t)blockIdx.x * 256 + threadIdx.x;
     if (v >= n_vec) return;                       // whole blocks of 32: n_vec % LPB == 0
-    const uint4 w = in[v];
+    const uint4 w = load_once(in + v);
     const uint32_t sb = act8_scale_byte<BF16>(w);
     float f[R::N];
     R::unpack(w, f);
     typename Codes<BF16>::type c;
     act8_encode(f, sb, c);
-    q[v] = c;
+    store_once(q + v, c);
     if (v % R::LPB == 0) scale[v / R::LPB] = (uint8_t)sb;
 }
 
@@ -64,19 +66,19 @@ __global__ __launch_bounds__(256) void act8_swiglu_vecs(const typename Codes<BF1
     const int64_t row = v / hv;
     const int64_t va = v + row * hv, vb = va + hv;      // row * 2 hv + column
     float a[R::N], b[R::N], y[R::N];
-    act8_decode(q[va], act8_step(scale[va / R::LPB]), a);
-    act8_decode(q[vb], act8_step(scale[vb / R::LPB]), b);
-    ab[va] = R::pack(a);
-    ab[vb] = R::pack(b);
+    act8_decode(load_once(q + va), act8_step(scale[va / R::LPB]), a);
+    act8_decode(load_once(q + vb), act8_step(scale[vb / R::LPB]), b);
+    store_once(ab + va, R::pack(a));
+    store_once(ab + vb, R::pack(b));
 #pragma unroll
     for (int i = 0; i < R::N; i++) y[i] = silu(a[i]) * b[i];
-    hp[v] = R::pack(y);
+    store_once(hp + v, R::pack(y));
 }
 
 // combine that keeps the experts' rows: out[t] = sum_j g[t,j] y[token_pos[t,j]]
 // (fp32 sum, ascending j) and the checkpoint of every row it reads. One wave
-// per token.
-template <bool BF16>
+// per token; U vectors of each of its k rows are in flight per lane.
+template <bool BF16, int KMAX, int U>
 __global__ __launch_bounds__(256) void combine_act8_rows(
     const uint4 *__restrict__ y, const float *__restrict__ gate,
     const int32_t *__restrict__ token_pos, int64_t T, int nv, int k, uint4 *__restrict__ out,
@@ -85,27 +87,43 @@ __global__ __launch_bounds__(256) void combine_act8_rows(
     const int lane = threadIdx.x & 63;
     const int64_t t = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6);
     if (t >= T) return;
-    for (int c = lane; c < nv; c += 64) {
-        float acc[R::N];
+    int32_t pos[KMAX];
+    float g[KMAX];
 #pragma unroll
-        for (int i = 0; i < R::N; i++) acc[i] = 0.f;
-        for (int j = 0; j < k; j++) {
-            const int32_t p = token_pos[t * k + j];
-            if (p < 0) continue;                       // dropped row
-            const float g = gate[t * k + j];
-            const int64_t v = (int64_t)p * nv + c;
-            const uint4 w = y[v];
-            const uint32_t sb = act8_scale_byte<BF16>(w);
-            float f[R::N];
-            R::unpack(w, f);
-            typename Codes<BF16>::type q;
-            act8_encode(f, sb, q);
-            y8[v] = q;
-            if (c % R::LPB == 0) y8_scale[v / R::LPB] = (uint8_t)sb;
+    for (int j = 0; j < KMAX; j++) {
+        pos[j] = j < k ? token_pos[t * k + j] : -1;
+        g[j] = j < k ? gate[t * k + j] : 0.f;
+    }
+    for (int c0 = lane; c0 < nv; c0 += 64 * U) {
+        uint4 w[U][KMAX];
 #pragma unroll
-            for (int i = 0; i < R::N; i++) acc[i] = fmaf(g, f[i], acc[i]);
+        for (int u = 0; u < U; u++)
+#pragma unroll
+            for (int j = 0; j < KMAX; j++)
+                if (c0 + 64 * u < nv && pos[j] >= 0) w[u][j] = load_once(y + (int64_t)pos[j] * nv + c0 + 64 * u);
+#pragma unroll
+        for (int u = 0; u < U; u++) {
+            const int c = c0 + 64 * u;
+            if (c >= nv) break;
+            float acc[R::N];
+#pragma unroll
+            for (int i = 0; i < R::N; i++) acc[i] = 0.f;
+#pragma unroll
+            for (int j = 0; j < KMAX; j++) {
+                if (pos[j] < 0) continue;                   // dropped row
+                const int64_t v = (int64_t)pos[j] * nv + c;
+                const uint32_t sb = act8_scale_byte<BF16>(w[u][j]);
+                float f[R::N];
+                R::unpack(w[u][j], f);
+                typename Codes<BF16>::type q;
+                act8_encode(f, sb, q);
+                y8[v] = q;
+                if (c % R::LPB == 0) y8_scale[v / R::LPB] = (uint8_t)sb;
+#pragma unroll
+                for (int i = 0; i < R::N; i++) acc[i] = fmaf(g[j], f[i], acc[i]);
+            }
+            out[t * nv + c] = R::pack(acc);
         }
-        out[t * nv + c] = R::pack(acc);
     }
 }
 
@@ -114,7 +132,9 @@ __global__ __launch_bounds__(256) void combine_act8_rows(
 //   dg_j = <dOut[t], y8[p_j]>,  dy_perm[p_j] = round(g_j dOut[t]),
 //   dlogits[t, e_j] = g_j sum_i g_i (dg_j - dg_i), 0 for unselected experts
 // (the gates sum to one; this form has no cancellation between large terms).
-template <bool BF16, int KMAX>
+// ROWS = false (the MXFP8 backward, whose quantiser forms dy_perm itself):
+// row_gate[p_j] = g_j instead of dy_perm's rows.
+template <bool BF16, int KMAX, int U, bool ROWS>
 __global__ __launch_bounds__(256) void combine_bwd_act8_rows(
     const uint4 *__restrict__ dout, const typename Codes<BF16>::type *__restrict__ y8,
     const uint8_t *__restrict__ y8_scale, const float *__restrict__ gate,
@@ -134,21 +154,41 @@ __global__ __launch_bounds__(256) void combine_bwd_act8_rows(
         g[j] = j < k ? gate[t * k + j] : 0.f;
         dot[j] = 0.f;
     }
-    for (int c = lane; c < nv; c += 64) {
-        float fo[R::N];
-        R::unpack(dout[t * nv + c], fo);
+    for (int c0 = lane; c0 < nv; c0 += 64 * U) {
+        uint4 wo[U];
+        typename Codes<BF16>::type q[U][KMAX];
+        uint8_t sc[U][KMAX];
 #pragma unroll
-        for (int j = 0; j < KMAX; j++) {
-            if (pos[j] < 0) continue;
-            const int64_t v = (int64_t)pos[j] * nv + c;
-            float fy[R::N], fd[R::N];
-            act8_decode(y8[v], act8_step(y8_scale[v / R::LPB]), fy);
+        for (int u = 0; u < U; u++) {
+            const int c = c0 + 64 * u;
+            if (c >= nv) break;
+            wo[u] = load_once(dout + t * nv + c);
 #pragma unroll
-            for (int i = 0; i < R::N; i++) {
-                dot[j] = fmaf(fo[i], fy[i], dot[j]);
-                fd[i] = g[j] * fo[i];
+            for (int j = 0; j < KMAX; j++) {
+                if (pos[j] < 0) continue;
+                const int64_t v = (int64_t)pos[j] * nv + c;
+                q[u][j] = load_once(y8 + v);
+                sc[u][j] = y8_scale[v / R::LPB];
             }
-            if (dy) dy[v] = R::pack(fd);
+        }
+#pragma unroll
+        for (int u = 0; u < U; u++) {
+            const int c = c0 + 64 * u;
+            if (c >= nv) break;
+            float fo[R::N];
+            R::unpack(wo[u], fo);
+#pragma unroll
+            for (int j = 0; j < KMAX; j++) {
+                if (pos[j] < 0) continue;
+                float fy[R::N], fd[R::N];
+                act8_decode(q[u][j], act8_step(sc[u][j]), fy);
+#pragma unroll
+                for (int i = 0; i < R::N; i++) {
+                    dot[j] = fmaf(fo[i], fy[i], dot[j]);
+                    fd[i] = g[j] * fo[i];
+                }
+                if constexpr (ROWS) dy[(int64_t)pos[j] * nv + c] = R::pack(fd);
+            }
         }
     }
 #pragma unroll
@@ -175,7 +215,7 @@ __global__ __launch_bounds__(256) void combine_bwd_act8_rows(
 #pragma unroll
         for (int j = 0; j < KMAX; j++) {
             if (dgate && j < k) dgate[t * k + j] = dot[j];
-            if (row_gate && pos[j] >= 0) row_gate[pos[j]] = g[j];
+            if (!ROWS && pos[j] >= 0) row_gate[pos[j]] = g[j];
         }
     }
 }
@@ -239,58 +279,70 @@ moe_status act8_swiglu_launch(const uint8_t *q, const uint8_t *scale, moe_dtype 
 
 constexpr int64_t kTokensALaunch = kMaxBlocks * 4;    // four tokens a workgroup
 
-moe_status combine_act8_launch(const void *y, moe_dtype dt, const float *gate,
-                               const int32_t *token_pos, int64_t T, int d, int k, void *out,
-                               uint8_t *y8, uint8_t *y8_scale, hipStream_t s) {
-    const bool bf = dt == MOE_BF16;
-    const int nv = d / (bf ? 8 : 4);
-    const uint4 *yy = reinterpret_cast<const uint4 *>(y);
-    for (int64_t t = 0; t < T; t += kTokensALaunch) {
-        const int64_t n = T - t < kTokensALaunch ? T - t : kTokensALaunch;
-        const unsigned nb = (unsigned)((n + 3) / 4);
-        uint4 *oo = reinterpret_cast<uint4 *>(out) + t * nv;
-        const float *g = gate + t * k;
-        const int32_t *tp = token_pos + t * k;
-        if (bf)
-            combine_act8_rows<true><<<nb, 256, 0, s>>>(yy, g, tp, n, nv, k, oo,
-                                                       reinterpret_cast<uint2 *>(y8), y8_scale);
-        else
-            combine_act8_rows<false><<<nb, 256, 0, s>>>(yy, g, tp, n, nv, k, oo,
-                                                        reinterpret_cast<uint32_t *>(y8), y8_scale);
-    }
-    return launch_status();
-}
-
 #define ACT8_KSWITCH(k, F) \
     ((k) <= 1 ? F(1) : (k) <= 2 ? F(2) : (k) <= 4 ? F(4) : F(8))
 
-// Exactly one of dy (the rows of dy_perm) and row_gate (each routed row's
-// gate, fp32) is given.
+template <bool BF16>
+static void combine_act8_run(const void *y, const float *gate, const int32_t *token_pos, int64_t T,
+                             int d, int k, void *out, uint8_t *y8, uint8_t *y8_scale,
+                             hipStream_t s) {
+    typedef typename Codes<BF16>::type C;
+    const int nv = d / Row16<BF16>::N;
+    for (int64_t t = 0; t < T; t += kTokensALaunch) {
+        const int64_t n = T - t < kTokensALaunch ? T - t : kTokensALaunch;
+        const unsigned nb = (unsigned)((n + 3) / 4);
+#define L(K)                                                                                     \
+    (combine_act8_rows<BF16, K, kCombineU><<<nb, 256, 0, s>>>(                                   \
+         reinterpret_cast<const uint4 *>(y), gate + t * k, token_pos + t * k, n, nv, k,          \
+         reinterpret_cast<uint4 *>(out) + t * nv, reinterpret_cast<C *>(y8), y8_scale), 0)
+        ACT8_KSWITCH(k, L);
+#undef L
+    }
+}
+
+moe_status combine_act8_launch(const void *y, moe_dtype dt, const float *gate,
+                               const int32_t *token_pos, int64_t T, int d, int k, void *out,
+                               uint8_t *y8, uint8_t *y8_scale, hipStream_t s) {
+    if (dt == MOE_BF16) combine_act8_run<true>(y, gate, token_pos, T, d, k, out, y8, y8_scale, s);
+    else combine_act8_run<false>(y, gate, token_pos, T, d, k, out, y8, y8_scale, s);
+    return launch_status();
+}
+
+template <bool BF16, bool ROWS>
+static void combine_bwd_act8_run(const void *dout, const uint8_t *y8, const uint8_t *y8_scale,
+                                 const float *gate, const int32_t *topk_idx,
+                                 const int32_t *token_pos, int64_t T, int d, int k, int E, void *dy,
+                                 float *row_gate, float *dlogits, float *dgate, hipStream_t s) {
+    typedef typename Codes<BF16>::type C;
+    const int nv = d / Row16<BF16>::N;
+    for (int64_t t = 0; t < T; t += kTokensALaunch) {
+        const int64_t n = T - t < kTokensALaunch ? T - t : kTokensALaunch;
+        const unsigned nb = (unsigned)((n + 3) / 4);
+#define L(K)                                                                                      \
+    (combine_bwd_act8_rows<BF16, K, kCombineBwdU, ROWS><<<nb, 256, 0, s>>>(                       \
+         reinterpret_cast<const uint4 *>(dout) + t * nv, reinterpret_cast<const C *>(y8),         \
+         y8_scale, gate + t * k, topk_idx + t * k, token_pos + t * k, n, nv, k, E,                \
+         reinterpret_cast<uint4 *>(dy), row_gate, dlogits + t * E, dgate ? dgate + t * k : nullptr), 0)
+        ACT8_KSWITCH(k, L);
+#undef L
+    }
+}
+
+// dy: the rows of dy_perm; without it (bf16) row_gate: each routed row's gate.
 moe_status combine_bwd_act8_launch(const void *dout, moe_dtype dt, const uint8_t *y8,
                                    const uint8_t *y8_scale, const float *gate,
                                    const int32_t *topk_idx, const int32_t *token_pos, int64_t T,
                                    int d, int k, int E, void *dy, float *row_gate, float *dlogits,
                                    float *dgate, hipStream_t s) {
-    const bool bf = dt == MOE_BF16;
-    const int nv = d / (bf ? 8 : 4);
-    uint4 *oo = reinterpret_cast<uint4 *>(dy);
-    for (int64_t t = 0; t < T; t += kTokensALaunch) {
-        const int64_t n = T - t < kTokensALaunch ? T - t : kTokensALaunch;
-        const unsigned nb = (unsigned)((n + 3) / 4);
-        const uint4 *dd = reinterpret_cast<const uint4 *>(dout) + t * nv;
-        const float *g = gate + t * k;
-        const int32_t *ti = topk_idx + t * k, *tp = token_pos + t * k;
-        float *dl = dlogits + t * E, *dg = dgate ? dgate + t * k : nullptr;
-#define L(K)                                                                                      \
-    (bf ? (combine_bwd_act8_rows<true, K><<<nb, 256, 0, s>>>(                                     \
-               dd, reinterpret_cast<const uint2 *>(y8), y8_scale, g, ti, tp, n, nv, k, E, oo,     \
-               row_gate, dl, dg), 0)                                                              \
-        : (combine_bwd_act8_rows<false, K><<<nb, 256, 0, s>>>(                                    \
-               dd, reinterpret_cast<const uint32_t *>(y8), y8_scale, g, ti, tp, n, nv, k, E, oo,  \
-               row_gate, dl, dg), 0))
-        ACT8_KSWITCH(k, L);
-#undef L
-    }
+    if (dt == MOE_F32)
+        combine_bwd_act8_run<false, true>(dout, y8, y8_scale, gate, topk_idx, token_pos, T, d, k, E,
+                                          dy, nullptr, dlogits, dgate, s);
+    else if (dy)
+        combine_bwd_act8_run<true, true>(dout, y8, y8_scale, gate, topk_idx, token_pos, T, d, k, E,
+                                         dy, nullptr, dlogits, dgate, s);
+    else
+        combine_bwd_act8_run<true, false>(dout, y8, y8_scale, gate, topk_idx, token_pos, T, d, k, E,
+                                          nullptr, row_gate, dlogits, dgate, s);
     return launch_status();
 }
 

@@ -62,6 +62,8 @@ __global__ __launch_bounds__(256) void w4_quantize_vecs(const uint4 *__restrict_
 // ---------------------------------------------------------------------------
 // the products
 
+constexpr int kW4Unroll = 4;
+
 // eight four-bit elements to bf16, scaled
 MOE_DEV bf16x8 w4_widen(uint32_t w, float s) {
     const auto p0 = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(w, s, 0);
@@ -73,21 +75,33 @@ MOE_DEV bf16x8 w4_widen(uint32_t w, float s) {
 }
 
 // The expert with rank `slot` among those with rows, and its rows; false if
-// there are fewer. E <= 256 threads look at one expert each.
+// there are fewer. Every wave finds it by itself: expert 64 i + lane in turn.
 MOE_DEV bool w4_active(const int32_t *offsets, int E, int slot, int &e, int &r0, int &r1) {
-    __shared__ int s_cnt[4], s_found[3];
-    const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
-    const int a = tid < E ? offsets[tid] : 0, b = tid < E ? offsets[tid + 1] : 0;
-    const uint64_t m = __ballot(b > a);
-    if (lane == 0) s_cnt[wave] = __popcll(m);
-    if (tid == 0) s_found[0] = -1;
-    __syncthreads();
-    int rank = __popcll(m & (((uint64_t)1 << lane) - 1));
-    for (int w = 0; w < wave; w++) rank += s_cnt[w];
-    if (b > a && rank == slot) { s_found[0] = tid; s_found[1] = a; s_found[2] = b; }
-    __syncthreads();
-    e = s_found[0]; r0 = s_found[1]; r1 = s_found[2];
-    return e >= 0;
+    const int lane = threadIdx.x & 63;
+    int a[4], b[4];
+#pragma unroll
+    for (int i = 0; i < 4; i++) {
+        const int x = 64 * i + lane;
+        a[i] = x < E ? offsets[x] : 0;
+        b[i] = x < E ? offsets[x + 1] : 0;
+    }
+    int before = 0;
+    bool found = false;
+#pragma unroll
+    for (int i = 0; i < 4; i++) {
+        const uint64_t m = __ballot(b[i] > a[i]);
+        const int n = __popcll(m);
+        if (!found && slot < before + n) {           // uniform
+            const int rank = before + __popcll(m & (((uint64_t)1 << lane) - 1));
+            const int l = __ffsll(__ballot(b[i] > a[i] && rank == slot)) - 1;
+            e = 64 * i + l;
+            r0 = __builtin_amdgcn_readlane(a[i], l);
+            r1 = __builtin_amdgcn_readlane(b[i], l);
+            found = true;
+        }
+        before += n;
+    }
+    return found;
 }
 
 struct W4Args {
@@ -100,11 +114,57 @@ struct W4Args {
     int K, h, d;
 };
 
-constexpr int kW4Unroll = 4;
+// Steps [s, s + U) of a wave's reduction, blocks 4 s' + g of every row: all
+// loads, then the products. TAIL: blocks past the row's end count as zeros
+// (both operands, whatever x holds).
+template <bool UP, int NT, int U, bool TAIL>
+MOE_DEV void w4_steps(int s, int g, int nblk, const uint8_t *q0, const uint8_t *q1,
+                      const uint8_t *s0, const uint8_t *s1, const uint16_t *const (&x)[NT],
+                      const uint16_t *const (&xl)[NT], f32x4 (&acc)[2][NT]) {
+    u32x4 w[U][2];
+    uint32_t sc[U][2];
+    const u32x4 zero = {0, 0, 0, 0};
+#pragma unroll
+    for (int u = 0; u < U; u++) {
+        const int c = TAIL ? min(4 * (s + u) + g, nblk - 1) : 4 * (s + u) + g;
+        w[u][0] = *reinterpret_cast<const u32x4 *>(q0 + 16 * c);
+        w[u][1] = *reinterpret_cast<const u32x4 *>(q1 + 16 * c);
+        sc[u][0] = s0[c];
+        sc[u][1] = s1[c];
+    }
+#pragma unroll
+    for (int u = 0; u < U; u++) {
+        const bool ok = !TAIL || 4 * (s + u) + g < nblk;
+        const int c = TAIL ? min(4 * (s + u) + g, nblk - 1) : 4 * (s + u) + g;
+        const float f0 = __uint_as_float(sc[u][0] << 23), f1 = __uint_as_float(sc[u][1] << 23);
+        const u32x4 w0 = ok ? w[u][0] : zero, w1 = ok ? w[u][1] : zero;
+#pragma unroll
+        for (int m = 0; m < 4; m++) {
+            const bf16x8 a0 = w4_widen(w0[m], f0), a1 = w4_widen(w1[m], f1);
+#pragma unroll
+            for (int t = 0; t < NT; t++) {
+                u32x4 v = *reinterpret_cast<const u32x4 *>(x[t] + 32 * c + 8 * m);
+                v = ok ? v : zero;
+                const bf16x8 b = __builtin_bit_cast(bf16x8, v);
+                acc[0][t] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(a0, b, acc[0][t], 0, 0, 0);
+                acc[1][t] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(a1, b, acc[1][t], 0, 0, 0);
+                if constexpr (!UP) {
+                    u32x4 vl = *reinterpret_cast<const u32x4 *>(xl[t] + 32 * c + 8 * m);
+                    vl = ok ? vl : zero;
+                    const bf16x8 bl = __builtin_bit_cast(bf16x8, vl);
+                    acc[0][t] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(a0, bl, acc[0][t], 0, 0, 0);
+                    acc[1][t] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(a1, bl, acc[1][t], 0, 0, 0);
+                }
+            }
+        }
+    }
+}
 
 // Rows [r, r + 16 NT) of the expert's rows [.., r1): two tiles of 16 weight
-// rows (gate and up, or 32 rows of W2), the reduction's steps dealt to the
-// four waves, their sums joined in LDS.
+// rows (gate and up, or 32 rows of W2), the reduction in four parts, one a
+// wave, joined in LDS. Lanes past the expert's last row compute the first
+// row once more (a token is a column of the product: it reaches no other)
+// and store nothing.
 template <bool UP, int NT>
 MOE_DEV void w4_rows(const W4Args &p, int64_t wrow0, int64_t wrow1, int n0, int r, int r1,
                      float (*red)[2][256]) {
@@ -115,60 +175,22 @@ MOE_DEV void w4_rows(const W4Args &p, int64_t wrow0, int64_t wrow1, int n0, int 
     const uint16_t *x[NT], *xl[NT];
 #pragma unroll
     for (int t = 0; t < NT; t++) {
-        const int row = r + 16 * t + i;
-        const bool ok = row < r1;
-        const int64_t src = ok ? (UP ? p.sorted_token[row] : row) : 0;
-        x[t] = ok ? p.x + src * p.K : nullptr;
-        xl[t] = ok && !UP ? p.lo + src * p.K : nullptr;
+        const int row = r + 16 * t + i < r1 ? r + 16 * t + i : r;
+        const int64_t src = UP ? p.sorted_token[row] : row;
+        x[t] = p.x + src * p.K;
+        xl[t] = UP ? nullptr : p.lo + src * p.K;
     }
     f32x4 acc[2][NT];
 #pragma unroll
     for (int z = 0; z < 2; z++)
 #pragma unroll
         for (int t = 0; t < NT; t++) acc[z][t] = f32x4{0.f, 0.f, 0.f, 0.f};
-    for (int s = wave; 4 * s < nblk; s += 4 * kW4Unroll) {
-        u32x4 w[kW4Unroll][2];
-        uint32_t sc[kW4Unroll][2];
-#pragma unroll
-        for (int u = 0; u < kW4Unroll; u++) {
-            const int c = 4 * (s + 4 * u) + g;
-            const bool ok = c < nblk;
-            w[u][0] = w[u][1] = u32x4{0, 0, 0, 0};
-            sc[u][0] = sc[u][1] = 127;
-            if (ok) {
-                w[u][0] = *reinterpret_cast<const u32x4 *>(q0 + 16 * c);
-                w[u][1] = *reinterpret_cast<const u32x4 *>(q1 + 16 * c);
-                sc[u][0] = s0[c];
-                sc[u][1] = s1[c];
-            }
-        }
-#pragma unroll
-        for (int u = 0; u < kW4Unroll; u++) {
-            const int c = 4 * (s + 4 * u) + g;
-            const bool ok = c < nblk;
-            if (4 * (s + 4 * u) >= nblk) break;   // uniform
-            const float f0 = __uint_as_float(sc[u][0] << 23), f1 = __uint_as_float(sc[u][1] << 23);
-#pragma unroll
-            for (int m = 0; m < 4; m++) {
-                const bf16x8 a0 = w4_widen(w[u][0][m], f0), a1 = w4_widen(w[u][1][m], f1);
-#pragma unroll
-                for (int t = 0; t < NT; t++) {
-                    u32x4 v = {0, 0, 0, 0};
-                    if (ok && x[t]) v = *reinterpret_cast<const u32x4 *>(x[t] + 32 * c + 8 * m);
-                    const bf16x8 b = __builtin_bit_cast(bf16x8, v);
-                    acc[0][t] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(a0, b, acc[0][t], 0, 0, 0);
-                    acc[1][t] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(a1, b, acc[1][t], 0, 0, 0);
-                    if constexpr (!UP) {
-                        u32x4 vl = {0, 0, 0, 0};
-                        if (ok && x[t]) vl = *reinterpret_cast<const u32x4 *>(xl[t] + 32 * c + 8 * m);
-                        const bf16x8 bl = __builtin_bit_cast(bf16x8, vl);
-                        acc[0][t] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(a0, bl, acc[0][t], 0, 0, 0);
-                        acc[1][t] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(a1, bl, acc[1][t], 0, 0, 0);
-                    }
-                }
-            }
-        }
-    }
+    const int steps = (nblk + 3) / 4, part = (steps + 3) / 4;
+    int s = wave * part;
+    const int end = min(s + part, steps), whole = min(end, nblk / 4);
+    for (; s + kW4Unroll <= whole; s += kW4Unroll)
+        w4_steps<UP, NT, kW4Unroll, false>(s, g, nblk, q0, q1, s0, s1, x, xl, acc);
+    for (; s < end; s++) w4_steps<UP, NT, 1, true>(s, g, nblk, q0, q1, s0, s1, x, xl, acc);
     // lane: token i, weight rows 4 g .. 4 g + 3
 #pragma unroll
     for (int t = 0; t < NT; t++) {
@@ -202,7 +224,7 @@ __global__ __launch_bounds__(256) void w4_product(W4Args p, const int32_t *__res
                                                   int E) {
     __shared__ float red[4][2][256];
     int e, r0, r1;
-    if (!w4_active(offsets, E, blockIdx.y, e, r0, r1)) return;
+    if (!w4_active(offsets, E, blockIdx.y, e, r0, r1)) return;      // the whole workgroup
     const int n0 = blockIdx.x * (UP ? 16 : 32);
     const int64_t base = (int64_t)e * (UP ? 2 * p.h : p.d);
     const int64_t w0 = base + n0, w1 = w0 + (UP ? p.h : 16);
