@@ -62,8 +62,6 @@ __global__ __launch_bounds__(256) void w4_quantize_vecs(const uint4 *__restrict_
 // ---------------------------------------------------------------------------
 // the products
 
-constexpr int kW4Unroll = 4;
-
 // eight four-bit elements to bf16, scaled
 MOE_DEV bf16x8 w4_widen(uint32_t w, float s) {
     const auto p0 = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(w, s, 0);
@@ -114,124 +112,214 @@ struct W4Args {
     int K, h, d;
 };
 
-// Steps [s, s + U) of a wave's reduction, blocks 4 s' + g of every row: all
-// loads, then the products. TAIL: blocks past the row's end count as zeros
-// (both operands, whatever x holds).
+// What a wave keeps in LDS of one step: both weight tiles (16 rows of 4
+// blocks, 16 bytes each), their scales, and per row tile (and half of h) 16
+// tokens of 4 blocks in 16-byte pieces.
+template <bool UP, int NT>
+struct W4Stage {
+    u32x4 w[2][64];
+    uint8_t sc[2][64];
+    u32x4 x[UP ? 1 : 2][NT][256];
+};
+
+// Pieces are kept at the place of their index with some of its bits flipped
+// by the row's, so that the 16 lanes that read one piece of 16 rows each meet
+// different banks.
+MOE_DEV int w4_wslot(int row, int blk) { return 4 * row + (blk ^ (row >> 2)); }
+MOE_DEV int w4_xslot(int row, int piece) { return 16 * row + (piece ^ (4 * (row & 3) + (row >> 2))); }
+
+// The lanes of a wave see each other's LDS writes in program order; this
+// keeps the compiler to that order.
+MOE_DEV void w4_lds_order() {
+    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+    __builtin_amdgcn_wave_barrier();
+}
+
+// Steps [s, s + U) of a wave's reduction: all global loads, then step by step
+// through LDS to the matrix units. Memory is read by quads of lanes, 64
+// contiguous bytes of a row each: lane l takes row l / 4 of the weights and of
+// the tokens, while the product wants row l % 16 (a load in the product's own
+// order has a lane per row and costs the first-level cache four times the
+// accesses). TAIL: blocks past the row's end count as zeros, of both operands.
 template <bool UP, int NT, int U, bool TAIL>
-MOE_DEV void w4_steps(int s, int g, int nblk, const uint8_t *q0, const uint8_t *q1,
-                      const uint8_t *s0, const uint8_t *s1, const uint16_t *const (&x)[NT],
-                      const uint16_t *const (&xl)[NT], f32x4 (&acc)[2][NT]) {
-    u32x4 w[U][2];
-    uint32_t sc[U][2];
+MOE_DEV void w4_steps(int s, int nblk, const uint8_t *q0, const uint8_t *q1, const uint8_t *s0,
+                      const uint8_t *s1, const uint16_t *const (&x)[2][NT], W4Stage<UP, NT> &st,
+                      f32x4 (&acc)[2][NT]) {
+    constexpr int P = UP ? 1 : 2;                 // h comes as two halves
+    const int lane = threadIdx.x & 63, g = lane >> 4, i = lane & 15, lr = lane >> 2, lc = lane & 3;
+    u32x4 w[U][2], xr[U][P][NT][4];
+    uint8_t sc[U][2];
     const u32x4 zero = {0, 0, 0, 0};
 #pragma unroll
     for (int u = 0; u < U; u++) {
-        const int c = TAIL ? min(4 * (s + u) + g, nblk - 1) : 4 * (s + u) + g;
-        w[u][0] = *reinterpret_cast<const u32x4 *>(q0 + 16 * c);
-        w[u][1] = *reinterpret_cast<const u32x4 *>(q1 + 16 * c);
-        sc[u][0] = s0[c];
-        sc[u][1] = s1[c];
+        const int c = 4 * (s + u) + lc;
+        const bool ok = !TAIL || c < nblk;
+        w[u][0] = w[u][1] = zero;
+        sc[u][0] = sc[u][1] = 127;
+        if (ok) {
+            w[u][0] = *reinterpret_cast<const u32x4 *>(q0 + 16 * c);
+            w[u][1] = *reinterpret_cast<const u32x4 *>(q1 + 16 * c);
+            sc[u][0] = s0[c];
+            sc[u][1] = s1[c];
+        }
     }
 #pragma unroll
+    for (int t = 0; t < NT; t++)
+#pragma unroll
+        for (int p = 0; p < P; p++)
+            if (x[p][t]) {
+#pragma unroll
+                for (int u = 0; u < U; u++)
+#pragma unroll
+                    for (int j = 0; j < 4; j++) {
+                        const int c = 4 * (s + u) + j;
+                        xr[u][p][t][j] = !TAIL || c < nblk
+                            ? *reinterpret_cast<const u32x4 *>(x[p][t] + 32 * c + 8 * lc) : zero;
+                    }
+            }
+#pragma unroll
     for (int u = 0; u < U; u++) {
-        const bool ok = !TAIL || 4 * (s + u) + g < nblk;
-        const int c = TAIL ? min(4 * (s + u) + g, nblk - 1) : 4 * (s + u) + g;
-        const float f0 = __uint_as_float(sc[u][0] << 23), f1 = __uint_as_float(sc[u][1] << 23);
-        const u32x4 w0 = ok ? w[u][0] : zero, w1 = ok ? w[u][1] : zero;
+        w4_lds_order();                           // the step before has been read
+#pragma unroll
+        for (int z = 0; z < 2; z++) {
+            st.w[z][w4_wslot(lr, lc)] = w[u][z];
+            st.sc[z][lane] = sc[u][z];
+        }
+#pragma unroll
+        for (int t = 0; t < NT; t++)
+#pragma unroll
+            for (int p = 0; p < P; p++)
+                if (x[p][t])
+#pragma unroll
+                    for (int j = 0; j < 4; j++) st.x[p][t][w4_xslot(lr, 4 * j + lc)] = xr[u][p][t][j];
+        w4_lds_order();
+        u32x4 a[2];
+        float f[2];
+#pragma unroll
+        for (int z = 0; z < 2; z++) {
+            a[z] = st.w[z][w4_wslot(i, g)];
+            f[z] = __uint_as_float((uint32_t)st.sc[z][4 * i + g] << 23);
+        }
 #pragma unroll
         for (int m = 0; m < 4; m++) {
-            const bf16x8 a0 = w4_widen(w0[m], f0), a1 = w4_widen(w1[m], f1);
+            const bf16x8 a0 = w4_widen(a[0][m], f[0]), a1 = w4_widen(a[1][m], f[1]);
 #pragma unroll
-            for (int t = 0; t < NT; t++) {
-                u32x4 v = *reinterpret_cast<const u32x4 *>(x[t] + 32 * c + 8 * m);
-                v = ok ? v : zero;
-                const bf16x8 b = __builtin_bit_cast(bf16x8, v);
-                acc[0][t] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(a0, b, acc[0][t], 0, 0, 0);
-                acc[1][t] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(a1, b, acc[1][t], 0, 0, 0);
-                if constexpr (!UP) {
-                    u32x4 vl = *reinterpret_cast<const u32x4 *>(xl[t] + 32 * c + 8 * m);
-                    vl = ok ? vl : zero;
-                    const bf16x8 bl = __builtin_bit_cast(bf16x8, vl);
-                    acc[0][t] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(a0, bl, acc[0][t], 0, 0, 0);
-                    acc[1][t] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(a1, bl, acc[1][t], 0, 0, 0);
+            for (int t = 0; t < NT; t++)
+#pragma unroll
+                for (int p = 0; p < P; p++) {
+                    const bf16x8 b = __builtin_bit_cast(bf16x8, st.x[p][t][w4_xslot(i, 4 * g + m)]);
+                    acc[0][t] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(a0, b, acc[0][t], 0, 0, 0);
+                    acc[1][t] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(a1, b, acc[1][t], 0, 0, 0);
                 }
-            }
         }
     }
 }
 
-// Rows [r, r + 16 NT) of the expert's rows [.., r1): two tiles of 16 weight
-// rows (gate and up, or 32 rows of W2), the reduction in four parts, one a
-// wave, joined in LDS. Lanes past the expert's last row compute the first
-// row once more (a token is a column of the product: it reaches no other)
-// and store nothing.
+// LDS of a workgroup: the waves' stages, then (SPLIT) their sums.
 template <bool UP, int NT>
+union W4Lds {
+    W4Stage<UP, NT> stage[4];
+    float red[4][2][256];
+};
+
+// N results of row `row`, columns from n: h as its two halves, or y.
+template <bool UP, int N>
+MOE_DEV void w4_store(const W4Args &p, int64_t row, int n, const float *v0, const float *v1) {
+    if constexpr (UP) {
+        uint16_t hi[N], lo[N];
+#pragma unroll
+        for (int q = 0; q < N; q++) {
+            const float a = v0[q], e = expf(-0.5f * fabsf(a));
+            const float o = (a < 0.f ? (a * e) * e : a) / fmaf(e, e, 1.f) * v1[q];
+            hi[q] = f32_to_bf16(o);
+            lo[q] = f32_to_bf16(o - bf16_to_f32(hi[q]));
+        }
+        __builtin_memcpy(p.hi_out + row * p.h + n, hi, sizeof(hi));
+        __builtin_memcpy(p.lo_out + row * p.h + n, lo, sizeof(lo));
+    } else {
+        __builtin_memcpy(p.y + row * p.d + n, v0, N * sizeof(float));
+        __builtin_memcpy(p.y + row * p.d + n + 16, v1, N * sizeof(float));
+    }
+}
+
+// Rows [r, r + 16 NT) of the expert's rows [.., r1), two tiles of 16 weight
+// rows: gate and up of 16 columns, or 32 rows of W2. SPLIT: a workgroup's
+// four waves take a quarter of the reduction each and join their sums in LDS;
+// otherwise each has tiles of its own. The columns of the product past the
+// expert's last row hold what LDS held (a token is a column: it reaches no
+// other) and are not stored.
+template <bool UP, int NT, int U, bool SPLIT>
 MOE_DEV void w4_rows(const W4Args &p, int64_t wrow0, int64_t wrow1, int n0, int r, int r1,
-                     float (*red)[2][256]) {
-    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, g = lane >> 4, i = lane & 15;
+                     W4Lds<UP, NT> &lds) {
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, lr = lane >> 2;
     const int nblk = p.K / 32;
-    const uint8_t *q0 = p.wq + (wrow0 + i) * (p.K / 2), *q1 = p.wq + (wrow1 + i) * (p.K / 2);
-    const uint8_t *s0 = p.ws + (wrow0 + i) * nblk, *s1 = p.ws + (wrow1 + i) * nblk;
-    const uint16_t *x[NT], *xl[NT];
+    const uint8_t *q0 = p.wq + (wrow0 + lr) * (p.K / 2), *q1 = p.wq + (wrow1 + lr) * (p.K / 2);
+    const uint8_t *s0 = p.ws + (wrow0 + lr) * nblk, *s1 = p.ws + (wrow1 + lr) * nblk;
+    const uint16_t *x[2][NT];
 #pragma unroll
     for (int t = 0; t < NT; t++) {
-        const int row = r + 16 * t + i < r1 ? r + 16 * t + i : r;
-        const int64_t src = UP ? p.sorted_token[row] : row;
-        x[t] = p.x + src * p.K;
-        xl[t] = UP ? nullptr : p.lo + src * p.K;
+        const int row = r + 16 * t + lr;
+        x[0][t] = x[1][t] = nullptr;
+        if (row < r1) {
+            const int64_t src = (UP ? p.sorted_token[row] : row) * (int64_t)p.K;
+            x[0][t] = p.x + src;
+            x[1][t] = UP ? nullptr : p.lo + src;
+        }
     }
     f32x4 acc[2][NT];
 #pragma unroll
     for (int z = 0; z < 2; z++)
 #pragma unroll
         for (int t = 0; t < NT; t++) acc[z][t] = f32x4{0.f, 0.f, 0.f, 0.f};
-    const int steps = (nblk + 3) / 4, part = (steps + 3) / 4;
-    int s = wave * part;
+    const int steps = (nblk + 3) / 4, part = SPLIT ? (steps + 3) / 4 : steps;
+    int s = SPLIT ? wave * part : 0;
     const int end = min(s + part, steps), whole = min(end, nblk / 4);
-    for (; s + kW4Unroll <= whole; s += kW4Unroll)
-        w4_steps<UP, NT, kW4Unroll, false>(s, g, nblk, q0, q1, s0, s1, x, xl, acc);
-    for (; s < end; s++) w4_steps<UP, NT, 1, true>(s, g, nblk, q0, q1, s0, s1, x, xl, acc);
-    // lane: token i, weight rows 4 g .. 4 g + 3
+    W4Stage<UP, NT> &st = lds.stage[wave];
+    for (; s + U <= whole; s += U)
+        w4_steps<UP, NT, U, false>(s, nblk, q0, q1, s0, s1, x, st, acc);
+    for (; s < end; s++) w4_steps<UP, NT, 1, true>(s, nblk, q0, q1, s0, s1, x, st, acc);
+    // lane: token lane % 16, weight rows 4 (lane / 16) .. + 3
+    const int i = lane & 15, n4 = 4 * (lane >> 4);
+    if constexpr (!SPLIT) {
+#pragma unroll
+        for (int t = 0; t < NT; t++) {
+            const int row = r + 16 * t + i;
+            const float v0[4] = {acc[0][t][0], acc[0][t][1], acc[0][t][2], acc[0][t][3]};
+            const float v1[4] = {acc[1][t][0], acc[1][t][1], acc[1][t][2], acc[1][t][3]};
+            if (row < r1) w4_store<UP, 4>(p, row, n0 + n4, v0, v1);
+        }
+        return;
+    }
 #pragma unroll
     for (int t = 0; t < NT; t++) {
-        __syncthreads();                          // the tile before has been read
+        __syncthreads();                          // the stages, or the tile before, have been read
 #pragma unroll
-        for (int z = 0; z < 2; z++)
-            *reinterpret_cast<f32x4 *>(&red[wave][z][i * 16 + 4 * g]) = acc[z][t];
+        for (int z = 0; z < 2; z++) *reinterpret_cast<f32x4 *>(&lds.red[wave][z][i * 16 + n4]) = acc[z][t];
         __syncthreads();
         const int tid = threadIdx.x, row = r + 16 * t + (tid >> 4), n = tid & 15;
         float v[2];
 #pragma unroll
         for (int z = 0; z < 2; z++)
-            v[z] = (red[0][z][tid] + red[1][z][tid]) + (red[2][z][tid] + red[3][z][tid]);
-        if (row >= r1) continue;
-        if constexpr (UP) {
-            const float a = v[0], e = expf(-0.5f * fabsf(a));
-            const float o = (a < 0.f ? (a * e) * e : a) / fmaf(e, e, 1.f) * v[1];
-            const uint16_t hi = f32_to_bf16(o);
-            p.hi_out[(int64_t)row * p.h + n0 + n] = hi;
-            p.lo_out[(int64_t)row * p.h + n0 + n] = f32_to_bf16(o - bf16_to_f32(hi));
-        } else {
-            p.y[(int64_t)row * p.d + n0 + n] = v[0];
-            p.y[(int64_t)row * p.d + n0 + 16 + n] = v[1];
-        }
+            v[z] = (lds.red[0][z][tid] + lds.red[1][z][tid]) + (lds.red[2][z][tid] + lds.red[3][z][tid]);
+        if (row < r1) w4_store<UP, 1>(p, row, n0 + n, &v[0], &v[1]);
     }
+    __syncthreads();                              // the sums have been read
 }
 
-// blockIdx.x: 16 columns of h (UP) or 32 of d; blockIdx.y: rank of an expert with rows
-template <bool UP>
-__global__ __launch_bounds__(256) void w4_product(W4Args p, const int32_t *__restrict__ offsets,
-                                                  int E) {
-    __shared__ float red[4][2][256];
+// blockIdx.y: rank of an expert with rows; blockIdx.x: 16 columns of h (UP) or
+// 32 of d, without SPLIT four times as many, a quarter for each wave
+template <bool UP, int NT, int U, bool SPLIT>
+__global__ __launch_bounds__(256, NT == 1 ? 3 : 2) void w4_product(
+    W4Args p, const int32_t *__restrict__ offsets, int E) {
+    __shared__ W4Lds<UP, NT> lds;
     int e, r0, r1;
     if (!w4_active(offsets, E, blockIdx.y, e, r0, r1)) return;      // the whole workgroup
-    const int n0 = blockIdx.x * (UP ? 16 : 32);
+    const int tile = SPLIT ? blockIdx.x : 4 * blockIdx.x + (threadIdx.x >> 6);
+    const int n0 = tile * (UP ? 16 : 32);
+    if (!SPLIT && n0 >= (UP ? p.h : p.d)) return;                   // this wave alone: no barriers
     const int64_t base = (int64_t)e * (UP ? 2 * p.h : p.d);
     const int64_t w0 = base + n0, w1 = w0 + (UP ? p.h : 16);
-    int r = r0;
-    for (; r1 - r > 32; r += 64) w4_rows<UP, 4>(p, w0, w1, n0, r, r1, red);
-    if (r1 - r > 16) w4_rows<UP, 2>(p, w0, w1, n0, r, r1, red);
-    else if (r1 > r) w4_rows<UP, 1>(p, w0, w1, n0, r, r1, red);
+    for (int r = r0; r < r1; r += 16 * NT) w4_rows<UP, NT, U, SPLIT>(p, w0, w1, n0, r, r1, lds);
 }
 
 // out[t] = sum_j g y[token_pos] (fp32, ascending j), 4 columns a thread
@@ -272,6 +360,7 @@ moe_status w4_quantize_launch(const void *in, moe_dtype dt, int64_t rows, int64_
     return launch_status();
 }
 
+#define SPLIT_MAX 2048
 static size_t round256(size_t b) { return (b + 255) & ~(size_t)255; }
 
 // workspace: h's upper halves, its lower halves [R, h] bf16, y [R, d] fp32
@@ -286,11 +375,23 @@ moe_status w4_experts_launch(const moe_w4_desc *w, hipStream_t s) {
     uint16_t *hi = reinterpret_cast<uint16_t *>(ws), *lo = reinterpret_cast<uint16_t *>(ws + half);
     float *y = reinterpret_cast<float *>(ws + 2 * half);
     const unsigned ny = (unsigned)(R < w->E ? R : w->E);
-    W4Args up = {reinterpret_cast<const uint16_t *>(w->x), nullptr, w->sorted_token, w->w1q, w->w1_scale,
-                 hi, lo, nullptr, w->d, w->h, w->d};
-    w4_product<true><<<dim3(w->h / 16, ny), 256, 0, s>>>(up, w->offsets, w->E);
-    W4Args down = {hi, lo, nullptr, w->w2q, w->w2_scale, nullptr, nullptr, y, w->h, w->h, w->d};
-    w4_product<false><<<dim3(w->d / 32, ny), 256, 0, s>>>(down, w->offsets, w->E);
+    const bool few = R <= 8 * (int64_t)w->E;
+    const W4Args up = {reinterpret_cast<const uint16_t *>(w->x), nullptr, w->sorted_token, w->w1q,
+                       w->w1_scale, hi, lo, nullptr, w->d, w->h, w->d};
+    const W4Args down = {hi, lo, nullptr, w->w2q, w->w2_scale, nullptr, nullptr, y, w->h, w->h, w->d};
+    const int nu = w->h / 16, nd = w->d / 32;
+    if (!few)
+        w4_product<true, 2, 2, false><<<dim3((nu + 3) / 4, ny), 256, 0, s>>>(up, w->offsets, w->E);
+    else if ((int64_t)nu * ny <= SPLIT_MAX)
+        w4_product<true, 1, 2, true><<<dim3(nu, ny), 256, 0, s>>>(up, w->offsets, w->E);
+    else
+        w4_product<true, 1, 2, false><<<dim3((nu + 3) / 4, ny), 256, 0, s>>>(up, w->offsets, w->E);
+    if (!few)
+        w4_product<false, 2, 1, false><<<dim3((nd + 3) / 4, ny), 256, 0, s>>>(down, w->offsets, w->E);
+    else if ((int64_t)nd * ny <= SPLIT_MAX)
+        w4_product<false, 1, 2, true><<<dim3(nd, ny), 256, 0, s>>>(down, w->offsets, w->E);
+    else
+        w4_product<false, 1, 2, false><<<dim3((nd + 3) / 4, ny), 256, 0, s>>>(down, w->offsets, w->E);
     const int cb = (w->d + 1023) / 1024;
     const int64_t piece = kMaxBlocks / cb;
     for (int64_t t = 0; t < w->T; t += piece) {
