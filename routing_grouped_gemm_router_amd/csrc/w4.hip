@@ -102,6 +102,10 @@ MOE_DEV bool w4_active(const int32_t *offsets, int E, int slot, int &e, int &r0,
     return found;
 }
 
+constexpr int kW4Tokens = 8;     // rows of an expert that a wave multiplies at once
+constexpr int kW4Steps = 2;      // steps of 128 reduction indices loaded at once
+constexpr int kW4WideTiles = 2;  // row tiles of 16 with many rows
+
 struct W4Args {
     const uint16_t *x;           // UP: x [T, d]; else h's upper halves [R, h]
     const uint16_t *lo;          // down: h's lower halves [R, h]
@@ -112,14 +116,27 @@ struct W4Args {
     int K, h, d;
 };
 
+// The two tiles of 16 weight rows that a wave multiplies (the same for all of
+// its lanes, so that the lanes need offsets of 32 bits alone).
+struct W4Tiles {
+    const uint8_t *q0, *q1, *s0, *s1;
+    MOE_DEV W4Tiles(const W4Args &p, int64_t row0, int64_t row1) {
+        const int nblk = p.K / 32;
+        q0 = p.wq + row0 * 16 * nblk; q1 = p.wq + row1 * 16 * nblk;
+        s0 = p.ws + row0 * nblk; s1 = p.ws + row1 * nblk;
+    }
+};
+
+MOE_DEV int w4_wave() { return __builtin_amdgcn_readfirstlane(threadIdx.x >> 6); }
+
 // What a wave keeps in LDS of one step: both weight tiles (16 rows of 4
-// blocks, 16 bytes each), their scales, and per row tile (and half of h) 16
-// tokens of 4 blocks in 16-byte pieces.
-template <bool UP, int NT>
+// blocks, 16 bytes each), their scales, and per half of h TOK tokens of 4
+// blocks in 16-byte pieces.
+template <bool UP, int TOK>
 struct W4Stage {
     u32x4 w[2][64];
     uint8_t sc[2][64];
-    u32x4 x[UP ? 1 : 2][NT][256];
+    u32x4 x[UP ? 1 : 2][TOK * 16];
 };
 
 // Pieces are kept at the place of their index with some of its bits flipped
@@ -136,46 +153,42 @@ MOE_DEV void w4_lds_order() {
 }
 
 // Steps [s, s + U) of a wave's reduction: all global loads, then step by step
-// through LDS to the matrix units. Memory is read by quads of lanes, 64
-// contiguous bytes of a row each: lane l takes row l / 4 of the weights and of
-// the tokens, while the product wants row l % 16 (a load in the product's own
-// order has a lane per row and costs the first-level cache four times the
-// accesses). TAIL: blocks past the row's end count as zeros, of both operands.
-template <bool UP, int NT, int U, bool TAIL>
-MOE_DEV void w4_steps(int s, int nblk, const uint8_t *q0, const uint8_t *q1, const uint8_t *s0,
-                      const uint8_t *s1, const uint16_t *const (&x)[2][NT], W4Stage<UP, NT> &st,
-                      f32x4 (&acc)[2][NT]) {
-    constexpr int P = UP ? 1 : 2;                 // h comes as two halves
+// through LDS to the matrix units. Memory is read in contiguous runs: the
+// weights by quads of lanes, 64 bytes of row lane / 4, the tokens by 16 lanes,
+// 256 bytes of token lane / 16, while the product wants row lane % 16 (a load
+// in the product's own order has a lane per row and costs the first-level
+// cache four times the accesses). TOK tokens fill the product's 16 columns over
+// and over. TAIL: blocks past the row's end count as zeros, of both operands.
+template <bool UP, int TOK, int U, bool TAIL>
+MOE_DEV void w4_steps(int s, int nblk, const W4Tiles &wt, const uint16_t *const (&x)[2][TOK / 4],
+                      W4Stage<UP, TOK> &st, f32x4 (&acc)[2]) {
+    constexpr int P = UP ? 1 : 2, J = TOK / 4;    // h comes as two halves
     const int lane = threadIdx.x & 63, g = lane >> 4, i = lane & 15, lr = lane >> 2, lc = lane & 3;
-    u32x4 w[U][2], xr[U][P][NT][4];
+    u32x4 w[U][2], xr[U][P][J];
     uint8_t sc[U][2];
     const u32x4 zero = {0, 0, 0, 0};
 #pragma unroll
     for (int u = 0; u < U; u++) {
         const int c = 4 * (s + u) + lc;
-        const bool ok = !TAIL || c < nblk;
         w[u][0] = w[u][1] = zero;
         sc[u][0] = sc[u][1] = 127;
-        if (ok) {
-            w[u][0] = *reinterpret_cast<const u32x4 *>(q0 + 16 * c);
-            w[u][1] = *reinterpret_cast<const u32x4 *>(q1 + 16 * c);
-            sc[u][0] = s0[c];
-            sc[u][1] = s1[c];
+        if (!TAIL || c < nblk) {
+            const uint32_t o = lr * nblk + c;     // block of the tile
+            w[u][0] = *reinterpret_cast<const u32x4 *>(wt.q0 + 16 * o);
+            w[u][1] = *reinterpret_cast<const u32x4 *>(wt.q1 + 16 * o);
+            sc[u][0] = wt.s0[o];
+            sc[u][1] = wt.s1[o];
         }
     }
 #pragma unroll
-    for (int t = 0; t < NT; t++)
+    for (int j = 0; j < J; j++)
 #pragma unroll
         for (int p = 0; p < P; p++)
-            if (x[p][t]) {
+            if (x[p][j]) {
 #pragma unroll
                 for (int u = 0; u < U; u++)
-#pragma unroll
-                    for (int j = 0; j < 4; j++) {
-                        const int c = 4 * (s + u) + j;
-                        xr[u][p][t][j] = !TAIL || c < nblk
-                            ? *reinterpret_cast<const u32x4 *>(x[p][t] + 32 * c + 8 * lc) : zero;
-                    }
+                    xr[u][p][j] = !TAIL || 4 * (s + u) + (i >> 2) < nblk
+                        ? *reinterpret_cast<const u32x4 *>(x[p][j] + 128 * (s + u) + 8 * i) : zero;
             }
 #pragma unroll
     for (int u = 0; u < U; u++) {
@@ -186,12 +199,10 @@ MOE_DEV void w4_steps(int s, int nblk, const uint8_t *q0, const uint8_t *q1, con
             st.sc[z][lane] = sc[u][z];
         }
 #pragma unroll
-        for (int t = 0; t < NT; t++)
+        for (int j = 0; j < J; j++)
 #pragma unroll
             for (int p = 0; p < P; p++)
-                if (x[p][t])
-#pragma unroll
-                    for (int j = 0; j < 4; j++) st.x[p][t][w4_xslot(lr, 4 * j + lc)] = xr[u][p][t][j];
+                if (x[p][j]) st.x[p][w4_xslot(4 * j + g, i)] = xr[u][p][j];
         w4_lds_order();
         u32x4 a[2];
         float f[2];
@@ -204,21 +215,19 @@ MOE_DEV void w4_steps(int s, int nblk, const uint8_t *q0, const uint8_t *q1, con
         for (int m = 0; m < 4; m++) {
             const bf16x8 a0 = w4_widen(a[0][m], f[0]), a1 = w4_widen(a[1][m], f[1]);
 #pragma unroll
-            for (int t = 0; t < NT; t++)
-#pragma unroll
-                for (int p = 0; p < P; p++) {
-                    const bf16x8 b = __builtin_bit_cast(bf16x8, st.x[p][t][w4_xslot(i, 4 * g + m)]);
-                    acc[0][t] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(a0, b, acc[0][t], 0, 0, 0);
-                    acc[1][t] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(a1, b, acc[1][t], 0, 0, 0);
-                }
+            for (int p = 0; p < P; p++) {
+                const bf16x8 b = __builtin_bit_cast(bf16x8, st.x[p][w4_xslot(i & (TOK - 1), 4 * g + m)]);
+                acc[0] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(a0, b, acc[0], 0, 0, 0);
+                acc[1] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(a1, b, acc[1], 0, 0, 0);
+            }
         }
     }
 }
 
-// LDS of a workgroup: the waves' stages, then (SPLIT) their sums.
-template <bool UP, int NT>
+// LDS of a workgroup: the waves' stages, then their sums.
+template <bool UP, int TOK>
 union W4Lds {
-    W4Stage<UP, NT> stage[4];
+    W4Stage<UP, TOK> stage[4];
     float red[4][2][256];
 };
 
@@ -242,23 +251,87 @@ MOE_DEV void w4_store(const W4Args &p, int64_t row, int n, const float *v0, cons
     }
 }
 
-// Rows [r, r + 16 NT) of the expert's rows [.., r1), two tiles of 16 weight
-// rows: gate and up of 16 columns, or 32 rows of W2. SPLIT: a workgroup's
-// four waves take a quarter of the reduction each and join their sums in LDS;
-// otherwise each has tiles of its own. The columns of the product past the
-// expert's last row hold what LDS held (a token is a column: it reaches no
-// other) and are not stored.
-template <bool UP, int NT, int U, bool SPLIT>
-MOE_DEV void w4_rows(const W4Args &p, int64_t wrow0, int64_t wrow1, int n0, int r, int r1,
-                     W4Lds<UP, NT> &lds) {
-    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, lr = lane >> 2;
+// Rows [r, r + TOK) of the expert's rows [.., r1), two tiles of 16 weight
+// rows: gate and up of 16 columns, or 32 rows of W2. The four waves take a
+// quarter of the reduction each and join their sums in LDS. The columns of the
+// product past the expert's last row hold what LDS held (a token is a column:
+// it reaches no other) and are not stored.
+template <bool UP, int TOK, int U>
+MOE_DEV void w4_rows(const W4Args &p, const W4Tiles &wt, int n0, int r, int r1,
+                     W4Lds<UP, TOK> &lds) {
+    const int lane = threadIdx.x & 63, wave = w4_wave(), g = lane >> 4, i = lane & 15;
     const int nblk = p.K / 32;
-    const uint8_t *q0 = p.wq + (wrow0 + lr) * (p.K / 2), *q1 = p.wq + (wrow1 + lr) * (p.K / 2);
-    const uint8_t *s0 = p.ws + (wrow0 + lr) * nblk, *s1 = p.ws + (wrow1 + lr) * nblk;
+    const uint16_t *x[2][TOK / 4];
+#pragma unroll
+    for (int j = 0; j < TOK / 4; j++) {
+        const int row = r + 4 * j + g;
+        x[0][j] = x[1][j] = nullptr;
+        if (row < r1) {
+            const int64_t src = (UP ? p.sorted_token[row] : row) * (int64_t)p.K;
+            x[0][j] = p.x + src;
+            x[1][j] = UP ? nullptr : p.lo + src;
+        }
+    }
+    f32x4 acc[2] = {f32x4{0.f, 0.f, 0.f, 0.f}, f32x4{0.f, 0.f, 0.f, 0.f}};
+    const int steps = (nblk + 3) / 4, part = (steps + 3) / 4;
+    int s = wave * part;
+    const int end = min(s + part, steps), whole = min(end, nblk / 4);
+    W4Stage<UP, TOK> &st = lds.stage[wave];
+    for (; s + U <= whole; s += U)
+        w4_steps<UP, TOK, U, false>(s, nblk, wt, x, st, acc);
+    for (; s < end; s++) w4_steps<UP, TOK, 1, true>(s, nblk, wt, x, st, acc);
+    // lane: column i (token i while i < TOK), weight rows 4 g .. 4 g + 3
+    __syncthreads();                              // the stages have been read
+#pragma unroll
+    for (int z = 0; z < 2; z++) *reinterpret_cast<f32x4 *>(&lds.red[wave][z][i * 16 + 4 * g]) = acc[z];
+    __syncthreads();
+    const int tid = threadIdx.x, tok = tid >> 4;
+    float v[2];
+#pragma unroll
+    for (int z = 0; z < 2; z++)
+        v[z] = (lds.red[0][z][tid] + lds.red[1][z][tid]) + (lds.red[2][z][tid] + lds.red[3][z][tid]);
+    if (tok < TOK && r + tok < r1) w4_store<UP, 1>(p, r + tok, n0 + (tid & 15), &v[0], &v[1]);
+    __syncthreads();                              // the sums have been read
+}
+
+// blockIdx.x: 16 columns of h (UP) or 32 of d; blockIdx.y: rank of an expert
+// with rows
+template <bool UP>
+__global__ __launch_bounds__(256, 4) void w4_product(W4Args p, const int32_t *__restrict__ offsets,
+                                                     int E) {
+    __shared__ W4Lds<UP, kW4Tokens> lds;
+    int e, r0, r1;
+    if (!w4_active(offsets, E, blockIdx.y, e, r0, r1)) return;      // the whole workgroup
+    const int n0 = blockIdx.x * (UP ? 16 : 32);
+    const int64_t w0 = (int64_t)e * (UP ? 2 * p.h : p.d) + n0;
+    const W4Tiles wt(p, w0, w0 + (UP ? p.h : 16));
+    for (int r = r0; r < r1; r += kW4Tokens)
+        w4_rows<UP, kW4Tokens, kW4Steps>(p, wt, n0, r, r1, lds);
+}
+
+// Many rows an expert: rows [r, r + 16 NT), every wave its own two tiles of
+// weight rows over the whole reduction, in pieces of 4 steps (512 elements).
+// The workgroup keeps a piece of its tokens in LDS for all four waves; a
+// wave's weights of the next piece, and the tokens', are in flight while the
+// piece is computed.
+template <bool UP, int NT>
+struct W4Wide {
+    u32x4 x[UP ? 1 : 2][NT][16 * 64];             // 16 tokens of 64 pieces of 16 bytes
+    u32x4 w[4][2][64];                            // a step of each wave
+    uint8_t sc[4][2][64];
+};
+
+template <bool UP, int NT>
+MOE_DEV void w4_rows_wide(const W4Args &p, const W4Tiles &wt, int n0, bool store, int r, int r1,
+                          W4Wide<UP, NT> &lds) {
+    constexpr int P = UP ? 1 : 2;
+    const int tid = threadIdx.x, lane = tid & 63, wave = w4_wave(), g = lane >> 4, i = lane & 15;
+    const int lr = lane >> 2, lc = lane & 3, xt = tid >> 4, xc = tid & 15;
+    const int nblk = p.K / 32, pieces = (nblk + 15) / 16;
     const uint16_t *x[2][NT];
 #pragma unroll
     for (int t = 0; t < NT; t++) {
-        const int row = r + 16 * t + lr;
+        const int row = r + 16 * t + xt;
         x[0][t] = x[1][t] = nullptr;
         if (row < r1) {
             const int64_t src = (UP ? p.sorted_token[row] : row) * (int64_t)p.K;
@@ -266,60 +339,171 @@ MOE_DEV void w4_rows(const W4Args &p, int64_t wrow0, int64_t wrow1, int n0, int 
             x[1][t] = UP ? nullptr : p.lo + src;
         }
     }
+    const u32x4 zero = {0, 0, 0, 0};
+    u32x4 w[4][2], xr[P][NT][4];
+    uint32_t sc[4][2];
+    // blocks past the row's end: zeros, of both operands
+    auto load_w = [&](int piece) {
+#pragma unroll
+        for (int u = 0; u < 4; u++) {
+            const int c = 16 * piece + 4 * u + lc;
+            w[u][0] = w[u][1] = zero;
+            sc[u][0] = sc[u][1] = 127;
+            if (c < nblk) {
+                const uint32_t o = lr * nblk + c;
+                w[u][0] = *reinterpret_cast<const u32x4 *>(wt.q0 + 16 * o);
+                w[u][1] = *reinterpret_cast<const u32x4 *>(wt.q1 + 16 * o);
+                sc[u][0] = wt.s0[o];
+                sc[u][1] = wt.s1[o];
+            }
+        }
+    };
+    auto load_x = [&](int piece) {
+#pragma unroll
+        for (int t = 0; t < NT; t++)
+#pragma unroll
+            for (int q = 0; q < P; q++)
+                if (x[q][t]) {
+#pragma unroll
+                    for (int j = 0; j < 4; j++) {
+                        const int c = 64 * piece + 16 * j + xc;      // 16-byte piece of the row
+                        xr[q][t][j] = c < 4 * nblk
+                            ? *reinterpret_cast<const u32x4 *>(x[q][t] + 8 * c) : zero;
+                    }
+                }
+    };
     f32x4 acc[2][NT];
 #pragma unroll
     for (int z = 0; z < 2; z++)
 #pragma unroll
         for (int t = 0; t < NT; t++) acc[z][t] = f32x4{0.f, 0.f, 0.f, 0.f};
-    const int steps = (nblk + 3) / 4, part = SPLIT ? (steps + 3) / 4 : steps;
-    int s = SPLIT ? wave * part : 0;
-    const int end = min(s + part, steps), whole = min(end, nblk / 4);
-    W4Stage<UP, NT> &st = lds.stage[wave];
-    for (; s + U <= whole; s += U)
-        w4_steps<UP, NT, U, false>(s, nblk, q0, q1, s0, s1, x, st, acc);
-    for (; s < end; s++) w4_steps<UP, NT, 1, true>(s, nblk, q0, q1, s0, s1, x, st, acc);
-    // lane: token lane % 16, weight rows 4 (lane / 16) .. + 3
-    const int i = lane & 15, n4 = 4 * (lane >> 4);
-    if constexpr (!SPLIT) {
+    load_w(0);
+    load_x(0);
+    for (int piece = 0; piece < pieces; piece++) {
+        __syncthreads();                          // the tokens' piece before has been read
 #pragma unroll
-        for (int t = 0; t < NT; t++) {
-            const int row = r + 16 * t + i;
-            const float v0[4] = {acc[0][t][0], acc[0][t][1], acc[0][t][2], acc[0][t][3]};
-            const float v1[4] = {acc[1][t][0], acc[1][t][1], acc[1][t][2], acc[1][t][3]};
-            if (row < r1) w4_store<UP, 4>(p, row, n0 + n4, v0, v1);
+        for (int t = 0; t < NT; t++)
+#pragma unroll
+            for (int q = 0; q < P; q++)
+                if (x[q][t])
+#pragma unroll
+                    for (int j = 0; j < 4; j++)
+                        lds.x[q][t][64 * xt + 16 * j + (xc ^ (4 * (xt & 3) + (xt >> 2)))] = xr[q][t][j];
+        u32x4 wc[4][2];
+        uint32_t cc[4][2];
+#pragma unroll
+        for (int u = 0; u < 4; u++)
+#pragma unroll
+            for (int z = 0; z < 2; z++) { wc[u][z] = w[u][z]; cc[u][z] = sc[u][z]; }
+        if (piece + 1 < pieces) {
+            load_w(piece + 1);
+            load_x(piece + 1);
         }
-        return;
+        __syncthreads();
+#pragma unroll
+        for (int u = 0; u < 4; u++) {
+            w4_lds_order();                       // the step before has been read
+#pragma unroll
+            for (int z = 0; z < 2; z++) {
+                lds.w[wave][z][w4_wslot(lr, lc)] = wc[u][z];
+                lds.sc[wave][z][lane] = (uint8_t)cc[u][z];
+            }
+            w4_lds_order();
+            u32x4 a[2];
+            float f[2];
+#pragma unroll
+            for (int z = 0; z < 2; z++) {
+                a[z] = lds.w[wave][z][w4_wslot(i, g)];
+                f[z] = __uint_as_float((uint32_t)lds.sc[wave][z][4 * i + g] << 23);
+            }
+#pragma unroll
+            for (int m = 0; m < 4; m++) {
+                const bf16x8 a0 = w4_widen(a[0][m], f[0]), a1 = w4_widen(a[1][m], f[1]);
+#pragma unroll
+                for (int t = 0; t < NT; t++)
+#pragma unroll
+                    for (int q = 0; q < P; q++) {
+                        const bf16x8 b = __builtin_bit_cast(
+                            bf16x8, lds.x[q][t][64 * i + 16 * u + ((4 * g + m) ^ (4 * (i & 3) + (i >> 2)))]);
+                        acc[0][t] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(a0, b, acc[0][t], 0, 0, 0);
+                        acc[1][t] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(a1, b, acc[1][t], 0, 0, 0);
+                    }
+            }
+        }
     }
+    // lane: token i, weight rows 4 g .. 4 g + 3
 #pragma unroll
     for (int t = 0; t < NT; t++) {
-        __syncthreads();                          // the stages, or the tile before, have been read
-#pragma unroll
-        for (int z = 0; z < 2; z++) *reinterpret_cast<f32x4 *>(&lds.red[wave][z][i * 16 + n4]) = acc[z][t];
-        __syncthreads();
-        const int tid = threadIdx.x, row = r + 16 * t + (tid >> 4), n = tid & 15;
-        float v[2];
-#pragma unroll
-        for (int z = 0; z < 2; z++)
-            v[z] = (lds.red[0][z][tid] + lds.red[1][z][tid]) + (lds.red[2][z][tid] + lds.red[3][z][tid]);
-        if (row < r1) w4_store<UP, 1>(p, row, n0 + n, &v[0], &v[1]);
+        const int row = r + 16 * t + i;
+        const float v0[4] = {acc[0][t][0], acc[0][t][1], acc[0][t][2], acc[0][t][3]};
+        const float v1[4] = {acc[1][t][0], acc[1][t][1], acc[1][t][2], acc[1][t][3]};
+        if (store && row < r1) w4_store<UP, 4>(p, row, n0 + 4 * g, v0, v1);
     }
-    __syncthreads();                              // the sums have been read
 }
 
-// blockIdx.y: rank of an expert with rows; blockIdx.x: 16 columns of h (UP) or
-// 32 of d, without SPLIT four times as many, a quarter for each wave
-template <bool UP, int NT, int U, bool SPLIT>
-__global__ __launch_bounds__(256, NT == 1 ? 3 : 2) void w4_product(
-    W4Args p, const int32_t *__restrict__ offsets, int E) {
-    __shared__ W4Lds<UP, NT> lds;
+// blockIdx.x: 64 columns of h (UP) or 128 of d, a quarter for each wave;
+// blockIdx.y: rank of an expert with rows
+template <bool UP, int NT>
+__global__ __launch_bounds__(256, 2) void w4_product_wide(W4Args p,
+                                                          const int32_t *__restrict__ offsets,
+                                                          int E) {
+    __shared__ W4Wide<UP, NT> lds;
     int e, r0, r1;
     if (!w4_active(offsets, E, blockIdx.y, e, r0, r1)) return;      // the whole workgroup
-    const int tile = SPLIT ? blockIdx.x : 4 * blockIdx.x + (threadIdx.x >> 6);
-    const int n0 = tile * (UP ? 16 : 32);
-    if (!SPLIT && n0 >= (UP ? p.h : p.d)) return;                   // this wave alone: no barriers
-    const int64_t base = (int64_t)e * (UP ? 2 * p.h : p.d);
-    const int64_t w0 = base + n0, w1 = w0 + (UP ? p.h : 16);
-    for (int r = r0; r < r1; r += 16 * NT) w4_rows<UP, NT, U, SPLIT>(p, w0, w1, n0, r, r1, lds);
+    const int n0 = (4 * blockIdx.x + w4_wave()) * (UP ? 16 : 32), n = UP ? p.h : p.d;
+    // a wave past the last column stages its share of the tokens and stores nothing
+    const int m0 = min(n0, n - (UP ? 16 : 32));
+    const int64_t w0 = (int64_t)e * (UP ? 2 * p.h : p.d) + m0;
+    const W4Tiles wt(p, w0, w0 + (UP ? p.h : 16));
+    for (int r = r0; r < r1; r += 16 * NT) w4_rows_wide<UP, NT>(p, wt, m0, n0 < n, r, r1, lds);
+}
+
+// A handful of rows: out[t] for 32 columns from the token's own experts, gates
+// and sum included, in one launch (no y, no combine; an expert that tokens
+// share is read once for each). Wave: slot wave % 4 and on, half wave / 4 of
+// the reduction.
+__global__ __launch_bounds__(512) void w4_down_tokens(W4Args p, const int32_t *__restrict__ offsets,
+                                                      int E, const float *__restrict__ gate,
+                                                      const int32_t *__restrict__ token_pos, int k,
+                                                      uint16_t *__restrict__ out) {
+    constexpr int U = 4;
+    __shared__ W4Stage<false, 4> stage[8];
+    __shared__ float red[2][8][32];
+    const int64_t t = blockIdx.y;
+    const int lane = threadIdx.x & 63, wave = w4_wave(), g = lane >> 4, i = lane & 15;
+    const int n0 = 32 * blockIdx.x, nblk = p.K / 32;
+    const int steps = (nblk + 3) / 4, part = (steps + 1) / 2, begin = (wave >> 2) * part;
+    const int end = min(begin + part, steps), whole = min(end, nblk / 4);
+    for (int j = wave & 3; j < k; j += 4) {
+        const int row = __builtin_amdgcn_readfirstlane(token_pos[t * k + j]);
+        f32x4 acc[2] = {f32x4{0.f, 0.f, 0.f, 0.f}, f32x4{0.f, 0.f, 0.f, 0.f}};
+        if (row >= 0) {                           // not dropped
+            int e = 0;                            // experts that end at or before the row
+#pragma unroll
+            for (int q = 0; q < 4; q++) {
+                const int x = 64 * q + lane;
+                e += __popcll(__ballot(x < E && offsets[x + 1] <= row));
+            }
+            const W4Tiles wt(p, (int64_t)e * p.d + n0, (int64_t)e * p.d + n0 + 16);
+            const int64_t src = (int64_t)row * p.K;
+            const uint16_t *x[2][1] = {{g == 0 ? p.x + src : nullptr}, {g == 0 ? p.lo + src : nullptr}};
+            int s = begin;
+            for (; s + U <= whole; s += U) w4_steps<false, 4, U, false>(s, nblk, wt, x, stage[wave], acc);
+            for (; s < end; s++) w4_steps<false, 4, 1, true>(s, nblk, wt, x, stage[wave], acc);
+        }
+        if (i == 0) {                             // column 0: the token
+#pragma unroll
+            for (int z = 0; z < 2; z++)
+                *reinterpret_cast<f32x4 *>(&red[wave >> 2][j][16 * z + 4 * g]) = acc[z];
+        }
+    }
+    __syncthreads();
+    if (threadIdx.x >= 32) return;
+    float v = 0.f;
+    for (int j = 0; j < k; j++)
+        if (token_pos[t * k + j] >= 0)
+            v = fmaf(gate[t * k + j], red[0][j][threadIdx.x] + red[1][j][threadIdx.x], v);
+    out[t * p.d + n0 + threadIdx.x] = f32_to_bf16(v);
 }
 
 // out[t] = sum_j g y[token_pos] (fp32, ascending j), 4 columns a thread
@@ -360,7 +544,6 @@ moe_status w4_quantize_launch(const void *in, moe_dtype dt, int64_t rows, int64_
     return launch_status();
 }
 
-#define SPLIT_MAX 2048
 static size_t round256(size_t b) { return (b + 255) & ~(size_t)255; }
 
 // workspace: h's upper halves, its lower halves [R, h] bf16, y [R, d] fp32
@@ -375,23 +558,34 @@ moe_status w4_experts_launch(const moe_w4_desc *w, hipStream_t s) {
     uint16_t *hi = reinterpret_cast<uint16_t *>(ws), *lo = reinterpret_cast<uint16_t *>(ws + half);
     float *y = reinterpret_cast<float *>(ws + 2 * half);
     const unsigned ny = (unsigned)(R < w->E ? R : w->E);
-    const bool few = R <= 8 * (int64_t)w->E;
     const W4Args up = {reinterpret_cast<const uint16_t *>(w->x), nullptr, w->sorted_token, w->w1q,
                        w->w1_scale, hi, lo, nullptr, w->d, w->h, w->d};
     const W4Args down = {hi, lo, nullptr, w->w2q, w->w2_scale, nullptr, nullptr, y, w->h, w->h, w->d};
     const int nu = w->h / 16, nd = w->d / 32;
-    if (!few)
-        w4_product<true, 2, 2, false><<<dim3((nu + 3) / 4, ny), 256, 0, s>>>(up, w->offsets, w->E);
-    else if ((int64_t)nu * ny <= SPLIT_MAX)
-        w4_product<true, 1, 2, true><<<dim3(nu, ny), 256, 0, s>>>(up, w->offsets, w->E);
+    // Which kernels, by rows an expert (R / E) and workgroups (all three
+    // launches, d = 2048, h = 1024; E = 128, k = 4 unless said):
+    //  - a handful of rows: the down product by token, T = 8 (R = E / 4) 27.1 us
+    //    against 31.4; where tokens share experts it reads them again, E = 8, k =
+    //    2, T = 16 (R = 4 E) 18.7 us against 16.4; T = 16 (4,096 workgroups) 48.8
+    //    against 47.7;
+    //  - eight rows an expert and up, and a workgroup of 64 columns for every
+    //    compute unit: the wide kernels, T = 256 134 us against 146; T = 128 129
+    //    against 107; E = 8, k = 2, T = 128 (128 workgroups) 43.3 against 41.0.
+    auto wide = [&](int n) { return R >= 8 * (int64_t)w->E && (int64_t)((n + 3) / 4) * ny >= 256; };
+    if (wide(nu))
+        w4_product_wide<true, kW4WideTiles><<<dim3((nu + 3) / 4, ny), 256, 0, s>>>(up, w->offsets, w->E);
     else
-        w4_product<true, 1, 2, false><<<dim3((nu + 3) / 4, ny), 256, 0, s>>>(up, w->offsets, w->E);
-    if (!few)
-        w4_product<false, 2, 1, false><<<dim3((nd + 3) / 4, ny), 256, 0, s>>>(down, w->offsets, w->E);
-    else if ((int64_t)nd * ny <= SPLIT_MAX)
-        w4_product<false, 1, 2, true><<<dim3(nd, ny), 256, 0, s>>>(down, w->offsets, w->E);
+        w4_product<true><<<dim3(nu, ny), 256, 0, s>>>(up, w->offsets, w->E);
+    if (R <= 2 * (int64_t)w->E && nd * R <= 2048) {
+        w4_down_tokens<<<dim3(nd, (unsigned)w->T), 512, 0, s>>>(
+            down, w->offsets, w->E, w->topk_gate, w->token_pos, w->k,
+            reinterpret_cast<uint16_t *>(w->out));
+        return launch_status();
+    }
+    if (wide(nd))
+        w4_product_wide<false, kW4WideTiles><<<dim3((nd + 3) / 4, ny), 256, 0, s>>>(down, w->offsets, w->E);
     else
-        w4_product<false, 1, 2, false><<<dim3((nd + 3) / 4, ny), 256, 0, s>>>(down, w->offsets, w->E);
+        w4_product<false><<<dim3(nd, ny), 256, 0, s>>>(down, w->offsets, w->E);
     const int cb = (w->d + 1023) / 1024;
     const int64_t piece = kMaxBlocks / cb;
     for (int64_t t = 0; t < w->T; t += piece) {
