@@ -602,9 +602,11 @@ moe_status moe_backward_act8(const moe_bwd_desc *b, const moe_act8_saved *c, voi
  * x8 [T, d], x8_scale [T, d/32]: both or neither; s as an 8-bit checkpoint
  * (the format of moe_act8_store), written from the same read. d: a multiple
  * of 32, at most 16384; T < 2^31; 0 < eps <= 1 (MOE_ERR_SHAPE otherwise).
- * Tensors, gamma, beta and x8 16-byte aligned. Sums are fp32 in a fixed order. A row
- * with a NaN or an infinity gives NaNs in that row alone. Outputs must not
- * overlap inputs. T = 0 is a no-op. */
+ * Tensors, gamma, beta and x8 16-byte aligned, mean and rstd 4-byte. Sums are
+ * fp32 in a fixed order: the sum of a row's squared distances from its mean
+ * has to be finite in fp32 (distances under 1e17). A row with a NaN or an
+ * infinity gives NaNs in that row alone. Outputs must not overlap inputs. T = 0
+ * is a no-op. */
 moe_status moe_layer_norm(const void *x, moe_dtype dt, const void *residual, const float *gamma,
                           const float *beta, float eps, int64_t T, int32_t d, void *y, void *sum,
                           float *mean, float *rstd, uint8_t *x8, uint8_t *x8_scale, void *stream);
@@ -644,8 +646,9 @@ moe_status moe_w4_quantize(const void *in, moe_dtype in_dt, int64_t rows, int64_
                            uint8_t *scale, void *stream);
 
 /* The expert layer's forward after the routing, for the few tokens of a
- * generation step (a few rows per expert; the weights of an expert are read
- * once per 64 of its rows), with W1, W2 in 4 bits:
+ * generation step (an expert's weights are read once for every 8 of its rows,
+ * or 32 with many: with hundreds of rows an expert moe_grouped_gemm is the
+ * faster way), with W1, W2 in 4 bits:
  *   H' = silu(a) b with a, b = W1[e] x[t],  out[t] = sum_j g[t, j] W2[e_j] H'
  * x, out [T, d] bf16; accumulation, H' (to 16 significant bits) and the
  * experts' outputs stay wider than bf16 until out is rounded. topk_gate,

@@ -1076,7 +1076,8 @@ class LayerNorm:
     input from forward to backward as an 8-bit checkpoint (33/64 of its bf16
     size), written by the forward's kernel; otherwise the backward reads x (or
     sum), which the caller must leave as it was. Buffers are allocated once
-    per (T, dtype, device) and reused."""
+    per (T, dtype, device) and reused: calls (or replays) of one object must
+    not overlap in time."""
 
     def __init__(self, weight: torch.Tensor, bias: torch.Tensor | None = None, eps: float = 1e-5,
                  act8: bool = False):
@@ -1539,7 +1540,8 @@ class MoELayerW4:
     with MXFP4 weights (moe_w4_experts), for a step's few tokens. w1 [E, 2h,
     d], w2 [E, d, h] (f32 or bf16) are quantised once and not kept. Buffers
     are allocated once per (T, device), so a step is kernel launches alone
-    and can be captured in a HIP graph."""
+    and can be captured in a HIP graph; calls (or replays) of one layer object
+    must not overlap in time, they share its buffers."""
 
     def __init__(self, w1: torch.Tensor, w2: torch.Tensor, k: int):
         self.E, h2, self.d = w1.shape

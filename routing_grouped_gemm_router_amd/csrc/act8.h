@@ -22,9 +22,9 @@
 
 namespace moe {
 
-// A grid has fewer than 2^32 threads: at most 2^23 workgroups of 256 a launch,
-// larger inputs in pieces.
-constexpr int64_t kMaxBlocks = 1 << 23;
+// A grid has fewer than 2^32 threads: at most 2^21 workgroups (of up to 1024)
+// a launch, larger inputs in pieces.
+constexpr int64_t kMaxBlocks = 1 << 21;
 
 // 16-byte vectors of a row: 8 bf16 or 4 fp32 elements
 template <bool BF16>

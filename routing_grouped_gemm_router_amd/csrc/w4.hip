@@ -16,9 +16,22 @@
 // scale block of 32 per lane. Which 8 of the 32 reduction indices a lane
 // brings is free as long as both operands agree: here lane l takes block
 // 4 s + l / 16 of row l % 16 in step s, 16 contiguous bytes, in four MFMAs,
-// so weights are read in their plain layout. h is handed on as the sum of two
-// bf16 (16 significant bits) and y in fp32: the only rounding to bf16 is
-// out's.
+// so weights are kept in their plain layout. h is handed on as the sum of two
+// bf16 (16 significant bits, two products) and y in fp32: the only rounding to
+// bf16 is out's.
+//
+// Bound by the weights' bytes with tokens for most experts, by the latency of
+// a launch and a chain of loads with few. d = 2048, h = 1024, E = 128, k = 4: 64
+// tokens (111 experts, 371 MB) 53 + 34 + 5 us, 4.0 TB/s of the 6.1 that a plain
+// read of memory reaches; one token (4 experts, 13 MB) 6.4 + 5.5 us. What it took:
+// no branch around a load (106 -> 77 us for gate and up), memory read by runs of
+// lanes and put into the product's order through LDS (77 -> 58 us: the
+// first-level cache looked up 39 million lines for the 4 million there are),
+// tokens no more than 8 at a time (down 47 -> 31 us; registers and LDS for 16
+// leave a third of the waves out). What is left is loads in flight: a wave
+// waits for its two steps, computes them, and asks for the next; a ring of
+// loads straight into LDS would keep more under way. Loads past the last-level
+// cache were slower here (55 -> 61 us).
 #include "act8.h"
 
 namespace moe {

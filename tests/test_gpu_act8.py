@@ -326,3 +326,46 @@ def test_layer_no_tokens():
     assert out.shape == (0, 128)
     g = layer.backward(torch.empty(0, 128, dtype=torch.bfloat16, device="cuda"))
     assert (g["dw1"] == 0).all() and (g["dw2"] == 0).all()
+
+
+@pytest.mark.parametrize("offset", [1, 4])
+def test_misaligned_tensors_are_refused(offset):
+    """A contiguous view that does not start on 16 bytes: an error, nothing enqueued."""
+    x = torch.zeros(4 * 64 + 16, device="cuda")[offset:offset + 4 * 64].view(4, 64)
+    q = torch.zeros(4 * 64 + 16, dtype=torch.uint8, device="cuda")[offset:offset + 4 * 64].view(4, 64)
+    s = torch.zeros(4, 2, dtype=torch.uint8, device="cuda")
+    ga = torch.ones(64, device="cuda")
+    calls = [lambda: moe.moe_act8_load(q, s), lambda: moe.moe_act8_swiglu(q, s)]
+    if offset % 4:
+        calls += [lambda: moe.moe_act8_store(x), lambda: moe.moe_layer_norm(x, ga)]
+    for call in calls:
+        with pytest.raises(moe.MoeError) as err:
+            call()
+        assert err.value.status == moe.MOE_ERR_ALIGN
+    other = torch.zeros(4, 128, device="cuda")[:, :64]
+    for call in (lambda: moe.moe_act8_store(other), lambda: moe.moe_layer_norm(other, ga)):
+        with pytest.raises(ValueError):
+            call()                                         # rows with gaps
+
+
+def test_offsets_past_32_bits():
+    """More vectors than one launch takes, more bytes than 32 bits count: the
+    last rows come out as they do by themselves, the rows behind stay."""
+    cols = 16384
+    rows = (1 << 29) // (cols // 8) + 3                    # 2^29 vectors of 8 bf16 a launch
+    x = torch.empty((rows, cols), dtype=torch.bfloat16, device="cuda")
+    x.fill_(0.5)
+    tail = torch.randn(7, cols, device="cuda").bfloat16()
+    x[-7:] = tail
+    q = torch.empty((rows + 1, cols), dtype=torch.uint8, device="cuda")
+    q[-1] = 9
+    q, s = moe.moe_act8_store(x, q[:rows], torch.empty((rows, cols // 32), dtype=torch.uint8, device="cuda"))
+    q1, s1 = moe.moe_act8_store(tail)
+    assert torch.equal(q[-7:], q1) and torch.equal(s[-7:], s1) and int(q[0, 0]) == 64
+    x.fill_(7)
+    moe.moe_act8_load(q, s, out=x)
+    assert torch.equal(x[-7:], moe.moe_act8_load(q1, s1)) and float(x[1, 1]) == 0.5
+    h = cols // 2
+    ab, hp = moe.moe_act8_swiglu(q, s, ab=x)
+    ab1, hp1 = moe.moe_act8_swiglu(q1, s1)
+    assert torch.equal(ab[-7:], ab1) and torch.equal(hp[-7:], hp1) and hp.shape == (rows, h)

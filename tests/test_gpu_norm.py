@@ -210,3 +210,25 @@ def test_nothing_else_is_written(T, d):
         dx=g["dx"][:n].view(T, d), dweight=g["dweight"][:d], dbias=g["dbias"][:d]))
     for k, v in dict(g, ws=ws).items():
         assert (v[-16:] == 9).all(), k
+
+
+def test_offsets_past_32_bits():
+    """More rows than one launch takes and more than 2^32 bytes: the last rows
+    come out as they do by themselves."""
+    d, T = 2080, (1 << 21) + 5                             # 2^21 workgroups of one row a launch
+    x = torch.empty((T, d), dtype=torch.bfloat16, device="cuda")
+    x.fill_(1)
+    tail = torch.randn(6, d, device="cuda").bfloat16()
+    x[-6:] = tail
+    ga = torch.ones(d, device="cuda")
+    f = moe.moe_layer_norm(x, ga, act8=True)
+    one = moe.moe_layer_norm(tail, ga, act8=True)
+    for k in ("y", "mean", "rstd", "x8", "x8_scale"):
+        assert torch.equal(f[k][-6:], one[k]), k
+    b = moe.moe_layer_norm_backward(f, x, ga, out=dict(
+        dx=f["y"], dweight=torch.empty(d, device="cuda"), dbias=torch.empty(d, device="cuda")))
+    b1 = moe.moe_layer_norm_backward(one, tail, ga)
+    assert torch.equal(b["dx"][-6:], b1["dx"])
+    # constant rows: xh = 0; dbias counts them, in fp32 sums of whole numbers below 2^24
+    assert torch.allclose(b["dweight"], b1["dweight"], atol=1e-5)
+    assert ((b["dbias"] - (T - 6) - b1["dbias"]).abs() <= 1.0).all()

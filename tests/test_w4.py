@@ -260,3 +260,19 @@ def test_two_streams():
                 got.append(moe.moe_w4_experts(x, r, *a))
         torch.cuda.synchronize()
         assert all(torch.equal(p, q) for p, q in zip(alone, got))
+
+
+@gpu
+def test_nan_token_reaches_no_other():
+    """A token with a NaN spoils its own output; the others share its experts."""
+    for T, E, k, d, h in ((6, 2, 2, 96, 64), (1, 4, 2, 64, 64), (300, 64, 2, 416, 224)):
+        w1q, s1, w2q, s2, _, _ = _weights(E, d, h, T)
+        x = dev(synth.normal((T, d), 10, 1, 1.0), torch.bfloat16)
+        r = moe.moe_route(dev(synth.normal((T, E), 10, 0, 1.0), torch.float32), k)
+        clean = moe.moe_w4_experts(x, r, w1q, s1, w2q, s2)
+        bad = x.clone()
+        bad[T // 2, 5], bad[T // 2, d - 1] = float("nan"), float("inf")
+        out = moe.moe_w4_experts(bad, r, w1q, s1, w2q, s2)
+        assert torch.isnan(out[T // 2]).all()
+        keep = torch.arange(T, device="cuda") != T // 2
+        assert torch.equal(out[keep], clean[keep])
