@@ -553,8 +553,9 @@ moe_status moe_act8_swiglu(const uint8_t *ab8, const uint8_t *ab8_scale, moe_dty
 
 /* moe_combine (the same out, bit for bit) that also stores the checkpoint of
  * every y_perm row it reads, from the same read: y8 [R, d], y8_scale
- * [R, d/32], R = the rows of y_perm. Rows that no token_pos names are left
- * as they were. */
+ * [R, d/32], R = the rows of y_perm, which token_pos stays below. Each row is
+ * named by at most one token_pos; those that none names are left as they
+ * were. */
 moe_status moe_combine_act8(const void *y_perm, moe_dtype dt, const float *topk_gate,
                             const int32_t *token_pos, int64_t T, int32_t d, int32_t k, void *out,
                             uint8_t *y8, uint8_t *y8_scale, void *stream);
@@ -564,8 +565,9 @@ moe_status moe_combine_act8(const void *y_perm, moe_dtype dt, const float *topk_
  *   dgate[t, j] = <dout[t], y8[token_pos[t, j]]>        (dgate may be null)
  *   dy_perm[token_pos[t, j]] = topk_gate[t, j] * dout[t], rounded to dt
  *   dlogits[t, e_i] = g_i sum_j g_j (dgate_i - dgate_j), 0 for unselected
- *   experts. A slot with token_pos < 0 counts as dgate = 0; rows of dy_perm
- *   that no token_pos names are left as they were. */
+ *   experts. A slot with token_pos < 0 counts as dgate = 0. Each row is named
+ *   by at most one token_pos; rows of dy_perm that none names are left as
+ *   they were. */
 moe_status moe_combine_backward_act8(const void *dout, moe_dtype dt, const uint8_t *y8,
                                      const uint8_t *y8_scale, const float *topk_gate,
                                      const int32_t *topk_idx, const int32_t *token_pos, int64_t T,

@@ -28,10 +28,12 @@
 // lanes and put into the product's order through LDS (77 -> 58 us: the
 // first-level cache looked up 39 million lines for the 4 million there are),
 // tokens no more than 8 at a time (down 47 -> 31 us; registers and LDS for 16
-// leave a third of the waves out). What is left is loads in flight: a wave
-// waits for its two steps, computes them, and asks for the next; a ring of
-// loads straight into LDS would keep more under way. Loads past the last-level
-// cache were slower here (55 -> 61 us).
+// leave a third of the waves out). What is left is the loads themselves: in the
+// same order, without the products, they take 48 and 30 us, 5 of them for the
+// scale bytes. Loads past the last-level cache (61 us), whole rows a wave (56
+// us), fewer and longer workgroups (55 to 62 us), the next step's lines touched
+// ahead (60 us) or more registers for loads (59 us) were slower than gate and
+// up's 53 us.
 #include "act8.h"
 
 namespace moe {

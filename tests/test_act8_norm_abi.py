@@ -190,3 +190,31 @@ def test_binding_refuses_what_does_not_fit():
         moe.MoELayer(w1, w2, 1, recompute=True, act8=True)
     with pytest.raises(ValueError):
         moe.LayerNorm(z(64)).backward(z(4, 64))
+
+
+def test_calls_go_to_the_tensors_gpu(monkeypatch):
+    """A call on a GPU that is not the current one makes it current for the
+    call and takes its stream; a refusal raises either way."""
+    seen, current = [], [1]
+
+    class Device:
+        def __init__(self, index):
+            self.index = index
+
+        def __enter__(self):
+            self.before, current[0] = current[0], self.index
+
+        def __exit__(self, *exc):
+            current[0] = self.before
+
+    monkeypatch.setattr(moe, "_cur_device", lambda: current[0])
+    monkeypatch.setattr(moe, "_raw_stream", lambda index: 100 + index)
+    monkeypatch.setattr(torch.cuda, "device", Device)
+    call = lambda a, stream: seen.append((a, stream, current[0])) or a
+    moe._enqueue("f", call, 0, 0)
+    moe._enqueue("f", call, 1, 0)
+    assert seen == [(0, 100, 0), (0, 101, 1)] and current == [1]
+    for index in (0, 1):
+        with pytest.raises(moe.MoeError):
+            moe._enqueue("f", call, index, moe.MOE_ERR_SHAPE)
+    assert current == [1]
