@@ -832,9 +832,9 @@ def moe_layer_norm(x: torch.Tensor, weight: torch.Tensor, bias: torch.Tensor | N
         _need_on(residual, (T, d), x.dtype, gpu, "residual")
     if out is None:
         dev = x.device
-        out = dict(y=torch.empty((T, d), dtype=x.dtype, device=dev))
+        out = dict(y=torch.empty_like(x))
         if residual is not None:
-            out["sum"] = torch.empty((T, d), dtype=x.dtype, device=dev)
+            out["sum"] = torch.empty_like(x)
         if stats:
             out["mean"] = torch.empty(T, dtype=f32, device=dev)
             out["rstd"] = torch.empty(T, dtype=f32, device=dev)
@@ -901,7 +901,7 @@ def moe_layer_norm_backward(saved: dict, dy: torch.Tensor, weight: torch.Tensor,
         if accumulate_dw:
             raise ValueError("accumulate_dw needs the gradients of an earlier backward (out)")
         dev = dy.device
-        out = dict(dx=torch.empty((T, d), dtype=dy.dtype, device=dev))
+        out = dict(dx=torch.empty_like(dy))
         if want_dweight:
             out["dweight"] = torch.empty(d, dtype=f32, device=dev)
         if want_dbias:
@@ -978,7 +978,7 @@ def moe_w4_experts(x: torch.Tensor, route: dict, w1q: torch.Tensor, w1_scale: to
     _need_on(tok, (T * k,), i32, gpu, "sorted_token")
     _need_on(off, (E + 1,), i32, gpu, "offsets")
     if out is None:
-        out = torch.empty((T, d), dtype=x.dtype, device=x.device)
+        out = torch.empty_like(x)
     else:
         _need_on(out, (T, d), x.dtype, gpu, "out")
     ws = _need_ws(ws, moe_w4_experts_workspace_size(T, k, d, h), x, gpu)
