@@ -1088,7 +1088,7 @@ class LayerNorm:
     def forward(self, x: torch.Tensor, residual: torch.Tensor | None = None) -> torch.Tensor:
         key = (x.shape, x.dtype, x.device, residual is None)
         if self._key != key:
-            self._out, self._ws, self.grads = None, None, None
+            self._out, self._ws, self.grads, self._key = None, None, None, None
         self._out = moe_layer_norm(x, self.weight, self.bias, self.eps, residual, self.act8,
                                    out=self._out)
         self._key = key
@@ -1105,8 +1105,9 @@ class LayerNorm:
         if accumulate_dw and self.grads is None:
             raise ValueError("accumulate_dw needs the gradients of an earlier backward")
         if self._ws is None:
-            wsb = moe_layer_norm_backward_workspace_size(_dt(dy), dy.shape[0], dy.shape[-1])
-            self._ws = torch.empty(max(wsb, 16), dtype=torch.uint8, device=dy.device)
+            y = self._out["y"]
+            wsb = moe_layer_norm_backward_workspace_size(_dt(y), *y.shape)
+            self._ws = torch.empty(max(wsb, 16), dtype=torch.uint8, device=y.device)
         self.grads = moe_layer_norm_backward(dict(self._out, x=self._x), dy, self.weight, dsum,
                                              out=self.grads, accumulate_dw=accumulate_dw,
                                              want_dbias=self.bias is not None, ws=self._ws)

@@ -372,6 +372,12 @@ constexpr int norm_group(int nv, bool bwd) {
 constexpr int norm_vecs(int nv, bool bwd) {
     return (nv + norm_group(nv, bwd) - 1) / norm_group(nv, bwd);
 }
+constexpr bool norm_covered() {
+    for (int nv = 4; nv <= 4096; nv += 4)
+        if (norm_vecs(nv, false) > 4 || norm_vecs(nv, true) > 4) return false;
+    return true;
+}
+static_assert(norm_covered(), "NORM_SWITCH has up to four vectors a thread");
 // whether any width (d = 32, 64, ..) of the type uses G threads of V vectors
 template <bool BF16>
 constexpr bool norm_used(int g, int v, bool bwd) {

@@ -232,3 +232,30 @@ def test_offsets_past_32_bits():
     # constant rows: xh = 0; dbias counts them, in fp32 sums of whole numbers below 2^24
     assert torch.allclose(b["dweight"], b1["dweight"], atol=1e-5)
     assert ((b["dbias"] - (T - 6) - b1["dbias"]).abs() <= 1.0).all()
+
+
+def test_refused_calls_leave_the_object_usable():
+    """A gradient of the wrong size, then a forward that is refused: neither
+    leaves buffers of the wrong size or a half-made state behind."""
+    n = lambda i, t: dev(synth.normal((t, 256), 41, i, 1.0), torch.float32)
+    w = dev(1 + synth.normal((256,), 41, 9, 0.1), torch.float32)
+    norm = moe.LayerNorm(w, None, EPS)
+    with pytest.raises(ValueError, match="without a forward"):
+        norm.backward(n(2, 300))
+    norm.forward(n(1, 300))
+    with pytest.raises(ValueError, match="x: expected"):
+        norm.backward(n(2, 3))
+    dx = norm.backward(n(2, 300))["dx"].clone()
+    assert torch.equal(dx, _fresh_dx(w, n(1, 300), n(2, 300)))
+    with pytest.raises(ValueError, match="residual"):
+        norm.forward(n(1, 8), n(3, 9))
+    with pytest.raises(ValueError, match="without a forward"):
+        norm.backward(n(2, 8))
+    norm.forward(n(1, 8), n(3, 8))
+    assert torch.equal(norm.backward(n(2, 8))["dx"], _fresh_dx(w, n(1, 8) + n(3, 8), n(2, 8)))
+
+
+def _fresh_dx(w, x, dy):
+    norm = moe.LayerNorm(w, None, EPS)
+    norm.forward(x)
+    return norm.backward(dy)["dx"]

@@ -165,3 +165,28 @@ def test_one_token_without_a_backward():
     whole = moe.moe_layer_norm(v["x"], v["g1"], v["b1"], EPS, residual=v["res"])
     one = moe.moe_layer_norm(x, v["g1"], v["b1"], EPS, residual=r, stats=False)
     assert torch.equal(one["y"], whole["y"][:1]) and torch.equal(one["sum"], whole["sum"][:1])
+
+
+@pytest.mark.parametrize("kind", ["bf16", "bf16 act8", "mxfp8 act8"])
+def test_micro_batches_accumulate(kind):
+    """Two backward passes of one forward, the second added to the first: the
+    weight gradients, the norm's among them, are exactly doubled (the same
+    sum twice, one fp32 addition), dx and the rest as before."""
+    v = _data(torch.bfloat16)
+    act8 = kind.endswith("act8")
+    norm = moe.LayerNorm(v["g2"], v["b1"], EPS, act8=act8)
+    make = moe.MoELayerMX if kind.startswith("mxfp8") else moe.MoELayer
+    w = (v["w1"].float(), v["w2"].float()) if make is moe.MoELayerMX else (v["w1"], v["w2"])
+    layer = make(*w, K, act8=act8, scratch={}, out_norm=norm)
+    layer.forward(v["x"], v["x"].float() @ v["wr"].t())
+    with pytest.raises(ValueError, match="earlier backward"):
+        layer.backward(v["dout"], accumulate_dw=True)
+    names = ("dx", "dlogits", "dw1", "dw2", "dnorm_weight", "dnorm_bias")
+    g = layer.backward(v["dout"])
+    one = {n: g[n].clone() for n in names}
+    g = layer.backward(v["dout"], accumulate_dw=True)
+    for n in names:
+        assert torch.equal(g[n], one[n] * (2 if n.startswith(("dw", "dnorm")) else 1)), n
+    g = layer.backward(v["dout"])
+    for n in names:
+        assert torch.equal(g[n], one[n]), n
