@@ -119,6 +119,7 @@ MOE_DEV bool w4_active(const int32_t *offsets, int E, int slot, int &e, int &r0,
 
 constexpr int kW4Tokens = 8;     // rows of an expert that a wave multiplies at once
 constexpr int kW4Steps = 2;      // steps of 128 reduction indices loaded at once
+constexpr int kW4MaxSteps = 4;   // the most that any kernel loads at once
 constexpr int kW4WideTiles = 2;  // row tiles of 16 with many rows
 
 struct W4Args {
@@ -144,13 +145,19 @@ struct W4Tiles {
 
 MOE_DEV int w4_wave() { return __builtin_amdgcn_readfirstlane(threadIdx.x >> 6); }
 
+// U bytes
+template <int U> struct W4Bytes;
+template <> struct W4Bytes<1> { typedef uint8_t type; };
+template <> struct W4Bytes<2> { typedef uint16_t type; };
+template <> struct W4Bytes<4> { typedef uint32_t type; };
+
 // What a wave keeps in LDS of one step: both weight tiles (16 rows of 4
-// blocks, 16 bytes each), their scales, and per half of h TOK tokens of 4
-// blocks in 16-byte pieces.
+// blocks, 16 bytes each) and, per half of h, TOK tokens of 4 blocks in 16-byte
+// pieces; and the scales of all steps that were loaded together.
 template <bool UP, int TOK>
 struct W4Stage {
     u32x4 w[2][64];
-    uint8_t sc[2][64];
+    uint8_t sc[2][16 * 4 * kW4MaxSteps];
     u32x4 x[UP ? 1 : 2][TOK * 16];
 };
 
@@ -167,64 +174,83 @@ MOE_DEV void w4_lds_order() {
     __builtin_amdgcn_wave_barrier();
 }
 
-// Steps [s, s + U) of a wave's reduction: all global loads, then step by step
-// through LDS to the matrix units. Memory is read in contiguous runs: the
-// weights by quads of lanes, 64 bytes of row lane / 4, the tokens by 16 lanes,
-// 256 bytes of token lane / 16, while the product wants row lane % 16 (a load
-// in the product's own order has a lane per row and costs the first-level
-// cache four times the accesses). TOK tokens fill the product's 16 columns over
-// and over. TAIL: blocks past the row's end count as zeros, of both operands.
-template <bool UP, int TOK, int U, bool TAIL>
-MOE_DEV void w4_steps(int s, int nblk, const W4Tiles &wt, const uint16_t *const (&x)[2][TOK / 4],
-                      W4Stage<UP, TOK> &st, f32x4 (&acc)[2]) {
-    constexpr int P = UP ? 1 : 2, J = TOK / 4;    // h comes as two halves
-    const int lane = threadIdx.x & 63, g = lane >> 4, i = lane & 15, lr = lane >> 2, lc = lane & 3;
-    u32x4 w[U][2], xr[U][P][J];
-    uint8_t sc[U][2];
-    const u32x4 zero = {0, 0, 0, 0};
+// The weights of steps [s, s + U) of a wave's reduction: per step a block of
+// each tile, and U scale bytes. Memory is read in contiguous runs, 64 bytes of
+// row lane / 4 by a quad of lanes. TAIL: blocks past the row's end count as
+// zeros.
+template <int U, bool TAIL>
+struct W4Loaded {
+    u32x4 w[U][2];
+    typename W4Bytes<U>::type sc[2];
+    MOE_DEV void load(int s, int nblk, const W4Tiles &wt) {
+        static_assert(U <= kW4MaxSteps && (!TAIL || U == 1));
+        const int lane = threadIdx.x & 63, lr = lane >> 2, lc = lane & 3;
+        const u32x4 zero = {0, 0, 0, 0};
 #pragma unroll
-    for (int u = 0; u < U; u++) {
-        const int c = 4 * (s + u) + lc;
-        w[u][0] = w[u][1] = zero;
-        sc[u][0] = sc[u][1] = 127;
-        if (!TAIL || c < nblk) {
-            const uint32_t o = lr * nblk + c;     // block of the tile
-            w[u][0] = *reinterpret_cast<const u32x4 *>(wt.q0 + 16 * o);
-            w[u][1] = *reinterpret_cast<const u32x4 *>(wt.q1 + 16 * o);
-            sc[u][0] = wt.s0[o];
-            sc[u][1] = wt.s1[o];
+        for (int u = 0; u < U; u++) {
+            const int c = 4 * (s + u) + lc;
+            w[u][0] = w[u][1] = zero;
+            if (!TAIL || c < nblk) {
+                const uint32_t o = lr * nblk + c;     // block of the tile
+                w[u][0] = *reinterpret_cast<const u32x4 *>(wt.q0 + 16 * o);
+                w[u][1] = *reinterpret_cast<const u32x4 *>(wt.q1 + 16 * o);
+            }
+        }
+        // scales of the U steps: 4 U bytes of a row, U (at any address) a lane
+        sc[0] = sc[1] = 127;
+        if (!TAIL || 4 * s + lc < nblk) {
+            const uint32_t o = lr * nblk + 4 * s + U * lc;
+            __builtin_memcpy(&sc[0], wt.s0 + o, U);
+            __builtin_memcpy(&sc[1], wt.s1 + o, U);
         }
     }
+};
+
+// Their products: the tokens' loads (16 lanes 256 bytes of token 4 j + lane /
+// 16, at x[.][j], for j < quads, which is uniform), then step by step through
+// LDS to the matrix units, which want row lane % 16 (a load in the product's
+// own order has a lane per row and costs the first-level cache four times the
+// accesses). TOK tokens fill the product's 16 columns over and over.
+template <bool UP, int TOK, int U, bool TAIL>
+MOE_DEV void w4_steps(int s, int nblk, const W4Loaded<U, TAIL> &l, int quads,
+                      const uint16_t *const (&x)[2][TOK / 4], W4Stage<UP, TOK> &st,
+                      f32x4 (&acc)[2]) {
+    constexpr int P = UP ? 1 : 2, J = TOK / 4;    // h comes as two halves
+    typedef typename W4Bytes<U>::type Sc;
+    const int lane = threadIdx.x & 63, g = lane >> 4, i = lane & 15, lr = lane >> 2, lc = lane & 3;
+    const u32x4 zero = {0, 0, 0, 0};
+    u32x4 xr[U][P][J];
 #pragma unroll
     for (int j = 0; j < J; j++)
+        if (j == 0 || j < quads) {
 #pragma unroll
-        for (int p = 0; p < P; p++)
-            if (x[p][j]) {
+            for (int p = 0; p < P; p++)
 #pragma unroll
                 for (int u = 0; u < U; u++)
                     xr[u][p][j] = !TAIL || 4 * (s + u) + (i >> 2) < nblk
                         ? *reinterpret_cast<const u32x4 *>(x[p][j] + 128 * (s + u) + 8 * i) : zero;
-            }
+        }
 #pragma unroll
     for (int u = 0; u < U; u++) {
         w4_lds_order();                           // the step before has been read
 #pragma unroll
         for (int z = 0; z < 2; z++) {
-            st.w[z][w4_wslot(lr, lc)] = w[u][z];
-            st.sc[z][lane] = sc[u][z];
+            st.w[z][w4_wslot(lr, lc)] = l.w[u][z];
+            if (u == 0) *reinterpret_cast<Sc *>(&st.sc[z][U * lane]) = l.sc[z];
         }
 #pragma unroll
         for (int j = 0; j < J; j++)
+            if (j == 0 || j < quads) {
 #pragma unroll
-            for (int p = 0; p < P; p++)
-                if (x[p][j]) st.x[p][w4_xslot(4 * j + g, i)] = xr[u][p][j];
+                for (int p = 0; p < P; p++) st.x[p][w4_xslot(4 * j + g, i)] = xr[u][p][j];
+            }
         w4_lds_order();
         u32x4 a[2];
         float f[2];
 #pragma unroll
         for (int z = 0; z < 2; z++) {
             a[z] = st.w[z][w4_wslot(i, g)];
-            f[z] = __uint_as_float((uint32_t)st.sc[z][4 * i + g] << 23);
+            f[z] = __uint_as_float((uint32_t)st.sc[z][4 * (U * i + u) + g] << 23);
         }
 #pragma unroll
         for (int m = 0; m < 4; m++) {
@@ -236,6 +262,31 @@ MOE_DEV void w4_steps(int s, int nblk, const W4Tiles &wt, const uint16_t *const 
                 acc[1] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(a1, b, acc[1], 0, 0, 0);
             }
         }
+    }
+}
+
+// Steps [s, end) of a wave, U at a time. address(): forms x, after the first
+// weights have been asked for.
+template <bool UP, int TOK, int U, class Address>
+MOE_DEV void w4_reduce(int s, int end, int nblk, const W4Tiles &wt, int quads, Address address,
+                       W4Stage<UP, TOK> &st, f32x4 (&acc)[2]) {
+    const uint16_t *x[2][TOK / 4];
+    const int whole = min(end, nblk / 4);
+    W4Loaded<U, false> l;
+    const bool any = s + U <= whole;
+    if (any) l.load(s, nblk, wt);
+    address(x);
+    if (any)
+        for (;;) {
+            w4_steps<UP, TOK>(s, nblk, l, quads, x, st, acc);
+            s += U;
+            if (s + U > whole) break;
+            l.load(s, nblk, wt);
+        }
+    for (; s < end; s++) {
+        W4Loaded<1, true> t;
+        t.load(s, nblk, wt);
+        w4_steps<UP, TOK>(s, nblk, t, quads, x, st, acc);
     }
 }
 
@@ -266,62 +317,67 @@ MOE_DEV void w4_store(const W4Args &p, int64_t row, int n, const float *v0, cons
     }
 }
 
-// Rows [r, r + TOK) of the expert's rows [.., r1), two tiles of 16 weight
-// rows: gate and up of 16 columns, or 32 rows of W2. The four waves take a
-// quarter of the reduction each and join their sums in LDS. The columns of the
-// product past the expert's last row hold what LDS held (a token is a column:
-// it reaches no other) and are not stored.
-template <bool UP, int TOK, int U>
-MOE_DEV void w4_rows(const W4Args &p, const W4Tiles &wt, int n0, int r, int r1,
+// Rows [r, r + TOK) of the expert's rows [.., r1). KS waves share the two
+// tiles of 16 weight rows (gate and up of 16 columns, or 32 rows of W2), a
+// part of the reduction each, and join their sums in LDS; 4 / KS such pairs
+// side by side, from column n0 of n. The columns of the product past the
+// expert's last row repeat it, or hold what LDS held (a token is a column: it
+// reaches no other), and are not stored.
+template <bool UP, int TOK, int U, int KS>
+MOE_DEV void w4_rows(const W4Args &p, const W4Tiles &wt, int n0, int n, int r, int r1,
                      W4Lds<UP, TOK> &lds) {
     const int lane = threadIdx.x & 63, wave = w4_wave(), g = lane >> 4, i = lane & 15;
     const int nblk = p.K / 32;
-    const uint16_t *x[2][TOK / 4];
+    auto address = [&](const uint16_t *(&x)[2][TOK / 4]) {
 #pragma unroll
-    for (int j = 0; j < TOK / 4; j++) {
-        const int row = r + 4 * j + g;
-        x[0][j] = x[1][j] = nullptr;
-        if (row < r1) {
+        for (int j = 0; j < TOK / 4; j++) {
+            const int row = min(r + 4 * j + g, r1 - 1);
             const int64_t src = (UP ? p.sorted_token[row] : row) * (int64_t)p.K;
             x[0][j] = p.x + src;
             x[1][j] = UP ? nullptr : p.lo + src;
         }
-    }
+    };
     f32x4 acc[2] = {f32x4{0.f, 0.f, 0.f, 0.f}, f32x4{0.f, 0.f, 0.f, 0.f}};
-    const int steps = (nblk + 3) / 4, part = (steps + 3) / 4;
-    int s = wave * part;
-    const int end = min(s + part, steps), whole = min(end, nblk / 4);
-    W4Stage<UP, TOK> &st = lds.stage[wave];
-    for (; s + U <= whole; s += U)
-        w4_steps<UP, TOK, U, false>(s, nblk, wt, x, st, acc);
-    for (; s < end; s++) w4_steps<UP, TOK, 1, true>(s, nblk, wt, x, st, acc);
+    const int steps = (nblk + 3) / 4, part = (steps + KS - 1) / KS, s = (wave % KS) * part;
+    w4_reduce<UP, TOK, U>(s, min(s + part, steps), nblk, wt, (r1 - r + 3) / 4, address,
+                          lds.stage[wave], acc);
     // lane: column i (token i while i < TOK), weight rows 4 g .. 4 g + 3
     __syncthreads();                              // the stages have been read
 #pragma unroll
     for (int z = 0; z < 2; z++) *reinterpret_cast<f32x4 *>(&lds.red[wave][z][i * 16 + 4 * g]) = acc[z];
     __syncthreads();
     const int tid = threadIdx.x, tok = tid >> 4;
-    float v[2];
 #pragma unroll
-    for (int z = 0; z < 2; z++)
-        v[z] = (lds.red[0][z][tid] + lds.red[1][z][tid]) + (lds.red[2][z][tid] + lds.red[3][z][tid]);
-    if (tok < TOK && r + tok < r1) w4_store<UP, 1>(p, r + tok, n0 + (tid & 15), &v[0], &v[1]);
+    for (int t = 0; t < 4 / KS; t++) {
+        float v[2];
+#pragma unroll
+        for (int z = 0; z < 2; z++) {
+            v[z] = 0;
+#pragma unroll
+            for (int q = 0; q < KS; q++) v[z] += lds.red[t * KS + q][z][tid];
+        }
+        const int n1 = n0 + t * (UP ? 16 : 32);
+        if (tok < TOK && r + tok < r1 && n1 < n) w4_store<UP, 1>(p, r + tok, n1 + (tid & 15), &v[0], &v[1]);
+    }
     __syncthreads();                              // the sums have been read
 }
 
-// blockIdx.x: 16 columns of h (UP) or 32 of d; blockIdx.y: rank of an expert
-// with rows
-template <bool UP>
+// blockIdx.x: 16 columns of h (UP) or 32 of d, times 4 / KS; blockIdx.y: rank
+// of an expert with rows
+template <bool UP, int KS>
 __global__ __launch_bounds__(256, 4) void w4_product(W4Args p, const int32_t *__restrict__ offsets,
                                                      int E) {
     __shared__ W4Lds<UP, kW4Tokens> lds;
     int e, r0, r1;
     if (!w4_active(offsets, E, blockIdx.y, e, r0, r1)) return;      // the whole workgroup
-    const int n0 = blockIdx.x * (UP ? 16 : 32);
-    const int64_t w0 = (int64_t)e * (UP ? 2 * p.h : p.d) + n0;
+    constexpr int C = UP ? 16 : 32;
+    const int n = UP ? p.h : p.d, n0 = blockIdx.x * C * (4 / KS);
+    // waves past the last column multiply it again and store nothing
+    const int m0 = min(n0 + w4_wave() / KS * C, n - C);
+    const int64_t w0 = (int64_t)e * (UP ? 2 * p.h : p.d) + m0;
     const W4Tiles wt(p, w0, w0 + (UP ? p.h : 16));
     for (int r = r0; r < r1; r += kW4Tokens)
-        w4_rows<UP, kW4Tokens, kW4Steps>(p, wt, n0, r, r1, lds);
+        w4_rows<UP, kW4Tokens, kW4Steps, KS>(p, wt, n0, n, r, r1, lds);
 }
 
 // Many rows an expert: rows [r, r + 16 NT), every wave its own two tiles of
@@ -483,41 +539,39 @@ __global__ __launch_bounds__(512) void w4_down_tokens(W4Args p, const int32_t *_
                                                       uint16_t *__restrict__ out) {
     constexpr int U = 4;
     __shared__ W4Stage<false, 4> stage[8];
-    __shared__ float red[2][8][32];
+    __shared__ float red[2][8][32], sg[8];
     const int64_t t = blockIdx.y;
     const int lane = threadIdx.x & 63, wave = w4_wave(), g = lane >> 4, i = lane & 15;
     const int n0 = 32 * blockIdx.x, nblk = p.K / 32;
     const int steps = (nblk + 3) / 4, part = (steps + 1) / 2, begin = (wave >> 2) * part;
-    const int end = min(begin + part, steps), whole = min(end, nblk / 4);
+    const int end = min(begin + part, steps);
+    int ends[4];                                  // of the experts' rows
+#pragma unroll
+    for (int q = 0; q < 4; q++) ends[q] = 64 * q + lane < E ? offsets[64 * q + lane + 1] : INT32_MAX;
     for (int j = wave & 3; j < k; j += 4) {
+        const float w = gate[t * k + j];
         const int row = __builtin_amdgcn_readfirstlane(token_pos[t * k + j]);
         f32x4 acc[2] = {f32x4{0.f, 0.f, 0.f, 0.f}, f32x4{0.f, 0.f, 0.f, 0.f}};
         if (row >= 0) {                           // not dropped
             int e = 0;                            // experts that end at or before the row
 #pragma unroll
-            for (int q = 0; q < 4; q++) {
-                const int x = 64 * q + lane;
-                e += __popcll(__ballot(x < E && offsets[x + 1] <= row));
-            }
+            for (int q = 0; q < 4; q++) e += __popcll(__ballot(ends[q] <= row));
             const W4Tiles wt(p, (int64_t)e * p.d + n0, (int64_t)e * p.d + n0 + 16);
             const int64_t src = (int64_t)row * p.K;
-            const uint16_t *x[2][1] = {{g == 0 ? p.x + src : nullptr}, {g == 0 ? p.lo + src : nullptr}};
-            int s = begin;
-            for (; s + U <= whole; s += U) w4_steps<false, 4, U, false>(s, nblk, wt, x, stage[wave], acc);
-            for (; s < end; s++) w4_steps<false, 4, 1, true>(s, nblk, wt, x, stage[wave], acc);
+            auto address = [&](const uint16_t *(&x)[2][1]) { x[0][0] = p.x + src; x[1][0] = p.lo + src; };
+            w4_reduce<false, 4, U>(begin, end, nblk, wt, 1, address, stage[wave], acc);
         }
         if (i == 0) {                             // column 0: the token
 #pragma unroll
             for (int z = 0; z < 2; z++)
                 *reinterpret_cast<f32x4 *>(&red[wave >> 2][j][16 * z + 4 * g]) = acc[z];
+            if (lane == 0 && wave < 4) sg[j] = row >= 0 ? w : 0.f;
         }
     }
     __syncthreads();
     if (threadIdx.x >= 32) return;
     float v = 0.f;
-    for (int j = 0; j < k; j++)
-        if (token_pos[t * k + j] >= 0)
-            v = fmaf(gate[t * k + j], red[0][j][threadIdx.x] + red[1][j][threadIdx.x], v);
+    for (int j = 0; j < k; j++) v = fmaf(sg[j], red[0][j][threadIdx.x] + red[1][j][threadIdx.x], v);
     out[t * p.d + n0 + threadIdx.x] = f32_to_bf16(v);
 }
 
@@ -586,11 +640,19 @@ moe_status w4_experts_launch(const moe_w4_desc *w, hipStream_t s) {
     //  - eight rows an expert and up, and a workgroup of 64 columns for every
     //    compute unit: the wide kernels, T = 256 134 us against 146; T = 128 129
     //    against 107; E = 8, k = 2, T = 128 (128 workgroups) 43.3 against 41.0.
+    //  - five workgroups a compute unit and up: two waves a reduction, not four,
+    //    so that half as many workgroups look for their expert and join sums:
+    //    T = 16 45.0 us against 47.7, T = 64 85.3 against 88.0, T = 128 101
+    //    against 104; fewer leave compute units out: E = 8, k = 2, T = 16 17.0
+    //    against 15.4.
     auto wide = [&](int n) { return R >= 8 * (int64_t)w->E && (int64_t)((n + 3) / 4) * ny >= 256; };
+    auto pairs = [&](int n) { return (int64_t)n * ny >= 1280; };
     if (wide(nu))
         w4_product_wide<true, kW4WideTiles><<<dim3((nu + 3) / 4, ny), 256, 0, s>>>(up, w->offsets, w->E);
+    else if (pairs(nu))
+        w4_product<true, 2><<<dim3((nu + 1) / 2, ny), 256, 0, s>>>(up, w->offsets, w->E);
     else
-        w4_product<true><<<dim3(nu, ny), 256, 0, s>>>(up, w->offsets, w->E);
+        w4_product<true, 4><<<dim3(nu, ny), 256, 0, s>>>(up, w->offsets, w->E);
     if (R <= 2 * (int64_t)w->E && nd * R <= 2048) {
         w4_down_tokens<<<dim3(nd, (unsigned)w->T), 512, 0, s>>>(
             down, w->offsets, w->E, w->topk_gate, w->token_pos, w->k,
@@ -599,8 +661,10 @@ moe_status w4_experts_launch(const moe_w4_desc *w, hipStream_t s) {
     }
     if (wide(nd))
         w4_product_wide<false, kW4WideTiles><<<dim3((nd + 3) / 4, ny), 256, 0, s>>>(down, w->offsets, w->E);
+    else if (pairs(nd))
+        w4_product<false, 2><<<dim3((nd + 1) / 2, ny), 256, 0, s>>>(down, w->offsets, w->E);
     else
-        w4_product<false><<<dim3(nd, ny), 256, 0, s>>>(down, w->offsets, w->E);
+        w4_product<false, 4><<<dim3(nd, ny), 256, 0, s>>>(down, w->offsets, w->E);
     const int cb = (w->d + 1023) / 1024;
     const int64_t piece = kMaxBlocks / cb;
     for (int64_t t = 0; t < w->T; t += piece) {
