@@ -119,7 +119,6 @@ MOE_DEV bool w4_active(const int32_t *offsets, int E, int slot, int &e, int &r0,
 
 constexpr int kW4Tokens = 8;     // rows of an expert that a wave multiplies at once
 constexpr int kW4Steps = 2;      // steps of 128 reduction indices loaded at once
-constexpr int kW4MaxSteps = 4;   // the most that any kernel loads at once
 constexpr int kW4WideTiles = 2;  // row tiles of 16 with many rows
 
 struct W4Args {
@@ -151,20 +150,21 @@ template <> struct W4Bytes<1> { typedef uint8_t type; };
 template <> struct W4Bytes<2> { typedef uint16_t type; };
 template <> struct W4Bytes<4> { typedef uint32_t type; };
 
-// What a wave keeps in LDS of one step: both weight tiles (16 rows of 4
-// blocks, 16 bytes each) and, per half of h, TOK tokens of 4 blocks in 16-byte
-// pieces; and the scales of all steps that were loaded together.
-template <bool UP, int TOK>
+// What a wave keeps in LDS: both weight tiles of the U steps that were loaded
+// together (16 rows of 4 U blocks, 16 bytes each) with their scales, and of one
+// step, per half of h, TOK tokens of 4 blocks in 16-byte pieces.
+template <bool UP, int TOK, int U>
 struct W4Stage {
-    u32x4 w[2][64];
-    uint8_t sc[2][16 * 4 * kW4MaxSteps];
+    u32x4 w[2][64 * U];
+    uint8_t sc[2][64 * U];
     u32x4 x[UP ? 1 : 2][TOK * 16];
 };
 
 // Pieces are kept at the place of their index with some of its bits flipped
 // by the row's, so that the 16 lanes that read one piece of 16 rows each meet
 // different banks.
-MOE_DEV int w4_wslot(int row, int blk) { return 4 * row + (blk ^ (row >> 2)); }
+template <int U>
+MOE_DEV int w4_wslot(int row, int blk) { return 4 * U * row + (blk ^ (row / (4 / U))); }
 MOE_DEV int w4_xslot(int row, int piece) { return 16 * row + (piece ^ (4 * (row & 3) + (row >> 2))); }
 
 // The lanes of a wave see each other's LDS writes in program order; this
@@ -174,29 +174,28 @@ MOE_DEV void w4_lds_order() {
     __builtin_amdgcn_wave_barrier();
 }
 
-// The weights of steps [s, s + U) of a wave's reduction: per step a block of
-// each tile, and U scale bytes. Memory is read in contiguous runs, 64 bytes of
-// row lane / 4 by a quad of lanes. TAIL: blocks past the row's end count as
-// zeros.
+// The weights of steps [s, s + U) of a wave's reduction: 4 U blocks of 16 rows
+// of each tile, and U scale bytes a lane. Memory is read in contiguous runs, 64
+// U bytes of a row by 4 U lanes. TAIL: blocks past the row's end count as zeros.
 template <int U, bool TAIL>
 struct W4Loaded {
-    u32x4 w[U][2];
-    typename W4Bytes<U>::type sc[2];
+    u32x4 w[U][2];                                // row 16 / U * q + lane / (4 U)
+    typename W4Bytes<U>::type sc[2];              // row lane / 4
     MOE_DEV void load(int s, int nblk, const W4Tiles &wt) {
-        static_assert(U <= kW4MaxSteps && (!TAIL || U == 1));
+        static_assert(!TAIL || U == 1);
         const int lane = threadIdx.x & 63, lr = lane >> 2, lc = lane & 3;
+        const int c = 4 * s + lane % (4 * U);
         const u32x4 zero = {0, 0, 0, 0};
 #pragma unroll
-        for (int u = 0; u < U; u++) {
-            const int c = 4 * (s + u) + lc;
-            w[u][0] = w[u][1] = zero;
+        for (int q = 0; q < U; q++) {
+            w[q][0] = w[q][1] = zero;
             if (!TAIL || c < nblk) {
-                const uint32_t o = lr * nblk + c;     // block of the tile
-                w[u][0] = *reinterpret_cast<const u32x4 *>(wt.q0 + 16 * o);
-                w[u][1] = *reinterpret_cast<const u32x4 *>(wt.q1 + 16 * o);
+                const uint32_t o = (16 / U * q + lane / (4 * U)) * nblk + c;     // block of the tile
+                w[q][0] = *reinterpret_cast<const u32x4 *>(wt.q0 + 16 * o);
+                w[q][1] = *reinterpret_cast<const u32x4 *>(wt.q1 + 16 * o);
             }
         }
-        // scales of the U steps: 4 U bytes of a row, U (at any address) a lane
+        // scales: 4 U bytes of a row, U (at any address) a lane
         sc[0] = sc[1] = 127;
         if (!TAIL || 4 * s + lc < nblk) {
             const uint32_t o = lr * nblk + 4 * s + U * lc;
@@ -207,17 +206,17 @@ struct W4Loaded {
 };
 
 // Their products: the tokens' loads (16 lanes 256 bytes of token 4 j + lane /
-// 16, at x[.][j], for j < quads, which is uniform), then step by step through
-// LDS to the matrix units, which want row lane % 16 (a load in the product's
-// own order has a lane per row and costs the first-level cache four times the
-// accesses). TOK tokens fill the product's 16 columns over and over.
-template <bool UP, int TOK, int U, bool TAIL>
+// 16, at x[.][j], for j < quads, which is uniform), then through LDS to the
+// matrix units, which want row lane % 16 (a load in the product's own order has
+// a lane per row and costs the first-level cache many times the accesses). TOK
+// tokens fill the product's 16 columns over and over.
+template <bool UP, int TOK, int U, int SU, bool TAIL>
 MOE_DEV void w4_steps(int s, int nblk, const W4Loaded<U, TAIL> &l, int quads,
-                      const uint16_t *const (&x)[2][TOK / 4], W4Stage<UP, TOK> &st,
+                      const uint16_t *const (&x)[2][(TOK + 3) / 4], W4Stage<UP, TOK, SU> &st,
                       f32x4 (&acc)[2]) {
-    constexpr int P = UP ? 1 : 2, J = TOK / 4;    // h comes as two halves
+    constexpr int P = UP ? 1 : 2, J = (TOK + 3) / 4;    // h comes as two halves
     typedef typename W4Bytes<U>::type Sc;
-    const int lane = threadIdx.x & 63, g = lane >> 4, i = lane & 15, lr = lane >> 2, lc = lane & 3;
+    const int lane = threadIdx.x & 63, g = lane >> 4, i = lane & 15;
     const u32x4 zero = {0, 0, 0, 0};
     u32x4 xr[U][P][J];
 #pragma unroll
@@ -230,26 +229,30 @@ MOE_DEV void w4_steps(int s, int nblk, const W4Loaded<U, TAIL> &l, int quads,
                     xr[u][p][j] = !TAIL || 4 * (s + u) + (i >> 2) < nblk
                         ? *reinterpret_cast<const u32x4 *>(x[p][j] + 128 * (s + u) + 8 * i) : zero;
         }
+    w4_lds_order();                               // the steps before have been read
+#pragma unroll
+    for (int z = 0; z < 2; z++) {
+#pragma unroll
+        for (int q = 0; q < U; q++)
+            st.w[z][w4_wslot<U>(16 / U * q + lane / (4 * U), lane % (4 * U))] = l.w[q][z];
+        *reinterpret_cast<Sc *>(&st.sc[z][U * lane]) = l.sc[z];
+    }
 #pragma unroll
     for (int u = 0; u < U; u++) {
-        w4_lds_order();                           // the step before has been read
-#pragma unroll
-        for (int z = 0; z < 2; z++) {
-            st.w[z][w4_wslot(lr, lc)] = l.w[u][z];
-            if (u == 0) *reinterpret_cast<Sc *>(&st.sc[z][U * lane]) = l.sc[z];
-        }
+        if (u) w4_lds_order();                    // the step before has been read
 #pragma unroll
         for (int j = 0; j < J; j++)
             if (j == 0 || j < quads) {
 #pragma unroll
-                for (int p = 0; p < P; p++) st.x[p][w4_xslot(4 * j + g, i)] = xr[u][p][j];
+                for (int p = 0; p < P; p++)
+                    if (TOK >= 4 || g == 0) st.x[p][w4_xslot(4 * j + g, i)] = xr[u][p][j];
             }
         w4_lds_order();
         u32x4 a[2];
         float f[2];
 #pragma unroll
         for (int z = 0; z < 2; z++) {
-            a[z] = st.w[z][w4_wslot(i, g)];
+            a[z] = st.w[z][w4_wslot<U>(i, 4 * u + g)];
             f[z] = __uint_as_float((uint32_t)st.sc[z][4 * (U * i + u) + g] << 23);
         }
 #pragma unroll
@@ -269,8 +272,8 @@ MOE_DEV void w4_steps(int s, int nblk, const W4Loaded<U, TAIL> &l, int quads,
 // weights have been asked for.
 template <bool UP, int TOK, int U, class Address>
 MOE_DEV void w4_reduce(int s, int end, int nblk, const W4Tiles &wt, int quads, Address address,
-                       W4Stage<UP, TOK> &st, f32x4 (&acc)[2]) {
-    const uint16_t *x[2][TOK / 4];
+                       W4Stage<UP, TOK, U> &st, f32x4 (&acc)[2]) {
+    const uint16_t *x[2][(TOK + 3) / 4];
     const int whole = min(end, nblk / 4);
     W4Loaded<U, false> l;
     const bool any = s + U <= whole;
@@ -291,9 +294,9 @@ MOE_DEV void w4_reduce(int s, int end, int nblk, const W4Tiles &wt, int quads, A
 }
 
 // LDS of a workgroup: the waves' stages, then their sums.
-template <bool UP, int TOK>
+template <bool UP, int TOK, int U>
 union W4Lds {
-    W4Stage<UP, TOK> stage[4];
+    W4Stage<UP, TOK, U> stage[4];
     float red[4][2][256];
 };
 
@@ -325,7 +328,7 @@ MOE_DEV void w4_store(const W4Args &p, int64_t row, int n, const float *v0, cons
 // reaches no other), and are not stored.
 template <bool UP, int TOK, int U, int KS>
 MOE_DEV void w4_rows(const W4Args &p, const W4Tiles &wt, int n0, int n, int r, int r1,
-                     W4Lds<UP, TOK> &lds) {
+                     W4Lds<UP, TOK, U> &lds) {
     const int lane = threadIdx.x & 63, wave = w4_wave(), g = lane >> 4, i = lane & 15;
     const int nblk = p.K / 32;
     auto address = [&](const uint16_t *(&x)[2][TOK / 4]) {
@@ -367,7 +370,7 @@ MOE_DEV void w4_rows(const W4Args &p, const W4Tiles &wt, int n0, int n, int r, i
 template <bool UP, int KS>
 __global__ __launch_bounds__(256, 4) void w4_product(W4Args p, const int32_t *__restrict__ offsets,
                                                      int E) {
-    __shared__ W4Lds<UP, kW4Tokens> lds;
+    __shared__ W4Lds<UP, kW4Tokens, kW4Steps> lds;
     int e, r0, r1;
     if (!w4_active(offsets, E, blockIdx.y, e, r0, r1)) return;      // the whole workgroup
     constexpr int C = UP ? 16 : 32;
@@ -476,7 +479,7 @@ MOE_DEV void w4_rows_wide(const W4Args &p, const W4Tiles &wt, int n0, bool store
             w4_lds_order();                       // the step before has been read
 #pragma unroll
             for (int z = 0; z < 2; z++) {
-                lds.w[wave][z][w4_wslot(lr, lc)] = wc[u][z];
+                lds.w[wave][z][w4_wslot<1>(lr, lc)] = wc[u][z];
                 lds.sc[wave][z][lane] = (uint8_t)cc[u][z];
             }
             w4_lds_order();
@@ -484,7 +487,7 @@ MOE_DEV void w4_rows_wide(const W4Args &p, const W4Tiles &wt, int n0, bool store
             float f[2];
 #pragma unroll
             for (int z = 0; z < 2; z++) {
-                a[z] = lds.w[wave][z][w4_wslot(i, g)];
+                a[z] = lds.w[wave][z][w4_wslot<1>(i, g)];
                 f[z] = __uint_as_float((uint32_t)lds.sc[wave][z][4 * i + g] << 23);
             }
 #pragma unroll
@@ -538,7 +541,7 @@ __global__ __launch_bounds__(512) void w4_down_tokens(W4Args p, const int32_t *_
                                                       const int32_t *__restrict__ token_pos, int k,
                                                       uint16_t *__restrict__ out) {
     constexpr int U = 4;
-    __shared__ W4Stage<false, 4> stage[8];
+    __shared__ W4Stage<false, 1, U> stage[8];
     __shared__ float red[2][8][32], sg[8];
     const int64_t t = blockIdx.y;
     const int lane = threadIdx.x & 63, wave = w4_wave(), g = lane >> 4, i = lane & 15;
@@ -559,7 +562,7 @@ __global__ __launch_bounds__(512) void w4_down_tokens(W4Args p, const int32_t *_
             const W4Tiles wt(p, (int64_t)e * p.d + n0, (int64_t)e * p.d + n0 + 16);
             const int64_t src = (int64_t)row * p.K;
             auto address = [&](const uint16_t *(&x)[2][1]) { x[0][0] = p.x + src; x[1][0] = p.lo + src; };
-            w4_reduce<false, 4, U>(begin, end, nblk, wt, 1, address, stage[wave], acc);
+            w4_reduce<false, 1, U>(begin, end, nblk, wt, 1, address, stage[wave], acc);
         }
         if (i == 0) {                             // column 0: the token
 #pragma unroll
