@@ -365,21 +365,34 @@ MOE_DEV void w4_rows(const W4Args &p, const W4Tiles &wt, int n0, int n, int r, i
     __syncthreads();                              // the sums have been read
 }
 
-// blockIdx.x: 16 columns of h (UP) or 32 of d, times 4 / KS; blockIdx.y: rank
+// An expert's rows are shared out to Z workgroups for each group of columns;
+// those Z are 8 apart, so that they run on one XCD and its cache serves the
+// weights again.
+MOE_DEV void w4_place(int Z, int &col, int &z) {
+    const int x = blockIdx.x;
+    col = Z == 1 ? x : x / (8 * Z) * 8 + x % 8;
+    z = Z == 1 ? 0 : x / 8 % Z;
+}
+static unsigned w4_grid(int cols, int Z) { return Z == 1 ? cols : (cols + 7) / 8 * 8 * Z; }
+
+// column group: 16 columns of h (UP) or 32 of d, times 4 / KS; blockIdx.y: rank
 // of an expert with rows
 template <bool UP, int KS>
 __global__ __launch_bounds__(256, 4) void w4_product(W4Args p, const int32_t *__restrict__ offsets,
-                                                     int E) {
+                                                     int E, int Z) {
     __shared__ W4Lds<UP, kW4Tokens, kW4Steps> lds;
     int e, r0, r1;
     if (!w4_active(offsets, E, blockIdx.y, e, r0, r1)) return;      // the whole workgroup
     constexpr int C = UP ? 16 : 32;
-    const int n = UP ? p.h : p.d, n0 = blockIdx.x * C * (4 / KS);
+    int col, z;
+    w4_place(Z, col, z);
+    const int n = UP ? p.h : p.d, n0 = col * C * (4 / KS);
+    if (n0 >= n) return;
     // waves past the last column multiply it again and store nothing
     const int m0 = min(n0 + w4_wave() / KS * C, n - C);
     const int64_t w0 = (int64_t)e * (UP ? 2 * p.h : p.d) + m0;
     const W4Tiles wt(p, w0, w0 + (UP ? p.h : 16));
-    for (int r = r0; r < r1; r += kW4Tokens)
+    for (int r = r0 + z * kW4Tokens; r < r1; r += Z * kW4Tokens)
         w4_rows<UP, kW4Tokens, kW4Steps, KS>(p, wt, n0, n, r, r1, lds);
 }
 
@@ -515,21 +528,24 @@ MOE_DEV void w4_rows_wide(const W4Args &p, const W4Tiles &wt, int n0, bool store
     }
 }
 
-// blockIdx.x: 64 columns of h (UP) or 128 of d, a quarter for each wave;
+// column group: 64 columns of h (UP) or 128 of d, a quarter for each wave;
 // blockIdx.y: rank of an expert with rows
 template <bool UP, int NT>
 __global__ __launch_bounds__(256, 2) void w4_product_wide(W4Args p,
                                                           const int32_t *__restrict__ offsets,
-                                                          int E) {
+                                                          int E, int Z) {
     __shared__ W4Wide<UP, NT> lds;
     int e, r0, r1;
     if (!w4_active(offsets, E, blockIdx.y, e, r0, r1)) return;      // the whole workgroup
-    const int n0 = (4 * blockIdx.x + w4_wave()) * (UP ? 16 : 32), n = UP ? p.h : p.d;
+    int col, z;
+    w4_place(Z, col, z);
+    const int n0 = (4 * col + w4_wave()) * (UP ? 16 : 32), n = UP ? p.h : p.d;
+    if (col * (UP ? 64 : 128) >= n) return;
     // a wave past the last column stages its share of the tokens and stores nothing
     const int m0 = min(n0, n - (UP ? 16 : 32));
     const int64_t w0 = (int64_t)e * (UP ? 2 * p.h : p.d) + m0;
     const W4Tiles wt(p, w0, w0 + (UP ? p.h : 16));
-    for (int r = r0; r < r1; r += 16 * NT) w4_rows_wide<UP, NT>(p, wt, m0, n0 < n, r, r1, lds);
+    for (int r = r0 + z * 16 * NT; r < r1; r += Z * 16 * NT) w4_rows_wide<UP, NT>(p, wt, m0, n0 < n, r, r1, lds);
 }
 
 // A handful of rows: out[t] for 32 columns from the token's own experts, gates
@@ -623,51 +639,66 @@ size_t w4_ws_bytes(int64_t R, int d, int h) {
     return 2 * round256((size_t)R * h * 2) + round256((size_t)R * d * 4);
 }
 
+// One of the two products over n columns. Which kernel, by rows an expert (R /
+// E) and workgroups (times of all launches of a call):
+//  - from twelve rows an expert, with a workgroup of 64 columns and 32 rows for
+//    every compute unit: the wide kernels. d = 2048, h = 1024, E = 128, k = 4, T =
+//    512 (16 rows) 150 us against 203; T = 256 (8 rows) 137 against 134. E = 16, k
+//    = 4, T = 64 (16 rows) 31 against 35, T = 32 28 against 25. d = 4096, h = 2048,
+//    E = 4, k = 2, T = 64 (128 workgroups) 79 against 46, T = 256 (512) 97 against
+//    128.
+//  - five workgroups a compute unit and up: two waves a reduction, not four, so
+//    that half as many workgroups look for their expert and join sums. d = 2048,
+//    h = 1024, E = 128, k = 4, T = 64 85.3 us against 88.0, E = 256, d = 1024, h =
+//    512, k = 8, T = 64 52 against 62; fewer leave compute units out: E = 8, k = 2,
+//    T = 16 16.4 against 15.1.
+// An expert's rows are shared out to as many workgroups as it takes for four a
+// compute unit (eight no better): d = 2048, h = 1024, E = 2, k = 2, T = 256 31 us
+// against 135 with one; d = 8192, h = 96, E = 4, k = 2, T = 128 32 against 84.
+template <bool UP>
+static void w4_product_launch(const moe_w4_desc &w, const W4Args &a, int n, hipStream_t s) {
+    const int64_t R = w.T * w.k;
+    const unsigned ny = (unsigned)(R < w.E ? R : w.E);
+    const int c = n / (UP ? 16 : 32), c2 = (c + 1) / 2, c4 = (c + 3) / 4;
+    auto split = [&](int cols, int rows) {
+        const int64_t each = (int64_t)rows * ny, parts = (R + each - 1) / each;
+        const int64_t z = 1024 / ((int64_t)cols * ny);
+        return (int)(z < 1 ? 1 : z < parts ? z : parts);
+    };
+    const int zw = split(c4, 16 * kW4WideTiles);
+    if (R >= 12 * (int64_t)w.E && (int64_t)c4 * ny * zw >= 256)
+        w4_product_wide<UP, kW4WideTiles><<<dim3(w4_grid(c4, zw), ny), 256, 0, s>>>(a, w.offsets, w.E, zw);
+    else if ((int64_t)c * ny >= 1280) {
+        const int z = split(c2, kW4Tokens);
+        w4_product<UP, 2><<<dim3(w4_grid(c2, z), ny), 256, 0, s>>>(a, w.offsets, w.E, z);
+    } else {
+        const int z = split(c, kW4Tokens);
+        w4_product<UP, 4><<<dim3(w4_grid(c, z), ny), 256, 0, s>>>(a, w.offsets, w.E, z);
+    }
+}
+
 moe_status w4_experts_launch(const moe_w4_desc *w, hipStream_t s) {
     const int64_t R = w->T * w->k;
     char *ws = reinterpret_cast<char *>(w->ws);
     const size_t half = round256((size_t)R * w->h * 2);
     uint16_t *hi = reinterpret_cast<uint16_t *>(ws), *lo = reinterpret_cast<uint16_t *>(ws + half);
     float *y = reinterpret_cast<float *>(ws + 2 * half);
-    const unsigned ny = (unsigned)(R < w->E ? R : w->E);
     const W4Args up = {reinterpret_cast<const uint16_t *>(w->x), nullptr, w->sorted_token, w->w1q,
                        w->w1_scale, hi, lo, nullptr, w->d, w->h, w->d};
     const W4Args down = {hi, lo, nullptr, w->w2q, w->w2_scale, nullptr, nullptr, y, w->h, w->h, w->d};
-    const int nu = w->h / 16, nd = w->d / 32;
-    // Which kernels, by rows an expert (R / E) and workgroups (all three
-    // launches, d = 2048, h = 1024; E = 128, k = 4 unless said):
-    //  - a handful of rows: the down product by token, T = 8 (R = E / 4) 27.1 us
-    //    against 31.4; where tokens share experts it reads them again, E = 8, k =
-    //    2, T = 16 (R = 4 E) 18.7 us against 16.4; T = 16 (4,096 workgroups) 48.8
-    //    against 47.7;
-    //  - eight rows an expert and up, and a workgroup of 64 columns for every
-    //    compute unit: the wide kernels, T = 256 134 us against 146; T = 128 129
-    //    against 107; E = 8, k = 2, T = 128 (128 workgroups) 43.3 against 41.0.
-    //  - five workgroups a compute unit and up: two waves a reduction, not four,
-    //    so that half as many workgroups look for their expert and join sums:
-    //    T = 16 45.0 us against 47.7, T = 64 85.3 against 88.0, T = 128 101
-    //    against 104; fewer leave compute units out: E = 8, k = 2, T = 16 17.0
-    //    against 15.4.
-    auto wide = [&](int n) { return R >= 8 * (int64_t)w->E && (int64_t)((n + 3) / 4) * ny >= 256; };
-    auto pairs = [&](int n) { return (int64_t)n * ny >= 1280; };
-    if (wide(nu))
-        w4_product_wide<true, kW4WideTiles><<<dim3((nu + 3) / 4, ny), 256, 0, s>>>(up, w->offsets, w->E);
-    else if (pairs(nu))
-        w4_product<true, 2><<<dim3((nu + 1) / 2, ny), 256, 0, s>>>(up, w->offsets, w->E);
-    else
-        w4_product<true, 4><<<dim3(nu, ny), 256, 0, s>>>(up, w->offsets, w->E);
+    const int nd = w->d / 32;
+    w4_product_launch<true>(*w, up, w->h, s);
+    // A handful of rows: the down product by token (all launches, d = 2048, h =
+    // 1024): E = 128, k = 4, T = 8 (R = E / 4) 25.7 us against 28.8; T = 16 (4,096
+    // workgroups) 44.9 against 45.0. Where tokens share experts it reads them
+    // again: E = 8, k = 2, T = 16 (R = 4 E) 18.8 us against 15.2.
     if (R <= 2 * (int64_t)w->E && nd * R <= 2048) {
         w4_down_tokens<<<dim3(nd, (unsigned)w->T), 512, 0, s>>>(
             down, w->offsets, w->E, w->topk_gate, w->token_pos, w->k,
             reinterpret_cast<uint16_t *>(w->out));
         return launch_status();
     }
-    if (wide(nd))
-        w4_product_wide<false, kW4WideTiles><<<dim3((nd + 3) / 4, ny), 256, 0, s>>>(down, w->offsets, w->E);
-    else if (pairs(nd))
-        w4_product<false, 2><<<dim3((nd + 1) / 2, ny), 256, 0, s>>>(down, w->offsets, w->E);
-    else
-        w4_product<false, 4><<<dim3(nd, ny), 256, 0, s>>>(down, w->offsets, w->E);
+    w4_product_launch<false>(*w, down, w->d, s);
     const int cb = (w->d + 1023) / 1024;
     const int64_t piece = kMaxBlocks / cb;
     for (int64_t t = 0; t < w->T; t += piece) {

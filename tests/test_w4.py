@@ -135,7 +135,8 @@ def _check(out, x, r, w1, w2):
 @pytest.mark.parametrize("T,d,h,E,k", [
     (1, 32, 32, 1, 1), (1, 2048, 1024, 8, 4), (2, 96, 160, 5, 3), (7, 416, 352, 16, 8), (64, 256, 128, 32, 4),
     (33, 160, 96, 2, 1), (50, 544, 64, 3, 2), (300, 64, 96, 4, 2), (1, 4128, 32, 4, 2), (3, 64, 2080, 256, 8),
-    (256, 416, 224, 64, 2), (160, 448, 2048, 16, 1), (90, 672, 352, 64, 2)])
+    (256, 416, 224, 64, 2), (160, 448, 2048, 16, 1), (90, 672, 352, 64, 2),
+    (400, 448, 2048, 16, 1), (200, 4128, 160, 4, 4), (130, 2048, 96, 2, 2)])
 def test_experts(T, d, h, E, k):
     """From one row per expert to many tiles of them; widths whose last step is partial."""
     w1q, s1, w2q, s2, w1, w2 = _weights(E, d, h, T + d)
@@ -162,6 +163,21 @@ def test_one_expert_takes_all(T):
     out = moe.moe_w4_experts(x, r, w1q, s1, w2q, s2, out=buf[:T], ws=ws[:wsb])
     _check(out, x, r, w1, w2)
     assert (buf[T] == 9).all() and (ws[wsb:] == 0xAB).all()
+
+
+@gpu
+@pytest.mark.parametrize("k,busy", [(1, (2,)), (2, (0, 3))])
+def test_rows_shared_out_unevenly(k, busy):
+    """Hundreds of rows for some of the experts, none for the others: more
+    tiles of rows than workgroups that share them, and workgroups without any."""
+    T, d, h, E = 300, 96, 2048, 4
+    w1q, s1, w2q, s2, w1, w2 = _weights(E, d, h, T)
+    lg = synth.normal((T, E), 8, 0, 1.0)
+    lg[:, list(busy)] += 50
+    x = dev(synth.normal((T, d), 8, 1, 1.0), torch.bfloat16)
+    r = moe.moe_route(dev(lg, torch.float32), k)
+    assert sorted(set(to_np(r["topk_idx"]).ravel())) == list(busy)
+    _check(moe.moe_w4_experts(x, r, w1q, s1, w2q, s2), x, r, w1, w2)
 
 
 @gpu
