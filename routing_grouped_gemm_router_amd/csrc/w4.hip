@@ -10,30 +10,33 @@
 //   a_r, b_r = W1[e] x[token of row r]   h_r = silu(a_r) b_r   y_r = W2[e] h_r
 //   out[t] = sum_j g[t, j] y[token_pos[t, j]]
 //
-// A wave multiplies 16 rows of weights by up to 16 tokens with
+// A wave multiplies 16 rows of weights by up to 16 columns with
 // v_mfma_f32_16x16x32_bf16: the four-bit elements are widened to bf16, which
 // holds them exactly with their scale (v_cvt_scalef32_pk_bf16_fp4), one
 // scale block of 32 per lane. Which 8 of the 32 reduction indices a lane
 // brings is free as long as both operands agree: here lane l takes block
 // 4 s + l / 16 of row l % 16 in step s, 16 contiguous bytes, in four MFMAs,
 // so weights are kept in their plain layout. h is handed on as the sum of two
-// bf16 (16 significant bits, two products) and y in fp32: the only rounding to
-// bf16 is out's.
+// bf16 (16 significant bits, each in columns of its own) and y in fp32: the
+// only rounding to bf16 is out's.
 //
 // Bound by the weights' bytes with tokens for most experts, by the latency of
 // a launch and a chain of loads with few. d = 2048, h = 1024, E = 128, k = 4: 64
-// tokens (111 experts, 371 MB) 53 + 34 + 5 us, 4.0 TB/s of the 6.1 that a plain
-// read of memory reaches; one token (4 experts, 13 MB) 6.4 + 5.5 us. What it took:
-// no branch around a load (106 -> 77 us for gate and up), memory read by runs of
-// lanes and put into the product's order through LDS (77 -> 58 us: the
-// first-level cache looked up 39 million lines for the 4 million there are),
-// tokens no more than 8 at a time (down 47 -> 31 us; registers and LDS for 16
-// leave a third of the waves out). What is left is the loads themselves: in the
-// same order, without the products, they take 48 and 30 us, 5 of them for the
-// scale bytes. Loads past the last-level cache (61 us), whole rows a wave (56
-// us), fewer and longer workgroups (55 to 62 us), the next step's lines touched
-// ahead (60 us) or more registers for loads (59 us) were slower than gate and
-// up's 53 us.
+// tokens (111 experts, 371 MB) 47 + 28 + 5 us, 4.7 TB/s of the 6.1 that a plain
+// read of memory reaches; one token (4 experts, 13 MB) 5.9 + 5.5 us. What it took
+// (gate and up, down at 64 tokens): no branch around a load (106 -> 77, ..),
+// memory read by runs of lanes and put into the product's order through LDS
+// (77 -> 58: the first-level cache looked up 39 million lines for the 4 million
+// there are), tokens no more than 8 at a time (.., 47 -> 34: registers and LDS
+// for 16 leave a third of the waves out), the scale bytes of two steps in one
+// load, weights asked for before the rows' tokens are known (53 -> 51, 34 ->
+// 32), half as many workgroups (51 -> 49, 32 -> 31), runs of whole cache lines
+// (49 -> 47), h's halves side by side in one product and LDS rows an odd number
+// of pieces apart, whose places are constants and not registers (.., 31 -> 28).
+// Slower were loads past the last-level cache, whole rows a wave, the next
+// step's weights in flight during a step (59 and 33 us one step at a time, no
+// gain and spilled registers two at a time), twice the registers for loads,
+// more waves with fewer loads each (55 and 37 us).
 #include "act8.h"
 
 namespace moe {
@@ -152,20 +155,20 @@ template <> struct W4Bytes<4> { typedef uint32_t type; };
 
 // What a wave keeps in LDS: both weight tiles of the U steps that were loaded
 // together (16 rows of 4 U blocks, 16 bytes each) with their scales, and of one
-// step, per half of h, TOK tokens of 4 blocks in 16-byte pieces.
+// step TOK tokens (their upper halves, then their lower ones, of h) of 4 blocks
+// in 16-byte pieces.
 template <bool UP, int TOK, int U>
 struct W4Stage {
-    u32x4 w[2][64 * U];
+    u32x4 w[2][16 * (4 * U + 1)];
     uint8_t sc[2][64 * U];
-    u32x4 x[UP ? 1 : 2][TOK * 16];
+    u32x4 x[(UP ? 1 : 2) * TOK * 17];
 };
 
-// Pieces are kept at the place of their index with some of its bits flipped
-// by the row's, so that the 16 lanes that read one piece of 16 rows each meet
-// different banks.
+// Rows are one piece apart from their length, an odd number, so that the 16
+// lanes that read one piece of 16 rows each meet different banks.
 template <int U>
-MOE_DEV int w4_wslot(int row, int blk) { return 4 * U * row + (blk ^ (row / (4 / U))); }
-MOE_DEV int w4_xslot(int row, int piece) { return 16 * row + (piece ^ (4 * (row & 3) + (row >> 2))); }
+MOE_DEV int w4_wslot(int row, int blk) { return (4 * U + 1) * row + blk; }
+MOE_DEV int w4_xslot(int row, int piece) { return 17 * row + piece; }
 
 // The lanes of a wave see each other's LDS writes in program order; this
 // keeps the compiler to that order.
@@ -206,17 +209,21 @@ struct W4Loaded {
 };
 
 // Their products: the tokens' loads (16 lanes 256 bytes of token 4 j + lane /
-// 16, at x[.][j], for j < quads, which is uniform), then through LDS to the
+// 16, at x[j] and, of h, its lower half lo elements on, for j < quads; both are
+// uniform), then through LDS to the
 // matrix units, which want row lane % 16 (a load in the product's own order has
 // a lane per row and costs the first-level cache many times the accesses). TOK
-// tokens fill the product's 16 columns over and over.
+// tokens fill the product's 16 columns over and over; of h, the upper halves
+// columns 0 to 7 and the lower ones columns 8 to 15, whose sum is the result.
 template <bool UP, int TOK, int U, int SU, bool TAIL>
 MOE_DEV void w4_steps(int s, int nblk, const W4Loaded<U, TAIL> &l, int quads,
-                      const uint16_t *const (&x)[2][(TOK + 3) / 4], W4Stage<UP, TOK, SU> &st,
+                      const uint16_t *const (&x)[(TOK + 3) / 4], int64_t lo, W4Stage<UP, TOK, SU> &st,
                       f32x4 (&acc)[2]) {
     constexpr int P = UP ? 1 : 2, J = (TOK + 3) / 4;    // h comes as two halves
     typedef typename W4Bytes<U>::type Sc;
+    static_assert(UP || TOK <= 8);
     const int lane = threadIdx.x & 63, g = lane >> 4, i = lane & 15;
+    const int column = (i & (TOK - 1)) + (UP ? 0 : i / 8 * TOK);
     const u32x4 zero = {0, 0, 0, 0};
     u32x4 xr[U][P][J];
 #pragma unroll
@@ -227,7 +234,7 @@ MOE_DEV void w4_steps(int s, int nblk, const W4Loaded<U, TAIL> &l, int quads,
 #pragma unroll
                 for (int u = 0; u < U; u++)
                     xr[u][p][j] = !TAIL || 4 * (s + u) + (i >> 2) < nblk
-                        ? *reinterpret_cast<const u32x4 *>(x[p][j] + 128 * (s + u) + 8 * i) : zero;
+                        ? *reinterpret_cast<const u32x4 *>(x[j] + p * lo + 128 * (s + u) + 8 * i) : zero;
         }
     w4_lds_order();                               // the steps before have been read
 #pragma unroll
@@ -245,7 +252,7 @@ MOE_DEV void w4_steps(int s, int nblk, const W4Loaded<U, TAIL> &l, int quads,
             if (j == 0 || j < quads) {
 #pragma unroll
                 for (int p = 0; p < P; p++)
-                    if (TOK >= 4 || g == 0) st.x[p][w4_xslot(4 * j + g, i)] = xr[u][p][j];
+                    if (TOK >= 4 || g == 0) st.x[w4_xslot(p * TOK + 4 * j + g, i)] = xr[u][p][j];
             }
         w4_lds_order();
         u32x4 a[2];
@@ -258,12 +265,9 @@ MOE_DEV void w4_steps(int s, int nblk, const W4Loaded<U, TAIL> &l, int quads,
 #pragma unroll
         for (int m = 0; m < 4; m++) {
             const bf16x8 a0 = w4_widen(a[0][m], f[0]), a1 = w4_widen(a[1][m], f[1]);
-#pragma unroll
-            for (int p = 0; p < P; p++) {
-                const bf16x8 b = __builtin_bit_cast(bf16x8, st.x[p][w4_xslot(i & (TOK - 1), 4 * g + m)]);
-                acc[0] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(a0, b, acc[0], 0, 0, 0);
-                acc[1] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(a1, b, acc[1], 0, 0, 0);
-            }
+            const bf16x8 b = __builtin_bit_cast(bf16x8, st.x[w4_xslot(column, 4 * g + m)]);
+            acc[0] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(a0, b, acc[0], 0, 0, 0);
+            acc[1] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(a1, b, acc[1], 0, 0, 0);
         }
     }
 }
@@ -272,8 +276,8 @@ MOE_DEV void w4_steps(int s, int nblk, const W4Loaded<U, TAIL> &l, int quads,
 // weights have been asked for.
 template <bool UP, int TOK, int U, class Address>
 MOE_DEV void w4_reduce(int s, int end, int nblk, const W4Tiles &wt, int quads, Address address,
-                       W4Stage<UP, TOK, U> &st, f32x4 (&acc)[2]) {
-    const uint16_t *x[2][(TOK + 3) / 4];
+                       int64_t lo, W4Stage<UP, TOK, U> &st, f32x4 (&acc)[2]) {
+    const uint16_t *x[(TOK + 3) / 4];
     const int whole = min(end, nblk / 4);
     W4Loaded<U, false> l;
     const bool any = s + U <= whole;
@@ -281,7 +285,7 @@ MOE_DEV void w4_reduce(int s, int end, int nblk, const W4Tiles &wt, int quads, A
     address(x);
     if (any)
         for (;;) {
-            w4_steps<UP, TOK>(s, nblk, l, quads, x, st, acc);
+            w4_steps<UP, TOK>(s, nblk, l, quads, x, lo, st, acc);
             s += U;
             if (s + U > whole) break;
             l.load(s, nblk, wt);
@@ -289,7 +293,7 @@ MOE_DEV void w4_reduce(int s, int end, int nblk, const W4Tiles &wt, int quads, A
     for (; s < end; s++) {
         W4Loaded<1, true> t;
         t.load(s, nblk, wt);
-        w4_steps<UP, TOK>(s, nblk, t, quads, x, st, acc);
+        w4_steps<UP, TOK>(s, nblk, t, quads, x, lo, st, acc);
     }
 }
 
@@ -331,19 +335,17 @@ MOE_DEV void w4_rows(const W4Args &p, const W4Tiles &wt, int n0, int n, int r, i
                      W4Lds<UP, TOK, U> &lds) {
     const int lane = threadIdx.x & 63, wave = w4_wave(), g = lane >> 4, i = lane & 15;
     const int nblk = p.K / 32;
-    auto address = [&](const uint16_t *(&x)[2][TOK / 4]) {
+    auto address = [&](const uint16_t *(&x)[TOK / 4]) {
 #pragma unroll
         for (int j = 0; j < TOK / 4; j++) {
             const int row = min(r + 4 * j + g, r1 - 1);
-            const int64_t src = (UP ? p.sorted_token[row] : row) * (int64_t)p.K;
-            x[0][j] = p.x + src;
-            x[1][j] = UP ? nullptr : p.lo + src;
+            x[j] = p.x + (UP ? p.sorted_token[row] : row) * (int64_t)p.K;
         }
     };
     f32x4 acc[2] = {f32x4{0.f, 0.f, 0.f, 0.f}, f32x4{0.f, 0.f, 0.f, 0.f}};
     const int steps = (nblk + 3) / 4, part = (steps + KS - 1) / KS, s = (wave % KS) * part;
     w4_reduce<UP, TOK, U>(s, min(s + part, steps), nblk, wt, (r1 - r + 3) / 4, address,
-                          lds.stage[wave], acc);
+                          UP ? 0 : p.lo - p.x, lds.stage[wave], acc);
     // lane: column i (token i while i < TOK), weight rows 4 g .. 4 g + 3
     __syncthreads();                              // the stages have been read
 #pragma unroll
@@ -357,7 +359,10 @@ MOE_DEV void w4_rows(const W4Args &p, const W4Tiles &wt, int n0, int n, int r, i
         for (int z = 0; z < 2; z++) {
             v[z] = 0;
 #pragma unroll
-            for (int q = 0; q < KS; q++) v[z] += lds.red[t * KS + q][z][tid];
+            for (int q = 0; q < KS; q++) {
+                v[z] += lds.red[t * KS + q][z][tid];
+                if (!UP) v[z] += lds.red[t * KS + q][z][(tid + 128) & 255];
+            }
         }
         const int n1 = n0 + t * (UP ? 16 : 32);
         if (tok < TOK && r + tok < r1 && n1 < n) w4_store<UP, 1>(p, r + tok, n1 + (tid & 15), &v[0], &v[1]);
@@ -404,7 +409,7 @@ __global__ __launch_bounds__(256, 4) void w4_product(W4Args p, const int32_t *__
 template <bool UP, int NT>
 struct W4Wide {
     u32x4 x[UP ? 1 : 2][NT][16 * 64];             // 16 tokens of 64 pieces of 16 bytes
-    u32x4 w[4][2][64];                            // a step of each wave
+    u32x4 w[4][2][80];                            // a step of each wave
     uint8_t sc[4][2][64];
 };
 
@@ -552,7 +557,7 @@ __global__ __launch_bounds__(256, 2) void w4_product_wide(W4Args p,
 // and sum included, in one launch (no y, no combine; an expert that tokens
 // share is read once for each). Wave: slot wave % 4 and on, half wave / 4 of
 // the reduction.
-__global__ __launch_bounds__(512) void w4_down_tokens(W4Args p, const int32_t *__restrict__ offsets,
+__global__ __launch_bounds__(512, 4) void w4_down_tokens(W4Args p, const int32_t *__restrict__ offsets,
                                                       int E, const float *__restrict__ gate,
                                                       const int32_t *__restrict__ token_pos, int k,
                                                       uint16_t *__restrict__ out) {
@@ -577,10 +582,14 @@ __global__ __launch_bounds__(512) void w4_down_tokens(W4Args p, const int32_t *_
             for (int q = 0; q < 4; q++) e += __popcll(__ballot(ends[q] <= row));
             const W4Tiles wt(p, (int64_t)e * p.d + n0, (int64_t)e * p.d + n0 + 16);
             const int64_t src = (int64_t)row * p.K;
-            auto address = [&](const uint16_t *(&x)[2][1]) { x[0][0] = p.x + src; x[1][0] = p.lo + src; };
-            w4_reduce<false, 1, U>(begin, end, nblk, wt, 1, address, stage[wave], acc);
+            auto address = [&](const uint16_t *(&x)[1]) { x[0] = p.x + src; };
+            w4_reduce<false, 1, U>(begin, end, nblk, wt, 1, address, p.lo - p.x, stage[wave], acc);
         }
-        if (i == 0) {                             // column 0: the token
+#pragma unroll
+        for (int z = 0; z < 2; z++)               // columns 0 and 8: the token's halves
+#pragma unroll
+            for (int q = 0; q < 4; q++) acc[z][q] += dpp_move<kDppRowRor8>(acc[z][q]);
+        if (i == 0) {
 #pragma unroll
             for (int z = 0; z < 2; z++)
                 *reinterpret_cast<f32x4 *>(&red[wave >> 2][j][16 * z + 4 * g]) = acc[z];
