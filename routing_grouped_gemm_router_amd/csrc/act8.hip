@@ -14,16 +14,17 @@
 // outputs once, at a large copy's rate (4.7 to 5.2 TB/s here) or above it.
 // What is read or written once and not soon again goes past the last-level
 // cache (load_once, store_once): store 77 -> 67 us for 65536 rows of 2048 bf16
-// (407 MB, 6.1 TB/s), combine 125 -> 100 us. The combine's checkpoint and dy_perm
-// are stored in the ordinary way: as store_once the combine took 111 us, and
-// dy_perm's made the GEMM that reads it next slower by more than the kernel
-// won.
+// (407 MB, 6.1 TB/s), combine with its checkpoint 125 -> 91 us. dy_perm is
+// stored in the ordinary way: the GEMM that reads it comes next, and a layer's
+// step gains nothing by the other (3.85 ms both ways), though combine and
+// backward in turn would take 159 us instead of 171.
 #include "act8.h"
 
 namespace moe {
 
-// vectors of each of a token's k rows in flight per lane (combine: 1 99 us, 2 and
-// 4 102 us; backward: 2 80 us, 4 81 us, one at a time 111 us)
+// vectors of each of a token's k rows in flight per thread (T = 16384, d = 2048,
+// k = 4: combine 1 91 us, 2 95 us; backward 1 and 2 80 us, 4 83 us; T = 512, d =
+// 4096, k = 8 backward 1 14.1 us, 2 12.3)
 constexpr int kCombineU = 1, kCombineBwdU = 2;
 
 // store: q, scale = checkpoint of in, a vector a thread (65536 x 2048 bf16: 67 us).
@@ -90,19 +91,52 @@ __global__ __launch_bounds__(256) void act8_swiglu_vecs(const typename Codes<BF1
     store_once(hp + v, R::pack(y));
 }
 
+// The combine kernels give a token G threads: less than a wave for narrow
+// rows, whole workgroups for wide rows of few tokens.
+template <int G>
+MOE_DEV int64_t token_of_group() {
+    return G >= 256 ? (int64_t)blockIdx.x : (int64_t)blockIdx.x * (256 / G) + threadIdx.x / G;
+}
+
+// Each of N values summed over the G threads of a token, in a fixed order; all
+// of them get the sums.
+template <int G, int N>
+MOE_DEV void group_sums(float (&v)[N]) {
+#pragma unroll
+    for (int j = 0; j < N; j++) {
+        if constexpr (G >= 64) v[j] = wave_sum(v[j]);
+        else
+#pragma unroll
+            for (int o = G / 2; o > 0; o >>= 1) v[j] += __shfl_xor(v[j], o);
+    }
+    if constexpr (G > 64) {
+        __shared__ float part[G / 64][N];
+        if (threadIdx.x % 64 == 0) {
+#pragma unroll
+            for (int j = 0; j < N; j++) part[threadIdx.x / 64][j] = v[j];
+        }
+        __syncthreads();
+#pragma unroll
+        for (int j = 0; j < N; j++) {
+            v[j] = part[0][j];
+            for (int w = 1; w < G / 64; w++) v[j] += part[w][j];
+        }
+    }
+}
+
 // combine that keeps the experts' rows: out[t] = sum_j g[t,j] y[token_pos[t,j]]
 // (fp32 sum, ascending j) and the checkpoint of every row it reads, from one
-// read: 474 MB at T = 16384, d = 2048, k = 4 bf16 in 92 to 114 us (after another
-// kernel's dirty lines), where the combine alone takes 61 and a store of its
-// own 67. One wave per token.
-template <bool BF16, int KMAX, int U>
-__global__ __launch_bounds__(256) void combine_act8_rows(
+// read: 474 MB at T = 16384, d = 2048, k = 4 bf16 in 91 us after its backward's
+// dirty lines, 80 without (5.2 to 5.9 TB/s), where the combine alone takes 61 and
+// a store of its own 67.
+template <bool BF16, int KMAX, int U, int G>
+__global__ __launch_bounds__(G > 256 ? G : 256) void combine_act8_rows(
     const uint4 *__restrict__ y, const float *__restrict__ gate,
     const int32_t *__restrict__ token_pos, int64_t T, int nv, int k, uint4 *__restrict__ out,
     typename Codes<BF16>::type *__restrict__ y8, uint8_t *__restrict__ y8_scale) {
     typedef Row16<BF16> R;
-    const int lane = threadIdx.x & 63;
-    const int64_t t = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6);
+    const int lane = threadIdx.x % G;
+    const int64_t t = token_of_group<G>();
     if (t >= T) return;
     int32_t pos[KMAX];
     float g[KMAX];
@@ -111,16 +145,16 @@ __global__ __launch_bounds__(256) void combine_act8_rows(
         pos[j] = j < k ? token_pos[t * k + j] : -1;
         g[j] = j < k ? gate[t * k + j] : 0.f;
     }
-    for (int c0 = lane; c0 < nv; c0 += 64 * U) {
+    for (int c0 = lane; c0 < nv; c0 += G * U) {
         uint4 w[U][KMAX];
 #pragma unroll
         for (int u = 0; u < U; u++)
 #pragma unroll
             for (int j = 0; j < KMAX; j++)
-                if (c0 + 64 * u < nv && pos[j] >= 0) w[u][j] = load_once(y + (int64_t)pos[j] * nv + c0 + 64 * u);
+                if (c0 + G * u < nv && pos[j] >= 0) w[u][j] = load_once(y + (int64_t)pos[j] * nv + c0 + G * u);
 #pragma unroll
         for (int u = 0; u < U; u++) {
-            const int c = c0 + 64 * u;
+            const int c = c0 + G * u;
             if (c >= nv) break;
             float acc[R::N];
 #pragma unroll
@@ -134,7 +168,7 @@ __global__ __launch_bounds__(256) void combine_act8_rows(
                 R::unpack(w[u][j], f);
                 typename Codes<BF16>::type q;
                 act8_encode(f, sb, q);
-                y8[v] = q;
+                store_once(y8 + v, q);
                 if (c % R::LPB == 0) y8_scale[v / R::LPB] = (uint8_t)sb;
 #pragma unroll
                 for (int i = 0; i < R::N; i++) acc[i] = fmaf(g[j], f[i], acc[i]);
@@ -150,19 +184,19 @@ __global__ __launch_bounds__(256) void combine_act8_rows(
 //   dlogits[t, e_j] = g_j sum_i g_i (dg_j - dg_i), 0 for unselected experts
 // (the gates sum to one; this form has no cancellation between large terms).
 // ROWS = false (the MXFP8 backward, whose quantiser forms dy_perm itself):
-// row_gate[p_j] = g_j instead of dy_perm's rows. One wave per token. 484 MB at T =
-// 16384, d = 2048, k = 4 bf16 in 81 us (6.0 TB/s); from bf16 rows it takes 100.
-template <bool BF16, int KMAX, int U, bool ROWS>
-__global__ __launch_bounds__(256) void combine_bwd_act8_rows(
+// row_gate[p_j] = g_j instead of dy_perm's rows. 484 MB at T = 16384, d = 2048, k
+// = 4 bf16 in 79 us (6.1 TB/s); from bf16 rows it takes 100.
+template <bool BF16, int KMAX, int U, bool ROWS, int G>
+__global__ __launch_bounds__(G > 256 ? G : 256) void combine_bwd_act8_rows(
     const uint4 *__restrict__ dout, const typename Codes<BF16>::type *__restrict__ y8,
     const uint8_t *__restrict__ y8_scale, const float *__restrict__ gate,
     const int32_t *__restrict__ topk_idx, const int32_t *__restrict__ token_pos, int64_t T, int nv,
     int k, int E, uint4 *__restrict__ dy, float *__restrict__ row_gate,
     float *__restrict__ dlogits, float *__restrict__ dgate) {
     typedef Row16<BF16> R;
-    const int lane = threadIdx.x & 63;
-    const int64_t t = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6);
-    if (t >= T) return;
+    const int lane = threadIdx.x % G;
+    const int64_t t = token_of_group<G>();
+    if (t >= T) return;                           // whole groups
     int32_t pos[KMAX], ex[KMAX];
     float g[KMAX], dot[KMAX];
 #pragma unroll
@@ -172,13 +206,13 @@ __global__ __launch_bounds__(256) void combine_bwd_act8_rows(
         g[j] = j < k ? gate[t * k + j] : 0.f;
         dot[j] = 0.f;
     }
-    for (int c0 = lane; c0 < nv; c0 += 64 * U) {
+    for (int c0 = lane; c0 < nv; c0 += G * U) {
         uint4 wo[U];
         typename Codes<BF16>::type q[U][KMAX];
         uint8_t sc[U][KMAX];
 #pragma unroll
         for (int u = 0; u < U; u++) {
-            const int c = c0 + 64 * u;
+            const int c = c0 + G * u;
             if (c >= nv) break;
             wo[u] = load_once(dout + t * nv + c);
 #pragma unroll
@@ -191,7 +225,7 @@ __global__ __launch_bounds__(256) void combine_bwd_act8_rows(
         }
 #pragma unroll
         for (int u = 0; u < U; u++) {
-            const int c = c0 + 64 * u;
+            const int c = c0 + G * u;
             if (c >= nv) break;
             float fo[R::N];
             R::unpack(wo[u], fo);
@@ -209,11 +243,10 @@ __global__ __launch_bounds__(256) void combine_bwd_act8_rows(
             }
         }
     }
+    group_sums<G>(dot);
 #pragma unroll
-    for (int j = 0; j < KMAX; j++) {
-        dot[j] = wave_sum(dot[j]);
+    for (int j = 0; j < KMAX; j++)
         if (pos[j] < 0) dot[j] = 0.f;   // dropped row: its gate had no effect
-    }
     float rg[KMAX];
 #pragma unroll
     for (int j = 0; j < KMAX; j++) {
@@ -222,7 +255,7 @@ __global__ __launch_bounds__(256) void combine_bwd_act8_rows(
         for (int i = 0; i < KMAX; i++) s = fmaf(g[i], dot[j] - dot[i], s);
         rg[j] = g[j] * s;
     }
-    for (int e = lane; e < E; e += 64) {
+    for (int e = lane; e < E; e += G) {
         float v = 0.f;
 #pragma unroll
         for (int j = 0; j < KMAX; j++)
@@ -295,25 +328,43 @@ moe_status act8_swiglu_launch(const uint8_t *q, const uint8_t *scale, moe_dtype 
     return launch_status();
 }
 
-constexpr int64_t kTokensALaunch = kMaxBlocks * 4;    // four tokens a workgroup
+// Threads of a token, nv vectors of 16 bytes a row (bf16, T = 32768, k = 8 unless
+// said):
+//  - 16 for rows of up to 16 vectors (d = 64: forward 21 us against 58 with a
+//    wave, backward 27 against 70), and up to 32 where the tokens fill the chip (d
+//    = 256: 47 against 71, 45 against 75; T = 4096, k = 4: 5.8 against 5.2);
+//  - forward: a workgroup of 256 from 128 vectors (d = 2048: 306 against 354; T =
+//    512: 7.4 against 17; d = 512: 97 against 86), of 1024 from 1024 (d = 8192: 1407
+//    against 1498; T = 512: 24 against 31; d = 2048: 445 against 360);
+//  - backward, whose sums cross the waves: a workgroup of 256 from 256 vectors if
+//    each thread has four or more (d = 4096: 706 against 748; d = 2048, k = 1: 60
+//    against 55), or from 128 where the waves of the tokens alone do not fill the
+//    chip (T = 512, d = 2048: 8.3 against 10.9; d = 16384: 40 against 63).
+static int combine_group(int nv, int64_t T, int k, bool backward) {
+    if (nv <= 16 || (nv <= 32 && T >= 16384)) return 16;
+    if (!backward) return nv >= 1024 ? 1024 : nv >= 128 ? 256 : 64;
+    return (nv >= 256 && nv * k >= 1024) || (nv >= 128 && T <= 2048) ? 256 : 64;
+}
 
-#define ACT8_KSWITCH(k, F) \
-    ((k) <= 1 ? F(1) : (k) <= 2 ? F(2) : (k) <= 4 ? F(4) : F(8))
+#define ACT8_KSWITCH(G, k, F) \
+    ((k) <= 1 ? F(1, G) : (k) <= 2 ? F(2, G) : (k) <= 4 ? F(4, G) : F(8, G))
 
 template <bool BF16>
 static void combine_act8_run(const void *y, const float *gate, const int32_t *token_pos, int64_t T,
                              int d, int k, void *out, uint8_t *y8, uint8_t *y8_scale,
                              hipStream_t s) {
     typedef typename Codes<BF16>::type C;
-    const int nv = d / Row16<BF16>::N;
-    for (int64_t t = 0; t < T; t += kTokensALaunch) {
-        const int64_t n = T - t < kTokensALaunch ? T - t : kTokensALaunch;
-        const unsigned nb = (unsigned)((n + 3) / 4);
-#define L(K)                                                                                     \
-    (combine_act8_rows<BF16, K, kCombineU><<<nb, 256, 0, s>>>(                                   \
+    const int nv = d / Row16<BF16>::N, group = combine_group(nv, T, k, false);
+    const int tokens = group < 256 ? 256 / group : 1, threads = group < 256 ? 256 : group;
+    for (int64_t t = 0; t < T; t += kMaxBlocks * tokens) {
+        const int64_t n = T - t < kMaxBlocks * tokens ? T - t : kMaxBlocks * tokens;
+        const unsigned nb = (unsigned)((n + tokens - 1) / tokens);
+#define L(K, G)                                                                                  \
+    (combine_act8_rows<BF16, K, kCombineU, G><<<nb, threads, 0, s>>>(                            \
          reinterpret_cast<const uint4 *>(y), gate + t * k, token_pos + t * k, n, nv, k,          \
          reinterpret_cast<uint4 *>(out) + t * nv, reinterpret_cast<C *>(y8), y8_scale), 0)
-        ACT8_KSWITCH(k, L);
+        group == 16 ? ACT8_KSWITCH(16, k, L) : group == 64 ? ACT8_KSWITCH(64, k, L)
+            : group == 256 ? ACT8_KSWITCH(256, k, L) : ACT8_KSWITCH(1024, k, L);
 #undef L
     }
 }
@@ -332,16 +383,18 @@ static void combine_bwd_act8_run(const void *dout, const uint8_t *y8, const uint
                                  const int32_t *token_pos, int64_t T, int d, int k, int E, void *dy,
                                  float *row_gate, float *dlogits, float *dgate, hipStream_t s) {
     typedef typename Codes<BF16>::type C;
-    const int nv = d / Row16<BF16>::N;
-    for (int64_t t = 0; t < T; t += kTokensALaunch) {
-        const int64_t n = T - t < kTokensALaunch ? T - t : kTokensALaunch;
-        const unsigned nb = (unsigned)((n + 3) / 4);
-#define L(K)                                                                                      \
-    (combine_bwd_act8_rows<BF16, K, kCombineBwdU, ROWS><<<nb, 256, 0, s>>>(                       \
+    const int nv = d / Row16<BF16>::N, group = combine_group(nv, T, k, true);
+    const int tokens = group < 256 ? 256 / group : 1, threads = group < 256 ? 256 : group;
+    for (int64_t t = 0; t < T; t += kMaxBlocks * tokens) {
+        const int64_t n = T - t < kMaxBlocks * tokens ? T - t : kMaxBlocks * tokens;
+        const unsigned nb = (unsigned)((n + tokens - 1) / tokens);
+#define L(K, G)                                                                                   \
+    (combine_bwd_act8_rows<BF16, K, kCombineBwdU, ROWS, G><<<nb, threads, 0, s>>>(                \
          reinterpret_cast<const uint4 *>(dout) + t * nv, reinterpret_cast<const C *>(y8),         \
          y8_scale, gate + t * k, topk_idx + t * k, token_pos + t * k, n, nv, k, E,                \
          reinterpret_cast<uint4 *>(dy), row_gate, dlogits + t * E, dgate ? dgate + t * k : nullptr), 0)
-        ACT8_KSWITCH(k, L);
+        group == 16 ? ACT8_KSWITCH(16, k, L) : group == 64 ? ACT8_KSWITCH(64, k, L)
+            : ACT8_KSWITCH(256, k, L);
 #undef L
     }
 }

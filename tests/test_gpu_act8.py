@@ -162,7 +162,8 @@ def _routing(T, E, k, seed, drop=0.0, spare=0):
 
 
 COMBINE = [(1, 32, 2, 1, 0, 0), (5, 96, 8, 2, 0, 3), (37, 352, 8, 3, 0.3, 2), (64, 2080, 16, 4, 0, 0),
-           (9, 256, 9, 5, 0.5, 0), (33, 544, 200, 8, 0.1, 7), (3, 16384, 4, 4, 0, 0)]
+           (9, 256, 9, 5, 0.5, 0), (33, 544, 200, 8, 0.1, 7), (3, 16384, 4, 4, 0, 0),
+           (16401, 192, 8, 1, 0.1, 1), (2050, 1056, 8, 8, 0.1, 0), (515, 8224, 5, 1, 0.2, 2)]
 
 
 @pytest.mark.parametrize("dt", ["bf16", "f32"])
@@ -203,7 +204,9 @@ def test_combine_backward(dt, T, d, E, k, drop, spare):
           (H[dt] + U) * np.abs(ref["dy_perm"][named]) + 2.0 ** -126, "dy_perm")
     assert (to_np(b["dy_perm"])[~named] == 5).all()
     mag = ops.combine_backward(np.abs(to_np(go)), np.abs(v), g, idx, pos, E)["dgate"]
-    tol = (d / 64 + 8) * U * mag
+    # roundings of a term: d / 64 products of a thread or fewer, d / 16 <= 16 where a token has 16
+    # threads, and up to 10 additions that join them
+    tol = (d / 64 + 26) * U * mag
     _near(to_np(b["dgate"]), ref["dgate"], tol + 2.0 ** -126, "dgate")
     # dlogits_i = g_i sum_j g_j (dg_i - dg_j): each dg's error, and 4k roundings of the terms
     top = g[:, :, None] * g[:, None, :]
