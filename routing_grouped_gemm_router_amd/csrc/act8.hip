@@ -17,7 +17,7 @@
 // (407 MB, 6.1 TB/s), combine with its checkpoint 125 -> 91 us. dy_perm is
 // stored in the ordinary way: the GEMM that reads it comes next, and a layer's
 // step gains nothing by the other (3.85 ms both ways), though combine and
-// backward in turn would take 159 us instead of 171.
+// backward in turn would take 171 us instead of 177.
 #include "act8.h"
 
 namespace moe {
@@ -126,8 +126,8 @@ MOE_DEV void group_sums(float (&v)[N]) {
 
 // combine that keeps the experts' rows: out[t] = sum_j g[t,j] y[token_pos[t,j]]
 // (fp32 sum, ascending j) and the checkpoint of every row it reads, from one
-// read: 474 MB at T = 16384, d = 2048, k = 4 bf16 in 91 us after its backward's
-// dirty lines, 80 without (5.2 to 5.9 TB/s), where the combine alone takes 61 and
+// read: 474 MB at T = 16384, d = 2048, k = 4 bf16 in 91 to 96 us after its
+// backward's dirty lines, 80 without (4.9 to 5.9 TB/s), where the combine alone takes 61 and
 // a store of its own 67.
 template <bool BF16, int KMAX, int U, int G>
 __global__ __launch_bounds__(G > 256 ? G : 256) void combine_act8_rows(
@@ -185,7 +185,7 @@ __global__ __launch_bounds__(G > 256 ? G : 256) void combine_act8_rows(
 // (the gates sum to one; this form has no cancellation between large terms).
 // ROWS = false (the MXFP8 backward, whose quantiser forms dy_perm itself):
 // row_gate[p_j] = g_j instead of dy_perm's rows. 484 MB at T = 16384, d = 2048, k
-// = 4 bf16 in 79 us (6.1 TB/s); from bf16 rows it takes 100.
+// = 4 bf16 in 79 to 93 us (5.2 to 6.1 TB/s); from bf16 rows it takes 100.
 template <bool BF16, int KMAX, int U, bool ROWS, int G>
 __global__ __launch_bounds__(G > 256 ? G : 256) void combine_bwd_act8_rows(
     const uint4 *__restrict__ dout, const typename Codes<BF16>::type *__restrict__ y8,
