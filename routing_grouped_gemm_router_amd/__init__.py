@@ -683,7 +683,7 @@ def _act8_need(q, scale, rows, cols, index, name):
 
 def _act8_new(rows, cols, dev):
     u8 = dict(dtype=torch.uint8, device=dev)
-    return torch.empty((rows, cols), **u8), torch.empty((rows, cols // 32), **u8)
+    return torch.empty(rows, cols, **u8), torch.empty(rows, cols // 32, **u8)
 
 
 def _act8_out(rows, cols, like, index, q, scale, name):
@@ -697,10 +697,11 @@ def _act8_out(rows, cols, like, index, q, scale, name):
 def _act8_in(q, scale, dtype, name):
     if dtype is not torch.bfloat16 and dtype is not torch.float32:
         raise ValueError(f"dtype: expected bf16 or f32, got {dtype}")
-    if q is None or q.dim() != 2 or q.shape[1] < 32 or q.shape[1] % 32:
+    shape = () if q is None else q.shape
+    if len(shape) != 2 or shape[1] < 32 or shape[1] % 32:
         raise ValueError(f"{name}: expected [rows, a multiple of 32], got "
-                         f"{None if q is None else tuple(q.shape)}")
-    rows, cols = q.shape
+                         f"{None if q is None else tuple(shape)}")
+    rows, cols = shape
     index = q.get_device()
     _act8_need(q, scale, rows, cols, index, name)
     return rows, cols, MOE_BF16 if dtype is torch.bfloat16 else MOE_F32, index
@@ -722,7 +723,7 @@ def moe_act8_load(q: torch.Tensor, scale: torch.Tensor, dtype: torch.dtype = tor
     """The values that a checkpoint stands for, as `dtype` (exact in both)."""
     rows, cols, dt, gpu = _act8_in(q, scale, dtype, "q")
     if out is None:
-        out = torch.empty((rows, cols), dtype=dtype, device=q.device)
+        out = torch.empty_like(q, dtype=dtype)
     else:
         _need_on(out, (rows, cols), dtype, gpu, "out")
     _enqueue("moe_act8_load", _lib.moe_act8_load, gpu, q.data_ptr(), scale.data_ptr(), dt, rows,
@@ -740,11 +741,11 @@ def moe_act8_swiglu(ab8: torch.Tensor, ab8_scale: torch.Tensor,
     if h % 32:
         raise ValueError(f"ab8: the hidden width must be a multiple of 32, got {h}")
     if ab is None:
-        ab = torch.empty((rows, cols), dtype=dtype, device=ab8.device)
+        ab = torch.empty_like(ab8, dtype=dtype)
     else:
         _need_on(ab, (rows, cols), dtype, gpu, "ab")
     if hp is None:
-        hp = torch.empty((rows, h), dtype=dtype, device=ab8.device)
+        hp = torch.empty(rows, h, dtype=dtype, device=ab8.device)
     else:
         _need_on(hp, (rows, h), dtype, gpu, "hp")
     _enqueue("moe_act8_swiglu", _lib.moe_act8_swiglu, gpu, ab8.data_ptr(), ab8_scale.data_ptr(),
@@ -771,7 +772,7 @@ def moe_combine_act8(y_perm: torch.Tensor, topk_gate: torch.Tensor, token_pos: t
     _need_on(token_pos, (T, k), torch.int32, gpu, "token_pos")
     _need_on(topk_gate, (T, k), torch.float32, gpu, "topk_gate")
     if out is None:
-        out = torch.empty((T, d), dtype=y_perm.dtype, device=y_perm.device)
+        out = torch.empty(T, d, dtype=y_perm.dtype, device=y_perm.device)
     else:
         _need_on(out, (T, d), y_perm.dtype, gpu, "out")
     y8, y8_scale = _act8_out(rows, d, y_perm, gpu, y8, y8_scale, "y8")
@@ -799,10 +800,10 @@ def moe_combine_backward_act8(dout: torch.Tensor, y8: torch.Tensor, y8_scale: to
     _need_on(token_pos, (T, k), torch.int32, gpu, "token_pos")
     if out is None:
         dev = dout.device
-        out = dict(dy_perm=torch.empty((R, d), dtype=dout.dtype, device=dev),
-                   dlogits=torch.empty((T, E), dtype=torch.float32, device=dev))
+        out = dict(dy_perm=torch.empty(R, d, dtype=dout.dtype, device=dev),
+                   dlogits=torch.empty(T, E, dtype=torch.float32, device=dev))
         if want_dgate:
-            out["dgate"] = torch.empty((T, k), dtype=torch.float32, device=dev)
+            out["dgate"] = torch.empty(T, k, dtype=torch.float32, device=dev)
     else:
         _need_on(out.get("dy_perm"), (R, d), dout.dtype, gpu, "dy_perm")
         _need_on(out.get("dlogits"), (T, E), torch.float32, gpu, "dlogits")
