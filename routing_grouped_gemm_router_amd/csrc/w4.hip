@@ -123,6 +123,7 @@ MOE_DEV bool w4_active(const int32_t *offsets, int E, int slot, int &e, int &r0,
 constexpr int kW4Tokens = 8;     // rows of an expert that a wave multiplies at once
 constexpr int kW4Steps = 2;      // steps of 128 reduction indices loaded at once
 constexpr int kW4WideTiles = 2;  // row tiles of 16 with many rows
+constexpr int kW4WideSteps(bool up) { return up ? 4 : 2; }    // steps of a piece
 
 struct W4Args {
     const uint16_t *x;           // UP: x [T, d]; else h's upper halves [R, h]
@@ -402,126 +403,138 @@ __global__ __launch_bounds__(256, 4) void w4_product(W4Args p, const int32_t *__
 }
 
 // Many rows an expert: rows [r, r + 16 NT), every wave its own two tiles of
-// weight rows over the whole reduction, in pieces of 4 steps (512 elements).
-// The workgroup keeps a piece of its tokens in LDS for all four waves; a
-// wave's weights of the next piece, and the tokens', are in flight while the
-// piece is computed.
-template <bool UP, int NT>
+// weight rows over the whole reduction, in pieces of PS steps. The workgroup
+// keeps a piece of its tokens in LDS for all four waves, a wave two steps of its
+// weights; the next piece, tokens and weights, is in flight while one is
+// computed.
+template <bool UP, int NT, int PS>
 struct W4Wide {
-    u32x4 x[UP ? 1 : 2][NT][16 * 64];             // 16 tokens of 64 pieces of 16 bytes
-    u32x4 w[4][2][80];                            // a step of each wave
-    uint8_t sc[4][2][64];
+    u32x4 x[UP ? 1 : 2][NT][16 * (16 * PS + 1)];  // 16 tokens of 16 PS pieces of 16 bytes
+    u32x4 w[4][2][16 * 9];
+    uint8_t sc[4][2][16 * 4 * PS];
 };
 
-template <bool UP, int NT>
+// A wave's weights of a piece. Blocks past the row's end repeat its last one
+// (no branch around a load) and count as zeros when they are used.
+template <int PS>
+struct W4Piece {
+    u32x4 w[PS / 2][2][2];                        // row 8 q + lane / 8
+    typename W4Bytes<PS>::type sc[2];             // row lane / 4, PS bytes
+    MOE_DEV void load(int piece, int nblk, const W4Tiles &wt) {
+        const int lane = threadIdx.x & 63;
+        const uint32_t os = (lane >> 2) * nblk + min(4 * PS * piece + PS * (lane & 3), nblk - PS);
+        __builtin_memcpy(&sc[0], wt.s0 + os, PS);
+        __builtin_memcpy(&sc[1], wt.s1 + os, PS);
+#pragma unroll
+        for (int v = 0; v < PS / 2; v++)
+#pragma unroll
+            for (int q = 0; q < 2; q++) {
+                const int c = min(4 * PS * piece + 8 * v + (lane & 7), nblk - 1);
+                const uint32_t o = (8 * q + (lane >> 3)) * nblk + c;
+                w[v][q][0] = *reinterpret_cast<const u32x4 *>(wt.q0 + 16 * o);
+                w[v][q][1] = *reinterpret_cast<const u32x4 *>(wt.q1 + 16 * o);
+            }
+    }
+};
+
+template <bool UP, int NT, int PS>
 MOE_DEV void w4_rows_wide(const W4Args &p, const W4Tiles &wt, int n0, bool store, int r, int r1,
-                          W4Wide<UP, NT> &lds) {
+                          W4Wide<UP, NT, PS> &lds) {
     constexpr int P = UP ? 1 : 2;
     const int tid = threadIdx.x, lane = tid & 63, wave = w4_wave(), g = lane >> 4, i = lane & 15;
-    const int lr = lane >> 2, lc = lane & 3, xt = tid >> 4, xc = tid & 15;
-    const int nblk = p.K / 32, pieces = (nblk + 15) / 16;
-    const uint16_t *x[2][NT];
+    const int xt = tid >> 4, xc = tid & 15;
+    const int nblk = p.K / 32, pieces = (nblk + 4 * PS - 1) / (4 * PS);
+    const int tiles = (r1 - r + 15) / 16;         // of tokens; uniform
+    const int64_t lo = UP ? 0 : p.lo - p.x;
+    const uint16_t *x[NT];
 #pragma unroll
     for (int t = 0; t < NT; t++) {
-        const int row = r + 16 * t + xt;
-        x[0][t] = x[1][t] = nullptr;
-        if (row < r1) {
-            const int64_t src = (UP ? p.sorted_token[row] : row) * (int64_t)p.K;
-            x[0][t] = p.x + src;
-            x[1][t] = UP ? nullptr : p.lo + src;
-        }
+        const int row = min(r + 16 * t + xt, r1 - 1);
+        x[t] = p.x + (UP ? p.sorted_token[row] : row) * (int64_t)p.K;
     }
     const u32x4 zero = {0, 0, 0, 0};
-    u32x4 w[4][2], xr[P][NT][4];
-    uint32_t sc[4][2];
-    // blocks past the row's end: zeros, of both operands
-    auto load_w = [&](int piece) {
-#pragma unroll
-        for (int u = 0; u < 4; u++) {
-            const int c = 16 * piece + 4 * u + lc;
-            w[u][0] = w[u][1] = zero;
-            sc[u][0] = sc[u][1] = 127;
-            if (c < nblk) {
-                const uint32_t o = lr * nblk + c;
-                w[u][0] = *reinterpret_cast<const u32x4 *>(wt.q0 + 16 * o);
-                w[u][1] = *reinterpret_cast<const u32x4 *>(wt.q1 + 16 * o);
-                sc[u][0] = wt.s0[o];
-                sc[u][1] = wt.s1[o];
-            }
-        }
-    };
+    u32x4 xr[P][NT][PS];
     auto load_x = [&](int piece) {
 #pragma unroll
         for (int t = 0; t < NT; t++)
+            if (t == 0 || t < tiles) {
 #pragma unroll
-            for (int q = 0; q < P; q++)
-                if (x[q][t]) {
+                for (int q = 0; q < P; q++)
 #pragma unroll
-                    for (int j = 0; j < 4; j++) {
-                        const int c = 64 * piece + 16 * j + xc;      // 16-byte piece of the row
-                        xr[q][t][j] = c < 4 * nblk
-                            ? *reinterpret_cast<const u32x4 *>(x[q][t] + 8 * c) : zero;
+                    for (int j = 0; j < PS; j++) {
+                        const int c = min(16 * PS * piece + 16 * j + xc, 4 * nblk - 1);
+                        xr[q][t][j] = *reinterpret_cast<const u32x4 *>(x[t] + q * lo + 8 * c);
                     }
-                }
+            }
     };
     f32x4 acc[2][NT];
 #pragma unroll
     for (int z = 0; z < 2; z++)
 #pragma unroll
         for (int t = 0; t < NT; t++) acc[z][t] = f32x4{0.f, 0.f, 0.f, 0.f};
-    load_w(0);
-    load_x(0);
-    for (int piece = 0; piece < pieces; piece++) {
+    auto step = [&](int piece, W4Piece<PS> &now, W4Piece<PS> &next) {
         __syncthreads();                          // the tokens' piece before has been read
 #pragma unroll
         for (int t = 0; t < NT; t++)
+            if (t == 0 || t < tiles) {
 #pragma unroll
-            for (int q = 0; q < P; q++)
-                if (x[q][t])
+                for (int q = 0; q < P; q++)
 #pragma unroll
-                    for (int j = 0; j < 4; j++)
-                        lds.x[q][t][64 * xt + 16 * j + (xc ^ (4 * (xt & 3) + (xt >> 2)))] = xr[q][t][j];
-        u32x4 wc[4][2];
-        uint32_t cc[4][2];
-#pragma unroll
-        for (int u = 0; u < 4; u++)
-#pragma unroll
-            for (int z = 0; z < 2; z++) { wc[u][z] = w[u][z]; cc[u][z] = sc[u][z]; }
+                    for (int j = 0; j < PS; j++) lds.x[q][t][(16 * PS + 1) * xt + 16 * j + xc] = xr[q][t][j];
+            }
         if (piece + 1 < pieces) {
-            load_w(piece + 1);
             load_x(piece + 1);
+            next.load(piece + 1, nblk, wt);
         }
         __syncthreads();
+        const int b0 = 4 * PS * piece;
 #pragma unroll
-        for (int u = 0; u < 4; u++) {
-            w4_lds_order();                       // the step before has been read
+        for (int v = 0; v < PS / 2; v++) {
+            w4_lds_order();                       // the steps before have been read
+            const bool in = b0 + 8 * v + (lane & 7) < nblk;
 #pragma unroll
             for (int z = 0; z < 2; z++) {
-                lds.w[wave][z][w4_wslot<1>(lr, lc)] = wc[u][z];
-                lds.sc[wave][z][lane] = (uint8_t)cc[u][z];
+#pragma unroll
+                for (int q = 0; q < 2; q++)
+                    lds.w[wave][z][9 * (8 * q + (lane >> 3)) + (lane & 7)] = in ? now.w[v][q][z] : zero;
+                if (v == 0) {
+                    const int past = b0 + PS * (lane & 3) - (nblk - PS);     // bytes read too early
+                    const uint32_t b = past <= 0 ? now.sc[z] : past < PS ? (uint32_t)now.sc[z] >> (8 * past) : 0;
+                    *reinterpret_cast<typename W4Bytes<PS>::type *>(&lds.sc[wave][z][PS * lane]) = b;
+                }
             }
             w4_lds_order();
-            u32x4 a[2];
-            float f[2];
 #pragma unroll
-            for (int z = 0; z < 2; z++) {
-                a[z] = lds.w[wave][z][w4_wslot<1>(i, g)];
-                f[z] = __uint_as_float((uint32_t)lds.sc[wave][z][4 * i + g] << 23);
-            }
+            for (int u = 2 * v; u < 2 * v + 2; u++) {
+                u32x4 a[2];
+                float f[2];
 #pragma unroll
-            for (int m = 0; m < 4; m++) {
-                const bf16x8 a0 = w4_widen(a[0][m], f[0]), a1 = w4_widen(a[1][m], f[1]);
+                for (int z = 0; z < 2; z++) {
+                    a[z] = lds.w[wave][z][9 * i + 4 * (u - 2 * v) + g];
+                    f[z] = __uint_as_float((uint32_t)lds.sc[wave][z][4 * (PS * i + u) + g] << 23);
+                }
 #pragma unroll
-                for (int t = 0; t < NT; t++)
+                for (int m = 0; m < 4; m++) {
+                    const bf16x8 a0 = w4_widen(a[0][m], f[0]), a1 = w4_widen(a[1][m], f[1]);
 #pragma unroll
-                    for (int q = 0; q < P; q++) {
-                        const bf16x8 b = __builtin_bit_cast(
-                            bf16x8, lds.x[q][t][64 * i + 16 * u + ((4 * g + m) ^ (4 * (i & 3) + (i >> 2)))]);
-                        acc[0][t] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(a0, b, acc[0][t], 0, 0, 0);
-                        acc[1][t] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(a1, b, acc[1][t], 0, 0, 0);
-                    }
+                    for (int t = 0; t < NT; t++)
+#pragma unroll
+                        for (int q = 0; q < P; q++) {
+                            const bf16x8 b = __builtin_bit_cast(
+                                bf16x8, lds.x[q][t][(16 * PS + 1) * i + 16 * u + 4 * g + m]);
+                            acc[0][t] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(a0, b, acc[0][t], 0, 0, 0);
+                            acc[1][t] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(a1, b, acc[1][t], 0, 0, 0);
+                        }
+                }
             }
         }
+    };
+    W4Piece<PS> even, odd;
+    load_x(0);
+    even.load(0, nblk, wt);
+    for (int piece = 0; piece < pieces; piece += 2) {
+        step(piece, even, odd);
+        if (piece + 1 < pieces) step(piece + 1, odd, even);
     }
     // lane: token i, weight rows 4 g .. 4 g + 3
 #pragma unroll
@@ -535,11 +548,11 @@ MOE_DEV void w4_rows_wide(const W4Args &p, const W4Tiles &wt, int n0, bool store
 
 // column group: 64 columns of h (UP) or 128 of d, a quarter for each wave;
 // blockIdx.y: rank of an expert with rows
-template <bool UP, int NT>
+template <bool UP, int NT, int PS>
 __global__ __launch_bounds__(256, 2) void w4_product_wide(W4Args p,
                                                           const int32_t *__restrict__ offsets,
                                                           int E, int Z) {
-    __shared__ W4Wide<UP, NT> lds;
+    __shared__ W4Wide<UP, NT, PS> lds;
     int e, r0, r1;
     if (!w4_active(offsets, E, blockIdx.y, e, r0, r1)) return;      // the whole workgroup
     int col, z;
@@ -550,7 +563,7 @@ __global__ __launch_bounds__(256, 2) void w4_product_wide(W4Args p,
     const int m0 = min(n0, n - (UP ? 16 : 32));
     const int64_t w0 = (int64_t)e * (UP ? 2 * p.h : p.d) + m0;
     const W4Tiles wt(p, w0, w0 + (UP ? p.h : 16));
-    for (int r = r0 + z * 16 * NT; r < r1; r += Z * 16 * NT) w4_rows_wide<UP, NT>(p, wt, m0, n0 < n, r, r1, lds);
+    for (int r = r0 + z * 16 * NT; r < r1; r += Z * 16 * NT) w4_rows_wide<UP, NT, PS>(p, wt, m0, n0 < n, r, r1, lds);
 }
 
 // A handful of rows: out[t] for 32 columns from the token's own experts, gates
@@ -675,8 +688,8 @@ static void w4_product_launch(const moe_w4_desc &w, const W4Args &a, int n, hipS
         return (int)(z < 1 ? 1 : z < parts ? z : parts);
     };
     const int zw = split(c4, 16 * kW4WideTiles);
-    if (R >= 12 * (int64_t)w.E && (int64_t)c4 * ny * zw >= 256)
-        w4_product_wide<UP, kW4WideTiles><<<dim3(w4_grid(c4, zw), ny), 256, 0, s>>>(a, w.offsets, w.E, zw);
+    if (R >= 12 * (int64_t)w.E && a.K >= 32 * kW4WideSteps(UP) && (int64_t)c4 * ny * zw >= 256)
+        w4_product_wide<UP, kW4WideTiles, kW4WideSteps(UP)><<<dim3(w4_grid(c4, zw), ny), 256, 0, s>>>(a, w.offsets, w.E, zw);
     else if ((int64_t)c * ny >= 1280) {
         const int z = split(c2, kW4Tokens);
         w4_product<UP, 2><<<dim3(w4_grid(c2, z), ny), 256, 0, s>>>(a, w.offsets, w.E, z);
