@@ -33,7 +33,7 @@
 // 32), half as many workgroups (51 -> 49, 32 -> 31), runs of whole cache lines
 // (49 -> 47), h's halves side by side in one product and LDS rows an odd number
 // of pieces apart, whose places are constants and not registers (.., 31 -> 28).
-// Slower were loads past the last-level cache, whole rows a wave, the next
+// The loads alone, in the same order, take 44 and 25. Slower were loads past the last-level cache, whole rows a wave, the next
 // step's weights in flight during a step (59 and 33 us one step at a time, no
 // gain and spilled registers two at a time), twice the registers for loads,
 // more waves with fewer loads each (55 and 37 us).
@@ -665,17 +665,16 @@ size_t w4_ws_bytes(int64_t R, int d, int h) {
 // E) and workgroups (times of all launches of a call):
 //  - from twelve rows an expert, with a workgroup of 64 columns and 32 rows for
 //    every compute unit: the wide kernels. d = 2048, h = 1024, E = 128, k = 4, T =
-//    512 (16 rows) 150 us against 203; T = 256 (8 rows) 137 against 134. E = 16, k
-//    = 4, T = 64 (16 rows) 31 against 35, T = 32 28 against 25. d = 4096, h = 2048,
-//    E = 4, k = 2, T = 64 (128 workgroups) 79 against 46, T = 256 (512) 97 against
-//    128.
+//    512 (16 rows) 134 us against 190; T = 256 (8 rows) 125 both ways; E = 16, k =
+//    4, T = 64 (16 rows) 29 against 34, T = 32 27 against 24. E = 8, k = 2, T = 128
+//    (128 workgroups) 41 against 30, T = 512 (512) 56 against 79.
 //  - five workgroups a compute unit and up: two waves a reduction, not four, so
 //    that half as many workgroups look for their expert and join sums. d = 2048,
 //    h = 1024, E = 128, k = 4, T = 64 85.3 us against 88.0, E = 256, d = 1024, h =
 //    512, k = 8, T = 64 52 against 62; fewer leave compute units out: E = 8, k = 2,
 //    T = 16 16.4 against 15.1.
 // An expert's rows are shared out to as many workgroups as it takes for four a
-// compute unit (eight no better): d = 2048, h = 1024, E = 2, k = 2, T = 256 31 us
+// compute unit (eight no better): d = 2048, h = 1024, E = 2, k = 2, T = 256 29 us
 // against 135 with one; d = 8192, h = 96, E = 4, k = 2, T = 128 32 against 84.
 template <bool UP>
 static void w4_product_launch(const moe_w4_desc &w, const W4Args &a, int n, hipStream_t s) {
