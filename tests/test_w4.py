@@ -136,7 +136,7 @@ def _check(out, x, r, w1, w2):
     (1, 32, 32, 1, 1), (1, 2048, 1024, 8, 4), (2, 96, 160, 5, 3), (7, 416, 352, 16, 8), (64, 256, 128, 32, 4),
     (33, 160, 96, 2, 1), (50, 544, 64, 3, 2), (300, 64, 96, 4, 2), (1, 4128, 32, 4, 2), (3, 64, 2080, 256, 8),
     (256, 416, 224, 64, 2), (160, 448, 2048, 16, 1), (90, 672, 352, 64, 2),
-    (400, 448, 2048, 16, 1), (200, 4128, 160, 4, 4), (130, 2048, 96, 2, 2)])
+    (400, 448, 2048, 16, 1), (200, 4128, 160, 4, 4), (130, 2048, 96, 2, 2), (256, 2080, 1056, 2, 2)])
 def test_experts(T, d, h, E, k):
     """From one row per expert to many tiles of them; widths whose last step is partial."""
     w1q, s1, w2q, s2, w1, w2 = _weights(E, d, h, T + d)
