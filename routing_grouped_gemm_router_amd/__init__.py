@@ -1014,6 +1014,60 @@ def _nbytes(ts) -> int:
     return sum(t.numel() * t.element_size() for t in ts if t is not None)
 
 
+def _tensors(v):
+    """The tensors in a (nested) dict of buffers."""
+    if isinstance(v, dict):
+        return [t for w in v.values() for t in _tensors(w)]
+    return [v] if isinstance(v, torch.Tensor) else []
+
+
+def _capturing(index: int) -> bool:
+    """Whether GPU `index`'s current stream is being captured into a graph."""
+    if _cur_device() == index:
+        return torch.cuda.is_current_stream_capturing()
+    with torch.cuda.device(index):
+        return torch.cuda.is_current_stream_capturing()
+
+
+# Bytes of buffers that a layer object keeps for sizes it was called with
+# before its last one: enough for the batch sizes of text generation, next to
+# nothing beside a training step's activations.
+_KEPT_BYTES = 64 << 20
+
+
+class _Sizes:
+    """The buffers of a layer object: a dict for each size it is called with.
+
+    A replay reads and writes the buffers of the call that was captured, so a
+    dict that was in use during a capture stays as long as the object does.
+    Of the others the last used stays, and earlier ones while they take
+    _KEPT_BYTES at most together."""
+
+    def __init__(self):
+        self._all, self._bytes, self._captured, self._last = {}, {}, set(), None
+
+    def at(self, key) -> dict:
+        """The dict of this size, the caller's to fill."""
+        if key != self._last:
+            if self._last is not None:
+                self._bytes[self._last] = _nbytes(_tensors(self._all[self._last]))
+            self._last = key
+            self._all[key] = self._all.pop(key, {})         # last used last
+            room = _KEPT_BYTES
+            for k in list(self._all)[-2::-1]:
+                if k not in self._captured:
+                    if 0 < self._bytes[k] <= room:
+                        room -= self._bytes[k]
+                    else:
+                        del self._all[k]
+        return self._all[key]
+
+    def mark(self, key, index):
+        """To be called whenever kernels that use the dict were enqueued."""
+        if key not in self._captured and _capturing(index):
+            self._captured.add(key)
+
+
 MOE_LB_NSTATS = 8
 LB_STAT_NAMES = ("loss", "soft_hard_balance", "hard_balance", "soft_balance", "max_load_over_mean",
                  "min_load_over_mean", "count_cv", "empty_experts")
@@ -1076,22 +1130,25 @@ class LayerNorm:
     residual and leaves that stream in `sum`. act8=True holds the normalised
     input from forward to backward as an 8-bit checkpoint (33/64 of its bf16
     size), written by the forward's kernel; otherwise the backward reads x (or
-    sum), which the caller must leave as it was. Buffers are allocated once
-    per (T, dtype, device) and reused: calls (or replays) of one object must
-    not overlap in time."""
+    sum), which the caller must leave as it was. Buffers are allocated at the
+    first call with a size and reused: calls (or replays) of one object must
+    not overlap in time. They stay for sizes that a captured graph uses, for
+    the last one, and for small earlier ones (64 MiB in all)."""
 
     def __init__(self, weight: torch.Tensor, bias: torch.Tensor | None = None, eps: float = 1e-5,
                  act8: bool = False):
         self.weight, self.bias, self.eps, self.act8 = weight, bias, eps, act8
         self.sum = None
-        self._key = None
+        self._sizes, self._key = _Sizes(), None
 
     def forward(self, x: torch.Tensor, residual: torch.Tensor | None = None) -> torch.Tensor:
         key = (x.shape, x.dtype, x.device, residual is None)
         if self._key != key:
-            self._out, self._ws, self.grads, self._key = None, None, None, None
-        self._out = moe_layer_norm(x, self.weight, self.bias, self.eps, residual, self.act8,
-                                   out=self._out)
+            self.grads = self._key = None
+        buf = self._sizes.at(key)
+        self._out = buf["out"] = moe_layer_norm(x, self.weight, self.bias, self.eps, residual,
+                                                self.act8, out=buf.get("out"))
+        self._sizes.mark(key, x.get_device())
         self._key = key
         self.sum = self._out.get("sum")
         self._x = None if self.act8 else (x if residual is None else self.sum)
@@ -1105,13 +1162,14 @@ class LayerNorm:
             raise ValueError("backward without a forward")
         if accumulate_dw and self.grads is None:
             raise ValueError("accumulate_dw needs the gradients of an earlier backward")
-        if self._ws is None:
-            y = self._out["y"]
+        buf, y = self._sizes.at(self._key), self._out["y"]
+        if "ws" not in buf:
             wsb = moe_layer_norm_backward_workspace_size(_dt(y), *y.shape)
-            self._ws = torch.empty(max(wsb, 16), dtype=torch.uint8, device=y.device)
-        self.grads = moe_layer_norm_backward(dict(self._out, x=self._x), dy, self.weight, dsum,
-                                             out=self.grads, accumulate_dw=accumulate_dw,
-                                             want_dbias=self.bias is not None, ws=self._ws)
+            buf["ws"] = torch.empty(max(wsb, 16), dtype=torch.uint8, device=y.device)
+        self.grads = buf["grads"] = moe_layer_norm_backward(
+            dict(self._out, x=self._x), dy, self.weight, dsum, out=buf.get("grads"),
+            accumulate_dw=accumulate_dw, want_dbias=self.bias is not None, ws=buf["ws"])
+        self._sizes.mark(self._key, y.get_device())
         return self.grads
 
     def held_bytes(self) -> int:
@@ -1541,16 +1599,18 @@ class MoELayerW4:
     """The layer's forward for text generation: routing, then the experts
     with MXFP4 weights (moe_w4_experts), for a step's few tokens. w1 [E, 2h,
     d], w2 [E, d, h] (f32 or bf16) are quantised once and not kept. Buffers
-    are allocated once per (T, device), so a step is kernel launches alone
-    and can be captured in a HIP graph; calls (or replays) of one layer object
-    must not overlap in time, they share its buffers."""
+    are allocated at the first call with a T and reused, so a step is kernel
+    launches alone and can be captured in a HIP graph, one for each batch
+    size; calls (or replays) of one layer object must not overlap in time,
+    they share its buffers. Those stay for every T that a captured graph uses,
+    for the last T, and for small earlier ones (64 MiB in all)."""
 
     def __init__(self, w1: torch.Tensor, w2: torch.Tensor, k: int):
         self.E, h2, self.d = w1.shape
         self.h, self.k = h2 // 2, k
         _need_on(w2, (self.E, self.d, self.h), w2.dtype, w1.get_device(), "w2")
         self.prepare_weights(w1, w2)
-        self._T = None
+        self._sizes = _Sizes()
 
     def prepare_weights(self, w1: torch.Tensor, w2: torch.Tensor):
         """Quantise the weights (again after they have changed)."""
@@ -1563,14 +1623,18 @@ class MoELayerW4:
         T, dev, gpu = x.shape[0], self.w1q.device, self.w1q.get_device()
         _need_on(x, (T, self.d), torch.bfloat16, gpu, "x")
         _need_on(logits, (T, self.E), torch.float32, gpu, "logits")
-        if self._T != T:
-            self.route, self.out = None, torch.empty((T, self.d), dtype=x.dtype, device=dev)
-            self.route_ws = torch.empty(max(moe_route_workspace_size(T, self.E, self.k), 1),
-                                        dtype=torch.uint8, device=dev)
-            wsb = moe_w4_experts_workspace_size(T, self.k, self.d, self.h)
-            self.ws = torch.empty(max(wsb, 16), dtype=torch.uint8, device=dev)
-            self._T = T
+        key = (T, dev)
+        buf = self._sizes.at(key)
         with torch.cuda.device(gpu):
-            self.route = moe_route(logits, self.k, out=self.route, ws=self.route_ws)
-        return moe_w4_experts(x, self.route, self.w1q, self.w1s, self.w2q, self.w2s, self.out,
-                              self.ws)
+            if not buf:
+                u8 = lambda n: torch.empty(n, dtype=torch.uint8, device=dev)
+                wsb = moe_w4_experts_workspace_size(T, self.k, self.d, self.h)
+                buf.update(route=None, out=torch.empty((T, self.d), dtype=x.dtype, device=dev),
+                           route_ws=u8(max(moe_route_workspace_size(T, self.E, self.k), 1)),
+                           ws=u8(max(wsb, 16)))
+            self.route = buf["route"] = moe_route(logits, self.k, out=buf["route"],
+                                                  ws=buf["route_ws"])
+        self.out = moe_w4_experts(x, self.route, self.w1q, self.w1s, self.w2q, self.w2s,
+                                  buf["out"], buf["ws"])
+        self._sizes.mark(key, gpu)
+        return self.out

@@ -1,0 +1,179 @@
+"""Which buffers the layer objects keep (no GPU needed: the library's calls
+are replaced by ones that allocate alike on the CPU)."""
+import pytest
+import torch
+
+import routing_grouped_gemm_router_amd as moe
+
+E, K, D, H = 8, 2, 64, 32
+MIB = 1 << 20
+
+
+@pytest.fixture
+def capture(monkeypatch):
+    """A switch: whether the current stream is being captured."""
+    on = [False]
+    monkeypatch.setattr(moe, "_capturing", lambda index: on[0])
+    return on
+
+
+def test_a_captured_size_stays(capture):
+    s = moe._Sizes()
+    fill = lambda key, n: s.at(key).setdefault("t", torch.empty(n, dtype=torch.uint8)).data_ptr()
+    big = 2 * moe._KEPT_BYTES
+    at = {}
+    for key in (1, 2):
+        at[key] = fill(key, big)
+        capture[0] = True
+        s.mark(key, 0)
+        capture[0] = False
+    for key in range(3, 9):
+        fill(key, big)
+        s.mark(key, 0)
+        assert set(s._all) == {1, 2, key}                  # and of the others the last alone
+    assert fill(1, big) == at[1] and fill(2, big) == at[2]
+
+
+def test_small_sizes_stay_up_to_a_limit(capture):
+    s = moe._Sizes()
+    fill = lambda key, n: s.at(key).setdefault("d", dict(t=torch.empty(n, dtype=torch.uint8)))["t"].data_ptr()
+    at = {key: fill(key, 16 * MIB) for key in range(4)}
+    assert all(fill(key, 16 * MIB) == at[key] for key in range(4))
+    fill(4, 16 * MIB)                                      # four of 16 MiB beside the last
+    assert sorted(s._all) == [0, 1, 2, 3, 4]
+    fill(5, 16 * MIB)                                      # the one that was used longest ago goes
+    assert sorted(s._all) == [1, 2, 3, 4, 5]
+    fill(6, 100 * MIB)
+    assert sorted(s._all) == [2, 3, 4, 5, 6]
+    fill(7, 1)                                             # the large one goes, small ones stay
+    assert sorted(s._all) == [2, 3, 4, 5, 7]
+    s.at(8)                                                # a refused call leaves nothing
+    s.at(7)
+    assert sorted(s._all) == [3, 4, 5, 7]                  # a byte and 64 MiB are too many
+
+
+class _Device:
+    def __init__(self, index):
+        pass
+
+    def __enter__(self):
+        pass
+
+    def __exit__(self, *exc):
+        pass
+
+
+@pytest.fixture
+def on_cpu(monkeypatch, capture):
+    """The layer objects' calls with tensors on the CPU and no arithmetic."""
+    monkeypatch.setattr(moe, "_need_on", lambda t, shape, dtype, index, name: None)
+    monkeypatch.setattr(torch.cuda, "device", _Device)
+    monkeypatch.setattr(moe, "_check", lambda name, st: None)
+    monkeypatch.setattr(moe, "_enqueue", lambda name, fn, index, *args: None)
+    monkeypatch.setattr(moe, "_stream", lambda: 0)
+    monkeypatch.setattr(moe, "_act_matrix",
+                        lambda x, name: (x.shape[0], x.shape[1], moe.MOE_BF16, -1))
+    monkeypatch.setattr(moe, "_need_ws", lambda ws, nbytes, like, gpu: ws)
+    monkeypatch.setattr(moe, "_need", lambda t, shape, dtype, name: None)
+
+    class Lib:
+        def __getattr__(self, name):
+            return getattr(lib, name) if name.endswith("_size") else lambda *args: 0
+
+    lib = moe._lib
+    monkeypatch.setattr(moe, "_lib", Lib())
+    return capture
+
+
+def _w4():
+    return moe.MoELayerW4(torch.zeros(E, 2 * H, D), torch.zeros(E, D, H), K)
+
+
+def _w4_step(layer, T):
+    layer.forward(torch.zeros(T, D, dtype=torch.bfloat16), torch.zeros(T, E))
+    return [t.data_ptr() for t in (layer.out, *layer.route.values())]
+
+
+def test_w4_layer_keeps_its_buffers(on_cpu):
+    """The addresses at a T are the same after calls at others."""
+    layer = _w4()
+    first = {T: _w4_step(layer, T) for T in (1, 4, 64)}
+    assert first == {T: _w4_step(layer, T) for T in (1, 4, 64)}
+    # sizes above what is kept: captured ones stay, in whatever order they come
+    big = {}
+    for T in (300000, 300001):
+        _w4_step(layer, T)
+        on_cpu[0] = True
+        big[T] = _w4_step(layer, T)
+        on_cpu[0] = False
+    for T in (300002, 300003, 1):
+        _w4_step(layer, T)
+    assert big == {T: _w4_step(layer, T) for T in big}
+    assert (300002, layer.w1q.device) not in layer._sizes._all
+
+
+def test_norm_keeps_its_buffers(on_cpu):
+    norm = moe.LayerNorm(torch.zeros(D), torch.zeros(D), act8=True)
+
+    def step(T, res):
+        x = torch.zeros(T, D)
+        norm.forward(x, x if res else None)
+        norm.backward(x)
+        return [t.data_ptr() for t in moe._tensors(dict(norm._out, g=norm.grads))]
+
+    sizes = [(1, False), (1, True), (7, True)]
+    first = {s: step(*s) for s in sizes}
+    assert first == {s: step(*s) for s in sizes}
+
+
+def test_norm_captured_in_its_backward_alone(on_cpu):
+    """An eager forward and a captured backward: what the forward left is read at every replay."""
+    norm = moe.LayerNorm(torch.zeros(D), None)
+    x = torch.zeros(400000, D)
+    norm.forward(x)
+    on_cpu[0] = True
+    norm.backward(x)
+    on_cpu[0] = False
+    at = (norm._out["mean"].data_ptr(), norm.grads["dx"].data_ptr())
+    for T in (400001, 400002):
+        norm.forward(torch.zeros(T, D))
+        norm.backward(torch.zeros(T, D))
+    norm.forward(x)
+    norm.backward(x)
+    assert at == (norm._out["mean"].data_ptr(), norm.grads["dx"].data_ptr())
+
+
+def test_norm_adds_to_gradients_of_one_size_only(on_cpu):
+    """Gradients of another size in between are not added to: refused as ever,
+    though the buffers of the first size are still there."""
+    norm = moe.LayerNorm(torch.zeros(D), None)
+    a, b = torch.zeros(3, D), torch.zeros(5, D)
+    for x in (a, b):
+        norm.forward(x)
+        norm.backward(x)
+    norm.forward(a)
+    with pytest.raises(ValueError, match="earlier backward"):
+        norm.backward(a, accumulate_dw=True)
+    norm.backward(a)
+    norm.backward(a, accumulate_dw=True)
+
+
+def test_capture_is_asked_of_the_buffers_gpu(monkeypatch):
+    """The stream that counts is the current one of the GPU that the buffers are on."""
+    current, seen = [1], []
+
+    class Device:
+        def __init__(self, index):
+            self.index = index
+
+        def __enter__(self):
+            self.before, current[0] = current[0], self.index
+
+        def __exit__(self, *exc):
+            current[0] = self.before
+
+    monkeypatch.setattr(moe, "_cur_device", lambda: current[0])
+    monkeypatch.setattr(torch.cuda, "device", Device)
+    monkeypatch.setattr(torch.cuda, "is_current_stream_capturing",
+                        lambda: seen.append(current[0]) or current[0] == 0)
+    assert moe._capturing(0) and not moe._capturing(1) and seen == [0, 1] and current == [1]
