@@ -1608,14 +1608,21 @@ class MoELayerW4:
     def __init__(self, w1: torch.Tensor, w2: torch.Tensor, k: int):
         self.E, h2, self.d = w1.shape
         self.h, self.k = h2 // 2, k
-        _need_on(w2, (self.E, self.d, self.h), w2.dtype, w1.get_device(), "w2")
+        self.w1q = self.w1s = self.w2q = self.w2s = None
         self.prepare_weights(w1, w2)
         self._sizes = _Sizes()
 
     def prepare_weights(self, w1: torch.Tensor, w2: torch.Tensor):
-        """Quantise the weights (again after they have changed)."""
-        self.w1q, self.w1s = moe_w4_quantize(w1)
-        self.w2q, self.w2s = moe_w4_quantize(w2)
+        """Quantise the weights, again after they have changed: into the same
+        tensors, so that the replays of a captured step take the new ones
+        (weights on another GPU get tensors there)."""
+        gpu = w1.get_device()
+        _need_on(w1, (self.E, 2 * self.h, self.d), w1.dtype, gpu, "w1")
+        _need_on(w2, (self.E, self.d, self.h), w2.dtype, gpu, "w2")
+        if self.w1q is not None and self.w1q.device != w1.device:
+            self.w1q = self.w1s = self.w2q = self.w2s = None
+        self.w1q, self.w1s = moe_w4_quantize(w1, self.w1q, self.w1s)
+        self.w2q, self.w2s = moe_w4_quantize(w2, self.w2q, self.w2s)
 
     def forward(self, x: torch.Tensor, logits: torch.Tensor) -> torch.Tensor:
         if x.dim() != 2 or x.shape[1] != self.d or x.dtype != torch.bfloat16:

@@ -177,3 +177,28 @@ def test_capture_is_asked_of_the_buffers_gpu(monkeypatch):
     monkeypatch.setattr(torch.cuda, "is_current_stream_capturing",
                         lambda: seen.append(current[0]) or current[0] == 0)
     assert moe._capturing(0) and not moe._capturing(1) and seen == [0, 1] and current == [1]
+
+
+def test_w4_weights_stay_in_their_tensors(on_cpu):
+    layer = _w4()
+    at = lambda: [t.data_ptr() for t in (layer.w1q, layer.w1s, layer.w2q, layer.w2s)]
+    first = at()
+    layer.prepare_weights(torch.ones(E, 2 * H, D), torch.ones(E, D, H))
+    assert at() == first
+
+
+@pytest.mark.parametrize("s1,s2", [((E, 2 * H, 2 * D), (E, 2 * D, H)), ((E, 2 * H, D), (E, D, 2 * H)),
+                                   ((E + 1, 2 * H, D), (E + 1, D, H))])
+def test_w4_weights_of_other_sizes_are_refused(on_cpu, monkeypatch, s1, s2):
+    """Before either of the two is written."""
+    layer, written = _w4(), []
+
+    def need_on(t, shape, dtype, index, name):
+        if tuple(t.shape) != shape:
+            raise ValueError(name)
+
+    monkeypatch.setattr(moe, "_need_on", need_on)
+    monkeypatch.setattr(moe, "moe_w4_quantize", lambda *args: written.append(args))
+    with pytest.raises(ValueError):
+        layer.prepare_weights(torch.ones(s1), torch.ones(s2))
+    assert not written

@@ -87,3 +87,22 @@ def test_norm_at_several_sizes(monkeypatch, act8):
     step(norm, other)
     _replays(graphs, inputs, [lambda x=x: step(eager, x) for x in inputs],
              lambda i: step(norm, other[:64 - i]))
+
+
+def test_w4_weights_change_between_replays():
+    """A captured step takes the weights that the layer was given last."""
+    w = [[dev(n(s, 2 + i, 0.05), torch.float32) for s in ((E, 2 * H, D), (E, D, H))] for i in range(3)]
+    layer = moe.MoELayerW4(*w[0], K)
+    x, lg = dev(n((4, D), 5, 1.0), torch.bfloat16), dev(n((4, E), 6, 1.0), torch.float32)
+    graph, got = _capture(lambda: layer.forward(x, lg))
+    seen = []
+    for i in (0, 1, 2, 0):
+        layer.prepare_weights(*w[i])
+        tensors, untouched = _fill(i + 1)
+        graph.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(got, moe.MoELayerW4(*w[i], K).forward(x, lg)), i
+        assert untouched(), i
+        del tensors
+        seen.append(got.clone())
+    assert torch.equal(seen[0], seen[3]) and not torch.equal(seen[0], seen[1])
