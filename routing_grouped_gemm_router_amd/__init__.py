@@ -1105,15 +1105,16 @@ class _Balance:
     def __init__(self, alpha: float):
         self.alpha = alpha
         self.stats = None
-        self.ws = None
 
-    def forward(self, logits, counts, k):
+    def forward(self, logits, counts, k, buf):
+        """buf: the layer's buffers of this size (_Sizes)."""
         T, E = logits.shape
         if self.stats is None:
             self.stats = torch.empty(MOE_LB_NSTATS, dtype=torch.float32, device=logits.device)
-        wsb = max(moe_load_balance_workspace_size(T, E), 4)
-        if self.ws is None or self.ws.numel() < wsb:
-            self.ws = torch.empty(wsb, dtype=torch.uint8, device=logits.device)
+        if "lb_ws" not in buf:
+            wsb = max(moe_load_balance_workspace_size(T, E), 4)
+            buf["lb_ws"] = torch.empty(wsb, dtype=torch.uint8, device=logits.device)
+        self.ws = buf["lb_ws"]
         self.logits, self.counts, self.k = logits, counts, k
         return moe_load_balance(logits, counts, k, self.alpha, stats=self.stats, ws=self.ws)
 
@@ -1144,7 +1145,7 @@ class LayerNorm:
     def forward(self, x: torch.Tensor, residual: torch.Tensor | None = None) -> torch.Tensor:
         key = (x.shape, x.dtype, x.device, residual is None)
         if self._key != key:
-            self.grads = self._key = None
+            self._out = self.grads = self._key = None
         buf = self._sizes.at(key)
         self._out = buf["out"] = moe_layer_norm(x, self.weight, self.bias, self.eps, residual,
                                                 self.act8, out=buf.get("out"))
@@ -1191,6 +1192,24 @@ def _norm_grads(norm, grads):
     return grads
 
 
+def _use_buffers(obj, key, new):
+    """The buffers of a size made the attributes of a layer object: new()'s,
+    or those of an earlier call. Returns the key and the size's dict, which
+    also keeps the gradients of the size's backward."""
+    if obj._T == key:
+        return key, obj._buf
+    if obj._T is not None:                        # no old tensor is kept from being freed
+        for name in obj._buf["tensors"]:
+            delattr(obj, name)
+        obj._T = obj._buf = None
+    obj.grads = None
+    buf = obj._sizes.at(key)
+    if "tensors" not in buf:
+        buf["tensors"] = new()
+    obj.__dict__.update(buf["tensors"])
+    return key, buf
+
+
 def _act8_buffers(R, d, h, dev):
     """The checkpoints that a layer holds: of A||B and of y_perm."""
     ab8, ab8_scale = _act8_new(R, 2 * h, dev)
@@ -1201,8 +1220,10 @@ def _act8_buffers(R, d, h, dev):
 class MoELayer:
     """Forward and backward of the MoE expert layer through the C ABI.
 
-    Buffers are allocated once per (T, dtype, device) and reused across calls, so a step
-    issues only kernel launches (no allocation, no device->host traffic).
+    Buffers are allocated at the first call with a (T, dtype, device) and reused, so a step
+    issues only kernel launches (no allocation, no device->host traffic) and can be captured
+    in a HIP graph. They stay for sizes that a captured graph uses, for the last one, and for
+    small earlier ones (64 MiB in all).
 
     recompute=True trades compute for activation memory (the trade-off the
     Olmo-core 3 report measures, kongchang.com "where the costs are"): the
@@ -1243,7 +1264,7 @@ class MoELayer:
         self.scratch, self.out_norm = scratch, out_norm
         self.balance = _Balance(aux_alpha) if aux_alpha is not None else None
         self.lb_stats = None
-        self._T = None
+        self._sizes, self._T = _Sizes(), None
 
     def _check_input(self, x, logits):
         if x.dim() != 2 or x.shape[1] != self.d:
@@ -1257,30 +1278,28 @@ class MoELayer:
         _need(logits, (x.shape[0], self.E), torch.float32, "logits")
 
     def _alloc(self, T, dev, dt):
-        key = (T, dt, str(dev))
-        if self._T == key:
-            return
+        self._T, self._buf = _use_buffers(self, (T, dt, str(dev)), lambda: self._new(T, dev, dt))
+
+    def _new(self, T, dev, dt) -> dict:
+        """The tensors of a size, by the names that they have in the object."""
         E, k, d, h = self.E, self.k, self.d, self.h
         R = T * k
         i32 = dict(dtype=torch.int32, device=dev)
-        self.route = dict(topk_idx=torch.empty((T, k), **i32),
-                          topk_gate=torch.empty((T, k), dtype=torch.float32, device=dev),
-                          counts=torch.empty(E, **i32), offsets=torch.empty(E + 1, **i32),
-                          token_pos=torch.empty((T, k), **i32), sorted_token=torch.empty(R, **i32),
-                          sorted_slot=torch.empty(R, **i32), tile_offsets=torch.empty(E + 1, **i32))
-        self.route_ws = torch.empty(max(moe_route_workspace_size(T, E, k), 1), dtype=torch.uint8,
-                                    device=dev)
+        route = dict(topk_idx=torch.empty((T, k), **i32),
+                     topk_gate=torch.empty((T, k), dtype=torch.float32, device=dev),
+                     counts=torch.empty(E, **i32), offsets=torch.empty(E + 1, **i32),
+                     token_pos=torch.empty((T, k), **i32), sorted_token=torch.empty(R, **i32),
+                     sorted_slot=torch.empty(R, **i32), tile_offsets=torch.empty(E + 1, **i32))
         own = (lambda name, shape: torch.empty(shape, dtype=dt, device=dev))
         tmp = ((lambda name, shape: _scratch(name, shape, dt, dev, self.scratch))
                if self.recompute or self.act8 else own)
-        self.x_perm = tmp("x_perm", (R, d))
-        self.ab = tmp("ab", (R, 2 * h))
-        self.hp = tmp("hp", (R, h))
-        self.y_perm = (tmp if self.act8 else own)("y_perm", (R, d))
-        self.ckpt = _act8_buffers(R, d, h, dev) if self.act8 else None
-        self.out = torch.empty((T, d), dtype=dt, device=dev)
-        self.grads = None
-        self._T = key
+        return dict(route=route,
+                    route_ws=torch.empty(max(moe_route_workspace_size(T, E, k), 1),
+                                         dtype=torch.uint8, device=dev),
+                    x_perm=tmp("x_perm", (R, d)), ab=tmp("ab", (R, 2 * h)), hp=tmp("hp", (R, h)),
+                    y_perm=(tmp if self.act8 else own)("y_perm", (R, d)),
+                    ckpt=_act8_buffers(R, d, h, dev) if self.act8 else None,
+                    out=torch.empty((T, d), dtype=dt, device=dev))
 
     def _gemm1(self, offsets):
         moe_grouped_gemm(MOE_GG_FWD, self.x_perm, self.w1, self.ab, offsets,
@@ -1293,7 +1312,7 @@ class MoELayer:
         self.x = x
         r = moe_route(logits, self.k, out=self.route, ws=self.route_ws)
         if self.balance is not None:
-            self.lb_stats = self.balance.forward(logits, r["counts"], self.k)
+            self.lb_stats = self.balance.forward(logits, r["counts"], self.k, self._buf)
         moe_permute(x, r["token_pos"], self.x_perm)
         self._gemm1(r["offsets"])
         if self.act8:
@@ -1304,6 +1323,7 @@ class MoELayer:
                              self.ckpt["y8"], self.ckpt["y8_scale"])
         else:
             moe_combine(self.y_perm, r["topk_gate"], r["token_pos"], self.out)
+        self._sizes.mark(self._T, x.get_device())
         return self.out if self.out_norm is None else self.out_norm.forward(self.out)
 
     def saved(self) -> dict:
@@ -1339,11 +1359,12 @@ class MoELayer:
             moe_permute(self.x, self.route["token_pos"], self.x_perm)
         if self.recompute:
             self._gemm1(self.route["offsets"])
-        self.grads = moe_backward(self.saved(), dout, self.E, self.k, self.d, self.h,
-                                  out=self.grads, accumulate_dw=accumulate_dw,
-                                  stage_events=stage_events, act8=self.ckpt)
+        self.grads = self._buf["grads"] = moe_backward(
+            self.saved(), dout, self.E, self.k, self.d, self.h, out=self._buf.get("grads"),
+            accumulate_dw=accumulate_dw, stage_events=stage_events, act8=self.ckpt)
         if self.balance is not None:
             self.balance.backward(self.grads["dlogits"])
+        self._sizes.mark(self._T, dout.get_device())
         return _norm_grads(self.out_norm, self.grads)
 
 
@@ -1359,26 +1380,18 @@ class MoELayerPadded(MoELayer):
         super().__init__(w1, w2, k)
         self.capacity = capacity
 
-    def _alloc(self, T, dev, dt):
-        if self._T == (T, dt, str(dev)):
-            return
-        super()._alloc(T, dev, dt)
+    def _new(self, T, dev, dt) -> dict:
         E, k, d, h, C = self.E, self.k, self.d, self.h, self.capacity
         P = max(E * C, 1)   # capacity 0 drops everything; keep the buffers non-null
-        self.pad = dict(token_pos=torch.empty((T, k), dtype=torch.int32, device=dev),
-                        offsets=torch.empty(E + 1, dtype=torch.int32, device=dev))
-        self.x_perm = torch.empty((P, d), dtype=dt, device=dev)
-        self.ab = torch.empty((P, 2 * h), dtype=dt, device=dev)
-        self.hp = torch.empty((P, h), dtype=dt, device=dev)
-        self.y_perm = torch.empty((P, d), dtype=dt, device=dev)
-        self.grads = dict(dx=torch.empty((T, d), dtype=dt, device=dev),
-                          dlogits=torch.empty((T, E), dtype=torch.float32, device=dev),
-                          dw1=torch.empty((E, 2 * h, d), dtype=torch.float32, device=dev),
-                          dw2=torch.empty((E, d, h), dtype=torch.float32, device=dev),
-                          dgate=torch.empty((T, k), dtype=torch.float32, device=dev),
-                          dy_perm=torch.empty((P, d), dtype=dt, device=dev),
-                          dab=torch.empty((P, 2 * h), dtype=dt, device=dev),
-                          dx_perm=torch.empty((P, d), dtype=dt, device=dev))
+        e = lambda *shape, dtype=dt: torch.empty(shape, dtype=dtype, device=dev)
+        f32 = torch.float32
+        return dict(super()._new(T, dev, dt), pad=dict(token_pos=e(T, k, dtype=torch.int32),
+                                                       offsets=e(E + 1, dtype=torch.int32)),
+                    x_perm=e(P, d), ab=e(P, 2 * h), hp=e(P, h), y_perm=e(P, d),
+                    pad_grads=dict(dx=e(T, d), dlogits=e(T, E, dtype=f32),
+                                   dw1=e(E, 2 * h, d, dtype=f32), dw2=e(E, d, h, dtype=f32),
+                                   dgate=e(T, k, dtype=f32), dy_perm=e(P, d), dab=e(P, 2 * h),
+                                   dx_perm=e(P, d)))
 
     def forward(self, x: torch.Tensor, logits: torch.Tensor) -> torch.Tensor:
         self._check_input(x, logits)
@@ -1394,6 +1407,7 @@ class MoELayerPadded(MoELayer):
                          MOE_EPI_SWIGLU_FWD, N=2 * self.h, K=d, aux_out=self.hp)
         moe_grouped_gemm(MOE_GG_FWD, self.hp, self.w2, self.y_perm, p["offsets"], N=d, K=self.h)
         moe_combine(self.y_perm, r["topk_gate"], p["token_pos"], self.out)
+        self._sizes.mark(self._T, x.get_device())
         return self.out
 
     def saved(self) -> dict:
@@ -1404,7 +1418,8 @@ class MoELayerPadded(MoELayer):
 
     def backward(self, dout: torch.Tensor, accumulate_dw: bool = False,
                  stage_events=None) -> dict:
-        moe_capacity_zero_rows(self.grads["dy_perm"], self.route["offsets"], self.capacity)
+        self._buf["grads"] = self.pad_grads
+        moe_capacity_zero_rows(self.pad_grads["dy_perm"], self.route["offsets"], self.capacity)
         return super().backward(dout, accumulate_dw, stage_events)
 
 
@@ -1440,7 +1455,7 @@ class MoELayerMX:
         self.balance = _Balance(aux_alpha) if aux_alpha is not None else None
         self.lb_stats = None
         self.prepare_weights(w1_master, w2_master)
-        self._T = None
+        self._sizes, self._T = _Sizes(), None
 
     def prepare_weights(self, w1: torch.Tensor, w2: torch.Tensor):
         """Re-quantise the fp32 masters, once per optimizer step: each master
@@ -1455,50 +1470,47 @@ class MoELayerMX:
             w2.reshape(E * d, h), g2)
 
     def _alloc(self, T, dev):
-        key = (T, str(dev))
-        if self._T == key:
-            return
+        self._T, self._buf = _use_buffers(self, (T, str(dev)), lambda: self._new(T, dev))
+
+    def _new(self, T, dev) -> dict:
+        """The tensors of a size, by the names that they have in the object."""
         E, k, d, h = self.E, self.k, self.d, self.h
         R = T * k
         i32 = dict(dtype=torch.int32, device=dev)
         bf = dict(dtype=torch.bfloat16, device=dev)
         u8 = dict(dtype=torch.uint8, device=dev)
-        self.route = dict(topk_idx=torch.empty((T, k), **i32),
-                          topk_gate=torch.empty((T, k), dtype=torch.float32, device=dev),
-                          counts=torch.empty(E, **i32), offsets=torch.empty(E + 1, **i32),
-                          token_pos=torch.empty((T, k), **i32), sorted_token=torch.empty(R, **i32),
-                          sorted_slot=torch.empty(R, **i32), tile_offsets=torch.empty(E + 1, **i32))
-        self.route_ws = torch.empty(max(moe_route_workspace_size(T, E, k), 1), **u8)
+        route = dict(topk_idx=torch.empty((T, k), **i32),
+                     topk_gate=torch.empty((T, k), dtype=torch.float32, device=dev),
+                     counts=torch.empty(E, **i32), offsets=torch.empty(E + 1, **i32),
+                     token_pos=torch.empty((T, k), **i32), sorted_token=torch.empty(R, **i32),
+                     sorted_slot=torch.empty(R, **i32), tile_offsets=torch.empty(E + 1, **i32))
         # dispatch payload, A||B, H' and its MXFP8 copy: scratch when recomputing
         shared = lambda name, shape, dt: _scratch("mx_" + name, shape, dt, dev, self.scratch)
         tmp = (shared if self.recompute
                else (lambda name, shape, dt: torch.empty(shape, dtype=dt, device=dev)))
-        self.xq = tmp("xq", (T, d), torch.uint8)
-        self.xs = tmp("xs", (T, d // 32), torch.uint8)
-        self.xpq = tmp("xpq", (R, d), torch.uint8)
-        self.xps = tmp("xps", (R, d // 32), torch.uint8)
-        self.ab = (shared if self.act8 else tmp)("ab", (R, 2 * h), torch.bfloat16)
-        # H' and its GEMM2 operand are read in the forward only
-        self.hp = shared("hp", (R, h), torch.bfloat16)
-        self.hpq = shared("hpq", (R, h), torch.uint8)
-        self.hps = shared("hps", (R, h // 32), torch.uint8)
         # H' along rows per expert (GEMM2 wgrad's operand), written by GEMM1
         # with GEMM2's; held instead of bf16 H' (when recomputing, the backward
         # quantises the H' it recomputes and these are scratch)
         nb = mxfp8_col_blocks(R, E)
         if not self.recompute:
-            self.hpc = torch.empty(nb * 32 * h, **u8)
-            self.hpcs = torch.empty(nb * h, **u8)
+            hpc, hpcs = torch.empty(nb * 32 * h, **u8), torch.empty(nb * h, **u8)
         else:
-            self.hpc = shared("hpc", (nb * 32 * h,), torch.uint8)
-            self.hpcs = shared("hpcs", (nb * h,), torch.uint8)
-        self.y_perm = (shared("y_perm", (R, d), torch.bfloat16) if self.act8
-                       else torch.empty((R, d), **bf))
-        self.ckpt = _act8_buffers(R, d, h, dev) if self.act8 else None
-        self.out = torch.empty((T, d), **bf)
-        self.grads = None
-        self.bwd_ws = None
-        self._T = key
+            hpc = shared("hpc", (nb * 32 * h,), torch.uint8)
+            hpcs = shared("hpcs", (nb * h,), torch.uint8)
+        return dict(route=route,
+                    route_ws=torch.empty(max(moe_route_workspace_size(T, E, k), 1), **u8),
+                    xq=tmp("xq", (T, d), torch.uint8), xs=tmp("xs", (T, d // 32), torch.uint8),
+                    xpq=tmp("xpq", (R, d), torch.uint8),
+                    xps=tmp("xps", (R, d // 32), torch.uint8),
+                    ab=(shared if self.act8 else tmp)("ab", (R, 2 * h), torch.bfloat16),
+                    # H' and its GEMM2 operand are read in the forward only
+                    hp=shared("hp", (R, h), torch.bfloat16),
+                    hpq=shared("hpq", (R, h), torch.uint8),
+                    hps=shared("hps", (R, h // 32), torch.uint8), hpc=hpc, hpcs=hpcs,
+                    y_perm=(shared("y_perm", (R, d), torch.bfloat16) if self.act8
+                            else torch.empty((R, d), **bf)),
+                    ckpt=_act8_buffers(R, d, h, dev) if self.act8 else None,
+                    out=torch.empty((T, d), **bf))
 
     def hp_quantised_in_gemm1(self) -> bool:
         """The forward's GEMM1 stores H' in both MXFP8 layouts (the backward's
@@ -1530,7 +1542,7 @@ class MoELayerMX:
         self.x = x
         r = moe_route(logits, self.k, out=self.route, ws=self.route_ws)
         if self.balance is not None:
-            self.lb_stats = self.balance.forward(logits, r["counts"], self.k)
+            self.lb_stats = self.balance.forward(logits, r["counts"], self.k, self._buf)
         fused = self.hp_quantised_in_gemm1()
         self._gemm1(x, r["offsets"], r["token_pos"], quantised_hp=fused)
         if self.act8:
@@ -1544,6 +1556,7 @@ class MoELayerMX:
                              self.ckpt["y8"], self.ckpt["y8_scale"])
         else:
             moe_combine(self.y_perm, r["topk_gate"], r["token_pos"], self.out)
+        self._sizes.mark(self._T, x.get_device())
         return self.out if self.out_norm is None else self.out_norm.forward(self.out)
 
     def quantize_hp(self, offsets):
@@ -1587,11 +1600,12 @@ class MoELayerMX:
         dout = _norm_backward(self.out_norm, dout, accumulate_dw)
         if self.recompute:
             self._gemm1(self.x, self.route["offsets"], self.route["token_pos"])
-        self.grads = moe_backward(self.saved(), dout, self.E, self.k, self.d, self.h,
-                                  out=self.grads, mxfp8=True, accumulate_dw=accumulate_dw,
-                                  stage_events=stage_events, act8=self.ckpt)
+        self.grads = self._buf["grads"] = moe_backward(
+            self.saved(), dout, self.E, self.k, self.d, self.h, out=self._buf.get("grads"),
+            mxfp8=True, accumulate_dw=accumulate_dw, stage_events=stage_events, act8=self.ckpt)
         if self.balance is not None:
             self.balance.backward(self.grads["dlogits"])
+        self._sizes.mark(self._T, dout.get_device())
         return _norm_grads(self.out_norm, self.grads)
 
 
@@ -1634,6 +1648,7 @@ class MoELayerW4:
         buf = self._sizes.at(key)
         with torch.cuda.device(gpu):
             if not buf:
+                self.route = self.out = None
                 u8 = lambda n: torch.empty(n, dtype=torch.uint8, device=dev)
                 wsb = moe_w4_experts_workspace_size(T, self.k, self.d, self.h)
                 buf.update(route=None, out=torch.empty((T, self.d), dtype=x.dtype, device=dev),

@@ -202,3 +202,76 @@ def test_w4_weights_of_other_sizes_are_refused(on_cpu, monkeypatch, s1, s2):
     with pytest.raises(ValueError):
         layer.prepare_weights(torch.ones(s1), torch.ones(s2))
     assert not written
+
+
+def _layer(kind):
+    w = torch.zeros(E, 2 * H, D), torch.zeros(E, D, H)
+    if kind == "padded":
+        return moe.MoELayerPadded(*w, K, 8)
+    opts = dict(aux_alpha=0.1, scratch={}, **({kind.split()[1]: True} if " " in kind else {}))
+    return (moe.MoELayerMX if kind.startswith("mxfp8") else moe.MoELayer)(*w, K, **opts)
+
+
+def _layer_step(layer, T, kind):
+    x = torch.zeros(T, D, dtype=torch.bfloat16 if kind.startswith("mxfp8") else torch.float32)
+    layer.forward(x, torch.zeros(T, E))
+    layer.backward(x)
+    own = {n: v for n, v in layer._buf["tensors"].items()}
+    assert all(getattr(layer, n) is v for n, v in own.items())
+    return [t.data_ptr() for t in moe._tensors(dict(layer._buf, grads=layer.grads))]
+
+
+KINDS = ["plain", "plain act8", "plain recompute", "mxfp8", "mxfp8 act8", "mxfp8 recompute", "padded"]
+
+
+@pytest.fixture
+def layers_on_cpu(on_cpu, monkeypatch):
+    """on_cpu for the layers with a backward."""
+    monkeypatch.setattr(moe.MoELayer, "_check_input", lambda self, x, logits: None)
+    for name in ("_act8_need", "_need_bytes", "moe_grouped_gemm", "moe_permute", "mxfp8_quantize"):
+        monkeypatch.setattr(moe, name, lambda *args, **kw: None)
+    monkeypatch.setattr(moe, "_p", lambda t: None)
+    return on_cpu
+
+
+@pytest.mark.parametrize("kind", KINDS)
+def test_layers_keep_the_buffers_of_captured_sizes(layers_on_cpu, monkeypatch, kind):
+    monkeypatch.setattr(moe, "_KEPT_BYTES", 0)
+    layer, at = _layer(kind), {}
+    for T in (96, 64):
+        _layer_step(layer, T, kind)
+        layers_on_cpu[0] = True
+        at[T] = _layer_step(layer, T, kind)
+        layers_on_cpu[0] = False
+    for T in (128, 160):                                   # larger: the balancing loss's workspace too
+        _layer_step(layer, T, kind)
+        assert len(layer._sizes._all) == 3                 # of the others the last alone
+    assert at == {T: _layer_step(layer, T, kind) for T in at}
+
+
+@pytest.mark.parametrize("kind", KINDS)
+def test_layers_add_to_gradients_of_one_size_only(layers_on_cpu, kind):
+    layer = _layer(kind)
+    x = {T: torch.zeros(T, D, dtype=torch.bfloat16 if kind.startswith("mxfp8") else torch.float32)
+         for T in (64, 96)}
+    forward = lambda T: layer.forward(x[T], torch.zeros(T, E))
+    for T in (64, 96, 64):
+        forward(T)
+        with pytest.raises(ValueError, match="earlier backward"):
+            layer.backward(x[T], accumulate_dw=True)
+        layer.backward(x[T])
+        forward(T)
+        layer.backward(x[T], accumulate_dw=True)
+
+
+def test_no_old_buffer_is_held_while_new_ones_are_made(layers_on_cpu, monkeypatch):
+    """A call with another size has freed the last one's tensors before it allocates."""
+    monkeypatch.setattr(moe, "_KEPT_BYTES", 0)
+    import weakref
+    layer = moe.MoELayer(torch.zeros(E, 2 * H, D), torch.zeros(E, D, H), K)
+    _layer_step(layer, 64, "plain")
+    old = [weakref.ref(t) for t in moe._tensors(layer._buf)]
+    new, seen = layer._new, []
+    monkeypatch.setattr(layer, "_new", lambda *a: seen.append([r() is None for r in old]) or new(*a))
+    layer.forward(torch.zeros(96, D), torch.zeros(96, E))
+    assert len(seen) == 1 and all(seen[0])

@@ -106,3 +106,36 @@ def test_w4_weights_change_between_replays():
         del tensors
         seen.append(got.clone())
     assert torch.equal(seen[0], seen[3]) and not torch.equal(seen[0], seen[1])
+
+
+@pytest.mark.parametrize("kind", ["bf16", "bf16 act8", "bf16 recompute", "mxfp8", "mxfp8 act8", "padded"])
+def test_layers_at_several_sizes(monkeypatch, kind):
+    """Forward and backward of the layers, with the balancing loss, one graph
+    for each micro-batch size."""
+    monkeypatch.setattr(moe, "_KEPT_BYTES", 0)
+    mx = kind.startswith("mxfp8")
+    w1, w2 = (dev(n(s, 2, 0.05), torch.float32 if mx else torch.bfloat16)
+              for s in ((E, 2 * H, D), (E, D, H)))
+    opt = {kind.split()[1]: True} if " " in kind else {}
+
+    def make():
+        if kind == "padded":
+            return moe.MoELayerPadded(w1, w2, K, 48)
+        norm = moe.LayerNorm(torch.ones(D, device="cuda"), None)
+        return (moe.MoELayerMX if mx else moe.MoELayer)(w1, w2, K, aux_alpha=0.01, scratch={},
+                                                        out_norm=norm, **opt)
+
+    layer, eager = make(), make()
+    wr = dev(n((E, D), 4, 0.2), torch.float32)
+
+    def step(lay, x):
+        out = lay.forward(x, x.float() @ wr.t())
+        g = lay.backward(x)
+        return (out, *(v for v in g.values() if v is not None and v.dtype == torch.float32), g["dx"])
+
+    inputs = [dev(n((T, D), 5, 1.0), torch.bfloat16) for T in (40, 96)]
+    graphs = [_capture(lambda: step(layer, x)) for x in inputs]
+    other = dev(n((256, D), 6, 1.0), torch.bfloat16)
+    step(layer, other)
+    _replays(graphs, inputs, [lambda x=x: step(eager, x) for x in inputs],
+             lambda i: step(layer, other[:256 - i]))
