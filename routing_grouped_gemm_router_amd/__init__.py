@@ -1454,20 +1454,27 @@ class MoELayerMX:
         self.fuse_hp = True
         self.balance = _Balance(aux_alpha) if aux_alpha is not None else None
         self.lb_stats = None
+        self.w1q = self.w2q = None
         self.prepare_weights(w1_master, w2_master)
         self._sizes, self._T = _Sizes(), None
 
     def prepare_weights(self, w1: torch.Tensor, w2: torch.Tensor):
         """Re-quantise the fp32 masters, once per optimizer step: each master
-        is read once and written in both orientations (mxfp8_quantize_both)."""
+        is read once and written in both orientations (mxfp8_quantize_both).
+        Again into the same tensors, so that the replays of a captured step
+        take the new weights (masters on another GPU get tensors there)."""
         E, d, h = self.E, self.d, self.h
         dev = w1.device
+        w1, w2 = w1.reshape(E * 2 * h, d), w2.reshape(E * d, h)
+        old = self.w1q is not None and self.w1q.device == dev
         g1 = torch.arange(0, E + 1, dtype=torch.int32, device=dev) * (2 * h)
         g2 = torch.arange(0, E + 1, dtype=torch.int32, device=dev) * d
         (self.w1q, self.w1s), (self.w1t, self.w1ts) = mxfp8_quantize_both(
-            w1.reshape(E * 2 * h, d), g1)
+            w1, g1,
+            out=(self.w1q, self.w1s, self.w1t, self.w1ts) if old else None)
         (self.w2q, self.w2s), (self.w2t, self.w2ts) = mxfp8_quantize_both(
-            w2.reshape(E * d, h), g2)
+            w2, g2,
+            out=(self.w2q, self.w2s, self.w2t, self.w2ts) if old else None)
 
     def _alloc(self, T, dev):
         self._T, self._buf = _use_buffers(self, (T, str(dev)), lambda: self._new(T, dev))

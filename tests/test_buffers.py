@@ -275,3 +275,17 @@ def test_no_old_buffer_is_held_while_new_ones_are_made(layers_on_cpu, monkeypatc
     monkeypatch.setattr(layer, "_new", lambda *a: seen.append([r() is None for r in old]) or new(*a))
     layer.forward(torch.zeros(96, D), torch.zeros(96, E))
     assert len(seen) == 1 and all(seen[0])
+
+
+def test_mxfp8_weights_stay_in_their_tensors(layers_on_cpu):
+    layer = _layer("mxfp8")
+    at = lambda: [getattr(layer, n).data_ptr() for n in ("w1q", "w1s", "w1t", "w1ts", "w2q", "w2s",
+                                                         "w2t", "w2ts")]
+    first = at()
+    layer.prepare_weights(torch.ones(E, 2 * H, D), torch.ones(E, D, H))
+    assert at() == first
+    layer.prepare_weights(torch.ones(E * 2 * H, D), torch.ones(E * D, H))
+    assert at() == first
+    for s1, s2 in (((E, 2 * H, 2 * D), (E, 2 * D, H)), ((E, 2 * H, D), (E, D, 2 * H))):
+        with pytest.raises(RuntimeError):
+            layer.prepare_weights(torch.ones(s1), torch.ones(s2))

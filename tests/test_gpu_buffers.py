@@ -139,3 +139,27 @@ def test_layers_at_several_sizes(monkeypatch, kind):
     step(layer, other)
     _replays(graphs, inputs, [lambda x=x: step(eager, x) for x in inputs],
              lambda i: step(layer, other[:256 - i]))
+
+
+def test_mxfp8_weights_change_between_replays():
+    """A captured training step takes the weights that were quantised last."""
+    w = [[dev(n(s, 2 + i, 0.05), torch.float32) for s in ((E, 2 * H, D), (E, D, H))] for i in range(2)]
+    layer = moe.MoELayerMX(*w[0], K, scratch={})
+    x, lg = dev(n((70, D), 5, 1.0), torch.bfloat16), dev(n((70, E), 6, 1.0), torch.float32)
+    names = ("dx", "dw1", "dw2", "dlogits")
+
+    def step(lay):
+        out = lay.forward(x, lg)
+        g = lay.backward(x)
+        return [out, *(g[k] for k in names)]
+
+    graph, got = _capture(lambda: step(layer))
+    for i in (1, 0, 1):
+        layer.prepare_weights(*w[i])
+        tensors, untouched = _fill(i + 1)
+        graph.replay()
+        torch.cuda.synchronize()
+        for a, b in zip(got, step(moe.MoELayerMX(*w[i], K, scratch={}))):
+            assert torch.equal(a, b), i
+        assert untouched(), i
+        del tensors
