@@ -305,7 +305,9 @@ union W4Lds {
     float red[4][2][256];
 };
 
-// N results of row `row`, columns from n: h as its two halves, or y.
+// N results of row `row`, columns from n: h as its two halves, or y. The upper
+// half of an h beyond bf16's largest value (0x7f7f) is that value, so that the
+// rest is finite where h is and the infinity where h is infinite.
 template <bool UP, int N>
 MOE_DEV void w4_store(const W4Args &p, int64_t row, int n, const float *v0, const float *v1) {
     if constexpr (UP) {
@@ -314,7 +316,8 @@ MOE_DEV void w4_store(const W4Args &p, int64_t row, int n, const float *v0, cons
         for (int q = 0; q < N; q++) {
             const float a = v0[q], e = expf(-0.5f * fabsf(a));
             const float o = (a < 0.f ? (a * e) * e : a) / fmaf(e, e, 1.f) * v1[q];
-            hi[q] = f32_to_bf16(o);
+            const float top = bf16_to_f32(0x7f7f);
+            hi[q] = f32_to_bf16(__builtin_amdgcn_fmed3f(o, -top, top));
             lo[q] = f32_to_bf16(o - bf16_to_f32(hi[q]));
         }
         __builtin_memcpy(p.hi_out + row * p.h + n, hi, sizeof(hi));
