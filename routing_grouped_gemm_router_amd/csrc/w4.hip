@@ -418,7 +418,8 @@ struct W4Wide {
 };
 
 // A wave's weights of a piece. Blocks past the row's end repeat its last one
-// (no branch around a load) and count as zeros when they are used.
+// (no branch around a load), with scale byte 0; they meet tokens that are zero
+// there. It is the tokens that have to be: they may hold infinities.
 template <int PS>
 struct W4Piece {
     u32x4 w[PS / 2][2][2];                        // row 8 q + lane / 8
@@ -483,7 +484,9 @@ MOE_DEV void w4_rows_wide(const W4Args &p, const W4Tiles &wt, int n0, bool store
 #pragma unroll
                 for (int q = 0; q < P; q++)
 #pragma unroll
-                    for (int j = 0; j < PS; j++) lds.x[q][t][(16 * PS + 1) * xt + 16 * j + xc] = xr[q][t][j];
+                    for (int j = 0; j < PS; j++)
+                        lds.x[q][t][(16 * PS + 1) * xt + 16 * j + xc] =
+                            16 * PS * piece + 16 * j + xc < 4 * nblk ? xr[q][t][j] : zero;
             }
         if (piece + 1 < pieces) {
             load_x(piece + 1);
@@ -494,12 +497,11 @@ MOE_DEV void w4_rows_wide(const W4Args &p, const W4Tiles &wt, int n0, bool store
 #pragma unroll
         for (int v = 0; v < PS / 2; v++) {
             w4_lds_order();                       // the steps before have been read
-            const bool in = b0 + 8 * v + (lane & 7) < nblk;
 #pragma unroll
             for (int z = 0; z < 2; z++) {
 #pragma unroll
                 for (int q = 0; q < 2; q++)
-                    lds.w[wave][z][9 * (8 * q + (lane >> 3)) + (lane & 7)] = in ? now.w[v][q][z] : zero;
+                    lds.w[wave][z][9 * (8 * q + (lane >> 3)) + (lane & 7)] = now.w[v][q][z];
                 if (v == 0) {
                     const int past = b0 + PS * (lane & 3) - (nblk - PS);     // bytes read too early
                     const uint32_t b = past <= 0 ? now.sc[z] : past < PS ? (uint32_t)now.sc[z] >> (8 * past) : 0;

@@ -1,5 +1,5 @@
 """The 4-bit products at the ends of the number range, through each of their
-kernels: H' beyond bf16's largest value, infinities in it, the first and the last
+kernels: H' beyond bf16's largest value, infinities, the first and the last
 scale bytes; and the quantisation there."""
 import numpy as np
 import pytest
@@ -60,7 +60,7 @@ def _check(out, x, r, w):
 
 
 @pytest.mark.parametrize("T,d,h,E,k", KERNELS)
-@pytest.mark.parametrize("last", [False])
+@pytest.mark.parametrize("last", [False, True])
 def test_hidden_beyond_bf16(T, d, h, E, k, last):
     """H' = (2^8 - 1)(2^8 + 1) 2^112 = 2^128 - 2^112 is finite in fp32 and rounds
     to infinity in bf16; in another token it is infinite in fp32 too. The hidden
@@ -86,6 +86,28 @@ def test_hidden_beyond_bf16(T, d, h, E, k, last):
     _check(out, x, r, w)
     over = x.clone()
     over[t, at[0]] = 2.0 ** 20
+    got = moe.moe_w4_experts(over, r, *args)
+    assert (got[t] == float("inf")).all()
+    rest = torch.arange(T, device="cuda") != t
+    assert torch.equal(got[rest], out[rest])
+
+
+@pytest.mark.parametrize("T,d,h,E,k", KERNELS)
+@pytest.mark.parametrize("last", [False, True])
+def test_infinite_input(T, d, h, E, k, last):
+    """An infinity in x, met by positive weights alone: infinite a, b, H' and
+    out, no NaN from the places past a row's end."""
+    w = Weights(d, h, E, T + d, 120, 120)
+    c = d - 1 if last else 0
+    w.c1[:, c] = 1 + w.c1[:, c] % 7
+    w.c2[:] = 1 + w.c2 % 7
+    x = dev(synth.normal((T, d), 5, 1, 1.0), torch.bfloat16)
+    r = _route(T, E, k)
+    args = w.cuda()
+    out = moe.moe_w4_experts(x, r, *args)
+    _check(out, x, r, w)
+    over, t = x.clone(), T // 2
+    over[t, c] = float("inf")
     got = moe.moe_w4_experts(over, r, *args)
     assert (got[t] == float("inf")).all()
     rest = torch.arange(T, device="cuda") != t
