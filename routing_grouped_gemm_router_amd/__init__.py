@@ -1021,12 +1021,16 @@ def _tensors(v):
     return [v] if isinstance(v, torch.Tensor) else []
 
 
+_cur_capturing = getattr(torch._C, "_cuda_isCurrentStreamCapturing", None) or (
+    torch.cuda.is_current_stream_capturing)
+
+
 def _capturing(index: int) -> bool:
     """Whether GPU `index`'s current stream is being captured into a graph."""
     if _cur_device() == index:
-        return torch.cuda.is_current_stream_capturing()
+        return _cur_capturing()
     with torch.cuda.device(index):
-        return torch.cuda.is_current_stream_capturing()
+        return _cur_capturing()
 
 
 # Bytes of buffers that a layer object keeps for sizes it was called with
@@ -1044,7 +1048,7 @@ class _Sizes:
     _KEPT_BYTES at most together."""
 
     def __init__(self):
-        self._all, self._bytes, self._captured, self._last = {}, {}, set(), None
+        self._all, self._bytes, self._last = {}, {}, None
 
     def at(self, key) -> dict:
         """The dict of this size, the caller's to fill."""
@@ -1055,17 +1059,18 @@ class _Sizes:
             self._all[key] = self._all.pop(key, {})         # last used last
             room = _KEPT_BYTES
             for k in list(self._all)[-2::-1]:
-                if k not in self._captured:
+                if "captured" not in self._all[k]:
                     if 0 < self._bytes[k] <= room:
                         room -= self._bytes[k]
                     else:
                         del self._all[k]
         return self._all[key]
 
-    def mark(self, key, index):
-        """To be called whenever kernels that use the dict were enqueued."""
-        if key not in self._captured and _capturing(index):
-            self._captured.add(key)
+
+def _mark(buf, index):
+    """To be called when kernels that use a size's dict have been enqueued."""
+    if "captured" not in buf and _capturing(index):
+        buf["captured"] = True
 
 
 MOE_LB_NSTATS = 8
@@ -1146,10 +1151,11 @@ class LayerNorm:
         key = (x.shape, x.dtype, x.device, residual is None)
         if self._key != key:
             self._out = self.grads = self._key = None
-        buf = self._sizes.at(key)
+            self._buf = self._sizes.at(key)
+        buf = self._buf
         self._out = buf["out"] = moe_layer_norm(x, self.weight, self.bias, self.eps, residual,
                                                 self.act8, out=buf.get("out"))
-        self._sizes.mark(key, x.get_device())
+        _mark(buf, x.get_device())
         self._key = key
         self.sum = self._out.get("sum")
         self._x = None if self.act8 else (x if residual is None else self.sum)
@@ -1163,14 +1169,15 @@ class LayerNorm:
             raise ValueError("backward without a forward")
         if accumulate_dw and self.grads is None:
             raise ValueError("accumulate_dw needs the gradients of an earlier backward")
-        buf, y = self._sizes.at(self._key), self._out["y"]
+        buf = self._buf
         if "ws" not in buf:
+            y = self._out["y"]
             wsb = moe_layer_norm_backward_workspace_size(_dt(y), *y.shape)
             buf["ws"] = torch.empty(max(wsb, 16), dtype=torch.uint8, device=y.device)
         self.grads = buf["grads"] = moe_layer_norm_backward(
             dict(self._out, x=self._x), dy, self.weight, dsum, out=buf.get("grads"),
             accumulate_dw=accumulate_dw, want_dbias=self.bias is not None, ws=buf["ws"])
-        self._sizes.mark(self._key, y.get_device())
+        _mark(buf, dy.get_device())
         return self.grads
 
     def held_bytes(self) -> int:
@@ -1323,7 +1330,7 @@ class MoELayer:
                              self.ckpt["y8"], self.ckpt["y8_scale"])
         else:
             moe_combine(self.y_perm, r["topk_gate"], r["token_pos"], self.out)
-        self._sizes.mark(self._T, x.get_device())
+        _mark(self._buf, x.get_device())
         return self.out if self.out_norm is None else self.out_norm.forward(self.out)
 
     def saved(self) -> dict:
@@ -1364,7 +1371,7 @@ class MoELayer:
             accumulate_dw=accumulate_dw, stage_events=stage_events, act8=self.ckpt)
         if self.balance is not None:
             self.balance.backward(self.grads["dlogits"])
-        self._sizes.mark(self._T, dout.get_device())
+        _mark(self._buf, dout.get_device())
         return _norm_grads(self.out_norm, self.grads)
 
 
@@ -1407,7 +1414,7 @@ class MoELayerPadded(MoELayer):
                          MOE_EPI_SWIGLU_FWD, N=2 * self.h, K=d, aux_out=self.hp)
         moe_grouped_gemm(MOE_GG_FWD, self.hp, self.w2, self.y_perm, p["offsets"], N=d, K=self.h)
         moe_combine(self.y_perm, r["topk_gate"], p["token_pos"], self.out)
-        self._sizes.mark(self._T, x.get_device())
+        _mark(self._buf, x.get_device())
         return self.out
 
     def saved(self) -> dict:
@@ -1563,7 +1570,7 @@ class MoELayerMX:
                              self.ckpt["y8"], self.ckpt["y8_scale"])
         else:
             moe_combine(self.y_perm, r["topk_gate"], r["token_pos"], self.out)
-        self._sizes.mark(self._T, x.get_device())
+        _mark(self._buf, x.get_device())
         return self.out if self.out_norm is None else self.out_norm.forward(self.out)
 
     def quantize_hp(self, offsets):
@@ -1612,7 +1619,7 @@ class MoELayerMX:
             mxfp8=True, accumulate_dw=accumulate_dw, stage_events=stage_events, act8=self.ckpt)
         if self.balance is not None:
             self.balance.backward(self.grads["dlogits"])
-        self._sizes.mark(self._T, dout.get_device())
+        _mark(self._buf, dout.get_device())
         return _norm_grads(self.out_norm, self.grads)
 
 
@@ -1631,7 +1638,7 @@ class MoELayerW4:
         self.h, self.k = h2 // 2, k
         self.w1q = self.w1s = self.w2q = self.w2s = None
         self.prepare_weights(w1, w2)
-        self._sizes = _Sizes()
+        self._sizes, self._T = _Sizes(), None
 
     def prepare_weights(self, w1: torch.Tensor, w2: torch.Tensor):
         """Quantise the weights, again after they have changed: into the same
@@ -1651,10 +1658,11 @@ class MoELayerW4:
         T, dev, gpu = x.shape[0], self.w1q.device, self.w1q.get_device()
         _need_on(x, (T, self.d), torch.bfloat16, gpu, "x")
         _need_on(logits, (T, self.E), torch.float32, gpu, "logits")
-        key = (T, dev)
-        buf = self._sizes.at(key)
+        if self._T != (T, gpu):
+            self._buf, self._T = self._sizes.at((T, gpu)), (T, gpu)
+        buf = self._buf
         with torch.cuda.device(gpu):
-            if not buf:
+            if "out" not in buf:
                 self.route = self.out = None
                 u8 = lambda n: torch.empty(n, dtype=torch.uint8, device=dev)
                 wsb = moe_w4_experts_workspace_size(T, self.k, self.d, self.h)
@@ -1665,5 +1673,5 @@ class MoELayerW4:
                                                   ws=buf["route_ws"])
         self.out = moe_w4_experts(x, self.route, self.w1q, self.w1s, self.w2q, self.w2s,
                                   buf["out"], buf["ws"])
-        self._sizes.mark(key, gpu)
+        _mark(buf, gpu)
         return self.out

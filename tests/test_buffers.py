@@ -25,11 +25,11 @@ def test_a_captured_size_stays(capture):
     for key in (1, 2):
         at[key] = fill(key, big)
         capture[0] = True
-        s.mark(key, 0)
+        moe._mark(s.at(key), 0)
         capture[0] = False
     for key in range(3, 9):
         fill(key, big)
-        s.mark(key, 0)
+        moe._mark(s.at(key), 0)
         assert set(s._all) == {1, 2, key}                  # and of the others the last alone
     assert fill(1, big) == at[1] and fill(2, big) == at[2]
 
@@ -109,7 +109,7 @@ def test_w4_layer_keeps_its_buffers(on_cpu):
     for T in (300002, 300003, 1):
         _w4_step(layer, T)
     assert big == {T: _w4_step(layer, T) for T in big}
-    assert (300002, layer.w1q.device) not in layer._sizes._all
+    assert (300002, layer.w1q.get_device()) not in layer._sizes._all
 
 
 def test_norm_keeps_its_buffers(on_cpu):
@@ -174,7 +174,7 @@ def test_capture_is_asked_of_the_buffers_gpu(monkeypatch):
 
     monkeypatch.setattr(moe, "_cur_device", lambda: current[0])
     monkeypatch.setattr(torch.cuda, "device", Device)
-    monkeypatch.setattr(torch.cuda, "is_current_stream_capturing",
+    monkeypatch.setattr(moe, "_cur_capturing",
                         lambda: seen.append(current[0]) or current[0] == 0)
     assert moe._capturing(0) and not moe._capturing(1) and seen == [0, 1] and current == [1]
 
