@@ -147,4 +147,12 @@ MOE_DEV void act8_decode(const uint2 &q, float step, float *f) {
 }
 MOE_DEV void act8_decode(const uint32_t &q, float step, float *f) { act8_decode4(q, step, f); }
 
+// silu(a) = a sigmoid(a), from E = exp(-|a| / 2): E^2 / (1 + E^2) for a < 0,
+// 1 / (1 + E^2) otherwise. exp(-a) itself would overflow below a = -88 and
+// lose the product a exp(a) where it is still a normal number.
+MOE_DEV float silu(float a) {
+    const float e = expf(-0.5f * fabsf(a));
+    return (a < 0.f ? (a * e) * e : a) / fmaf(e, e, 1.f);
+}
+
 }  // namespace moe

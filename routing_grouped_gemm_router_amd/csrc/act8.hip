@@ -60,14 +60,6 @@ __global__ __launch_bounds__(256) void act8_load_vecs(const typename Codes<BF16>
     out[v] = R::pack(f);
 }
 
-// silu(a) = a sigmoid(a), from E = exp(-|a| / 2): E^2 / (1 + E^2) for a < 0,
-// 1 / (1 + E^2) otherwise. exp(-a) itself would overflow below a = -88 and
-// lose the product a exp(a) where it is still a normal number.
-MOE_DEV float silu(float a) {
-    const float e = expf(-0.5f * fabsf(a));
-    return (a < 0.f ? (a * e) * e : a) / fmaf(e, e, 1.f);
-}
-
 // A||B and H' = silu(a) b from the checkpoint of A||B [rows, 2h]; hv = vectors
 // of h. 65536 x 2048 bf16: 541 MB in 90 us, 6.0 TB/s.
 template <bool BF16>

@@ -314,8 +314,7 @@ MOE_DEV void w4_store(const W4Args &p, int64_t row, int n, const float *v0, cons
         uint16_t hi[N], lo[N];
 #pragma unroll
         for (int q = 0; q < N; q++) {
-            const float a = v0[q], e = expf(-0.5f * fabsf(a));
-            const float o = (a < 0.f ? (a * e) * e : a) / fmaf(e, e, 1.f) * v1[q];
+            const float o = silu(v0[q]) * v1[q];
             const float top = bf16_to_f32(0x7f7f);
             hi[q] = f32_to_bf16(__builtin_amdgcn_fmed3f(o, -top, top));
             lo[q] = f32_to_bf16(o - bf16_to_f32(hi[q]));
