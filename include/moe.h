@@ -649,11 +649,19 @@ moe_status moe_w4_quantize(const void *in, moe_dtype in_dt, int64_t rows, int64_
 
 /* The expert layer's forward after the routing, for the few tokens of a
  * generation step (an expert's weights are read once for every 8 of its rows,
- * or 32 with many: with hundreds of rows an expert moe_grouped_gemm is the
- * faster way), with W1, W2 in 4 bits:
+ * or 32 with many), with W1, W2 in 4 bits:
  *   H' = silu(a) b with a, b = W1[e] x[t],  out[t] = sum_j g[t, j] W2[e_j] H'
- * x, out [T, d] bf16; accumulation, H' (to 16 significant bits) and the
- * experts' outputs stay wider than bf16 until out is rounded. topk_gate,
+ * x, out [T, d] bf16; accumulation, H' (to 16 significant bits, over fp32's
+ * whole range) and the experts' outputs stay wider than bf16 until out is
+ * rounded. A token with infinities or NaNs reaches no other.
+ * With many rows an expert the grouped GEMMs are the faster way. us for
+ * everything after the routing, here / in MXFP8 / in bf16, by rows an expert:
+ *   E = 128, k = 4, d = 2048, h = 1024: 32 rows 205 / 224 / 382, 64 rows 337 /
+ *     240 / 405, 128 rows 579 / 320 / 476
+ *   E = 8, k = 2, d = 2048, h = 1024: 128 rows 52 / 58 / 59, 256 rows 99 / 61 / 64
+ *   E = 2, k = 2, d = 8192, h = 4096: 128 rows 120 / 142 / 214, 512 rows 424 /
+ *     421 / 720
+ * topk_gate,
  * token_pos, sorted_token and offsets are moe_route's for the T tokens
  * (token_pos < 0: that slot adds nothing). w1q [E, 2h, d/2], w1_scale [E, 2h,
  * d/32], w2q [E, d, h/2], w2_scale [E, d, h/32] as moe_w4_quantize writes

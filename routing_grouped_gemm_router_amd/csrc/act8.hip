@@ -330,8 +330,11 @@ moe_status act8_swiglu_launch(const uint8_t *q, const uint8_t *scale, moe_dtype 
 //    against 1498; T = 512: 24 against 31; d = 2048: 445 against 360);
 //  - backward, whose sums cross the waves: a workgroup of 256 from 256 vectors if
 //    each thread has four or more (d = 4096: 706 against 748; d = 2048, k = 1: 60
-//    against 55), or from 128 where the waves of the tokens alone do not fill the
-//    chip (T = 512, d = 2048: 8.3 against 10.9; d = 16384: 40 against 63).
+//    against 55; at the border, T = 16384, d = 2048, k = 4: 94.5 against 102, with
+//    its forward 189 against 197; fp32 d = 1024: 83 against 93; below it, k = 2:
+//    56 against 59, and d = 1024, k = 8: 118 against 95), or from 128 where the
+//    waves of the tokens alone do not fill the chip (T = 512, d = 2048: 8.3 against
+//    10.9; d = 16384: 40 against 63).
 static int combine_group(int nv, int64_t T, int k, bool backward) {
     if (nv <= 16 || (nv <= 32 && T >= 16384)) return 16;
     if (!backward) return nv >= 1024 ? 1024 : nv >= 128 ? 256 : 64;

@@ -433,8 +433,12 @@ moe_status norm_fwd_launch(const void *x, moe_dtype dt, const void *res, const f
 
 // Workgroups of the backward, and rows of its partial sums: by the sizes
 // alone, so that the workspace is the same on every device. Two a compute
-// unit, but the partial sums (8 bytes a column, written and read back) stay
-// an eighth of the rows' bytes, while there is one a compute unit.
+// unit, but no more than an eighth of the rows, while there is one a compute
+// unit: the partial sums are 8 bytes a column, written and read back, so T / 8
+// workgroups move 2 T d bytes beside a bf16 backward's 6 T d (a third, from
+// 2048 to 4096 rows; from a checkpoint two fifths). More rows make that less,
+// as 1 / T; below 2048 rows the 256 workgroups' part is the larger the fewer
+// rows there are.
 static int64_t norm_bwd_blocks(int64_t T, int nv) {
     const int g = norm_group(nv, true), rpb = norm_threads(g) / g;
     const int64_t most = (T + rpb - 1) / rpb, few = most < 256 ? most : 256;
