@@ -7,14 +7,14 @@
 // bits they take 33/64 of their bf16 size and nothing is computed twice but
 // H' = silu(a) b, which follows from A||B. At T = 16384, d = 2048, h = 1024, E =
 // 128, k = 4 in bf16 a layer holds 265 MiB instead of 897 and its forward plus
-// backward takes 3.82 ms instead of 3.60 (recomputing holds 257 MiB and takes
-// 4.30 ms).
+// backward takes 3.91 ms instead of 3.69 (recomputing holds 257 MiB and takes
+// 4.40 ms).
 //
 // All kernels are bound by memory: each reads its inputs once and writes its
 // outputs once, at a large copy's rate (4.7 to 5.2 TB/s here) or above it.
 // What is read or written once and not soon again goes past the last-level
-// cache (load_once, store_once): store 77 -> 67 us for 65536 rows of 2048 bf16
-// (407 MB, 6.1 TB/s), combine with its checkpoint 125 -> 91 us. dy_perm is
+// cache (load_once, store_once): store 77 -> 68 us for 65536 rows of 2048 bf16
+// (407 MB, 6.0 TB/s), combine with its checkpoint 125 -> 95 us. dy_perm is
 // stored in the ordinary way: the GEMM that reads it comes next, and a layer's
 // step gains nothing by the other (3.85 ms both ways), though combine and
 // backward in turn would take 171 us instead of 177.
@@ -27,7 +27,7 @@ namespace moe {
 // 4096, k = 8 backward 1 14.1 us, 2 12.3)
 constexpr int kCombineU = 1, kCombineBwdU = 2;
 
-// store: q, scale = checkpoint of in, a vector a thread (65536 x 2048 bf16: 67 us).
+// store: q, scale = checkpoint of in, a vector a thread (65536 x 2048 bf16: 68 us).
 // Blocks of 32 lie in rows of a multiple
 // of 32, so the matrix is one run of blocks.
 template <bool BF16>
@@ -47,7 +47,7 @@ __global__ __launch_bounds__(256) void act8_store_vecs(const uint4 *__restrict__
     if (v % R::LPB == 0) scale[v / R::LPB] = (uint8_t)sb;
 }
 
-// load: the values a checkpoint stands for (65536 x 2048 bf16: 62 to 70 us)
+// load: the values a checkpoint stands for (65536 x 2048 bf16: 62 to 77 us)
 template <bool BF16>
 __global__ __launch_bounds__(256) void act8_load_vecs(const typename Codes<BF16>::type *__restrict__ q,
                                                       const uint8_t *__restrict__ scale,
@@ -61,7 +61,7 @@ __global__ __launch_bounds__(256) void act8_load_vecs(const typename Codes<BF16>
 }
 
 // A||B and H' = silu(a) b from the checkpoint of A||B [rows, 2h]; hv = vectors
-// of h. 65536 x 2048 bf16: 541 MB in 90 us, 6.0 TB/s.
+// of h. 65536 x 2048 bf16: 541 MB in 91 us, 5.9 TB/s.
 template <bool BF16>
 __global__ __launch_bounds__(256) void act8_swiglu_vecs(const typename Codes<BF16>::type *__restrict__ q,
                                                         const uint8_t *__restrict__ scale,
@@ -118,9 +118,9 @@ MOE_DEV void group_sums(float (&v)[N]) {
 
 // combine that keeps the experts' rows: out[t] = sum_j g[t,j] y[token_pos[t,j]]
 // (fp32 sum, ascending j) and the checkpoint of every row it reads, from one
-// read: 474 MB at T = 16384, d = 2048, k = 4 bf16 in 91 to 96 us after its
-// backward's dirty lines, 80 without (4.9 to 5.9 TB/s), where the combine alone takes 61 and
-// a store of its own 67.
+// read: 474 MB at T = 16384, d = 2048, k = 4 bf16 in 95 us after its
+// backward's dirty lines, 80 without (5.0 to 5.9 TB/s), where the combine alone takes 61 and
+// a store of its own 68.
 template <bool BF16, int KMAX, int U, int G>
 __global__ __launch_bounds__(G > 256 ? G : 256) void combine_act8_rows(
     const uint4 *__restrict__ y, const float *__restrict__ gate,
@@ -177,7 +177,7 @@ __global__ __launch_bounds__(G > 256 ? G : 256) void combine_act8_rows(
 // (the gates sum to one; this form has no cancellation between large terms).
 // ROWS = false (the MXFP8 backward, whose quantiser forms dy_perm itself):
 // row_gate[p_j] = g_j instead of dy_perm's rows. 484 MB at T = 16384, d = 2048, k
-// = 4 bf16 in 79 to 93 us (5.2 to 6.1 TB/s); from bf16 rows it takes 100.
+// = 4 bf16 in 93 us after the forward (81 to 98; 5.2 TB/s); from bf16 rows it takes 100.
 template <bool BF16, int KMAX, int U, bool ROWS, int G>
 __global__ __launch_bounds__(G > 256 ? G : 256) void combine_bwd_act8_rows(
     const uint4 *__restrict__ dout, const typename Codes<BF16>::type *__restrict__ y8,

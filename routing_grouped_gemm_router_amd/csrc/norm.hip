@@ -14,9 +14,9 @@
 // stays in its threads' registers from its load to its last store, in its own
 // type (unpacking a bf16 again is cheaper than holding it as fp32). The rate is
 // a large copy's, 4.7 to 5.2 TB/s on this card: 16384 x 2048 bf16 with a
-// residual and a checkpoint, forward 303 MB in 54.6 us (5.5 TB/s), backward from
-// the checkpoint with a stream gradient 236 MB in 45.0 us (5.2 TB/s) and 4.6 us for
-// the weights' sums; 32768 x 4096 202 and 182 us (6.0 and 5.2 TB/s); over widths
+// residual and a checkpoint, forward 303 MB in 57 us (5.3 TB/s), backward from
+// the checkpoint with a stream gradient 236 MB in 47 us (5.0 TB/s) and 4.5 us for
+// the weights' sums; 32768 x 4096 201 and 185 us (6.0 and 5.1 TB/s); over widths
 // from 32 to 16384, 256 MiB of rows: 4.4 to 5.4 TB/s forward, 3.4 to 4.9 backward
 // (the ends of the backward's range: few columns a thread to sum over, or no
 // registers to load ahead).

@@ -22,8 +22,8 @@
 //
 // Bound by the weights' bytes with tokens for most experts, by the latency of
 // a launch and a chain of loads with few. d = 2048, h = 1024, E = 128, k = 4: 64
-// tokens (111 experts, 371 MB) 47 + 28 + 5 us, 4.7 TB/s of the 6.1 that a plain
-// read of memory reaches; one token (4 experts, 13 MB) 5.9 + 5.5 us. What it took
+// tokens (111 experts, 371 MB) 48 + 28 + 5 us, 4.6 TB/s of the 6.1 that a plain
+// read of memory reaches; one token (4 experts, 13 MB) 6.1 + 5.9 us. What it took
 // (gate and up, down at 64 tokens): no branch around a load (106 -> 77, ..),
 // memory read by runs of lanes and put into the product's order through LDS
 // (77 -> 58: the first-level cache looked up 39 million lines for the 4 million
@@ -42,7 +42,9 @@
 namespace moe {
 
 // ---------------------------------------------------------------------------
-// quantisation: thread = 8 elements, 4 lanes a block of 32
+// quantisation: thread = 8 elements, 4 lanes a block of 32. Bound by memory: 128
+// experts of d = 2048, h = 1024 from fp32 635 us for 3.65 GB (5.7 TB/s), from bf16
+// 331 us for 2.04 GB (6.2 TB/s).
 
 template <bool BF16>
 __global__ __launch_bounds__(256) void w4_quantize_vecs(const uint4 *__restrict__ in, int64_t n8,
@@ -671,7 +673,7 @@ size_t w4_ws_bytes(int64_t R, int d, int h) {
 //    every compute unit: the wide kernels. d = 2048, h = 1024, E = 128, k = 4, T =
 //    512 (16 rows) 134 us against 190; T = 256 (8 rows) 125 both ways; E = 16, k =
 //    4, T = 64 (16 rows) 29 against 34, T = 32 27 against 24. E = 8, k = 2, T = 128
-//    (128 workgroups) 41 against 30, T = 512 (512) 56 against 79.
+//    (128 workgroups) 41 against 30, T = 512 (512) 54 against 79.
 //  - five workgroups a compute unit and up: two waves a reduction, not four, so
 //    that half as many workgroups look for their expert and join sums. d = 2048,
 //    h = 1024, E = 128, k = 4, T = 64 85.3 us against 88.0, E = 256, d = 1024, h =
