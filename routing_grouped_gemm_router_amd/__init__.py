@@ -1207,7 +1207,7 @@ def _use_buffers(obj, key, new):
         return key, obj._buf
     if obj._T is not None:                        # no old tensor is kept from being freed
         for name in obj._buf["tensors"]:
-            delattr(obj, name)
+            obj.__dict__.pop(name, None)
         obj._T = obj._buf = None
     obj.grads = None
     buf = obj._sizes.at(key)
@@ -1469,7 +1469,8 @@ class MoELayerMX:
         """Re-quantise the fp32 masters, once per optimizer step: each master
         is read once and written in both orientations (mxfp8_quantize_both).
         Again into the same tensors, so that the replays of a captured step
-        take the new weights (masters on another GPU get tensors there)."""
+        take the new weights (masters on another GPU get tensors there): the
+        call must not overlap with the layer's others."""
         E, d, h = self.E, self.d, self.h
         dev = w1.device
         w1, w2 = w1.reshape(E * 2 * h, d), w2.reshape(E * d, h)
@@ -1477,11 +1478,9 @@ class MoELayerMX:
         g1 = torch.arange(0, E + 1, dtype=torch.int32, device=dev) * (2 * h)
         g2 = torch.arange(0, E + 1, dtype=torch.int32, device=dev) * d
         (self.w1q, self.w1s), (self.w1t, self.w1ts) = mxfp8_quantize_both(
-            w1, g1,
-            out=(self.w1q, self.w1s, self.w1t, self.w1ts) if old else None)
+            w1, g1, out=(self.w1q, self.w1s, self.w1t, self.w1ts) if old else None)
         (self.w2q, self.w2s), (self.w2t, self.w2ts) = mxfp8_quantize_both(
-            w2, g2,
-            out=(self.w2q, self.w2s, self.w2t, self.w2ts) if old else None)
+            w2, g2, out=(self.w2q, self.w2s, self.w2t, self.w2ts) if old else None)
 
     def _alloc(self, T, dev):
         self._T, self._buf = _use_buffers(self, (T, str(dev)), lambda: self._new(T, dev))
@@ -1643,7 +1642,8 @@ class MoELayerW4:
     def prepare_weights(self, w1: torch.Tensor, w2: torch.Tensor):
         """Quantise the weights, again after they have changed: into the same
         tensors, so that the replays of a captured step take the new ones
-        (weights on another GPU get tensors there)."""
+        (weights on another GPU get tensors there): the call must not overlap
+        with the layer's others."""
         gpu = w1.get_device()
         _need_on(w1, (self.E, 2 * self.h, self.d), w1.dtype, gpu, "w1")
         _need_on(w2, (self.E, self.d, self.h), w2.dtype, gpu, "w2")
@@ -1663,7 +1663,7 @@ class MoELayerW4:
         buf = self._buf
         with torch.cuda.device(gpu):
             if "out" not in buf:
-                self.route = self.out = None
+                self.route = self.route_ws = self.ws = self.out = None
                 u8 = lambda n: torch.empty(n, dtype=torch.uint8, device=dev)
                 wsb = moe_w4_experts_workspace_size(T, self.k, self.d, self.h)
                 buf.update(route=None, out=torch.empty((T, self.d), dtype=x.dtype, device=dev),
@@ -1671,6 +1671,7 @@ class MoELayerW4:
                            ws=u8(max(wsb, 16)))
             self.route = buf["route"] = moe_route(logits, self.k, out=buf["route"],
                                                   ws=buf["route_ws"])
+        self.route_ws, self.ws = buf["route_ws"], buf["ws"]
         self.out = moe_w4_experts(x, self.route, self.w1q, self.w1s, self.w2q, self.w2s,
                                   buf["out"], buf["ws"])
         _mark(buf, gpu)
