@@ -453,6 +453,14 @@ moe_status mxfp8_quantize_both(const void *in, moe_dtype in_dt, int64_t rows, in
                                const int32_t *group_offsets, int32_t n_groups, uint8_t *q_rows,
                                uint8_t *s_rows, uint8_t *q_cols, uint8_t *s_cols, void *stream);
 
+/* The values that row-block MXFP8 stands for (axis = 1 of mxfp8_quantize):
+ * out [rows, cols] = e * 2^(scale - 127), NaNs for scale byte 255. Exact in
+ * fp32, and in bf16 down to its smallest normal number. out_dt: MOE_F32 or
+ * MOE_BF16; cols: a multiple of 32 below 2^20; q and out 16-byte aligned,
+ * scale at any address. rows = 0 is a no-op. */
+moe_status mxfp8_dequantize(const uint8_t *q, const uint8_t *scale, moe_dtype out_dt, int64_t rows,
+                            int64_t cols, void *out, void *stream);
+
 /* ------------------------------------------------------------------ */
 /* Padded-capacity alternative (for comparison)                         */
 
@@ -632,6 +640,79 @@ moe_status moe_layer_norm_backward(const void *dy, moe_dtype dt, const void *x, 
                                    const float *gamma, const void *dsum, int64_t T, int32_t d,
                                    void *dx, float *dgamma, float *dbeta, int32_t accumulate_dw,
                                    void *ws, size_t ws_bytes, void *stream);
+
+/* ------------------------------------------------------------------ */
+/* Root-mean-square norm                                                */
+
+/* The norm without a mean, over rows of d elements, with an output in 8 bits:
+ *   s = x, or s = x + residual rounded to dt (then stored in sum)
+ *   rstd = 1 / sqrt(sum(s^2) / d + eps)
+ *   y = s * rstd * gamma, rounded to dt
+ *   yq, yq_scale = y in MXFP8 along the row: the bytes that mxfp8_quantize
+ *       with axis = 1 gives for the stored y, what MXFP8 products of the rows
+ *       take (the layer's dispatch, moe_w4_gemm)
+ * y [T, d] in dt may be null if yq [T, d] and yq_scale [T, d/32] are given
+ * (both or neither). rstd [T] fp32 may be null. The rest (x, residual, sum,
+ * gamma, x8, x8_scale, eps, T, d, alignment, dt) as in moe_layer_norm. Sums are
+ * fp32 in a fixed order: the sum of a row's squares has to be finite in fp32
+ * (values under 1e17). A row with a NaN gives NaNs in that row alone; of a row
+ * with an infinity rstd is 0, so its finite elements give 0 and the infinity a
+ * NaN. Outputs must not overlap inputs. T = 0 is a no-op. */
+moe_status moe_rms_norm(const void *x, moe_dtype dt, const void *residual, const float *gamma,
+                        float eps, int64_t T, int32_t d, void *y, void *sum, float *rstd,
+                        uint8_t *yq, uint8_t *yq_scale, uint8_t *x8, uint8_t *x8_scale,
+                        void *stream);
+
+/* Its backward, with xh = s * rstd and g = dy * gamma:
+ *   dx = rstd * (g - xh * mean(g * xh)) (+ dsum), rounded to dt
+ *   dgamma[c] = sum_t dy[t, c] xh[t, c]
+ * (the gradient of y; the rounding to 8 bits is taken as the identity).
+ * Arguments as in moe_layer_norm_backward, without mean and dbeta; ws:
+ * moe_rms_norm_backward_workspace_size bytes, needed when dgamma is given. */
+size_t moe_rms_norm_backward_workspace_size(moe_dtype dt, int64_t T, int32_t d);
+moe_status moe_rms_norm_backward(const void *dy, moe_dtype dt, const void *x, const uint8_t *x8,
+                                 const uint8_t *x8_scale, const float *rstd, const float *gamma,
+                                 const void *dsum, int64_t T, int32_t d, void *dx, float *dgamma,
+                                 int32_t accumulate_dw, void *ws, size_t ws_bytes, void *stream);
+
+/* ------------------------------------------------------------------ */
+/* The gradients' norm, and clipping                                    */
+
+/* Over a list of n_grads tensors (0 to MOE_GRAD_MAX), whose descriptors are
+ * host memory that is read during the call only:
+ *   norm = sqrt(sum over the tensors of their elements' squares)
+ *   out  = data * min(1, max_norm / (norm + 1e-6))
+ * data, out: device, n elements of dtype (MOE_F32 or MOE_BF16, which may be
+ * mixed) at any multiple of the element's size; may be null where n = 0. out
+ * null: in place. A tensor in place is not written where the factor is one.
+ * norm: device fp32, one element. Squares and sums are fp64 in an order that
+ * depends on the sizes alone; the factor is rounded once to fp32, the product
+ * once to dtype. An infinite norm gives the factor 0 (and NaNs where the
+ * infinities are), a NaN a NaN factor: check norm to skip such a step.
+ *
+ * moe_grad_norm: norm alone (out is ignored).
+ * moe_clip_grad_norm: norm and out.
+ * moe_grad_clip: out, from a norm that is given (one that several GPUs' norms
+ *   were joined to, or that covers tensors outside the list).
+ * Clipping writes: no two outs may overlap, nor an out another tensor's data,
+ * nor its own but for being it (MOE_ERR_SHAPE). ws:
+ * moe_grad_norm_workspace_size bytes, 16-byte aligned. max_norm >= 0 and not a
+ * NaN (MOE_ERR_SHAPE). */
+#define MOE_GRAD_MAX 4096
+typedef struct moe_grad {
+    const void *data;
+    void *out;
+    int64_t n;
+    int32_t dtype;
+} moe_grad;
+
+size_t moe_grad_norm_workspace_size(int32_t n_grads);
+moe_status moe_grad_norm(const moe_grad *grads, int32_t n_grads, float *norm, void *ws,
+                         size_t ws_bytes, void *stream);
+moe_status moe_clip_grad_norm(const moe_grad *grads, int32_t n_grads, float max_norm, float *norm,
+                              void *ws, size_t ws_bytes, void *stream);
+moe_status moe_grad_clip(const moe_grad *grads, int32_t n_grads, const float *norm, float max_norm,
+                         void *stream);
 
 /* ------------------------------------------------------------------ */
 /* The experts for few tokens, weights in 4 bits                        */

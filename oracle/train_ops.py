@@ -71,6 +71,23 @@ def layer_norm_backward(s, mean, rstd, dy, gamma, dsum=None):
     return dx, (dy * xh).sum(axis=0), dy.sum(axis=0)
 
 
+def rms_norm(s, gamma, eps):
+    """Root-mean-square norm of rows s [T, d]: y = s rstd gamma, rstd."""
+    s = np.asarray(s, np.float64)
+    rstd = 1.0 / np.sqrt((s * s).sum(1) / s.shape[1] + eps)
+    return s * rstd[:, None] * np.asarray(gamma, np.float64), rstd
+
+
+def rms_norm_backward(s, rstd, dy, gamma, dsum=None):
+    """dx (the gradient of s, plus dsum), dgamma."""
+    s, dy, r = (np.asarray(a, np.float64) for a in (s, dy, np.asarray(rstd)[:, None]))
+    xh, g = s * r, dy * np.asarray(gamma, np.float64)
+    dx = r * (g - xh * (g * xh).mean(1, keepdims=True))
+    if dsum is not None:
+        dx = dx + np.asarray(dsum, np.float64)
+    return dx, (dy * xh).sum(0)
+
+
 def combine(y, gate, token_pos):
     """out[t] = sum_j gate[t, j] y[token_pos[t, j]]; a negative position adds nothing."""
     keep = token_pos >= 0

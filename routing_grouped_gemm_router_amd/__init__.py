@@ -157,6 +157,24 @@ def _load():
     lib.moe_layer_norm_backward.argtypes = [_P, _I32, _P, _P, _P, _P, _P, _P, _P, _I64, _I32, _P,
                                             _P, _P, _I32, _P, _SZ, _P]
     lib.moe_layer_norm_backward.restype = _I32
+    lib.moe_rms_norm.argtypes = [_P, _I32, _P, _P, ctypes.c_float, _I64, _I32, _P, _P, _P, _P, _P,
+                                 _P, _P, _P]
+    lib.moe_rms_norm.restype = _I32
+    lib.moe_rms_norm_backward_workspace_size.argtypes = [_I32, _I64, _I32]
+    lib.moe_rms_norm_backward_workspace_size.restype = _SZ
+    lib.moe_rms_norm_backward.argtypes = [_P, _I32, _P, _P, _P, _P, _P, _P, _I64, _I32, _P, _P,
+                                          _I32, _P, _SZ, _P]
+    lib.moe_rms_norm_backward.restype = _I32
+    lib.mxfp8_dequantize.argtypes = [_P, _P, _I32, _I64, _I64, _P, _P]
+    lib.mxfp8_dequantize.restype = _I32
+    lib.moe_grad_norm_workspace_size.argtypes = [_I32]
+    lib.moe_grad_norm_workspace_size.restype = _SZ
+    lib.moe_grad_norm.argtypes = [_P, _I32, _P, _P, _SZ, _P]
+    lib.moe_grad_norm.restype = _I32
+    lib.moe_clip_grad_norm.argtypes = [_P, _I32, ctypes.c_float, _P, _P, _SZ, _P]
+    lib.moe_clip_grad_norm.restype = _I32
+    lib.moe_grad_clip.argtypes = [_P, _I32, _P, ctypes.c_float, _P]
+    lib.moe_grad_clip.restype = _I32
     lib.moe_w4_quantize.argtypes = [_P, _I32, _I64, _I64, _P, _P, _P]
     lib.moe_w4_quantize.restype = _I32
     lib.moe_w4_experts_workspace_size.argtypes = [_I64, _I32, _I32, _I32]
@@ -925,6 +943,211 @@ def moe_layer_norm_backward(saved: dict, dy: torch.Tensor, weight: torch.Tensor,
 
 
 # ---------------------------------------------------------------------------
+# the root-mean-square norm with an output in 8 bits
+
+
+def moe_rms_norm(x: torch.Tensor, weight: torch.Tensor, eps: float = 1e-6,
+                 residual: torch.Tensor | None = None, quantize: bool = False, want_y: bool = True,
+                 act8: bool = False, stats: bool = True, out: dict | None = None) -> dict:
+    """Root-mean-square norm over the rows of x [T, d], or of x + residual
+    (see moe.h). Returns a dict: y (unless want_y is False, which needs
+    quantize); with a residual sum; with stats rstd [T] fp32 for the backward;
+    with quantize yq and yq_scale, y in MXFP8 along its rows; with act8 x8 and
+    x8_scale, the normalised input's 8-bit checkpoint. `out`: a dict of an
+    earlier call with the same arguments, whose tensors are written again."""
+    T, d, dt, gpu = _act_matrix(x, "x")
+    f32 = torch.float32
+    if not (want_y or quantize):
+        raise ValueError("want_y=False needs quantize=True")
+    _need_on(weight, (d,), f32, gpu, "weight")
+    if residual is not None:
+        _need_on(residual, (T, d), x.dtype, gpu, "residual")
+    if out is None:
+        dev = x.device
+        out = {}
+        if want_y:
+            out["y"] = torch.empty_like(x)
+        if residual is not None:
+            out["sum"] = torch.empty_like(x)
+        if stats:
+            out["rstd"] = torch.empty(T, dtype=f32, device=dev)
+        if quantize:
+            out["yq"], out["yq_scale"] = _act8_new(T, d, dev)
+        if act8:
+            out["x8"], out["x8_scale"] = _act8_new(T, d, dev)
+    else:
+        if want_y:
+            _need_on(out.get("y"), (T, d), x.dtype, gpu, "y")
+        if residual is not None:
+            _need_on(out.get("sum"), (T, d), x.dtype, gpu, "sum")
+        if stats:
+            _need_on(out.get("rstd"), (T,), f32, gpu, "rstd")
+        if quantize:
+            _act8_need(out.get("yq"), out.get("yq_scale"), T, d, gpu, "yq")
+        if act8:
+            _act8_need(out.get("x8"), out.get("x8_scale"), T, d, gpu, "x8")
+    _enqueue("moe_rms_norm", _lib.moe_rms_norm, gpu, x.data_ptr(), dt, _ptr(residual),
+             weight.data_ptr(), eps, T, d, out["y"].data_ptr() if want_y else None,
+             None if residual is None else out["sum"].data_ptr(),
+             out["rstd"].data_ptr() if stats else None,
+             out["yq"].data_ptr() if quantize else None,
+             out["yq_scale"].data_ptr() if quantize else None,
+             out["x8"].data_ptr() if act8 else None,
+             out["x8_scale"].data_ptr() if act8 else None)
+    return out
+
+
+def moe_rms_norm_backward_workspace_size(dtype: int, T: int, d: int) -> int:
+    return _lib.moe_rms_norm_backward_workspace_size(dtype, T, d)
+
+
+def moe_rms_norm_backward(saved: dict, dy: torch.Tensor, weight: torch.Tensor,
+                          dsum: torch.Tensor | None = None, out: dict | None = None,
+                          accumulate_dw: bool = False, want_dweight: bool = True,
+                          ws: torch.Tensor | None = None) -> dict:
+    """Backward of moe_rms_norm (see moe.h). saved: rstd, and the normalised
+    input as x or as x8 and x8_scale (x, if both are there). Returns a dict:
+    dx [T, d] (with a residual, its gradient too) and dweight [d] fp32. dsum:
+    the gradient that reaches x (or sum) by its other uses, added to dx. out:
+    tensors of an earlier call; accumulate_dw adds to its dweight."""
+    T, d, dt, gpu = _act_matrix(dy, "dy")
+    f32 = torch.float32
+    x = saved.get("x")
+    x8 = x8s = None
+    if x is not None:
+        _need_on(x, (T, d), dy.dtype, gpu, "x")
+    else:
+        x8, x8s = saved.get("x8"), saved.get("x8_scale")
+        _act8_need(x8, x8s, T, d, gpu, "x8")
+    rstd = saved.get("rstd")
+    _need_on(rstd, (T,), f32, gpu, "rstd")
+    _need_on(weight, (d,), f32, gpu, "weight")
+    if dsum is not None:
+        _need_on(dsum, (T, d), dy.dtype, gpu, "dsum")
+    if out is None:
+        if accumulate_dw:
+            raise ValueError("accumulate_dw needs the gradients of an earlier backward (out)")
+        out = dict(dx=torch.empty_like(dy))
+        if want_dweight:
+            out["dweight"] = torch.empty(d, dtype=f32, device=dy.device)
+    else:
+        _need_on(out.get("dx"), (T, d), dy.dtype, gpu, "dx")
+        if want_dweight:
+            _need_on(out.get("dweight"), (d,), f32, gpu, "dweight")
+    if want_dweight:
+        ws = _need_ws(ws, moe_rms_norm_backward_workspace_size(dt, T, d), dy, gpu)
+    _enqueue("moe_rms_norm_backward", _lib.moe_rms_norm_backward, gpu, dy.data_ptr(), dt, _ptr(x),
+             _ptr(x8), _ptr(x8s), rstd.data_ptr(), weight.data_ptr(), _ptr(dsum), T, d,
+             out["dx"].data_ptr(), out["dweight"].data_ptr() if want_dweight else None,
+             1 if accumulate_dw else 0, _ptr(ws), 0 if ws is None else ws.numel())
+    return out
+
+
+def mxfp8_dequantize(q: torch.Tensor, scale: torch.Tensor, dtype: torch.dtype = torch.bfloat16,
+                     out: torch.Tensor | None = None) -> torch.Tensor:
+    """The values that MXFP8 rows (q [rows, cols], scale [rows, cols/32]) stand
+    for, as `dtype` (see moe.h)."""
+    rows, cols, dt, gpu = _act8_in(q, scale, dtype, "q")
+    if out is None:
+        out = torch.empty_like(q, dtype=dtype)
+    else:
+        _need_on(out, (rows, cols), dtype, gpu, "out")
+    _enqueue("mxfp8_dequantize", _lib.mxfp8_dequantize, gpu, q.data_ptr(), scale.data_ptr(), dt,
+             rows, cols, out.data_ptr())
+    return out
+
+
+# ---------------------------------------------------------------------------
+# the gradients' norm, and clipping
+
+MOE_GRAD_MAX = 4096
+_GRAD_DT = {torch.float32: MOE_F32, torch.bfloat16: MOE_BF16}
+
+
+def _grad_list(grads, out=None):
+    """The C descriptors (moe_grad: data, out, n, dtype) of a list of
+    tensors, their number and their GPU."""
+    grads = list(grads)
+    if not grads:
+        raise ValueError("grads: expected at least one tensor")
+    if out is not None:
+        out = list(out)
+        if len(out) != len(grads):
+            raise ValueError(f"out: expected {len(grads)} tensors, got {len(out)}")
+    gpu = grads[0].get_device()
+    v = []
+    for i, g in enumerate(grads):
+        dt = _GRAD_DT.get(g.dtype)
+        if dt is None or gpu < 0 or g.get_device() != gpu or not g.is_contiguous():
+            raise ValueError(f"grads[{i}]: expected a contiguous f32 or bf16 tensor on "
+                             f"{'a GPU' if gpu < 0 else f'cuda:{gpu}'}, got {g.dtype} "
+                             f"(contiguous={g.is_contiguous()}, device={g.device})")
+        o = 0
+        if out is not None:
+            o = out[i]
+            if o.dtype is not g.dtype or o.shape != g.shape or o.get_device() != gpu or \
+                    not o.is_contiguous():
+                raise ValueError(f"out[{i}]: expected a contiguous {g.dtype} {tuple(g.shape)} on "
+                                 f"cuda:{gpu}, got {o.dtype} {tuple(o.shape)} (contiguous="
+                                 f"{o.is_contiguous()}, device={o.device})")
+            o = o.data_ptr()
+        v += (g.data_ptr(), o, g.numel(), dt)
+    return (_I64 * len(v))(*v), len(grads), gpu, grads[0].device
+
+
+def _grad_norm_args(n, dev, gpu, norm, ws):
+    if norm is None:
+        norm = torch.empty((), dtype=torch.float32, device=dev)
+    elif norm.dtype is not torch.float32 or norm.numel() != 1 or norm.get_device() != gpu:
+        raise ValueError(f"norm: expected one f32 element on cuda:{gpu}, got {norm.dtype} "
+                         f"{tuple(norm.shape)} on {norm.device}")
+    wsb = _lib.moe_grad_norm_workspace_size(n)
+    if ws is None:
+        ws = torch.empty(max(wsb, 16), dtype=torch.uint8, device=dev)
+    else:
+        _need_bytes(ws, wsb, "ws")
+        if ws.get_device() != gpu:
+            raise ValueError(f"ws: expected on cuda:{gpu}, got {ws.device}")
+    return norm, ws
+
+
+def moe_grad_norm_workspace_size(n_grads: int) -> int:
+    return _lib.moe_grad_norm_workspace_size(n_grads)
+
+
+def moe_grad_norm(grads, norm: torch.Tensor | None = None,
+                  ws: torch.Tensor | None = None) -> torch.Tensor:
+    """The norm of all elements of a list of f32 and bf16 tensors (see moe.h):
+    one f32 element on their GPU."""
+    v, n, gpu, dev = _grad_list(grads)
+    norm, ws = _grad_norm_args(n, dev, gpu, norm, ws)
+    _enqueue("moe_grad_norm", _lib.moe_grad_norm, gpu, v, n, norm.data_ptr(), ws.data_ptr(),
+             ws.numel())
+    return norm
+
+
+def moe_clip_grad_norm(grads, max_norm: float, out=None, norm: torch.Tensor | None = None,
+                       ws: torch.Tensor | None = None) -> torch.Tensor:
+    """moe_grad_norm, and every tensor times min(1, max_norm / (norm + 1e-6)),
+    in place or into the tensors of `out`. Returns the norm in front of it."""
+    v, n, gpu, dev = _grad_list(grads, out)
+    norm, ws = _grad_norm_args(n, dev, gpu, norm, ws)
+    _enqueue("moe_clip_grad_norm", _lib.moe_clip_grad_norm, gpu, v, n, max_norm, norm.data_ptr(),
+             ws.data_ptr(), ws.numel())
+    return norm
+
+
+def moe_grad_clip(grads, norm: torch.Tensor, max_norm: float, out=None):
+    """The clipping alone, with a norm that is given (one f32 element on the
+    tensors' GPU)."""
+    v, n, gpu, _ = _grad_list(grads, out)
+    if norm is None or norm.dtype is not torch.float32 or norm.numel() != 1 or \
+            norm.get_device() != gpu:
+        raise ValueError(f"norm: expected one f32 element on cuda:{gpu}")
+    _enqueue("moe_grad_clip", _lib.moe_grad_clip, gpu, v, n, norm.data_ptr(), max_norm)
+
+
+# ---------------------------------------------------------------------------
 # the experts for few tokens, weights in 4 bits
 
 
@@ -1184,6 +1407,62 @@ class LayerNorm:
         """Bytes held from forward to backward (x, or sum, is the caller's)."""
         o = self._out
         return _nbytes([o["mean"], o["rstd"], o.get("x8"), o.get("x8_scale")])
+
+
+class RMSNorm:
+    """A root-mean-square norm with its gradient, in front of the layer or
+    behind it (the layers' `out_norm`): LayerNorm without a mean and a bias.
+
+    weight: [d] fp32. forward(x, residual) normalises x + residual and leaves
+    that stream in `sum`. quantize=True also writes y in MXFP8, left in `q` (a
+    pair of elements and scales): what MoELayerMX.forward and
+    MoELayerW4.prompt take as `xq` in place of quantising x themselves.
+    act8=True and the buffers as in LayerNorm."""
+
+    def __init__(self, weight: torch.Tensor, eps: float = 1e-6, act8: bool = False,
+                 quantize: bool = False):
+        self.weight, self.eps, self.act8, self.quantize = weight, eps, act8, quantize
+        self.sum = self.q = None
+        self._sizes, self._key = _Sizes(), None
+
+    def forward(self, x: torch.Tensor, residual: torch.Tensor | None = None) -> torch.Tensor:
+        key = (x.shape, x.dtype, x.device, residual is None)
+        if self._key != key:
+            self._out = self.grads = self._key = None
+            self._buf = self._sizes.at(key)
+        buf = self._buf
+        self._out = buf["out"] = moe_rms_norm(x, self.weight, self.eps, residual, self.quantize,
+                                              act8=self.act8, out=buf.get("out"))
+        _mark(buf, x.get_device())
+        self._key = key
+        self.sum = self._out.get("sum")
+        self.q = (self._out["yq"], self._out["yq_scale"]) if self.quantize else None
+        self._x = None if self.act8 else (x if residual is None else self.sum)
+        return self._out["y"]
+
+    def backward(self, dy: torch.Tensor, dsum: torch.Tensor | None = None,
+                 accumulate_dw: bool = False) -> dict:
+        """dict of dx (the gradient of x and of the residual) and dweight.
+        dsum: the gradient that reaches sum by its other uses."""
+        if self._key is None:
+            raise ValueError("backward without a forward")
+        if accumulate_dw and self.grads is None:
+            raise ValueError("accumulate_dw needs the gradients of an earlier backward")
+        buf = self._buf
+        if "ws" not in buf:
+            y = self._out["y"]
+            wsb = moe_rms_norm_backward_workspace_size(_dt(y), *y.shape)
+            buf["ws"] = torch.empty(max(wsb, 16), dtype=torch.uint8, device=y.device)
+        self.grads = buf["grads"] = moe_rms_norm_backward(
+            dict(self._out, x=self._x), dy, self.weight, dsum, out=buf.get("grads"),
+            accumulate_dw=accumulate_dw, ws=buf["ws"])
+        _mark(buf, dy.get_device())
+        return self.grads
+
+    def held_bytes(self) -> int:
+        """Bytes held from forward to backward (x, or sum, is the caller's)."""
+        o = self._out
+        return _nbytes([o["rstd"], o.get("x8"), o.get("x8_scale")])
 
 
 def _norm_backward(norm, dout, accumulate_dw):
@@ -1530,19 +1809,22 @@ class MoELayerMX:
         recomputation of GEMM1 stores bf16 H', which moe_backward quantises)."""
         return self.fuse_hp
 
-    def _gemm1(self, x, offsets, token_pos, quantised_hp: bool = False):
+    def _gemm1(self, x, offsets, token_pos, quantised_hp: bool = False, xq: tuple | None = None):
         """Quantised dispatch of x and GEMM1 + SwiGLU (forward, and again in
         the backward when recomputing). quantised_hp: H' goes straight to its
         two MXFP8 layouts instead of bf16."""
-        mxfp8_quantize(x, 1, q=self.xq, scale=self.xs)
-        moe_permute(self.xq, token_pos, self.xpq, x_scale=self.xs, x_perm_scale=self.xps)
+        q, s = xq or mxfp8_quantize(x, 1, q=self.xq, scale=self.xs)
+        moe_permute(q, token_pos, self.xpq, x_scale=s, x_perm_scale=self.xps)
         hp = (dict(aux_out=self.hpq, aux_out_scale=self.hps, aux_out_cols=self.hpc,
                    aux_out_cols_scale=self.hpcs) if quantised_hp else dict(aux_out=self.hp))
         moe_grouped_gemm(MOE_GG_FWD, self.xpq, self.w1q, self.ab, offsets, MOE_EPI_SWIGLU_FWD,
                          N=2 * self.h, K=self.d, a_scale=self.xps, b_scale=self.w1s,
                          dtype=MOE_MXFP8, **hp)
 
-    def forward(self, x: torch.Tensor, logits: torch.Tensor) -> torch.Tensor:
+    def forward(self, x: torch.Tensor, logits: torch.Tensor, xq: tuple | None = None) -> torch.Tensor:
+        """xq: x in MXFP8 along its rows (elements [T, d], scales [T, d/32]),
+        where the norm in front has written it (RMSNorm.q), read during the
+        forward only; else the layer quantises x. It must be x's own."""
         if x.dim() != 2 or x.shape[1] != self.d or x.dtype != torch.bfloat16:
             raise ValueError(f"x: expected bf16 [T, {self.d}], got {x.dtype} {tuple(x.shape)}")
         if x.device != self.w1q.device:
@@ -1551,13 +1833,15 @@ class MoELayerMX:
         _need(logits, (x.shape[0], self.E), torch.float32, "logits")
         T, d = x.shape
         h = self.h
+        if xq is not None:
+            _act8_need(xq[0], xq[1], T, d, x.get_device(), "xq")
         self._alloc(T, x.device)
         self.x = x
         r = moe_route(logits, self.k, out=self.route, ws=self.route_ws)
         if self.balance is not None:
             self.lb_stats = self.balance.forward(logits, r["counts"], self.k, self._buf)
         fused = self.hp_quantised_in_gemm1()
-        self._gemm1(x, r["offsets"], r["token_pos"], quantised_hp=fused)
+        self._gemm1(x, r["offsets"], r["token_pos"], quantised_hp=fused, xq=xq)
         if self.act8:
             moe_act8_store(self.ab, self.ckpt["ab8"], self.ckpt["ab8_scale"])
         if not fused:

@@ -5,6 +5,8 @@
 // device memory, allocates, copies device->host or synchronises.
 #include <string.h>
 
+#include <algorithm>
+
 #include "common.h"
 
 namespace moe {
@@ -73,6 +75,23 @@ moe_status norm_bwd_launch(const void *dy, moe_dtype dt, const void *x, const ui
                            const float *gamma, const void *dsum, int64_t T, int d, void *dx,
                            float *dgamma, float *dbeta, bool accumulate, float *part,
                            hipStream_t s);
+
+moe_status rms_fwd_launch(const void *x, moe_dtype dt, const void *res, const float *gamma,
+                          float eps, int64_t T, int d, void *y, void *sum, float *rstd,
+                          uint8_t *x8, uint8_t *x8_scale, uint8_t *yq, uint8_t *yq_scale,
+                          hipStream_t s);
+size_t rms_bwd_ws_bytes(moe_dtype dt, int64_t T, int d);
+moe_status rms_bwd_launch(const void *dy, moe_dtype dt, const void *x, const uint8_t *x8,
+                          const uint8_t *x8_scale, const float *rstd, const float *gamma,
+                          const void *dsum, int64_t T, int d, void *dx, float *dgamma,
+                          bool accumulate, float *part, hipStream_t s);
+moe_status mxfp8_dequantize_launch(const uint8_t *q, const uint8_t *scale, moe_dtype dt,
+                                   int64_t rows, int64_t cols, void *out, hipStream_t s);
+size_t grad_norm_ws_bytes(int n);
+moe_status grad_norm_launch(const moe_grad *g, int n, float *norm, void *ws, hipStream_t s);
+// ws null: with the norm that is given
+moe_status grad_clip_launch(const moe_grad *g, int n, float max_norm, float *norm, void *ws,
+                            hipStream_t s);
 
 moe_status w4_quantize_launch(const void *in, moe_dtype dt, int64_t rows, int64_t cols, uint8_t *q,
                               uint8_t *scale, hipStream_t s);
@@ -664,6 +683,137 @@ moe_status moe_layer_norm_backward(const void *dy, moe_dtype dt, const void *x, 
     return norm_bwd_launch(dy, dt, x, x8, x8_scale, mean, rstd, gamma, dsum, T, d, dx, dgamma,
                            dbeta, accumulate_dw, params ? (float *)ws : nullptr,
                            (hipStream_t)stream);
+}
+
+moe_status moe_rms_norm(const void *x, moe_dtype dt, const void *residual, const float *gamma,
+                        float eps, int64_t T, int32_t d, void *y, void *sum, float *rstd,
+                        uint8_t *yq, uint8_t *yq_scale, uint8_t *x8, uint8_t *x8_scale,
+                        void *stream) {
+    moe_status st = check_norm(dt, T, d);
+    if (st != MOE_OK) return st;
+    if (!(eps > 0.f) || eps > 1.f) return MOE_ERR_SHAPE;
+    if (T == 0) return MOE_OK;
+    if (!x || !gamma || (!y && !yq) || !residual != !sum || !x8 != !x8_scale || !yq != !yq_scale)
+        return MOE_ERR_NULL;
+    const void *al[] = {x, residual, gamma, y, sum, x8, yq};
+    for (const void *p : al)
+        if (!aligned16(p)) return MOE_ERR_ALIGN;
+    if (!aligned4(rstd)) return MOE_ERR_ALIGN;
+    return rms_fwd_launch(x, dt, residual, gamma, eps, T, d, y, sum, rstd, x8, x8_scale, yq,
+                          yq_scale, (hipStream_t)stream);
+}
+
+size_t moe_rms_norm_backward_workspace_size(moe_dtype dt, int64_t T, int32_t d) {
+    return check_norm(dt, T, d) == MOE_OK ? rms_bwd_ws_bytes(dt, T, d) : 0;
+}
+
+moe_status moe_rms_norm_backward(const void *dy, moe_dtype dt, const void *x, const uint8_t *x8,
+                                 const uint8_t *x8_scale, const float *rstd, const float *gamma,
+                                 const void *dsum, int64_t T, int32_t d, void *dx, float *dgamma,
+                                 int32_t accumulate_dw, void *ws, size_t ws_bytes, void *stream) {
+    moe_status st = check_norm(dt, T, d);
+    if (st != MOE_OK) return st;
+    if (accumulate_dw != 0 && accumulate_dw != 1) return MOE_ERR_DTYPE;
+    if (T > 0) {
+        if (!dy || !gamma || !rstd || !dx || !x == !x8 || !x8 != !x8_scale) return MOE_ERR_NULL;
+        const void *al[] = {dy, x, x8, gamma, dsum, dx};
+        for (const void *p : al)
+            if (!aligned16(p)) return MOE_ERR_ALIGN;
+        if (dgamma) {
+            if (ws_bytes < rms_bwd_ws_bytes(dt, T, d)) return MOE_ERR_WORKSPACE;
+            if (!ws) return MOE_ERR_NULL;
+            if (!aligned16(ws)) return MOE_ERR_ALIGN;
+        }
+    }
+    if (!aligned4(rstd) || !aligned4(dgamma)) return MOE_ERR_ALIGN;
+    return rms_bwd_launch(dy, dt, x, x8, x8_scale, rstd, gamma, dsum, T, d, dx, dgamma,
+                          accumulate_dw, dgamma ? (float *)ws : nullptr, (hipStream_t)stream);
+}
+
+moe_status mxfp8_dequantize(const uint8_t *q, const uint8_t *scale, moe_dtype out_dt, int64_t rows,
+                            int64_t cols, void *out, void *stream) {
+    moe_status st = check_act8_matrix(out_dt, rows, cols);
+    if (st != MOE_OK || rows == 0) return st;
+    if (!q || !scale || !out) return MOE_ERR_NULL;
+    if (!aligned16(q) || !aligned16(out)) return MOE_ERR_ALIGN;
+    return mxfp8_dequantize_launch(q, scale, out_dt, rows, cols, out, (hipStream_t)stream);
+}
+
+// Descriptors of a list of gradients; writes: what is written may overlap
+// nothing else of the list.
+static moe_status check_grads(const moe_grad *g, int32_t n, bool writes) {
+    if (n < 0 || n > MOE_GRAD_MAX) return MOE_ERR_SHAPE;
+    if (n > 0 && !g) return MOE_ERR_NULL;
+    for (int i = 0; i < n; i++) {
+        if (g[i].dtype != MOE_F32 && g[i].dtype != MOE_BF16) return MOE_ERR_DTYPE;
+        if (g[i].n < 0 || g[i].n >= ((int64_t)1 << 56)) return MOE_ERR_SHAPE;
+        if (g[i].n == 0) continue;
+        if (!g[i].data) return MOE_ERR_NULL;
+        const uintptr_t mask = g[i].dtype == MOE_BF16 ? 1 : 3;
+        if (((uintptr_t)g[i].data & mask) || (writes && ((uintptr_t)g[i].out & mask)))
+            return MOE_ERR_ALIGN;
+    }
+    if (!writes) return MOE_OK;
+    struct Span { uintptr_t at, end; };
+    Span out[MOE_GRAD_MAX];                          // 64 KiB of stack: nothing is allocated
+    int m = 0;
+    auto bytes = [&](int i) { return (uintptr_t)g[i].n * (g[i].dtype == MOE_BF16 ? 2 : 4); };
+    for (int i = 0; i < n; i++) {
+        if (g[i].n == 0) continue;
+        const uintptr_t at = (uintptr_t)(g[i].out ? g[i].out : g[i].data);
+        out[m++] = {at, at + bytes(i)};
+    }
+    std::sort(out, out + m, [](const Span &a, const Span &b) { return a.at < b.at; });
+    for (int i = 1; i < m; i++)
+        if (out[i].at < out[i - 1].end) return MOE_ERR_SHAPE;
+    for (int i = 0; i < n; i++) {
+        if (g[i].n == 0 || !g[i].out) continue;      // in place: checked above
+        const uintptr_t at = (uintptr_t)g[i].data, end = at + bytes(i);
+        // the first span that ends after `at`
+        const Span *p = std::lower_bound(out, out + m, at, [](const Span &a, uintptr_t v) { return a.end <= v; });
+        if (p == out + m || p->at >= end) continue;
+        if (g[i].out != g[i].data) return MOE_ERR_SHAPE;
+    }
+    return MOE_OK;
+}
+
+size_t moe_grad_norm_workspace_size(int32_t n_grads) {
+    return n_grads >= 0 && n_grads <= MOE_GRAD_MAX ? grad_norm_ws_bytes(n_grads) : 0;
+}
+
+static moe_status check_grad_norm(const moe_grad *g, int32_t n, bool writes, const float *norm,
+                                  const void *ws, size_t ws_bytes) {
+    const moe_status st = check_grads(g, n, writes);
+    if (st != MOE_OK) return st;
+    if (!norm || (n > 0 && !ws)) return MOE_ERR_NULL;
+    if (!aligned4(norm) || !aligned16(ws)) return MOE_ERR_ALIGN;
+    return ws_bytes < grad_norm_ws_bytes(n) ? MOE_ERR_WORKSPACE : MOE_OK;
+}
+
+moe_status moe_grad_norm(const moe_grad *grads, int32_t n_grads, float *norm, void *ws,
+                         size_t ws_bytes, void *stream) {
+    const moe_status st = check_grad_norm(grads, n_grads, false, norm, ws, ws_bytes);
+    return st != MOE_OK ? st : grad_norm_launch(grads, n_grads, norm, ws, (hipStream_t)stream);
+}
+
+moe_status moe_clip_grad_norm(const moe_grad *grads, int32_t n_grads, float max_norm, float *norm,
+                              void *ws, size_t ws_bytes, void *stream) {
+    if (!(max_norm >= 0.f)) return MOE_ERR_SHAPE;
+    const moe_status st = check_grad_norm(grads, n_grads, true, norm, ws, ws_bytes);
+    if (st != MOE_OK) return st;
+    if (n_grads == 0) return grad_norm_launch(grads, 0, norm, ws, (hipStream_t)stream);
+    return grad_clip_launch(grads, n_grads, max_norm, norm, ws, (hipStream_t)stream);
+}
+
+moe_status moe_grad_clip(const moe_grad *grads, int32_t n_grads, const float *norm, float max_norm,
+                         void *stream) {
+    if (!(max_norm >= 0.f)) return MOE_ERR_SHAPE;
+    const moe_status st = check_grads(grads, n_grads, true);
+    if (st != MOE_OK) return st;
+    if (!norm) return MOE_ERR_NULL;
+    if (!aligned4(norm)) return MOE_ERR_ALIGN;
+    return grad_clip_launch(grads, n_grads, max_norm, const_cast<float *>(norm), nullptr,
+                            (hipStream_t)stream);
 }
 
 moe_status moe_w4_quantize(const void *in, moe_dtype in_dt, int64_t rows, int64_t cols, uint8_t *q,

@@ -1,0 +1,259 @@
+// clip.hip -- the global norm of many gradients, and their clipping.
+//
+//   N = sqrt(sum_i sum_e g_i[e]^2),  out_i = g_i min(1, max_norm / (N + 1e-6)).
+//
+// The squares are formed and summed in fp64: every fp32 or bf16 value's square
+// is a normal fp64 number, so nothing overflows or vanishes where the norm
+// itself is representable, and the sum of billions of squares loses nothing.
+// The order is fixed by the sizes alone (no atomics).
+//
+// A list's tensors are cut into chunks of 32 KiB, walked by a grid that fits
+// the chip; the list travels in the kernel's arguments (kGradMax tensors a
+// launch), so a call needs no table in device memory and can be captured.
+// The bound is memory: one read for the norm, one read and one write to clip.
+#include <algorithm>
+
+#include "act8.h"
+#include "common.h"
+
+namespace moe {
+
+constexpr int kGradMax = 64;            // tensors of a launch
+constexpr int kChunkBytes = 32768;      // of a tensor: 8 vectors a thread
+constexpr int kGradBlocks = 2048;       // workgroups of a launch: eight a compute unit
+
+struct GradItem {
+    const char *in;
+    char *out;
+    int64_t n;          // elements
+    int64_t first;      // chunks of the tensors in front of it
+    int32_t bf16;
+};
+struct GradArgs {
+    GradItem t[kGradMax];
+    int64_t chunks;
+    int32_t count;
+};
+
+// Vectors of 16 bytes at any element's address (the memory unit takes loads
+// and stores that are not aligned to their size).
+typedef uint32_t u32x4_any __attribute__((ext_vector_type(4), aligned(2)));
+
+template <bool BF16>
+MOE_DEV float grad_elem(const char *p, int64_t i) {
+    if constexpr (BF16) return bf16_to_f32(reinterpret_cast<const uint16_t *>(p)[i]);
+    else return reinterpret_cast<const float *>(p)[i];
+}
+
+// f(first byte, elements) of the chunks blockIdx.x, blockIdx.x + gridDim.x, ..
+// of a list; BACK: counted from its end. s_first: the list's `first`, in LDS.
+template <bool BACK, typename F>
+MOE_DEV void for_chunks(const GradArgs &a, F f) {
+    for (int64_t i = blockIdx.x; i < a.chunks; i += gridDim.x) {
+        const int64_t c = BACK ? a.chunks - 1 - i : i;
+        int lo = 0, hi = a.count - 1;   // the last tensor that starts at or before chunk c
+        while (lo < hi) {
+            const int mid = (lo + hi + 1) >> 1;
+            if (a.t[mid].first <= c) lo = mid; else hi = mid - 1;
+        }
+        const GradItem &t = a.t[lo];
+        const int64_t per = t.bf16 ? kChunkBytes / 2 : kChunkBytes / 4;
+        const int64_t e0 = (c - t.first) * per;
+        const int64_t left = t.n - e0;
+        f(t, e0, (int)(left < per ? left : per));
+    }
+}
+
+template <bool BF16>
+MOE_DEV double chunk_squares(const char *p, int64_t e0, int n) {
+    typedef Row16<BF16> R;
+    p += e0 * (BF16 ? 2 : 4);
+    const int nv = n / R::N;
+    double s[2] = {0., 0.};
+    auto add = [&](const u32x4 &w) {
+        float f[R::N];
+        R::unpack(make_uint4(w.x, w.y, w.z, w.w), f);
+#pragma unroll
+        for (int e = 0; e < R::N; e++) {
+            const double x = f[e];
+            s[e & 1] = fma(x, x, s[e & 1]);
+        }
+    };
+    const u32x4_any *v = reinterpret_cast<const u32x4_any *>(p);
+    if (n == (BF16 ? kChunkBytes / 2 : kChunkBytes / 4)) {
+        u32x4 w[8];
+#pragma unroll
+        for (int i = 0; i < 8; i++) w[i] = v[threadIdx.x + 256 * i];
+#pragma unroll
+        for (int i = 0; i < 8; i++) add(w[i]);
+    } else {
+        for (int i = threadIdx.x; i < nv; i += 256) add(v[i]);
+        for (int i = nv * R::N + threadIdx.x; i < n; i += 256) {
+            const double x = grad_elem<BF16>(p, i);
+            s[0] = fma(x, x, s[0]);
+        }
+    }
+    return s[0] + s[1];
+}
+
+// Sum over the workgroup's 256 threads, in a fixed order; all get it.
+MOE_DEV double block_sum(double v) {
+    __shared__ double w[4];
+    v = wave_sum(v);
+    if ((threadIdx.x & 63) == 0) w[threadIdx.x >> 6] = v;
+    __syncthreads();
+    return (w[0] + w[1]) + (w[2] + w[3]);
+}
+
+// part[blockIdx.x] = the sum of squares of the workgroup's chunks
+__global__ __launch_bounds__(256) void grad_squares(GradArgs a, double *__restrict__ part) {
+    double s = 0.;
+    for_chunks<false>(a, [&](const GradItem &t, int64_t e0, int n) {
+        s += t.bf16 ? chunk_squares<true>(t.in, e0, n) : chunk_squares<false>(t.in, e0, n);
+    });
+    s = block_sum(s);
+    if (threadIdx.x == 0) part[blockIdx.x] = s;
+}
+
+// the partial sums' root, by one workgroup's threads
+MOE_DEV double norm_of(const double *__restrict__ part, int np) {
+    double s = 0.;
+    for (int i = threadIdx.x; i < np; i += 256) s += part[i];
+    return sqrt(block_sum(s));
+}
+
+__global__ __launch_bounds__(256) void grad_finish(const double *__restrict__ part, int np,
+                                                   float *__restrict__ norm) {
+    const double v = norm_of(part, np);
+    if (threadIdx.x == 0) *norm = (float)v;
+}
+
+MOE_DEV float clip_scale(double norm, float max_norm) {
+    const double q = (double)max_norm / (norm + 1e-6);
+    return q >= 1. ? 1.f : (float)q;             // a NaN stays one
+}
+
+template <bool BF16>
+MOE_DEV void chunk_scale(const GradItem &t, int64_t e0, int n, float scale) {
+    typedef Row16<BF16> R;
+    constexpr int S = BF16 ? 2 : 4;
+    const char *p = t.in + e0 * S;
+    char *o = t.out + e0 * S;
+    const int nv = n / R::N;
+    const u32x4_any *v = reinterpret_cast<const u32x4_any *>(p);
+    u32x4_any *q = reinterpret_cast<u32x4_any *>(o);
+    auto scaled = [&](const u32x4 &w) {
+        float f[R::N];
+        R::unpack(make_uint4(w.x, w.y, w.z, w.w), f);
+#pragma unroll
+        for (int e = 0; e < R::N; e++) f[e] *= scale;
+        const uint4 r = R::pack(f);
+        return u32x4{r.x, r.y, r.z, r.w};
+    };
+    if (n == kChunkBytes / S) {
+        u32x4 w[8];
+#pragma unroll
+        for (int i = 0; i < 8; i++) w[i] = v[threadIdx.x + 256 * i];
+#pragma unroll
+        for (int i = 0; i < 8; i++) q[threadIdx.x + 256 * i] = scaled(w[i]);
+    } else {
+        for (int i = threadIdx.x; i < nv; i += 256) q[i] = scaled(v[i]);
+        for (int i = nv * R::N + threadIdx.x; i < n; i += 256) {
+            const float x = grad_elem<BF16>(p, i) * scale;
+            if constexpr (BF16) reinterpret_cast<uint16_t *>(o)[i] = f32_to_bf16(x);
+            else reinterpret_cast<float *>(o)[i] = x;
+        }
+    }
+}
+
+// out = in * scale; the scale from the partial sums (part; workgroup 0 then
+// leaves the norm) or from *norm. A scale of one leaves tensors that are
+// written in place as they are.
+__global__ __launch_bounds__(256) void grad_scale(GradArgs a, const double *__restrict__ part,
+                                                  int np, float *__restrict__ norm,
+                                                  float max_norm) {
+    double v;
+    if (part) {
+        v = norm_of(part, np);
+        if (blockIdx.x == 0 && threadIdx.x == 0) *norm = (float)v;
+    } else {
+        v = *norm;
+    }
+    const float scale = clip_scale(v, max_norm);
+    for_chunks<true>(a, [&](const GradItem &t, int64_t e0, int n) {
+        if (scale == 1.f && t.in == t.out) return;
+        if (t.bf16) chunk_scale<true>(t, e0, n, scale);
+        else chunk_scale<false>(t, e0, n, scale);
+    });
+}
+
+// ---------------------------------------------------------------------------
+// launchers
+
+// The next launch's tensors of a list from item i on (empty ones left out);
+// returns the item after them.
+static int grad_args(const moe_grad *g, int n, int i, GradArgs &a) {
+    a.count = 0;
+    a.chunks = 0;
+    for (; i < n && a.count < kGradMax; i++) {
+        if (g[i].n == 0) continue;
+        const int64_t bytes = g[i].n * (g[i].dtype == MOE_BF16 ? 2 : 4);
+        GradItem &t = a.t[a.count++];
+        t.in = (const char *)g[i].data;
+        t.out = (char *)(g[i].out ? g[i].out : g[i].data);
+        t.n = g[i].n;
+        t.first = a.chunks;
+        t.bf16 = g[i].dtype == MOE_BF16;
+        a.chunks += (bytes + kChunkBytes - 1) / kChunkBytes;
+    }
+    return i;
+}
+
+static unsigned grad_blocks(const GradArgs &a) {
+    return (unsigned)(a.chunks < kGradBlocks ? a.chunks : kGradBlocks);
+}
+
+size_t grad_norm_ws_bytes(int n) {
+    return (size_t)((n + kGradMax - 1) / kGradMax) * kGradBlocks * sizeof(double);
+}
+
+// the partial sums of a list; their number
+static int grad_squares_launch(const moe_grad *g, int n, double *part, hipStream_t s) {
+    int np = 0;
+    GradArgs a;
+    for (int i = 0; i < n;) {
+        i = grad_args(g, n, i, a);
+        if (a.count == 0) break;
+        const unsigned nb = grad_blocks(a);
+        grad_squares<<<nb, 256, 0, s>>>(a, part + np);
+        np += (int)nb;
+    }
+    return np;
+}
+
+moe_status grad_norm_launch(const moe_grad *g, int n, float *norm, void *ws, hipStream_t s) {
+    const int np = grad_squares_launch(g, n, (double *)ws, s);
+    grad_finish<<<1, 256, 0, s>>>((const double *)ws, np, norm);
+    return launch_status();
+}
+
+moe_status grad_clip_launch(const moe_grad *g, int n, float max_norm, float *norm, void *ws,
+                            hipStream_t s) {
+    const double *part = nullptr;
+    int np = 0;
+    if (ws) {
+        np = grad_squares_launch(g, n, (double *)ws, s);
+        // few partial sums: every workgroup adds them itself
+        if (np > 0 && np <= kGradBlocks) part = (const double *)ws;
+        else grad_finish<<<1, 256, 0, s>>>((const double *)ws, np, norm);
+    }
+    GradArgs a;
+    for (int i = 0; i < n;) {
+        i = grad_args(g, n, i, a);
+        if (a.count == 0) break;
+        grad_scale<<<grad_blocks(a), 256, 0, s>>>(a, part, np, norm, max_norm);
+    }
+    return launch_status();
+}
+
+}  // namespace moe

@@ -28,6 +28,7 @@
 // Each kernel reads its input once and writes each output once; the encoding
 // arithmetic is about half of the time of the both-layouts kernels, memory
 // traffic the rest.
+#include "act8.h"
 #include "common.h"
 #include "mx_encode.h"
 
@@ -86,6 +87,33 @@ __global__ __launch_bounds__(256) void mx_quant_rows(const void *__restrict__ in
     for (int i = 0; i < 4; i++) w[i] = e4m3x4(f[4 * i], f[4 * i + 1], f[4 * i + 2], f[4 * i + 3], sb);
     reinterpret_cast<uint4 *>(q)[gid] = make_uint4(w[0], w[1], w[2], w[3]);
     if ((threadIdx.x & 1) == 0) scale[blk] = (uint8_t)sb;
+}
+
+// axis 1, back: the values e * 2^(sb - 127) that row blocks stand for, a vector
+// of the output a thread. An element is exact in fp32 (v_cvt_pk_f32_fp8), and so
+// is its scaling by ldexp, which keeps subnormals; scale byte 255 is a NaN.
+template <bool BF16>
+__global__ __launch_bounds__(256) void mx_dequant_rows(const typename Codes<BF16>::type *__restrict__ q,
+                                                       const uint8_t *__restrict__ scale,
+                                                       int64_t n_vec, uint4 *__restrict__ out) {
+    typedef Row16<BF16> R;
+    const int64_t v = (int64_t)blockIdx.x * 256 + threadIdx.x;
+    if (v >= n_vec) return;
+    typename Codes<BF16>::type c = load_once(q + v);
+    const uint32_t sb = scale[v / R::LPB];
+    float f[R::N];
+    const uint32_t *w = reinterpret_cast<const uint32_t *>(&c);
+#pragma unroll
+    for (int i = 0; i < R::N / 4; i++) {
+        typedef float f32x2 __attribute__((ext_vector_type(2)));
+        const f32x2 lo = __builtin_amdgcn_cvt_pk_f32_fp8((int)w[i], false);
+        const f32x2 hi = __builtin_amdgcn_cvt_pk_f32_fp8((int)w[i], true);
+        f[4 * i] = lo.x; f[4 * i + 1] = lo.y; f[4 * i + 2] = hi.x; f[4 * i + 3] = hi.y;
+    }
+#pragma unroll
+    for (int i = 0; i < R::N; i++)
+        f[i] = sb == 255 ? __builtin_nanf("") : ldexpf(f[i], (int)sb - 127);
+    out[v] = R::pack(f);
 }
 
 // Inclusive prefix sum over a 256-thread workgroup (s_w: 4 ints of LDS).
@@ -473,6 +501,27 @@ moe_status mxfp8_quantize_launch(const void *in, moe_dtype in_dt, int64_t rows, 
                 (const float *)in, rows, cols, group_offsets, n_groups, row_map, q, scale, nullptr,
                 nullptr);
     }
+    return launch_status();
+}
+
+template <bool BF16>
+static void mx_dequant_run(const uint8_t *q, const uint8_t *scale, int64_t n, void *out,
+                           hipStream_t s) {
+    typedef Row16<BF16> R;
+    typedef typename Codes<BF16>::type C;
+    const int64_t n_vec = n / R::N;
+    for (int64_t v = 0; v < n_vec; v += kMaxBlocks * 256) {
+        const int64_t m = n_vec - v < kMaxBlocks * 256 ? n_vec - v : kMaxBlocks * 256;
+        mx_dequant_rows<BF16><<<(unsigned)((m + 255) / 256), 256, 0, s>>>(
+            reinterpret_cast<const C *>(q) + v, scale + v / R::LPB, m,
+            reinterpret_cast<uint4 *>(out) + v);
+    }
+}
+
+moe_status mxfp8_dequantize_launch(const uint8_t *q, const uint8_t *scale, moe_dtype dt,
+                                   int64_t rows, int64_t cols, void *out, hipStream_t s) {
+    if (dt == MOE_BF16) mx_dequant_run<true>(q, scale, rows * cols, out, s);
+    else mx_dequant_run<false>(q, scale, rows * cols, out, s);
     return launch_status();
 }
 

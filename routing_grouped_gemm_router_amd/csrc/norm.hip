@@ -1,10 +1,15 @@
-// norm.hip -- layer norm, forward and backward.
+// norm.hip -- layer norm and root-mean-square norm, forward and backward.
 //
 //   s = x (+ res),  mu = mean(s),  r = 1 / sqrt(mean((s - mu)^2) + eps)
 //   y = (s - mu) r gamma + beta
 // and, with g = dy gamma and xh = (s - mu) r,
 //   dx = r (g - mean(g) - xh mean(g xh)) (+ dsum),
 //   dgamma = sum_t dy xh,  dbeta = sum_t dy.
+// The root-mean-square norm (RMS) is the same without a mean and without beta:
+//   r = 1 / sqrt(mean(s^2) + eps),  y = s r gamma,
+//   dx = r (g - xh mean(g xh)) (+ dsum),  dgamma = sum_t dy xh,  xh = s r.
+// It can write y as MXFP8 too, or alone (mx_encode.h), the rows that the 8-bit
+// experts take: the bytes that quantising the stored y gives.
 // s may be kept between the two passes as an 8-bit checkpoint (act8.h),
 // written from the forward's registers and read by the backward in place of
 // s. All sums and statistics are fp32, in a fixed order (no atomics); the
@@ -21,8 +26,29 @@
 // (the ends of the backward's range: few columns a thread to sum over, or no
 // registers to load ahead).
 #include "act8.h"
+#include "mx_encode.h"
 
 namespace moe {
+
+// The MXFP8 bytes and scale of this lane's vector of a block of 32 (f: its
+// elements as the norm's type rounds them). The block's 4 (bf16) or 8 (fp32)
+// neighbouring lanes must be active.
+template <bool BF16>
+MOE_DEV uint32_t mx_encode_vec(const float *f, typename Codes<BF16>::type &q) {
+    float m = 0.f;
+#pragma unroll
+    for (int e = 0; e < Row16<BF16>::N; e++) m = fmaxf(m, fabsf(f[e]));
+    m = fmaxf(m, dpp_move<kDppXor1>(m));
+    m = fmaxf(m, dpp_move<kDppXor2>(m));
+    if constexpr (!BF16) m = fmaxf(m, dpp_move<kDppHalfMirror>(m));
+    const uint32_t sb = mx_scale_byte(m);
+    if constexpr (BF16) {
+        q.x = e4m3x4(f[0], f[1], f[2], f[3], sb);
+        q.y = e4m3x4(f[4], f[5], f[6], f[7], sb);
+    } else
+        q = e4m3x4(f[0], f[1], f[2], f[3], sb);
+    return sb;
+}
 
 // Sum of v over the threads of a row within their wave: G = 4, 8, 16, 32 or
 // all 64 neighbouring lanes (G >= 64).
@@ -84,13 +110,15 @@ MOE_DEV void load_params(const float *p, int c, float *f) {
 }
 
 // G threads a row, V 16-byte vectors a thread (vector lane + i G of the row).
-template <bool BF16, int G, int V>
+// RMS: no mean (and none stored), no beta; y may be null if yq is not.
+template <bool BF16, int G, int V, bool RMS>
 __global__ __launch_bounds__(norm_threads(G)) void norm_fwd(
     const uint4 *__restrict__ x, const uint4 *__restrict__ res, const float *__restrict__ gamma,
     const float *__restrict__ beta, float eps, int64_t T, int nv, float inv_d,
     uint4 *__restrict__ y, uint4 *__restrict__ sum, float *__restrict__ mean,
     float *__restrict__ rstd, typename Codes<BF16>::type *__restrict__ x8,
-    uint8_t *__restrict__ x8_scale) {
+    uint8_t *__restrict__ x8_scale, typename Codes<BF16>::type *__restrict__ yq,
+    uint8_t *__restrict__ yq_scale) {
     typedef Row16<BF16> R;
     __shared__ float red[2][16];
     const int lane = threadIdx.x % G;
@@ -117,21 +145,26 @@ __global__ __launch_bounds__(norm_threads(G)) void norm_fwd(
             R::unpack(w[i], f);
         }
 #pragma unroll
-        for (int e = 0; e < R::N; e++) s1 += f[e];
+        for (int e = 0; e < R::N; e++) s1 = RMS ? fmaf(f[e], f[e], s1) : s1 + f[e];
     }
-    const float mu = row_sum<G>(s1, red[0]) * inv_d;
-    float s2 = 0.f;
+    s1 = row_sum<G>(s1, red[0]);
+    float mu = 0.f, s2 = s1;
+    if constexpr (!RMS) {
+        mu = s1 * inv_d;
+        s2 = 0.f;
 #pragma unroll
-    for (int i = 0; i < V; i++) {
-        if (lane + i * G >= nv) continue;
-        float f[R::N];
-        R::unpack(w[i], f);
+        for (int i = 0; i < V; i++) {
+            if (lane + i * G >= nv) continue;
+            float f[R::N];
+            R::unpack(w[i], f);
 #pragma unroll
-        for (int e = 0; e < R::N; e++) s2 = fmaf(f[e] - mu, f[e] - mu, s2);
+            for (int e = 0; e < R::N; e++) s2 = fmaf(f[e] - mu, f[e] - mu, s2);
+        }
+        s2 = row_sum<G>(s2, red[1]);
     }
-    const float r = 1.f / sqrtf(fmaf(row_sum<G>(s2, red[1]), inv_d, eps));
+    const float r = 1.f / sqrtf(fmaf(s2, inv_d, eps));
     if (lane == 0) {
-        if (mean) mean[t] = mu;
+        if (!RMS && mean) mean[t] = mu;
         if (rstd) rstd[t] = r;
     }
 #pragma unroll
@@ -142,13 +175,21 @@ __global__ __launch_bounds__(norm_threads(G)) void norm_fwd(
         R::unpack(w[i], f);
         load_params<BF16>(gamma, c, ga);
 #pragma unroll
-        for (int e = 0; e < R::N; e++) o[e] = (f[e] - mu) * r * ga[e];
-        if (beta) {
+        for (int e = 0; e < R::N; e++) o[e] = (RMS ? f[e] : f[e] - mu) * r * ga[e];
+        if (!RMS && beta) {
             load_params<BF16>(beta, c, ga);
 #pragma unroll
             for (int e = 0; e < R::N; e++) o[e] += ga[e];
         }
-        y[base + c] = R::pack(o);
+        const uint4 p = R::pack(o);
+        if (!RMS || y) y[base + c] = p;
+        if (RMS && yq) {
+            typename Codes<BF16>::type q;
+            R::unpack(p, o);
+            const uint32_t sb = mx_encode_vec<BF16>(o, q);
+            yq[base + c] = q;
+            if (c % R::LPB == 0) yq_scale[(base + c) / R::LPB] = (uint8_t)sb;
+        }
         if (x8) {
             const uint32_t sb = act8_scale_byte<BF16>(w[i]);
             typename Codes<BF16>::type q;
@@ -175,7 +216,8 @@ struct NormRow {
 // of it is computed: with two workgroups a compute unit (so that the partial
 // sums stay small) nothing else would hide the two reductions of a row (16384 x
 // 2048 74.7 -> 53.4 us, 32768 x 4096 267 -> 180 us).
-template <bool BF16, int G, int V, bool CKPT>
+// RMS: mean is not read, and the workgroups leave part[blockIdx.x][d].
+template <bool BF16, int G, int V, bool CKPT, bool RMS>
 __global__ __launch_bounds__(norm_threads(G)) void norm_bwd(
     const uint4 *__restrict__ dy, const uint4 *__restrict__ x,
     const typename Codes<BF16>::type *__restrict__ x8, const uint8_t *__restrict__ x8_scale,
@@ -202,7 +244,7 @@ __global__ __launch_bounds__(norm_threads(G)) void norm_bwd(
     auto load = [&](Row &w, int64_t t) {
         if (t >= T) return;
         const int64_t base = t * nv;
-        w.mu = mean[t];
+        w.mu = RMS ? 0.f : mean[t];
         w.r = rstd[t];
 #pragma unroll
         for (int i = 0; i < V; i++) {
@@ -239,25 +281,27 @@ __global__ __launch_bounds__(norm_threads(G)) void norm_bwd(
             if (RELOAD) load_params<BF16>(gamma, lane + i * G, ga + i * R::N);
 #pragma unroll
             for (int e = 0; e < R::N; e++) {
-                const float h = (f[e] - w.mu) * w.r;
+                const float h = (RMS ? f[e] : f[e] - w.mu) * w.r;
                 xh[i * R::N + e] = h;
                 dg[i * R::N + e] = fmaf(g[e], h, dg[i * R::N + e]);
-                db[i * R::N + e] += g[e];
                 const float gw = g[e] * ga[i * R::N + e];
-                c1 += gw;
+                if constexpr (!RMS) {
+                    db[i * R::N + e] += g[e];
+                    c1 += gw;
+                }
                 c2 = fmaf(gw, h, c2);
             }
         }
-        c1 = group_sum<G>(c1);
+        if constexpr (!RMS) c1 = group_sum<G>(c1);
         c2 = group_sum<G>(c2);
         if constexpr (G >= 256) {
             // one barrier a row: the next row writes the other half
             if ((threadIdx.x & 63) == 0) {
-                red[par][0][threadIdx.x >> 6] = c1;
+                if constexpr (!RMS) red[par][0][threadIdx.x >> 6] = c1;
                 red[par][1][threadIdx.x >> 6] = c2;
             }
             __syncthreads();
-            c1 = waves_sum<G>(red[par][0]);
+            if constexpr (!RMS) c1 = waves_sum<G>(red[par][0]);
             c2 = waves_sum<G>(red[par][1]);
         }
         c1 *= inv_d;
@@ -284,12 +328,12 @@ __global__ __launch_bounds__(norm_threads(G)) void norm_bwd(
     if (!part) return;
     // the workgroup's rows together, in the order of their row slots
     const int64_t d = (int64_t)nv * R::N;
-    float *pg = part + (int64_t)blockIdx.x * 2 * d, *pb = pg + d;
+    float *pg = part + (int64_t)blockIdx.x * (RMS ? 1 : 2) * d, *pb = pg + d;
 #pragma unroll
     for (int i = 0; i < V; i++) {
         const int c = lane + i * G;
 #pragma unroll
-        for (int z = 0; z < 2; z++) {
+        for (int z = 0; z < (RMS ? 1 : 2); z++) {
             float *a = (z ? db : dg) + i * R::N, *p = z ? pb : pg;
             if constexpr (G >= 256) {
                 if (c < nv)
@@ -315,7 +359,7 @@ __global__ __launch_bounds__(norm_threads(G)) void norm_bwd(
     }
 }
 
-// dgamma, dbeta = (+=) the workgroups' sums: 32 columns a workgroup, the sums
+// dgamma, dbeta (gridDim.y = 2; 1: dgamma alone) = (+=) the workgroups' sums: 32 columns a workgroup, the sums
 // dealt to 32 slices (16 loads of each in flight), the slices added in order.
 // Bound by latency: 512 sums of 2 x 2048 columns (8.4 MB) in 4.6 us; one load at
 // a time took 17 us.
@@ -323,7 +367,7 @@ __global__ __launch_bounds__(1024) void norm_bwd_params(const float *__restrict_
                                                         int d, float *__restrict__ dgamma,
                                                         float *__restrict__ dbeta, int accumulate) {
     __shared__ float s_p[32][33];
-    const int z = blockIdx.y;
+    const int z = blockIdx.y, nz = gridDim.y;
     float *out = z ? dbeta : dgamma;
     if (!out) return;
     const int col = blockIdx.x * 32 + (threadIdx.x & 31), sl = threadIdx.x >> 5;
@@ -332,7 +376,7 @@ __global__ __launch_bounds__(1024) void norm_bwd_params(const float *__restrict_
     for (int i0 = sl; i0 < np; i0 += 32 * 16) {
         float v[16];
 #pragma unroll
-        for (int i = 0; i < 16; i++) v[i] = i0 + 32 * i < np ? p[(int64_t)(i0 + 32 * i) * 2 * d] : 0.f;
+        for (int i = 0; i < 16; i++) v[i] = i0 + 32 * i < np ? p[(int64_t)(i0 + 32 * i) * nz * d] : 0.f;
 #pragma unroll
         for (int i = 0; i < 16; i++) s += v[i];
     }
@@ -397,11 +441,11 @@ constexpr bool norm_used(int g, int v, bool bwd) {
     NORM_IFS(4, BWD, F) NORM_IFS(8, BWD, F) NORM_IFS(16, BWD, F) NORM_IFS(32, BWD, F)        \
     NORM_IFS(64, BWD, F) NORM_IFS(256, BWD, F) NORM_IFS(512, BWD, F) NORM_IFS(1024, BWD, F)
 
-template <bool BF16>
+template <bool BF16, bool RMS>
 static moe_status norm_fwd_run(const void *x, const void *res, const float *gamma,
                                const float *beta, float eps, int64_t T, int d, void *y, void *sum,
                                float *mean, float *rstd, uint8_t *x8, uint8_t *x8_scale,
-                               hipStream_t s) {
+                               uint8_t *yq, uint8_t *yq_scale, hipStream_t s) {
     typedef typename Codes<BF16>::type C;
     const int nv = d / Row16<BF16>::N, g = norm_group(nv, false), v = norm_vecs(nv, false);
     const int nt = norm_threads(g), rows = nt / g;
@@ -412,10 +456,11 @@ static moe_status norm_fwd_run(const void *x, const void *res, const float *gamm
         const unsigned nb = (unsigned)((n + rows - 1) / rows);
         const int64_t o = t * nv;
 #define F(G, V)                                                                                  \
-    norm_fwd<BF16, G, V><<<nb, nt, 0, s>>>(                                                      \
+    norm_fwd<BF16, G, V, RMS><<<nb, nt, 0, s>>>(                                                 \
         at<const uint4>(x, o), at<const uint4>(res, o), gamma, beta, eps, n, nv, inv_d,          \
         at<uint4>(y, o), at<uint4>(sum, o), at<float>(mean, t), at<float>(rstd, t), at<C>(x8, o), \
-        at<uint8_t>(x8_scale, o / Row16<BF16>::LPB))
+        at<uint8_t>(x8_scale, o / Row16<BF16>::LPB), at<C>(yq, o),                               \
+        at<uint8_t>(yq_scale, o / Row16<BF16>::LPB))
         NORM_SWITCH(false, F)
 #undef F
     }
@@ -427,8 +472,17 @@ moe_status norm_fwd_launch(const void *x, moe_dtype dt, const void *res, const f
                            float *mean, float *rstd, uint8_t *x8, uint8_t *x8_scale,
                            hipStream_t s) {
     return dt == MOE_BF16
-               ? norm_fwd_run<true>(x, res, gamma, beta, eps, T, d, y, sum, mean, rstd, x8, x8_scale, s)
-               : norm_fwd_run<false>(x, res, gamma, beta, eps, T, d, y, sum, mean, rstd, x8, x8_scale, s);
+               ? norm_fwd_run<true, false>(x, res, gamma, beta, eps, T, d, y, sum, mean, rstd, x8, x8_scale, nullptr, nullptr, s)
+               : norm_fwd_run<false, false>(x, res, gamma, beta, eps, T, d, y, sum, mean, rstd, x8, x8_scale, nullptr, nullptr, s);
+}
+
+moe_status rms_fwd_launch(const void *x, moe_dtype dt, const void *res, const float *gamma,
+                          float eps, int64_t T, int d, void *y, void *sum, float *rstd,
+                          uint8_t *x8, uint8_t *x8_scale, uint8_t *yq, uint8_t *yq_scale,
+                          hipStream_t s) {
+    return dt == MOE_BF16
+               ? norm_fwd_run<true, true>(x, res, gamma, nullptr, eps, T, d, y, sum, nullptr, rstd, x8, x8_scale, yq, yq_scale, s)
+               : norm_fwd_run<false, true>(x, res, gamma, nullptr, eps, T, d, y, sum, nullptr, rstd, x8, x8_scale, yq, yq_scale, s);
 }
 
 // Workgroups of the backward, and rows of its partial sums: by the sizes
@@ -449,8 +503,9 @@ static int64_t norm_bwd_blocks(int64_t T, int nv) {
 size_t norm_bwd_ws_bytes(moe_dtype dt, int64_t T, int d) {
     return (size_t)norm_bwd_blocks(T, d / (dt == MOE_BF16 ? 8 : 4)) * 2 * d * sizeof(float);
 }
+size_t rms_bwd_ws_bytes(moe_dtype dt, int64_t T, int d) { return norm_bwd_ws_bytes(dt, T, d) / 2; }
 
-template <bool BF16>
+template <bool BF16, bool RMS>
 static moe_status norm_bwd_run(const void *dy, const void *x, const uint8_t *x8,
                                const uint8_t *x8_scale, const float *mean, const float *rstd,
                                const float *gamma, const void *dsum, int64_t T, int d, void *dx,
@@ -461,7 +516,7 @@ static moe_status norm_bwd_run(const void *dy, const void *x, const uint8_t *x8,
     const int np = (int)norm_bwd_blocks(T, nv);
     const float inv_d = 1.f / (float)d;
 #define F2(G, V, K)                                                                              \
-    norm_bwd<BF16, G, V, K><<<np, norm_threads(G), 0, s>>>(                                      \
+    norm_bwd<BF16, G, V, K, RMS><<<np, norm_threads(G), 0, s>>>(                                      \
         at<const uint4>(dy, 0), at<const uint4>(x, 0), at<const C>(x8, 0), x8_scale, mean, rstd, \
         gamma, at<const uint4>(dsum, 0), T, nv, inv_d, at<uint4>(dx, 0), part)
 #define F(G, V) if (x8) F2(G, V, true); else F2(G, V, false)
@@ -469,7 +524,7 @@ static moe_status norm_bwd_run(const void *dy, const void *x, const uint8_t *x8,
 #undef F
 #undef F2
     if (dgamma || dbeta)
-        norm_bwd_params<<<dim3(d / 32, 2), 1024, 0, s>>>(part, np, d, dgamma, dbeta, accumulate);
+        norm_bwd_params<<<dim3(d / 32, RMS ? 1 : 2), 1024, 0, s>>>(part, np, d, dgamma, dbeta, accumulate);
     return launch_status();
 }
 
@@ -479,8 +534,17 @@ moe_status norm_bwd_launch(const void *dy, moe_dtype dt, const void *x, const ui
                            float *dgamma, float *dbeta, bool accumulate, float *part,
                            hipStream_t s) {
     return dt == MOE_BF16
-               ? norm_bwd_run<true>(dy, x, x8, x8_scale, mean, rstd, gamma, dsum, T, d, dx, dgamma, dbeta, accumulate, part, s)
-               : norm_bwd_run<false>(dy, x, x8, x8_scale, mean, rstd, gamma, dsum, T, d, dx, dgamma, dbeta, accumulate, part, s);
+               ? norm_bwd_run<true, false>(dy, x, x8, x8_scale, mean, rstd, gamma, dsum, T, d, dx, dgamma, dbeta, accumulate, part, s)
+               : norm_bwd_run<false, false>(dy, x, x8, x8_scale, mean, rstd, gamma, dsum, T, d, dx, dgamma, dbeta, accumulate, part, s);
+}
+
+moe_status rms_bwd_launch(const void *dy, moe_dtype dt, const void *x, const uint8_t *x8,
+                          const uint8_t *x8_scale, const float *rstd, const float *gamma,
+                          const void *dsum, int64_t T, int d, void *dx, float *dgamma,
+                          bool accumulate, float *part, hipStream_t s) {
+    return dt == MOE_BF16
+               ? norm_bwd_run<true, true>(dy, x, x8, x8_scale, nullptr, rstd, gamma, dsum, T, d, dx, dgamma, nullptr, accumulate, part, s)
+               : norm_bwd_run<false, true>(dy, x, x8, x8_scale, nullptr, rstd, gamma, dsum, T, d, dx, dgamma, nullptr, accumulate, part, s);
 }
 
 }  // namespace moe
