@@ -1813,8 +1813,10 @@ class MoELayerMX:
         """Quantised dispatch of x and GEMM1 + SwiGLU (forward, and again in
         the backward when recomputing). quantised_hp: H' goes straight to its
         two MXFP8 layouts instead of bf16."""
-        q, s = xq or mxfp8_quantize(x, 1, q=self.xq, scale=self.xs)
-        moe_permute(q, token_pos, self.xpq, x_scale=s, x_perm_scale=self.xps)
+        if xq is None:
+            mxfp8_quantize(x, 1, q=self.xq, scale=self.xs)
+            xq = self.xq, self.xs
+        moe_permute(xq[0], token_pos, self.xpq, x_scale=xq[1], x_perm_scale=self.xps)
         hp = (dict(aux_out=self.hpq, aux_out_scale=self.hps, aux_out_cols=self.hpc,
                    aux_out_cols_scale=self.hpcs) if quantised_hp else dict(aux_out=self.hp))
         moe_grouped_gemm(MOE_GG_FWD, self.xpq, self.w1q, self.ab, offsets, MOE_EPI_SWIGLU_FWD,
