@@ -35,7 +35,7 @@ from collections import defaultdict
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 # the sources that make up the grouped GEMM kernel
-GEMM_SOURCES = ("csrc/gemm.hip", "csrc/copy_plan.h", "csrc/common.h", "csrc/mx_encode.h",
+GEMM_SOURCES = ("csrc/gemm.hip", "csrc/gemm_device.h", "csrc/copy_plan.h", "csrc/common.h", "csrc/mx_encode.h",
                 "../include/moe.h")
 # the sources of the row movers, the routing kernels and the MXFP8 quantisers
 ROW_SOURCES = ("csrc/rows.hip", "csrc/route.hip", "csrc/mxfp8.hip", "csrc/common.h",
