@@ -770,6 +770,51 @@ typedef struct moe_w4_desc {
 size_t moe_w4_experts_workspace_size(int64_t T, int32_t k, int32_t d, int32_t h);
 moe_status moe_w4_experts(const moe_w4_desc *w, void *stream);
 
+/* ------------------------------------------------------------------ */
+/* Products of 8-bit rows with 4-bit weights, grouped by expert          */
+
+/* C[r, n] = sum_k A[src(r), k] * B[g][n, k] for the rows r in [offsets[g],
+ * offsets[g+1]) of group g, src(r) = a_rows[r], or r where a_rows is null:
+ * the forward of moe_grouped_gemm with weights in 4 bits, for the many rows of
+ * a prompt or a training batch. Both operands are widened by nothing: MXFP8
+ * and MXFP4 values meet in the matrix units, sums are fp32.
+ *   a, a_scale  MXFP8 along its rows, [*, K] and [*, K/32] (mxfp8_quantize
+ *               axis 1, moe_rms_norm's yq); every src(r) is one of its rows
+ *   b, b_scale  MXFP4 [E, N, K/2], [E, N, K/32] (moe_w4_quantize)
+ *   epilogue MOE_EPI_NONE: c = C in bf16 [rows, N], c_scale null; N a
+ *               multiple of 32
+ *   epilogue MOE_EPI_SWIGLU_FWD (N = 2h, gate rows first): H' = silu(a) b in
+ *               fp32, rounded once, to MXFP8 along h: c [rows, h] and c_scale
+ *               [rows, h/32]; the gate and up values are not stored. h a
+ *               multiple of 32, at most 8192
+ * rows = offsets[n_groups] < 2^31; K: a multiple of 128, K and N at most
+ * 16384; a, b and c 16-byte, the scales 4-byte aligned. A row with NaNs reaches
+ * no other. Rows outside all groups are not written; rows = 0 is a no-op. */
+typedef struct moe_w4_gemm_desc {
+    int32_t n_groups;
+    int32_t epilogue;
+    int64_t rows;
+    int32_t N, K;
+    const int32_t *offsets;
+    const int32_t *a_rows;
+    const uint8_t *a;
+    const uint8_t *a_scale;
+    const uint8_t *b;
+    const uint8_t *b_scale;
+    void *c;
+    uint8_t *c_scale;
+} moe_w4_gemm_desc;
+
+moe_status moe_w4_gemm(const moe_w4_gemm_desc *g, void *stream);
+
+/* moe_w4_experts for the many tokens of a prompt: x comes in MXFP8 (w->x the
+ * E4M3 bytes [T, d], x_scale [T, d/32], 4-byte aligned) and H' is rounded to
+ * MXFP8 along h between the two products (moe_w4_gemm), the experts' outputs to
+ * bf16 in front of the combine. d and h: multiples of 128; the rest as in
+ * moe_w4_experts, but for ws: moe_w4_experts8_workspace_size bytes. */
+size_t moe_w4_experts8_workspace_size(int64_t T, int32_t k, int32_t d, int32_t h);
+moe_status moe_w4_experts8(const moe_w4_desc *w, const uint8_t *x_scale, void *stream);
+
 #ifdef __cplusplus
 }
 #endif

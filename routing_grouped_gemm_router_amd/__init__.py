@@ -75,6 +75,12 @@ class W4Desc(ctypes.Structure):
                 ("ws", _P), ("ws_bytes", _SZ)]
 
 
+class W4GemmDesc(ctypes.Structure):
+    _fields_ = [("n_groups", _I32), ("epilogue", _I32), ("rows", _I64), ("N", _I32), ("K", _I32),
+                ("offsets", _P), ("a_rows", _P), ("a", _P), ("a_scale", _P), ("b", _P),
+                ("b_scale", _P), ("c", _P), ("c_scale", _P)]
+
+
 class BwdWsLayout(ctypes.Structure):
     _fields_ = [(n, _SZ) for n in ("row_q", "row_s", "col0_q", "col0_s", "col1_q", "col1_s",
                                    "total")]
@@ -181,6 +187,12 @@ def _load():
     lib.moe_w4_experts_workspace_size.restype = _SZ
     lib.moe_w4_experts.argtypes = [ctypes.POINTER(W4Desc), _P]
     lib.moe_w4_experts.restype = _I32
+    lib.moe_w4_gemm.argtypes = [ctypes.POINTER(W4GemmDesc), _P]
+    lib.moe_w4_gemm.restype = _I32
+    lib.moe_w4_experts8_workspace_size.argtypes = [_I64, _I32, _I32, _I32]
+    lib.moe_w4_experts8_workspace_size.restype = _SZ
+    lib.moe_w4_experts8.argtypes = [ctypes.POINTER(W4Desc), _P, _P]
+    lib.moe_w4_experts8.restype = _I32
     return lib
 
 
@@ -1176,15 +1188,9 @@ def moe_w4_experts_workspace_size(T: int, k: int, d: int, h: int) -> int:
     return _lib.moe_w4_experts_workspace_size(T, k, d, h)
 
 
-def moe_w4_experts(x: torch.Tensor, route: dict, w1q: torch.Tensor, w1_scale: torch.Tensor,
-                   w2q: torch.Tensor, w2_scale: torch.Tensor, out: torch.Tensor | None = None,
-                   ws: torch.Tensor | None = None) -> torch.Tensor:
-    """The expert layer's forward for few tokens after the routing, weights
-    as moe_w4_quantize writes them (see moe.h). route: moe_route's dict for
-    these tokens (topk_gate, token_pos, sorted_token, offsets are read)."""
-    T, d, dt, gpu = _act_matrix(x, "x")
-    if dt != MOE_BF16:
-        raise ValueError(f"x: expected bf16, got {x.dtype}")
+def _w4_operands(T, d, route, w1q, w1_scale, w2q, w2_scale, gpu):
+    """E, k, h of the experts' calls, their operands checked, and the
+    routing's tensors that they read."""
     u8, i32 = torch.uint8, torch.int32
     if w1q is None or w1q.dim() != 3 or w1q.shape[1] % 64:
         raise ValueError("w1q: expected [E, 2h, d/2] with h a multiple of 32")
@@ -1201,6 +1207,19 @@ def moe_w4_experts(x: torch.Tensor, route: dict, w1q: torch.Tensor, w1_scale: to
     _need_on(pos, (T, k), i32, gpu, "token_pos")
     _need_on(tok, (T * k,), i32, gpu, "sorted_token")
     _need_on(off, (E + 1,), i32, gpu, "offsets")
+    return E, k, h, gate, pos, tok, off
+
+
+def moe_w4_experts(x: torch.Tensor, route: dict, w1q: torch.Tensor, w1_scale: torch.Tensor,
+                   w2q: torch.Tensor, w2_scale: torch.Tensor, out: torch.Tensor | None = None,
+                   ws: torch.Tensor | None = None) -> torch.Tensor:
+    """The expert layer's forward for few tokens after the routing, weights
+    as moe_w4_quantize writes them (see moe.h). route: moe_route's dict for
+    these tokens (topk_gate, token_pos, sorted_token, offsets are read)."""
+    T, d, dt, gpu = _act_matrix(x, "x")
+    if dt != MOE_BF16:
+        raise ValueError(f"x: expected bf16, got {x.dtype}")
+    E, k, h, gate, pos, tok, off = _w4_operands(T, d, route, w1q, w1_scale, w2q, w2_scale, gpu)
     if out is None:
         out = torch.empty_like(x)
     else:
@@ -1210,6 +1229,69 @@ def moe_w4_experts(x: torch.Tensor, route: dict, w1q: torch.Tensor, w1_scale: to
                off.data_ptr(), w1q.data_ptr(), w1_scale.data_ptr(), w2q.data_ptr(),
                w2_scale.data_ptr(), out.data_ptr(), ws.data_ptr(), ws.numel())
     _enqueue("moe_w4_experts", _lib.moe_w4_experts, gpu, ctypes.byref(w))
+    return out
+
+
+def moe_w4_gemm(a: torch.Tensor, a_scale: torch.Tensor, bq: torch.Tensor, b_scale: torch.Tensor,
+                offsets: torch.Tensor, epilogue: int = MOE_EPI_NONE,
+                a_rows: torch.Tensor | None = None, out: torch.Tensor | None = None,
+                out_scale: torch.Tensor | None = None):
+    """Grouped product of MXFP8 rows with MXFP4 weights (see moe.h): a [*, K]
+    and a_scale, bq [E, N, K/2] and b_scale, offsets [E+1]. a_rows (int32): row
+    r of the product reads a[a_rows[r]]; else a's rows are the product's.
+    Returns out, bf16 [rows, N]; with MOE_EPI_SWIGLU_FWD (out, out_scale), H' in
+    MXFP8 [rows, N/2]. offsets[E] and a_rows stay within the tensors: the
+    caller's to keep, they are read on the device."""
+    total, K, _, gpu = _act8_in(a, a_scale, torch.bfloat16, "a")
+    if bq is None or bq.dim() != 3:
+        raise ValueError("bq: expected [E, N, K/2]")
+    E, N = bq.shape[0], bq.shape[1]
+    _need_on(bq, (E, N, K // 2), torch.uint8, gpu, "bq")
+    _need_on(b_scale, (E, N, K // 32), torch.uint8, gpu, "b_scale")
+    _need_on(offsets, (E + 1,), torch.int32, gpu, "offsets")
+    rows = total
+    if a_rows is not None:
+        rows = a_rows.numel()
+        _need_on(a_rows, (rows,), torch.int32, gpu, "a_rows")
+    swiglu = epilogue == MOE_EPI_SWIGLU_FWD
+    if swiglu:
+        if N % 64:
+            raise ValueError(f"bq: N = 2h with h a multiple of 32, got {N}")
+        out, out_scale = _act8_out(rows, N // 2, a, gpu, out, out_scale, "out")
+    elif out is None:
+        out = torch.empty(rows, N, dtype=torch.bfloat16, device=a.device)
+    else:
+        _need_on(out, (rows, N), torch.bfloat16, gpu, "out")
+    if not swiglu and out_scale is not None:
+        raise ValueError("out_scale: only the SwiGLU epilogue writes 8 bits")
+    g = W4GemmDesc(E, epilogue, rows, N, K, offsets.data_ptr(), _ptr(a_rows), a.data_ptr(),
+                   a_scale.data_ptr(), bq.data_ptr(), b_scale.data_ptr(), out.data_ptr(),
+                   _ptr(out_scale))
+    _enqueue("moe_w4_gemm", _lib.moe_w4_gemm, gpu, ctypes.byref(g))
+    return (out, out_scale) if swiglu else out
+
+
+def moe_w4_experts8_workspace_size(T: int, k: int, d: int, h: int) -> int:
+    return _lib.moe_w4_experts8_workspace_size(T, k, d, h)
+
+
+def moe_w4_experts8(xq: torch.Tensor, x_scale: torch.Tensor, route: dict, w1q: torch.Tensor,
+                    w1_scale: torch.Tensor, w2q: torch.Tensor, w2_scale: torch.Tensor,
+                    out: torch.Tensor | None = None,
+                    ws: torch.Tensor | None = None) -> torch.Tensor:
+    """moe_w4_experts for the many tokens of a prompt, their rows in MXFP8
+    (xq [T, d], x_scale [T, d/32]; see moe.h): out [T, d] bf16."""
+    T, d, _, gpu = _act8_in(xq, x_scale, torch.bfloat16, "xq")
+    E, k, h, gate, pos, tok, off = _w4_operands(T, d, route, w1q, w1_scale, w2q, w2_scale, gpu)
+    if out is None:
+        out = torch.empty(T, d, dtype=torch.bfloat16, device=xq.device)
+    else:
+        _need_on(out, (T, d), torch.bfloat16, gpu, "out")
+    ws = _need_ws(ws, moe_w4_experts8_workspace_size(T, k, d, h), xq, gpu)
+    w = W4Desc(d, h, E, k, T, xq.data_ptr(), gate.data_ptr(), pos.data_ptr(), tok.data_ptr(),
+               off.data_ptr(), w1q.data_ptr(), w1_scale.data_ptr(), w2q.data_ptr(),
+               w2_scale.data_ptr(), out.data_ptr(), ws.data_ptr(), ws.numel())
+    _enqueue("moe_w4_experts8", _lib.moe_w4_experts8, gpu, ctypes.byref(w), x_scale.data_ptr())
     return out
 
 
@@ -1916,7 +1998,10 @@ class MoELayerW4:
     launches alone and can be captured in a HIP graph, one for each batch
     size; calls (or replays) of one layer object must not overlap in time,
     they share its buffers. Those stay for every T that a captured graph uses,
-    for the last T, and for small earlier ones (64 MiB in all)."""
+    for the last T, and for small earlier ones (64 MiB in all).
+
+    prompt() is the same for a prompt's many tokens, with rows and H' in MXFP8
+    (moe_w4_experts8; d and h multiples of 128)."""
 
     def __init__(self, w1: torch.Tensor, w2: torch.Tensor, k: int):
         self.E, h2, self.d = w1.shape
@@ -1941,24 +2026,51 @@ class MoELayerW4:
     def forward(self, x: torch.Tensor, logits: torch.Tensor) -> torch.Tensor:
         if x.dim() != 2 or x.shape[1] != self.d or x.dtype != torch.bfloat16:
             raise ValueError(f"x: expected bf16 [T, {self.d}], got {x.dtype} {tuple(x.shape)}")
-        T, dev, gpu = x.shape[0], self.w1q.device, self.w1q.get_device()
+        T, gpu = x.shape[0], self.w1q.get_device()
         _need_on(x, (T, self.d), torch.bfloat16, gpu, "x")
+        buf = self._route(logits, T, gpu, (T, gpu), moe_w4_experts_workspace_size)
+        self.out = moe_w4_experts(x, self.route, self.w1q, self.w1s, self.w2q, self.w2s,
+                                  buf["out"], buf["ws"])
+        _mark(buf, gpu)
+        return self.out
+
+    def prompt(self, x: torch.Tensor | None, logits: torch.Tensor,
+               xq: tuple | None = None) -> torch.Tensor:
+        """The forward of a prompt's T tokens. xq: x in MXFP8 along its rows
+        (elements [T, d], scales [T, d/32]), where the norm in front has written
+        it (RMSNorm.q); x may then be None. Else the layer quantises x (bf16)."""
+        gpu, T = self.w1q.get_device(), logits.shape[0]
+        if xq is None:
+            _need_on(x, (T, self.d), torch.bfloat16, gpu, "x")
+        else:
+            _act8_need(xq[0], xq[1], T, self.d, gpu, "xq")
+        buf = self._route(logits, T, gpu, (T, gpu, "prompt"), moe_w4_experts8_workspace_size)
+        if xq is None:
+            if "xq" not in buf:
+                buf["xq"], buf["xs"] = _act8_new(T, self.d, self.w1q.device)
+            xq = buf["xq"], buf["xs"]
+            with torch.cuda.device(gpu):
+                mxfp8_quantize(x, 1, q=xq[0], scale=xq[1])
+        self.out = moe_w4_experts8(xq[0], xq[1], self.route, self.w1q, self.w1s, self.w2q, self.w2s,
+                                   buf["out"], buf["ws"])
+        _mark(buf, gpu)
+        return self.out
+
+    def _route(self, logits, T, gpu, key, ws_size) -> dict:
+        """The buffers of a size, with the routing of its logits in them."""
         _need_on(logits, (T, self.E), torch.float32, gpu, "logits")
-        if self._T != (T, gpu):
-            self._buf, self._T = self._sizes.at((T, gpu)), (T, gpu)
-        buf = self._buf
+        if self._T != key:
+            self._buf, self._T = self._sizes.at(key), key
+        buf, dev = self._buf, self.w1q.device
         with torch.cuda.device(gpu):
             if "out" not in buf:
                 self.route = self.route_ws = self.ws = self.out = None
                 u8 = lambda n: torch.empty(n, dtype=torch.uint8, device=dev)
-                wsb = moe_w4_experts_workspace_size(T, self.k, self.d, self.h)
-                buf.update(route=None, out=torch.empty((T, self.d), dtype=x.dtype, device=dev),
+                wsb = ws_size(T, self.k, self.d, self.h)
+                buf.update(route=None, out=torch.empty((T, self.d), dtype=torch.bfloat16, device=dev),
                            route_ws=u8(max(moe_route_workspace_size(T, self.E, self.k), 1)),
                            ws=u8(max(wsb, 16)))
             self.route = buf["route"] = moe_route(logits, self.k, out=buf["route"],
                                                   ws=buf["route_ws"])
         self.route_ws, self.ws = buf["route_ws"], buf["ws"]
-        self.out = moe_w4_experts(x, self.route, self.w1q, self.w1s, self.w2q, self.w2s,
-                                  buf["out"], buf["ws"])
-        _mark(buf, gpu)
-        return self.out
+        return buf

@@ -97,6 +97,9 @@ moe_status w4_quantize_launch(const void *in, moe_dtype dt, int64_t rows, int64_
                               uint8_t *scale, hipStream_t s);
 size_t w4_ws_bytes(int64_t R, int d, int h);
 moe_status w4_experts_launch(const moe_w4_desc *w, hipStream_t s);
+moe_status w4_gemm_launch(const moe_w4_gemm_desc &g, hipStream_t s);
+size_t w4_experts8_ws_bytes(int64_t R, int d, int h);
+moe_status w4_experts8_launch(const moe_w4_desc &w, const uint8_t *x_scale, hipStream_t s);
 
 // Queried at every launch (a host-side lookup in the runtime, no device
 // work), so the library holds no mutable state for it.
@@ -847,6 +850,48 @@ moe_status moe_w4_experts(const moe_w4_desc *w, void *stream) {
         return MOE_ERR_ALIGN;
     if (w->ws_bytes < w4_ws_bytes(w->T * w->k, w->d, w->h)) return MOE_ERR_WORKSPACE;
     return w4_experts_launch(w, (hipStream_t)stream);
+}
+
+moe_status moe_w4_gemm(const moe_w4_gemm_desc *g, void *stream) {
+    if (!g) return MOE_ERR_NULL;
+    const bool swiglu = g->epilogue == MOE_EPI_SWIGLU_FWD;
+    if (!swiglu && g->epilogue != MOE_EPI_NONE) return MOE_ERR_DTYPE;
+    if (g->n_groups < 1 || g->n_groups > 256 || g->rows < 0 || g->rows >= ((int64_t)1 << 31) ||
+        !width_ok(g->N) || !width_ok(g->K) || g->K % 128 || (swiglu && g->N % 64))
+        return MOE_ERR_SHAPE;
+    if (g->rows == 0) return MOE_OK;
+    if (!g->offsets || !g->a || !g->a_scale || !g->b || !g->b_scale || !g->c ||
+        swiglu == !g->c_scale)
+        return MOE_ERR_NULL;
+    if (!aligned16(g->a) || !aligned16(g->b) || !aligned16(g->c) || !aligned4(g->a_scale) ||
+        !aligned4(g->b_scale) || !aligned4(g->c_scale) || !aligned4(g->offsets) ||
+        !aligned4(g->a_rows))
+        return MOE_ERR_ALIGN;
+    return w4_gemm_launch(*g, (hipStream_t)stream);
+}
+
+static bool w4_wide_ok(int64_t T, int32_t k, int32_t d, int32_t h) {
+    return w4_shape_ok(T, k, d, h) && d % 128 == 0 && h % 128 == 0;
+}
+
+size_t moe_w4_experts8_workspace_size(int64_t T, int32_t k, int32_t d, int32_t h) {
+    return w4_wide_ok(T, k, d, h) ? w4_experts8_ws_bytes(T * k, d, h) : 0;
+}
+
+moe_status moe_w4_experts8(const moe_w4_desc *w, const uint8_t *x_scale, void *stream) {
+    if (!w) return MOE_ERR_NULL;
+    if (!routing_shape_ok(w->T, w->E, w->k) || !w4_wide_ok(w->T, w->k, w->d, w->h))
+        return MOE_ERR_SHAPE;
+    if (w->T == 0) return MOE_OK;
+    if (!w->x || !x_scale || !w->topk_gate || !w->token_pos || !w->sorted_token || !w->offsets ||
+        !w->w1q || !w->w1_scale || !w->w2q || !w->w2_scale || !w->out || !w->ws)
+        return MOE_ERR_NULL;
+    if (!aligned16(w->x) || !aligned16(w->out) || !aligned16(w->w1q) || !aligned16(w->w2q) ||
+        !aligned16(w->ws) || !aligned4(x_scale) || !aligned4(w->w1_scale) ||
+        !aligned4(w->w2_scale))
+        return MOE_ERR_ALIGN;
+    if (w->ws_bytes < w4_experts8_ws_bytes(w->T * w->k, w->d, w->h)) return MOE_ERR_WORKSPACE;
+    return w4_experts8_launch(*w, x_scale, (hipStream_t)stream);
 }
 
 size_t mxfp8_col_blocks(int64_t rows, int32_t n_groups) { return moe::mxfp8_col_blocks(rows, n_groups); }

@@ -1,0 +1,316 @@
+// w4_gemm.hip -- grouped products of MXFP8 rows with MXFP4 weights, and the
+// experts' forward of a prompt built on them.
+//
+//   C[r, n] = sum_k A[src(r), k] B[e(r)][n, k],  src(r) = a_rows[r] or r,
+// E4M3 elements on the left, E2M1 on the right, both with an E8M0 scale per 32
+// along k, in v_mfma_scale_f32_32x32x64_f8f6f4 with fp32 sums. The instruction
+// takes the two formats as they are stored and runs at the rate of E4M3 (4.6
+// PFLOP/s in a loop of nothing else on this card, 8x8 and 8x4 alike): 4-bit
+// weights halve what is read of them, from HBM and from LDS.
+//
+// The weights are the instruction's first operand, the rows its second, so
+// that a lane holds 16 of 32 neighbouring outputs n of one row: two lanes hold
+// a 32-element block of H', whose scale is one exchange away, and the outputs
+// leave in 16-byte pieces after one 32-lane swap a register.
+//
+// Tiles, schedule and copies into LDS as in the grouped GEMM (gemm_device.h):
+// a persistent grid walks each expert's tiles, an XCD its own weight panels.
+// Every wave copies and multiplies; two workgroups a compute unit cover each
+// other's barriers and epilogues. A step is 128 of K: 128 bytes of each row, 64
+// of each weight row, four scales of each.
+#include "common.h"
+#include "copy_plan.h"
+#include "gemm_device.h"
+#include "mx_encode.h"
+
+namespace moe {
+
+moe_status combine_launch(const void *y, moe_dtype dt, const float *gate,
+                          const int32_t *token_pos, int64_t T, int d, int k, void *out,
+                          bool unit_gate, hipStream_t s);
+
+// Rows of 64 bytes in LDS: four lie in one sweep of the 64 banks, so the
+// 16-byte pieces are swizzled by (row / 4) % 4, which puts the 16 rows that a
+// ds_read_b128 serves at once on 16 different bank groups.
+MOE_DEV int w4_chunk(int row, int c) { return row * 4 + (c ^ ((row >> 2) & 3)); }
+
+struct W4GemmTile {
+    int e, row0, row_end, nt;
+};
+
+// BM rows x BN weight rows a tile, WM x WN waves. SWIGLU: the weight rows of a
+// wave are gate rows, then the up rows of the same hidden units; c is E4M3 H'
+// [rows, N / 2] with c_scale. Otherwise c is bf16 [rows, N].
+template <bool SWIGLU, int BM, int BN, int WM, int WN, int OCC>
+__global__ __launch_bounds__(WM *WN * 64) __attribute__((amdgpu_waves_per_eu(OCC, OCC)))
+void w4_gemm_tiles(moe_w4_gemm_desc g) {
+    constexpr int NW = WM * WN, WTM = BM / WM, WTN = BN / WN, TM = WTM / 32, TN = WTN / 32;
+    static_assert(!SWIGLU || TN % 2 == 0, "gate and up of a unit in one wave");
+    static_assert(NW * 64 >= 256, "the tile table's scan");
+    constexpr int IPA = BM * 8 / 64 / NW, IPB = BN * 4 / 64 / NW;     // 16-byte copies a lane
+    static_assert(IPA * 64 * NW == BM * 8 && IPB * 64 * NW == BN * 4, "whole copies");
+    constexpr int SROWS = BM + BN, SPW = (SROWS / 64 + NW - 1) / NW;  // scale words
+    static_assert(BM % 64 == 0 && BN % 64 == 0, "a wave's scale words are of one operand");
+    constexpr int STAGE = BM * 8 + BN * 4 + SROWS / 4;                // uint4
+    __shared__ __attribute__((aligned(1024))) uint4 pool[2 * STAGE];
+    __shared__ int32_t s_off[257], s_tile[257], s_chunk[257], s_xpre[kXcdChunks + 1];
+
+    const int tid = threadIdx.x, lane = tid & 63, half = lane >> 5;
+    const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+    const int wm = wave / WN, wn = wave % WN;
+    const int E = g.n_groups, K = g.K, N = g.N, h = N / 2;
+    const int xcd = blockIdx.x & 7, workers = gridDim.x >> 3;
+    build_tile_table(g.offsets, E, BM, s_off, s_tile);
+    const int n_tiles = SWIGLU ? (h + BN / 2 - 1) / (BN / 2) : (N + BN - 1) / BN;
+    const RowSchedule rs = build_row_schedule(s_tile, E, n_tiles, xcd, s_chunk, s_xpre);
+    const int nk = K / 128;
+
+    // weight row (of N) of the tile's row n, the last one past the end
+    auto b_row = [&](int nt, int n) {
+        if constexpr (SWIGLU) {
+            constexpr int HW = WTN / 2;
+            const int o = n % WTN, j = min(nt * (BN / 2) + n / WTN * HW + o % HW, h - 1);
+            return o < HW ? j : h + j;
+        } else {
+            return min(nt * BN + n, N - 1);
+        }
+    };
+    auto decode = [&](int pos) {
+        W4GemmTile t;
+        int mt;
+        decode_row_tile(rs, s_tile, s_chunk, s_xpre, E, xcd, pos, t.e, mt, t.nt);
+        t.row0 = s_off[t.e] + mt * BM;
+        t.row_end = s_off[t.e + 1];
+        return t;
+    };
+
+    // this lane's copy sources of the tile set up last, at step 0
+    const uint8_t *pa[IPA], *ps[SPW];
+    uint32_t ob[IPB];
+    const char *pb = nullptr;
+    auto setup = [&](const W4GemmTile &t) {
+        // row r of the tile in A; past the group's end its last row
+        auto src = [&](int r) {
+            const int gr = min(t.row0 + r, t.row_end - 1);
+            return (int64_t)(g.a_rows ? g.a_rows[gr] : gr);
+        };
+#pragma unroll
+        for (int i = 0; i < IPA; i++) {
+            const int p = (wave * IPA + i) * 64 + lane, r = p >> 3;
+            pa[i] = g.a + src(r) * K + ((p & 7) ^ kl_swz(r)) * 16;
+        }
+        pb = uniform_ptr(reinterpret_cast<const char *>(g.b) + (int64_t)t.e * N * (K / 2));
+#pragma unroll
+        for (int i = 0; i < IPB; i++) {
+            const int p = (wave * IPB + i) * 64 + lane, r = p >> 2;
+            ob[i] = (uint32_t)b_row(t.nt, r) * (uint32_t)(K / 2) + ((p & 3) ^ ((r >> 2) & 3)) * 16;
+        }
+#pragma unroll
+        for (int q = 0; q < SPW; q++) {
+            const int s0 = (q * NW + wave) * 64;                  // wave-uniform
+            if (s0 < BM) ps[q] = g.a_scale + src(s0 + lane) * (K / 32);
+            else if (s0 < SROWS)
+                ps[q] = g.b_scale + ((int64_t)t.e * N + b_row(t.nt, s0 + lane - BM)) * (K / 32);
+        }
+    };
+    auto issue = [&](int kt, int buf) {
+        uint4 *st = pool + buf * STAGE;
+#pragma unroll
+        for (int i = 0; i < IPB; i++)
+            dma16s(ob[i], pb + kt * 64, st + BM * 8 + (wave * IPB + i) * 64);
+#pragma unroll
+        for (int i = 0; i < IPA; i++) dma16(pa[i] + kt * 128, st + (wave * IPA + i) * 64);
+#pragma unroll
+        for (int q = 0; q < SPW; q++)
+            if ((q * NW + wave) * 64 < SROWS)
+                dma4(ps[q] + kt * 4, st + BM * 8 + BN * 4 + (q * NW + wave) * 16);
+    };
+
+    f32x16 acc[TN][TM];
+    // rows r0 .. r0 + 31 of the stage, K slice s (64 wide): K 16 half .. + 15 of
+    // the slice in dwords 0-3, 32 + 16 half .. + 15 in dwords 4-7; weights: K 32
+    // half .. + 31 in dwords 0-3 (both layouts measured on the GPU)
+    auto frag_a = [&](const uint4 *st, int r0, int s) {
+        const int row = r0 + (lane & 31);
+        const uint4 c0 = st[kl_chunk(row, 4 * s + half)], c1 = st[kl_chunk(row, 4 * s + 2 + half)];
+        return i32x8{(int)c0.x, (int)c0.y, (int)c0.z, (int)c0.w, (int)c1.x, (int)c1.y, (int)c1.z, (int)c1.w};
+    };
+    auto frag_b = [&](const uint4 *st, int r0, int s) {
+        const uint4 c = st[BM * 8 + w4_chunk(r0 + (lane & 31), 2 * s + half)];
+        return i32x8{(int)c.x, (int)c.y, (int)c.z, (int)c.w, 0, 0, 0, 0};
+    };
+    auto compute = [&](int buf) {
+        const uint4 *st = pool + buf * STAGE;
+        const uint32_t *sw = reinterpret_cast<const uint32_t *>(st + BM * 8 + BN * 4);
+        // byte 2 s + half is the scale of this lane's row for slice s
+        uint32_t sa[TM], sb[TN];
+#pragma unroll
+        for (int i = 0; i < TM; i++) sa[i] = sw[wm * WTM + i * 32 + (lane & 31)] >> (8 * half);
+#pragma unroll
+        for (int j = 0; j < TN; j++) sb[j] = sw[BM + wn * WTN + j * 32 + (lane & 31)] >> (8 * half);
+        i32x8 fa[2][TM], fb[2][TN];
+#pragma unroll
+        for (int i = 0; i < TM; i++) fa[0][i] = frag_a(st, wm * WTM + i * 32, 0);
+#pragma unroll
+        for (int j = 0; j < TN; j++) fb[0][j] = frag_b(st, wn * WTN + j * 32, 0);
+        // slice 0 with the reads of slice 1 between its products
+#pragma unroll
+        for (int t = 0; t < TM * TN; t++) {
+            if (t < TM) fa[1][t] = frag_a(st, wm * WTM + t * 32, 1);
+            else if (t < TM + TN) fb[1][t - TM] = frag_b(st, wn * WTN + (t - TM) * 32, 1);
+            __builtin_amdgcn_sched_barrier(0);
+            const int j = t / TM, i = t % TM;
+            acc[j][i] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(
+                fb[0][j], fa[0][i], acc[j][i], 4, 0, 0, (int)sb[j], 0, (int)sa[i]);
+            __builtin_amdgcn_sched_barrier(0);
+        }
+#pragma unroll
+        for (int j = 0; j < TN; j++)
+#pragma unroll
+            for (int i = 0; i < TM; i++)
+                acc[j][i] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(
+                    fb[1][j], fa[1][i], acc[j][i], 4, 0, 2, (int)sb[j], 2, (int)sa[i]);
+    };
+    // acc[j][i][4 q + x]: row i * 32 + lane % 32 of the wave, output j * 32 + 8 q +
+    // 4 half + x. v_permlane32_swap gives the lower half of the lanes both
+    // halves' values of one register and the upper half the other's.
+    auto swap32 = [](uint32_t lo, uint32_t up, uint32_t &first, uint32_t &second) {
+        const auto r = __builtin_amdgcn_permlane32_swap(lo, up, false, false);
+        first = r[0];
+        second = r[1];
+    };
+    auto epilogue = [&](const W4GemmTile &t) {
+#pragma unroll
+        for (int i = 0; i < TM; i++) {
+            const int row = t.row0 + wm * WTM + i * 32 + (lane & 31);
+            const bool ok = row < t.row_end;
+            if constexpr (SWIGLU) {
+                uint8_t *c = reinterpret_cast<uint8_t *>(g.c) + (int64_t)row * h;
+#pragma unroll
+                for (int j = 0; j < TN / 2; j++) {
+                    const int n = t.nt * (BN / 2) + wn * (WTN / 2) + j * 32;
+                    if (n >= h) continue;                         // wave-uniform
+                    float f[16], am = 0.f;
+#pragma unroll
+                    for (int v = 0; v < 16; v++) {
+                        f[v] = silu_f(acc[j][i][v]) * acc[j + TN / 2][i][v];
+                        am = fmaxf(am, fabsf(f[v]));
+                    }
+                    const uint32_t sb = mx_scale_byte(max_xor32(am));
+                    uint32_t w[4], o[4];
+#pragma unroll
+                    for (int q = 0; q < 4; q++)
+                        w[q] = e4m3x4(f[4 * q], f[4 * q + 1], f[4 * q + 2], f[4 * q + 3], sb);
+                    swap32(w[0], w[2], o[0], o[1]);
+                    swap32(w[1], w[3], o[2], o[3]);
+                    if (ok) {
+                        *reinterpret_cast<uint4 *>(c + n + 16 * half) = make_uint4(o[0], o[1], o[2], o[3]);
+                        if (half == 0) g.c_scale[(int64_t)row * (h / 32) + n / 32] = (uint8_t)sb;
+                    }
+                }
+            } else {
+                uint16_t *c = reinterpret_cast<uint16_t *>(g.c) + (int64_t)row * N;
+#pragma unroll
+                for (int j = 0; j < TN; j++) {
+                    const int n = t.nt * BN + wn * WTN + j * 32;
+                    if (n >= N) continue;
+#pragma unroll
+                    for (int q = 0; q < 4; q += 2) {
+                        uint32_t o[4];
+#pragma unroll
+                        for (int x = 0; x < 2; x++)
+                            swap32(pack_bf16x2(acc[j][i][4 * q + 2 * x], acc[j][i][4 * q + 2 * x + 1]),
+                                   pack_bf16x2(acc[j][i][4 * q + 4 + 2 * x], acc[j][i][4 * q + 5 + 2 * x]),
+                                   o[x], o[2 + x]);
+                        if (ok)
+                            *reinterpret_cast<uint4 *>(c + n + 8 * (q + half)) =
+                                make_uint4(o[0], o[1], o[2], o[3]);
+                    }
+                }
+            }
+        }
+    };
+
+    int pos = blockIdx.x >> 3, buf = 0;
+    if (pos >= rs.total) return;                                  // the whole workgroup
+    W4GemmTile cur = decode(pos);
+    setup(cur);
+    issue(0, 0);
+    while (true) {
+#pragma unroll
+        for (int j = 0; j < TN; j++)
+#pragma unroll
+            for (int i = 0; i < TM; i++)
+#pragma unroll
+                for (int v = 0; v < 16; v++) acc[j][i][v] = 0.f;
+        const int npos = pos + workers;
+        const bool more = npos < rs.total;
+        // a wave whose rows all lie past the group's end only copies
+        const bool mine = cur.row0 + wm * WTM < cur.row_end;
+        W4GemmTile nxt = cur;
+        for (int kt = 0; kt < nk; kt++, buf ^= 1) {
+            wait_vmem<0>();              // this wave's copies of the step have landed,
+            lds_sync();                  // everybody's, and the other buffer has been read
+            if (kt + 1 < nk) issue(kt + 1, buf ^ 1);
+            else if (more) {
+                nxt = decode(npos);
+                setup(nxt);
+                issue(0, buf ^ 1);
+            }
+            if (mine) compute(buf);
+        }
+        if (mine) epilogue(cur);
+        if (!more) break;
+        cur = nxt;
+        pos = npos;
+    }
+}
+
+// ---------------------------------------------------------------------------
+// launchers
+
+template <bool SWIGLU, int BM, int BN, int WM, int WN, int OCC>
+static void w4_gemm_run(const moe_w4_gemm_desc &g, hipStream_t s) {
+    constexpr int per_cu = OCC * 4 / (WM * WN);
+    const int grid = (num_cus() * per_cu + 7) / 8 * 8;
+    w4_gemm_tiles<SWIGLU, BM, BN, WM, WN, OCC><<<grid, WM * WN * 64, 0, s>>>(g);
+}
+
+moe_status w4_gemm_launch(const moe_w4_gemm_desc &g, hipStream_t s) {
+    if (g.epilogue == MOE_EPI_SWIGLU_FWD) w4_gemm_run<true, 128, 256, 2, 2, 2>(g, s);
+    else w4_gemm_run<false, 128, 256, 2, 2, 2>(g, s);
+    return launch_status();
+}
+
+static size_t round256(size_t b) { return (b + 255) & ~(size_t)255; }
+
+// H' in MXFP8 [R, h], its scales, y bf16 [R, d]
+size_t w4_experts8_ws_bytes(int64_t R, int d, int h) {
+    return round256((size_t)R * h) + round256((size_t)R * (h / 32)) + round256((size_t)R * d * 2);
+}
+
+moe_status w4_experts8_launch(const moe_w4_desc &w, const uint8_t *x_scale, hipStream_t s) {
+    const int64_t R = w.T * w.k;
+    uint8_t *hq = (uint8_t *)w.ws, *hs = hq + round256((size_t)R * w.h);
+    uint8_t *y = hs + round256((size_t)R * (w.h / 32));
+    moe_w4_gemm_desc g = {};
+    g.n_groups = w.E;
+    g.rows = R;
+    g.offsets = w.offsets;
+    g.epilogue = MOE_EPI_SWIGLU_FWD;
+    g.N = 2 * w.h; g.K = w.d;
+    g.a = (const uint8_t *)w.x; g.a_scale = x_scale; g.a_rows = w.sorted_token;
+    g.b = w.w1q; g.b_scale = w.w1_scale;
+    g.c = hq; g.c_scale = hs;
+    moe_status st = w4_gemm_launch(g, s);
+    if (st != MOE_OK) return st;
+    g.epilogue = MOE_EPI_NONE;
+    g.N = w.d; g.K = w.h;
+    g.a = hq; g.a_scale = hs; g.a_rows = nullptr;
+    g.b = w.w2q; g.b_scale = w.w2_scale;
+    g.c = y; g.c_scale = nullptr;
+    if ((st = w4_gemm_launch(g, s)) != MOE_OK) return st;
+    return combine_launch(y, MOE_BF16, w.topk_gate, w.token_pos, w.T, w.d, w.k, w.out, false, s);
+}
+
+}  // namespace moe
