@@ -19,22 +19,33 @@ MOE_DEV void load_offsets(const int32_t *offsets, int E, int32_t *s_off) {
     __syncthreads();
 }
 
+// out[0] = 0, out[i + 1] = the sum of v over threads 0 .. i, for i < n with 4 <=
+// n <= 256; blockDim.x >= 256. By lanes, then by waves, whose sums pass through
+// out: three barriers, where a scan in LDS takes sixteen. Starts after the
+// caller's last barrier and ends with one.
+MOE_DEV void scan256(int32_t v, int n, int32_t *out) {
+    const int tid = threadIdx.x, lane = tid & 63;
+#pragma unroll
+    for (int o = 1; o < 64; o <<= 1) {
+        const int32_t t = __shfl_up(v, o, 64);
+        if (lane >= o) v += t;
+    }
+    if (tid < 256 && lane == 63) out[tid >> 6] = v;
+    __syncthreads();
+    const int32_t w0 = out[0], w1 = out[1], w2 = out[2];
+    __syncthreads();
+    if (tid < n) out[tid + 1] = v + (tid >= 64 ? w0 : 0) + (tid >= 128 ? w1 : 0) + (tid >= 192 ? w2 : 0);
+    if (tid == 0) out[0] = 0;
+    __syncthreads();
+}
+
 // Loads offsets[0..E] into s_off and builds s_tile[e] = sum_{e'<e} ceil(c_e'/BM).
 // The scan needs blockDim.x >= 256 (E <= 256). Returns the total number of m-tiles.
 MOE_DEV int build_tile_table(const int32_t *offsets, int E, int BM, int32_t *s_off,
                              int32_t *s_tile) {
     const int tid = threadIdx.x;
     load_offsets(offsets, E, s_off);
-    int32_t c = tid < E ? (s_off[tid + 1] - s_off[tid] + BM - 1) / BM : 0;
-    if (tid < 256) s_tile[tid + 1] = c;
-    if (tid == 0) s_tile[0] = 0;
-    __syncthreads();
-    for (int o = 1; o < 256; o <<= 1) {
-        int32_t v = (tid < 256 && tid >= o) ? s_tile[tid + 1 - o] : 0;
-        __syncthreads();
-        if (tid < 256) s_tile[tid + 1] += v;
-        __syncthreads();
-    }
+    scan256(tid < E ? (s_off[tid + 1] - s_off[tid] + BM - 1) / BM : 0, 256, s_tile);
     return s_tile[E];
 }
 
@@ -125,15 +136,7 @@ MOE_DEV RowSchedule build_row_schedule(const int32_t *s_tile, int E, int n_tiles
     const int chm = max(kChunkM, (mt_total + (kMaxChunks - 256) - 1) / (kMaxChunks - 256));
     int32_t nc = 0;
     if (tid < E) nc = chunk_count(s_tile[tid + 1] - s_tile[tid], chm);
-    if (tid < 256) s_chunk[tid + 1] = nc;
-    if (tid == 0) s_chunk[0] = 0;
-    __syncthreads();
-    for (int o = 1; o < 256; o <<= 1) {
-        int32_t v = (tid < 256 && tid >= o) ? s_chunk[tid + 1 - o] : 0;
-        __syncthreads();
-        if (tid < 256) s_chunk[tid + 1] += v;
-        __syncthreads();
-    }
+    scan256(nc, 256, s_chunk);
     const int C = s_chunk[E];
     const int cx = C > xcd ? (C - xcd + 7) / 8 : 0;     // chunks of this XCD (<= 256)
     int32_t t = 0;
@@ -145,15 +148,7 @@ MOE_DEV RowSchedule build_row_schedule(const int32_t *s_tile, int E, int n_tiles
         t = chunk_mtiles(mt_e, chm, ci) * n_tiles;
     }
     // (C <= kMaxChunks by the choice of chm, so cx <= kXcdChunks)
-    if (tid < kXcdChunks) s_xpre[tid + 1] = t;
-    if (tid == 0) s_xpre[0] = 0;
-    __syncthreads();
-    for (int o = 1; o < kXcdChunks; o <<= 1) {
-        int32_t v = (tid < kXcdChunks && tid >= o) ? s_xpre[tid + 1 - o] : 0;
-        __syncthreads();
-        if (tid < kXcdChunks) s_xpre[tid + 1] += v;
-        __syncthreads();
-    }
+    scan256(t, kXcdChunks, s_xpre);
     RowSchedule r;
     r.n_tiles = n_tiles;
     r.chm = chm;

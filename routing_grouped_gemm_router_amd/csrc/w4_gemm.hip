@@ -41,7 +41,7 @@ struct W4GemmTile {
 // BM rows x BN weight rows a tile, WM x WN waves. SWIGLU: the weight rows of a
 // wave are gate rows, then the up rows of the same hidden units; c is E4M3 H'
 // [rows, N / 2] with c_scale. Otherwise c is bf16 [rows, N].
-template <bool SWIGLU, int BM, int BN, int WM, int WN, int OCC>
+template <bool SWIGLU, int BM, int BN, int WM, int WN, int STAGES, int OCC>
 __global__ __launch_bounds__(WM *WN * 64) __attribute__((amdgpu_waves_per_eu(OCC, OCC)))
 void w4_gemm_tiles(moe_w4_gemm_desc g) {
     constexpr int NW = WM * WN, WTM = BM / WM, WTN = BN / WN, TM = WTM / 32, TN = WTN / 32;
@@ -51,14 +51,19 @@ void w4_gemm_tiles(moe_w4_gemm_desc g) {
     static_assert(IPA * 64 * NW == BM * 8 && IPB * 64 * NW == BN * 4, "whole copies");
     constexpr int SROWS = BM + BN, SPW = (SROWS / 64 + NW - 1) / NW;  // scale words
     static_assert(BM % 64 == 0 && BN % 64 == 0, "a wave's scale words are of one operand");
-    constexpr int STAGE = BM * 8 + BN * 4 + SROWS / 4;                // uint4
-    __shared__ __attribute__((aligned(1024))) uint4 pool[2 * STAGE];
+    static_assert(STAGES >= 2 && STAGES <= 5, "two slots of four steps of scales");
+    constexpr int STAGE = BM * 8 + BN * 4;                            // uint4
+    __shared__ __attribute__((aligned(1024))) uint4 pool[STAGES * STAGE];
+    // scale words: a slot for each stage, 4 bytes a row, or where a row's scales
+    // come in whole 16-byte groups two slots of four steps
+    __shared__ __attribute__((aligned(1024))) uint4 scales[2 * SROWS];
     __shared__ int32_t s_off[257], s_tile[257], s_chunk[257], s_xpre[kXcdChunks + 1];
 
     const int tid = threadIdx.x, lane = tid & 63, half = lane >> 5;
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int wm = wave / WN, wn = wave % WN;
     const int E = g.n_groups, K = g.K, N = g.N, h = N / 2;
+    const bool batched = (K / 32) % 16 == 0;
     const int xcd = blockIdx.x & 7, workers = gridDim.x >> 3;
     build_tile_table(g.offsets, E, BM, s_off, s_tile);
     const int n_tiles = SWIGLU ? (h + BN / 2 - 1) / (BN / 2) : (N + BN - 1) / BN;
@@ -84,10 +89,11 @@ void w4_gemm_tiles(moe_w4_gemm_desc g) {
         return t;
     };
 
-    // this lane's copy sources of the tile set up last, at step 0
+    // the copies: this lane's sources of tile ipos, whose step ikt is the next
     const uint8_t *pa[IPA], *ps[SPW];
     uint32_t ob[IPB];
     const char *pb = nullptr;
+    int ipos = blockIdx.x >> 3, ikt = 0, issued = 0, slot = 1;
     auto setup = [&](const W4GemmTile &t) {
         // row r of the tile in A; past the group's end its last row
         auto src = [&](int r) {
@@ -113,17 +119,34 @@ void w4_gemm_tiles(moe_w4_gemm_desc g) {
                 ps[q] = g.b_scale + ((int64_t)t.e * N + b_row(t.nt, s0 + lane - BM)) * (K / 32);
         }
     };
-    auto issue = [&](int kt, int buf) {
+    // enqueue the next step's copies, if there is one, into stage buf
+    auto issue = [&](int buf) {
+        if (ipos >= rs.total) return;
+        if (ikt == 0) setup(decode(ipos));
         uint4 *st = pool + buf * STAGE;
+        // scales first: a wait for the step's operands then covers them
+        if (!batched) {
+#pragma unroll
+            for (int q = 0; q < SPW; q++)
+                if ((q * NW + wave) * 64 < SROWS)
+                    dma4(ps[q] + ikt * 4, scales + buf * (SROWS / 4) + (q * NW + wave) * 16);
+        } else if ((ikt & 3) == 0) {
+            slot ^= 1;
+#pragma unroll
+            for (int q = 0; q < SPW; q++)
+                if ((q * NW + wave) * 64 < SROWS)
+                    dma16(ps[q] + ikt * 4, scales + slot * SROWS + (q * NW + wave) * 64);
+        }
 #pragma unroll
         for (int i = 0; i < IPB; i++)
-            dma16s(ob[i], pb + kt * 64, st + BM * 8 + (wave * IPB + i) * 64);
+            dma16s(ob[i], pb + ikt * 64, st + BM * 8 + (wave * IPB + i) * 64);
 #pragma unroll
-        for (int i = 0; i < IPA; i++) dma16(pa[i] + kt * 128, st + (wave * IPA + i) * 64);
-#pragma unroll
-        for (int q = 0; q < SPW; q++)
-            if ((q * NW + wave) * 64 < SROWS)
-                dma4(ps[q] + kt * 4, st + BM * 8 + BN * 4 + (q * NW + wave) * 16);
+        for (int i = 0; i < IPA; i++) dma16(pa[i] + ikt * 128, st + (wave * IPA + i) * 64);
+        issued++;
+        if (++ikt == nk) {
+            ikt = 0;
+            ipos += workers;
+        }
     };
 
     f32x16 acc[TN][TM];
@@ -139,37 +162,42 @@ void w4_gemm_tiles(moe_w4_gemm_desc g) {
         const uint4 c = st[BM * 8 + w4_chunk(r0 + (lane & 31), 2 * s + half)];
         return i32x8{(int)c.x, (int)c.y, (int)c.z, (int)c.w, 0, 0, 0, 0};
     };
-    auto compute = [&](int buf) {
+    auto compute = [&](int buf, int kt, int slot) {
         const uint4 *st = pool + buf * STAGE;
-        const uint32_t *sw = reinterpret_cast<const uint32_t *>(st + BM * 8 + BN * 4);
+        const uint32_t *sw = reinterpret_cast<const uint32_t *>(
+            scales + (batched ? slot * SROWS : buf * (SROWS / 4))) + (batched ? kt & 3 : 0);
+        const int sp = batched ? 4 : 1;
         // byte 2 s + half is the scale of this lane's row for slice s
         uint32_t sa[TM], sb[TN];
 #pragma unroll
-        for (int i = 0; i < TM; i++) sa[i] = sw[wm * WTM + i * 32 + (lane & 31)] >> (8 * half);
+        for (int i = 0; i < TM; i++) sa[i] = sw[(wm * WTM + i * 32 + (lane & 31)) * sp] >> (8 * half);
 #pragma unroll
-        for (int j = 0; j < TN; j++) sb[j] = sw[BM + wn * WTN + j * 32 + (lane & 31)] >> (8 * half);
-        i32x8 fa[2][TM], fb[2][TN];
+        for (int j = 0; j < TN; j++) sb[j] = sw[(BM + wn * WTN + j * 32 + (lane & 31)) * sp] >> (8 * half);
+        i32x8 fa[2][TM], fb[TN];
+#pragma unroll
+        for (int j = 0; j < TN; j++) fb[j] = frag_b(st, wn * WTN + j * 32, 0);
 #pragma unroll
         for (int i = 0; i < TM; i++) fa[0][i] = frag_a(st, wm * WTM + i * 32, 0);
+        // the reads of slice 1 between the products of slice 0; a weight fragment
+        // takes the place of the one whose products have just been issued
 #pragma unroll
-        for (int j = 0; j < TN; j++) fb[0][j] = frag_b(st, wn * WTN + j * 32, 0);
-        // slice 0 with the reads of slice 1 between its products
+        for (int j = 0; j < TN; j++) {
 #pragma unroll
-        for (int t = 0; t < TM * TN; t++) {
-            if (t < TM) fa[1][t] = frag_a(st, wm * WTM + t * 32, 1);
-            else if (t < TM + TN) fb[1][t - TM] = frag_b(st, wn * WTN + (t - TM) * 32, 1);
-            __builtin_amdgcn_sched_barrier(0);
-            const int j = t / TM, i = t % TM;
-            acc[j][i] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(
-                fb[0][j], fa[0][i], acc[j][i], 4, 0, 0, (int)sb[j], 0, (int)sa[i]);
-            __builtin_amdgcn_sched_barrier(0);
+            for (int i = 0; i < TM; i++) {
+                __builtin_amdgcn_sched_barrier(0);
+                acc[j][i] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(
+                    fb[j], fa[0][i], acc[j][i], 4, 0, 0, (int)sb[j], 0, (int)sa[i]);
+                __builtin_amdgcn_sched_barrier(0);
+                if (j * TM + i < TM) fa[1][j * TM + i] = frag_a(st, wm * WTM + (j * TM + i) * 32, 1);
+            }
+            fb[j] = frag_b(st, wn * WTN + j * 32, 1);
         }
 #pragma unroll
         for (int j = 0; j < TN; j++)
 #pragma unroll
             for (int i = 0; i < TM; i++)
                 acc[j][i] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(
-                    fb[1][j], fa[1][i], acc[j][i], 4, 0, 2, (int)sb[j], 2, (int)sa[i]);
+                    fb[j], fa[1][i], acc[j][i], 4, 0, 2, (int)sb[j], 2, (int)sa[i]);
     };
     // acc[j][i][4 q + x]: row i * 32 + lane % 32 of the wave, output j * 32 + 8 q +
     // 4 half + x. v_permlane32_swap gives the lower half of the lanes both
@@ -231,54 +259,68 @@ void w4_gemm_tiles(moe_w4_gemm_desc g) {
         }
     };
 
-    int pos = blockIdx.x >> 3, buf = 0;
-    if (pos >= rs.total) return;                                  // the whole workgroup
-    W4GemmTile cur = decode(pos);
-    setup(cur);
-    issue(0, 0);
-    while (true) {
+
+    const int first = blockIdx.x >> 3;
+    if (first >= rs.total) return;                                // the whole workgroup
+    for (int i = 0; i < STAGES - 1; i++) issue(i);
+    int step = 0, buf = 0, batch = 1;
+    for (int pos = first; pos < rs.total; pos += workers) {
+        const W4GemmTile cur = decode(pos);
 #pragma unroll
         for (int j = 0; j < TN; j++)
 #pragma unroll
             for (int i = 0; i < TM; i++)
 #pragma unroll
                 for (int v = 0; v < 16; v++) acc[j][i][v] = 0.f;
-        const int npos = pos + workers;
-        const bool more = npos < rs.total;
         // a wave whose rows all lie past the group's end only copies
         const bool mine = cur.row0 + wm * WTM < cur.row_end;
-        W4GemmTile nxt = cur;
-        for (int kt = 0; kt < nk; kt++, buf ^= 1) {
-            wait_vmem<0>();              // this wave's copies of the step have landed,
-            lds_sync();                  // everybody's, and the other buffer has been read
-            if (kt + 1 < nk) issue(kt + 1, buf ^ 1);
-            else if (more) {
-                nxt = decode(npos);
-                setup(nxt);
-                issue(0, buf ^ 1);
-            }
-            if (mine) compute(buf);
+        for (int kt = 0; kt < nk; kt++, step++) {
+            // this wave's copies of the step have landed: at most those of the
+            // STAGES - 2 steps behind it may be in flight (loads return in order;
+            // a store or a scale copy among them makes the wait longer, not shorter)
+            if (issued - step >= STAGES - 1) wait_vmem<(STAGES - 2) * (IPA + IPB)>();
+            else wait_vmem<0>();
+            lds_sync();                  // everybody's, and the stage before has been read
+            issue(buf == 0 ? STAGES - 1 : buf - 1);
+            if ((kt & 3) == 0) batch ^= 1;
+            if (mine) compute(buf, kt, batch);
+            if (++buf == STAGES) buf = 0;
         }
         if (mine) epilogue(cur);
-        if (!more) break;
-        cur = nxt;
-        pos = npos;
     }
 }
 
 // ---------------------------------------------------------------------------
 // launchers
 
-template <bool SWIGLU, int BM, int BN, int WM, int WN, int OCC>
+template <bool SWIGLU, int BM, int BN, int WM, int WN, int STAGES, int OCC>
 static void w4_gemm_run(const moe_w4_gemm_desc &g, hipStream_t s) {
     constexpr int per_cu = OCC * 4 / (WM * WN);
     const int grid = (num_cus() * per_cu + 7) / 8 * 8;
-    w4_gemm_tiles<SWIGLU, BM, BN, WM, WN, OCC><<<grid, WM * WN * 64, 0, s>>>(g);
+    w4_gemm_tiles<SWIGLU, BM, BN, WM, WN, STAGES, OCC><<<grid, WM * WN * 64, 0, s>>>(g);
+}
+// Large tiles where they fill the chip and an expert's rows fill most of one,
+// small ones otherwise: a large tile moves 32 KiB for 2^22 products where two
+// small ones of half its columns move 48, a small one leaves fewer rows of a
+// group's last tile empty and gives more workgroups. us, large / small:
+//   E = 128, k = 4, up (K = N = 2048): 32 rows an expert 69 / 65, 128 rows 110 /
+//     152, 512 rows 293 / 463
+//   E = 32, 31 rows an expert (256 large tiles): up 27.7 / 20.3, down (K = 1024)
+//     17.1 / 14.7
+static bool w4_small_tiles(const moe_w4_gemm_desc &g) {
+    const int64_t tiles = (g.rows / 128 + g.n_groups / 2) * ((g.N + 255) / 256);
+    return g.rows <= 64 * (int64_t)g.n_groups || tiles < 512;
+}
+
+template <bool SWIGLU>
+static void w4_gemm_pick(const moe_w4_gemm_desc &g, hipStream_t s) {
+    if (w4_small_tiles(g)) w4_gemm_run<SWIGLU, 64, 128, 2, 2, 3, 2>(g, s);
+    else w4_gemm_run<SWIGLU, 128, 256, 2, 2, 2, 2>(g, s);
 }
 
 moe_status w4_gemm_launch(const moe_w4_gemm_desc &g, hipStream_t s) {
-    if (g.epilogue == MOE_EPI_SWIGLU_FWD) w4_gemm_run<true, 128, 256, 2, 2, 2>(g, s);
-    else w4_gemm_run<false, 128, 256, 2, 2, 2>(g, s);
+    if (g.epilogue == MOE_EPI_SWIGLU_FWD) w4_gemm_pick<true>(g, s);
+    else w4_gemm_pick<false>(g, s);
     return launch_status();
 }
 
