@@ -13,7 +13,9 @@ the saved tensors and intermediates as torch allocations.
 """
 from __future__ import annotations
 
+import array
 import ctypes
+import operator
 import os
 
 import torch
@@ -1076,51 +1078,60 @@ MOE_GRAD_MAX = 4096
 _GRAD_DT = {torch.float32: MOE_F32, torch.bfloat16: MOE_BF16}
 
 
+_t_ptr, _t_numel, _t_gpu = torch.Tensor.data_ptr, torch.Tensor.numel, torch.Tensor.get_device
+_t_contiguous, _t_dtype = torch.Tensor.is_contiguous, operator.attrgetter("dtype")
+
+
+def _grad_bad(name, t, i, gpu, want):
+    raise ValueError(f"{name}[{i}]: expected a contiguous {want} on "
+                     f"{'a GPU' if gpu < 0 else f'cuda:{gpu}'}, got {t.dtype} {tuple(t.shape)} "
+                     f"(contiguous={t.is_contiguous()}, device={t.device})")
+
+
 def _grad_list(grads, out=None):
     """The C descriptors (moe_grad: data, out, n, dtype) of a list of
-    tensors, their number and their GPU."""
-    grads = list(grads)
-    if not grads:
-        raise ValueError("grads: expected at least one tensor")
-    if out is not None:
+    tensors, their address and number, and the tensors' GPU. Checked by whole
+    lists: a model's list is long, and a call's host time is its length's."""
+    if not isinstance(grads, (list, tuple)):
+        grads = list(grads)
+    if out is not None and not isinstance(out, (list, tuple)):
         out = list(out)
-        if len(out) != len(grads):
-            raise ValueError(f"out: expected {len(grads)} tensors, got {len(out)}")
+    n = len(grads)
+    if not n:
+        raise ValueError("grads: expected at least one tensor")
+    if out is not None and len(out) != n:
+        raise ValueError(f"out: expected {n} tensors, got {len(out)}")
     gpu = grads[0].get_device()
-    v = []
-    for i, g in enumerate(grads):
-        dt = _GRAD_DT.get(g.dtype)
-        if dt is None or gpu < 0 or g.get_device() != gpu or not g.is_contiguous():
-            raise ValueError(f"grads[{i}]: expected a contiguous f32 or bf16 tensor on "
-                             f"{'a GPU' if gpu < 0 else f'cuda:{gpu}'}, got {g.dtype} "
-                             f"(contiguous={g.is_contiguous()}, device={g.device})")
-        o = 0
-        if out is not None:
-            o = out[i]
-            if o.dtype is not g.dtype or o.shape != g.shape or o.get_device() != gpu or \
-                    not o.is_contiguous():
-                raise ValueError(f"out[{i}]: expected a contiguous {g.dtype} {tuple(g.shape)} on "
-                                 f"cuda:{gpu}, got {o.dtype} {tuple(o.shape)} (contiguous="
-                                 f"{o.is_contiguous()}, device={o.device})")
-            o = o.data_ptr()
-        v += (g.data_ptr(), o, g.numel(), dt)
-    return (_I64 * len(v))(*v), len(grads), gpu, grads[0].device
+    dts = list(map(_t_dtype, grads))
+    codes = list(map(_GRAD_DT.get, dts))
+    if gpu < 0 or None in codes or not all(map(_t_contiguous, grads)) or \
+            any(map(gpu.__ne__, map(_t_gpu, grads))):
+        for i, t in enumerate(grads):
+            if gpu < 0 or codes[i] is None or t.get_device() != gpu or not t.is_contiguous():
+                _grad_bad("grads", t, i, gpu, "f32 or bf16 tensor")
+    sizes = array.array("q", map(_t_numel, grads))
+    v = array.array("q", bytes(32 * n))
+    v[0::4] = array.array("q", map(_t_ptr, grads))
+    v[2::4] = sizes
+    v[3::4] = array.array("q", codes)
+    if out is not None:
+        if list(map(_t_dtype, out)) != dts or array.array("q", map(_t_numel, out)) != sizes or \
+                not all(map(_t_contiguous, out)) or any(map(gpu.__ne__, map(_t_gpu, out))):
+            for i, (t, g) in enumerate(zip(out, grads)):
+                if t.dtype is not g.dtype or t.numel() != g.numel() or t.get_device() != gpu or \
+                        not t.is_contiguous():
+                    _grad_bad("out", t, i, gpu, f"{g.dtype} tensor of {g.numel()} elements")
+        v[1::4] = array.array("q", map(_t_ptr, out))
+    return v, v.buffer_info()[0], n, gpu, grads[0]
 
 
-def _grad_norm_args(n, dev, gpu, norm, ws):
+def _grad_norm_args(n, like, gpu, norm, ws):
     if norm is None:
-        norm = torch.empty((), dtype=torch.float32, device=dev)
+        norm = torch.empty((), dtype=torch.float32, device=like.device)
     elif norm.dtype is not torch.float32 or norm.numel() != 1 or norm.get_device() != gpu:
         raise ValueError(f"norm: expected one f32 element on cuda:{gpu}, got {norm.dtype} "
                          f"{tuple(norm.shape)} on {norm.device}")
-    wsb = _lib.moe_grad_norm_workspace_size(n)
-    if ws is None:
-        ws = torch.empty(max(wsb, 16), dtype=torch.uint8, device=dev)
-    else:
-        _need_bytes(ws, wsb, "ws")
-        if ws.get_device() != gpu:
-            raise ValueError(f"ws: expected on cuda:{gpu}, got {ws.device}")
-    return norm, ws
+    return norm, _need_ws(ws, _lib.moe_grad_norm_workspace_size(n), like, gpu)
 
 
 def moe_grad_norm_workspace_size(n_grads: int) -> int:
@@ -1131,9 +1142,9 @@ def moe_grad_norm(grads, norm: torch.Tensor | None = None,
                   ws: torch.Tensor | None = None) -> torch.Tensor:
     """The norm of all elements of a list of f32 and bf16 tensors (see moe.h):
     one f32 element on their GPU."""
-    v, n, gpu, dev = _grad_list(grads)
-    norm, ws = _grad_norm_args(n, dev, gpu, norm, ws)
-    _enqueue("moe_grad_norm", _lib.moe_grad_norm, gpu, v, n, norm.data_ptr(), ws.data_ptr(),
+    v, at, n, gpu, like = _grad_list(grads)
+    norm, ws = _grad_norm_args(n, like, gpu, norm, ws)
+    _enqueue("moe_grad_norm", _lib.moe_grad_norm, gpu, at, n, norm.data_ptr(), ws.data_ptr(),
              ws.numel())
     return norm
 
@@ -1141,10 +1152,11 @@ def moe_grad_norm(grads, norm: torch.Tensor | None = None,
 def moe_clip_grad_norm(grads, max_norm: float, out=None, norm: torch.Tensor | None = None,
                        ws: torch.Tensor | None = None) -> torch.Tensor:
     """moe_grad_norm, and every tensor times min(1, max_norm / (norm + 1e-6)),
-    in place or into the tensors of `out`. Returns the norm in front of it."""
-    v, n, gpu, dev = _grad_list(grads, out)
-    norm, ws = _grad_norm_args(n, dev, gpu, norm, ws)
-    _enqueue("moe_clip_grad_norm", _lib.moe_clip_grad_norm, gpu, v, n, max_norm, norm.data_ptr(),
+    in place or into the tensors of `out` (of the same types and numbers of
+    elements). Returns the norm in front of it."""
+    v, at, n, gpu, like = _grad_list(grads, out)
+    norm, ws = _grad_norm_args(n, like, gpu, norm, ws)
+    _enqueue("moe_clip_grad_norm", _lib.moe_clip_grad_norm, gpu, at, n, max_norm, norm.data_ptr(),
              ws.data_ptr(), ws.numel())
     return norm
 
@@ -1152,11 +1164,11 @@ def moe_clip_grad_norm(grads, max_norm: float, out=None, norm: torch.Tensor | No
 def moe_grad_clip(grads, norm: torch.Tensor, max_norm: float, out=None):
     """The clipping alone, with a norm that is given (one f32 element on the
     tensors' GPU)."""
-    v, n, gpu, _ = _grad_list(grads, out)
+    v, at, n, gpu, _ = _grad_list(grads, out)
     if norm is None or norm.dtype is not torch.float32 or norm.numel() != 1 or \
             norm.get_device() != gpu:
         raise ValueError(f"norm: expected one f32 element on cuda:{gpu}")
-    _enqueue("moe_grad_clip", _lib.moe_grad_clip, gpu, v, n, norm.data_ptr(), max_norm)
+    _enqueue("moe_grad_clip", _lib.moe_grad_clip, gpu, at, n, norm.data_ptr(), max_norm)
 
 
 # ---------------------------------------------------------------------------

@@ -187,8 +187,45 @@ __global__ __launch_bounds__(256) void grad_scale(GradArgs a, const double *__re
     });
 }
 
+// The whole of a short list in one workgroup: a launch costs the host more
+// than the GPU needs for it. The order of the sum is the workgroup's own.
+__global__ __launch_bounds__(1024) void grad_clip_few(GradArgs a, float *__restrict__ norm,
+                                                      float max_norm, int clip) {
+    __shared__ double w[16];
+    auto each = [&](auto f) {
+        for (int i = 0; i < a.count; i++) f(a.t[i]);
+    };
+    double s = 0.;
+    each([&](const GradItem &t) {
+        for (int i = threadIdx.x; i < (int)t.n; i += 1024) {
+            const double x = t.bf16 ? grad_elem<true>(t.in, i) : grad_elem<false>(t.in, i);
+            s = fma(x, x, s);
+        }
+    });
+    s = wave_sum(s);
+    if ((threadIdx.x & 63) == 0) w[threadIdx.x >> 6] = s;
+    __syncthreads();
+    s = 0.;
+#pragma unroll
+    for (int i = 0; i < 16; i++) s += w[i];
+    const double v = sqrt(s);
+    if (threadIdx.x == 0) *norm = (float)v;
+    if (!clip) return;
+    const float scale = clip_scale(v, max_norm);
+    each([&](const GradItem &t) {
+        if (scale == 1.f && t.in == t.out) return;
+        for (int i = threadIdx.x; i < (int)t.n; i += 1024) {
+            if (t.bf16) reinterpret_cast<uint16_t *>(t.out)[i] = f32_to_bf16(grad_elem<true>(t.in, i) * scale);
+            else reinterpret_cast<float *>(t.out)[i] = grad_elem<false>(t.in, i) * scale;
+        }
+    });
+}
+
 // ---------------------------------------------------------------------------
 // launchers
+
+// Elements that one workgroup takes.
+constexpr int64_t kGradFew = 16384;
 
 // The next launch's tensors of a list from item i on (empty ones left out);
 // returns the item after them.
@@ -231,7 +268,19 @@ static int grad_squares_launch(const moe_grad *g, int n, double *part, hipStream
     return np;
 }
 
+// Whether the list is one for grad_clip_few: a then holds all of it.
+static bool grad_few(const moe_grad *g, int n, GradArgs &a) {
+    int64_t total = 0;
+    for (int i = 0; i < n && total <= kGradFew; i++) total += g[i].n;
+    return total <= kGradFew && grad_args(g, n, 0, a) == n;
+}
+
 moe_status grad_norm_launch(const moe_grad *g, int n, float *norm, void *ws, hipStream_t s) {
+    GradArgs a;
+    if (grad_few(g, n, a)) {
+        grad_clip_few<<<1, 1024, 0, s>>>(a, norm, 0.f, 0);
+        return launch_status();
+    }
     const int np = grad_squares_launch(g, n, (double *)ws, s);
     grad_finish<<<1, 256, 0, s>>>((const double *)ws, np, norm);
     return launch_status();
@@ -241,13 +290,17 @@ moe_status grad_clip_launch(const moe_grad *g, int n, float max_norm, float *nor
                             hipStream_t s) {
     const double *part = nullptr;
     int np = 0;
+    GradArgs a;
+    if (ws && grad_few(g, n, a)) {
+        grad_clip_few<<<1, 1024, 0, s>>>(a, norm, max_norm, 1);
+        return launch_status();
+    }
     if (ws) {
         np = grad_squares_launch(g, n, (double *)ws, s);
         // few partial sums: every workgroup adds them itself
         if (np > 0 && np <= kGradBlocks) part = (const double *)ws;
         else grad_finish<<<1, 256, 0, s>>>((const double *)ws, np, norm);
     }
-    GradArgs a;
     for (int i = 0; i < n;) {
         i = grad_args(g, n, i, a);
         if (a.count == 0) break;
