@@ -216,8 +216,9 @@ struct NormRow {
 // of it is computed: with two workgroups a compute unit (so that the partial
 // sums stay small) nothing else would hide the two reductions of a row (16384 x
 // 2048 74.7 -> 53.4 us, 32768 x 4096 267 -> 180 us).
-// RMS: mean is not read, and the workgroups leave part[blockIdx.x][d].
-template <bool BF16, int G, int V, bool CKPT, bool RMS>
+// RMS: mean is not read, and the workgroups leave part[blockIdx.x][d]. ONCE: the
+// rows are read past the last-level cache (kOnceBytes).
+template <bool BF16, int G, int V, bool CKPT, bool RMS, bool ONCE>
 __global__ __launch_bounds__(norm_threads(G)) void norm_bwd(
     const uint4 *__restrict__ dy, const uint4 *__restrict__ x,
     const typename Codes<BF16>::type *__restrict__ x8, const uint8_t *__restrict__ x8_scale,
@@ -250,13 +251,13 @@ __global__ __launch_bounds__(norm_threads(G)) void norm_bwd(
         for (int i = 0; i < V; i++) {
             const int c = lane + i * G;
             if (c >= nv) continue;
-            w.dy[i] = dy[base + c];
+            w.dy[i] = ONCE ? load_once(dy + base + c) : dy[base + c];
             if constexpr (CKPT) {
                 w.q[i] = x8[base + c];
                 w.sc[i] = x8_scale[(base + c) / R::LPB];
             } else
-                w.x[i] = x[base + c];
-            if (dsum) w.ds[i] = dsum[base + c];
+                w.x[i] = ONCE ? load_once(x + base + c) : x[base + c];
+            if (dsum) w.ds[i] = ONCE ? load_once(dsum + base + c) : dsum[base + c];
         }
     };
     int par = 0;
@@ -505,6 +506,13 @@ size_t norm_bwd_ws_bytes(moe_dtype dt, int64_t T, int d) {
 }
 size_t rms_bwd_ws_bytes(moe_dtype dt, int64_t T, int d) { return norm_bwd_ws_bytes(dt, T, d) / 2; }
 
+// Bytes of a matrix from which the RMS backward reads its rows past the
+// last-level cache (256 MiB), where a part of them would only push out the
+// rest: bf16 with a stream gradient, 32768 x 4096 204 -> 177 us, 65536 x 1024 103
+// -> 87, 16384 x 2048 behind its forward 130 -> 123; but where all of it is there
+// already, 16384 x 2048 45 -> 49 and 1003 x 4128 fp32 14.2 -> 15.0.
+constexpr int64_t kOnceBytes = 64 << 20;
+
 template <bool BF16, bool RMS>
 static moe_status norm_bwd_run(const void *dy, const void *x, const uint8_t *x8,
                                const uint8_t *x8_scale, const float *mean, const float *rstd,
@@ -515,14 +523,17 @@ static moe_status norm_bwd_run(const void *dy, const void *x, const uint8_t *x8,
     const int nv = d / Row16<BF16>::N, g = norm_group(nv, true), v = norm_vecs(nv, true);
     const int np = (int)norm_bwd_blocks(T, nv);
     const float inv_d = 1.f / (float)d;
-#define F2(G, V, K)                                                                              \
-    norm_bwd<BF16, G, V, K, RMS><<<np, norm_threads(G), 0, s>>>(                                      \
+    const bool once = T * nv * 16 >= kOnceBytes;
+#define F3(G, V, K, O)                                                                            \
+    norm_bwd<BF16, G, V, K, RMS, O><<<np, norm_threads(G), 0, s>>>(                              \
         at<const uint4>(dy, 0), at<const uint4>(x, 0), at<const C>(x8, 0), x8_scale, mean, rstd, \
         gamma, at<const uint4>(dsum, 0), T, nv, inv_d, at<uint4>(dx, 0), part)
-#define F(G, V) if (x8) F2(G, V, true); else F2(G, V, false)
+#define F2(G, V, K) if (RMS && once) F3(G, V, K, RMS); else F3(G, V, K, false)
+#define F(G, V) if (x8) { F2(G, V, true); } else { F2(G, V, false); }
     if (np > 0) { NORM_SWITCH(true, F) }
 #undef F
 #undef F2
+#undef F3
     if (dgamma || dbeta)
         norm_bwd_params<<<dim3(d / 32, RMS ? 1 : 2), 1024, 0, s>>>(part, np, d, dgamma, dbeta, accumulate);
     return launch_status();
