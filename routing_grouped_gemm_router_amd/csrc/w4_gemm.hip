@@ -53,6 +53,8 @@ void w4_gemm_tiles(moe_w4_gemm_desc g) {
     static_assert(BM % 64 == 0 && BN % 64 == 0, "a wave's scale words are of one operand");
     static_assert(STAGES >= 2 && STAGES <= 5, "two slots of four steps of scales");
     constexpr int STAGE = BM * 8 + BN * 4;                            // uint4
+    // the grid has as many workgroups as fit: LDS with the tables' 4.1 KiB
+    static_assert((STAGES * STAGE + 2 * SROWS) * 16 + 4096 <= 163840 / (OCC * 4 / NW), "LDS");
     __shared__ __attribute__((aligned(1024))) uint4 pool[STAGES * STAGE];
     // scale words: a slot for each stage, 4 bytes a row, or where a row's scales
     // come in whole 16-byte groups two slots of four steps
@@ -299,22 +301,25 @@ static void w4_gemm_run(const moe_w4_gemm_desc &g, hipStream_t s) {
     const int grid = (num_cus() * per_cu + 7) / 8 * 8;
     w4_gemm_tiles<SWIGLU, BM, BN, WM, WN, STAGES, OCC><<<grid, WM * WN * 64, 0, s>>>(g);
 }
-// Large tiles where they fill the chip and an expert's rows fill most of one,
-// small ones otherwise: a large tile moves 32 KiB for 2^22 products where two
-// small ones of half its columns move 48, a small one leaves fewer rows of a
-// group's last tile empty and gives more workgroups. us, large / small:
-//   E = 128, k = 4, up (K = N = 2048): 32 rows an expert 69 / 65, 128 rows 110 /
-//     152, 512 rows 293 / 463
-//   E = 32, 31 rows an expert (256 large tiles): up 27.7 / 20.3, down (K = 1024)
-//     17.1 / 14.7
-static bool w4_small_tiles(const moe_w4_gemm_desc &g) {
-    const int64_t tiles = (g.rows / 128 + g.n_groups / 2) * ((g.N + 255) / 256);
-    return g.rows <= 64 * (int64_t)g.n_groups || tiles < 512;
-}
-
+// The tile by the rows of a group (r, on average over the groups that can have
+// any) and the number of large tiles: large ones (128 rows x 256) move the fewest
+// bytes a product, medium ones (128 x 128) where the large leave compute units
+// without one, small ones (64 x 128, in three stages) where the weights' stream
+// is what counts or nothing fills the chip. us, up (K = N = 2048) unless said
+// otherwise, small / medium / large:
+//   E = 128: r = 32 65 / - / 70, r = 40 70 / 83 / 70, r = 64 94 / 85 / 72, r = 128 152 / - /
+//     106, r = 512 463 / 350 / 288
+//   E = 32: r = 31 20 / - / 27, r = 64 (256 tiles) 33 / 24 / 28
+//   E = 8: r = 32 (48 tiles) 15.6 / 16.6 / 23.3, r = 256 (160) 29 / 22 / 26, r = 512 (288)
+//     40 / 34 / 31
+//   E = 8, r = 64, K = 1024 (64 tiles) 11.0 / 12.4 / 15.7
 template <bool SWIGLU>
 static void w4_gemm_pick(const moe_w4_gemm_desc &g, hipStream_t s) {
-    if (w4_small_tiles(g)) w4_gemm_run<SWIGLU, 64, 128, 2, 2, 3, 2>(g, s);
+    const int64_t groups = g.rows < g.n_groups ? g.rows : g.n_groups;
+    const int64_t half = g.rows / 64 + groups, m = half > 2 * groups ? half : 2 * groups;
+    const int64_t tiles = m * ((g.N + 255) / 256) / 2;
+    if (g.rows <= 40 * groups || tiles <= 64) w4_gemm_run<SWIGLU, 64, 128, 2, 2, 3, 2>(g, s);
+    else if (tiles <= 256) w4_gemm_run<SWIGLU, 128, 128, 2, 2, 2, 2>(g, s);
     else w4_gemm_run<SWIGLU, 128, 256, 2, 2, 2, 2>(g, s);
 }
 
