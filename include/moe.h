@@ -787,9 +787,12 @@ moe_status moe_w4_experts(const moe_w4_desc *w, void *stream);
  *               fp32, rounded once, to MXFP8 along h: c [rows, h] and c_scale
  *               [rows, h/32]; the gate and up values are not stored. h a
  *               multiple of 32, at most 8192
- * rows = offsets[n_groups] < 2^31; K: a multiple of 128, K and N at most
- * 16384; a, b and c 16-byte, the scales 4-byte aligned. A row with NaNs reaches
- * no other. Rows outside all groups are not written; rows = 0 is a no-op. */
+ * rows (at least offsets[n_groups]) < 2^31; K: a multiple of 128, K and N at
+ * most 16384; a, b and c 16-byte aligned, a_scale and b_scale 4-byte, with K a
+ * multiple of 512 16-byte. The order of a sum depends on K alone: a row's result
+ * does not depend on the rows, groups or columns around it. A row with NaNs
+ * reaches no other. Rows outside all groups are not written; rows = 0 is a
+ * no-op. */
 typedef struct moe_w4_gemm_desc {
     int32_t n_groups;
     int32_t epilogue;
@@ -808,10 +811,10 @@ typedef struct moe_w4_gemm_desc {
 moe_status moe_w4_gemm(const moe_w4_gemm_desc *g, void *stream);
 
 /* moe_w4_experts for the many tokens of a prompt: x comes in MXFP8 (w->x the
- * E4M3 bytes [T, d], x_scale [T, d/32], 4-byte aligned) and H' is rounded to
- * MXFP8 along h between the two products (moe_w4_gemm), the experts' outputs to
- * bf16 in front of the combine. d and h: multiples of 128; the rest as in
- * moe_w4_experts, but for ws: moe_w4_experts8_workspace_size bytes. */
+ * E4M3 bytes [T, d], x_scale [T, d/32]) and H' is rounded to MXFP8 along h
+ * between the two products (moe_w4_gemm, with its alignments), the experts'
+ * outputs to bf16 in front of the combine. d and h: multiples of 128; the rest
+ * as in moe_w4_experts, but for ws: moe_w4_experts8_workspace_size bytes. */
 size_t moe_w4_experts8_workspace_size(int64_t T, int32_t k, int32_t d, int32_t h);
 moe_status moe_w4_experts8(const moe_w4_desc *w, const uint8_t *x_scale, void *stream);
 

@@ -852,6 +852,11 @@ moe_status moe_w4_experts(const moe_w4_desc *w, void *stream) {
     return w4_experts_launch(w, (hipStream_t)stream);
 }
 
+// scales that are read 16 bytes at once where a row has whole 16 of them
+static bool w4_scale_aligned(const uint8_t *p, int32_t K) {
+    return K % 512 ? aligned4(p) : aligned16(p);
+}
+
 moe_status moe_w4_gemm(const moe_w4_gemm_desc *g, void *stream) {
     if (!g) return MOE_ERR_NULL;
     const bool swiglu = g->epilogue == MOE_EPI_SWIGLU_FWD;
@@ -863,9 +868,9 @@ moe_status moe_w4_gemm(const moe_w4_gemm_desc *g, void *stream) {
     if (!g->offsets || !g->a || !g->a_scale || !g->b || !g->b_scale || !g->c ||
         swiglu == !g->c_scale)
         return MOE_ERR_NULL;
-    if (!aligned16(g->a) || !aligned16(g->b) || !aligned16(g->c) || !aligned4(g->a_scale) ||
-        !aligned4(g->b_scale) || !aligned4(g->c_scale) || !aligned4(g->offsets) ||
-        !aligned4(g->a_rows))
+    if (!aligned16(g->a) || !aligned16(g->b) || !aligned16(g->c) ||
+        !w4_scale_aligned(g->a_scale, g->K) || !w4_scale_aligned(g->b_scale, g->K) ||
+        !aligned4(g->offsets) || !aligned4(g->a_rows))
         return MOE_ERR_ALIGN;
     return w4_gemm_launch(*g, (hipStream_t)stream);
 }
@@ -887,8 +892,8 @@ moe_status moe_w4_experts8(const moe_w4_desc *w, const uint8_t *x_scale, void *s
         !w->w1q || !w->w1_scale || !w->w2q || !w->w2_scale || !w->out || !w->ws)
         return MOE_ERR_NULL;
     if (!aligned16(w->x) || !aligned16(w->out) || !aligned16(w->w1q) || !aligned16(w->w2q) ||
-        !aligned16(w->ws) || !aligned4(x_scale) || !aligned4(w->w1_scale) ||
-        !aligned4(w->w2_scale))
+        !aligned16(w->ws) || !w4_scale_aligned(x_scale, w->d) ||
+        !w4_scale_aligned(w->w1_scale, w->d) || !w4_scale_aligned(w->w2_scale, w->h))
         return MOE_ERR_ALIGN;
     if (w->ws_bytes < w4_experts8_ws_bytes(w->T * w->k, w->d, w->h)) return MOE_ERR_WORKSPACE;
     return w4_experts8_launch(*w, x_scale, (hipStream_t)stream);

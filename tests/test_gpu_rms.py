@@ -226,6 +226,19 @@ def test_offsets_past_32_bits():
     assert torch.equal(b["dx"][-6:], b1["dx"])
 
 
+@pytest.mark.parametrize("dt,T,d", [("bf16", 8200, 4096), ("f32", 4100, 4128), ("bf16", 33000, 1056)])
+@pytest.mark.parametrize("act8", [False, True])
+def test_backward_of_large_matrices(dt, T, d, act8):
+    """Matrices beyond what the last-level cache is used for (their kernel is
+    one of its own, whose roundings may fall elsewhere): the formula."""
+    x, ds, ga = _inputs(T, d, dt, 5)
+    dy = dev(synth.normal((T, d), 9, 2, 1.0), DT[dt])
+    f = moe.moe_rms_norm(x, ga, EPS, act8=act8)
+    b = moe.moe_rms_norm_backward(f if act8 else dict(f, x=x), dy, ga, ds)
+    s = ops.act8_decode(to_np(f["x8"]).view(np.int8), to_np(f["x8_scale"])) if act8 else _f64(x)
+    _check_backward(b, s, _f64(f["rstd"]), dy, ga, ds, dt, T, "large")
+
+
 @pytest.mark.parametrize("dt", ["bf16", "f32"])
 def test_dequantize_every_code(dt):
     """Every element under every scale byte: exact in fp32, rounded once in

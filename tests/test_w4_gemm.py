@@ -50,7 +50,8 @@ def test_gemm_refusals():
         assert status(**{n: U}) == 4, n
     for n in ("a_scale", "b_scale", "offsets", "a_rows"):
         assert status(**{n: F + 2}) == 4, n
-    assert status(epilogue=1, c_scale=F + 1) == 4
+    for n in ("a_scale", "b_scale"):
+        assert status(**{n: F + 4}, K=512) == 4 and status(**{n: F + 4}, K=640, rows=0) == 0
     assert status(rows=0, a=None, c=None, offsets=None) == 0
 
 
@@ -76,6 +77,7 @@ def test_experts8_refusals():
     for n in ("x", "out", "w1q", "w2q", "ws"):
         assert status(**{n: U}) == 4, n
     assert status(w1_scale=F + 2) == 4 and status(w2_scale=F + 1) == 4 and status(xs=F + 2) == 4
+    assert status(d=512, w1_scale=F + 4) == 4 and status(d=512, xs=F + 4) == 4 and status(h=512, w2_scale=F + 4) == 4
     need = moe.moe_w4_experts8_workspace_size(4, 2, 128, 128)
     assert need == 8 * 128 + 256 + 8 * 128 * 2 and status(ws_bytes=need - 1) == 5
     assert status(T=0, x=None, out=None, ws=None) == 0
@@ -154,6 +156,46 @@ def test_whole_numbers(kind, E, N, K, gather):
     assert np.array_equal(ref * 4, np.rint(ref * 4))
     assert torch.equal(got[:R].cpu(), want)
     assert (out[0] == 7).all() and (out[R + 1:] == 7).all()
+
+
+@gpu
+@pytest.mark.parametrize("gather", [False, True])
+@pytest.mark.parametrize("E,N,K,counts", [
+    (3, 16384, 128, (300, 0, 213)), (8, 8192, 384, (130, 64, 256, 0, 1, 127, 129, 400)),
+    (2, 16384, 512, (385, 640)), (5, 2080, 640, (700, 13, 129, 500, 255)),
+    # medium tiles
+    (2, 4096, 512, (150, 61)), (6, 1056, 1024, (90, 190, 33, 0, 64, 65))])
+def test_whole_numbers_many_rows(E, N, K, counts, gather):
+    """The larger tiles' sizes, on sums that fp32 holds; every group by itself
+    (small tiles) gives the same bits on values that are rounded."""
+    rng = np.random.default_rng(N + K + gather)
+    off = np.concatenate([[0], np.cumsum(counts)]).astype(np.int32)
+    R = int(off[-1])
+    total = R // 2 if gather else R
+    a, sa = _whole((total, K), rng, min(1.0, 24 / K))
+    b, sb = _whole((E, N, K), rng, 0.5)
+    rows = rng.integers(0, total, R).astype(np.int32) if gather else np.arange(R, dtype=np.int32)
+    aq, as_, bq, bs, o, ar = _cuda(_e4m3(a), sa, _e2m1(b), sb, off, rows)
+    got = moe.moe_w4_gemm(aq, as_, bq, bs, o, a_rows=ar if gather else None)
+    av, bv = _val(a, sa), _val(b, sb)
+    ref = np.concatenate([av[rows[off[e]:off[e + 1]]] @ bv[e].T for e in range(E)])
+    assert torch.equal(got.cpu(), torch.from_numpy(ref).to(torch.bfloat16))
+    x = torch.randint(0, 256, aq.shape, dtype=U8, device="cuda")
+    x[(x & 0x7F) == 0x7F] = 0x70                            # no NaNs
+    w = torch.randint(0, 256, bq.shape, dtype=U8, device="cuda")
+    epi = moe.MOE_EPI_SWIGLU_FWD if N % 64 == 0 else moe.MOE_EPI_NONE
+    for ep in {moe.MOE_EPI_NONE, epi}:
+        whole = moe.moe_w4_gemm(x, as_, w, bs, o, ep, ar if gather else None)
+        for e in range(E):
+            sl = slice(int(off[e]), min(int(off[e + 1]), int(off[e]) + 40))
+            if sl.start == sl.stop:
+                continue
+            one = moe.moe_w4_gemm(x, as_, w[e:e + 1], bs[e:e + 1],
+                                  torch.tensor([0, sl.stop - sl.start], dtype=I32, device="cuda"), ep,
+                                  ar[sl].contiguous() if gather else torch.arange(sl.start, sl.stop, dtype=I32,
+                                                                                  device="cuda"))
+            for p, q in zip(whole if ep else (whole,), one if ep else (one,)):
+                assert torch.equal(p[sl], q), (ep, e)
 
 
 def _real(rows, cols, seed, i):
@@ -353,6 +395,36 @@ def test_prompt_object():
         layer.prompt(None, logits)
     with pytest.raises(ValueError, match="xq"):
         layer.prompt(None, logits, xq=(norm.q[0][:5], norm.q[1][:5]))
+
+
+@gpu
+def test_another_stream():
+    """On a stream of its own, behind work that makes the inputs there."""
+    (xq, xs), v, w1, w2, w, r = _layer(300, 256, 128, 4, 2, 67)
+    want = moe.moe_w4_experts8(xq, xs, r, *w)
+    torch.cuda.synchronize()
+    side = torch.cuda.Stream()
+    with torch.cuda.stream(side):
+        x2, s2 = torch.zeros_like(xq), torch.zeros_like(xs)
+        x2.copy_(xq)
+        s2.copy_(xs)
+        got = moe.moe_w4_experts8(x2, s2, r, *w)
+    side.synchronize()
+    assert torch.equal(got, want)
+
+
+@gpu
+def test_dropped_slots():
+    """Slots with a negative position add nothing; their rows are computed."""
+    (xq, xs), v, w1, w2, w, r = _layer(50, 128, 128, 3, 2, 68)
+    full = moe.moe_w4_experts8(xq, xs, r, *w)
+    cut = dict(r, token_pos=r["token_pos"].clone(), topk_gate=r["topk_gate"].clone())
+    cut["token_pos"][::3, 1] = -1
+    got = moe.moe_w4_experts8(xq, xs, cut, *w)
+    gate = r["topk_gate"].clone()
+    gate[::3, 1] = 0
+    want = moe.moe_w4_experts8(xq, xs, dict(r, topk_gate=gate), *w)
+    assert torch.equal(got, want) and not torch.equal(got, full)
 
 
 @gpu
