@@ -59,6 +59,20 @@ MOE_DEV int find_group(const int32_t *s_tile, int E, int mt) {
     return lo;
 }
 
+// The same for the whole wave at once: how many of pre[1 .. n] (n <= 256, not
+// decreasing) are <= v, the last i with pre[i] <= v where pre[0] is. Four reads
+// in flight where the search by halves waits for eight in turn. All lanes active.
+MOE_DEV int count_up_to(const int32_t *pre, int n, int v) {
+    const int lane = threadIdx.x & 63;
+    bool le[4];
+#pragma unroll
+    for (int j = 0; j < 4; j++) le[j] = 1 + lane + 64 * j <= n && pre[1 + lane + 64 * j] <= v;
+    int c = 0;
+#pragma unroll
+    for (int j = 0; j < 4; j++) c += __popcll(__ballot(le[j]));
+    return c;
+}
+
 // silu(a) = a * sigmoid(a), the sigmoid by the hardware reciprocal (1 ulp)
 // instead of a correctly rounded divide: the SwiGLU epilogues' VALU work is
 // exposed between tiles (GEMM2 dgrad + SwiGLU backward 6 % faster; the
@@ -161,15 +175,12 @@ MOE_DEV RowSchedule build_row_schedule(const int32_t *s_tile, int E, int n_tiles
 MOE_DEV void decode_row_tile(const RowSchedule &rs, const int32_t *s_tile, const int32_t *s_chunk,
                              const int32_t *s_xpre, int E, int xcd, int p, int &e, int &mt_e,
                              int &nt) {
-    int lo = 0, hi = kXcdChunks;          // largest lc with s_xpre[lc] <= p
-    while (lo < hi) {
-        int mid = (lo + hi + 1) >> 1;
-        if (s_xpre[mid] <= p) lo = mid; else hi = mid - 1;
-    }
-    // entries past this XCD's chunk count repeat the total, which is > p
-    const int c = xcd + 8 * lo;
-    const int o = p - s_xpre[lo];
-    e = find_group(s_chunk, E, c);
+    // the last lc with s_xpre[lc] <= p (entries past this XCD's chunk count
+    // repeat the total, which is > p), then the chunk's group
+    const int lc = count_up_to(s_xpre, kXcdChunks, p);
+    const int c = xcd + 8 * lc;
+    const int o = p - s_xpre[lc];
+    e = count_up_to(s_chunk, E, c);
     // m-tile fastest within the chunk: the XCD's concurrent tiles cover all
     // of the chunk's m-tiles and a few weight panels, so each weight panel
     // is fetched into the XCD's L2 once and shared by the chunk's m-tiles

@@ -96,6 +96,7 @@ void w4_gemm_tiles(moe_w4_gemm_desc g) {
     uint32_t ob[IPB];
     const char *pb = nullptr;
     int ipos = blockIdx.x >> 3, ikt = 0, issued = 0, slot = 1;
+    W4GemmTile ahead{};                  // the tile set up last
     auto setup = [&](const W4GemmTile &t) {
         // row r of the tile in A; past the group's end its last row
         auto src = [&](int r) {
@@ -124,7 +125,10 @@ void w4_gemm_tiles(moe_w4_gemm_desc g) {
     // enqueue the next step's copies, if there is one, into stage buf
     auto issue = [&](int buf) {
         if (ipos >= rs.total) return;
-        if (ikt == 0) setup(decode(ipos));
+        if (ikt == 0) {
+            ahead = decode(ipos);
+            setup(ahead);
+        }
         uint4 *st = pool + buf * STAGE;
         // scales first: a wait for the step's operands then covers them
         if (!batched) {
@@ -267,7 +271,8 @@ void w4_gemm_tiles(moe_w4_gemm_desc g) {
     for (int i = 0; i < STAGES - 1; i++) issue(i);
     int step = 0, buf = 0, batch = 1;
     for (int pos = first; pos < rs.total; pos += workers) {
-        const W4GemmTile cur = decode(pos);
+        // (of a tile of fewer steps than stages the copies are past the next one)
+        const W4GemmTile cur = (ikt == 0 ? ipos - workers : ipos) == pos ? ahead : decode(pos);
 #pragma unroll
         for (int j = 0; j < TN; j++)
 #pragma unroll
