@@ -121,6 +121,7 @@ struct RowSchedule {
     int n_tiles;      // n-tiles per m-tile
     int chm;          // m-tiles per chunk
     int total;        // tiles owned by this workgroup's XCD
+    int split;        // column parts of a chunk, as a power of two
 };
 
 // s_tile: exclusive prefix of m-tiles per group (from build_tile_table).
@@ -141,9 +142,15 @@ MOE_DEV int chunk_first(int mt_e, int chm, int ci) {
     const int n = chunk_count(mt_e, chm);
     return ci * (mt_e / n) + min(ci, mt_e % n);
 }
+// first n-tile of column part j of a chunk
+MOE_DEV int part_first(int n_tiles, int split, int j) { return (n_tiles * j) >> split; }
 
+// units > 0: the chunks are cut by columns too, into 2, 4, .. 64 equal parts, until
+// there are that many of them: with few chunks some XCDs have less to do than
+// others, or nothing. A weight panel is still one XCD's alone; the chunk's
+// activation rows are read by several.
 MOE_DEV RowSchedule build_row_schedule(const int32_t *s_tile, int E, int n_tiles, int xcd,
-                                       int32_t *s_chunk, int32_t *s_xpre) {
+                                       int32_t *s_chunk, int32_t *s_xpre, int units = 0) {
     const int tid = threadIdx.x;
     const int mt_total = s_tile[E];
     // chunk size: at least kChunkM m-tiles, more when needed to stay within kMaxChunks
@@ -151,21 +158,25 @@ MOE_DEV RowSchedule build_row_schedule(const int32_t *s_tile, int E, int n_tiles
     int32_t nc = 0;
     if (tid < E) nc = chunk_count(s_tile[tid + 1] - s_tile[tid], chm);
     scan256(nc, 256, s_chunk);
-    const int C = s_chunk[E];
+    int split = 0;
+    while (split < 6 && (s_chunk[E] << split) < units) split++;
+    const int C = s_chunk[E] << split;
     const int cx = C > xcd ? (C - xcd + 7) / 8 : 0;     // chunks of this XCD (<= 256)
     int32_t t = 0;
     if (tid < cx) {
         const int c = xcd + 8 * tid;
-        const int e = find_group(s_chunk, E, c);
-        const int ci = c - s_chunk[e];
+        const int e = find_group(s_chunk, E, c >> split);
+        const int ci = (c >> split) - s_chunk[e];
         const int mt_e = s_tile[e + 1] - s_tile[e];
-        t = chunk_mtiles(mt_e, chm, ci) * n_tiles;
+        const int j = c & ((1 << split) - 1);
+        t = chunk_mtiles(mt_e, chm, ci) * (part_first(n_tiles, split, j + 1) - part_first(n_tiles, split, j));
     }
     // (C <= kMaxChunks by the choice of chm, so cx <= kXcdChunks)
     scan256(t, kXcdChunks, s_xpre);
     RowSchedule r;
     r.n_tiles = n_tiles;
     r.chm = chm;
+    r.split = split;
     r.total = s_xpre[cx];
     (void)cx;
     return r;
@@ -178,7 +189,7 @@ MOE_DEV void decode_row_tile(const RowSchedule &rs, const int32_t *s_tile, const
     // the last lc with s_xpre[lc] <= p (entries past this XCD's chunk count
     // repeat the total, which is > p), then the chunk's group
     const int lc = count_up_to(s_xpre, kXcdChunks, p);
-    const int c = xcd + 8 * lc;
+    const int u = xcd + 8 * lc, c = u >> rs.split;
     const int o = p - s_xpre[lc];
     e = count_up_to(s_chunk, E, c);
     // m-tile fastest within the chunk: the XCD's concurrent tiles cover all
@@ -187,7 +198,7 @@ MOE_DEV void decode_row_tile(const RowSchedule &rs, const int32_t *s_tile, const
     const int ci = c - s_chunk[e];
     const int cm = chunk_mtiles(s_tile[e + 1] - s_tile[e], rs.chm, ci);
     mt_e = chunk_first(s_tile[e + 1] - s_tile[e], rs.chm, ci) + o % cm;
-    nt = o / cm;
+    nt = part_first(rs.n_tiles, rs.split, u & ((1 << rs.split) - 1)) + o / cm;
 }
 
 // A condition that holds for the whole wave or for none of its lanes, taken

@@ -17,7 +17,16 @@
 // a persistent grid walks each expert's tiles, an XCD its own weight panels.
 // Every wave copies and multiplies; two workgroups a compute unit cover each
 // other's barriers and epilogues. A step is 128 of K: 128 bytes of each row, 64
-// of each weight row, four scales of each.
+// of each weight row, four scales of each. H' is rounded once, from fp32 to the
+// MXFP8 that the second product multiplies; y once, to bf16 in front of the
+// combine, as in the grouped GEMMs.
+//
+// 65536 rows, up and down: E = 128, d = 2048, h = 1024 288 and 178 us (1.9 and
+// 1.55 PFLOP/s); E = 8, d = 4096, h = 2048 937 and 543 us (2.35 and 2.0). Products
+// and their LDS reads alone, in a loop, reach 3.2 PFLOP/s on random data, where
+// the chip's power holds the clock at 1.9 GHz. What is on top of that: the copies,
+// whose 64-byte weight rows cost the L1 a whole line each (alone 194 us of E =
+// 128's up), and the outputs' stores, which come all at once (63 us of its down).
 #include "common.h"
 #include "copy_plan.h"
 #include "gemm_device.h"
@@ -33,6 +42,13 @@ moe_status combine_launch(const void *y, moe_dtype dt, const float *gate,
 // 16-byte pieces are swizzled by (row / 4) % 4, which puts the 16 rows that a
 // ds_read_b128 serves at once on 16 different bank groups.
 MOE_DEV int w4_chunk(int row, int c) { return row * 4 + (c ^ ((row >> 2) & 3)); }
+
+// Chunks of the schedule, at least: two an XCD. One, all parts equal, is as good
+// with 8 groups or more alike (K = N = 2048: within 2 %), with groups of unlike
+// sizes worse (2048 rows of 8 groups, N = 8192, K = 4096: 200 us where no chunk is cut,
+// 199 with 8, 182 with 16, 185 with 32, 190 with 64). 2 groups of 512 rows, K = N =
+// 8192: 213 us where none is cut, 70 with 16.
+constexpr int kUnits = 16;
 
 struct W4GemmTile {
     int e, row0, row_end, nt;
@@ -69,7 +85,7 @@ void w4_gemm_tiles(moe_w4_gemm_desc g) {
     const int xcd = blockIdx.x & 7, workers = gridDim.x >> 3;
     build_tile_table(g.offsets, E, BM, s_off, s_tile);
     const int n_tiles = SWIGLU ? (h + BN / 2 - 1) / (BN / 2) : (N + BN - 1) / BN;
-    const RowSchedule rs = build_row_schedule(s_tile, E, n_tiles, xcd, s_chunk, s_xpre);
+    const RowSchedule rs = build_row_schedule(s_tile, E, n_tiles, xcd, s_chunk, s_xpre, kUnits);
     const int nk = K / 128;
 
     // weight row (of N) of the tile's row n, the last one past the end
@@ -265,7 +281,6 @@ void w4_gemm_tiles(moe_w4_gemm_desc g) {
         }
     };
 
-
     const int first = blockIdx.x >> 3;
     if (first >= rs.total) return;                                // the whole workgroup
     for (int i = 0; i < STAGES - 1; i++) issue(i);
@@ -312,18 +327,19 @@ static void w4_gemm_run(const moe_w4_gemm_desc &g, hipStream_t s) {
 // without one, small ones (64 x 128, in three stages) where the weights' stream
 // is what counts or nothing fills the chip. us, up (K = N = 2048) unless said
 // otherwise, small / medium / large:
-//   E = 128: r = 32 65 / - / 70, r = 40 70 / 83 / 70, r = 64 94 / 85 / 72, r = 128 152 / - /
-//     106, r = 512 463 / 350 / 288
-//   E = 32: r = 31 20 / - / 27, r = 64 (256 tiles) 33 / 24 / 28
-//   E = 8: r = 32 (48 tiles) 15.6 / 16.6 / 23.3, r = 256 (160) 29 / 22 / 26, r = 512 (288)
-//     40 / 34 / 31
-//   E = 8, r = 64, K = 1024 (64 tiles) 11.0 / 12.4 / 15.7
+//   E = 128: r = 32 59 / 74 / 67, r = 40 62 / 75 / 67, r = 64 84 / 79 / 71, r = 128 139 / 123 /
+//     102, r = 512 458 / 326 / 283
+//   E = 32: r = 31 18.5 / 20.6 / 26, r = 64 (256 tiles) 28 / 22 / 27
+//   E = 8: r = 32 (64 tiles) 14.1 / 15.6 / 22, r = 175 (120) 16.6 / 17.5 / 24, r = 256 (160)
+//     25 / 19.7 / 24, r = 512 (288) 36 / 32 / 30
+//   E = 2, K = N = 8192: r = 64 (64 tiles) 41 / 48 / 69, r = 128 (96) 42 / 51 / 73, r = 256
+//     (160; every tile full) 50 / 53 / 74, r = 512 (288; full) 96 / 69 / 81
 template <bool SWIGLU>
 static void w4_gemm_pick(const moe_w4_gemm_desc &g, hipStream_t s) {
     const int64_t groups = g.rows < g.n_groups ? g.rows : g.n_groups;
     const int64_t half = g.rows / 64 + groups, m = half > 2 * groups ? half : 2 * groups;
     const int64_t tiles = m * ((g.N + 255) / 256) / 2;
-    if (g.rows <= 40 * groups || tiles <= 64) w4_gemm_run<SWIGLU, 64, 128, 2, 2, 3, 2>(g, s);
+    if (g.rows <= 40 * groups || tiles <= 128) w4_gemm_run<SWIGLU, 64, 128, 2, 2, 3, 2>(g, s);
     else if (tiles <= 256) w4_gemm_run<SWIGLU, 128, 128, 2, 2, 2, 2>(g, s);
     else w4_gemm_run<SWIGLU, 128, 256, 2, 2, 2, 2>(g, s);
 }
