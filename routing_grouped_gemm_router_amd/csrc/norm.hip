@@ -24,7 +24,10 @@
 // the weights' sums; 32768 x 4096 201 and 185 us (6.0 and 5.1 TB/s); over widths
 // from 32 to 16384, 256 MiB of rows: 4.4 to 5.4 TB/s forward, 3.4 to 4.9 backward
 // (the ends of the backward's range: few columns a thread to sum over, or no
-// registers to load ahead).
+// registers to load ahead). The root-mean-square norm: 16384 x 2048 bf16 with a
+// residual, into s, y and MXFP8 55 us (304 MB, 5.5 TB/s), backward with a stream
+// gradient 46 us (5.9 TB/s) and 4 us for the weights' sum; 8192 x 4096 into s and
+// MXFP8 alone 44 us (236 MB, 5.4 TB/s); one row of 2048 1.9 us.
 #include "act8.h"
 #include "mx_encode.h"
 

@@ -116,6 +116,33 @@ def test_many_tensors(count):
     _check(g, src, norm, 2.0)
 
 
+@pytest.mark.parametrize("sizes", [
+    [1], [64], [1023, 1], [16384], [16385], [1024] * 16, [1024] * 15 + [1025], [1] * 16, [1] * 17,
+    [0, 5000, 0, 1025, 0, 0, 3, 4096, 0], [2, 16000], [0] * 70 + [900, 65] + [0] * 30])
+@pytest.mark.parametrize("kind", ["f32", "bf16", "mixed"])
+def test_short_lists(sizes, kind):
+    """Up to 16 pieces of 1024 elements take one launch, more of them several:
+    the norm, in place, into other tensors and by a given norm."""
+    dts = [{"f32": F32, "bf16": BF16}.get(kind) or (F32 if i % 2 else BF16) for i in range(len(sizes))]
+    for pad in (0, 1):
+        g, flats = _tensors(sizes, dts, 21, pad)
+        src, before = [t.clone() for t in g], {dt: f.clone() for dt, f in flats.items()}
+        o, oflats = _tensors(sizes, dts, 22, pad)
+        norm = _norm64(g)
+        n = moe.moe_grad_norm(g)
+        assert abs(float(n) - norm) <= 2 * U * norm
+        assert torch.equal(moe.moe_clip_grad_norm(g, 0.25, out=o), n)
+        _check(o, src, norm, 0.25)
+        assert all(torch.equal(f, before[dt]) for dt, f in flats.items())
+        assert torch.equal(moe.moe_clip_grad_norm(g, 0.25), n)
+        assert all(torch.equal(a, b) for a, b in zip(g, o))
+        for t, b in zip(g, src):
+            t.copy_(b)
+        assert all(torch.equal(f, before[dt]) for dt, f in flats.items())   # between them
+        moe.moe_grad_clip(g, n, 0.25)
+        _check(g, src, norm, 0.25)
+
+
 def test_all_empty():
     e = torch.empty(0, device="cuda")
     assert float(moe.moe_grad_norm([e, e])) == 0.0
