@@ -695,8 +695,9 @@ moe_status moe_rms_norm_backward(const void *dy, moe_dtype dt, const void *x, co
  * moe_grad_clip: out, from a norm that is given (one that several GPUs' norms
  *   were joined to, or that covers tensors outside the list).
  * Clipping writes: no two outs may overlap, nor an out another tensor's data,
- * nor its own but for being it (MOE_ERR_SHAPE). ws:
- * moe_grad_norm_workspace_size bytes, 16-byte aligned. max_norm >= 0 and not a
+ * nor its own but for being it (MOE_ERR_SHAPE). norm and ws lie outside all
+ * tensors of the list. ws: moe_grad_norm_workspace_size bytes, one for every
+ * call that may overlap in time, 16-byte aligned. max_norm >= 0 and not a
  * NaN (MOE_ERR_SHAPE). */
 #define MOE_GRAD_MAX 4096
 typedef struct moe_grad {
@@ -792,7 +793,7 @@ moe_status moe_w4_experts(const moe_w4_desc *w, void *stream);
  * multiple of 512 16-byte. The order of a sum depends on K alone: a row's result
  * does not depend on the rows, groups or columns around it. A row with NaNs
  * reaches no other. Rows outside all groups are not written; rows = 0 is a
- * no-op. */
+ * no-op. c and c_scale overlap none of the inputs. */
 typedef struct moe_w4_gemm_desc {
     int32_t n_groups;
     int32_t epilogue;

@@ -1520,7 +1520,7 @@ class RMSNorm:
         self._sizes, self._key = _Sizes(), None
 
     def forward(self, x: torch.Tensor, residual: torch.Tensor | None = None) -> torch.Tensor:
-        key = (x.shape, x.dtype, x.device, residual is None)
+        key = (x.shape, x.dtype, x.device, residual is None, self.quantize, self.act8)
         if self._key != key:
             self._out = self.grads = self._key = None
             self._buf = self._sizes.at(key)

@@ -368,3 +368,21 @@ def test_refused_calls_leave_the_object_usable():
     assert torch.equal(norm.backward(n(2, 8))["dx"], want)
     with pytest.raises(ValueError, match="want_y"):
         moe.moe_rms_norm(n(1, 8), w, want_y=False)
+
+
+def test_an_objects_outputs_may_change():
+    """quantize and act8 set and taken back between two forwards of a size."""
+    x = dev(synth.normal((33, 96), 31, 0, 1.0), torch.bfloat16)
+    norm = moe.RMSNorm(dev(synth.normal((96,), 31, 1, 1.0), torch.float32))
+    y = norm.forward(x).clone()
+    assert norm.q is None
+    norm.quantize = True
+    assert torch.equal(norm.forward(x), y)
+    q, s = moe.mxfp8_quantize(y, 1)
+    assert torch.equal(norm.q[0].view(-1), q.view(-1)) and torch.equal(norm.q[1].view(-1), s.view(-1))
+    norm.act8 = True
+    assert torch.equal(norm.forward(x), y)
+    norm.backward(y)
+    norm.quantize = norm.act8 = False
+    assert torch.equal(norm.forward(x), y) and norm.q is None
+    norm.backward(y)
