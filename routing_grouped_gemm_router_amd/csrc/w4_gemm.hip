@@ -17,16 +17,22 @@
 // a persistent grid walks each expert's tiles, an XCD its own weight panels.
 // Every wave copies and multiplies; two workgroups a compute unit cover each
 // other's barriers and epilogues. A step is 128 of K: 128 bytes of each row, 64
-// of each weight row, four scales of each. H' is rounded once, from fp32 to the
-// MXFP8 that the second product multiplies; y once, to bf16 in front of the
-// combine, as in the grouped GEMMs.
+// of each weight row, four scales of each. Where a row's scales come in whole 16
+// bytes (K a multiple of 512) those of four steps are copied together and read from
+// LDS once, into two registers a row from which the instruction picks its byte (up,
+// K = N = 2048, 8 experts of 256 rows 19.6 -> 17.9 us against a read a step, 65536 rows
+// of 128 experts 280 -> 272). H' is rounded once, from fp32 to the MXFP8 that the
+// second product multiplies; y once, to bf16 in front of the combine, as in the
+// grouped GEMMs.
 //
-// 65536 rows, up and down: E = 128, d = 2048, h = 1024 288 and 178 us (1.9 and
-// 1.55 PFLOP/s); E = 8, d = 4096, h = 2048 937 and 543 us (2.35 and 2.0). Products
+// 65536 rows, up and down: E = 128, d = 2048, h = 1024 272 and 179 us (2.0 and
+// 1.54 PFLOP/s); E = 8, d = 4096, h = 2048 917 and 537 us (2.4 and 2.05). Products
 // and their LDS reads alone, in a loop, reach 3.2 PFLOP/s on random data, where
 // the chip's power holds the clock at 1.9 GHz. What is on top of that: the copies,
 // whose 64-byte weight rows cost the L1 a whole line each (alone 194 us of E =
 // 128's up), and the outputs' stores, which come all at once (63 us of its down).
+#include <type_traits>
+
 #include "common.h"
 #include "copy_plan.h"
 #include "gemm_device.h"
@@ -43,11 +49,11 @@ moe_status combine_launch(const void *y, moe_dtype dt, const float *gate,
 // ds_read_b128 serves at once on 16 different bank groups.
 MOE_DEV int w4_chunk(int row, int c) { return row * 4 + (c ^ ((row >> 2) & 3)); }
 
-// Chunks of the schedule, at least: two an XCD. One, all parts equal, is as good
-// with 8 groups or more alike (K = N = 2048: within 2 %), with groups of unlike
-// sizes worse (2048 rows of 8 groups, N = 8192, K = 4096: 200 us where no chunk is cut,
-// 199 with 8, 182 with 16, 185 with 32, 190 with 64). 2 groups of 512 rows, K = N =
-// 8192: 213 us where none is cut, 70 with 16.
+// Chunks of the schedule, at least: two an XCD. One an XCD is as good with 8
+// groups alike (K = N = 2048: within 2 %), with unlike ones worse (2048 rows of 8
+// groups, N = 8192, K = 4096, small tiles: 200 us where no chunk is cut, 199 with 8,
+// 182 with 16, 185 with 32, 190 with 64). 2 groups of 512 rows, K = N = 8192, large
+// tiles: 213 us where none is cut, 85 with 16.
 constexpr int kUnits = 16;
 
 struct W4GemmTile {
@@ -57,7 +63,7 @@ struct W4GemmTile {
 // BM rows x BN weight rows a tile, WM x WN waves. SWIGLU: the weight rows of a
 // wave are gate rows, then the up rows of the same hidden units; c is E4M3 H'
 // [rows, N / 2] with c_scale. Otherwise c is bf16 [rows, N].
-template <bool SWIGLU, int BM, int BN, int WM, int WN, int STAGES, int OCC>
+template <bool SWIGLU, bool BATCHED, int BM, int BN, int WM, int WN, int STAGES, int OCC>
 __global__ __launch_bounds__(WM *WN * 64) __attribute__((amdgpu_waves_per_eu(OCC, OCC)))
 void w4_gemm_tiles(moe_w4_gemm_desc g) {
     constexpr int NW = WM * WN, WTM = BM / WM, WTN = BN / WN, TM = WTM / 32, TN = WTN / 32;
@@ -67,7 +73,7 @@ void w4_gemm_tiles(moe_w4_gemm_desc g) {
     static_assert(IPA * 64 * NW == BM * 8 && IPB * 64 * NW == BN * 4, "whole copies");
     constexpr int SROWS = BM + BN, SPW = (SROWS / 64 + NW - 1) / NW;  // scale words
     static_assert(BM % 64 == 0 && BN % 64 == 0, "a wave's scale words are of one operand");
-    static_assert(STAGES >= 2 && STAGES <= 5, "two slots of four steps of scales");
+    static_assert(STAGES == 2 || STAGES == 3, "two slots of four steps of scales");
     constexpr int STAGE = BM * 8 + BN * 4;                            // uint4
     // the grid has as many workgroups as fit: LDS with the tables' 4.1 KiB
     static_assert((STAGES * STAGE + 2 * SROWS) * 16 + 4096 <= 163840 / (OCC * 4 / NW), "LDS");
@@ -81,7 +87,6 @@ void w4_gemm_tiles(moe_w4_gemm_desc g) {
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int wm = wave / WN, wn = wave % WN;
     const int E = g.n_groups, K = g.K, N = g.N, h = N / 2;
-    const bool batched = (K / 32) % 16 == 0;
     const int xcd = blockIdx.x & 7, workers = gridDim.x >> 3;
     build_tile_table(g.offsets, E, BM, s_off, s_tile);
     const int n_tiles = SWIGLU ? (h + BN / 2 - 1) / (BN / 2) : (N + BN - 1) / BN;
@@ -139,20 +144,22 @@ void w4_gemm_tiles(moe_w4_gemm_desc g) {
         }
     };
     // enqueue the next step's copies, if there is one, into stage buf
-    auto issue = [&](int buf) {
+    auto issue = [&](int buf, auto phase) {
+        // BATCHED: the step of its four, known here; else any
+        constexpr int P = decltype(phase)::value;
         if (ipos >= rs.total) return;
-        if (ikt == 0) {
+        if ((!BATCHED || P == 0) && ikt == 0) {
             ahead = decode(ipos);
             setup(ahead);
         }
         uint4 *st = pool + buf * STAGE;
         // scales first: a wait for the step's operands then covers them
-        if (!batched) {
+        if constexpr (!BATCHED) {
 #pragma unroll
             for (int q = 0; q < SPW; q++)
                 if ((q * NW + wave) * 64 < SROWS)
                     dma4(ps[q] + ikt * 4, scales + buf * (SROWS / 4) + (q * NW + wave) * 16);
-        } else if ((ikt & 3) == 0) {
+        } else if constexpr (P == 0) {
             slot ^= 1;
 #pragma unroll
             for (int q = 0; q < SPW; q++)
@@ -165,7 +172,8 @@ void w4_gemm_tiles(moe_w4_gemm_desc g) {
 #pragma unroll
         for (int i = 0; i < IPA; i++) dma16(pa[i] + ikt * 128, st + (wave * IPA + i) * 64);
         issued++;
-        if (++ikt == nk) {
+        ikt++;
+        if ((!BATCHED || P == 3) && ikt == nk) {
             ikt = 0;
             ipos += workers;
         }
@@ -184,17 +192,31 @@ void w4_gemm_tiles(moe_w4_gemm_desc g) {
         const uint4 c = st[BM * 8 + w4_chunk(r0 + (lane & 31), 2 * s + half)];
         return i32x8{(int)c.x, (int)c.y, (int)c.z, (int)c.w, 0, 0, 0, 0};
     };
-    auto compute = [&](int buf, int kt, int slot) {
+    // Scale bytes of this lane's rows: for slice s of a step the byte half + 2 s of
+    // the row's word. BATCHED: those of four steps in two registers a row, which
+    // the instruction picks by itself; else of one step.
+    constexpr int SW = BATCHED ? 2 : 1;
+    uint32_t sa[TM][SW], sb[TN][SW];
+    auto read_scale = [&](int slot, int r, uint32_t (&o)[SW]) {
+        if constexpr (BATCHED) {
+            const uint4 w = scales[slot * SROWS + r];
+            const uint32_t sel = half ? 0x07050301 : 0x06040200;
+            o[0] = __builtin_amdgcn_perm(w.y, w.x, sel);
+            o[1] = __builtin_amdgcn_perm(w.w, w.z, sel);
+        } else {
+            o[0] = reinterpret_cast<const uint32_t *>(scales)[slot * SROWS + r] >> (8 * half);
+        }
+    };
+    auto read_scales = [&](int slot) {
+#pragma unroll
+        for (int i = 0; i < TM; i++) read_scale(slot, wm * WTM + i * 32 + (lane & 31), sa[i]);
+#pragma unroll
+        for (int j = 0; j < TN; j++) read_scale(slot, BM + wn * WTN + j * 32 + (lane & 31), sb[j]);
+    };
+    auto compute = [&](int buf, auto step_of_four) {
+        constexpr int Q = decltype(step_of_four)::value;
+        constexpr int W = BATCHED ? Q >> 1 : 0, S0 = BATCHED ? 2 * (Q & 1) : 0, S1 = BATCHED ? S0 + 1 : 2;
         const uint4 *st = pool + buf * STAGE;
-        const uint32_t *sw = reinterpret_cast<const uint32_t *>(
-            scales + (batched ? slot * SROWS : buf * (SROWS / 4))) + (batched ? kt & 3 : 0);
-        const int sp = batched ? 4 : 1;
-        // byte 2 s + half is the scale of this lane's row for slice s
-        uint32_t sa[TM], sb[TN];
-#pragma unroll
-        for (int i = 0; i < TM; i++) sa[i] = sw[(wm * WTM + i * 32 + (lane & 31)) * sp] >> (8 * half);
-#pragma unroll
-        for (int j = 0; j < TN; j++) sb[j] = sw[(BM + wn * WTN + j * 32 + (lane & 31)) * sp] >> (8 * half);
         i32x8 fa[2][TM], fb[TN];
 #pragma unroll
         for (int j = 0; j < TN; j++) fb[j] = frag_b(st, wn * WTN + j * 32, 0);
@@ -208,7 +230,7 @@ void w4_gemm_tiles(moe_w4_gemm_desc g) {
             for (int i = 0; i < TM; i++) {
                 __builtin_amdgcn_sched_barrier(0);
                 acc[j][i] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(
-                    fb[j], fa[0][i], acc[j][i], 4, 0, 0, (int)sb[j], 0, (int)sa[i]);
+                    fb[j], fa[0][i], acc[j][i], 4, 0, S0, (int)sb[j][W], S0, (int)sa[i][W]);
                 __builtin_amdgcn_sched_barrier(0);
                 if (j * TM + i < TM) fa[1][j * TM + i] = frag_a(st, wm * WTM + (j * TM + i) * 32, 1);
             }
@@ -219,7 +241,7 @@ void w4_gemm_tiles(moe_w4_gemm_desc g) {
 #pragma unroll
             for (int i = 0; i < TM; i++)
                 acc[j][i] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(
-                    fb[j], fa[1][i], acc[j][i], 4, 0, 2, (int)sb[j], 2, (int)sa[i]);
+                    fb[j], fa[1][i], acc[j][i], 4, 0, S1, (int)sb[j][W], S1, (int)sa[i][W]);
     };
     // acc[j][i][4 q + x]: row i * 32 + lane % 32 of the wave, output j * 32 + 8 q +
     // 4 half + x. v_permlane32_swap gives the lower half of the lanes both
@@ -283,7 +305,8 @@ void w4_gemm_tiles(moe_w4_gemm_desc g) {
 
     const int first = blockIdx.x >> 3;
     if (first >= rs.total) return;                                // the whole workgroup
-    for (int i = 0; i < STAGES - 1; i++) issue(i);
+    issue(0, std::integral_constant<int, 0>{});
+    if constexpr (STAGES > 2) issue(1, std::integral_constant<int, 1>{});
     int step = 0, buf = 0, batch = 1;
     for (int pos = first; pos < rs.total; pos += workers) {
         // (of a tile of fewer steps than stages the copies are past the next one)
@@ -296,17 +319,32 @@ void w4_gemm_tiles(moe_w4_gemm_desc g) {
                 for (int v = 0; v < 16; v++) acc[j][i][v] = 0.f;
         // a wave whose rows all lie past the group's end only copies
         const bool mine = cur.row0 + wm * WTM < cur.row_end;
-        for (int kt = 0; kt < nk; kt++, step++) {
+        auto next = [&](auto q) {
             // this wave's copies of the step have landed: at most those of the
             // STAGES - 2 steps behind it may be in flight (loads return in order;
             // a store or a scale copy among them makes the wait longer, not shorter)
             if (issued - step >= STAGES - 1) wait_vmem<(STAGES - 2) * (IPA + IPB)>();
             else wait_vmem<0>();
             lds_sync();                  // everybody's, and the stage before has been read
-            issue(buf == 0 ? STAGES - 1 : buf - 1);
-            if ((kt & 3) == 0) batch ^= 1;
-            if (mine) compute(buf, kt, batch);
+            issue(buf == 0 ? STAGES - 1 : buf - 1,
+                  std::integral_constant<int, (decltype(q)::value + STAGES - 1) & 3>{});
+            if constexpr (decltype(q)::value == 0) {
+                if constexpr (BATCHED) batch ^= 1;
+                if (mine) read_scales(BATCHED ? batch : buf);
+            }
+            if (mine) compute(buf, q);
             if (++buf == STAGES) buf = 0;
+            step++;
+        };
+        if constexpr (BATCHED) {
+            for (int kt = 0; kt < nk; kt += 4) {
+                next(std::integral_constant<int, 0>{});
+                next(std::integral_constant<int, 1>{});
+                next(std::integral_constant<int, 2>{});
+                next(std::integral_constant<int, 3>{});
+            }
+        } else {
+            for (int kt = 0; kt < nk; kt++) next(std::integral_constant<int, 0>{});
         }
         if (mine) epilogue(cur);
     }
@@ -319,28 +357,33 @@ template <bool SWIGLU, int BM, int BN, int WM, int WN, int STAGES, int OCC>
 static void w4_gemm_run(const moe_w4_gemm_desc &g, hipStream_t s) {
     constexpr int per_cu = OCC * 4 / (WM * WN);
     const int grid = (num_cus() * per_cu + 7) / 8 * 8;
-    w4_gemm_tiles<SWIGLU, BM, BN, WM, WN, STAGES, OCC><<<grid, WM * WN * 64, 0, s>>>(g);
+    if (g.K % 512 == 0)
+        w4_gemm_tiles<SWIGLU, true, BM, BN, WM, WN, STAGES, OCC><<<grid, WM * WN * 64, 0, s>>>(g);
+    else
+        w4_gemm_tiles<SWIGLU, false, BM, BN, WM, WN, STAGES, OCC><<<grid, WM * WN * 64, 0, s>>>(g);
 }
+
 // The tile by the rows of a group (r, on average over the groups that can have
 // any) and the number of large tiles: large ones (128 rows x 256) move the fewest
-// bytes a product, medium ones (128 x 128) where the large leave compute units
-// without one, small ones (64 x 128, in three stages) where the weights' stream
-// is what counts or nothing fills the chip. us, up (K = N = 2048) unless said
-// otherwise, small / medium / large:
-//   E = 128: r = 32 59 / 74 / 67, r = 40 62 / 75 / 67, r = 64 84 / 79 / 71, r = 128 139 / 123 /
-//     102, r = 512 458 / 326 / 283
-//   E = 32: r = 31 18.5 / 20.6 / 26, r = 64 (256 tiles) 28 / 22 / 27
-//   E = 8: r = 32 (64 tiles) 14.1 / 15.6 / 22, r = 175 (120) 16.6 / 17.5 / 24, r = 256 (160)
-//     25 / 19.7 / 24, r = 512 (288) 36 / 32 / 30
-//   E = 2, K = N = 8192: r = 64 (64 tiles) 41 / 48 / 69, r = 128 (96) 42 / 51 / 73, r = 256
-//     (160; every tile full) 50 / 53 / 74, r = 512 (288; full) 96 / 69 / 81
+// bytes a product, medium ones (128 x 128) where the large would not fill the two
+// workgroups of every compute unit, small ones (64 x 128, in three stages) where
+// the weights' stream is what counts or few have a tile at all. us, up (K = N =
+// 2048) unless said otherwise, small / medium / large:
+//   E = 128: r = 32 56 / 67 / 69, r = 48 64 / 71 / 72, r = 64 80 / 74 / 75, r = 128 124 / 113 /
+//     106, r = 512 371 / 297 / 271
+//   E = 32: r = 40 17.4 / 19.2 / 25, r = 64 (256 large tiles) 23.5 / 20.5 / 26, r = 256 (640)
+//     53 / 47 / 46
+//   E = 8: r = 32 (64) 10.7 / 12.8 / 19.6, r = 175 (120) 13.9 / 14.4 / 21, r = 256 (160) 20.3 /
+//     18.7 / 22, r = 512 (288) 29 / 28 / 30, r = 1024 (544) 46 / 43 / 46, r = 1280 (672) 59 / 52 / 49
+//   E = 2, K = N = 8192: r = 128 (96) 29 / 44 / 61, r = 256 (160) 45 / 45 / 62, r = 512
+//     (288) 84 / 68 / 72, r = 1300 (672) 207 / 180 / 152
 template <bool SWIGLU>
 static void w4_gemm_pick(const moe_w4_gemm_desc &g, hipStream_t s) {
     const int64_t groups = g.rows < g.n_groups ? g.rows : g.n_groups;
     const int64_t half = g.rows / 64 + groups, m = half > 2 * groups ? half : 2 * groups;
     const int64_t tiles = m * ((g.N + 255) / 256) / 2;
-    if (g.rows <= 40 * groups || tiles <= 128) w4_gemm_run<SWIGLU, 64, 128, 2, 2, 3, 2>(g, s);
-    else if (tiles <= 256) w4_gemm_run<SWIGLU, 128, 128, 2, 2, 2, 2>(g, s);
+    if (g.rows <= 48 * groups || tiles <= 128) w4_gemm_run<SWIGLU, 64, 128, 2, 2, 3, 2>(g, s);
+    else if (tiles <= 512) w4_gemm_run<SWIGLU, 128, 128, 2, 2, 2, 2>(g, s);
     else w4_gemm_run<SWIGLU, 128, 256, 2, 2, 2, 2>(g, s);
 }
 

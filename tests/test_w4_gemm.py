@@ -165,7 +165,9 @@ def test_whole_numbers(kind, E, N, K, gather):
     (2, 16384, 512, (385, 640)), (5, 2080, 640, (700, 13, 129, 500, 255)),
     (2, 4096, 512, (150, 61)), (6, 1056, 1024, (90, 190, 33, 0, 64, 65)),
     # medium tiles
-    (2, 8192, 512, (300, 261)), (6, 4128, 1024, (190, 250, 133, 0, 64, 65)), (1, 16384, 640, (250,))])
+    (2, 8192, 512, (300, 261)), (6, 4128, 1024, (190, 250, 133, 0, 64, 65)), (1, 16384, 640, (250,)),
+    # large ones, with scales of one step and of four at a time
+    (3, 16384, 640, (700, 33, 500)), (4, 16384, 1024, (700, 33, 500, 129))])
 def test_whole_numbers_many_rows(E, N, K, counts, gather):
     """The larger tiles' sizes, on sums that fp32 holds; every group by itself
     (small tiles) gives the same bits on values that are rounded."""
