@@ -28,6 +28,8 @@
 // residual, into s, y and MXFP8 55 us (304 MB, 5.5 TB/s), backward with a stream
 // gradient 46 us (5.9 TB/s) and 4 us for the weights' sum; 8192 x 4096 into s and
 // MXFP8 alone 44 us (236 MB, 5.4 TB/s); one row of 2048 1.9 us.
+#include <type_traits>
+
 #include "act8.h"
 #include "mx_encode.h"
 
@@ -65,8 +67,22 @@ MOE_DEV float swap32_sum(float v) {
                                                     false);
     return __uint_as_float(r[0]) + __uint_as_float(r[1]);
 }
-template <int G>
-MOE_DEV float group_sum(float v) {
+MOE_DEV double swap16_sum(double v) {
+    const auto l = __builtin_amdgcn_permlane16_swap(__double2loint(v), __double2loint(v), false, false);
+    const auto h = __builtin_amdgcn_permlane16_swap(__double2hiint(v), __double2hiint(v), false, false);
+    return __hiloint2double(h[0], l[0]) + __hiloint2double(h[1], l[1]);
+}
+MOE_DEV double swap32_sum(double v) {
+    const auto l = __builtin_amdgcn_permlane32_swap(__double2loint(v), __double2loint(v), false, false);
+    const auto h = __builtin_amdgcn_permlane32_swap(__double2hiint(v), __double2hiint(v), false, false);
+    return __hiloint2double(h[0], l[0]) + __hiloint2double(h[1], l[1]);
+}
+template <int CTRL>
+MOE_DEV double dpp_move(double v) {
+    return __hiloint2double(dpp_move<CTRL>(__double2hiint(v)), dpp_move<CTRL>(__double2loint(v)));
+}
+template <int G, typename F>
+MOE_DEV F group_sum(F v) {
     v += dpp_move<kDppXor1>(v);
     v += dpp_move<kDppXor2>(v);
     if constexpr (G >= 8) v += dpp_move<kDppHalfMirror>(v);
@@ -78,18 +94,18 @@ MOE_DEV float group_sum(float v) {
 
 // The waves' sums of a row that is a workgroup (G = 256, 512 or 1024
 // threads), added in a fixed order.
-template <int G>
-MOE_DEV float waves_sum(const float *q) {
-    float v = 0.f;
+template <int G, typename F>
+MOE_DEV F waves_sum(const F *q) {
+    F v = 0;
 #pragma unroll
     for (int i = 0; i < G / 64; i += 4) v += (q[i] + q[i + 1]) + (q[i + 2] + q[i + 3]);
     return v;
 }
 
-// Sum over the row's G threads (red: G / 64 floats of LDS, its own for every
+// Sum over the row's G threads (red: G / 64 values in LDS, its own for every
 // call between two barriers of the row).
-template <int G>
-MOE_DEV float row_sum(float v, float *red) {
+template <int G, typename F>
+MOE_DEV F row_sum(F v, F *red) {
     v = group_sum<G>(v);
     if constexpr (G >= 256) {
         if ((threadIdx.x & 63) == 0) red[threadIdx.x >> 6] = v;
@@ -112,18 +128,39 @@ MOE_DEV void load_params(const float *p, int c, float *f) {
     }
 }
 
+// 1 / sqrt(a) in two parts whose sum is off by some 2^-45 of it: the hardware's
+// reciprocal root and one step of Newton's iteration, whose residual 1 - a r^2 the
+// fused products give exactly. Where a or r^2 leaves fp32's range, lo is 0.
+MOE_DEV void rsqrt_hi_lo(double a, float &hi, float &lo) {
+    const float ah = (float)a, al = (float)(a - (double)ah);
+    // (the instruction takes subnormal numbers as zeros)
+    const float r = ah < 1e-36f ? 1.f / sqrtf(ah) : __builtin_amdgcn_rsqf(ah), q = r * r;
+    float e = fmaf(-ah, q, 1.f);
+    e = fmaf(-ah, fmaf(r, r, -q), e);
+    e = fmaf(-al, q, e);
+    const float c = fabsf(e) < 1e-3f ? 0.5f * r * e : 0.f;
+    hi = r + c;
+    lo = c == 0.f ? 0.f : (r - hi) + c;
+}
+
 // G threads a row, V 16-byte vectors a thread (vector lane + i G of the row).
-// RMS: no mean (and none stored), no beta; y may be null if yq is not.
+// RMS: no mean (and none stored), no beta; y may be null if yq is not. A row's sum
+// is joined in fp64 and s r gamma rounded once, to fp32, in front of y's own
+// rounding: an element of y on the wrong side of a bf16 step may be one of yq on
+// the wrong side of an E4M3 step, a sixteenth of its value. What it takes more
+// than two products an element hides behind the loads.
 template <bool BF16, int G, int V, bool RMS>
 __global__ __launch_bounds__(norm_threads(G)) void norm_fwd(
     const uint4 *__restrict__ x, const uint4 *__restrict__ res, const float *__restrict__ gamma,
-    const float *__restrict__ beta, float eps, int64_t T, int nv, float inv_d,
-    uint4 *__restrict__ y, uint4 *__restrict__ sum, float *__restrict__ mean,
+    const float *__restrict__ beta, float eps, int64_t T, int nv,
+    typename std::conditional<RMS, double, float>::type inv_d, uint4 *__restrict__ y,
+    uint4 *__restrict__ sum, float *__restrict__ mean,
     float *__restrict__ rstd, typename Codes<BF16>::type *__restrict__ x8,
     uint8_t *__restrict__ x8_scale, typename Codes<BF16>::type *__restrict__ yq,
     uint8_t *__restrict__ yq_scale) {
     typedef Row16<BF16> R;
-    __shared__ float red[2][16];
+    typedef typename std::conditional<RMS, double, float>::type Sum;
+    __shared__ Sum red[RMS ? 1 : 2][16];
     const int lane = threadIdx.x % G;
     const int64_t t = (int64_t)blockIdx.x * (norm_threads(G) / G) + threadIdx.x / G;
     if (t >= T) return;                         // G >= 256: never (one row a workgroup)
@@ -150,11 +187,13 @@ __global__ __launch_bounds__(norm_threads(G)) void norm_fwd(
 #pragma unroll
         for (int e = 0; e < R::N; e++) s1 = RMS ? fmaf(f[e], f[e], s1) : s1 + f[e];
     }
-    s1 = row_sum<G>(s1, red[0]);
-    float mu = 0.f, s2 = s1;
-    if constexpr (!RMS) {
+    float mu = 0.f, r, rl = 0.f;
+    if constexpr (RMS) {
+        rsqrt_hi_lo(fma(row_sum<G>((double)s1, red[0]), inv_d, (double)eps), r, rl);
+    } else {
+        s1 = row_sum<G>(s1, red[0]);
         mu = s1 * inv_d;
-        s2 = 0.f;
+        float s2 = 0.f;
 #pragma unroll
         for (int i = 0; i < V; i++) {
             if (lane + i * G >= nv) continue;
@@ -164,8 +203,8 @@ __global__ __launch_bounds__(norm_threads(G)) void norm_fwd(
             for (int e = 0; e < R::N; e++) s2 = fmaf(f[e] - mu, f[e] - mu, s2);
         }
         s2 = row_sum<G>(s2, red[1]);
+        r = 1.f / sqrtf(fmaf(s2, inv_d, eps));
     }
-    const float r = 1.f / sqrtf(fmaf(s2, inv_d, eps));
     if (lane == 0) {
         if (!RMS && mean) mean[t] = mu;
         if (rstd) rstd[t] = r;
@@ -178,7 +217,14 @@ __global__ __launch_bounds__(norm_threads(G)) void norm_fwd(
         R::unpack(w[i], f);
         load_params<BF16>(gamma, c, ga);
 #pragma unroll
-        for (int e = 0; e < R::N; e++) o[e] = (RMS ? f[e] : f[e] - mu) * r * ga[e];
+        for (int e = 0; e < R::N; e++) {
+            if constexpr (RMS) {
+                // (f r + l) gamma; l gamma held in range for the sake of an infinite gamma
+                const float h = f[e] * r, l = fmaf(f[e], rl, fmaf(f[e], r, -h));
+                o[e] = fmaf(h, ga[e], __builtin_amdgcn_fmed3f(l * ga[e], -3e38f, 3e38f));
+            } else
+                o[e] = (f[e] - mu) * r * ga[e];
+        }
         if (!RMS && beta) {
             load_params<BF16>(beta, c, ga);
 #pragma unroll
@@ -453,7 +499,8 @@ static moe_status norm_fwd_run(const void *x, const void *res, const float *gamm
     typedef typename Codes<BF16>::type C;
     const int nv = d / Row16<BF16>::N, g = norm_group(nv, false), v = norm_vecs(nv, false);
     const int nt = norm_threads(g), rows = nt / g;
-    const float inv_d = 1.f / (float)d;
+    typedef typename std::conditional<RMS, double, float>::type Inv;
+    const Inv inv_d = (Inv)1 / (Inv)d;
     const int64_t piece = kMaxBlocks * rows;
     for (int64_t t = 0; t < T; t += piece) {
         const int64_t n = T - t < piece ? T - t : piece;

@@ -92,6 +92,45 @@ def test_forward(dt, T, d):
 
 
 @pytest.mark.parametrize("dt", ["bf16", "f32"])
+@pytest.mark.parametrize("d", [32, 64, 96, 160, 288, 512, 2048, 2080, 4128, 8224, 16384])
+def test_rounded_once(dt, d):
+    """Whole numbers up to 8, whose squares' sum (at most 2^20) fp32 holds: rstd
+    is then known to 2^-46, s rstd gamma to 2^-45 or better, and rounded to fp32
+    it is the 64-bit value's rounding but for one element in 2^20 (those that lie
+    so close to the middle of two fp32 numbers). None may differ in bf16."""
+    rng = np.random.default_rng(d)
+    T = 37
+    s = rng.integers(-8, 9, (T, d)).astype(np.float64)
+    ga = (1 + 0.1 * rng.normal(size=d)).astype(np.float32)
+    out = moe.moe_rms_norm(dev(s, DT[dt]), torch.from_numpy(ga).cuda(), EPS)
+    y, rstd = ops.rms_norm(s, ga.astype(np.float64), float(np.float32(EPS)))
+    want = torch.from_numpy(y.astype(np.float32)).to(DT[dt])
+    diff = int((out["y"].cpu() != want).sum())
+    assert diff <= (1 if dt == "f32" else 0), diff
+    assert np.array_equal(to_np(out["rstd"]), np.asarray(rstd, np.float64).astype(np.float32).ravel())
+
+
+@pytest.mark.parametrize("dt", ["bf16", "f32"])
+@pytest.mark.parametrize("gamma", [np.inf, -np.inf, 3e38, 1e-45])
+def test_extreme_weights(dt, gamma):
+    """A weight beyond the values' range: the formula's infinities, zeros and
+    NaNs (of a zero times an infinity), nothing else."""
+    s = np.array([[1.0, -2.0, 0.0, 3.0] * 16, [0.0] * 64, [1e-3, -1e3, 5.0, 0.25] * 16])
+    ga = np.ones(64, np.float32)
+    ga[::3] = gamma
+    out = moe.moe_rms_norm(dev(s, DT[dt]), torch.from_numpy(ga).cuda(), EPS)
+    x = dev(s, DT[dt]).double().cpu()
+    r = 1 / torch.sqrt((x * x).mean(1, keepdim=True) + EPS)
+    want = (x * r * torch.from_numpy(ga).double()).float().to(DT[dt])
+    got = out["y"].cpu()
+    assert torch.equal(torch.isnan(got), torch.isnan(want)) and torch.equal(torch.isinf(got), torch.isinf(want))
+    ok = torch.isfinite(want)
+    d = (got.double() - want.double()).abs()[ok]
+    # half a step of each side's rounding, and fp32's
+    assert (d <= want.double().abs()[ok] * (2 * H[dt] + 48 * U) + 2.0 ** -133).all()
+
+
+@pytest.mark.parametrize("dt", ["bf16", "f32"])
 @pytest.mark.parametrize("d", [64, 1024, 4096])
 def test_forward_hard_rows(dt, d):
     """Constant rows, zeros, tiny and huge ones, an outlier; a NaN or an
