@@ -787,9 +787,10 @@ moe_status moe_w4_experts(const moe_w4_desc *w, void *stream);
  *   epilogue MOE_EPI_SWIGLU_FWD (N = 2h, gate rows first): H' = silu(a) b in
  *               fp32, rounded once, to MXFP8 along h: c [rows, h] and c_scale
  *               [rows, h/32]; the gate and up values are not stored. h a
- *               multiple of 32, at most 8192
- * rows (at least offsets[n_groups]) < 2^31; K: a multiple of 128, K and N at
- * most 16384; a, b and c 16-byte aligned, a_scale and b_scale 4-byte, with K a
+ *               multiple of 32, at most 8192. An H' beyond fp32's range is
+ *               outside the contract, as an infinity is in mxfp8_quantize
+ * n_groups at most 256; rows (at least offsets[n_groups]) at most 2^31 - 256; K:
+ * a multiple of 128, K and N at most 16384; a, b and c 16-byte aligned, a_scale and b_scale 4-byte, with K a
  * multiple of 512 16-byte. The order of a sum depends on K alone: a row's result
  * does not depend on the rows, groups or columns around it. A row with NaNs
  * reaches no other. Rows outside all groups are not written; rows = 0 is a

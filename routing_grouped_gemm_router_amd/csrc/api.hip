@@ -861,7 +861,8 @@ moe_status moe_w4_gemm(const moe_w4_gemm_desc *g, void *stream) {
     if (!g) return MOE_ERR_NULL;
     const bool swiglu = g->epilogue == MOE_EPI_SWIGLU_FWD;
     if (!swiglu && g->epilogue != MOE_EPI_NONE) return MOE_ERR_DTYPE;
-    if (g->n_groups < 1 || g->n_groups > 256 || g->rows < 0 || g->rows >= ((int64_t)1 << 31) ||
+    // (a tile's rows past the last group stay within 32 bits)
+    if (g->n_groups < 1 || g->n_groups > 256 || g->rows < 0 || g->rows > ((int64_t)1 << 31) - 256 ||
         !width_ok(g->N) || !width_ok(g->K) || g->K % 128 || (swiglu && g->N % 64))
         return MOE_ERR_SHAPE;
     if (g->rows == 0) return MOE_OK;

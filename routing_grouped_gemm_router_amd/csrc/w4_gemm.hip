@@ -251,36 +251,55 @@ void w4_gemm_tiles(moe_w4_gemm_desc g) {
         first = r[0];
         second = r[1];
     };
-    auto epilogue = [&](const W4GemmTile &t) {
+    // H' of the wave's tile in acc[j < TN / 2] to E4M3, by encode
+    auto store_hidden = [&](const W4GemmTile &t, auto encode) {
 #pragma unroll
         for (int i = 0; i < TM; i++) {
             const int row = t.row0 + wm * WTM + i * 32 + (lane & 31);
-            const bool ok = row < t.row_end;
-            if constexpr (SWIGLU) {
-                uint8_t *c = reinterpret_cast<uint8_t *>(g.c) + (int64_t)row * h;
+            uint8_t *c = reinterpret_cast<uint8_t *>(g.c) + (int64_t)row * h;
 #pragma unroll
-                for (int j = 0; j < TN / 2; j++) {
-                    const int n = t.nt * (BN / 2) + wn * (WTN / 2) + j * 32;
-                    if (n >= h) continue;                         // wave-uniform
-                    float f[16], am = 0.f;
+            for (int j = 0; j < TN / 2; j++) {
+                const int n = t.nt * (BN / 2) + wn * (WTN / 2) + j * 32;
+                if (n >= h) continue;                             // wave-uniform
+                const f32x16 &f = acc[j][i];
+                float am = 0.f;
+#pragma unroll
+                for (int v = 0; v < 16; v++) am = fmaxf(am, fabsf(f[v]));
+                const uint32_t sb = mx_scale_byte(max_xor32(am));
+                uint32_t w[4], o[4];
+#pragma unroll
+                for (int q = 0; q < 4; q++) w[q] = encode(f[4 * q], f[4 * q + 1], f[4 * q + 2], f[4 * q + 3], sb);
+                swap32(w[0], w[2], o[0], o[1]);
+                swap32(w[1], w[3], o[2], o[3]);
+                if (row < t.row_end) {
+                    *reinterpret_cast<uint4 *>(c + n + 16 * half) = make_uint4(o[0], o[1], o[2], o[3]);
+                    if (half == 0) g.c_scale[(int64_t)row * (h / 32) + n / 32] = (uint8_t)sb;
+                }
+            }
+        }
+    };
+    auto epilogue = [&](const W4GemmTile &t) {
+        if constexpr (SWIGLU) {
+            // the encoder's form (NaNs or none) by one vote a tile: 1 % of the
+            // kernel against one for every four values
+            bool nan = false;
+#pragma unroll
+            for (int i = 0; i < TM; i++)
+#pragma unroll
+                for (int j = 0; j < TN / 2; j++)
 #pragma unroll
                     for (int v = 0; v < 16; v++) {
-                        f[v] = silu_f(acc[j][i][v]) * acc[j + TN / 2][i][v];
-                        am = fmaxf(am, fabsf(f[v]));
+                        acc[j][i][v] = silu_f(acc[j][i][v]) * acc[j + TN / 2][i][v];
+                        nan |= __builtin_isnan(acc[j][i][v]);
                     }
-                    const uint32_t sb = mx_scale_byte(max_xor32(am));
-                    uint32_t w[4], o[4];
+            auto finite = [](float x, float y, float z, float w, uint32_t sb) { return e4m3x4_finite(x, y, z, w, sb); };
+            auto any = [](float x, float y, float z, float w, uint32_t sb) { return e4m3x4_select(x, y, z, w, sb); };
+            if (__ballot(nan) == 0) store_hidden(t, finite);
+            else store_hidden(t, any);
+        } else {
 #pragma unroll
-                    for (int q = 0; q < 4; q++)
-                        w[q] = e4m3x4(f[4 * q], f[4 * q + 1], f[4 * q + 2], f[4 * q + 3], sb);
-                    swap32(w[0], w[2], o[0], o[1]);
-                    swap32(w[1], w[3], o[2], o[3]);
-                    if (ok) {
-                        *reinterpret_cast<uint4 *>(c + n + 16 * half) = make_uint4(o[0], o[1], o[2], o[3]);
-                        if (half == 0) g.c_scale[(int64_t)row * (h / 32) + n / 32] = (uint8_t)sb;
-                    }
-                }
-            } else {
+            for (int i = 0; i < TM; i++) {
+                const int row = t.row0 + wm * WTM + i * 32 + (lane & 31);
                 uint16_t *c = reinterpret_cast<uint16_t *>(g.c) + (int64_t)row * N;
 #pragma unroll
                 for (int j = 0; j < TN; j++) {
@@ -294,7 +313,7 @@ void w4_gemm_tiles(moe_w4_gemm_desc g) {
                             swap32(pack_bf16x2(acc[j][i][4 * q + 2 * x], acc[j][i][4 * q + 2 * x + 1]),
                                    pack_bf16x2(acc[j][i][4 * q + 4 + 2 * x], acc[j][i][4 * q + 5 + 2 * x]),
                                    o[x], o[2 + x]);
-                        if (ok)
+                        if (row < t.row_end)
                             *reinterpret_cast<uint4 *>(c + n + 8 * (q + half)) =
                                 make_uint4(o[0], o[1], o[2], o[3]);
                     }

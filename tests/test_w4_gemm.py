@@ -39,7 +39,7 @@ def test_gemm_refusals():
             setattr(g, n, v)
         return lib.moe_w4_gemm(ctypes.byref(g), None)
 
-    for kw in (dict(n_groups=0), dict(n_groups=257), dict(rows=-1), dict(rows=1 << 31), dict(N=48), dict(N=0),
+    for kw in (dict(n_groups=0), dict(n_groups=257), dict(rows=-1), dict(rows=1 << 31), dict(rows=(1 << 31) - 255), dict(N=48), dict(N=0),
                dict(N=16384 + 32), dict(K=64), dict(K=160), dict(K=16384 + 128), dict(epilogue=1, N=96, c_scale=F)):
         assert status(**kw) == 2, kw
     assert status(epilogue=2) == 3 and status(epilogue=7) == 3
