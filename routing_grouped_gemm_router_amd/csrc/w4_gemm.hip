@@ -69,15 +69,23 @@ void w4_gemm_tiles(moe_w4_gemm_desc g) {
     constexpr int NW = WM * WN, WTM = BM / WM, WTN = BN / WN, TM = WTM / 32, TN = WTN / 32;
     static_assert(!SWIGLU || TN % 2 == 0, "gate and up of a unit in one wave");
     static_assert(NW * 64 >= 256, "the tile table's scan");
-    constexpr int IPA = BM * 8 / 64 / NW, IPB = BN * 4 / 64 / NW;     // 16-byte copies a lane
-    static_assert(IPA * 64 * NW == BM * 8 && IPB * 64 * NW == BN * 4, "whole copies");
+    // Weights in whole 128-byte lines, of two steps, where LDS has room for two such
+    // (the L1 takes a whole line's time for the 64 bytes of one step; K = N = 2048,
+    // small tiles: 128 experts of 32 rows 57.6 -> 54.5 us, medium ones: 2 experts of 512
+    // rows, K = N = 8192, 65.9 -> 62.9; 8 experts of 32 rows 10.6 -> 10.9)
+    constexpr bool LINES = BATCHED && BN <= 128;
+    constexpr int BP = LINES ? 8 : 4;                                 // 16-byte pieces of a weight row
+    constexpr int IPA = BM * 8 / 64 / NW, IPB = BN * BP / 64 / NW;    // 16-byte copies a lane
+    static_assert(IPA * 64 * NW == BM * 8 && IPB * 64 * NW == BN * BP, "whole copies");
     constexpr int SROWS = BM + BN, SPW = (SROWS / 64 + NW - 1) / NW;  // scale words
     static_assert(BM % 64 == 0 && BN % 64 == 0, "a wave's scale words are of one operand");
     static_assert(STAGES == 2 || STAGES == 3, "two slots of four steps of scales");
-    constexpr int STAGE = BM * 8 + BN * 4;                            // uint4
+    constexpr int AST = BM * 8, BST = BN * BP, BSTAGES = LINES ? 2 : STAGES;   // uint4
+    constexpr int POOL = STAGES * AST + BSTAGES * BST;
+    static_assert(!LINES || STAGES <= 3, "a line's place is free again when the next but one is copied");
     // the grid has as many workgroups as fit: LDS with the tables' 4.1 KiB
-    static_assert((STAGES * STAGE + 2 * SROWS) * 16 + 4096 <= 163840 / (OCC * 4 / NW), "LDS");
-    __shared__ __attribute__((aligned(1024))) uint4 pool[STAGES * STAGE];
+    static_assert((POOL + 2 * SROWS) * 16 + 4048 <= 163840 / (OCC * 4 / NW), "LDS");
+    __shared__ __attribute__((aligned(1024))) uint4 pool[POOL];
     // scale words: a slot for each stage, 4 bytes a row, or where a row's scales
     // come in whole 16-byte groups two slots of four steps
     __shared__ __attribute__((aligned(1024))) uint4 scales[2 * SROWS];
@@ -132,8 +140,9 @@ void w4_gemm_tiles(moe_w4_gemm_desc g) {
         pb = uniform_ptr(reinterpret_cast<const char *>(g.b) + (int64_t)t.e * N * (K / 2));
 #pragma unroll
         for (int i = 0; i < IPB; i++) {
-            const int p = (wave * IPB + i) * 64 + lane, r = p >> 2;
-            ob[i] = (uint32_t)b_row(t.nt, r) * (uint32_t)(K / 2) + ((p & 3) ^ ((r >> 2) & 3)) * 16;
+            const int p = (wave * IPB + i) * 64 + lane, r = p / BP;
+            ob[i] = (uint32_t)b_row(t.nt, r) * (uint32_t)(K / 2) +
+                    ((p % BP) ^ (LINES ? kl_swz(r) : (r >> 2) & 3)) * 16;
         }
 #pragma unroll
         for (int q = 0; q < SPW; q++) {
@@ -152,7 +161,6 @@ void w4_gemm_tiles(moe_w4_gemm_desc g) {
             ahead = decode(ipos);
             setup(ahead);
         }
-        uint4 *st = pool + buf * STAGE;
         // scales first: a wait for the step's operands then covers them
         if constexpr (!BATCHED) {
 #pragma unroll
@@ -166,11 +174,13 @@ void w4_gemm_tiles(moe_w4_gemm_desc g) {
                 if ((q * NW + wave) * 64 < SROWS)
                     dma16(ps[q] + ikt * 4, scales + slot * SROWS + (q * NW + wave) * 64);
         }
+        if (!LINES || (P & 1) == 0) {
+            uint4 *bt = pool + STAGES * AST + (LINES ? P >> 1 : buf) * BST;
 #pragma unroll
-        for (int i = 0; i < IPB; i++)
-            dma16s(ob[i], pb + ikt * 64, st + BM * 8 + (wave * IPB + i) * 64);
+            for (int i = 0; i < IPB; i++) dma16s(ob[i], pb + ikt * 64, bt + (wave * IPB + i) * 64);
+        }
 #pragma unroll
-        for (int i = 0; i < IPA; i++) dma16(pa[i] + ikt * 128, st + (wave * IPA + i) * 64);
+        for (int i = 0; i < IPA; i++) dma16(pa[i] + ikt * 128, pool + buf * AST + (wave * IPA + i) * 64);
         issued++;
         ikt++;
         if ((!BATCHED || P == 3) && ikt == nk) {
@@ -189,7 +199,8 @@ void w4_gemm_tiles(moe_w4_gemm_desc g) {
         return i32x8{(int)c0.x, (int)c0.y, (int)c0.z, (int)c0.w, (int)c1.x, (int)c1.y, (int)c1.z, (int)c1.w};
     };
     auto frag_b = [&](const uint4 *st, int r0, int s) {
-        const uint4 c = st[BM * 8 + w4_chunk(r0 + (lane & 31), 2 * s + half)];
+        const int row = r0 + (lane & 31);
+        const uint4 c = st[LINES ? kl_chunk(row, 2 * s + half) : w4_chunk(row, 2 * s + half)];
         return i32x8{(int)c.x, (int)c.y, (int)c.z, (int)c.w, 0, 0, 0, 0};
     };
     // Scale bytes of this lane's rows: for slice s of a step the byte half + 2 s of
@@ -216,10 +227,11 @@ void w4_gemm_tiles(moe_w4_gemm_desc g) {
     auto compute = [&](int buf, auto step_of_four) {
         constexpr int Q = decltype(step_of_four)::value;
         constexpr int W = BATCHED ? Q >> 1 : 0, S0 = BATCHED ? 2 * (Q & 1) : 0, S1 = BATCHED ? S0 + 1 : 2;
-        const uint4 *st = pool + buf * STAGE;
+        const uint4 *st = pool + buf * AST, *bt = pool + STAGES * AST + (LINES ? Q >> 1 : buf) * BST;
+        constexpr int B0 = LINES ? 2 * (Q & 1) : 0;      // the step's first slice in bt
         i32x8 fa[2][TM], fb[TN];
 #pragma unroll
-        for (int j = 0; j < TN; j++) fb[j] = frag_b(st, wn * WTN + j * 32, 0);
+        for (int j = 0; j < TN; j++) fb[j] = frag_b(bt, wn * WTN + j * 32, B0);
 #pragma unroll
         for (int i = 0; i < TM; i++) fa[0][i] = frag_a(st, wm * WTM + i * 32, 0);
         // the reads of slice 1 between the products of slice 0; a weight fragment
@@ -234,7 +246,7 @@ void w4_gemm_tiles(moe_w4_gemm_desc g) {
                 __builtin_amdgcn_sched_barrier(0);
                 if (j * TM + i < TM) fa[1][j * TM + i] = frag_a(st, wm * WTM + (j * TM + i) * 32, 1);
             }
-            fb[j] = frag_b(st, wn * WTN + j * 32, 1);
+            fb[j] = frag_b(bt, wn * WTN + j * 32, B0 + 1);
         }
 #pragma unroll
         for (int j = 0; j < TN; j++)
@@ -342,12 +354,14 @@ void w4_gemm_tiles(moe_w4_gemm_desc g) {
             // this wave's copies of the step have landed: at most those of the
             // STAGES - 2 steps behind it may be in flight (loads return in order;
             // a store or a scale copy among them makes the wait longer, not shorter)
-            if (issued - step >= STAGES - 1) wait_vmem<(STAGES - 2) * (IPA + IPB)>();
+            constexpr int Q = decltype(q)::value;
+            constexpr int BEHIND = !LINES ? (STAGES - 2) * (IPA + IPB) : STAGES == 2 ? 0 : IPA + (Q & 1) * IPB;
+            if (issued - step >= STAGES - 1) wait_vmem<BEHIND>();
             else wait_vmem<0>();
             lds_sync();                  // everybody's, and the stage before has been read
             issue(buf == 0 ? STAGES - 1 : buf - 1,
-                  std::integral_constant<int, (decltype(q)::value + STAGES - 1) & 3>{});
-            if constexpr (decltype(q)::value == 0) {
+                  std::integral_constant<int, (Q + STAGES - 1) & 3>{});
+            if constexpr (Q == 0) {
                 if constexpr (BATCHED) batch ^= 1;
                 if (mine) read_scales(BATCHED ? batch : buf);
             }
@@ -388,14 +402,14 @@ static void w4_gemm_run(const moe_w4_gemm_desc &g, hipStream_t s) {
 // workgroups of every compute unit, small ones (64 x 128, in three stages) where
 // the weights' stream is what counts or few have a tile at all. us, up (K = N =
 // 2048) unless said otherwise, small / medium / large:
-//   E = 128: r = 32 56 / 67 / 69, r = 48 64 / 71 / 72, r = 64 80 / 74 / 75, r = 128 124 / 113 /
-//     106, r = 512 371 / 297 / 271
-//   E = 32: r = 40 17.4 / 19.2 / 25, r = 64 (256 large tiles) 23.5 / 20.5 / 26, r = 256 (640)
-//     53 / 47 / 46
-//   E = 8: r = 32 (64) 10.7 / 12.8 / 19.6, r = 175 (120) 13.9 / 14.4 / 21, r = 256 (160) 20.3 /
-//     18.7 / 22, r = 512 (288) 29 / 28 / 30, r = 1024 (544) 46 / 43 / 46, r = 1280 (672) 59 / 52 / 49
-//   E = 2, K = N = 8192: r = 128 (96) 29 / 44 / 61, r = 256 (160) 45 / 45 / 62, r = 512
-//     (288) 84 / 68 / 72, r = 1300 (672) 207 / 180 / 152
+//   E = 128: r = 32 53 / 68 / 69, r = 48 61 / 70 / 71, r = 64 76 / 73 / 74, r = 128 120 / 113 /
+//     105, r = 512 354 / 294 / 275
+//   E = 32: r = 40 16.6 / 19.4 / 25, r = 64 (256 large tiles) 23 / 20 / 26, r = 256 (640)
+//     50 / 46.5 / 46.7
+//   E = 8: r = 32 (64) 10.9 / 13.2 / 19.5, r = 175 (120) 14.2 / 14.8 / 21, r = 256 (160) 19.4 /
+//     18.6 / 22, r = 512 (288) 28 / 28 / 30, r = 1024 (544) 44 / 41 / 45, r = 1280 (672) 54 / 50 / 47
+//   E = 2, K = N = 8192: r = 128 (96) 29 / 44 / 61, r = 256 (160) 41 / 45 / 62, r = 512
+//     (288) 79 / 64 / 71, r = 1300 (672) 194 / 173 / 151
 template <bool SWIGLU>
 static void w4_gemm_pick(const moe_w4_gemm_desc &g, hipStream_t s) {
     const int64_t groups = g.rows < g.n_groups ? g.rows : g.n_groups;
