@@ -739,10 +739,12 @@ moe_status moe_w4_quantize(const void *in, moe_dtype in_dt, int64_t rows, int64_
  * With many rows an expert moe_w4_experts8 (below) and the MXFP8 grouped GEMMs
  * are the faster ways, for some more roundings. us for everything after the
  * routing, from x in bf16: here / moe_w4_experts8 / MXFP8, by rows an expert:
- *   E = 128, k = 4, d = 2048, h = 1024: 8 rows 124 / 100 / 200, 32 rows 202 / 112 /
- *     214, 128 rows 552 / 189 / 287, 512 rows 1990 / 521 / 760
- *   E = 8, k = 2, d = 2048, h = 1024: 64 rows 42 / 28 / 50, 256 rows 97 / 40 / 55
- *   E = 2, k = 2, d = 8192, h = 4096: 64 rows 79 / 54 / 132, 512 rows 395 / 119 / 396
+ *   E = 128, k = 4, d = 2048, h = 1024: 4 rows 94 / 96 / 196, 8 rows 123 / 97 / 197,
+ *     32 rows 194 / 108 / 208, 128 rows 555 / 187 / 289, 512 rows 2018 / 498 / 732
+ *   E = 8, k = 2, d = 2048, h = 1024: 16 rows 21 / 26 / 49, 32 rows 31 / 27 / 50, 256
+ *     rows 80 / 39 / 54
+ *   E = 2, k = 2, d = 8192, h = 4096: 16 rows 39 / 50 / 128, 32 rows 68 / 51 / 129, 512
+ *     rows 386 / 109 / 396
  * topk_gate,
  * token_pos, sorted_token and offsets are moe_route's for the T tokens
  * (token_pos < 0: that slot adds nothing). w1q [E, 2h, d/2], w1_scale [E, 2h,
