@@ -1105,23 +1105,23 @@ def _grad_list(grads, out=None):
     dts = list(map(_t_dtype, grads))
     codes = list(map(_GRAD_DT.get, dts))
     if gpu < 0 or None in codes or not all(map(_t_contiguous, grads)) or \
-            any(map(gpu.__ne__, map(_t_gpu, grads))):
+            list(map(_t_gpu, grads)) != [gpu] * n:
         for i, t in enumerate(grads):
             if gpu < 0 or codes[i] is None or t.get_device() != gpu or not t.is_contiguous():
                 _grad_bad("grads", t, i, gpu, "f32 or bf16 tensor")
-    sizes = array.array("q", map(_t_numel, grads))
+    sizes = list(map(_t_numel, grads))
     v = array.array("q", bytes(32 * n))
-    v[0::4] = array.array("q", map(_t_ptr, grads))
-    v[2::4] = sizes
+    v[0::4] = array.array("q", list(map(_t_ptr, grads)))
+    v[2::4] = array.array("q", sizes)
     v[3::4] = array.array("q", codes)
     if out is not None:
-        if list(map(_t_dtype, out)) != dts or array.array("q", map(_t_numel, out)) != sizes or \
-                not all(map(_t_contiguous, out)) or any(map(gpu.__ne__, map(_t_gpu, out))):
+        if list(map(_t_dtype, out)) != dts or list(map(_t_numel, out)) != sizes or \
+                not all(map(_t_contiguous, out)) or list(map(_t_gpu, out)) != [gpu] * n:
             for i, (t, g) in enumerate(zip(out, grads)):
                 if t.dtype is not g.dtype or t.numel() != g.numel() or t.get_device() != gpu or \
                         not t.is_contiguous():
                     _grad_bad("out", t, i, gpu, f"{g.dtype} tensor of {g.numel()} elements")
-        v[1::4] = array.array("q", map(_t_ptr, out))
+        v[1::4] = array.array("q", list(map(_t_ptr, out)))
     return v, v.buffer_info()[0], n, gpu, grads[0]
 
 
