@@ -25,12 +25,12 @@
 // second product multiplies; y once, to bf16 in front of the combine, as in the
 // grouped GEMMs.
 //
-// 65536 rows, up and down: E = 128, d = 2048, h = 1024 272 and 179 us (2.0 and
-// 1.54 PFLOP/s); E = 8, d = 4096, h = 2048 917 and 537 us (2.4 and 2.05). Products
-// and their LDS reads alone, in a loop, reach 3.2 PFLOP/s on random data, where
-// the chip's power holds the clock at 1.9 GHz. What is on top of that: the copies,
-// whose 64-byte weight rows cost the L1 a whole line each (alone 194 us of E =
-// 128's up), and the outputs' stores, which come all at once (63 us of its down).
+// 65536 rows, up and down: E = 128, d = 2048, h = 1024 270 and 174 us (2.0 and
+// 1.58 PFLOP/s); E = 8, d = 4096, h = 2048 900 and 510 us (2.45 and 2.15). Of E =
+// 128's up the copies and outputs alone take 228 us (64-byte weight rows cost the L1
+// a whole line each), products, LDS reads and outputs alone 207 (on random data the
+// chip's power holds the clock at 1.9 GHz); of its down the copies and outputs 187,
+// without the outputs 130: a tile's outputs come all at once.
 #include <type_traits>
 
 #include "common.h"
@@ -311,23 +311,36 @@ void w4_gemm_tiles(moe_w4_gemm_desc g) {
         } else {
 #pragma unroll
             for (int i = 0; i < TM; i++) {
-                const int row = t.row0 + wm * WTM + i * 32 + (lane & 31);
-                uint16_t *c = reinterpret_cast<uint16_t *>(g.c) + (int64_t)row * N;
+                const int row = t.row0 + wm * WTM + i * 32 + (lane & 15);
+                uint16_t *c = reinterpret_cast<uint16_t *>(g.c) + (int64_t)row * N + 8 * half + (lane & 16);
 #pragma unroll
                 for (int j = 0; j < TN; j++) {
                     const int n = t.nt * BN + wn * WTN + j * 32;
-                    if (n >= N) continue;
+                    if (n >= N) continue;                         // wave-uniform
+                    const f32x16 &f = acc[j][i];
+                    uint32_t o[2][4];
 #pragma unroll
-                    for (int q = 0; q < 4; q += 2) {
-                        uint32_t o[4];
+                    for (int q = 0; q < 2; q++)
 #pragma unroll
                         for (int x = 0; x < 2; x++)
-                            swap32(pack_bf16x2(acc[j][i][4 * q + 2 * x], acc[j][i][4 * q + 2 * x + 1]),
-                                   pack_bf16x2(acc[j][i][4 * q + 4 + 2 * x], acc[j][i][4 * q + 5 + 2 * x]),
-                                   o[x], o[2 + x]);
-                        if (row < t.row_end)
-                            *reinterpret_cast<uint4 *>(c + n + 8 * (q + half)) =
-                                make_uint4(o[0], o[1], o[2], o[3]);
+                            swap32(pack_bf16x2(f[8 * q + 2 * x], f[8 * q + 2 * x + 1]),
+                                   pack_bf16x2(f[8 * q + 4 + 2 * x], f[8 * q + 5 + 2 * x]), o[q][x],
+                                   o[q][2 + x]);
+                    // then columns 8 half + 16 (lane / 16 % 2) of rows 0-15 and of rows
+                    // 16-31: 64 bytes of a row an instruction, not 32 (1 to 2 %). Past
+                    // the last-level cache the large outputs left 13 % sooner, and a
+                    // combine behind them took 4 % of both longer.
+#pragma unroll
+                    for (int x = 0; x < 4; x++) {
+                        const auto r = __builtin_amdgcn_permlane16_swap(o[0][x], o[1][x], false, false);
+                        o[0][x] = r[0];
+                        o[1][x] = r[1];
+                    }
+#pragma unroll
+                    for (int q = 0; q < 2; q++) {
+                        if (row + 16 * q >= t.row_end) continue;
+                        *reinterpret_cast<uint4 *>(c + q * 16 * N + n) =
+                            make_uint4(o[q][0], o[q][1], o[q][2], o[q][3]);
                     }
                 }
             }
