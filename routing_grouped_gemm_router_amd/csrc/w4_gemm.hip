@@ -22,8 +22,9 @@
 // LDS once, into two registers a row from which the instruction picks its byte (up,
 // K = N = 2048, 8 experts of 256 rows 19.6 -> 17.9 us against a read a step, 65536 rows
 // of 128 experts 280 -> 272). H' is rounded once, from fp32 to the MXFP8 that the
-// second product multiplies; y once, to bf16 in front of the combine, as in the
-// grouped GEMMs.
+// second product multiplies; the prompt's y once, to fp16 of a block's own scale
+// (kOutHalf): rounded to bf16 it would cost the output as much as out's own rounding
+// (2.5e-3 from 64 bits in the 2-norm and not 1.7e-3), for 1 % of the time.
 //
 // 65536 rows, up and down: E = 128, d = 2048, h = 1024 270 and 174 us (2.0 and
 // 1.58 PFLOP/s); E = 8, d = 4096, h = 2048 900 and 510 us (2.45 and 2.15). Of E =
@@ -33,16 +34,13 @@
 // without the outputs 130: a tile's outputs come all at once.
 #include <type_traits>
 
+#include "act8.h"
 #include "common.h"
 #include "copy_plan.h"
 #include "gemm_device.h"
 #include "mx_encode.h"
 
 namespace moe {
-
-moe_status combine_launch(const void *y, moe_dtype dt, const float *gate,
-                          const int32_t *token_pos, int64_t T, int d, int k, void *out,
-                          bool unit_gate, hipStream_t s);
 
 // Rows of 64 bytes in LDS: four lie in one sweep of the 64 banks, so the
 // 16-byte pieces are swizzled by (row / 4) % 4, which puts the 16 rows that a
@@ -56,16 +54,25 @@ MOE_DEV int w4_chunk(int row, int c) { return row * 4 + (c ^ ((row >> 2) & 3)); 
 // tiles: 213 us where none is cut, 85 with 16.
 constexpr int kUnits = 16;
 
+typedef _Float16 f16x2 __attribute__((ext_vector_type(2)));
+MOE_DEV uint32_t pack_f16x2(float a, float b) { return __builtin_bit_cast(uint32_t, f16x2{(_Float16)a, (_Float16)b}); }
+
 struct W4GemmTile {
     int e, row0, row_end, nt;
 };
 
-// BM rows x BN weight rows a tile, WM x WN waves. SWIGLU: the weight rows of a
-// wave are gate rows, then the up rows of the same hidden units; c is E4M3 H'
-// [rows, N / 2] with c_scale. Otherwise c is bf16 [rows, N].
-template <bool SWIGLU, bool BATCHED, int BM, int BN, int WM, int WN, int STAGES, int OCC>
+// What a tile's sums become. kOutHidden: the weight rows of a wave are gate rows,
+// then the up rows of the same hidden units; c is E4M3 H' [rows, N / 2] with c_scale.
+// kOutBf16: c is bf16 [rows, N]. kOutHalf: c is fp16 [rows, N], per 32 columns times
+// 2^(c_scale - 127): 11 significant bits or more of what counts in a block, in the
+// bytes of bf16 and one more in 64.
+enum { kOutBf16, kOutHidden, kOutHalf };
+
+// BM rows x BN weight rows a tile, WM x WN waves.
+template <int OUT, bool BATCHED, int BM, int BN, int WM, int WN, int STAGES, int OCC>
 __global__ __launch_bounds__(WM *WN * 64) __attribute__((amdgpu_waves_per_eu(OCC, OCC)))
 void w4_gemm_tiles(moe_w4_gemm_desc g) {
+    constexpr bool SWIGLU = OUT == kOutHidden;
     constexpr int NW = WM * WN, WTM = BM / WM, WTN = BN / WN, TM = WTM / 32, TN = WTN / 32;
     static_assert(!SWIGLU || TN % 2 == 0, "gate and up of a unit in one wave");
     static_assert(NW * 64 >= 256, "the tile table's scan");
@@ -313,19 +320,33 @@ void w4_gemm_tiles(moe_w4_gemm_desc g) {
             for (int i = 0; i < TM; i++) {
                 const int row = t.row0 + wm * WTM + i * 32 + (lane & 15);
                 uint16_t *c = reinterpret_cast<uint16_t *>(g.c) + (int64_t)row * N + 8 * half + (lane & 16);
+                uint32_t exps = 0;                                // of the TN blocks (kOutHalf)
 #pragma unroll
                 for (int j = 0; j < TN; j++) {
                     const int n = t.nt * BN + wn * WTN + j * 32;
                     if (n >= N) continue;                         // wave-uniform
                     const f32x16 &f = acc[j][i];
+                    float mult = 1.f;
+                    if constexpr (OUT == kOutHalf) {
+                        float am = 0.f;
+#pragma unroll
+                        for (int v = 0; v < 16; v++) am = fmaxf(am, fabsf(f[v]));
+                        // the largest to 2^14 .. 2^15
+                        const int sb = max((int)(__float_as_uint(max_xor32(am)) >> 23) - 14, 0);
+                        mult = __uint_as_float((uint32_t)(254 - sb) << 23);
+                        exps |= (uint32_t)sb << (8 * j);
+                    }
+                    auto pack = [&](float a, float b) {
+                        if constexpr (OUT == kOutHalf) return pack_f16x2(a * mult, b * mult);
+                        else return pack_bf16x2(a, b);
+                    };
                     uint32_t o[2][4];
 #pragma unroll
                     for (int q = 0; q < 2; q++)
 #pragma unroll
                         for (int x = 0; x < 2; x++)
-                            swap32(pack_bf16x2(f[8 * q + 2 * x], f[8 * q + 2 * x + 1]),
-                                   pack_bf16x2(f[8 * q + 4 + 2 * x], f[8 * q + 5 + 2 * x]), o[q][x],
-                                   o[q][2 + x]);
+                            swap32(pack(f[8 * q + 2 * x], f[8 * q + 2 * x + 1]),
+                                   pack(f[8 * q + 4 + 2 * x], f[8 * q + 5 + 2 * x]), o[q][x], o[q][2 + x]);
                     // then columns 8 half + 16 (lane / 16 % 2) of rows 0-15 and of rows
                     // 16-31: 64 bytes of a row an instruction, not 32 (1 to 2 %). Past
                     // the last-level cache the large outputs left 13 % sooner, and a
@@ -342,6 +363,14 @@ void w4_gemm_tiles(moe_w4_gemm_desc g) {
                         *reinterpret_cast<uint4 *>(c + q * 16 * N + n) =
                             make_uint4(o[q][0], o[q][1], o[q][2], o[q][3]);
                     }
+                }
+                if constexpr (OUT == kOutHalf) {
+                    // N is a multiple of 128 here: all of the blocks or none
+                    const int r = t.row0 + wm * WTM + i * 32 + (lane & 31), n = t.nt * BN + wn * WTN;
+                    typedef typename std::conditional<TN == 4, uint32_t, uint16_t>::type Exps;
+                    static_assert(TN == 4 || TN == 2, "a store of whole words");
+                    if (half == 0 && r < t.row_end && n < N)
+                        *reinterpret_cast<Exps *>(g.c_scale + (int64_t)r * (N / 32) + n / 32) = (Exps)exps;
                 }
             }
         }
@@ -399,14 +428,14 @@ void w4_gemm_tiles(moe_w4_gemm_desc g) {
 // ---------------------------------------------------------------------------
 // launchers
 
-template <bool SWIGLU, int BM, int BN, int WM, int WN, int STAGES, int OCC>
+template <int OUT, int BM, int BN, int WM, int WN, int STAGES, int OCC>
 static void w4_gemm_run(const moe_w4_gemm_desc &g, hipStream_t s) {
     constexpr int per_cu = OCC * 4 / (WM * WN);
     const int grid = (num_cus() * per_cu + 7) / 8 * 8;
     if (g.K % 512 == 0)
-        w4_gemm_tiles<SWIGLU, true, BM, BN, WM, WN, STAGES, OCC><<<grid, WM * WN * 64, 0, s>>>(g);
+        w4_gemm_tiles<OUT, true, BM, BN, WM, WN, STAGES, OCC><<<grid, WM * WN * 64, 0, s>>>(g);
     else
-        w4_gemm_tiles<SWIGLU, false, BM, BN, WM, WN, STAGES, OCC><<<grid, WM * WN * 64, 0, s>>>(g);
+        w4_gemm_tiles<OUT, false, BM, BN, WM, WN, STAGES, OCC><<<grid, WM * WN * 64, 0, s>>>(g);
 }
 
 // The tile by the rows of a group (r, on average over the groups that can have
@@ -423,33 +452,93 @@ static void w4_gemm_run(const moe_w4_gemm_desc &g, hipStream_t s) {
 //     18.6 / 22, r = 512 (288) 28 / 28 / 30, r = 1024 (544) 44 / 41 / 45, r = 1280 (672) 54 / 50 / 47
 //   E = 2, K = N = 8192: r = 128 (96) 29 / 44 / 61, r = 256 (160) 41 / 45 / 62, r = 512
 //     (288) 79 / 64 / 71, r = 1300 (672) 194 / 173 / 151
-template <bool SWIGLU>
+template <int OUT>
 static void w4_gemm_pick(const moe_w4_gemm_desc &g, hipStream_t s) {
     const int64_t groups = g.rows < g.n_groups ? g.rows : g.n_groups;
     const int64_t half = g.rows / 64 + groups, m = half > 2 * groups ? half : 2 * groups;
     const int64_t tiles = m * ((g.N + 255) / 256) / 2;
-    if (g.rows <= 48 * groups || tiles <= 128) w4_gemm_run<SWIGLU, 64, 128, 2, 2, 3, 2>(g, s);
-    else if (tiles <= 512) w4_gemm_run<SWIGLU, 128, 128, 2, 2, 2, 2>(g, s);
-    else w4_gemm_run<SWIGLU, 128, 256, 2, 2, 2, 2>(g, s);
+    if (g.rows <= 48 * groups || tiles <= 128) w4_gemm_run<OUT, 64, 128, 2, 2, 3, 2>(g, s);
+    else if (tiles <= 512) w4_gemm_run<OUT, 128, 128, 2, 2, 2, 2>(g, s);
+    else w4_gemm_run<OUT, 128, 256, 2, 2, 2, 2>(g, s);
 }
 
+// MOE_EPI_NONE with a c_scale: kOutHalf
 moe_status w4_gemm_launch(const moe_w4_gemm_desc &g, hipStream_t s) {
-    if (g.epilogue == MOE_EPI_SWIGLU_FWD) w4_gemm_pick<true>(g, s);
-    else w4_gemm_pick<false>(g, s);
+    if (g.epilogue == MOE_EPI_SWIGLU_FWD) w4_gemm_pick<kOutHidden>(g, s);
+    else if (g.c_scale) w4_gemm_pick<kOutHalf>(g, s);
+    else w4_gemm_pick<kOutBf16>(g, s);
     return launch_status();
+}
+
+// out[t] = sum_j g[t, j] y[token_pos[t, j]], y as kOutHalf leaves it, sums in fp32:
+// a token a wave, all loads of kUnrollY column chunks in flight before the first
+// sum. A lane reads one block's exponent of those chunks and hands it to the four
+// that need it. Bound by memory (16384 tokens of 4 rows of
+// 2048: 343 MB in 54 us, 6.4 TB/s).
+constexpr int kUnrollY = 4;
+template <int KMAX>
+__global__ __launch_bounds__(256) void w4_combine_half(const uint4 *__restrict__ y, const uint8_t *__restrict__ scale,
+                                                       const float *__restrict__ gate,
+                                                       const int32_t *__restrict__ token_pos, int64_t T, int nv,
+                                                       int k, uint4 *__restrict__ out) {
+    const int lane = threadIdx.x & 63;
+    const int64_t t = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6);
+    if (t >= T) return;
+    int32_t pos[KMAX];
+    float g[KMAX];
+#pragma unroll
+    for (int j = 0; j < KMAX; j++) {
+        pos[j] = j < k ? token_pos[t * k + j] : -1;
+        g[j] = j < k ? gate[t * k + j] : 0.f;
+    }
+    for (int base = 0; base < nv; base += 64 * kUnrollY) {
+        uint4 v[kUnrollY][KMAX];
+        int e[KMAX];
+#pragma unroll
+        for (int j = 0; j < KMAX; j++) {
+            e[j] = 0;
+            if (pos[j] < 0) continue;
+            const int64_t row = (int64_t)pos[j] * nv;
+            if (lane < 16 * kUnrollY && base + 4 * lane < nv) e[j] = scale[(row + base) / 4 + lane];
+#pragma unroll
+            for (int u = 0; u < kUnrollY; u++)
+                if (base + 64 * u + lane < nv) v[u][j] = load_once(y + row + base + 64 * u + lane);
+        }
+#pragma unroll
+        for (int u = 0; u < kUnrollY; u++) {
+            float acc[8] = {};
+#pragma unroll
+            for (int j = 0; j < KMAX; j++) {
+                const int ex = __shfl(e[j], 16 * u + lane / 4) - 127;
+                if (pos[j] < 0) continue;
+                const uint32_t w[4] = {v[u][j].x, v[u][j].y, v[u][j].z, v[u][j].w};
+#pragma unroll
+                for (int i = 0; i < 4; i++) {
+                    const f16x2 f = __builtin_bit_cast(f16x2, w[i]);
+                    acc[2 * i] = fmaf(g[j], ldexpf((float)f.x, ex), acc[2 * i]);
+                    acc[2 * i + 1] = fmaf(g[j], ldexpf((float)f.y, ex), acc[2 * i + 1]);
+                }
+            }
+            const int c = base + 64 * u + lane;
+            if (c < nv)
+                out[t * nv + c] = make_uint4(pack_bf16x2(acc[0], acc[1]), pack_bf16x2(acc[2], acc[3]),
+                                             pack_bf16x2(acc[4], acc[5]), pack_bf16x2(acc[6], acc[7]));
+        }
+    }
 }
 
 static size_t round256(size_t b) { return (b + 255) & ~(size_t)255; }
 
-// H' in MXFP8 [R, h], its scales, y bf16 [R, d]
+// H' in MXFP8 [R, h], its scales, y fp16 [R, d], its scales
 size_t w4_experts8_ws_bytes(int64_t R, int d, int h) {
-    return round256((size_t)R * h) + round256((size_t)R * (h / 32)) + round256((size_t)R * d * 2);
+    return round256((size_t)R * h) + round256((size_t)R * (h / 32)) + round256((size_t)R * d * 2) +
+           round256((size_t)R * (d / 32));
 }
 
 moe_status w4_experts8_launch(const moe_w4_desc &w, const uint8_t *x_scale, hipStream_t s) {
     const int64_t R = w.T * w.k;
     uint8_t *hq = (uint8_t *)w.ws, *hs = hq + round256((size_t)R * w.h);
-    uint8_t *y = hs + round256((size_t)R * (w.h / 32));
+    uint8_t *y = hs + round256((size_t)R * (w.h / 32)), *ys = y + round256((size_t)R * w.d * 2);
     moe_w4_gemm_desc g = {};
     g.n_groups = w.E;
     g.rows = R;
@@ -465,9 +554,19 @@ moe_status w4_experts8_launch(const moe_w4_desc &w, const uint8_t *x_scale, hipS
     g.N = w.d; g.K = w.h;
     g.a = hq; g.a_scale = hs; g.a_rows = nullptr;
     g.b = w.w2q; g.b_scale = w.w2_scale;
-    g.c = y; g.c_scale = nullptr;
+    g.c = y; g.c_scale = ys;
     if ((st = w4_gemm_launch(g, s)) != MOE_OK) return st;
-    return combine_launch(y, MOE_BF16, w.topk_gate, w.token_pos, w.T, w.d, w.k, w.out, false, s);
+    const unsigned nb = (unsigned)((w.T + 3) / 4);
+    const int nv = w.d / 8;
+    auto combine = [&](auto kmax) {
+        w4_combine_half<decltype(kmax)::value><<<nb, 256, 0, s>>>(
+            (const uint4 *)y, ys, w.topk_gate, w.token_pos, w.T, nv, w.k, (uint4 *)w.out);
+    };
+    if (w.k <= 1) combine(std::integral_constant<int, 1>{});
+    else if (w.k <= 2) combine(std::integral_constant<int, 2>{});
+    else if (w.k <= 4) combine(std::integral_constant<int, 4>{});
+    else combine(std::integral_constant<int, 8>{});
+    return launch_status();
 }
 
 }  // namespace moe

@@ -279,23 +279,30 @@ def _layer(T, d, h, E, k, seed):
 
 @gpu
 @pytest.mark.parametrize("T,d,h,E,k", [(1, 128, 128, 2, 1), (5, 256, 128, 256, 8), (150, 512, 256, 5, 2),
-                                       (1030, 384, 640, 8, 3), (600, 2048, 1024, 16, 4)])
+                                       (1030, 384, 640, 8, 3), (600, 2048, 1024, 16, 4), (40, 2432, 128, 4, 2),
+                                       (9, 16384, 128, 2, 2)])
 def test_experts8(T, d, h, E, k):
-    """The calls that it is made of, bit for bit; the whole against 64 bits.
+    """The calls that it is made of, to their roundings; the whole against 64 bits.
 
     Its tolerance by arithmetic: with X = 2^(floor(log2 amax) - 8), a block's
     scale, an element of H' is off by at most 2^-4 of itself or 2^-10 X, X <=
     2^-8 amax; one above 448 X is taken to 448 X, by less than 64 X, an eighth of
     itself. The down product carries the sum of these magnitudes, 2^-3 |H'| +
     2^-18 amax, into an output. The products' own errors are 1e-3 of their
-    largest result (see above), a and b's through H' by silu' <= 1.1; then y
-    and out are rounded to bf16, 2^-8 each."""
+    largest result (see above), a and b's through H' by silu' <= 1.1; then y is
+    rounded to fp16 with its block's largest between 2^14 and 2^15, 2^-11 of the
+    value or half of a smallest step, 2^-25 in 2^14 of the largest, and out to
+    bf16, 2^-8."""
     (xq, xs), v, w1, w2, w, r = _layer(T, d, h, E, k, 63)
     got = moe.moe_w4_experts8(xq, xs, r, *w)
     hq, hs = moe.moe_w4_gemm(xq, xs, w[0], w[1], r["offsets"], moe.MOE_EPI_SWIGLU_FWD, r["sorted_token"])
     y = moe.moe_w4_gemm(hq, hs, w[2], w[3], r["offsets"])
-    assert torch.equal(got, moe.moe_combine(y, r["topk_gate"], r["token_pos"]))
     idx, gate = to_np(r["topk_idx"]), to_np(r["topk_gate"])
+    # the sum of y in bf16 (2^-8 of each term and of the result), fp32's own errors
+    # beside it nothing
+    parts = np.abs(to_np(y)[to_np(r["token_pos"])].astype(np.float64)) * gate[:, :, None]
+    whole = to_np(moe.moe_combine(y, r["topk_gate"], r["token_pos"])).astype(np.float64)
+    assert (np.abs(to_np(got) - whole) <= (2.0 ** -8 + 2.0 ** -10) * parts.sum(1) + 2.0 ** -7 * np.abs(whole)).all()
     ref, tol = np.zeros((T, d)), np.zeros((T, d))
     for e in range(E):
         t, j = np.nonzero(idx == e)
@@ -308,10 +315,44 @@ def test_experts8(T, d, h, E, k):
             amax = np.repeat(np.abs(hid).reshape(len(t), -1, 32).max(2), 32, axis=1)
             eh = eh * (1 + 2.0 ** -3) + 2.0 ** -3 * np.abs(hid) + 2.0 ** -18 * amax
             out, ey = hid @ w2[2][e].T, eh @ np.abs(w2[2][e]).T
-            ey = ey + 1e-3 * np.abs(out).max() + 2.0 ** -8 * (np.abs(out) + ey)
+            ey = ey + 1e-3 * np.abs(out).max()
+            most = np.repeat((np.abs(out) + ey).reshape(len(t), -1, 32).max(2), 32, axis=1)
+            ey = ey + 2.0 ** -11 * (np.abs(out) + ey) + 2.0 ** -39 * most
             ref[t] += gate[t, j][:, None] * out
             tol[t] += gate[t, j][:, None] * ey
     assert (np.abs(to_np(got) - ref) <= tol + 2.0 ** -8 * (np.abs(ref) + tol)).all()
+
+
+@gpu
+def test_experts8_of_many_magnitudes():
+    """Outputs of one token from 2^-70 to 2^70, next to each other and block by
+    block: each as near as its own magnitude lets fp16 of the block's scale be. H' =
+    silu(a) b is a whole block of the same value, which E4M3 holds, so that y's is
+    the only rounding but out's."""
+    T, d, h, E = 70, 512, 128, 3
+    one = lambda *s: torch.full(s, 127, dtype=U8, device="cuda")
+    xq = torch.full((T, d), 0x38, dtype=U8, device="cuda")              # ones
+    w1 = torch.zeros(E, 2 * h, d // 2, dtype=U8, device="cuda")
+    w1[:, :h, 0] = 0x07                                                 # a = 6
+    w1[:, h:, 0] = 0x02                                                 # b = 1
+    rng = np.random.default_rng(5)
+    c = rng.integers(0, 16, (E, d, h)).astype(np.uint8)
+    base = np.repeat(rng.integers(60, 190, (E, d // 32)), 32, axis=1)
+    s2 = np.repeat((base + rng.integers(-8, 9, (E, d)))[:, :, None], h // 32, axis=2).astype(np.uint8)
+    w2, s2c = _cuda(w4.pack(c.reshape(E * d, h)).reshape(E, d, h // 2), s2)
+    r = moe.moe_route(dev(synth.normal((T, E), 70, 0, 1.0), torch.float32), 1)
+    got = to_np(moe.moe_w4_experts8(xq, one(T, d // 32), r, w1, one(E, 2 * h, d // 32), w2, s2c)).astype(np.float64)
+    hq, hs = moe.moe_w4_gemm(xq, one(T, d // 32), w1, one(E, 2 * h, d // 32), r["offsets"], moe.MOE_EPI_SWIGLU_FWD,
+                             r["sorted_token"])
+    hid = float(oracle.mxfp8_dequantize_rowwise(to_np(hq), to_np(hs))[0, 0])
+    y = hid * w4.decode(c.reshape(E * d, h), s2.reshape(E * d, h // 32)).reshape(E, d, h).sum(2)
+    ref = y[to_np(r["topk_idx"])[:, 0]]
+    top = hid * np.abs(w4.decode(c.reshape(E * d, h), s2.reshape(E * d, h // 32))).reshape(E, d, h).sum(2)
+    err = 1e-4 * top                                                    # the matrix units' sums
+    most = np.repeat((np.abs(y) + err).reshape(E, -1, 32).max(2), 32, axis=1)
+    tol = (err + 2.0 ** -11 * (np.abs(y) + err) + 2.0 ** -39 * most)[to_np(r["topk_idx"])[:, 0]]
+    assert np.isfinite(got).all() and np.abs(ref).max() > 2.0 ** 50 and np.abs(ref[ref != 0]).min() < 2.0 ** -50
+    assert (np.abs(got - ref) <= tol + 2.0 ** -8 * (np.abs(ref) + tol)).all()
 
 
 @gpu
