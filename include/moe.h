@@ -686,9 +686,11 @@ moe_status moe_rms_norm_backward(const void *dy, moe_dtype dt, const void *x, co
  * mixed) at any multiple of the element's size; may be null where n = 0. out
  * null: in place. A tensor in place is not written where the factor is one.
  * norm: device fp32, one element. Squares and sums are fp64 in an order that
- * depends on the sizes alone; the factor is rounded once to fp32, the product
- * once to dtype. An infinite norm gives the factor 0 (and NaNs where the
- * infinities are), a NaN a NaN factor: check norm to skip such a step.
+ * depends on the sizes alone; the factor comes from that sum (in moe_grad_clip
+ * from the fp32 norm as it is given) and is rounded once, to fp32, the product to
+ * fp32 and from there to dtype. An infinite norm, and so one beyond fp32's range,
+ * gives the factor 0 (and NaNs where the infinities are), a NaN a NaN factor:
+ * check norm to skip such a step.
  *
  * moe_grad_norm: norm alone (out is ignored).
  * moe_clip_grad_norm: norm and out.

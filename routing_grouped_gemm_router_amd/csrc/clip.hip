@@ -154,21 +154,27 @@ __global__ __launch_bounds__(256) void grad_squares(GradArgs a, double *__restri
     if (threadIdx.x == 0) part[blockIdx.x] = s;
 }
 
-// the partial sums' root, by one workgroup's threads
-MOE_DEV double norm_of(const double *__restrict__ part, int np) {
+// the partial sums' sum, by one workgroup's threads
+MOE_DEV double sum_of(const double *part, int np) {
     double s = 0.;
     for (int i = threadIdx.x; i < np; i += 256) s += part[i];
-    return sqrt(block_sum(s));
+    return block_sum(s);
 }
 
-// the norm from up to 2048 partial sums of each launch: 5 us, a chain of latencies
-__global__ __launch_bounds__(256) void grad_finish(const double *__restrict__ part, int np,
-                                                   float *__restrict__ norm) {
-    const double v = norm_of(part, np);
-    if (threadIdx.x == 0) *norm = (float)v;
+// the norm from up to 2048 partial sums of each launch: 5 us, a chain of latencies.
+// Their sum takes the place of the first of them, for a clipping behind it.
+__global__ __launch_bounds__(256) void grad_finish(double *part, int np, float *__restrict__ norm) {
+    const double s = sum_of(part, np);
+    if (threadIdx.x == 0) {
+        *norm = (float)sqrt(s);
+        part[0] = s;
+    }
 }
 
+// A norm beyond fp32's range is infinite here as it is to the caller: a clipping
+// by the norm that was returned has the same factor, 0.
 MOE_DEV float clip_scale(double norm, float max_norm) {
+    if (__builtin_isinf((float)norm)) return 0.f;
     const double q = (double)max_norm / (norm + 1e-6);
     return q >= 1. ? 1.f : (float)q;             // a NaN stays one
 }
@@ -208,15 +214,16 @@ MOE_DEV void chunk_scale(const GradItem &t, int64_t e0, int n, float scale) {
 
 // out = in * scale; the scale from the partial sums (part; workgroup 0 then
 // leaves the norm) or from *norm. A scale of one leaves tensors that are
-// written in place as they are. The product is rounded once, to the output's
-// type. Every workgroup adds the partial sums itself, from the last-level cache,
-// in the same order: a launch for them alone costs 5 us and another gap.
+// written in place as they are. The product is rounded to fp32 and from there to
+// the output's type (bf16: at most 2^-24 of the value beyond half a step). Every
+// workgroup adds the partial sums itself, from the last-level cache, in the same
+// order: a launch for them alone costs 5 us and another gap.
 __global__ __launch_bounds__(256) void grad_scale(GradArgs a, const double *__restrict__ part,
                                                   int np, float *__restrict__ norm,
                                                   float max_norm) {
     double v;
     if (part) {
-        v = norm_of(part, np);
+        v = sqrt(sum_of(part, np));
         if (blockIdx.x == 0 && threadIdx.x == 0) *norm = (float)v;
     } else {
         v = *norm;
@@ -340,7 +347,7 @@ moe_status grad_norm_launch(const moe_grad *g, int n, float *norm, void *ws, hip
         return launch_status();
     }
     const int np = grad_squares_launch(g, n, (double *)ws, s);
-    grad_finish<<<1, 256, 0, s>>>((const double *)ws, np, norm);
+    grad_finish<<<1, 256, 0, s>>>((double *)ws, np, norm);
     return launch_status();
 }
 
@@ -356,8 +363,11 @@ moe_status grad_clip_launch(const moe_grad *g, int n, float max_norm, float *nor
     if (ws) {
         np = grad_squares_launch(g, n, (double *)ws, s);
         // few partial sums: every workgroup adds them itself
-        if (np > 0 && np <= kGradBlocks) part = (const double *)ws;
-        else grad_finish<<<1, 256, 0, s>>>((const double *)ws, np, norm);
+        if (np > kGradBlocks) {
+            grad_finish<<<1, 256, 0, s>>>((double *)ws, np, norm);
+            np = 1;
+        }
+        part = (const double *)ws;
     }
     for (int i = 0; i < n;) {
         i = grad_args(g, n, i, a);

@@ -284,3 +284,52 @@ def test_refusals():
     two = moe.moe_grad_norm([g, g])                       # read only: counts twice
     want = math.sqrt(2) * _norm64([g])
     assert abs(float(two) - want) <= 2 * U * want
+
+
+# One launch; few partial sums; more partial sums than workgroups (a launch of 64
+# such tensors has 2368 chunks).
+LENGTHS = {"short": [900, 65], "one tensor": [70000], "few sums": [8192 * 5 + 1] * 70, "many sums": [300000] * 130}
+
+
+@pytest.mark.parametrize("sizes", LENGTHS.values(), ids=LENGTHS)
+def test_the_factor_is_rounded_once(sizes):
+    """Whole numbers, whose squares' sum fp64 holds: the factor is the 64-bit
+    norm's, rounded to fp32, whatever the list's length (max_norm is one for which
+    the norm's own rounding would show), and an fp32 product's one rounding gives
+    every bit. moe_grad_clip takes the norm as fp32 holds it."""
+    g, _ = _tensors(sizes, [F32] * len(sizes), 31, 1)
+    for t in g:
+        t.mul_(50).round_()
+    norm = math.sqrt(sum(int((t.double() ** 2).sum()) for t in g))
+    rounded = float(np.float32(norm))
+    factor = lambda n, m: np.float32(float(np.float32(m)) / (n + 1e-6))
+    max_norm = next(m / 64 for m in range(1, 512) if factor(norm, m / 64) != factor(rounded, m / 64))
+    want = [to_np(t) * factor(norm, max_norm) for t in g]
+    given = [to_np(t) * factor(rounded, max_norm) for t in g]
+    o = [torch.empty_like(t) for t in g]
+    n = moe.moe_clip_grad_norm(g, max_norm, out=o)
+    assert float(n) == rounded
+    assert all(np.array_equal(to_np(a), b) for a, b in zip(o, want))
+    moe.moe_grad_clip(g, n, max_norm, out=o)
+    assert all(np.array_equal(to_np(a), b) for a, b in zip(o, given))
+    moe.moe_clip_grad_norm(g, max_norm)
+    assert all(np.array_equal(to_np(a), b) for a, b in zip(g, want))
+
+
+@pytest.mark.parametrize("max_norm", [0.0, 1.0, 3e38, math.inf])
+@pytest.mark.parametrize("sizes", LENGTHS.values(), ids=LENGTHS)
+def test_a_norm_past_fp32(sizes, max_norm):
+    """Finite gradients with a norm beyond fp32's range: the norm is infinite and
+    the factor 0, in lists of every length, in place and not, and by that norm."""
+    g = [torch.full((s,), 3e38, device="cuda") for s in sizes]
+    for t in g:
+        t[::2] *= -1
+    o = [torch.ones_like(t) for t in g]
+    n = moe.moe_clip_grad_norm(g, max_norm, out=o)
+    assert float(n) == math.inf and float(moe.moe_grad_norm(g)) == math.inf
+    assert all((t == 0).all() for t in o)
+    p = [torch.ones_like(t) for t in g]
+    moe.moe_grad_clip(g, n, max_norm, out=p)
+    assert all((t == 0).all() for t in p)
+    moe.moe_clip_grad_norm(g, max_norm)
+    assert all((t == 0).all() for t in g)
