@@ -1090,8 +1090,10 @@ def _grad_bad(name, t, i, gpu, want):
 
 def _grad_list(grads, out=None):
     """The C descriptors (moe_grad: data, out, n, dtype) of a list of
-    tensors, their address and number, and the tensors' GPU. Checked by whole
-    lists: a model's list is long, and a call's host time is its length's."""
+    tensors, their address and number, the tensors' GPU, and the lists of the
+    tensors, which the caller holds until its kernels are enqueued (an iterator's
+    tensors are in no other place). Checked by whole lists: a model's list is
+    long, and a call's host time is its length's."""
     if not isinstance(grads, (list, tuple)):
         grads = list(grads)
     if out is not None and not isinstance(out, (list, tuple)):
@@ -1122,7 +1124,7 @@ def _grad_list(grads, out=None):
                         not t.is_contiguous():
                     _grad_bad("out", t, i, gpu, f"{g.dtype} tensor of {g.numel()} elements")
         v[1::4] = array.array("q", list(map(_t_ptr, out)))
-    return v, v.buffer_info()[0], n, gpu, grads[0]
+    return v, v.buffer_info()[0], n, gpu, (grads, out)
 
 
 def _grad_norm_args(n, like, gpu, norm, ws):
@@ -1142,8 +1144,8 @@ def moe_grad_norm(grads, norm: torch.Tensor | None = None,
                   ws: torch.Tensor | None = None) -> torch.Tensor:
     """The norm of all elements of a list of f32 and bf16 tensors (see moe.h):
     one f32 element on their GPU."""
-    v, at, n, gpu, like = _grad_list(grads)
-    norm, ws = _grad_norm_args(n, like, gpu, norm, ws)
+    v, at, n, gpu, held = _grad_list(grads)
+    norm, ws = _grad_norm_args(n, held[0][0], gpu, norm, ws)
     _enqueue("moe_grad_norm", _lib.moe_grad_norm, gpu, at, n, norm.data_ptr(), ws.data_ptr(),
              ws.numel())
     return norm
@@ -1154,8 +1156,8 @@ def moe_clip_grad_norm(grads, max_norm: float, out=None, norm: torch.Tensor | No
     """moe_grad_norm, and every tensor times min(1, max_norm / (norm + 1e-6)),
     in place or into the tensors of `out` (of the same types and numbers of
     elements). Returns the norm in front of it."""
-    v, at, n, gpu, like = _grad_list(grads, out)
-    norm, ws = _grad_norm_args(n, like, gpu, norm, ws)
+    v, at, n, gpu, held = _grad_list(grads, out)
+    norm, ws = _grad_norm_args(n, held[0][0], gpu, norm, ws)
     _enqueue("moe_clip_grad_norm", _lib.moe_clip_grad_norm, gpu, at, n, max_norm, norm.data_ptr(),
              ws.data_ptr(), ws.numel())
     return norm
@@ -1164,7 +1166,7 @@ def moe_clip_grad_norm(grads, max_norm: float, out=None, norm: torch.Tensor | No
 def moe_grad_clip(grads, norm: torch.Tensor, max_norm: float, out=None):
     """The clipping alone, with a norm that is given (one f32 element on the
     tensors' GPU)."""
-    v, at, n, gpu, _ = _grad_list(grads, out)
+    v, at, n, gpu, held = _grad_list(grads, out)
     if norm is None or norm.dtype is not torch.float32 or norm.numel() != 1 or \
             norm.get_device() != gpu:
         raise ValueError(f"norm: expected one f32 element on cuda:{gpu}")

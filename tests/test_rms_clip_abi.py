@@ -3,6 +3,7 @@ gradients' norm and clipping (no GPU needed): each bad argument gives the
 documented status before anything is enqueued, and the binding raises on
 tensors that do not fit."""
 import ctypes
+import weakref
 
 import pytest
 import torch
@@ -131,3 +132,32 @@ def test_binding_refuses():
         moe.moe_clip_grad_norm([x], 1.0, out=[x, x])
     with pytest.raises(ValueError, match="GPU"):
         moe.mxfp8_dequantize(x.to(torch.uint8), torch.zeros(4, 2, dtype=torch.uint8))
+
+
+@pytest.mark.parametrize("call", ["norm", "clip", "clip into others", "by a norm"])
+def test_tensors_live_until_the_call(monkeypatch, call):
+    """Tensors that only an iterator hands out are still there when the kernels
+    are enqueued: their memory must not have gone to the workspace before."""
+    class OnGpu(torch.Tensor):
+        def get_device(self):
+            return 0
+
+    refs, alive = [], []
+
+    def tensors():
+        for _ in range(5):
+            t = torch.ones(64).as_subclass(OnGpu)
+            refs.append(weakref.ref(t))
+            yield t
+
+    monkeypatch.setattr(moe, "_t_gpu", lambda t: 0)
+    monkeypatch.setattr(moe, "_enqueue", lambda *a: alive.extend(r() is not None for r in refs))
+    if call == "norm":
+        moe.moe_grad_norm(tensors())
+    elif call == "clip":
+        moe.moe_clip_grad_norm(tensors(), 1.0)
+    elif call == "clip into others":
+        moe.moe_clip_grad_norm(tensors(), 1.0, out=tensors())
+    else:
+        moe.moe_grad_clip(tensors(), torch.ones(()).as_subclass(OnGpu), 1.0, out=tensors())
+    assert alive and all(alive)
