@@ -494,3 +494,77 @@ def test_no_rows_and_refusals():
     r = moe.moe_route(torch.zeros(3, E, device="cuda"), 2)
     with pytest.raises(ValueError, match="ws"):
         moe.moe_w4_experts8(z(3, d), z(3, 4), r, *w, ws=z(16))
+
+
+# T, d, h, E, k of experts whose down product takes each tile with scales of one step
+# (h no multiple of 512) and of four; on the larger tiles also a d that leaves some
+# of the last tile's columns past its end.
+FORMS = [(1000, 640, 128, 32, 1), (1000, 512, 512, 32, 1), (3, 4224, 1024, 2, 1),            # small
+         (600, 8064, 640, 2, 1), (600, 8192, 512, 2, 1),                                     # medium
+         (1400, 16384, 128, 2, 1), (1400, 16256, 640, 2, 1), (1400, 16384, 512, 2, 1),       # large
+         (1400, 16256, 1024, 2, 1)]
+
+
+@gpu
+@pytest.mark.parametrize("T,d,h,E,k", FORMS)
+def test_experts8_exact_on_every_tile(T, d, h, E, k):
+    """H' known and held by E4M3, y a whole number of half-units that fp32's sums and
+    fp16 of a block's scale hold: out is y rounded once.
+
+    Gate inputs are 6, whose silu, 5.985, goes to 6 under any power of two; the up
+    inputs b = x[t, c] u[j] are 0 or up to 4 in magnitude, so H' = 6 b. y / 6 = sum_j
+    b_j w2[n, j] is a whole number of halves, at most 341 (asserted): y has 11 bits."""
+    rng = np.random.default_rng(d + h)
+    xv = np.zeros((T, d))
+    xv[:, 0] = 1
+    xv[:, 1:5] = rng.integers(-2, 3, (T, 4))
+    u, col = rng.integers(-2, 3, (E, h)), rng.integers(1, 5, (E, h))
+    w1 = np.zeros((E, 2 * h, d), np.int8)
+    w1[np.arange(E)[:, None], h + np.arange(h), col] = u
+    code = np.array([4 | 8, 2 | 8, 0, 2, 4], np.uint8)[w1 + 2]        # -2 .. 2 in E2M1
+    code[:, :h, 0] = 7                                                # 6
+    c, sc = _whole((E, d, h), rng, min(1.0, 16 / h))
+    w2 = _val(c, sc)
+    part = np.stack([np.where(col == i, u, 0) for i in range(1, 5)], 1).astype(np.float64)     # [E, 4, h]
+    v = np.stack([w2[e] @ part[e].T for e in range(E)])               # [E, d, 4]
+    r = moe.moe_route(dev(rng.normal(size=(T, E)), torch.float32), k)
+    idx = to_np(r["topk_idx"])[:, 0]
+    ref = np.zeros((T, d))
+    for e in range(E):
+        ref[idx == e] = xv[idx == e, 1:5] @ v[e].T
+    assert np.abs(ref).max() <= 341 and np.array_equal(2 * ref, np.rint(2 * ref)) and (to_np(r["topk_gate"]) == 1).all()
+    one = lambda *s: torch.full(s, 127, dtype=U8, device="cuda")
+    xq, w1q, w2q, w2s = _cuda(_e4m3(xv), w4.pack(code.reshape(E * 2 * h, d)).reshape(E, 2 * h, d // 2), _e2m1(c), sc)
+    got = moe.moe_w4_experts8(xq, one(T, d // 32), r, w1q, one(E, 2 * h, d // 32), w2q, w2s)
+    assert torch.equal(got.cpu(), torch.from_numpy(6 * ref).to(torch.bfloat16))
+
+
+def _random_experts(T, d, h, E, k, seed):
+    g = torch.Generator(device="cuda")
+    g.manual_seed(seed)
+    n = lambda *s: torch.randn(s, generator=g, device="cuda")
+    w = [t.view(E, -1, t.shape[-1]) for rows, cols in ((2 * h, d), (d, h))
+         for t in moe.moe_w4_quantize(n(E * rows, cols) * cols ** -0.5)]
+    return moe.mxfp8_quantize(n(T, d), 1), w, n(T, E)
+
+
+@gpu
+@pytest.mark.parametrize("T,d,h,E,k", [(T // 2 if E == 2 and T > 3 else T, d, h, E, 2) for T, d, h, E, _ in FORMS] +
+                         [(100, 4224, 128, 16, 8), (90, 2176, 512, 16, 5), (33, 7168, 256, 8, 7)])
+def test_experts8_tokens_by_themselves(T, d, h, E, k):
+    """A token's result does not depend on the others, whatever tile their number
+    leads to, nor on the call: the first 40 by themselves give the same bits."""
+    (xq, xs), w, logits = _random_experts(T, d, h, E, k, T + d)
+    full = moe.moe_w4_experts8(xq, xs, moe.moe_route(logits, k), *w)
+    assert torch.equal(full, moe.moe_w4_experts8(xq, xs, moe.moe_route(logits, k), *w))
+    n = min(T, 40)
+    few = moe.moe_w4_experts8(xq[:n], xs[:n], moe.moe_route(logits[:n].contiguous(), k), *w)
+    assert torch.isfinite(full).all() and full.abs().max() > 0.5
+    assert torch.equal(full[:n], few)
+
+
+@gpu
+@pytest.mark.parametrize("T,d,h,E,k", [(100, 4224, 128, 16, 8), (33, 2176, 256, 8, 6)])
+def test_experts8_of_many_slots(T, d, h, E, k):
+    """Five to eight slots a token with rows of more than one piece of the combine."""
+    test_experts8(T, d, h, E, k)
