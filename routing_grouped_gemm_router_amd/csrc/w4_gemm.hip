@@ -556,11 +556,14 @@ moe_status w4_experts8_launch(const moe_w4_desc &w, const uint8_t *x_scale, hipS
     g.b = w.w2q; g.b_scale = w.w2_scale;
     g.c = y; g.c_scale = ys;
     if ((st = w4_gemm_launch(g, s)) != MOE_OK) return st;
-    const unsigned nb = (unsigned)((w.T + 3) / 4);
     const int nv = w.d / 8;
     auto combine = [&](auto kmax) {
-        w4_combine_half<decltype(kmax)::value><<<nb, 256, 0, s>>>(
-            (const uint4 *)y, ys, w.topk_gate, w.token_pos, w.T, nv, w.k, (uint4 *)w.out);
+        for (int64_t t = 0; t < w.T; t += 4 * kMaxBlocks) {
+            const int64_t n = w.T - t < 4 * kMaxBlocks ? w.T - t : 4 * kMaxBlocks;
+            w4_combine_half<decltype(kmax)::value><<<(unsigned)((n + 3) / 4), 256, 0, s>>>(
+                (const uint4 *)y, ys, w.topk_gate + t * w.k, w.token_pos + t * w.k, n, nv, w.k,
+                (uint4 *)w.out + t * nv);
+        }
     };
     if (w.k <= 1) combine(std::integral_constant<int, 1>{});
     else if (w.k <= 2) combine(std::integral_constant<int, 2>{});

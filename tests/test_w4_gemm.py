@@ -568,3 +568,24 @@ def test_experts8_tokens_by_themselves(T, d, h, E, k):
 def test_experts8_of_many_slots(T, d, h, E, k):
     """Five to eight slots a token with rows of more than one piece of the combine."""
     test_experts8(T, d, h, E, k)
+
+
+@gpu
+def test_experts8_of_many_tokens():
+    """2^26 tokens and more, of which one launch of the combine takes 2^23: every
+    1024 of them the same, and the same as 1024 by themselves."""
+    T, n, d, h = (1 << 26) + 1024 + 5, 1024, 128, 128
+    (xq, xs), w, _ = _random_experts(n, d, h, 1, 1, 9)
+    g = torch.Generator(device="cuda")
+    g.manual_seed(3)
+    gate = torch.rand((n, 1), generator=g, device="cuda")
+    over = lambda t: t.repeat((T + n - 1) // n, 1)[:T]
+    pos = torch.arange(T, dtype=I32, device="cuda")
+    route = lambda m, gt: dict(topk_gate=gt, token_pos=pos[:m, None], sorted_token=pos[:m],
+                               offsets=torch.tensor([0, m], dtype=I32, device="cuda"))
+    want = moe.moe_w4_experts8(xq, xs, route(n, gate), *w)
+    out = torch.full((T + 1, d), 7.0, dtype=torch.bfloat16, device="cuda")
+    moe.moe_w4_experts8(over(xq), over(xs), route(T, over(gate)), *w, out=out[:T])
+    assert (out[T] == 7).all() and torch.equal(out[T // n * n:T], want[:T % n])
+    for part in out[:T // n * n].view(-1, n, d).split(4096):
+        assert (part == want).all()
