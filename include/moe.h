@@ -820,8 +820,8 @@ moe_status moe_w4_gemm(const moe_w4_gemm_desc *g, void *stream);
  * E4M3 bytes [T, d], x_scale [T, d/32]) and H' is rounded to MXFP8 along h
  * between the two products (moe_w4_gemm, with its alignments), the experts'
  * outputs in front of the combine to 11 bits, times a power of two for each 32
- * of them. d and h: multiples of 128; the rest as in moe_w4_experts, but for ws:
- * moe_w4_experts8_workspace_size bytes. */
+ * of them. d and h: multiples of 128; T k at most 2^31 - 256; the rest as in
+ * moe_w4_experts, but for ws: moe_w4_experts8_workspace_size bytes. */
 size_t moe_w4_experts8_workspace_size(int64_t T, int32_t k, int32_t d, int32_t h);
 moe_status moe_w4_experts8(const moe_w4_desc *w, const uint8_t *x_scale, void *stream);
 

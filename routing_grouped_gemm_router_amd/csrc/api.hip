@@ -857,12 +857,14 @@ static bool w4_scale_aligned(const uint8_t *p, int32_t K) {
     return K % 512 ? aligned4(p) : aligned16(p);
 }
 
+// rows of w4_gemm's products: a tile's rows past the last group stay within 32 bits
+constexpr int64_t kW4GemmRows = ((int64_t)1 << 31) - 256;
+
 moe_status moe_w4_gemm(const moe_w4_gemm_desc *g, void *stream) {
     if (!g) return MOE_ERR_NULL;
     const bool swiglu = g->epilogue == MOE_EPI_SWIGLU_FWD;
     if (!swiglu && g->epilogue != MOE_EPI_NONE) return MOE_ERR_DTYPE;
-    // (a tile's rows past the last group stay within 32 bits)
-    if (g->n_groups < 1 || g->n_groups > 256 || g->rows < 0 || g->rows > ((int64_t)1 << 31) - 256 ||
+    if (g->n_groups < 1 || g->n_groups > 256 || g->rows < 0 || g->rows > kW4GemmRows ||
         !width_ok(g->N) || !width_ok(g->K) || g->K % 128 || (swiglu && g->N % 64))
         return MOE_ERR_SHAPE;
     if (g->rows == 0) return MOE_OK;
@@ -877,7 +879,7 @@ moe_status moe_w4_gemm(const moe_w4_gemm_desc *g, void *stream) {
 }
 
 static bool w4_wide_ok(int64_t T, int32_t k, int32_t d, int32_t h) {
-    return w4_shape_ok(T, k, d, h) && d % 128 == 0 && h % 128 == 0;
+    return w4_shape_ok(T, k, d, h) && d % 128 == 0 && h % 128 == 0 && T * k <= kW4GemmRows;
 }
 
 size_t moe_w4_experts8_workspace_size(int64_t T, int32_t k, int32_t d, int32_t h) {

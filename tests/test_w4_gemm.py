@@ -589,3 +589,18 @@ def test_experts8_of_many_tokens():
     assert (out[T] == 7).all() and torch.equal(out[T // n * n:T], want[:T % n])
     for part in out[:T // n * n].view(-1, n, d).split(4096):
         assert (part == want).all()
+
+
+def test_experts8_rows_past_the_products():
+    """The products' rows end at 2^31 - 256; so do the experts' T k."""
+    w = moe.W4Desc()
+    for n, v in dict(d=128, h=128, E=8, ws_bytes=1 << 62).items():
+        setattr(w, n, v)
+    for n in ("x", "topk_gate", "token_pos", "sorted_token", "offsets", "w1q", "w1_scale", "w2q", "w2_scale", "out"):
+        setattr(w, n, F)
+    size = moe.moe_w4_experts8_workspace_size
+    for T, k in (((1 << 31) - 255, 1), ((1 << 30) - 127, 2), ((1 << 28) - 31, 8)):
+        w.T, w.k, w.ws = T, k, F
+        assert lib.moe_w4_experts8(ctypes.byref(w), F, None) == 2 and size(T, k, 128, 128) == 0
+        w.T, w.ws = T - 1, None                       # the last one of a size: the next check's turn
+        assert lib.moe_w4_experts8(ctypes.byref(w), F, None) == 1 and size(T - 1, k, 128, 128) > 0
