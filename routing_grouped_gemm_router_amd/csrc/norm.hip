@@ -557,11 +557,21 @@ size_t norm_bwd_ws_bytes(moe_dtype dt, int64_t T, int d) {
 size_t rms_bwd_ws_bytes(moe_dtype dt, int64_t T, int d) { return norm_bwd_ws_bytes(dt, T, d) / 2; }
 
 // Bytes of a matrix from which the RMS backward reads its rows past the
-// last-level cache (256 MiB), where a part of them would only push out the
-// rest: bf16 with a stream gradient, 32768 x 4096 204 -> 177 us, 65536 x 1024 103
-// -> 87, 16384 x 2048 behind its forward 130 -> 123; but where all of it is there
-// already, 16384 x 2048 45 -> 49 and 1003 x 4128 fp32 14.2 -> 15.0.
-constexpr int64_t kOnceBytes = 64 << 20;
+// last-level cache (256 MiB), where a part of them would only push out the rest.
+// us, through the cache -> past it, bf16 d = 2048 with a stream gradient: directly
+// behind its forward; behind work that leaves dy and dsum in the cache and x not,
+// as a training step's does; called again on the same rows:
+//   32 MiB  27.8 -> 30.5   32.1 -> 30.4   28.0 -> 30.8
+//   40      34.5 -> 34.2   36.1 -> 35.6   32.9 -> 35.8
+//   64      51.4 -> 50.3   49.6 -> 50.1   46.9 -> 52.2
+//   72      64.8 -> 53.4   54.9 -> 54.4   54.5 -> 55.4
+//   128    115.5 -> 92.1  116.8 -> 91.9  100.1 -> 90.7
+// The first two at 32 and 40 MiB: without dsum 24.0 -> 27.2, 28.7 -> 26.3 and 30.0 ->
+// 30.5, 33.0 -> 30.1; from a checkpoint 27.5 -> 28.8, 33.1 -> 31.2 and 34.6 -> 33.4,
+// 39.3 -> 36.2; fp32 d = 4096 26.3 -> 28.9, 28.9 -> 28.6 and 39.2 -> 39.3, 41.8 -> 38.2.
+// With none of the rows in the cache past it is faster at every size (8 MiB 18.3 ->
+// 16.1, 64 MiB 83.5 -> 54.2). The layer norm's backward is without it, as it was.
+constexpr int64_t kOnceBytes = 40 << 20;
 
 template <bool BF16, bool RMS>
 static moe_status norm_bwd_run(const void *dy, const void *x, const uint8_t *x8,
