@@ -442,23 +442,29 @@ static void w4_gemm_run(const moe_w4_gemm_desc &g, hipStream_t s) {
 // any) and the number of large tiles: large ones (128 rows x 256) move the fewest
 // bytes a product, medium ones (128 x 128) where the large would not fill the two
 // workgroups of every compute unit, small ones (64 x 128, in three stages) where
-// the weights' stream is what counts or few have a tile at all. us, up (K = N =
-// 2048) unless said otherwise, small / medium / large:
-//   E = 128: r = 32 53 / 68 / 69, r = 48 61 / 70 / 71, r = 64 76 / 73 / 74, r = 128 120 / 113 /
-//     105, r = 512 354 / 294 / 275
-//   E = 32: r = 40 16.6 / 19.4 / 25, r = 64 (256 large tiles) 23 / 20 / 26, r = 256 (640)
-//     50 / 46.5 / 46.7
-//   E = 8: r = 32 (64) 10.9 / 13.2 / 19.5, r = 175 (120) 14.2 / 14.8 / 21, r = 256 (160) 19.4 /
-//     18.6 / 22, r = 512 (288) 28 / 28 / 30, r = 1024 (544) 44 / 41 / 45, r = 1280 (672) 54 / 50 / 47
-//   E = 2, K = N = 8192: r = 128 (96) 29 / 44 / 61, r = 256 (160) 41 / 45 / 62, r = 512
-//     (288) 79 / 64 / 71, r = 1300 (672) 194 / 173 / 151
+// the weights' stream is what counts or few have a tile at all. us, up (gathered rows
+// of a random routing, K = N = 2048 unless said otherwise), small / medium / large (in
+// brackets the large tiles):
+//   E = 128: r = 32 52 / 67 / 69, r = 48 58 / 67 / 69, r = 64 (1024) 74 / 72 / 73, r = 128 115 /
+//     112 / 102, r = 512 353 / 302 / 270
+//   E = 64: r = 48 27 / 33 / 37, r = 64 (512) 36 / 34 / 38, r = 96 (640) 42 / 37.5 / 41
+//   E = 32: r = 40 16 / 19 / 25, r = 64 (256) 23 / 20 / 25, r = 192 (512) 41 / 35.0 / 34.7, r =
+//     256 (640) 49.5 / 46.0 / 45.6, r = 288 (704) 51 / 46.7 / 45.7
+//   E = 16: r = 512 (576) 45 / 40.5 / 45, r = 576 (640) 50 / 42 / 46, r = 704 (768) 70 / 50 / 48
+//   E = 8: r = 32 (64) 10.9 / 13.2 / 19.4, r = 175 (116) 13.9 / 14.5 / 20.6, r = 256 (160) 18.6 /
+//     17.8 / 20.8, r = 512 (288) 27 / 27 / 30, r = 960 (512) 43 / 36.5 / 35.4, r = 1024 (544)
+//     44 / 41 / 45, r = 1216 (640) 60 / 43.5 / 47, r = 1280 (672) 53 / 50 / 47
+//   E = 2, K = N = 8192: r = 128 (96) 35 / 43 / 61, r = 256 (160) 55 / 50 / 61, r = 512
+//     (288) 87 / 89 / 89, r = 1100 (576) 159 / 144 / 149, r = 1300 (672) 188 / 173 / 152
+// The large tiles pay from where they fill the compute units' places a second time
+// by some: up to 640 of them the medium ones take 3 % more to 10 % less.
 template <int OUT>
 static void w4_gemm_pick(const moe_w4_gemm_desc &g, hipStream_t s) {
     const int64_t groups = g.rows < g.n_groups ? g.rows : g.n_groups;
     const int64_t half = g.rows / 64 + groups, m = half > 2 * groups ? half : 2 * groups;
     const int64_t tiles = m * ((g.N + 255) / 256) / 2;
     if (g.rows <= 48 * groups || tiles <= 128) w4_gemm_run<OUT, 64, 128, 2, 2, 3, 2>(g, s);
-    else if (tiles <= 512) w4_gemm_run<OUT, 128, 128, 2, 2, 2, 2>(g, s);
+    else if (tiles <= 640) w4_gemm_run<OUT, 128, 128, 2, 2, 2, 2>(g, s);
     else w4_gemm_run<OUT, 128, 256, 2, 2, 2, 2>(g, s);
 }
 
