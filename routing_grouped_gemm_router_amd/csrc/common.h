@@ -73,6 +73,10 @@ MOE_DEV float max_xor32(float v) {
     return fmaxf(__uint_as_float(r[0]), __uint_as_float(r[1]));
 }
 
+// A grid has fewer than 2^32 threads (more wrap, without an error): at most 2^21 workgroups (of up
+// to 1024) a launch, larger inputs in pieces.
+constexpr int64_t kMaxBlocks = 1 << 21;
+
 inline int cdiv(int64_t a, int64_t b) { return (int)((a + b - 1) / b); }
 
 inline bool aligned16(const void *p) { return ((uintptr_t)p & 15u) == 0; }

@@ -15,6 +15,7 @@
 namespace moe {
 
 constexpr int kRowWaves = 4;
+constexpr int64_t kRowPiece = kMaxBlocks * kRowWaves;   // tokens of a launch
 constexpr int kUnroll = 4;   // combine kernels: 16-byte column chunks per lane in flight together
 
 // Non-temporal 16-byte loads of rows read exactly once (the combine kernels'
@@ -260,14 +261,18 @@ moe_status permute_launch(const void *x, const uint8_t *x_scale, moe_dtype dt, i
     if (T == 0) return MOE_OK;
     const int esize = dt == MOE_F32 ? 4 : dt == MOE_BF16 ? 2 : 1;
     const int n16 = (int)((int64_t)d * esize / 16);
-    const unsigned nb = (unsigned)((T + kRowWaves - 1) / kRowWaves);
+    for (int64_t t = 0; t < T; t += kRowPiece) {
+        const int64_t n = T - t < kRowPiece ? T - t : kRowPiece;
+        const unsigned nb = (unsigned)((n + kRowWaves - 1) / kRowWaves);
+        const uint4 *xx = reinterpret_cast<const uint4 *>(x) + t * n16;
+        const int32_t *pos = token_pos + t * k;
 #define L(K)                                                                                  \
-    (permute_rows16<K><<<nb, 256, 0, s>>>(reinterpret_cast<const uint4 *>(x), T, n16, k,     \
-                                          token_pos, reinterpret_cast<uint4 *>(x_perm)), 0)
-    MOE_KSWITCH(k, L);
+    (permute_rows16<K><<<nb, 256, 0, s>>>(xx, n, n16, k, pos, reinterpret_cast<uint4 *>(x_perm)), 0)
+        MOE_KSWITCH(k, L);
 #undef L
-    if (dt == MOE_MXFP8)
-        permute_rows_bytes<<<nb, 256, 0, s>>>(x_scale, T, d / 32, k, token_pos, x_perm_scale);
+        if (dt == MOE_MXFP8)
+            permute_rows_bytes<<<nb, 256, 0, s>>>(x_scale + t * (d / 32), n, d / 32, k, pos, x_perm_scale);
+    }
     return launch_status();
 }
 
@@ -277,16 +282,21 @@ moe_status combine_launch(const void *y, moe_dtype dt, const float *gate,
     if (T == 0) return MOE_OK;
     const bool bf = dt == MOE_BF16;
     const int n16 = d * (bf ? 2 : 4) / 16;
-    const unsigned nb = (unsigned)((T + kRowWaves - 1) / kRowWaves);
     const uint4 *yy = reinterpret_cast<const uint4 *>(y);
-    uint4 *oo = reinterpret_cast<uint4 *>(out);
+    for (int64_t t = 0; t < T; t += kRowPiece) {
+        const int64_t n = T - t < kRowPiece ? T - t : kRowPiece;
+        const unsigned nb = (unsigned)((n + kRowWaves - 1) / kRowWaves);
+        const float *g = unit_gate ? nullptr : gate + t * k;
+        const int32_t *pos = token_pos + t * k;
+        uint4 *oo = reinterpret_cast<uint4 *>(out) + t * n16;
 #define L(K)                                                                                      \
-    (bf ? (unit_gate ? (combine_rows<true, true, K><<<nb, 256, 0, s>>>(yy, gate, token_pos, T, n16, k, oo), 0) \
-                     : (combine_rows<true, false, K><<<nb, 256, 0, s>>>(yy, gate, token_pos, T, n16, k, oo), 0)) \
-        : (unit_gate ? (combine_rows<false, true, K><<<nb, 256, 0, s>>>(yy, gate, token_pos, T, n16, k, oo), 0) \
-                     : (combine_rows<false, false, K><<<nb, 256, 0, s>>>(yy, gate, token_pos, T, n16, k, oo), 0)))
-    MOE_KSWITCH(k, L);
+    (bf ? (unit_gate ? (combine_rows<true, true, K><<<nb, 256, 0, s>>>(yy, g, pos, n, n16, k, oo), 0) \
+                     : (combine_rows<true, false, K><<<nb, 256, 0, s>>>(yy, g, pos, n, n16, k, oo), 0)) \
+        : (unit_gate ? (combine_rows<false, true, K><<<nb, 256, 0, s>>>(yy, g, pos, n, n16, k, oo), 0) \
+                     : (combine_rows<false, false, K><<<nb, 256, 0, s>>>(yy, g, pos, n, n16, k, oo), 0)))
+        MOE_KSWITCH(k, L);
 #undef L
+    }
     return launch_status();
 }
 
@@ -300,19 +310,25 @@ moe_status combine_bwd_launch(const void *dout, const void *y, moe_dtype dt, con
     const bool bf = dt == MOE_BF16;
     if (row_gate_only && !bf) return MOE_ERR_DTYPE;
     const int n16 = d * (bf ? 2 : 4) / 16;
-    const unsigned nb = (unsigned)((T + kRowWaves - 1) / kRowWaves);
-    const uint4 *dd = reinterpret_cast<const uint4 *>(dout);
     const uint4 *yy = reinterpret_cast<const uint4 *>(y);
     uint4 *oo = reinterpret_cast<uint4 *>(dy);
+    for (int64_t t = 0; t < T; t += kRowPiece) {
+        const int64_t n = T - t < kRowPiece ? T - t : kRowPiece;
+        const unsigned nb = (unsigned)((n + kRowWaves - 1) / kRowWaves);
+        const uint4 *dd = reinterpret_cast<const uint4 *>(dout) + t * n16;
+        const float *g = gate + t * k;
+        const int32_t *idx = topk_idx + t * k, *pos = token_pos + t * k;
+        float *dl = dlogits + t * E, *dg = dgate ? dgate + t * k : nullptr;
 #define L(K)                                                                                        \
-    (row_gate_only ? (combine_bwd_rows<true, K, false><<<nb, 256, 0, s>>>(dd, yy, gate, topk_idx,  \
-                                                        token_pos, T, n16, k, E, oo, dlogits, dgate), 0) \
-    : bf ? (combine_bwd_rows<true, K><<<nb, 256, 0, s>>>(dd, yy, gate, topk_idx, token_pos, T, n16, \
-                                                        k, E, oo, dlogits, dgate), 0)               \
-        : (combine_bwd_rows<false, K><<<nb, 256, 0, s>>>(dd, yy, gate, topk_idx, token_pos, T,   \
-                                                         n16, k, E, oo, dlogits, dgate), 0))
-    MOE_KSWITCH(k, L);
+    (row_gate_only ? (combine_bwd_rows<true, K, false><<<nb, 256, 0, s>>>(dd, yy, g, idx, pos, n,   \
+                                                        n16, k, E, oo, dl, dg), 0)                  \
+    : bf ? (combine_bwd_rows<true, K><<<nb, 256, 0, s>>>(dd, yy, g, idx, pos, n, n16, k, E, oo, dl, \
+                                                        dg), 0)                                     \
+        : (combine_bwd_rows<false, K><<<nb, 256, 0, s>>>(dd, yy, g, idx, pos, n, n16, k, E, oo, dl, \
+                                                         dg), 0))
+        MOE_KSWITCH(k, L);
 #undef L
+    }
     return launch_status();
 }
 

@@ -1,0 +1,57 @@
+"""Sizes past what one launch takes: a grid of 2^32 threads or more wraps without
+an error. Rows repeat a block of 1024, so that the whole output can be checked
+against that block's."""
+import pytest
+import torch
+
+pytestmark = pytest.mark.gpu
+
+if torch.cuda.is_available():
+    import routing_grouped_gemm_router_amd as moe
+
+N = 1024
+T = (1 << 26) + N + 5                       # a wave a token: 2^32 threads and more
+
+
+def _block(shape, seed, dtype):
+    g = torch.Generator(device="cuda")
+    g.manual_seed(seed)
+    if dtype is torch.uint8:
+        return torch.randint(0, 256, shape, generator=g, dtype=dtype, device="cuda")
+    return torch.randn(shape, generator=g, device="cuda").to(dtype)
+
+
+def _over(block):
+    return block.repeat((T + N - 1) // N, 1)[:T]
+
+
+def _same(big, block):
+    """Whether every row of big is its row of the repeated block."""
+    whole = big.shape[0] // N * N
+    ok = torch.equal(big[whole:], block[:big.shape[0] - whole])
+    return ok and all((p == block).all() for p in big[:whole].view(-1, *block.shape).split(4096))
+
+
+def _mirrored():
+    """token_pos of T tokens, each to the mirror of its row."""
+    return torch.arange(T - 1, -1, -1, dtype=torch.int32, device="cuda")[:, None]
+
+
+@pytest.mark.parametrize("mx", [False, True])
+def test_permute(mx):
+    x = _block((N, 32), 1, torch.uint8 if mx else torch.bfloat16)
+    pos = _mirrored()
+    if mx:
+        s = _block((N, 1), 2, torch.uint8)
+        got, gs = moe.moe_permute(_over(x), pos, x_scale=_over(s))
+        assert _same(gs.flip(0), s)
+    else:
+        got = moe.moe_permute(_over(x), pos)
+    assert _same(got.flip(0), x)
+
+
+@pytest.mark.parametrize("dt", [torch.bfloat16, torch.float32])
+def test_combine(dt):
+    y, gate = _block((N, 32), 3, dt), _block((N, 1), 4, torch.float32)
+    out = moe.moe_combine(_over(y).flip(0), _over(gate), _mirrored())
+    assert _same(out, (y.float() * gate).to(dt))
