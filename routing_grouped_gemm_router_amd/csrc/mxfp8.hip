@@ -488,10 +488,16 @@ moe_status mxfp8_quantize_launch(const void *in, moe_dtype in_dt, int64_t rows, 
                                  hipStream_t s) {
     const bool bf = in_dt == MOE_BF16;
     if (axis == 1) {
-        const int64_t n_blocks = rows * cols / 32;
-        const unsigned grid = (unsigned)((n_blocks * 2 + 255) / 256);
-        if (bf) mx_quant_rows<true><<<grid, 256, 0, s>>>(in, n_blocks, cols, row_map, q, scale);
-        else mx_quant_rows<false><<<grid, 256, 0, s>>>(in, n_blocks, cols, row_map, q, scale);
+        const int64_t most = kMaxBlocks * 256 * 16 / cols, piece = most > 0 ? most : 1;   // rows of a launch
+        for (int64_t r = 0; r < rows; r += piece) {
+            const int64_t n = rows - r < piece ? rows - r : piece, n_blocks = n * cols / 32;
+            const unsigned grid = (unsigned)((n_blocks * 2 + 255) / 256);
+            const char *p = (const char *)in + (row_map ? 0 : r * cols * (bf ? 2 : 4));
+            const int32_t *map = row_map ? row_map + r : nullptr;
+            uint8_t *qr = q + r * cols, *sr = scale + r * (cols / 32);
+            if (bf) mx_quant_rows<true><<<grid, 256, 0, s>>>(p, n_blocks, cols, map, qr, sr);
+            else mx_quant_rows<false><<<grid, 256, 0, s>>>(p, n_blocks, cols, map, qr, sr);
+        }
     } else {
         const int ng = group_offsets ? n_groups : 1;
         if (bf)

@@ -55,3 +55,29 @@ def test_combine(dt):
     y, gate = _block((N, 32), 3, dt), _block((N, 1), 4, torch.float32)
     out = moe.moe_combine(_over(y).flip(0), _over(gate), _mirrored())
     assert _same(out, (y.float() * gate).to(dt))
+
+
+@pytest.mark.parametrize("dt", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("cols", [4096, 4096 - 32])
+def test_quantise_rows(dt, cols):
+    """2^36 elements, gathered from the block's rows: two threads a block of 32."""
+    rows = (1 << 36) // cols + N + 5
+    torch.cuda.empty_cache()
+    x = _block((N, cols), 5, dt)
+    q, s = moe.mxfp8_quantize(x, 1)
+    got, gs = moe.mxfp8_quantize(x, 1, row_map=torch.arange(rows, dtype=torch.int32, device="cuda") % N)
+    assert _same(got, q) and _same(gs, s)
+
+
+@pytest.mark.parametrize("dt", [torch.bfloat16, torch.float32])
+def test_quantise_whole_rows(dt):
+    """The rows' own order over several launches: 2^33 elements each."""
+    rows, cols = (1 << 22) + N + 5, 4096
+    torch.cuda.empty_cache()
+    x = _block((N, cols), 7, dt)
+    big = torch.empty(rows, cols, dtype=dt, device="cuda")
+    big[:rows // N * N].view(-1, N, cols).copy_(x.expand(rows // N, N, cols))
+    big[rows // N * N:] = x[:rows % N]
+    got, gs = moe.mxfp8_quantize(big, 1)
+    q, s = moe.mxfp8_quantize(x, 1)
+    assert _same(got, q) and _same(gs, s)
