@@ -300,11 +300,15 @@ moe_status route_launch(const float *logits, int64_t T, int E, int k, int tile_m
                         int32_t *tile_offsets, void *ws, hipStream_t s) {
     const int64_t nchunks = (T + kChunk - 1) / kChunk;
     int32_t *chunk_counts = reinterpret_cast<int32_t *>(ws);
-    if (nchunks > 0) {
-        dim3 g((unsigned)nchunks);
+    for (int64_t c = 0; c < nchunks; c += kMaxBlocks) {
+        const dim3 g((unsigned)(nchunks - c < kMaxBlocks ? nchunks - c : kMaxBlocks));
+        const int64_t t = c * kChunk, n = T - t < kMaxBlocks * kChunk ? T - t : kMaxBlocks * kChunk;
         switch (k) {
-#define MOE_RS(K) \
-    case K: route_select<K><<<g, kChunk * 8, 0, s>>>(logits, T, E, k, topk_idx, topk_gate, token_pos, chunk_counts); break;
+#define MOE_RS(K)                                                                                        \
+    case K:                                                                                              \
+        route_select<K><<<g, kChunk * 8, 0, s>>>(logits + t * E, n, E, k, topk_idx + t * k,              \
+                                                 topk_gate + t * k, token_pos + t * k, chunk_counts + c * E); \
+        break;
             MOE_RS(1) MOE_RS(2) MOE_RS(3) MOE_RS(4) MOE_RS(5) MOE_RS(6) MOE_RS(7) MOE_RS(8)
 #undef MOE_RS
             default: return MOE_ERR_SHAPE;

@@ -81,3 +81,26 @@ def test_quantise_whole_rows(dt):
     got, gs = moe.mxfp8_quantize(big, 1)
     q, s = moe.mxfp8_quantize(x, 1)
     assert _same(got, q) and _same(gs, s)
+
+
+def test_route():
+    """2^29 tokens of two experts, eight threads a token: every token's row is its
+    own, the rows of an expert in the order of their tokens."""
+    M, rep = 1 << 20, (1 << 9) + 1
+    torch.cuda.empty_cache()
+    block = _block((M, 2), 6, torch.float32)
+    tokens = M * rep
+    r = moe.moe_route(block.repeat(rep, 1), 1)
+    idx = (block[:, 1] > block[:, 0]).int()
+    ones = int(idx.sum())
+    assert r["counts"].tolist() == [rep * (M - ones), rep * ones] and r["offsets"].tolist() == [0, rep * (M - ones), tokens]
+    # a token's row: those of its expert in its block before it, and in the blocks before that
+    rank = torch.where(idx == 1, idx.cumsum(0), (1 - idx).cumsum(0)) - 1
+    first = torch.where(idx == 1, rep * (M - ones), 0) + rank
+    step = torch.where(idx == 1, ones, M - ones)
+    for i in (0, 1, 2, rep // 2, rep - 2, rep - 1):
+        at = slice(i * M, (i + 1) * M)
+        pos = r["token_pos"][at, 0]
+        assert torch.equal(pos.long(), first + i * step)
+        assert torch.equal(r["topk_idx"][at, 0], idx) and (r["topk_gate"][at] == 1).all()
+        assert torch.equal(r["sorted_token"][pos.long()], torch.arange(i * M, (i + 1) * M, dtype=torch.int32, device="cuda"))
