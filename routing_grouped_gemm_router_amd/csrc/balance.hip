@@ -48,11 +48,11 @@ template <int EPL>   // experts per lane: ceil(E / 64)
 __global__ __launch_bounds__(256) void lb_partial(const float *__restrict__ logits,
                                                   const int32_t *__restrict__ counts, int64_t T, int E,
                                                   int k, float coef, float *__restrict__ partial,
-                                                  float *__restrict__ dlogits) {
+                                                  float *__restrict__ dlogits, int64_t chunk0) {
     __shared__ float f_s[kLbMaxE];
     __shared__ float acc_s[4][kLbMaxE];
     const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
-    const int64_t chunk = blockIdx.x;
+    const int64_t chunk = chunk0 + blockIdx.x;
     const int64_t t0 = chunk * kLbChunk, t1 = min<int64_t>(T, t0 + kLbChunk);
     const float rows = (float)((double)T * k);
     for (int e = tid; e < E; e += 256) f_s[e] = (float)counts[e] / rows;
@@ -209,12 +209,14 @@ moe_status load_balance_launch(const float *logits, const int32_t *counts, int64
     const int64_t nchunks = (T + kLbChunk - 1) / kLbChunk;
     float *partial = reinterpret_cast<float *>(ws);
     const float coef = (float)((double)alpha * E / (double)T);
-    const dim3 g((unsigned)nchunks);
-    switch ((E + 63) / 64) {
-        case 1: lb_partial<1><<<g, 256, 0, s>>>(logits, counts, T, E, k, coef, partial, dlogits); break;
-        case 2: lb_partial<2><<<g, 256, 0, s>>>(logits, counts, T, E, k, coef, partial, dlogits); break;
-        case 3: lb_partial<3><<<g, 256, 0, s>>>(logits, counts, T, E, k, coef, partial, dlogits); break;
-        default: lb_partial<4><<<g, 256, 0, s>>>(logits, counts, T, E, k, coef, partial, dlogits); break;
+    for (int64_t c = 0; c < nchunks; c += kMaxBlocks) {
+        const dim3 g((unsigned)(nchunks - c < kMaxBlocks ? nchunks - c : kMaxBlocks));
+        switch ((E + 63) / 64) {
+            case 1: lb_partial<1><<<g, 256, 0, s>>>(logits, counts, T, E, k, coef, partial, dlogits, c); break;
+            case 2: lb_partial<2><<<g, 256, 0, s>>>(logits, counts, T, E, k, coef, partial, dlogits, c); break;
+            case 3: lb_partial<3><<<g, 256, 0, s>>>(logits, counts, T, E, k, coef, partial, dlogits, c); break;
+            default: lb_partial<4><<<g, 256, 0, s>>>(logits, counts, T, E, k, coef, partial, dlogits, c); break;
+        }
     }
     double *P = reinterpret_cast<double *>(reinterpret_cast<char *>(ws) + lb_partial_bytes(nchunks, E));
     lb_reduce<<<E, 256, 0, s>>>(partial, nchunks, E, T, P);

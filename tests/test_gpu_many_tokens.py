@@ -104,3 +104,24 @@ def test_route():
         assert torch.equal(pos.long(), first + i * step)
         assert torch.equal(r["topk_idx"][at, 0], idx) and (r["topk_gate"][at] == 1).all()
         assert torch.equal(r["sorted_token"][pos.long()], torch.arange(i * M, (i + 1) * M, dtype=torch.int32, device="cuda"))
+
+
+def test_load_balance():
+    """2^30 tokens of two experts, four threads a token. With the block's counts times
+    the repetitions f (3/4 and 1/4) and P stay as they are: P's sums are fp32 in a chunk
+    of 64 tokens, the same on both sides, and fp64 from there on, and a statistic is
+    rounded once. The gradient is the block's divided by the repetitions: its factor
+    alpha E / T and two products round here and the comparison's product does, one
+    product rounds there (its factor is a power of two): 5 u."""
+    M, rep, u = 1 << 20, (1 << 10) + 1, 2.0 ** -24
+    torch.cuda.empty_cache()
+    block = _block((M, 2), 8, torch.float32)
+    counts = torch.tensor([3 << 18, 1 << 18], dtype=torch.int32, device="cuda")
+    d1 = torch.zeros_like(block)
+    want = moe.moe_load_balance(block, counts, 1, 0.5, dlogits=d1)
+    big = block.repeat(rep, 1)
+    d = torch.zeros_like(big)
+    got = moe.moe_load_balance(big, counts * rep, 1, 0.5, dlogits=d)
+    assert torch.allclose(got, want, rtol=2 * u, atol=0)
+    for part in d.view(rep, M, 2).split(64):
+        assert ((part * rep - d1).abs() <= 5 * u * d1.abs() + 1e-35).all()
