@@ -455,7 +455,9 @@ moe_status mxfp8_quantize_both(const void *in, moe_dtype in_dt, int64_t rows, in
 
 /* The values that row-block MXFP8 stands for (axis = 1 of mxfp8_quantize):
  * out [rows, cols] = e * 2^(scale - 127), NaNs for scale byte 255. Exact in
- * fp32, and in bf16 down to its smallest normal number. out_dt: MOE_F32 or
+ * fp32, and in bf16 down to its smallest normal number; what is beyond the
+ * type's range (scale bytes from 247 on, which finite input never gets from
+ * mxfp8_quantize) is an infinity. out_dt: MOE_F32 or
  * MOE_BF16; cols: a multiple of 32 below 2^20; q and out 16-byte aligned,
  * scale at any address. rows = 0 is a no-op. */
 moe_status mxfp8_dequantize(const uint8_t *q, const uint8_t *scale, moe_dtype out_dt, int64_t rows,
@@ -653,9 +655,9 @@ moe_status moe_layer_norm_backward(const void *dy, moe_dtype dt, const void *x, 
  *       take (the layer's dispatch, moe_w4_gemm)
  * y [T, d] in dt may be null if yq [T, d] and yq_scale [T, d/32] are given
  * (both or neither). rstd [T] fp32 may be null. The rest (x, residual, sum,
- * gamma, x8, x8_scale, eps, T, d, alignment, dt) as in moe_layer_norm. Sums are
- * fp32 in a fixed order: the sum of a row's squares has to be finite in fp32
- * (values under 1e17). A row with a NaN gives NaNs in that row alone; of a row
+ * gamma, x8, x8_scale, eps, T, d, alignment, dt) as in moe_layer_norm. A row's
+ * squares are summed in fp32 by its threads, whose sums are joined in fp64, in a
+ * fixed order: the sums have to be finite in fp32 (values under 1e17). A row with a NaN gives NaNs in that row alone; of a row
  * with an infinity rstd is 0, so its finite elements give 0 and the infinity a
  * NaN. Outputs must not overlap inputs. T = 0 is a no-op. */
 moe_status moe_rms_norm(const void *x, moe_dtype dt, const void *residual, const float *gamma,
@@ -741,12 +743,12 @@ moe_status moe_w4_quantize(const void *in, moe_dtype in_dt, int64_t rows, int64_
  * With many rows an expert moe_w4_experts8 (below) and the MXFP8 grouped GEMMs
  * are the faster ways, for some more roundings. us for everything after the
  * routing, from x in bf16: here / moe_w4_experts8 / MXFP8, by rows an expert:
- *   E = 128, k = 4, d = 2048, h = 1024: 4 rows 94 / 96 / 196, 8 rows 123 / 97 / 197,
- *     32 rows 194 / 108 / 208, 128 rows 555 / 187 / 289, 512 rows 2018 / 498 / 732
- *   E = 8, k = 2, d = 2048, h = 1024: 16 rows 21 / 26 / 49, 32 rows 31 / 27 / 50, 256
- *     rows 80 / 39 / 54
- *   E = 2, k = 2, d = 8192, h = 4096: 16 rows 39 / 50 / 128, 32 rows 68 / 51 / 129, 512
- *     rows 386 / 109 / 396
+ *   E = 128, k = 4, d = 2048, h = 1024: 4 rows 94 / 93 / 189, 8 rows 127 / 97 / 197,
+ *     32 rows 193 / 109 / 211, 128 rows 554 / 186 / 294, 512 rows 1973 / 498 / 717
+ *   E = 8, k = 2, d = 2048, h = 1024: 16 rows 21 / 24 / 47, 32 rows 29 / 25 / 48, 256
+ *     rows 90 / 39 / 54
+ *   E = 2, k = 2, d = 8192, h = 4096: 16 rows 40 / 51 / 128, 32 rows 69 / 52 / 129, 512
+ *     rows 377 / 108 / 404
  * topk_gate,
  * token_pos, sorted_token and offsets are moe_route's for the T tokens
  * (token_pos < 0: that slot adds nothing). w1q [E, 2h, d/2], w1_scale [E, 2h,
@@ -794,8 +796,8 @@ moe_status moe_w4_experts(const moe_w4_desc *w, void *stream);
  *               multiple of 32, at most 8192. An H' beyond fp32's range is
  *               outside the contract, as an infinity is in mxfp8_quantize
  * n_groups at most 256; rows (at least offsets[n_groups]) at most 2^31 - 256; K:
- * a multiple of 128, K and N at most 16384; a, b and c 16-byte aligned, a_scale and b_scale 4-byte, with K a
- * multiple of 512 16-byte. The order of a sum depends on K alone: a row's result
+ * a multiple of 128, K and N at most 16384; a, b and c 16-byte aligned, a_scale and
+ * b_scale 4-byte, with K a multiple of 512 16-byte. The order of a sum depends on K alone: a row's result
  * does not depend on the rows, groups or columns around it. A row with NaNs
  * reaches no other. Rows outside all groups are not written; rows = 0 is a
  * no-op. c and c_scale overlap none of the inputs. */

@@ -60,11 +60,13 @@ MOE_DEV void store_any(u32x4_any *p, const u32x4 &v) {
     else *p = v;
 }
 
-// Chunks at a list's end that the norm leaves in the last-level cache (256
+// Chunks at a launch's end that the norm leaves in the last-level cache (256
 // MiB, of which a list that is clipped into other tensors has half), and that
-// the clipping, which walks the list backwards, finds there. The others are
+// the clipping, which walks a launch's chunks backwards, finds there. The others are
 // read and written past it: 3.2 GB norm 520 -> 463 us, clipping 1240 -> 1165 us;
-// 21 MB, all of which stays, 18.2 us for both and 20.3 past it.
+// 21 MB, all of which stays, 18.2 us for both and 20.3 past it. Those lists are one
+// launch. Of a list of more than kGradMax tensors the launches go forwards in both
+// passes and each keeps its own last chunks, most of which the next ones push out.
 constexpr int64_t kGradKept = (128 << 20) / kChunkBytes;
 
 template <bool BF16>
@@ -83,9 +85,9 @@ MOE_DEV int tensor_of(const GradArgs &a, int64_t c) {
     return lo;
 }
 
-// f(tensor, first element, elements, whether the chunk is one of the list's
+// f(tensor, first element, elements, whether the chunk is one of the launch's
 // last kGradKept) for the chunks blockIdx.x, blockIdx.x + gridDim.x, .. of a
-// list; BACK: counted from its end.
+// launch; BACK: counted from its end.
 template <bool BACK, typename F>
 MOE_DEV void for_chunks(const GradArgs &a, F f) {
     for (int64_t i = blockIdx.x; i < a.chunks; i += gridDim.x) {

@@ -12,8 +12,10 @@
 // experts take: the bytes that quantising the stored y gives.
 // s may be kept between the two passes as an 8-bit checkpoint (act8.h),
 // written from the forward's registers and read by the backward in place of
-// s. All sums and statistics are fp32, in a fixed order (no atomics); the
-// variance is taken about the mean, from the row in registers.
+// s. All sums and statistics are fp32, in a fixed order (no atomics), but for
+// the root-mean-square norm's forward, which joins its threads' fp32 sums and
+// takes their root in fp64; the variance is taken about the mean, from the row in
+// registers.
 //
 // Both passes are bound by memory and read and write every row once; a row
 // stays in its threads' registers from its load to its last store, in its own

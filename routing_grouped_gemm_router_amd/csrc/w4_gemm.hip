@@ -24,14 +24,18 @@
 // of 128 experts 280 -> 272). H' is rounded once, from fp32 to the MXFP8 that the
 // second product multiplies; the prompt's y once, to fp16 of a block's own scale
 // (kOutHalf): rounded to bf16 it would cost the output as much as out's own rounding
-// (2.5e-3 from 64 bits in the 2-norm and not 1.7e-3), for 1 % of the time.
+// (2.5e-3 from 64 bits in the 2-norm and not 1.8e-3), for 1 % of the time. Of those
+// 1.8e-3 out's rounding is 1.66e-3; the rest is H' on another E4M3 code than the exact
+// value's, 7 elements in 10,000, from the matrix unit's sums (off by some 4.4e-6 of their
+// rms; the fp32 SwiGLU adds 1 in 10 million).
 //
 // 65536 rows, up and down: E = 128, d = 2048, h = 1024 270 and 174 us (2.0 and
 // 1.58 PFLOP/s); E = 8, d = 4096, h = 2048 900 and 510 us (2.45 and 2.15). Of E =
-// 128's up the copies and outputs alone take 228 us (64-byte weight rows cost the L1
-// a whole line each), products, LDS reads and outputs alone 207 (on random data the
-// chip's power holds the clock at 1.9 GHz); of its down the copies and outputs 187,
-// without the outputs 130: a tile's outputs come all at once.
+// 128's up (279 us in that run) the copies and outputs alone take 235 us (64-byte
+// weight rows cost the L1 a whole line each), the copies 203, products, LDS reads and
+// outputs without copies 221 (on random data the chip's power holds the clock at 1.9
+// GHz); of its down (177) the copies and outputs 175, the copies 87, copies and
+// products without outputs 121: a tile's outputs come all at once.
 #include <type_traits>
 
 #include "act8.h"
@@ -349,8 +353,8 @@ void w4_gemm_tiles(moe_w4_gemm_desc g) {
                                    pack(f[8 * q + 4 + 2 * x], f[8 * q + 5 + 2 * x]), o[q][x], o[q][2 + x]);
                     // then columns 8 half + 16 (lane / 16 % 2) of rows 0-15 and of rows
                     // 16-31: 64 bytes of a row an instruction, not 32 (1 to 2 %). Past
-                    // the last-level cache the large outputs left 13 % sooner, and a
-                    // combine behind them took 4 % of both longer.
+                    // the last-level cache 268 MB in bf16 left 14 % sooner, and where a
+                    // combine read them behind it both together took 4 % longer.
 #pragma unroll
                     for (int x = 0; x < 4; x++) {
                         const auto r = __builtin_amdgcn_permlane16_swap(o[0][x], o[1][x], false, false);
@@ -480,7 +484,8 @@ moe_status w4_gemm_launch(const moe_w4_gemm_desc &g, hipStream_t s) {
 // a token a wave, all loads of kUnrollY column chunks in flight before the first
 // sum. A lane reads one block's exponent of those chunks and hands it to the four
 // that need it. Bound by memory (16384 tokens of 4 rows of
-// 2048: 343 MB in 54 us, 6.4 TB/s).
+// 2048: 343 MB in 54 us, 6.4 TB/s). With five to eight rows it has 200 registers, two
+// waves a SIMD: 5.4 TB/s with 5 and 6, 4.6 with 8.
 constexpr int kUnrollY = 4;
 template <int KMAX>
 __global__ __launch_bounds__(256) void w4_combine_half(const uint4 *__restrict__ y, const uint8_t *__restrict__ scale,
