@@ -657,9 +657,9 @@ moe_status moe_layer_norm_backward(const void *dy, moe_dtype dt, const void *x, 
  * (both or neither). rstd [T] fp32 may be null. The rest (x, residual, sum,
  * gamma, x8, x8_scale, eps, T, d, alignment, dt) as in moe_layer_norm. A row's
  * squares are summed in fp32 by its threads, whose sums are joined in fp64, in a
- * fixed order: the sums have to be finite in fp32 (values under 1e17). A row with a NaN gives NaNs in that row alone; of a row
- * with an infinity rstd is 0, so its finite elements give 0 and the infinity a
- * NaN. Outputs must not overlap inputs. T = 0 is a no-op. */
+ * fixed order: the sums have to be finite in fp32 (values under 1e17). A row with
+ * a NaN gives NaNs in that row alone; of a row with an infinity rstd is 0, so its
+ * finite elements give 0 and the infinity a NaN. Outputs must not overlap inputs. T = 0 is a no-op. */
 moe_status moe_rms_norm(const void *x, moe_dtype dt, const void *residual, const float *gamma,
                         float eps, int64_t T, int32_t d, void *y, void *sum, float *rstd,
                         uint8_t *yq, uint8_t *yq_scale, uint8_t *x8, uint8_t *x8_scale,
@@ -797,10 +797,10 @@ moe_status moe_w4_experts(const moe_w4_desc *w, void *stream);
  *               outside the contract, as an infinity is in mxfp8_quantize
  * n_groups at most 256; rows (at least offsets[n_groups]) at most 2^31 - 256; K:
  * a multiple of 128, K and N at most 16384; a, b and c 16-byte aligned, a_scale and
- * b_scale 4-byte, with K a multiple of 512 16-byte. The order of a sum depends on K alone: a row's result
- * does not depend on the rows, groups or columns around it. A row with NaNs
- * reaches no other. Rows outside all groups are not written; rows = 0 is a
- * no-op. c and c_scale overlap none of the inputs. */
+ * b_scale 4-byte, with K a multiple of 512 16-byte. The order of a sum depends on
+ * K alone: a row's result does not depend on the rows, groups or columns around
+ * it. A row with NaNs reaches no other. Rows outside all groups are not written;
+ * rows = 0 is a no-op. c and c_scale overlap none of the inputs. */
 typedef struct moe_w4_gemm_desc {
     int32_t n_groups;
     int32_t epilogue;

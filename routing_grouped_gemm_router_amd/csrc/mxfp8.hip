@@ -488,7 +488,7 @@ moe_status mxfp8_quantize_launch(const void *in, moe_dtype in_dt, int64_t rows, 
                                  hipStream_t s) {
     const bool bf = in_dt == MOE_BF16;
     if (axis == 1) {
-        const int64_t most = kMaxBlocks * 256 * 16 / cols, piece = most > 0 ? most : 1;   // rows of a launch
+        const int64_t piece = kMaxBlocks * 256 * 16 / cols;   // rows of a launch: 8192 and more
         for (int64_t r = 0; r < rows; r += piece) {
             const int64_t n = rows - r < piece ? rows - r : piece, n_blocks = n * cols / 32;
             const unsigned grid = (unsigned)((n_blocks * 2 + 255) / 256);
